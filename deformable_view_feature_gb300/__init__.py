@@ -28,7 +28,9 @@ from . import build as _build
 
 __all__ = ["da_forward", "da_backward", "da_forward_fused", "da_backward_fused", "da_forward_projected",
            "da_backward_projected", "warpaffine_u8", "warpaffine_preprocess", "backward_workspace_size",
-           "backward_path", "da_backward_bin", "DeformableAggregationFunction", "HostPipeline", "DaError", "library_path", "load_library", "da_version"]
+           "backward_path", "da_backward_bin", "DeformableAggregationFunction", "HostPipeline", "DaError", "library_path", "load_library", "da_version",
+           "gn_forward", "gn_backward", "GroupNormActFunction", "dattn_forward", "dattn_backward", "dattn_path",
+           "relative_buckets", "DifferentialAttentionFunction"]
 
 DA_F32, DA_BF16, DA_F16 = 0, 1, 2
 _STATUS = {0: "DA_OK", 1: "DA_ERR_NULL", 2: "DA_ERR_SHAPE", 3: "DA_ERR_ALIGN",
@@ -105,6 +107,18 @@ def load_library():
     lib.da_backward_fused_workspace_size.restype = ctypes.c_int
     lib.da_backward_workspace_size.argtypes = [ctypes.POINTER(DaDims), ctypes.POINTER(ctypes.c_size_t)]
     lib.da_backward_workspace_size.restype = ctypes.c_int
+    psize = ctypes.POINTER(ctypes.c_size_t)
+    lib.gn_workspace_size.argtypes = [vp, vp, vp, ctypes.c_int32, psize]
+    lib.gn_forward.argtypes = [vp] * 9 + [ctypes.c_size_t, vp]
+    lib.gn_backward.argtypes = [vp] * 12 + [ctypes.c_size_t, vp]
+    lib.dattn_path.argtypes = [vp]
+    lib.dattn_workspace_size.argtypes = [vp, ctypes.c_int32, psize]
+    lib.dattn_forward.argtypes = [vp] * 5 + [ctypes.c_size_t, vp]
+    lib.dattn_backward.argtypes = [vp] * 11 + [ctypes.c_size_t, vp]
+    for f in (lib.gn_workspace_size, lib.gn_forward, lib.gn_backward, lib.dattn_workspace_size, lib.dattn_forward,
+              lib.dattn_backward):
+        f.restype = ctypes.c_int
+    lib.dattn_path.restype = ctypes.c_int32
     lib.da_status_string.argtypes = [ctypes.c_int]
     lib.da_status_string.restype = ctypes.c_char_p
     lib.da_last_error.argtypes = []
@@ -616,3 +630,8 @@ class DeformableAggregationFunction(torch.autograd.Function):
         if mc_ms_feat.dtype != torch.float32:
             gf = gf.to(mc_ms_feat.dtype)
         return gf, None, None, gl, gw
+
+
+from .attention import (DifferentialAttentionFunction, dattn_backward, dattn_forward, dattn_path,  # noqa: E402
+                        relative_buckets)
+from .norm import GroupNormActFunction, gn_backward, gn_forward  # noqa: E402

@@ -1,0 +1,233 @@
+"""Differential attention with a learned relative position bias by buckets (include/dattn.h).
+
+Each head has two query and two key vectors and one value; its output is the
+difference of two softmax maps over the keys, weighted by a learned lam:
+
+    out = (softmax(q0 k0 + bias) - lam * softmax(q1 k1 + bias)) v
+
+    buckets = relative_buckets(32, 128).cuda()                    # once
+    out = dattn_forward(q, k, v, lam, bias_table=table, bucket_map=buckets)
+    out, saved = dattn_forward(..., keep_for_backward=True)
+    grad_q, grad_k, grad_v, grad_lam, grad_table = dattn_backward(q, k, v, lam, out, saved, grad_out, ...)
+
+``DifferentialAttentionFunction`` wraps the two as a torch autograd function.
+The functions only marshal arguments; the arithmetic runs in the library's CUDA
+kernels and there is no fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import DA_BF16, DA_F16, DA_F32, DaError, _check, _dptr, load_library
+
+__all__ = ["dattn_forward", "dattn_backward", "dattn_path", "relative_buckets", "DifferentialAttentionFunction"]
+
+_DTYPES = {torch.float32: DA_F32, torch.bfloat16: DA_BF16, torch.float16: DA_F16}
+
+
+class DattnProblem(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "num_queries", "num_keys", "num_heads", "num_kv_heads", "width",
+                                               "value_width", "dtype", "num_buckets", "reach", "causal")]
+                + [("scale", ctypes.c_float)] + [(n, ctypes.c_void_p) for n in ("q", "k", "v")]
+                + [("q_stride", ctypes.c_int64 * 4), ("k_stride", ctypes.c_int64 * 4), ("v_stride", ctypes.c_int64 * 3)]
+                + [(n, ctypes.c_void_p) for n in ("lam", "bias_table", "bucket_map", "pos_q", "pos_k", "key_mask",
+                                                  "key_lengths")])
+
+
+def relative_buckets(num_buckets: int, max_distance: int, bidirectional: bool = True) -> torch.Tensor:
+    """Bucket of each relative position r = key - query in -max_distance ..
+    max_distance, as int32 [2 * max_distance + 1] (a bucket_map for
+    dattn_forward; farther positions take the ends' buckets).
+
+    With bidirectional, one half of the buckets is for keys at or before the
+    query and the other for keys after it; without, all are for keys at or
+    before it and later keys share bucket 0. Half of each side's buckets hold
+    one distance each; the others grow with the logarithm of the distance. The
+    borders are decided in whole numbers: with e single-distance buckets and w
+    others, distance n lies t or more buckets past e when
+    n**w * e**t >= max_distance**t * e**w."""
+    side = num_buckets // 2 if bidirectional else num_buckets
+    if side < 1 or max_distance < 1:
+        raise ValueError("relative_buckets needs a bucket per side and max_distance >= 1")
+    e = max(side // 2, 1)
+    w = side - e
+    of = []
+    for r in range(-max_distance, max_distance + 1):
+        n = abs(r) if bidirectional else max(-r, 0)
+        t = 0
+        if n >= e:
+            while t + 1 < w and n ** w * e ** (t + 1) >= max_distance ** (t + 1) * e ** w:
+                t += 1
+            n = e + t
+        of.append(min(n, side - 1) + (side if bidirectional and r > 0 else 0))
+    return torch.tensor(of, dtype=torch.int32)
+
+
+def _strided(t: torch.Tensor, name: str) -> int:
+    """Data pointer of a q, k or v whose last dimension is contiguous."""
+    if t.numel() == 0:
+        return None
+    if not t.is_cuda:
+        raise ValueError("device tensors must live on a CUDA device")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _small(t: Optional[torch.Tensor], name: str, shape, dtype) -> Optional[int]:
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}")
+    return _dptr(t)
+
+
+def _problem(q, k, v, lam, bias_table, bucket_map, pos_q, pos_k, key_mask, key_lengths, causal, scale) -> DattnProblem:
+    if q.dim() != 5 or q.shape[3] != 2:
+        raise ValueError("q must be [B, Lq, H, 2, D]")
+    if k.dim() != 5 or k.shape[3] != 2:
+        raise ValueError("k must be [B, Lk, Hkv, 2, D]")
+    if v.dim() != 4:
+        raise ValueError("v must be [B, Lk, Hkv, Dv]")
+    B, Lq, H, _, D = q.shape
+    _, Lk, Hkv, _, Dk = k.shape
+    Dv = v.shape[3]
+    if k.shape[0] != B or tuple(v.shape[:3]) != (B, Lk, Hkv) or Dk != D:
+        raise ValueError("q, k and v disagree on batch, keys, heads or width")
+    if q.dtype not in _DTYPES:
+        raise TypeError("q, k and v must be float32, bfloat16 or float16")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must have one type")
+    if (bias_table is None) != (bucket_map is None):
+        raise ValueError("bias_table and bucket_map go together")
+    p = DattnProblem(batch=B, num_queries=Lq, num_keys=Lk, num_heads=H, num_kv_heads=Hkv, width=D, value_width=Dv,
+                     dtype=_DTYPES[q.dtype], causal=int(bool(causal)), scale=D ** -0.5 if scale is None else scale,
+                     q=_strided(q, "q"), k=_strided(k, "k"), v=_strided(v, "v"))
+    p.q_stride[:] = q.stride()[:4]
+    p.k_stride[:] = k.stride()[:4]
+    p.v_stride[:] = v.stride()[:3]
+    p.lam = _small(lam, "lam", (H,), torch.float32)
+    if bias_table is not None:
+        if bias_table.dim() != 2 or bucket_map.dim() != 1 or bucket_map.shape[0] % 2 != 1:
+            raise ValueError("bias_table must be [num_buckets, H] and bucket_map [2 * reach + 1]")
+        p.num_buckets, p.reach = bias_table.shape[0], bucket_map.shape[0] // 2
+        p.bias_table = _small(bias_table, "bias_table", (p.num_buckets, H), torch.float32)
+        p.bucket_map = _small(bucket_map, "bucket_map", (2 * p.reach + 1,), torch.int32)
+    p.pos_q = _small(pos_q, "pos_q", (B, Lq), torch.int32)
+    p.pos_k = _small(pos_k, "pos_k", (B, Lk), torch.int32)
+    p.key_mask = _small(key_mask, "key_mask", (B, Lk), torch.bool)
+    p.key_lengths = _small(key_lengths, "key_lengths", (B,), torch.int32)
+    return p
+
+
+def _scratch(lib, p, backward, device):
+    n = ctypes.c_size_t(0)
+    _check(lib.dattn_workspace_size(ctypes.byref(p), backward, ctypes.byref(n)))
+    return torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None, n.value
+
+
+def dattn_path(q, k, v, lam, **options) -> str:
+    """Which kernels dattn_forward and dattn_backward take for these
+    arguments: "tensor" (the tensor cores) or "general" (fp32 units)."""
+    r = load_library().dattn_path(ctypes.byref(_options(q, k, v, lam, **options)))
+    if r < 0:
+        raise DaError(4, load_library().da_last_error().decode(errors="replace"))
+    return "tensor" if r == 1 else "general"
+
+
+def _options(q, k, v, lam, bias_table=None, bucket_map=None, pos_q=None, pos_k=None, key_mask=None, key_lengths=None,
+             causal=False, scale=None) -> DattnProblem:
+    return _problem(q, k, v, lam, bias_table, bucket_map, pos_q, pos_k, key_mask, key_lengths, causal, scale)
+
+
+def dattn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
+                  bias_table: Optional[torch.Tensor] = None, bucket_map: Optional[torch.Tensor] = None,
+                  pos_q: Optional[torch.Tensor] = None, pos_k: Optional[torch.Tensor] = None,
+                  key_mask: Optional[torch.Tensor] = None, key_lengths: Optional[torch.Tensor] = None,
+                  causal: bool = False, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                  keep_for_backward: bool = False, stream=None):
+    """Forward pass on the current (or given) CUDA stream; returns out
+    [B, Lq, H, Dv] in q's type, with keep_for_backward (out, saved).
+
+    q [B, Lq, H, 2, D], k [B, Lk, Hkv, 2, D], v [B, Lk, Hkv, Dv], H a multiple
+    of Hkv, any strides with a contiguous last dimension; lam fp32 [H];
+    bias_table fp32 [num_buckets, H] with bucket_map int32 [2 * reach + 1]
+    (relative_buckets); pos_q, pos_k int32 [B, L], in (-2**30, 2**30), default
+    the indices, the queries being the last; key_mask bool [B, Lk];
+    key_lengths int32 [B]. A query that sees no key gives 0. scale defaults to
+    D ** -0.5. What the call allocates belongs to the stream it runs on."""
+    lib = load_library()
+    p = _problem(q, k, v, lam, bias_table, bucket_map, pos_q, pos_k, key_mask, key_lengths, causal, scale)
+    shape = (p.batch, p.num_queries, p.num_heads, p.value_width)
+    if out is not None and (tuple(out.shape) != shape or out.dtype != q.dtype):
+        raise ValueError(f"out must be {q.dtype} {shape}")
+    with torch.cuda.stream(stream):
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out1 = lse = None
+        if keep_for_backward:
+            out1 = torch.empty(shape, dtype=q.dtype, device=q.device)
+            lse = torch.empty(p.batch, p.num_heads, 2, p.num_queries, dtype=torch.float32, device=q.device)
+        ws, n = _scratch(lib, p, 0, q.device)
+        _check(lib.dattn_forward(ctypes.byref(p), _dptr(out), _dptr(out1), _dptr(lse), _dptr(ws), n,
+                                 torch.cuda.current_stream().cuda_stream or None))
+    return (out, (out1, lse)) if keep_for_backward else out
+
+
+def dattn_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor, out: torch.Tensor, saved,
+                   grad_out: torch.Tensor, bias_table: Optional[torch.Tensor] = None,
+                   bucket_map: Optional[torch.Tensor] = None, pos_q: Optional[torch.Tensor] = None,
+                   pos_k: Optional[torch.Tensor] = None, key_mask: Optional[torch.Tensor] = None,
+                   key_lengths: Optional[torch.Tensor] = None, causal: bool = False, scale: Optional[float] = None,
+                   stream=None):
+    """Backward pass of dattn_forward(..., keep_for_backward=True) with the
+    same arguments; returns (grad_q, grad_k, grad_v contiguous in q's type,
+    grad_lam fp32 [H], grad_table fp32 [num_buckets, H] or None)."""
+    lib = load_library()
+    p = _problem(q, k, v, lam, bias_table, bucket_map, pos_q, pos_k, key_mask, key_lengths, causal, scale)
+    shape = (p.batch, p.num_queries, p.num_heads, p.value_width)
+    out1, lse = saved
+    for name, t in (("out", out), ("saved[0]", out1), ("grad_out", grad_out)):
+        if tuple(t.shape) != shape or t.dtype != q.dtype:
+            raise ValueError(f"{name} must be {q.dtype} {shape}")
+    if tuple(lse.shape) != (p.batch, p.num_heads, 2, p.num_queries) or lse.dtype != torch.float32:
+        raise ValueError("saved[1] must be what dattn_forward returned")
+    with torch.cuda.stream(stream):
+        gq, gk, gv = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v))
+        gl = torch.empty_like(lam)
+        gt = torch.empty_like(bias_table) if bias_table is not None else None
+        ws, n = _scratch(lib, p, 1, q.device)
+        _check(lib.dattn_backward(ctypes.byref(p), _dptr(out), _dptr(out1), _dptr(lse), _dptr(grad_out), _dptr(gq),
+                                  _dptr(gk), _dptr(gv), _dptr(gl), _dptr(gt), _dptr(ws), n,
+                                  torch.cuda.current_stream().cuda_stream or None))
+    return gq, gk, gv, gl, gt
+
+
+class DifferentialAttentionFunction(torch.autograd.Function):
+    """Autograd wrapper: apply(q, k, v, lam, bias_table, bucket_map, pos_q,
+    pos_k, key_mask, key_lengths, causal, scale) -> out, with gradients for q,
+    k, v, lam and bias_table."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, lam, bias_table=None, bucket_map=None, pos_q=None, pos_k=None, key_mask=None,
+                key_lengths=None, causal=False, scale=None):
+        q, k, v = (t if t.shape[-1] == 1 or t.stride(-1) == 1 else t.contiguous() for t in (q, k, v))
+        lam = lam.contiguous()
+        bias_table = None if bias_table is None else bias_table.contiguous()
+        opt = dict(bias_table=bias_table, bucket_map=bucket_map, pos_q=pos_q, pos_k=pos_k, key_mask=key_mask,
+                   key_lengths=key_lengths, causal=causal, scale=scale)
+        out, saved = dattn_forward(q, k, v, lam, **opt, keep_for_backward=True)
+        ctx.save_for_backward(q, k, v, lam, out, *saved, bias_table, bucket_map, pos_q, pos_k, key_mask, key_lengths)
+        ctx.rest = (causal, scale)
+        return out
+
+    @staticmethod
+    def backward(ctx, grad_output):
+        q, k, v, lam, out, out1, lse, *opt = ctx.saved_tensors
+        names = ("bias_table", "bucket_map", "pos_q", "pos_k", "key_mask", "key_lengths")
+        gq, gk, gv, gl, gt = dattn_backward(q, k, v, lam, out, (out1, lse), grad_output.to(q.dtype).contiguous(),
+                                            **dict(zip(names, opt)), causal=ctx.rest[0], scale=ctx.rest[1])
+        return gq, gk, gv, gl, gt, None, None, None, None, None, None, None

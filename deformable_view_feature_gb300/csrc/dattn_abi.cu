@@ -1,0 +1,215 @@
+// extern "C" entry points of the differential attention (include/dattn.h):
+// validation, the plan (kernels, split over the keys, workspace) and launches.
+#include <cmath>
+
+#include "dattn_internal.cuh"
+
+namespace da {
+namespace {
+
+struct DattnPlan {
+    DattnArgs a;
+    int elem;
+    bool tensor;
+    size_t part_o, part_ml, delta, part_table, total;
+};
+
+size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// CTAs per tile of rows. Where the tiles alone leave most of the 152 SMs
+// without work, the keys are split among enough CTAs to give each one about
+// one, and no fewer than two key tiles (128 keys) to each.
+int split_count(int64_t tiles, int keys)
+{
+    if (tiles <= 0 || tiles > 76) return 1;
+    const int64_t most = keys / 128, want = 152 / tiles;
+    return static_cast<int>(most < 1 ? 1 : want < most ? want : most);
+}
+
+da_status dattn_plan(const dattn_problem *pr, bool backward, DattnPlan &p)
+{
+    if (!pr) return fail(DA_ERR_NULL, "problem is NULL");
+    const dattn_problem &d = *pr;
+    if (d.batch < 0 || d.num_queries < 0 || d.num_keys < 0) return fail(DA_ERR_SHAPE, "negative size");
+    if (d.num_heads < 1 || d.num_kv_heads < 1 || d.num_heads % d.num_kv_heads != 0)
+        return fail(DA_ERR_SHAPE, "num_heads (%d) must be a positive multiple of num_kv_heads (%d)", d.num_heads,
+                    d.num_kv_heads);
+    if (d.width < 1 || d.value_width < 1) return fail(DA_ERR_SHAPE, "width %d and value_width %d must be positive", d.width, d.value_width);
+    if (d.width > DATTN_MAX_WIDTH || d.value_width > DATTN_MAX_VALUE_WIDTH)
+        return fail(DA_ERR_UNSUPPORTED, "width %d or value_width %d exceeds %d or %d", d.width, d.value_width,
+                    DATTN_MAX_WIDTH, DATTN_MAX_VALUE_WIDTH);
+    if (d.dtype != DA_F32 && d.dtype != DA_BF16 && d.dtype != DA_F16) return fail(DA_ERR_SHAPE, "unknown dtype %d", d.dtype);
+    if (!std::isfinite(d.scale)) return fail(DA_ERR_SHAPE, "scale must be finite");
+    if (d.batch > 65535 || d.num_kv_heads > 65535) return fail(DA_ERR_UNSUPPORTED, "batch or num_kv_heads exceeds 65535");
+    const int G = d.num_heads / d.num_kv_heads;
+    const int64_t rows = static_cast<int64_t>(d.num_queries) * G;
+    if (rows > INT32_MAX - 1024 || d.num_keys > INT32_MAX - 1024 || d.num_queries > (1 << 29) || d.num_keys > (1 << 29))
+        return fail(DA_ERR_UNSUPPORTED, "sequences too long: %d queries, %d keys", d.num_queries, d.num_keys);
+    if (d.num_buckets < 0) return fail(DA_ERR_SHAPE, "negative num_buckets");
+    if (d.num_buckets > 0) {
+        if (d.reach < 1) return fail(DA_ERR_SHAPE, "reach %d must be positive", d.reach);
+        if (d.reach > DATTN_MAX_REACH) return fail(DA_ERR_UNSUPPORTED, "reach %d exceeds %d", d.reach, DATTN_MAX_REACH);
+        if (static_cast<int64_t>(d.num_buckets) * G > DATTN_MAX_TABLE)
+            return fail(DA_ERR_UNSUPPORTED, "num_buckets * num_heads / num_kv_heads = %lld exceeds %d",
+                        static_cast<long long>(d.num_buckets) * G, DATTN_MAX_TABLE);
+    }
+    for (int i = 0; i < 4; ++i)
+        if (d.q_stride[i] < 0 || d.k_stride[i] < 0 || (i < 3 && d.v_stride[i] < 0))
+            return fail(DA_ERR_SHAPE, "strides must not be negative");
+    DattnArgs &a = p.a;
+    a.q = d.q;
+    a.k = d.k;
+    a.v = d.v;
+    for (int i = 0; i < 4; ++i) {
+        a.qs[i] = d.q_stride[i];
+        a.ks[i] = d.k_stride[i];
+        if (i < 3) a.vs[i] = d.v_stride[i];
+    }
+    a.lam = d.lam;
+    a.table = d.bias_table;
+    a.bmap = d.bucket_map;
+    a.pos_q = d.pos_q;
+    a.pos_k = d.pos_k;
+    a.lengths = d.key_lengths;
+    a.mask = d.key_mask;
+    a.B = d.batch;
+    a.Lq = d.num_queries;
+    a.Lk = d.num_keys;
+    a.H = d.num_heads;
+    a.Hkv = d.num_kv_heads;
+    a.G = G;
+    a.D = d.width;
+    a.Dv = d.value_width;
+    a.nb = d.num_buckets;
+    a.reach = d.num_buckets > 0 ? d.reach : 0;
+    a.causal = d.causal != 0;
+    a.rows = static_cast<int32_t>(rows);
+    a.div_G = FastDiv::make(static_cast<uint32_t>(G));
+    a.scale = d.scale;
+    a.scale_log2 = static_cast<float>(static_cast<double>(d.scale) * 1.4426950408889634);
+    p.elem = d.dtype == DA_F32 ? 4 : 2;
+    p.tensor = false;
+    const int64_t bn = static_cast<int64_t>(a.B) * a.Hkv;
+    size_t at = 0;
+    a.splits = 1;
+    a.keys_per_split = a.Lk > 0 ? a.Lk : 1;
+    if (!backward) {
+        const int qt = dattn_general_row_tile(a);
+        const int n = split_count(bn * ((rows + qt - 1) / qt), a.Lk);
+        if (n > 1) {
+            a.keys_per_split = ((a.Lk + n - 1) / n + 63) / 64 * 64;
+            a.splits = (a.Lk + a.keys_per_split - 1) / a.keys_per_split;
+        }
+        if (a.splits > 1) {
+            p.part_o = at;
+            at += round256(sizeof(float) * bn * rows * a.splits * 2 * a.Dv);
+            p.part_ml = at;
+            at += round256(sizeof(float) * bn * rows * a.splits * 4);
+        }
+    } else {
+        const int kt = dattn_general_key_tile(a);
+        a.table_ctas = (a.Lk + kt - 1) / kt;
+        p.delta = at;
+        at += round256(sizeof(float) * bn * 2 * rows);
+        p.part_table = at;
+        at += round256(sizeof(float) * bn * a.table_ctas * a.nb * G);
+    }
+    p.total = at;
+    return DA_OK;
+}
+
+da_status dattn_buffers(DattnPlan &p, void *ws, size_t ws_bytes)
+{
+    DattnArgs &a = p.a;
+    const int64_t nq = static_cast<int64_t>(a.B) * a.rows, nk = static_cast<int64_t>(a.B) * a.Lk;
+    if ((nq > 0 && !a.q) || (nk > 0 && (!a.k || !a.v))) return fail(DA_ERR_NULL, "q, k or v is NULL");
+    if (!a.lam) return fail(DA_ERR_NULL, "lam is NULL");
+    if (a.nb > 0 && (!a.table || !a.bmap)) return fail(DA_ERR_NULL, "bias_table or bucket_map is NULL");
+    const void *elems[] = {a.q, a.k, a.v, a.out, a.out1, a.grad_out, a.grad_q, a.grad_k, a.grad_v};
+    for (const void *x : elems)
+        if (!aligned(x, p.elem)) return fail(DA_ERR_ALIGN, "q, k, v, outputs and gradients must be aligned to their elements");
+    const void *words[] = {a.lam, a.table, a.bmap, a.pos_q, a.pos_k, a.lengths, a.lse, a.grad_lam, a.grad_table};
+    for (const void *x : words)
+        if (!aligned(x, 4)) return fail(DA_ERR_ALIGN, "fp32 and int32 tensors must be 4-byte aligned");
+    if (p.total > 0) {
+        if (!ws || ws_bytes < p.total)
+            return fail(DA_ERR_WORKSPACE, "workspace of %zu bytes; %zu are needed", ws ? ws_bytes : size_t{0}, p.total);
+        if (!aligned(ws, 256)) return fail(DA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    }
+    char *w = static_cast<char *>(ws);
+    a.part_o = reinterpret_cast<float *>(w + p.part_o);
+    a.part_ml = reinterpret_cast<float *>(w + p.part_ml);
+    a.delta = reinterpret_cast<float *>(w + p.delta);
+    a.part_table = reinterpret_cast<float *>(w + p.part_table);
+    return DA_OK;
+}
+
+}  // namespace
+}  // namespace da
+
+extern "C" {
+
+int32_t dattn_path(const dattn_problem *p)
+{
+    da::DattnPlan pl{};
+    return da::dattn_plan(p, false, pl) == DA_OK ? static_cast<int32_t>(pl.tensor) : -1;
+}
+
+da_status dattn_workspace_size(const dattn_problem *p, int32_t backward, size_t *bytes)
+{
+    if (!bytes) return da::fail(DA_ERR_NULL, "bytes is NULL");
+    da::DattnPlan pl{};
+    const da_status st = da::dattn_plan(p, backward != 0, pl);
+    if (st == DA_OK) *bytes = pl.total;
+    return st;
+}
+
+da_status dattn_forward(const dattn_problem *p, void *out, void *out1, float *lse, void *workspace,
+                        size_t workspace_bytes, da_stream_t stream)
+{
+    da::DattnPlan pl{};
+    da_status st = da::dattn_plan(p, false, pl);
+    if (st != DA_OK) return st;
+    pl.a.out = out;
+    pl.a.out1 = out1;
+    pl.a.lse = lse;
+    if ((st = da::dattn_buffers(pl, workspace, workspace_bytes)) != DA_OK) return st;
+    if (static_cast<int64_t>(pl.a.B) * pl.a.rows == 0) return DA_OK;
+    if (!out) return da::fail(DA_ERR_NULL, "out is NULL");
+    if ((out1 == nullptr) != (lse == nullptr)) return da::fail(DA_ERR_NULL, "out1 and lse go together");
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = da::dattn_forward_general(pl.a, p->dtype, cs);
+    if (e == cudaSuccess && pl.a.splits > 1) e = da::dattn_merge(pl.a, p->dtype, cs);
+    return e == cudaSuccess ? DA_OK : da::cuda_fail(e, "differential attention launch");
+}
+
+da_status dattn_backward(const dattn_problem *p, const void *out, const void *out1, const float *lse,
+                         const void *grad_out, void *grad_q, void *grad_k, void *grad_v, float *grad_lam,
+                         float *grad_table, void *workspace, size_t workspace_bytes, da_stream_t stream)
+{
+    da::DattnPlan pl{};
+    da_status st = da::dattn_plan(p, true, pl);
+    if (st != DA_OK) return st;
+    da::DattnArgs &a = pl.a;
+    a.out = const_cast<void *>(out);
+    a.out1 = const_cast<void *>(out1);
+    a.lse = const_cast<float *>(lse);
+    a.grad_out = grad_out;
+    a.grad_q = grad_q;
+    a.grad_k = grad_k;
+    a.grad_v = grad_v;
+    a.grad_lam = grad_lam;
+    a.grad_table = grad_table;
+    if ((st = da::dattn_buffers(pl, workspace, workspace_bytes)) != DA_OK) return st;
+    if (static_cast<int64_t>(a.B) * a.rows > 0 && (!out || !out1 || !lse || !grad_out || !grad_q))
+        return da::fail(DA_ERR_NULL, "out, out1, lse, grad_out or grad_q is NULL");
+    if (static_cast<int64_t>(a.B) * a.Lk > 0 && (!grad_k || !grad_v)) return da::fail(DA_ERR_NULL, "grad_k or grad_v is NULL");
+    if (!grad_lam || (a.nb > 0 && !grad_table)) return da::fail(DA_ERR_NULL, "grad_lam or grad_table is NULL");
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (a.B > 0) e = da::dattn_backward_general(a, p->dtype, cs);
+    if (e == cudaSuccess) e = da::dattn_finish_backward(a, cs);
+    return e == cudaSuccess ? DA_OK : da::cuda_fail(e, "differential attention backward launch");
+}
+
+}  // extern "C"

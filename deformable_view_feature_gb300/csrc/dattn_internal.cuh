@@ -1,0 +1,74 @@
+// Declarations shared by the differential-attention translation units
+// (include/dattn.h). Nothing here is exported.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "da_internal.cuh"
+#include "dattn.h"
+
+namespace da {
+
+// The problem as the kernels see it. The G = H / Hkv query heads that share a
+// key head are handled together: a "row" is one (query, head) pair, row r of
+// key head n being query r / G of head n*G + r % G. One token of a serving
+// batch thus still fills a tile with its G heads, and keys are read once for
+// all of them.
+struct DattnArgs {
+    const void *q, *k, *v;
+    int64_t qs[4], ks[4], vs[3];
+    const float *lam, *table;
+    const int32_t *bmap, *pos_q, *pos_k, *lengths;
+    const uint8_t *mask;
+    int32_t B, Lq, Lk, H, Hkv, G, D, Dv, nb, reach, causal;
+    int32_t rows;       // Lq * G
+    FastDiv div_G;
+    float scale;        // of the scores
+    float scale_log2;   // scale * log2(e): scores are kept times log2(e)
+    void *out, *out1;   // forward outputs (backward: inputs)
+    float *lse;         // [B, H, 2, Lq]
+    // Forward split over the keys: `splits` CTAs share a tile of rows, each
+    // leaving its unnormalised sums [.., 2, Dv], and maximum and sum [.., 2, 2].
+    int32_t splits, keys_per_split;
+    float *part_o, *part_ml;
+    // Backward.
+    const void *grad_out;
+    void *grad_q, *grad_k, *grad_v;
+    float *grad_lam, *grad_table;
+    float *delta;       // [B, Hkv, 2, rows] the d_m of dattn.h
+    float *part_table;  // [key-tile CTAs, nb * G]
+    int32_t table_ctas; // key tiles per (b, key head)
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ int dattn_length(const DattnArgs &a, int b)
+{
+    return a.lengths ? min(max(a.lengths[b], 0), a.Lk) : a.Lk;
+}
+
+template <typename T> __device__ __forceinline__ float dattn_float(T v);
+template <> __device__ __forceinline__ float dattn_float(float v) { return v; }
+template <> __device__ __forceinline__ float dattn_float(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float dattn_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T dattn_round(float v);
+template <> __device__ __forceinline__ float dattn_round(float v) { return v; }
+template <> __device__ __forceinline__ __half dattn_round(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 dattn_round(float v) { return __float2bfloat16_rn(v); }
+
+// Launches. `split_for` CTAs per tile of rows were chosen by the plan.
+cudaError_t dattn_forward_general(const DattnArgs &a, int dtype, cudaStream_t st);
+cudaError_t dattn_backward_general(const DattnArgs &a, int dtype, cudaStream_t st);
+cudaError_t dattn_merge(const DattnArgs &a, int dtype, cudaStream_t st);
+cudaError_t dattn_finish_backward(const DattnArgs &a, cudaStream_t st);
+int dattn_general_row_tile(const DattnArgs &a);   // rows of a forward tile
+int dattn_general_key_tile(const DattnArgs &a);   // keys of a backward key tile
+
+}  // namespace da
