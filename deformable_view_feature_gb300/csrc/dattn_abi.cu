@@ -2,10 +2,61 @@
 // validation, the plan (kernels, split over the keys, workspace) and launches.
 #include <cmath>
 
-#include "dattn_internal.cuh"
+#include "dattn_tc.cuh"
 
 namespace da {
+
+da_status tensor_map(CUtensorMap &m, int dtype, const void *base, int width, int maps, int heads, int length, int batch,
+                     int64_t s_map, int64_t s_head, int64_t s_len, int64_t s_batch, int box_width, int box_heads, int box_len)
+{
+    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult r{};
+        return cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+                       r == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<Encode>(f)
+                   : nullptr;
+    }();
+    if (!encode) return fail(DA_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+    const cuuint64_t dims[5] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(maps), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(length), static_cast<cuuint64_t>(batch)};
+    const int64_t s[4] = {s_map, s_head, s_len, s_batch};
+    cuuint64_t strides[4];
+    for (int i = 0; i < 4; ++i)  // the stride of a dimension of one is never used, but is checked
+        strides[i] = dims[i + 1] == 1 ? 16 : static_cast<cuuint64_t>(s[i]) * 2;
+    const cuuint32_t box[5] = {static_cast<cuuint32_t>(box_width), 1, static_cast<cuuint32_t>(box_heads),
+                               static_cast<cuuint32_t>(box_len), 1};
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    const CUresult r = encode(&m, dtype == DA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+                              const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              box_width == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? DA_OK : fail(DA_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", static_cast<int>(r));
+}
+
 namespace {
+
+// The tensor-core kernels' rule. 16-bit types; widths that their tiles hold
+// and whose rows are multiples of 16 bytes; the group of heads within a tile
+// and its expanded bias within 32 KB; and what a TMA box needs: 16-byte
+// aligned addresses and strides, none of them zero.
+bool tensor_serves(const dattn_problem &d)
+{
+    if (d.dtype != DA_BF16 && d.dtype != DA_F16) return false;
+    const int G = d.num_heads / d.num_kv_heads;
+    if (d.width % 8 || d.value_width % 8 || d.width > 64 || d.value_width > 128 || G > 128) return false;
+    if (d.batch < 1 || d.num_queries < 1 || d.num_keys < 1) return false;
+    if (d.num_buckets > 0 && G * (2 * d.reach + 1) > 8192) return false;
+    if (!aligned(d.q, 16) || !aligned(d.k, 16) || !aligned(d.v, 16)) return false;
+    const int nq[4] = {d.batch, d.num_queries, d.num_heads, 2}, nk[4] = {d.batch, d.num_keys, d.num_kv_heads, 2};
+    auto fits = [](int64_t stride, int size) { return size == 1 || (stride > 0 && stride % 8 == 0 && stride < (int64_t{1} << 38)); };
+    for (int i = 0; i < 4; ++i)
+        if (!fits(d.q_stride[i], nq[i]) || !fits(d.k_stride[i], nk[i]) || (i < 3 && !fits(d.v_stride[i], nk[i]))) return false;
+    return true;
+}
 
 struct DattnPlan {
     DattnArgs a;
@@ -88,17 +139,17 @@ da_status dattn_plan(const dattn_problem *pr, bool backward, DattnPlan &p)
     a.scale = d.scale;
     a.scale_log2 = static_cast<float>(static_cast<double>(d.scale) * 1.4426950408889634);
     p.elem = d.dtype == DA_F32 ? 4 : 2;
-    p.tensor = false;
+    p.tensor = tensor_serves(d);
     const int64_t bn = static_cast<int64_t>(a.B) * a.Hkv;
     size_t at = 0;
     a.splits = 1;
     a.keys_per_split = a.Lk > 0 ? a.Lk : 1;
     if (!backward) {
-        const int qt = dattn_general_row_tile(a);
+        const int qt = p.tensor ? 128 / G * G : dattn_general_row_tile(a);
         const int n = split_count(bn * ((rows + qt - 1) / qt), a.Lk);
         if (n > 1) {
             a.keys_per_split = ((a.Lk + n - 1) / n + 63) / 64 * 64;
-            a.splits = (a.Lk + a.keys_per_split - 1) / a.keys_per_split;
+            a.splits = p.tensor ? n : (a.Lk + a.keys_per_split - 1) / a.keys_per_split;
         }
         if (a.splits > 1) {
             p.part_o = at;
@@ -178,7 +229,10 @@ da_status dattn_forward(const dattn_problem *p, void *out, void *out1, float *ls
     if (!out) return da::fail(DA_ERR_NULL, "out is NULL");
     if ((out1 == nullptr) != (lse == nullptr)) return da::fail(DA_ERR_NULL, "out1 and lse go together");
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = da::dattn_forward_general(pl.a, p->dtype, cs);
+    if (pl.tensor) {
+        if ((st = da::dattn_forward_tensor(pl.a, p->dtype, cs)) != DA_OK) return st;
+    }
+    cudaError_t e = pl.tensor ? cudaSuccess : da::dattn_forward_general(pl.a, p->dtype, cs);
     if (e == cudaSuccess && pl.a.splits > 1) e = da::dattn_merge(pl.a, p->dtype, cs);
     return e == cudaSuccess ? DA_OK : da::cuda_fail(e, "differential attention launch");
 }
@@ -210,6 +264,18 @@ da_status dattn_backward(const dattn_problem *p, const void *out, const void *ou
     if (a.B > 0) e = da::dattn_backward_general(a, p->dtype, cs);
     if (e == cudaSuccess) e = da::dattn_finish_backward(a, cs);
     return e == cudaSuccess ? DA_OK : da::cuda_fail(e, "differential attention backward launch");
+}
+
+da_status dattn_device_status(uint32_t *gave_up, da_stream_t stream)
+{
+    if (!gave_up) return da::fail(DA_ERR_NULL, "gave_up is NULL");
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    uint32_t *word = da::dattn_gave_up_word();
+    if (!word) return da::cuda_fail(cudaGetLastError(), "address of the status word");
+    cudaError_t e = cudaMemcpyAsync(gave_up, word, sizeof *word, cudaMemcpyDeviceToHost, cs);
+    if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof *word, cs);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(cs);
+    return e == cudaSuccess ? DA_OK : da::cuda_fail(e, "status word");
 }
 
 }  // extern "C"

@@ -1,0 +1,440 @@
+// Differential attention forward on the tensor cores (include/dattn.h), for
+// bf16 and fp16.
+//
+// One CTA takes 128 rows (queries x the heads that share a key head) and
+// walks over the keys in tiles of 128. The two softmax maps take the place of
+// the two row tiles by which such a kernel usually keeps both of its units
+// busy: while the four warps of map 0 turn scores into weights, the tensor
+// core forms P v and the next scores of map 1, and the other way round; K is
+// loaded once for both scores and V once for both products.
+//
+// Warps: 0-3 softmax of map 0 and 4-7 of map 1 (a thread per row, so row
+// maxima and sums need no exchange), 8 loads by TMA, 9 issues the products,
+// 10 prepares each tile's positions and masks. Tensor memory: scores of each
+// map, 128 columns, whose first 64 then hold the map's weights in 16 bits as
+// the operand of P v, and the two outputs. A thread raises its row's reference
+// maximum, and rescales the row's output, only when a tile exceeds it by more
+// than 2^8: fp32 sums keep their digits and weights up to 256 fit both types.
+#include "dattn_tc.cuh"
+
+namespace da {
+namespace {
+
+using namespace tc;
+
+constexpr int kTile = 128;            // rows, and keys per step
+constexpr int kFwdThreads = 11 * 32;
+constexpr float kSlack = 8.f;         // log2 of how far weights may exceed 1
+
+// What the softmax warps need to know of a tile of keys.
+struct KeyInfo {
+    int pos[kTile];
+    uint32_t valid[4];  // one bit per key
+    int lo, hi;         // smallest and largest position
+    uint32_t all;       // every key is to be used
+    uint32_t pad;
+};
+
+template <int DP, int VP> struct FwdShared {
+    static constexpr int row = DP * 2;                 // bytes of a row of q or k
+    static constexpr int map = kTile * row;            // of one map's tile
+    static constexpr int vblock = kTile * 128;         // of 64 columns of V
+    static constexpr int stage = 2 * map + (VP / 64) * vblock;
+    // As many steps ahead as fit beside the bias table.
+    static constexpr int stages = stage > 49152 ? 2 : stage > 32768 ? 3 : 4;
+    static constexpr int bytes = 2 * map + stages * stage;
+};
+
+struct FwdBars {
+    uint64_t q_full, fin;
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], info[4], v_ready[4];
+    uint64_t s_full[2], p_full[2], o_done[2];
+    uint32_t tmem, gave_up;
+};
+
+// Device word for waits that ran out (dattn_device_status).
+__device__ uint32_t g_gave_up;
+
+template <typename T, int DP, int VP>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    dattn_fwd_tc_kernel(const __grid_constant__ DattnArgs a, const __grid_constant__ CUtensorMap mq,
+                        const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv)
+{
+    using F = FwdShared<DP, VP>;
+    constexpr int NS = F::stages;
+    constexpr bool bf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
+    extern __shared__ unsigned char raw[];
+    unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
+    __shared__ FwdBars bars;
+    __shared__ KeyInfo infos[NS];
+    __shared__ float row_l[2][kTile], row_m[2][kTile];
+    float *table = reinterpret_cast<float *>(base + F::bytes);  // [G][2 reach + 1], times log2(e)
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int LP = kTile / a.G;  // queries of a tile
+    const int tile = blockIdx.x / a.splits, split = blockIdx.x - tile * a.splits;
+    const int n = blockIdx.y, b = blockIdx.z, l0 = tile * LP;
+    const int len = dattn_length(a, b);
+    int end = len;
+    // Keys after the tile's last query end the walk where positions are indices.
+    if (a.causal && !a.pos_q && !a.pos_k) end = min(end, max(len - a.Lq + min(l0 + LP, a.Lq), 0));
+    const int per = ((end + kTile - 1) / kTile + a.splits - 1) / a.splits * kTile;
+    const int jb = split * per;
+    end = min(end, jb + per);
+    const int T_ = end > jb ? (end - jb + kTile - 1) / kTile : 0;
+    const int span = 2 * a.reach + 1;
+
+    if (threadIdx.x == 0) {
+        bar_init(&bars.q_full, 1);
+        bar_init(&bars.fin, 1);
+        for (int s = 0; s < NS; ++s) {
+            bar_init(&bars.k_full[s], 1);
+            bar_init(&bars.k_empty[s], 1);
+            bar_init(&bars.v_full[s], 1);
+            bar_init(&bars.v_empty[s], 1);
+            bar_init(&bars.info[s], 1);
+            bar_init(&bars.v_ready[s], 1);
+        }
+        for (int m = 0; m < 2; ++m) {
+            bar_init(&bars.s_full[m], 1);
+            bar_init(&bars.p_full[m], 4);
+            bar_init(&bars.o_done[m], 1);
+        }
+        bars.gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tma_prefetch(&mq);
+        tma_prefetch(&mk);
+        tma_prefetch(&mv);
+    }
+    if (warp == 9) tmem_alloc(&bars.tmem, 512);
+    if (a.nb)
+        for (int i = threadIdx.x; i < a.G * span; i += kFwdThreads) {
+            const int g = i / span, bucket = min(max(a.bmap[i - g * span], 0), a.nb - 1);
+            table[i] = a.table[bucket * a.H + n * a.G + g] * kLog2e;
+        }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = bars.tmem;
+    volatile uint32_t *gave_up = &bars.gave_up;
+    const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 256 + VP};
+    const uint32_t sq = smem_addr(base), sst = sq + 2 * F::map;
+
+    if (warp == 8) {
+        if (lane == 0 && T_ > 0) {
+            bar_expect(&bars.q_full, 2 * F::row * a.G * LP);
+            for (int m = 0; m < 2; ++m) tma_load(&mq, &bars.q_full, base + m * F::map, 0, m, n * a.G, l0, b);
+            for (int t = 0; t < T_; ++t) {
+                const int s = t % NS;
+                const uint32_t parity = (t / NS) & 1;
+                unsigned char *st = base + 2 * F::map + s * F::stage;
+                bar_wait(&bars.k_empty[s], parity ^ 1, gave_up);
+                bar_expect(&bars.k_full[s], 2 * F::map);
+                for (int m = 0; m < 2; ++m) tma_load(&mk, &bars.k_full[s], st + m * F::map, 0, m, n, jb + t * kTile, b);
+                bar_wait(&bars.v_empty[s], parity ^ 1, gave_up);
+                bar_expect(&bars.v_full[s], (VP / 64) * F::vblock);
+                for (int c = 0; c < VP / 64; ++c)
+                    tma_load(&mv, &bars.v_full[s], st + 2 * F::map + c * F::vblock, c * 64, 0, n, jb + t * kTile, b);
+            }
+            if (*gave_up) {  // leave no copy in flight
+                bar_drain(&bars.q_full, 0);
+                for (int t = max(0, T_ - NS); t < T_; ++t) {
+                    bar_drain(&bars.k_full[t % NS], (t / NS) & 1);
+                    bar_drain(&bars.v_full[t % NS], (t / NS) & 1);
+                }
+            }
+        }
+    } else if (warp == 9) {
+        if (lane == 0 && T_ > 0) {
+            constexpr uint32_t iqk = shape(bf16, kTile, false), ipv = shape(bf16, VP, true);
+            auto scores = [&](int m, int t) {
+                const uint32_t k = sst + (t % NS) * F::stage + m * F::map;
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i)
+                    mma_ss(tS[m], along_row<F::row>(sq + m * F::map, i), along_row<F::row>(k, i), iqk, i > 0);
+                mma_commit(&bars.s_full[m]);
+            };
+            bar_wait(&bars.q_full, 0, gave_up);
+            bar_wait(&bars.k_full[0], 0, gave_up);
+            fence_after();
+            scores(0, 0);
+            scores(1, 0);
+            mma_commit(&bars.k_empty[0]);
+            for (int t = 0; t < T_; ++t) {
+                const int s = t % NS;
+                const uint32_t v = sst + s * F::stage + 2 * F::map;
+                bar_wait(&bars.v_full[s], (t / NS) & 1, gave_up);
+                bar_wait(&bars.v_ready[s], (t / NS) & 1, gave_up);
+                for (int m = 0; m < 2; ++m) {
+                    bar_wait(&bars.p_full[m], t & 1, gave_up);
+                    fence_after();
+#pragma unroll
+                    for (int i = 0; i < kTile / 16; ++i)
+                        mma_ts(tO[m], tS[m] + i * 8, over_rows<128>(v, i, F::vblock), ipv, t > 0 || i > 0);
+                    mma_commit(&bars.o_done[m]);
+                    if (t + 1 < T_) {
+                        if (m == 0) bar_wait(&bars.k_full[(t + 1) % NS], ((t + 1) / NS) & 1, gave_up);
+                        scores(m, t + 1);  // after P v, which reads its weights from these columns
+                    }
+                }
+                mma_commit(&bars.v_empty[s]);
+                if (t + 1 < T_) mma_commit(&bars.k_empty[(t + 1) % NS]);
+            }
+            mma_commit(&bars.fin);
+            bar_drain(&bars.fin, 0);
+        }
+    } else if (warp == 10) {
+        for (int t = 0; t < T_; ++t) {
+            const int s = t % NS, j0 = jb + t * kTile;
+            KeyInfo &ki = infos[s];
+            // The slot is free once P v of NS steps ago is done: the softmax
+            // warps had by then read its infos, and the products its V.
+            bar_wait_warp(&bars.v_empty[s], ((t / NS) & 1) ^ 1, gave_up);
+            int lo = INT32_MAX, hi = INT32_MIN;
+            uint32_t every = 0xffffffffu, stale = 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int j = j0 + c * 32 + lane;
+                const bool in = j < end;
+                const int64_t at = static_cast<int64_t>(b) * a.Lk + j;
+                const bool use = in && (!a.mask || a.mask[at]);
+                const int pos = in && a.pos_k ? a.pos_k[at] : j;
+                ki.pos[c * 32 + lane] = pos;
+                const uint32_t bits = __ballot_sync(0xffffffffu, use);
+                // Unused keys inside the tensor; past its end TMA wrote zeros.
+                const uint32_t bad = __ballot_sync(0xffffffffu, !use && j < a.Lk);
+                every &= bits;
+                stale |= bad;
+                if (lane == 0) ki.valid[c] = bits;
+                if (use) {
+                    lo = min(lo, pos);
+                    hi = max(hi, pos);
+                }
+            }
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            if (lane == 0) {
+                ki.lo = lo;
+                ki.hi = hi;
+                ki.all = every == 0xffffffffu;
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bars.info[s]);
+            if (stale) {  // 0 * NaN is NaN: the rows of V of unused keys become zeros
+                bar_wait_warp(&bars.v_full[s], (t / NS) & 1, gave_up);
+                unsigned char *v = base + 2 * F::map + s * F::stage + 2 * F::map;
+                for (int r = lane >> 3; r < kTile; r += 4)
+                    if (!(ki.valid[r >> 5] >> (r & 31) & 1))
+                        for (int c = 0; c < VP / 64; ++c)
+                            *reinterpret_cast<uint4 *>(v + c * F::vblock + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                fence_async();
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bars.v_ready[s]);
+        }
+    } else {
+        const int m = warp >> 2, rl = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int dl = static_cast<int>(a.div_G.div(rl)), g = rl - dl * a.G, l = l0 + dl;
+        const bool live = rl < LP * a.G && l < a.Lq;
+        const int pos = !live ? 0 : a.pos_q ? a.pos_q[static_cast<int64_t>(b) * a.Lq + l] : len - a.Lq + l;
+        const float *tb = table + g * span + a.reach;  // a row past the tile's heads still reads inside the table
+        float ref = -INFINITY;
+        float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+        for (int t = 0; t < T_; ++t) {
+            const KeyInfo &ki = infos[t % NS];
+            bar_wait_warp(&bars.info[t % NS], (t / NS) & 1, gave_up);
+            const int rlo = ki.lo - pos, rhi = ki.hi - pos;
+            // One bias for the row's whole tile, and nothing hidden.
+            const bool even = !live || (ki.all && !(a.causal && rhi > 0) &&
+                                        (a.nb == 0 || rlo >= a.reach || rhi <= -a.reach || rlo == rhi));
+            const bool fast = __all_sync(0xffffffffu, even) && a.scale_log2 >= 0.f;
+            bar_wait_warp(&bars.s_full[m], t & 1, gave_up);
+            fence_after();
+            float s[kTile];
+            tmem_load(tS[m] + lanes, s);
+            float mul = a.scale_log2, add = 0.f;
+            if (fast) {
+                if (a.nb) add = tb[min(max(rlo, -a.reach), a.reach)];
+            } else {
+                const float mul_all = a.scale_log2;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t valid = ki.valid[c];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int rel = ki.pos[c * 32 + i] - pos;
+                        float x = s[c * 32 + i] * mul_all;
+                        if (a.nb) x += tb[min(max(rel, -a.reach), a.reach)];
+                        s[c * 32 + i] = (valid >> i & 1) && !(a.causal && rel > 0) ? x : -INFINITY;
+                    }
+                }
+                mul = 1.f;
+            }
+            float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int i = 4; i < kTile - 4; i += 8)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) top[c] = max3(top[c], s[i + c], s[i + 4 + c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], s[kTile - 4 + c]);
+            const float best = fmaf(max3(fmaxf(top[0], top[1]), top[2], top[3]), mul, add);
+            // Each row by its own scores alone, so that its roundings do not
+            // depend on its neighbours'; rows past the end hold stale values.
+            const bool raise = live && best > ref + kSlack;
+            if (__any_sync(0xffffffffu, raise)) {
+                const float next = raise ? best : ref;
+                const float shrink = raise ? ex2(ref - next) : 1.f;
+                ref = next;
+                const float2 sh = {shrink, shrink};
+                sum[0] = mul2(sum[0], sh);
+                sum[1] = mul2(sum[1], sh);
+                if (t > 0) {
+                    bar_wait_warp(&bars.o_done[m], (t - 1) & 1, gave_up);
+                    fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < VP; c += 32) {
+                        float o[32];
+                        tmem_load(tO[m] + lanes + c, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] *= shrink;
+                        tmem_store(tO[m] + lanes + c, o);
+                    }
+                }
+            }
+            const float off = add - (ref == -INFINITY ? 0.f : ref);
+            const float2 mul_2 = {mul, mul}, off_2 = {off, off};
+            uint32_t p[kTile / 2];
+#pragma unroll
+            for (int i = 0; i < kTile / 2; ++i) {
+                float2 x = fma2({s[2 * i], s[2 * i + 1]}, mul_2, off_2);
+                x.x = ex2(x.x);
+                x.y = ex2(x.y);
+                sum[i & 1] = add2(sum[i & 1], x);
+                p[i] = pack2<T>(x.x, x.y);
+            }
+            tmem_store(tS[m] + lanes, p);
+            tmem_store_wait();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bars.p_full[m]);
+        }
+        row_l[m][rl] = sum[0].x + sum[0].y + (sum[1].x + sum[1].y);
+        row_m[m][rl] = ref;
+        if (T_ > 0)
+            for (int i = 0; i < 2; ++i) bar_wait_warp(&bars.o_done[i], (T_ - 1) & 1, gave_up);
+        fence_after();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float s0 = row_l[0][rl], s1 = row_l[1][rl];
+        const float w0 = s0 == 0.f ? 0.f : 1.f / s0, w1 = s1 == 0.f ? 0.f : 1.f / s1;
+        const int h = n * a.G + (live ? g : 0);
+        const float nan = *gave_up ? NAN : 0.f;
+        const float lam = a.lam[h] + nan;
+        const int64_t at = ((static_cast<int64_t>(b) * a.Lq + l) * a.H + h) * a.Dv;
+        const int64_t pt = ((static_cast<int64_t>(b) * a.Hkv + n) * a.rows + static_cast<int64_t>(l) * a.G + g) * a.splits + split;
+        const bool wide = aligned16(a.out) && aligned16(a.out1);
+        // The warps of map m write the m-th half of the columns.
+#pragma unroll 1
+        for (int c = m * (VP / 2); c < (m + 1) * (VP / 2); c += 32) {
+            float x[32], y[32];
+            __syncwarp();
+            if (T_ > 0) {
+                tmem_load(tO[0] + lanes + c, x);
+                tmem_load(tO[1] + lanes + c, y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = y[i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                if (!live || c + i >= a.Dv) continue;
+                if (a.splits > 1) {
+                    float *o = a.part_o + pt * 2 * a.Dv + c + i;
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {
+                        *reinterpret_cast<float4 *>(o + e) = make_float4(x[i + e], x[i + e + 1], x[i + e + 2], x[i + e + 3]);
+                        *reinterpret_cast<float4 *>(o + a.Dv + e) = make_float4(y[i + e], y[i + e + 1], y[i + e + 2], y[i + e + 3]);
+                    }
+                    continue;
+                }
+                uint32_t u[4], w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float y0 = y[i + 2 * e] * w1, y1 = y[i + 2 * e + 1] * w1;
+                    u[e] = pack2<T>(fmaf(-lam, y0, x[i + 2 * e] * w0), fmaf(-lam, y1, x[i + 2 * e + 1] * w0));
+                    w[e] = pack2<T>(y0 + nan, y1 + nan);
+                }
+                T *o = static_cast<T *>(a.out) + at + c + i, *o1 = static_cast<T *>(a.out1) + at + c + i;
+                if (wide) {
+                    *reinterpret_cast<uint4 *>(o) = make_uint4(u[0], u[1], u[2], u[3]);
+                    if (a.out1) *reinterpret_cast<uint4 *>(o1) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        o[e] = reinterpret_cast<const T *>(u)[e];
+                        if (a.out1) o1[e] = reinterpret_cast<const T *>(w)[e];
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        if (live) {
+            const float s = row_l[m][rl];
+            if (a.splits > 1) {
+                a.part_ml[(pt * 2 + m) * 2] = ref;
+                a.part_ml[(pt * 2 + m) * 2 + 1] = s + nan;
+            } else if (a.lse) {
+                a.lse[((static_cast<int64_t>(b) * a.H + h) * 2 + m) * a.Lq + l] = s == 0.f ? INFINITY : ref + log2f(s);
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        fence_after();
+        tmem_free(tmem, 512);
+    }
+    if (threadIdx.x == 0 && *gave_up) atomicOr(&g_gave_up, 1u);
+}
+
+template <typename T, int DP, int VP>
+cudaError_t launch_fwd(const DattnArgs &a, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st)
+{
+    using F = FwdShared<DP, VP>;
+    const size_t smem = F::bytes + 1024 + sizeof(float) * (a.nb ? a.G * (2 * a.reach + 1) : 0);
+    const auto kernel = dattn_fwd_tc_kernel<T, DP, VP>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int LP = kTile / a.G;
+    const dim3 grid(static_cast<unsigned>((a.Lq + LP - 1) / LP * a.splits), a.Hkv, a.B);
+    kernel<<<grid, kFwdThreads, smem, st>>>(a, mq, mk, mv);
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t fwd_widths(const DattnArgs &a, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st)
+{
+    if (a.D <= 32) return a.Dv <= 64 ? launch_fwd<T, 32, 64>(a, mq, mk, mv, st) : launch_fwd<T, 32, 128>(a, mq, mk, mv, st);
+    return a.Dv <= 64 ? launch_fwd<T, 64, 64>(a, mq, mk, mv, st) : launch_fwd<T, 64, 128>(a, mq, mk, mv, st);
+}
+
+}  // namespace
+
+uint32_t *dattn_gave_up_word()
+{
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_gave_up) == cudaSuccess ? static_cast<uint32_t *>(p) : nullptr;
+}
+
+da_status dattn_forward_tensor(const DattnArgs &a, int dtype, cudaStream_t st)
+{
+    const int wide = a.D <= 32 ? 32 : 64, LP = kTile / a.G;
+    CUtensorMap mq, mk, mv;
+    da_status e = tensor_map(mq, dtype, a.q, a.D, 2, a.H, a.Lq, a.B, a.qs[3], a.qs[2], a.qs[1], a.qs[0], wide, a.G, LP);
+    if (e == DA_OK) e = tensor_map(mk, dtype, a.k, a.D, 2, a.Hkv, a.Lk, a.B, a.ks[3], a.ks[2], a.ks[1], a.ks[0], wide, 1, kTile);
+    if (e == DA_OK) e = tensor_map(mv, dtype, a.v, a.Dv, 1, a.Hkv, a.Lk, a.B, 0, a.vs[2], a.vs[1], a.vs[0], 64, 1, kTile);
+    if (e != DA_OK) return e;
+    const cudaError_t c = dtype == DA_BF16 ? fwd_widths<__nv_bfloat16>(a, mq, mk, mv, st) : fwd_widths<__half>(a, mq, mk, mv, st);
+    return c == cudaSuccess ? DA_OK : cuda_fail(c, "differential attention launch");
+}
+
+}  // namespace da

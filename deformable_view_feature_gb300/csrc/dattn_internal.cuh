@@ -63,7 +63,8 @@ template <> __device__ __forceinline__ float dattn_round(float v) { return v; }
 template <> __device__ __forceinline__ __half dattn_round(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 dattn_round(float v) { return __float2bfloat16_rn(v); }
 
-// Launches. `split_for` CTAs per tile of rows were chosen by the plan.
+da_status dattn_forward_tensor(const DattnArgs &a, int dtype, cudaStream_t st);
+uint32_t *dattn_gave_up_word();
 cudaError_t dattn_forward_general(const DattnArgs &a, int dtype, cudaStream_t st);
 cudaError_t dattn_backward_general(const DattnArgs &a, int dtype, cudaStream_t st);
 cudaError_t dattn_merge(const DattnArgs &a, int dtype, cudaStream_t st);

@@ -113,6 +113,14 @@ da_status dattn_backward(const dattn_problem *p, const void *out, const void *ou
                          const void *grad_out, void *grad_q, void *grad_k, void *grad_v, float *grad_lam,
                          float *grad_table, void *workspace, size_t workspace_bytes, da_stream_t stream);
 
+/*
+ * The kernels' waits on their own copies and products end after a bounded
+ * number of tries. A wait that ran out (none does in a sound run) sets a word
+ * on the device and turns the call's outputs into NaN. This call waits for
+ * `stream`, reads the word into *gave_up (host) and clears it.
+ */
+da_status dattn_device_status(uint32_t *gave_up, da_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
