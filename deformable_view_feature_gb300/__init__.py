@@ -111,7 +111,7 @@ def load_library():
     lib.gn_workspace_size.argtypes = [vp, vp, vp, ctypes.c_int32, psize]
     lib.gn_forward.argtypes = [vp] * 9 + [ctypes.c_size_t, vp]
     lib.gn_backward.argtypes = [vp] * 12 + [ctypes.c_size_t, vp]
-    lib.dattn_path.argtypes = [vp]
+    lib.dattn_path.argtypes = [vp, ctypes.c_int32]
     lib.dattn_workspace_size.argtypes = [vp, ctypes.c_int32, psize]
     lib.dattn_forward.argtypes = [vp] * 5 + [ctypes.c_size_t, vp]
     lib.dattn_backward.argtypes = [vp] * 11 + [ctypes.c_size_t, vp]

@@ -129,10 +129,10 @@ def _scratch(lib, p, backward, device):
     return torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None, n.value
 
 
-def dattn_path(q, k, v, lam, **options) -> str:
-    """Which kernels dattn_forward and dattn_backward take for these
+def dattn_path(q, k, v, lam, backward: bool = False, **options) -> str:
+    """Which kernels dattn_forward (or dattn_backward) takes for these
     arguments: "tensor" (the tensor cores) or "general" (fp32 units)."""
-    r = load_library().dattn_path(ctypes.byref(_options(q, k, v, lam, **options)))
+    r = load_library().dattn_path(ctypes.byref(_options(q, k, v, lam, **options)), int(backward))
     if r < 0:
         raise DaError(4, load_library().da_last_error().decode(errors="replace"))
     return "tensor" if r == 1 else "general"

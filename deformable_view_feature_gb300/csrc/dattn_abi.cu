@@ -43,13 +43,16 @@ namespace {
 // and whose rows are multiples of 16 bytes; the group of heads within a tile
 // and its expanded bias within 32 KB; and what a TMA box needs: 16-byte
 // aligned addresses and strides, none of them zero.
-bool tensor_serves(const dattn_problem &d)
+// The backward kernels' shared memory leaves room for half of that bias, and
+// for sums of at most 32 buckets.
+bool tensor_serves(const dattn_problem &d, bool backward)
 {
     if (d.dtype != DA_BF16 && d.dtype != DA_F16) return false;
     const int G = d.num_heads / d.num_kv_heads;
     if (d.width % 8 || d.value_width % 8 || d.width > 64 || d.value_width > 128 || G > 128) return false;
     if (d.batch < 1 || d.num_queries < 1 || d.num_keys < 1) return false;
-    if (d.num_buckets > 0 && G * (2 * d.reach + 1) > 8192) return false;
+    if (d.num_buckets > 0 && G * (2 * d.reach + 1) > (backward ? 4096 : 8192)) return false;
+    if (backward && d.num_buckets > 32) return false;
     if (!aligned(d.q, 16) || !aligned(d.k, 16) || !aligned(d.v, 16)) return false;
     const int nq[4] = {d.batch, d.num_queries, d.num_heads, 2}, nk[4] = {d.batch, d.num_keys, d.num_kv_heads, 2};
     auto fits = [](int64_t stride, int size) { return size == 1 || (stride > 0 && stride % 8 == 0 && stride < (int64_t{1} << 38)); };
@@ -139,7 +142,7 @@ da_status dattn_plan(const dattn_problem *pr, bool backward, DattnPlan &p)
     a.scale = d.scale;
     a.scale_log2 = static_cast<float>(static_cast<double>(d.scale) * 1.4426950408889634);
     p.elem = d.dtype == DA_F32 ? 4 : 2;
-    p.tensor = tensor_serves(d);
+    p.tensor = tensor_serves(d, backward);
     const int64_t bn = static_cast<int64_t>(a.B) * a.Hkv;
     size_t at = 0;
     a.splits = 1;
@@ -158,6 +161,8 @@ da_status dattn_plan(const dattn_problem *pr, bool backward, DattnPlan &p)
             at += round256(sizeof(float) * bn * rows * a.splits * 4);
         }
     } else {
+        // Sized for the general kernels too, which take over where grad_out
+        // turns out not to be aligned.
         const int kt = dattn_general_key_tile(a);
         a.table_ctas = (a.Lk + kt - 1) / kt;
         p.delta = at;
@@ -200,10 +205,10 @@ da_status dattn_buffers(DattnPlan &p, void *ws, size_t ws_bytes)
 
 extern "C" {
 
-int32_t dattn_path(const dattn_problem *p)
+int32_t dattn_path(const dattn_problem *p, int32_t backward)
 {
     da::DattnPlan pl{};
-    return da::dattn_plan(p, false, pl) == DA_OK ? static_cast<int32_t>(pl.tensor) : -1;
+    return da::dattn_plan(p, backward != 0, pl) == DA_OK ? static_cast<int32_t>(pl.tensor) : -1;
 }
 
 da_status dattn_workspace_size(const dattn_problem *p, int32_t backward, size_t *bytes)
@@ -261,7 +266,12 @@ da_status dattn_backward(const dattn_problem *p, const void *out, const void *ou
     if (!grad_lam || (a.nb > 0 && !grad_table)) return da::fail(DA_ERR_NULL, "grad_lam or grad_table is NULL");
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    if (a.B > 0) e = da::dattn_backward_general(a, p->dtype, cs);
+    if (pl.tensor && da::aligned(grad_out, 16) && da::aligned(out, 16) && da::aligned(out1, 16)) {
+        a.table_ctas = (a.Lk + 127) / 128;
+        if ((st = da::dattn_backward_tensor(a, p->dtype, cs)) != DA_OK) return st;
+    } else if (a.B > 0) {
+        e = da::dattn_backward_general(a, p->dtype, cs);
+    }
     if (e == cudaSuccess) e = da::dattn_finish_backward(a, cs);
     return e == cudaSuccess ? DA_OK : da::cuda_fail(e, "differential attention backward launch");
 }
@@ -270,11 +280,15 @@ da_status dattn_device_status(uint32_t *gave_up, da_stream_t stream)
 {
     if (!gave_up) return da::fail(DA_ERR_NULL, "gave_up is NULL");
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    uint32_t *word = da::dattn_gave_up_word();
-    if (!word) return da::cuda_fail(cudaGetLastError(), "address of the status word");
-    cudaError_t e = cudaMemcpyAsync(gave_up, word, sizeof *word, cudaMemcpyDeviceToHost, cs);
-    if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof *word, cs);
+    uint32_t *words[2] = {da::dattn_gave_up_word(), da::dattn_gave_up_backward_word()}, got[2] = {0, 0};
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+        if (!words[i]) return da::cuda_fail(cudaGetLastError(), "address of a status word");
+        e = cudaMemcpyAsync(&got[i], words[i], sizeof got[i], cudaMemcpyDeviceToHost, cs);
+        if (e == cudaSuccess) e = cudaMemsetAsync(words[i], 0, sizeof got[i], cs);
+    }
     if (e == cudaSuccess) e = cudaStreamSynchronize(cs);
+    *gave_up = got[0] | got[1];
     return e == cudaSuccess ? DA_OK : da::cuda_fail(e, "status word");
 }
 

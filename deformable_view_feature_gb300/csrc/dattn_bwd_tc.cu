@@ -1,0 +1,818 @@
+// Differential attention backward on the tensor cores (include/dattn.h), for
+// bf16 and fp16.
+//
+// Two kernels, each of which forms the scores again from q, k and the saved
+// log-sums. The first owns 128 rows and walks over the keys in tiles of 64:
+// grad_q, and the d_m in full fp32 precision. The second owns 128 keys and
+// walks over the queries of every head that shares them in tiles of 64:
+// grad_k, grad_v and the bias table's gradient. Forming e and the scores twice
+// costs 28 D products per pair in place of 20 D, but no sum then crosses CTAs:
+// no fp32 image of grad_q, no atomics, the same bits in every run.
+//
+// Since e = g v^T serves both maps, and P_0 - lam P_1 is formed before its
+// product with g, a pair costs three products forward and three (grad_k twice,
+// grad_v) or two (grad_q twice) back. All products sum in tensor memory; the
+// weights and s_m go through shared memory as 16-bit operands.
+//
+// Warps: 0-7 compute (two threads per row or key, each with half of a tile's
+// 64 columns of both maps), 8 loads by TMA, 9 issues the products, 10 prepares
+// positions, masks and per-query values. The scores of step t+1 are formed as
+// soon as the compute warps hold those of step t in registers.
+#include "dattn_tc.cuh"
+
+namespace da {
+namespace {
+
+using namespace tc;
+
+constexpr int kOwn = 128;   // rows or keys that a CTA owns
+constexpr int kStep = 64;   // keys or queries of a step
+constexpr int kBwdThreads = 11 * 32;
+constexpr int kBlock = 128; // bytes of a row of 64 columns
+
+__device__ uint32_t g_gave_up_backward;
+
+template <typename T> constexpr bool is_bf16 = !std::is_same<T, __half>::value;
+
+// 32 columns of one row of a [128][64] operand of 16 bits, swizzled as TMA
+// would: 16-byte piece i of row r lies at piece i ^ (r % 8).
+__device__ __forceinline__ void store_operand(unsigned char *tile, int row, int half, const uint32_t (&p)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4 *>(tile + row * kBlock + (((half * 4 + i) ^ (row & 7)) << 4)) =
+            make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+}
+
+// Zeroes row r of a tile whose rows have `bytes` bytes, by 8 lanes.
+__device__ __forceinline__ void zero_row(unsigned char *tile, int row, int bytes, int lane8)
+{
+    if (lane8 * 16 < bytes) *reinterpret_cast<uint4 *>(tile + row * bytes + lane8 * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// A row of 32 values times `f`, rounded, `count` of them from column c.
+template <typename T> __device__ __forceinline__ void store_row(T *dst, const float (&x)[32], float f, int count, bool wide)
+{
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+        if (i >= count) continue;
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = pack2<T>(x[i + 2 * e] * f, x[i + 2 * e + 1] * f);
+        if (wide) {
+            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[i + e] = reinterpret_cast<const T *>(u)[e];
+        }
+    }
+}
+
+// ---- grad_q ----------------------------------------------------------------
+
+template <int DP, int VP> struct GradQShared {
+    static constexpr int row = DP * 2;
+    static constexpr int q = kOwn * row, g = kOwn * kBlock;       // one map, one block of 64 columns
+    static constexpr int k = kStep * row, v = kStep * kBlock;
+    static constexpr int stage = 2 * k + (VP / 64) * v;
+    static constexpr int stages = stage > 16384 ? 3 : 4;
+    static constexpr int s = kOwn * kBlock;                       // s_m as an operand
+    static constexpr int at_g = 2 * q, at_stage = at_g + (VP / 64) * g, at_s = at_stage + stages * stage,
+                         bytes = at_s + 2 * s;
+};
+
+struct QKeyInfo {
+    int pos[kStep];
+    uint32_t valid[2];
+    int lo, hi;
+    uint32_t all, pad[3];
+};
+
+struct QBars {
+    uint64_t q_full, fin, s_full[2], ds_full, ds_free;
+    uint64_t kv_full[4], kv_empty[4], info[4], ready[4];
+    uint32_t tmem, gave_up;
+};
+
+template <typename T, int DP, int VP>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    dattn_grad_q_tc_kernel(const __grid_constant__ DattnArgs a, const __grid_constant__ CUtensorMap mq,
+                           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                           const __grid_constant__ CUtensorMap mg)
+{
+    using F = GradQShared<DP, VP>;
+    constexpr int NS = F::stages;
+    extern __shared__ unsigned char raw[];
+    unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
+    __shared__ QBars bars;
+    __shared__ QKeyInfo infos[NS];
+    __shared__ float part[2][2][kOwn];
+    float *table = reinterpret_cast<float *>(base + F::bytes);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int LP = kOwn / a.G;
+    const int n = blockIdx.y, b = blockIdx.z, l0 = blockIdx.x * LP;
+    const int len = dattn_length(a, b);
+    int end = len;
+    if (a.causal && !a.pos_q && !a.pos_k) end = min(end, max(len - a.Lq + min(l0 + LP, a.Lq), 0));
+    const int T_ = (end + kStep - 1) / kStep;
+    const int span = 2 * a.reach + 1;
+
+    if (threadIdx.x == 0) {
+        bar_init(&bars.q_full, 1);
+        bar_init(&bars.fin, 1);
+        bar_init(&bars.s_full[0], 1);
+        bar_init(&bars.s_full[1], 1);
+        bar_init(&bars.ds_full, 8);
+        bar_init(&bars.ds_free, 1);
+        for (int s = 0; s < NS; ++s) {
+            bar_init(&bars.kv_full[s], 1);
+            bar_init(&bars.kv_empty[s], 1);
+            bar_init(&bars.info[s], 1);
+            bar_init(&bars.ready[s], 1);
+        }
+        bars.gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tma_prefetch(&mq);
+        tma_prefetch(&mk);
+        tma_prefetch(&mv);
+        tma_prefetch(&mg);
+    }
+    if (warp == 9) tmem_alloc(&bars.tmem, 512);
+    if (a.nb)
+        for (int i = threadIdx.x; i < a.G * span; i += kBwdThreads) {
+            const int g = i / span, bucket = min(max(a.bmap[i - g * span], 0), a.nb - 1);
+            table[i] = a.table[bucket * a.H + n * a.G + g] * kLog2e;
+        }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = bars.tmem;
+    volatile uint32_t *gave_up = &bars.gave_up;
+    // Scores and e of two steps, 64 columns each, then grad_q of each map.
+    auto tS = [&](int buf, int which) { return tmem + buf * 192 + which * 64; };
+    auto tQ = [&](int m) { return tmem + 384 + m * DP; };
+    const uint32_t sbase = smem_addr(base);
+
+    if (warp == 8) {
+        if (lane == 0 && T_ > 0) {
+            bar_expect(&bars.q_full, 2 * F::row * a.G * LP + (VP / 64) * kBlock * a.G * LP);
+            for (int m = 0; m < 2; ++m) tma_load(&mq, &bars.q_full, base + m * F::q, 0, m, n * a.G, l0, b);
+            for (int c = 0; c < VP / 64; ++c) tma_load(&mg, &bars.q_full, base + F::at_g + c * F::g, c * 64, 0, n * a.G, l0, b);
+            for (int t = 0; t < T_; ++t) {
+                const int s = t % NS;
+                unsigned char *st = base + F::at_stage + s * F::stage;
+                bar_wait(&bars.kv_empty[s], ((t / NS) & 1) ^ 1, gave_up);
+                bar_expect(&bars.kv_full[s], F::stage);
+                for (int m = 0; m < 2; ++m) tma_load(&mk, &bars.kv_full[s], st + m * F::k, 0, m, n, t * kStep, b);
+                for (int c = 0; c < VP / 64; ++c)
+                    tma_load(&mv, &bars.kv_full[s], st + 2 * F::k + c * F::v, c * 64, 0, n, t * kStep, b);
+            }
+            if (*gave_up) {
+                bar_drain(&bars.q_full, 0);
+                for (int t = max(0, T_ - NS); t < T_; ++t) bar_drain(&bars.kv_full[t % NS], (t / NS) & 1);
+            }
+        }
+    } else if (warp == 9) {
+        if (lane == 0 && T_ > 0) {
+            constexpr uint32_t is = shape(is_bf16<T>, kStep, false), iq = shape(is_bf16<T>, DP, true);
+            auto scores = [&](int t) {
+                const uint32_t st = sbase + F::at_stage + (t % NS) * F::stage;
+                bar_wait(&bars.kv_full[t % NS], (t / NS) & 1, gave_up);
+                bar_wait(&bars.ready[t % NS], (t / NS) & 1, gave_up);
+                fence_after();
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < DP / 16; ++i)
+                        mma_ss(tS(t & 1, m), along_row<F::row>(sbase + m * F::q, i), along_row<F::row>(st + m * F::k, i), is, i > 0);
+#pragma unroll
+                for (int i = 0; i < VP / 16; ++i)
+                    mma_ss(tS(t & 1, 2), along_row<128>(sbase + F::at_g + (i / 4) * F::g, i % 4),
+                           along_row<128>(st + 2 * F::k + (i / 4) * F::v, i % 4), is, i > 0);
+                mma_commit(&bars.s_full[t & 1]);
+            };
+            bar_wait(&bars.q_full, 0, gave_up);
+            scores(0);
+            for (int t = 0; t < T_; ++t) {
+                if (t + 1 < T_) scores(t + 1);  // its columns were read by the end of step t - 1
+                bar_wait(&bars.ds_full, t & 1, gave_up);
+                fence_after();
+                const uint32_t st = sbase + F::at_stage + (t % NS) * F::stage;
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < kStep / 16; ++i)
+                        mma_ss(tQ(m), along_row<128>(sbase + F::at_s + m * F::s, i), over_rows<F::row>(st + m * F::k, i, F::k), iq,
+                               t > 0 || i > 0);
+                mma_commit(&bars.ds_free);
+                mma_commit(&bars.kv_empty[t % NS]);
+            }
+            mma_commit(&bars.fin);
+            bar_drain(&bars.fin, 0);
+        }
+    } else if (warp == 10) {
+        for (int t = 0; t < T_; ++t) {
+            const int s = t % NS, j0 = t * kStep;
+            QKeyInfo &ki = infos[s];
+            bar_wait_warp(&bars.kv_empty[s], ((t / NS) & 1) ^ 1, gave_up);
+            int lo = INT32_MAX, hi = INT32_MIN;
+            uint32_t every = 0xffffffffu, stale = 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int j = j0 + c * 32 + lane;
+                const bool in = j < end;
+                const int64_t at = static_cast<int64_t>(b) * a.Lk + j;
+                const bool use = in && (!a.mask || a.mask[at]);
+                const int pos = in && a.pos_k ? a.pos_k[at] : j;
+                ki.pos[c * 32 + lane] = pos;
+                const uint32_t bits = __ballot_sync(0xffffffffu, use);
+                every &= bits;
+                stale |= __ballot_sync(0xffffffffu, !use && j < a.Lk);
+                if (lane == 0) ki.valid[c] = bits;
+                if (use) {
+                    lo = min(lo, pos);
+                    hi = max(hi, pos);
+                }
+            }
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            if (lane == 0) {
+                ki.lo = lo;
+                ki.hi = hi;
+                ki.all = every == 0xffffffffu;
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bars.info[s]);
+            if (stale) {  // unused keys: 0 * NaN in s k would be NaN
+                bar_wait_warp(&bars.kv_full[s], (t / NS) & 1, gave_up);
+                unsigned char *st = base + F::at_stage + s * F::stage;
+                for (int r = lane >> 3; r < kStep; r += 4)
+                    if (!(ki.valid[r >> 5] >> (r & 31) & 1))
+                        for (int m = 0; m < 2; ++m) zero_row(st + m * F::k, r, F::row, lane & 7);
+                fence_async();
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bars.ready[s]);
+        }
+    } else {
+        const int half = warp >> 2, rl = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int dl = static_cast<int>(a.div_G.div(rl)), g = rl - dl * a.G, l = l0 + dl;
+        const bool live = rl < LP * a.G && l < a.Lq;
+        const int h = n * a.G + (live ? g : 0);
+        const int pos = !live ? 0 : a.pos_q ? a.pos_q[static_cast<int64_t>(b) * a.Lq + l] : len - a.Lq + l;
+        const float *tb = table + g * span + a.reach;
+        const float lam = a.lam[h], nlam = -lam;
+        float lse[2] = {INFINITY, INFINITY}, d[2] = {0.f, 0.f};
+        if (live) {
+            const int64_t at = ((static_cast<int64_t>(b) * a.Lq + l) * a.H + h) * a.Dv;
+            const T *pg = static_cast<const T *>(a.grad_out) + at, *po = static_cast<const T *>(a.out) + at,
+                    *p1 = static_cast<const T *>(a.out1) + at;
+            for (int c = half * 8; c < a.Dv; c += 16) {
+                const uint4 ug = *reinterpret_cast<const uint4 *>(pg + c), uo = *reinterpret_cast<const uint4 *>(po + c),
+                            u1 = *reinterpret_cast<const uint4 *>(p1 + c);
+                const T *vg = reinterpret_cast<const T *>(&ug), *vo = reinterpret_cast<const T *>(&uo), *v1 = reinterpret_cast<const T *>(&u1);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    d[0] = fmaf(dattn_float(vg[e]), dattn_float(vo[e]), d[0]);
+                    d[1] = fmaf(dattn_float(vg[e]), dattn_float(v1[e]), d[1]);
+                }
+            }
+            for (int m = 0; m < 2; ++m) lse[m] = a.lse[((static_cast<int64_t>(b) * a.H + h) * 2 + m) * a.Lq + l];
+        }
+        part[0][half][rl] = d[0];
+        part[1][half][rl] = d[1];
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        d[1] = part[1][0][rl] + part[1][1][rl];
+        d[0] = fmaf(lam, d[1], part[0][0][rl] + part[0][1][rl]);  // out = o_0 - lam o_1
+        const bool none = lse[0] == INFINITY;  // sees no key: whatever g holds there is not used
+        if (none) d[0] = d[1] = 0.f;
+        const float2 nd[2] = {{-d[0], -d[0]}, {-d[1], -d[1]}};
+        float2 rest[2] = {{0.f, 0.f}, {0.f, 0.f}};
+        for (int t = 0; t < T_; ++t) {
+            const QKeyInfo &ki = infos[t % NS];
+            bar_wait_warp(&bars.info[t % NS], (t / NS) & 1, gave_up);
+            const int rlo = ki.lo - pos, rhi = ki.hi - pos;
+            const bool even = !live || (ki.all && !none && !(a.causal && rhi > 0) &&
+                                        (a.nb == 0 || rlo >= a.reach || rhi <= -a.reach || rlo == rhi));
+            const bool fast = __all_sync(0xffffffffu, even);
+            bar_wait_warp(&bars.s_full[t & 1], (t >> 1) & 1, gave_up);
+            fence_after();
+            float e[32], x[2][32];
+            tmem_load(tS(t & 1, 2) + lanes + half * 32, e);
+            tmem_load(tS(t & 1, 0) + lanes + half * 32, x[0]);
+            tmem_load(tS(t & 1, 1) + lanes + half * 32, x[1]);
+            float add[2] = {-lse[0], -lse[1]}, mul = a.scale_log2;
+            if (fast) {
+                if (a.nb) {
+                    const float bias = tb[min(max(rlo, -a.reach), a.reach)];
+                    add[0] += bias;
+                    add[1] += bias;
+                }
+            } else {
+                const uint32_t valid = ki.valid[half];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int rel = ki.pos[half * 32 + i] - pos;
+                    const float bias = a.nb ? tb[min(max(rel, -a.reach), a.reach)] : 0.f;
+                    const bool on = (valid >> i & 1) && !(a.causal && rel > 0) && !none;
+                    x[0][i] = on ? fmaf(x[0][i], mul, bias + add[0]) : -INFINITY;
+                    x[1][i] = on ? fmaf(x[1][i], mul, bias + add[1]) : -INFINITY;
+                    e[i] = on ? e[i] : 0.f;  // may be NaN where nothing is seen
+                }
+                mul = 1.f;
+                add[0] = add[1] = 0.f;
+            }
+            uint32_t p[2][16];
+            const float2 mul_2 = {mul, mul}, a0 = {add[0], add[0]}, a1 = {add[1], add[1]}, nl = {nlam, nlam};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 ei = {e[2 * i], e[2 * i + 1]};
+                float2 w0 = fma2({x[0][2 * i], x[0][2 * i + 1]}, mul_2, a0), w1 = fma2({x[1][2 * i], x[1][2 * i + 1]}, mul_2, a1);
+                w0.x = ex2(w0.x);
+                w0.y = ex2(w0.y);
+                w1.x = ex2(w1.x);
+                w1.y = ex2(w1.y);
+                const float2 s0 = mul2(w0, add2(ei, nd[0])), s1 = mul2(w1, add2(ei, nd[1]));
+                rest[0] = add2(rest[0], s0);
+                rest[1] = add2(rest[1], s1);
+                const float2 s1l = mul2(s1, nl);
+                p[0][i] = pack2<T>(s0.x, s0.y);
+                p[1][i] = pack2<T>(s1l.x, s1l.y);
+            }
+            if (t > 0) bar_wait_warp(&bars.ds_free, (t - 1) & 1, gave_up);
+            for (int m = 0; m < 2; ++m) store_operand(base + F::at_s + m * F::s, rl, half, p[m]);
+            fence_async();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bars.ds_full);
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        for (int m = 0; m < 2; ++m) part[m][half][rl] = rest[m].x + rest[m].y;
+        if (T_ > 0) bar_wait(&bars.fin, 0, gave_up);
+        fence_after();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const int m = half;  // the warps of each half write one map
+        const float nan = *gave_up ? NAN : 0.f;
+        if (live)
+            a.delta[((static_cast<int64_t>(b) * a.Hkv + n) * 2 + m) * a.rows + static_cast<int64_t>(l) * a.G + g] =
+                d[m] + part[m][0][rl] + part[m][1][rl] + nan;
+        T *dst = static_cast<T *>(a.grad_q) + (((static_cast<int64_t>(b) * a.Lq + l) * a.H + h) * 2 + m) * a.D;
+        const bool wide = aligned16(a.grad_q);
+#pragma unroll 1
+        for (int c = 0; c < DP; c += 32) {
+            float x[32];
+            __syncwarp();
+            if (T_ > 0) {
+                tmem_load(tQ(m) + lanes + c, x);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = 0.f;
+            }
+            if (live) store_row(dst + c, x, a.scale + nan, a.D - c, wide);
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        fence_after();
+        tmem_free(tmem, 512);
+    }
+    if (threadIdx.x == 0 && *gave_up) atomicOr(&g_gave_up_backward, 1u);
+}
+
+// ---- grad_k, grad_v, grad_table --------------------------------------------
+
+template <int DP, int VP> struct GradKVShared {
+    static constexpr int row = DP * 2;
+    static constexpr int k = kOwn * row, v = kOwn * kBlock;       // one map, one block of 64 columns
+    static constexpr int q = kStep * row, g = kStep * kBlock;
+    static constexpr int stage = 2 * q + (VP / 64) * g;
+    static constexpr int stages = stage > 24576 ? 2 : 3;
+    static constexpr int s = kOwn * kBlock;                       // P_0 - lam P_1 and s_m as operands
+    static constexpr int at_v = 2 * k, at_stage = at_v + (VP / 64) * v, at_s = at_stage + stages * stage,
+                         bytes = at_s + 3 * s;
+    static constexpr int table(int nb, int reach) { return nb ? 4 * (2 * reach + 1) + (2 * reach + 4) / 4 * 4 + 4 * 256 * nb : 0; }
+};
+
+// Per-query values of a step, the queries' positions among them.
+struct QueryInfo {
+    float nlse[2][kStep], nd[2][kStep];  // minus the log-sums, minus d_m
+    int pos[kStep];
+    int lo, hi;
+    uint32_t all, pad;
+};
+
+struct KVBars {
+    uint64_t kv_full, kv_ready, fin, s_full, s_free, ds_full, ds_free;
+    uint64_t q_full[3], q_empty[3], info[3], ready[3];
+    uint32_t tmem, gave_up;
+};
+
+template <typename T, int DP, int VP>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    dattn_grad_kv_tc_kernel(const __grid_constant__ DattnArgs a, const __grid_constant__ CUtensorMap mq,
+                            const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                            const __grid_constant__ CUtensorMap mg)
+{
+    using F = GradKVShared<DP, VP>;
+    constexpr int NS = F::stages;
+    extern __shared__ unsigned char raw[];
+    unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
+    __shared__ KVBars bars;
+    __shared__ QueryInfo infos[NS];
+    const int span = 2 * a.reach + 1;
+    // Bias of the head at hand by relative position, its bucket, and every
+    // compute thread's own sums per bucket.
+    float *table = reinterpret_cast<float *>(base + F::bytes);
+    uint8_t *bucket = reinterpret_cast<uint8_t *>(table + span);
+    float *sums = reinterpret_cast<float *>(bucket + (span + 3) / 4 * 4);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n = blockIdx.y, b = blockIdx.z, j0 = blockIdx.x * kOwn;
+    const int len = dattn_length(a, b);
+    int first = 0;
+    if (a.causal && !a.pos_q && !a.pos_k) first = min(max(j0 - (len - a.Lq), 0), a.Lq);
+    const int per = j0 < len ? (a.Lq - first + kStep - 1) / kStep : 0;  // steps for each head
+    const int T_ = per * a.G;
+
+    if (threadIdx.x == 0) {
+        bar_init(&bars.kv_full, 1);
+        bar_init(&bars.kv_ready, 1);
+        bar_init(&bars.fin, 1);
+        bar_init(&bars.s_full, 1);
+        bar_init(&bars.s_free, 8);
+        bar_init(&bars.ds_full, 8);
+        bar_init(&bars.ds_free, 1);
+        for (int s = 0; s < NS; ++s) {
+            bar_init(&bars.q_full[s], 1);
+            bar_init(&bars.q_empty[s], 1);
+            bar_init(&bars.info[s], 1);
+            bar_init(&bars.ready[s], 1);
+        }
+        bars.gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tma_prefetch(&mq);
+        tma_prefetch(&mk);
+        tma_prefetch(&mv);
+        tma_prefetch(&mg);
+    }
+    if (warp == 9) tmem_alloc(&bars.tmem, 512);
+    if (a.nb)
+        for (int i = threadIdx.x; i < span; i += kBwdThreads)
+            bucket[i] = static_cast<uint8_t>(min(max(a.bmap[i], 0), a.nb - 1));
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = bars.tmem;
+    volatile uint32_t *gave_up = &bars.gave_up;
+    auto tS = [&](int which) { return tmem + which * 64; };
+    const uint32_t tV = tmem + 192;
+    auto tK = [&](int m) { return tmem + 192 + VP + m * DP; };
+    const uint32_t sbase = smem_addr(base);
+
+    if (warp == 8) {
+        if (lane == 0 && T_ > 0) {
+            bar_expect(&bars.kv_full, F::at_stage);
+            for (int m = 0; m < 2; ++m) tma_load(&mk, &bars.kv_full, base + m * F::k, 0, m, n, j0, b);
+            for (int c = 0; c < VP / 64; ++c) tma_load(&mv, &bars.kv_full, base + F::at_v + c * F::v, c * 64, 0, n, j0, b);
+            for (int t = 0; t < T_; ++t) {
+                const int s = t % NS, h = n * a.G + t / per, l = first + (t % per) * kStep;
+                unsigned char *st = base + F::at_stage + s * F::stage;
+                bar_wait(&bars.q_empty[s], ((t / NS) & 1) ^ 1, gave_up);
+                bar_expect(&bars.q_full[s], F::stage);
+                for (int m = 0; m < 2; ++m) tma_load(&mq, &bars.q_full[s], st + m * F::q, 0, m, h, l, b);
+                for (int c = 0; c < VP / 64; ++c) tma_load(&mg, &bars.q_full[s], st + 2 * F::q + c * F::g, c * 64, 0, h, l, b);
+            }
+            if (*gave_up) {
+                bar_drain(&bars.kv_full, 0);
+                for (int t = max(0, T_ - NS); t < T_; ++t) bar_drain(&bars.q_full[t % NS], (t / NS) & 1);
+            }
+        }
+    } else if (warp == 9) {
+        if (lane == 0 && T_ > 0) {
+            constexpr uint32_t is = shape(is_bf16<T>, kStep, false), iv = shape(is_bf16<T>, VP, true),
+                               ik = shape(is_bf16<T>, DP, true);
+            auto scores = [&](int t) {
+                const uint32_t st = sbase + F::at_stage + (t % NS) * F::stage;
+                bar_wait(&bars.q_full[t % NS], (t / NS) & 1, gave_up);
+                bar_wait(&bars.ready[t % NS], (t / NS) & 1, gave_up);
+                if (t > 0) bar_wait(&bars.s_free, (t - 1) & 1, gave_up);
+                fence_after();
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < DP / 16; ++i)
+                        mma_ss(tS(m), along_row<F::row>(sbase + m * F::k, i), along_row<F::row>(st + m * F::q, i), is, i > 0);
+#pragma unroll
+                for (int i = 0; i < VP / 16; ++i)
+                    mma_ss(tS(2), along_row<128>(sbase + F::at_v + (i / 4) * F::v, i % 4),
+                           along_row<128>(st + 2 * F::q + (i / 4) * F::g, i % 4), is, i > 0);
+                mma_commit(&bars.s_full);
+            };
+            bar_wait(&bars.kv_full, 0, gave_up);
+            bar_wait(&bars.kv_ready, 0, gave_up);
+            scores(0);
+            for (int t = 0; t < T_; ++t) {
+                if (t + 1 < T_) scores(t + 1);
+                bar_wait(&bars.ds_full, t & 1, gave_up);
+                fence_after();
+                const uint32_t st = sbase + F::at_stage + (t % NS) * F::stage;
+#pragma unroll
+                for (int i = 0; i < kStep / 16; ++i)
+                    mma_ss(tV, along_row<128>(sbase + F::at_s, i), over_rows<128>(st + 2 * F::q, i, F::g), iv, t > 0 || i > 0);
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < kStep / 16; ++i)
+                        mma_ss(tK(m), along_row<128>(sbase + F::at_s + (1 + m) * F::s, i), over_rows<F::row>(st + m * F::q, i, F::q), ik,
+                               t > 0 || i > 0);
+                mma_commit(&bars.ds_free);
+                mma_commit(&bars.q_empty[t % NS]);
+            }
+            mma_commit(&bars.fin);
+            bar_drain(&bars.fin, 0);
+        }
+    } else if (warp == 10) {
+        if (T_ > 0) {
+            // Keys that are not to be used become zeros, once.
+            bar_wait_warp(&bars.kv_full, 0, gave_up);
+            bool any = false;
+            for (int r = lane >> 3; r < kOwn; r += 4) {
+                const int j = j0 + r;
+                if (j < a.Lk && (j >= len || (a.mask && !a.mask[static_cast<int64_t>(b) * a.Lk + j]))) {
+                    for (int m = 0; m < 2; ++m) zero_row(base + m * F::k, r, F::row, lane & 7);
+                    for (int c = 0; c < VP / 64; ++c) zero_row(base + F::at_v + c * F::v, r, kBlock, lane & 7);
+                    any = true;
+                }
+            }
+            if (any) fence_async();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bars.kv_ready);
+        }
+        for (int t = 0; t < T_; ++t) {
+            const int s = t % NS, g = t / per, h = n * a.G + g, l0 = first + (t % per) * kStep;
+            QueryInfo &qi = infos[s];
+            bar_wait_warp(&bars.q_empty[s], ((t / NS) & 1) ^ 1, gave_up);
+            int lo = INT32_MAX, hi = INT32_MIN;
+            uint32_t none[2];
+            bool every = true;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int i = c * 32 + lane, l = l0 + i;
+                const bool in = l < a.Lq;
+                float lse = INFINITY;
+                for (int m = 0; m < 2; ++m) {
+                    const float x = in ? a.lse[((static_cast<int64_t>(b) * a.H + h) * 2 + m) * a.Lq + l] : INFINITY;
+                    qi.nlse[m][i] = -x;
+                    qi.nd[m][i] = in ? -a.delta[((static_cast<int64_t>(b) * a.Hkv + n) * 2 + m) * a.rows + static_cast<int64_t>(l) * a.G + g] : 0.f;
+                    lse = m == 0 ? x : lse;
+                }
+                const int pos = !in ? 0 : a.pos_q ? a.pos_q[static_cast<int64_t>(b) * a.Lq + l] : len - a.Lq + l;
+                qi.pos[i] = pos;
+                none[c] = __ballot_sync(0xffffffffu, in && lse == INFINITY);
+                if (in) {
+                    lo = min(lo, pos);
+                    hi = max(hi, pos);
+                }
+            }
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            every = (none[0] | none[1]) == 0;
+            if (lane == 0) {
+                qi.lo = lo;
+                qi.hi = hi;
+                qi.all = every;
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bars.info[s]);
+            if (!every) {  // queries that see nothing take no part, whatever q and g hold
+                bar_wait_warp(&bars.q_full[s], (t / NS) & 1, gave_up);
+                unsigned char *st = base + F::at_stage + s * F::stage;
+                for (int r = lane >> 3; r < kStep; r += 4)
+                    if (none[r >> 5] >> (r & 31) & 1) {
+                        for (int m = 0; m < 2; ++m) zero_row(st + m * F::q, r, F::row, lane & 7);
+                        for (int c = 0; c < VP / 64; ++c) zero_row(st + 2 * F::q + c * F::g, r, kBlock, lane & 7);
+                    }
+                fence_async();
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bars.ready[s]);
+        }
+    } else {
+        const int half = warp >> 2, rl = (warp & 3) * 32 + lane, tid = threadIdx.x;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int j = j0 + rl;
+        const int64_t kat = static_cast<int64_t>(b) * a.Lk + j;
+        const bool use = j < len && (!a.mask || a.mask[kat]);
+        const int pos = use && a.pos_k ? a.pos_k[kat] : j;
+        float *mine = sums + tid;
+        for (int g = 0; g < a.G; ++g) {
+            if (a.nb) {  // this head's bias, and sums from zero
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                for (int i = tid; i < span; i += 256) table[i] = a.table[bucket[i] * a.H + n * a.G + g] * kLog2e;
+                for (int i = 0; i < a.nb; ++i) mine[i * 256] = 0.f;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+            }
+            const float nlam = -a.lam[n * a.G + g];
+            for (int u = 0; u < per; ++u) {
+                const int t = g * per + u;
+                const QueryInfo &qi = infos[t % NS];
+                bar_wait_warp(&bars.info[t % NS], (t / NS) & 1, gave_up);
+                const int rlo = pos - qi.hi, rhi = pos - qi.lo;
+                const bool same = rlo >= a.reach || rhi <= -a.reach || rlo == rhi;  // one bucket for the whole step
+                const bool even = !use || (!(a.causal && rhi > 0) && (a.nb == 0 || same));
+                const bool fast = __all_sync(0xffffffffu, even);
+                bar_wait_warp(&bars.s_full, t & 1, gave_up);
+                fence_after();
+                float e[32], x[2][32];
+                tmem_load(tS(2) + lanes + half * 32, e);
+                tmem_load(tS(0) + lanes + half * 32, x[0]);
+                tmem_load(tS(1) + lanes + half * 32, x[1]);
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&bars.s_free);
+                float add = 0.f, mul = a.scale_log2;
+                int where = 0;
+                if (fast) {
+                    if (a.nb) {
+                        where = min(max(rlo, -a.reach), a.reach) + a.reach;
+                        add = table[where];
+                    }
+                    if (!use) add = -INFINITY;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int rel = pos - qi.pos[half * 32 + i];
+                        const float bias = a.nb ? table[min(max(rel, -a.reach), a.reach) + a.reach] : 0.f;
+                        const bool on = use && !(a.causal && rel > 0);
+                        x[0][i] = on ? fmaf(x[0][i], mul, bias) : -INFINITY;
+                        x[1][i] = on ? fmaf(x[1][i], mul, bias) : -INFINITY;
+                    }
+                    mul = 1.f;
+                }
+                const float2 mul_2 = {mul, mul}, add_2 = {add, add}, nl = {nlam, nlam};
+                float2 total = {0.f, 0.f};
+                uint32_t pw[16], p0[16], p1[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 l0 = *reinterpret_cast<const float2 *>(&qi.nlse[0][half * 32 + 2 * i]);
+                    const float2 l1 = *reinterpret_cast<const float2 *>(&qi.nlse[1][half * 32 + 2 * i]);
+                    const float2 d0 = *reinterpret_cast<const float2 *>(&qi.nd[0][half * 32 + 2 * i]);
+                    const float2 d1 = *reinterpret_cast<const float2 *>(&qi.nd[1][half * 32 + 2 * i]);
+                    const float2 ei = {e[2 * i], e[2 * i + 1]};
+                    float2 w0 = fma2({x[0][2 * i], x[0][2 * i + 1]}, mul_2, add2(add_2, l0));
+                    float2 w1 = fma2({x[1][2 * i], x[1][2 * i + 1]}, mul_2, add2(add_2, l1));
+                    w0.x = ex2(w0.x);
+                    w0.y = ex2(w0.y);
+                    w1.x = ex2(w1.x);
+                    w1.y = ex2(w1.y);
+                    w1 = mul2(w1, nl);
+                    const float2 s0 = mul2(w0, add2(ei, d0)), s1 = mul2(w1, add2(ei, d1)), w = add2(w0, w1);
+                    const float2 both = add2(s0, s1);
+                    total = add2(total, both);
+                    x[0][2 * i] = both.x;  // kept for the buckets
+                    x[0][2 * i + 1] = both.y;
+                    pw[i] = pack2<T>(w.x, w.y);
+                    p0[i] = pack2<T>(s0.x, s0.y);
+                    p1[i] = pack2<T>(s1.x, s1.y);
+                }
+                if (a.nb) {
+                    if (fast) {
+                        mine[bucket[where] * 256] += total.x + total.y;
+                    } else {
+                        // Runs of one bucket are summed before they are added.
+                        int last = bucket[min(max(pos - qi.pos[half * 32], -a.reach), a.reach) + a.reach];
+                        float run = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int k = bucket[min(max(pos - qi.pos[half * 32 + i], -a.reach), a.reach) + a.reach];
+                            if (k != last) {
+                                mine[last * 256] += run;
+                                run = 0.f;
+                                last = k;
+                            }
+                            run += x[0][i];
+                        }
+                        mine[last * 256] += run;
+                    }
+                }
+                if (t > 0) bar_wait_warp(&bars.ds_free, (t - 1) & 1, gave_up);
+                store_operand(base + F::at_s, rl, half, pw);
+                store_operand(base + F::at_s + F::s, rl, half, p0);
+                store_operand(base + F::at_s + 2 * F::s, rl, half, p1);
+                fence_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&bars.ds_full);
+            }
+            if (a.nb) {
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                float *out = a.part_table + ((static_cast<int64_t>(b) * a.Hkv + n) * a.table_ctas + blockIdx.x) * a.nb * a.G;
+                for (int k = warp; k < a.nb; k += 8) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s += sums[k * 256 + i * 32 + lane];
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                    if (lane == 0) out[k * a.G + g] = *gave_up ? NAN : s;
+                }
+            }
+        }
+        if (T_ > 0) bar_wait(&bars.fin, 0, gave_up);
+        fence_after();
+        const float nan = *gave_up ? NAN : 0.f;
+        const bool in = j < a.Lk;
+        const int64_t at = kat * a.Hkv + n;
+        const bool wide_k = aligned16(a.grad_k), wide_v = aligned16(a.grad_v);
+        // The warps of each half write half of grad_v's columns and one map of grad_k.
+#pragma unroll 1
+        for (int c = 0; c < VP / 2 + DP; c += 32) {
+            const bool of_v = c < VP / 2;
+            const int col = of_v ? half * (VP / 2) + c : c - VP / 2;
+            float x[32];
+            __syncwarp();
+            if (T_ > 0) {
+                tmem_load((of_v ? tV : tK(half)) + lanes + col, x);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = 0.f;
+            }
+            if (!in) continue;
+            if (of_v) store_row(static_cast<T *>(a.grad_v) + at * a.Dv + col, x, 1.f + nan, a.Dv - col, wide_v);
+            else store_row(static_cast<T *>(a.grad_k) + (at * 2 + half) * a.D + col, x, a.scale + nan, a.D - col, wide_k);
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        fence_after();
+        tmem_free(tmem, 512);
+    }
+    if (threadIdx.x == 0 && *gave_up) atomicOr(&g_gave_up_backward, 1u);
+}
+
+struct BwdMaps {
+    CUtensorMap q, k, v, g;
+};
+
+template <typename K>
+cudaError_t launch_bwd(K kernel, dim3 grid, size_t smem, const DattnArgs &a, const BwdMaps &m, cudaStream_t st)
+{
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kBwdThreads, smem, st>>>(a, m.q, m.k, m.v, m.g);
+    return cudaGetLastError();
+}
+
+template <typename T, int DP, int VP>
+cudaError_t bwd_kernels(const DattnArgs &a, const BwdMaps &own_rows, const BwdMaps &own_keys, cudaStream_t st)
+{
+    using Q = GradQShared<DP, VP>;
+    using KV = GradKVShared<DP, VP>;
+    const int LP = kOwn / a.G;
+    const cudaError_t e = launch_bwd(dattn_grad_q_tc_kernel<T, DP, VP>, dim3((a.Lq + LP - 1) / LP, a.Hkv, a.B),
+                                     Q::bytes + 1024 + sizeof(float) * (a.nb ? a.G * (2 * a.reach + 1) : 0), a, own_rows, st);
+    if (e != cudaSuccess) return e;
+    return launch_bwd(dattn_grad_kv_tc_kernel<T, DP, VP>, dim3((a.Lk + kOwn - 1) / kOwn, a.Hkv, a.B),
+                      KV::bytes + 1024 + KV::table(a.nb, a.reach), a, own_keys, st);
+}
+
+template <typename T> cudaError_t bwd_widths(const DattnArgs &a, const BwdMaps &r, const BwdMaps &k, cudaStream_t st)
+{
+    if (a.D <= 32) return a.Dv <= 64 ? bwd_kernels<T, 32, 64>(a, r, k, st) : bwd_kernels<T, 32, 128>(a, r, k, st);
+    return a.Dv <= 64 ? bwd_kernels<T, 64, 64>(a, r, k, st) : bwd_kernels<T, 64, 128>(a, r, k, st);
+}
+
+}  // namespace
+
+uint32_t *dattn_gave_up_backward_word()
+{
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_gave_up_backward) == cudaSuccess ? static_cast<uint32_t *>(p) : nullptr;
+}
+
+da_status dattn_backward_tensor(const DattnArgs &a, int dtype, cudaStream_t st)
+{
+    const int wide = a.D <= 32 ? 32 : 64, LP = kOwn / a.G;
+    const int64_t gl = static_cast<int64_t>(a.H) * a.Dv, gb = gl * a.Lq;  // strides of grad_out
+    BwdMaps r, k;
+    da_status e = DA_OK;
+    auto make = [&](CUtensorMap &m, const void *p, int width, int maps, int heads, int len, const int64_t *s, int64_t s_map, int bw, int bh, int bl) {
+        if (e == DA_OK) e = tensor_map(m, dtype, p, width, maps, heads, len, a.B, s_map, s[2], s[1], s[0], bw, bh, bl);
+    };
+    const int64_t gs[3] = {gb, gl, a.Dv};
+    make(r.q, a.q, a.D, 2, a.H, a.Lq, a.qs, a.qs[3], wide, a.G, LP);
+    make(r.g, a.grad_out, a.Dv, 1, a.H, a.Lq, gs, 0, 64, a.G, LP);
+    make(r.k, a.k, a.D, 2, a.Hkv, a.Lk, a.ks, a.ks[3], wide, 1, kStep);
+    make(r.v, a.v, a.Dv, 1, a.Hkv, a.Lk, a.vs, 0, 64, 1, kStep);
+    make(k.q, a.q, a.D, 2, a.H, a.Lq, a.qs, a.qs[3], wide, 1, kStep);
+    make(k.g, a.grad_out, a.Dv, 1, a.H, a.Lq, gs, 0, 64, 1, kStep);
+    make(k.k, a.k, a.D, 2, a.Hkv, a.Lk, a.ks, a.ks[3], wide, 1, kOwn);
+    make(k.v, a.v, a.Dv, 1, a.Hkv, a.Lk, a.vs, 0, 64, 1, kOwn);
+    if (e != DA_OK) return e;
+    const cudaError_t c = dtype == DA_BF16 ? bwd_widths<__nv_bfloat16>(a, r, k, st) : bwd_widths<__half>(a, r, k, st);
+    return c == cudaSuccess ? DA_OK : cuda_fail(c, "differential attention backward launch");
+}
+
+}  // namespace da

@@ -406,6 +406,7 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_co
         for (int m = 0; m < 2; ++m) {
             lse[m][i] = ri[i].l < 0 ? INFINITY : a.lse[((static_cast<int64_t>(b) * a.H + h) * 2 + m) * a.Lq + ri[i].l];
             rest[m][i] = 0.f;
+            if (lse[m][i] == INFINITY) dl[m][i] = 0.f;  // sees no key: whatever grad_out holds there is not used
 #pragma unroll
             for (int c = 0; c < F::ND; ++c) acc[m][i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
         }

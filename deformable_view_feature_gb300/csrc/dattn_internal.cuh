@@ -64,7 +64,9 @@ template <> __device__ __forceinline__ __half dattn_round(float v) { return __fl
 template <> __device__ __forceinline__ __nv_bfloat16 dattn_round(float v) { return __float2bfloat16_rn(v); }
 
 da_status dattn_forward_tensor(const DattnArgs &a, int dtype, cudaStream_t st);
-uint32_t *dattn_gave_up_word();
+da_status dattn_backward_tensor(const DattnArgs &a, int dtype, cudaStream_t st);
+uint32_t *dattn_gave_up_word();           // of the forward kernels
+uint32_t *dattn_gave_up_backward_word();  // of the backward kernels
 cudaError_t dattn_forward_general(const DattnArgs &a, int dtype, cudaStream_t st);
 cudaError_t dattn_backward_general(const DattnArgs &a, int dtype, cudaStream_t st);
 cudaError_t dattn_merge(const DattnArgs &a, int dtype, cudaStream_t st);

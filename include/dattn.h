@@ -82,9 +82,10 @@ typedef struct dattn_problem {
     const int32_t *key_lengths;  /* device [B] int32, or NULL */
 } dattn_problem;
 
-/* Which kernels a problem takes (a host-only rule on types, sizes and
- * alignment): 1 the tensor-core ones, 0 the general ones, < 0 invalid. */
-int32_t dattn_path(const dattn_problem *p);
+/* Which kernels dattn_forward (backward == 0) or dattn_backward takes (a
+ * host-only rule on types, sizes and alignment): 1 the tensor-core ones, 0 the
+ * general ones, < 0 invalid. */
+int32_t dattn_path(const dattn_problem *p, int32_t backward);
 
 /* Bytes of device scratch of dattn_forward (backward == 0) or dattn_backward. */
 da_status dattn_workspace_size(const dattn_problem *p, int32_t backward, size_t *bytes);
