@@ -149,6 +149,8 @@ def _check(status: int):
 
 def _host_i32(t) -> torch.Tensor:
     """The small map tables travel as host int32 arrays (copied if on a device)."""
+    if type(t) is torch.Tensor and t.dtype == torch.int32 and t.device.type == "cpu" and t.is_contiguous():
+        return t.detach() if t.requires_grad else t
     t = torch.as_tensor(t)
     return t.detach().to(device="cpu", dtype=torch.int32).contiguous()
 
@@ -167,6 +169,27 @@ def _stream_handle(stream) -> Optional[int]:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream or None
+
+
+class _on_stream:
+    """The stream a call runs on, current for what it allocates: `stream`, or
+    the device's current one. Yields the handle for the library."""
+
+    __slots__ = ("given", "context", "device")
+
+    def __init__(self, stream, device: torch.device):
+        self.given, self.device = stream, device
+
+    def __enter__(self) -> Optional[int]:
+        if self.given is None:
+            return torch.cuda.current_stream(self.device.index).cuda_stream or None
+        self.context = torch.cuda.stream(self.given)
+        self.context.__enter__()
+        return self.given.cuda_stream or None
+
+    def __exit__(self, *exc):
+        if self.given is not None:
+            self.context.__exit__(*exc)
 
 
 def _dims(feat: torch.Tensor, ss: torch.Tensor, loc: torch.Tensor, weights: torch.Tensor) -> DaDims:

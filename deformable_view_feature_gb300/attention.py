@@ -21,7 +21,7 @@ from typing import Optional
 
 import torch
 
-from . import DA_BF16, DA_F16, DA_F32, DaError, _check, _dptr, load_library
+from . import DA_BF16, DA_F16, DA_F32, DaError, _check, _dptr, _on_stream, load_library
 
 __all__ = ["dattn_forward", "dattn_backward", "dattn_path", "relative_buckets", "DifferentialAttentionFunction"]
 
@@ -80,8 +80,8 @@ def _strided(t: torch.Tensor, name: str) -> int:
 def _small(t: Optional[torch.Tensor], name: str, shape, dtype) -> Optional[int]:
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)}")
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {shape}")
     return _dptr(t)
 
 
@@ -103,24 +103,19 @@ def _problem(q, k, v, lam, bias_table, bucket_map, pos_q, pos_k, key_mask, key_l
         raise TypeError("q, k and v must have one type")
     if (bias_table is None) != (bucket_map is None):
         raise ValueError("bias_table and bucket_map go together")
-    p = DattnProblem(batch=B, num_queries=Lq, num_keys=Lk, num_heads=H, num_kv_heads=Hkv, width=D, value_width=Dv,
-                     dtype=_DTYPES[q.dtype], causal=int(bool(causal)), scale=D ** -0.5 if scale is None else scale,
-                     q=_strided(q, "q"), k=_strided(k, "k"), v=_strided(v, "v"))
-    p.q_stride[:] = q.stride()[:4]
-    p.k_stride[:] = k.stride()[:4]
-    p.v_stride[:] = v.stride()[:3]
-    p.lam = _small(lam, "lam", (H,), torch.float32)
+    num_buckets = reach = 0
     if bias_table is not None:
         if bias_table.dim() != 2 or bucket_map.dim() != 1 or bucket_map.shape[0] % 2 != 1:
             raise ValueError("bias_table must be [num_buckets, H] and bucket_map [2 * reach + 1]")
-        p.num_buckets, p.reach = bias_table.shape[0], bucket_map.shape[0] // 2
-        p.bias_table = _small(bias_table, "bias_table", (p.num_buckets, H), torch.float32)
-        p.bucket_map = _small(bucket_map, "bucket_map", (2 * p.reach + 1,), torch.int32)
-    p.pos_q = _small(pos_q, "pos_q", (B, Lq), torch.int32)
-    p.pos_k = _small(pos_k, "pos_k", (B, Lk), torch.int32)
-    p.key_mask = _small(key_mask, "key_mask", (B, Lk), torch.bool)
-    p.key_lengths = _small(key_lengths, "key_lengths", (B,), torch.int32)
-    return p
+        num_buckets, reach = bias_table.shape[0], bucket_map.shape[0] // 2
+    return DattnProblem(B, Lq, Lk, H, Hkv, D, Dv, _DTYPES[q.dtype], num_buckets, reach, 1 if causal else 0,
+                        D ** -0.5 if scale is None else scale, _strided(q, "q"), _strided(k, "k"), _strided(v, "v"),
+                        q.stride()[:4], k.stride()[:4], v.stride()[:3], _small(lam, "lam", (H,), torch.float32),
+                        _small(bias_table, "bias_table", (num_buckets, H), torch.float32),
+                        _small(bucket_map, "bucket_map", (2 * reach + 1,), torch.int32),
+                        _small(pos_q, "pos_q", (B, Lq), torch.int32), _small(pos_k, "pos_k", (B, Lk), torch.int32),
+                        _small(key_mask, "key_mask", (B, Lk), torch.bool),
+                        _small(key_lengths, "key_lengths", (B,), torch.int32))
 
 
 def _scratch(lib, p, backward, device):
@@ -164,7 +159,7 @@ def dattn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.
     shape = (p.batch, p.num_queries, p.num_heads, p.value_width)
     if out is not None and (tuple(out.shape) != shape or out.dtype != q.dtype):
         raise ValueError(f"out must be {q.dtype} {shape}")
-    with torch.cuda.stream(stream):
+    with _on_stream(stream, q.device) as handle:
         if out is None:
             out = torch.empty(shape, dtype=q.dtype, device=q.device)
         out1 = lse = None
@@ -173,7 +168,7 @@ def dattn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.
             lse = torch.empty(p.batch, p.num_heads, 2, p.num_queries, dtype=torch.float32, device=q.device)
         ws, n = _scratch(lib, p, 0, q.device)
         _check(lib.dattn_forward(ctypes.byref(p), _dptr(out), _dptr(out1), _dptr(lse), _dptr(ws), n,
-                                 torch.cuda.current_stream().cuda_stream or None))
+                                 handle))
     return (out, (out1, lse)) if keep_for_backward else out
 
 
@@ -195,14 +190,14 @@ def dattn_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch
             raise ValueError(f"{name} must be {q.dtype} {shape}")
     if tuple(lse.shape) != (p.batch, p.num_heads, 2, p.num_queries) or lse.dtype != torch.float32:
         raise ValueError("saved[1] must be what dattn_forward returned")
-    with torch.cuda.stream(stream):
+    with _on_stream(stream, q.device) as handle:
         gq, gk, gv = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v))
         gl = torch.empty_like(lam)
         gt = torch.empty_like(bias_table) if bias_table is not None else None
         ws, n = _scratch(lib, p, 1, q.device)
         _check(lib.dattn_backward(ctypes.byref(p), _dptr(out), _dptr(out1), _dptr(lse), _dptr(grad_out), _dptr(gq),
                                   _dptr(gk), _dptr(gv), _dptr(gl), _dptr(gt), _dptr(ws), n,
-                                  torch.cuda.current_stream().cuda_stream or None))
+                                  handle))
     return gq, gk, gv, gl, gt
 
 

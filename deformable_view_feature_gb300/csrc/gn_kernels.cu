@@ -1,10 +1,19 @@
 // Group norm with an activation over packed channels-last maps (include/gn.h).
 //
-// A map is cut into tiles of `tr` rows. One pass takes every tile's sums, one
-// CTA per (batch item, map) joins them in the order of the tiles, and a second
-// pass over the tiles writes the outputs. A CTA's threads form a grid of
-// 16-byte columns x rows of its tile, so every access is a full row segment
-// and a thread keeps its channels' parameters in registers.
+// A map is cut into tiles of `tr` rows, and each pass is one kernel of two
+// CTAs per tile, ordered by a ticket that a CTA draws when it starts: first a
+// tile's sums, and some hundred tiles later, when its map's sums are complete,
+// the same tile's outputs. That distance keeps what lies between in the 129 MB
+// L2, so the second reading of a tile comes from there and device memory is
+// read once. In between, CTAs of their own join the map's sums, in a fixed
+// order. A CTA's threads form a grid of 4-channel columns
+// x rows of its tile, so every access is a full row segment and a thread keeps
+// its channels' parameters in registers.
+//
+// The wait for a map's sums cannot stall: a CTA that waits has a later ticket
+// than every tile it waits for, and those, already running, are summed without
+// waiting. It is bounded all the same; a wait that ran out turns the outputs
+// into NaN and sets a word that gn_device_status reads.
 //
 // Forward statistics: a tile sums x - p and (x - p)^2 per channel, p being
 // the tile's first row, and turns them into a mean and a sum of squared
@@ -22,6 +31,9 @@ namespace da {
 namespace {
 
 constexpr int kGnThreads = 256;
+constexpr int kGnCtas = 3;         // resident per SM: up to 85 registers a thread
+constexpr int kGnSmall = 65536;    // bytes of a map that one CTA takes alone
+constexpr int kGnTries = 1 << 22;  // of a wait, about a microsecond each at most
 
 struct GnMap {
     int32_t rows, start;  // pixels, first feature row
@@ -38,8 +50,14 @@ struct GnArgs {
     float *sums;         // backward: [B, maps, 2, C]
     float *group;        // backward: [B, maps, G, 2] mean(gamma*h), mean(gamma*h*n)
     float *grad_gamma, *grad_beta;
+    // Counters, zero at launch: tickets drawn, joins done, then per (batch
+    // item, map) tiles summed and joins done.
+    uint32_t *queue, *all_done, *tiles_done, *ready;
+    int32_t ntiles, lag; // tiles in all, tiles between a tile's sums and its outputs
+    int32_t joins;       // CTAs that share a map's join
     int64_t rows;        // per batch item
     int32_t B, C, G, Cg, nmaps, S, K, tiles, tr, affine_scales;
+    FastDiv div_Cg;
     float eps;
     GnMap maps[DA_MAX_MAPS];
 };
@@ -53,40 +71,104 @@ template <> __device__ __forceinline__ float from_f(float v) { return v; }
 template <> __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
 
-// V consecutive channels: 16 bytes, or one element where rows are not
-// multiples of 16 bytes.
-template <typename T, int V> struct alignas(sizeof(T) * V) Pack {
-    T v[V];
-};
+// V consecutive channels as they are loaded: 16 or 8 bytes, or one element
+// where rows are not multiples of 16 bytes.
+template <int BYTES> struct Raw;
+template <> struct Raw<16> { using type = uint4; };
+template <> struct Raw<8> { using type = uint2; };
+template <> struct Raw<4> { using type = uint32_t; };
+template <> struct Raw<2> { using type = unsigned short; };
+template <typename T, int V> using Pack = typename Raw<static_cast<int>(sizeof(T)) * V>::type;
 
-template <typename T, int V> __device__ __forceinline__ void load_row(const void *base, int64_t at, float (&f)[V])
+__device__ __forceinline__ void two(uint32_t w, float &a, float &b, const __nv_bfloat16 *)
 {
-    const Pack<T, V> p = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(base) + at);
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = to_f(p.v[i]);
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void two(uint32_t w, float &a, float &b, const __half *)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    a = f.x;
+    b = f.y;
+}
+__device__ __forceinline__ uint32_t two(float a, float b, const __nv_bfloat16 *)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t two(float a, float b, const __half *)
+{
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+template <typename T, int V> __device__ __forceinline__ void unpack(const Pack<T, V> &p, float (&f)[V])
+{
+    if constexpr (V == 1) {
+        f[0] = to_f(*reinterpret_cast<const T *>(&p));
+    } else if constexpr (sizeof(T) == 4) {
+        f[0] = __uint_as_float(p.x);
+        f[1] = __uint_as_float(p.y);
+        f[2] = __uint_as_float(p.z);
+        f[3] = __uint_as_float(p.w);
+    } else {
+        two(p.x, f[0], f[1], static_cast<const T *>(nullptr));
+        two(p.y, f[2], f[3], static_cast<const T *>(nullptr));
+        if constexpr (V == 8) {
+            two(p.z, f[4], f[5], static_cast<const T *>(nullptr));
+            two(p.w, f[6], f[7], static_cast<const T *>(nullptr));
+        }
+    }
+}
+
+// LAST: the data's last use, so that it leaves the caches first, like what is
+// stored.
+template <typename T, int V, bool LAST> __device__ __forceinline__ Pack<T, V> load_pack(const T *base, int at)
+{
+    const auto *p = reinterpret_cast<const Pack<T, V> *>(base + at);
+    return LAST ? __ldcs(p) : __ldcg(p);
 }
 
 template <typename T, int V> __device__ __forceinline__ void store_row(void *base, int64_t at, const float (&f)[V])
 {
     Pack<T, V> p;
-#pragma unroll
-    for (int i = 0; i < V; ++i) p.v[i] = from_f<T>(f[i]);
-    *reinterpret_cast<Pack<T, V> *>(static_cast<T *>(base) + at) = p;
+    if constexpr (V == 1) {
+        const T v = from_f<T>(f[0]);
+        p = *reinterpret_cast<const Pack<T, V> *>(&v);
+    } else if constexpr (sizeof(T) == 4) {
+        p = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    } else if constexpr (V == 4) {
+        p = make_uint2(two(f[0], f[1], static_cast<const T *>(nullptr)), two(f[2], f[3], static_cast<const T *>(nullptr)));
+    } else {
+        p = make_uint4(two(f[0], f[1], static_cast<const T *>(nullptr)), two(f[2], f[3], static_cast<const T *>(nullptr)),
+                       two(f[4], f[5], static_cast<const T *>(nullptr)), two(f[6], f[7], static_cast<const T *>(nullptr)));
+    }
+    __stcs(reinterpret_cast<Pack<T, V> *>(static_cast<T *>(base) + at), p);
+}
+
+// 1 / (1 + exp(-z)) by the hardware's 2^x and reciprocal (each within a few
+// units in the last place); exp(-z) past the largest number gives 0.
+__device__ __forceinline__ float logistic(float z)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
 }
 
 // act(z), and act'(z) for the backward pass.
 template <int ACT> __device__ __forceinline__ float act_of(float z)
 {
     if (ACT == GN_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays NaN
-    if (ACT == GN_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+    if (ACT == GN_ACT_SILU) return z * logistic(z);
     return z;
 }
 template <int ACT> __device__ __forceinline__ float act_slope(float z)
 {
     if (ACT == GN_ACT_RELU) return z > 0.f ? 1.f : 0.f;
     if (ACT == GN_ACT_SILU) {
-        const float s = __fdividef(1.f, 1.f + __expf(-z));
-        return s * (1.f + z * (1.f - s));
+        const float s = logistic(z);
+        return fmaf(z * s, 1.f - s, s);
     }
     return 1.f;
 }
@@ -133,6 +215,54 @@ template <int V> __device__ __forceinline__ Cover cover(int C)
     return c;
 }
 
+// The lane's rows of a tile, U at a time; of one tensor, or of two at the same
+// places (if TWO). begin() sends the first loads, which need nothing but the
+// tile, ahead of whatever else the CTA has to wait for; each() then calls
+// use(offset from the column's place in the tile's first row, x, g) per row.
+template <typename T, int V, bool TWO, bool LAST, int U> struct Rows {
+    Pack<T, V> p[U], q[TWO ? U : 1];
+    const T *px, *pg;
+    int o, step, end;
+
+    __device__ __forceinline__ void load()
+    {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (o + u * step < end) {
+                p[u] = load_pack<T, V, LAST>(px, o + u * step);
+                if (TWO) q[u] = load_pack<T, V, LAST>(pg, o + u * step);
+            }
+    }
+    __device__ __forceinline__ void begin(const Cover &c, bool on, int rows, int C, const void *x, const void *g, int64_t at)
+    {
+        px = static_cast<const T *>(x) + at;
+        pg = static_cast<const T *>(g) + at;
+        step = c.lanes * C;
+        o = c.lane * C;
+        end = on ? rows * C : 0;
+        load();
+    }
+    template <typename Use> __device__ __forceinline__ void each(Use use)
+    {
+        while (o < end) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (o + u * step < end) {
+                    float v[V], h[V];
+                    unpack<T, V>(p[u], v);
+                    if (TWO) unpack<T, V>(q[u], h);
+                    use(o + u * step, v, h);
+                }
+            o += U * step;
+            load();
+        }
+    }
+};
+
+// Rows to a batch: 128 bytes of x, or 64 of x and grad_out each, to a thread.
+template <typename T, int V> constexpr int kFwdRows = V == 1 ? 8 : 128 / (V * static_cast<int>(sizeof(T)));
+template <typename T, int V> constexpr int kBwdRows = V == 1 ? 4 : 64 / (V * static_cast<int>(sizeof(T)));
+
 // Sums over the row lanes of two values per channel, in the order of the
 // lanes. The sums of channel i of column c are left in scratch[c*V + i] and
 // scratch[second + c*V + i], second = lanes * cols * V.
@@ -169,24 +299,21 @@ template <typename T, int V> __device__ void tile_stats(const GnArgs &a, const T
     for (int c0 = 0; c0 < c.ncols; c0 += c.cols) {
         const int col = c0 + c.col;
         const bool on = c.on && col < c.ncols;
+        const int64_t at = t.row * a.C + static_cast<int64_t>(on ? col : 0) * V;
+        Rows<T, V, false, false, kFwdRows<T, V>> rows;
+        rows.begin(c, on, t.rows, a.C, a.x, a.x, at);
         float p[V], s[V], q[V];
+        unpack<T, V>(load_pack<T, V, false>(static_cast<const T *>(a.x) + at, 0), p);
 #pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = s[i] = q[i] = 0.f;
-        if (on) {
-            const int64_t at = t.row * a.C + static_cast<int64_t>(col) * V;
-            load_row<T, V>(a.x, at, p);
-#pragma unroll 4
-            for (int r = c.lane; r < t.rows; r += c.lanes) {
-                float v[V];
-                load_row<T, V>(a.x, at + static_cast<int64_t>(r) * a.C, v);
+        for (int i = 0; i < V; ++i) s[i] = q[i] = 0.f;
+        rows.each([&](int, const float (&v)[V], const float (&)[V]) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float d = v[i] - p[i];
-                    s[i] += d;
-                    q[i] = fmaf(d, d, q[i]);
-                }
+            for (int i = 0; i < V; ++i) {
+                const float d = v[i] - p[i];
+                s[i] += d;
+                q[i] = fmaf(d, d, q[i]);
             }
-        }
+        });
         const int w = min(c.cols, c.ncols - c0) * V;
         const int second = c.lanes * c.cols * V;
         lane_sums<V>(c, s, q, scratch);
@@ -221,60 +348,92 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// One warp per group: joins the tiles' means and squared deviations.
-__device__ void join_stats(const GnArgs &a, int b, int map)
+// The groups' statistics of a map from its tiles' means and squared
+// deviations: `lanes` threads per group take every lanes-th tile each, then
+// the lanes in order.
+__device__ void join_stats(const GnArgs &a, int b, int map, float *smem)
 {
     const GnMap m = a.maps[map];
-    const int n = (m.rows + a.tr - 1) / a.tr;
-    const int lane = threadIdx.x & 31;
-    const float *part = a.part + (static_cast<int64_t>(b) * a.tiles + m.tile0) * a.G * 2;
-    const float inv_rows = 1.f / static_cast<float>(m.rows);
-    for (int g = threadIdx.x >> 5; g < a.G; g += kGnThreads / 32) {
-        // The mean is taken about the first tile's, the deviations about it.
-        const float base = part[g * 2];
-        float s = 0.f;
-        for (int t = lane; t < n; t += 32)
-            s += (part[(static_cast<int64_t>(t) * a.G + g) * 2] - base) * static_cast<float>(min(a.tr, m.rows - t * a.tr));
-        const float mean = base + warp_sum(s) * inv_rows;
-        float q = 0.f;
-        for (int t = lane; t < n; t += 32) {
-            const float *p = part + (static_cast<int64_t>(t) * a.G + g) * 2;
-            const float d = p[0] - mean;
-            q += p[1] + d * d * static_cast<float>(min(a.tr, m.rows - t * a.tr)) * static_cast<float>(a.Cg);
+    const int n = (m.rows + a.tr - 1) / a.tr, tid = threadIdx.x;
+    const float2 *part = reinterpret_cast<const float2 *>(a.part) + (static_cast<int64_t>(b) * a.tiles + m.tile0) * a.G;
+    float2 *out = reinterpret_cast<float2 *>(a.stats) + (static_cast<int64_t>(b) * a.nmaps + map) * a.G;
+    for (int g0 = 0; g0 < a.G; g0 += kGnThreads) {
+        const int w = min(a.G - g0, kGnThreads), lanes = kGnThreads / w, lane = tid / w, g = g0 + tid - lane * w;
+        float mean = 0.f, m2 = 0.f, count = 0.f;
+        if (lane < lanes)
+            for (int t = lane; t < n; t += 8 * lanes) {
+                float2 p[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (t + u * lanes < n) p[u] = __ldcg(part + static_cast<int64_t>(t + u * lanes) * a.G + g);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (t + u * lanes < n) {
+                        const float k = static_cast<float>(min(a.tr, m.rows - (t + u * lanes) * a.tr)), d = p[u].x - mean;
+                        const float share = k / (count + k);
+                        mean = fmaf(d, share, mean);
+                        m2 += p[u].y + d * d * (count * share) * static_cast<float>(a.Cg);
+                        count += k;
+                    }
+            }
+        smem[tid] = mean;
+        smem[kGnThreads + tid] = m2;
+        smem[2 * kGnThreads + tid] = count;
+        __syncthreads();
+        if (tid < w) {
+            for (int l = 1; l < lanes; ++l) {
+                const float k = smem[2 * kGnThreads + l * w + tid];
+                if (k == 0.f) break;
+                const float d = smem[l * w + tid] - mean, share = k / (count + k);
+                mean = fmaf(d, share, mean);
+                m2 += smem[kGnThreads + l * w + tid] + d * d * (count * share) * static_cast<float>(a.Cg);
+                count += k;
+            }
+            out[g] = make_float2(mean, 1.f / sqrtf(m2 / (count * static_cast<float>(a.Cg)) + a.eps));
         }
-        q = warp_sum(q);
-        if (lane == 0) {
-            float *o = a.stats + ((static_cast<int64_t>(b) * a.nmaps + map) * a.G + g) * 2;
-            o[0] = mean;
-            o[1] = 1.f / sqrtf(q * inv_rows / static_cast<float>(a.Cg) + a.eps);
-        }
+        __syncthreads();
     }
 }
 
-template <typename T, int V, int ACT> __device__ void tile_apply(const GnArgs &a, const Tile &t)
+template <typename T, int V> __device__ void tile_nan(const GnArgs &a, const Tile &t)
+{
+    float nan[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) nan[i] = NAN;
+    for (int i = threadIdx.x; i < t.rows * (a.C / V); i += kGnThreads) store_row<T, V>(a.y, t.row * a.C + static_cast<int64_t>(i) * V, nan);
+}
+
+template <typename T, int V, int ACT, typename Ready> __device__ void tile_apply(const GnArgs &a, const Tile &t, Ready ready)
 {
     const Cover c = cover<V>(a.C);
-    if (!c.on) return;
     const float *st = a.stats + (static_cast<int64_t>(t.b) * a.nmaps + t.map) * a.G * 2;
     const int aff = a.affine_scales ? a.maps[t.map].scale * a.C : 0;
-    for (int col = c.col; col < c.ncols; col += c.cols) {
+    for (int c0 = 0; c0 < c.ncols; c0 += c.cols) {
+        const int col = c0 + c.col;
+        const bool on = c.on && col < c.ncols;
+        const int64_t at = t.row * a.C + static_cast<int64_t>(on ? col : 0) * V;
+        Rows<T, V, false, true, kFwdRows<T, V>> rows;
+        rows.begin(c, on, t.rows, a.C, a.x, a.x, at);
         float mean[V], mul[V], add[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int ch = col * V + i, g = ch / a.Cg;
-            mean[i] = st[g * 2];
-            mul[i] = st[g * 2 + 1] * a.gamma[aff + ch];
+            const int ch = (on ? col : 0) * V + i;
+            mul[i] = a.gamma[aff + ch];
             add[i] = a.beta[aff + ch];
         }
-        const int64_t at = t.row * a.C + static_cast<int64_t>(col) * V;
-#pragma unroll 4
-        for (int r = c.lane; r < t.rows; r += c.lanes) {
-            float v[V];
-            load_row<T, V>(a.x, at + static_cast<int64_t>(r) * a.C, v);
+        if (c0 == 0 && !ready()) return tile_nan<T, V>(a, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int g = static_cast<int>(a.div_Cg.div((on ? col : 0) * V + i));
+            const float2 ms = __ldcg(reinterpret_cast<const float2 *>(st) + g);
+            mean[i] = ms.x;
+            mul[i] *= ms.y;
+        }
+        rows.each([&](int o, float (&v)[V], const float (&)[V]) {
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = act_of<ACT>(fmaf(v[i] - mean[i], mul[i], add[i]));
-            store_row<T, V>(a.y, at + static_cast<int64_t>(r) * a.C, v);
-        }
+            store_row<T, V>(a.y, at + o, v);
+        });
     }
 }
 
@@ -289,34 +448,30 @@ template <typename T, int V, int ACT> __device__ void tile_sums(const GnArgs &a,
     float *part = a.part + static_cast<int64_t>(id) * 2 * a.C;
     for (int c0 = 0; c0 < c.ncols; c0 += c.cols) {
         const int col = c0 + c.col;
-        float p[V], q[V];
+        const bool on = c.on && col < c.ncols;
+        const int64_t at = t.row * a.C + static_cast<int64_t>(on ? col : 0) * V;
+        Rows<T, V, true, false, kBwdRows<T, V>> rows;
+        rows.begin(c, on, t.rows, a.C, a.x, a.g, at);
+        float p[V], q[V], mean[V], rstd[V], gam[V], bet[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = q[i] = 0.f;
-        if (c.on && col < c.ncols) {
-            float mean[V], rstd[V], gam[V], bet[V];
+        for (int i = 0; i < V; ++i) {
+            const int ch = (on ? col : 0) * V + i, g = static_cast<int>(a.div_Cg.div(ch));
+            const float2 ms = __ldg(reinterpret_cast<const float2 *>(st) + g);
+            mean[i] = ms.x;
+            rstd[i] = ms.y;
+            gam[i] = a.gamma[aff + ch];
+            bet[i] = a.beta[aff + ch];
+            p[i] = q[i] = 0.f;
+        }
+        rows.each([&](int, const float (&v)[V], const float (&h)[V]) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int ch = col * V + i, g = ch / a.Cg;
-                mean[i] = st[g * 2];
-                rstd[i] = st[g * 2 + 1];
-                gam[i] = a.gamma[aff + ch];
-                bet[i] = a.beta[aff + ch];
+                const float n = (v[i] - mean[i]) * rstd[i];
+                const float d = h[i] * act_slope<ACT>(fmaf(n, gam[i], bet[i]));
+                p[i] += d;
+                q[i] = fmaf(d, n, q[i]);
             }
-            const int64_t at = t.row * a.C + static_cast<int64_t>(col) * V;
-#pragma unroll 4
-            for (int r = c.lane; r < t.rows; r += c.lanes) {
-                float v[V], h[V];
-                load_row<T, V>(a.x, at + static_cast<int64_t>(r) * a.C, v);
-                load_row<T, V>(a.g, at + static_cast<int64_t>(r) * a.C, h);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float n = (v[i] - mean[i]) * rstd[i];
-                    const float d = h[i] * act_slope<ACT>(fmaf(n, gam[i], bet[i]));
-                    p[i] += d;
-                    q[i] = fmaf(d, n, q[i]);
-                }
-            }
-        }
+        });
         const int w = min(c.cols, c.ncols - c0) * V;
         const int second = c.lanes * c.cols * V;
         lane_sums<V>(c, p, q, smem);
@@ -328,130 +483,256 @@ template <typename T, int V, int ACT> __device__ void tile_sums(const GnArgs &a,
     }
 }
 
-// Joins the tiles of (b, map): the channels' sums and the groups' means.
-__device__ void join_sums(const GnArgs &a, int b, int map, float *smem)
+// The sums of h and h*n over a map, for the groups [g0, g1), from its tiles',
+// and the groups' means of gamma*h and gamma*h*n. `lanes` threads per channel
+// and sum take every lanes-th tile each, then the lanes in order.
+__device__ void join_sums(const GnArgs &a, int b, int map, int g0, int g1, float *smem)
 {
     const GnMap m = a.maps[map];
-    const int n = (m.rows + a.tr - 1) / a.tr;
+    const int n = (m.rows + a.tr - 1) / a.tr, tid = threadIdx.x, first = g0 * a.Cg, channels = (g1 - g0) * a.Cg;
     const float *part = a.part + (static_cast<int64_t>(b) * a.tiles + m.tile0) * 2 * a.C;
     float *sums = a.sums + (static_cast<int64_t>(b) * a.nmaps + map) * 2 * a.C;
-    const int aff = a.affine_scales ? m.scale * a.C : 0;
-    for (int i = threadIdx.x; i < 2 * a.C; i += kGnThreads) {
+    for (int i0 = 0; i0 < 2 * channels; i0 += kGnThreads) {
+        const int w = min(2 * channels - i0, kGnThreads), lanes = kGnThreads / w, lane = tid / w, i = i0 + tid - lane * w;
+        const int at = i < channels ? first + i : a.C + first + i - channels;
         float s = 0.f;
-#pragma unroll 8
-        for (int t = 0; t < n; ++t) s += part[static_cast<int64_t>(t) * 2 * a.C + i];
-        sums[i] = s;
-        smem[i] = s * a.gamma[aff + (i >= a.C ? i - a.C : i)];
+        if (lane < lanes)
+            for (int t = lane; t < n; t += 16 * lanes) {
+                float p[16];
+#pragma unroll
+                for (int u = 0; u < 16; ++u) p[u] = t + u * lanes < n ? __ldcg(part + static_cast<int64_t>(t + u * lanes) * 2 * a.C + at) : 0.f;
+#pragma unroll
+                for (int u = 0; u < 16; ++u) s += p[u];
+            }
+        smem[tid] = s;
+        __syncthreads();
+        if (tid < w) {
+            for (int l = 1; l < lanes; ++l) s += smem[l * w + tid];
+            sums[at] = s;
+        }
+        __syncthreads();
     }
-    __syncthreads();
+    const int aff = a.affine_scales ? m.scale * a.C : 0;
     const float inv = 1.f / (static_cast<float>(m.rows) * static_cast<float>(a.Cg));
-    for (int i = threadIdx.x; i < 2 * a.G; i += kGnThreads) {
+    for (int i = 2 * g0 + tid; i < 2 * g1; i += kGnThreads) {
         const int g = i >> 1, base = (i & 1) * a.C + g * a.Cg;
         float s = 0.f;
-        for (int j = 0; j < a.Cg; ++j) s += smem[base + j];
+        for (int j = 0; j < a.Cg; ++j) s = fmaf(__ldcg(sums + base + j), a.gamma[aff + g * a.Cg + j], s);
         a.group[(static_cast<int64_t>(b) * a.nmaps + map) * a.G * 2 + i] = s * inv;
+    }
+    __syncthreads();
+}
+
+// grad_gamma and grad_beta: the maps' sums in the order (batch item, map).
+__device__ void param_grads(const GnArgs &a)
+{
+    const int scales = a.affine_scales ? a.S : 1, maps = a.B * a.nmaps;
+    for (int i = threadIdx.x; i < 2 * scales * a.C; i += kGnThreads) {
+        const int which = i >= scales * a.C, at = i - which * scales * a.C, s = at / a.C, ch = at - s * a.C;
+        const float *p = a.sums + which * a.C + ch;
+        float sum = 0.f;
+        if (a.affine_scales) {
+#pragma unroll 4
+            for (int m = s; m < maps; m += a.S) sum += __ldcg(p + static_cast<int64_t>(m) * 2 * a.C);  // map (k, s) is k*S + s
+        } else {
+#pragma unroll 16
+            for (int m = 0; m < maps; ++m) sum += __ldcg(p + static_cast<int64_t>(m) * 2 * a.C);
+        }
+        (which ? a.grad_gamma : a.grad_beta)[at] = sum;
     }
 }
 
-template <typename T, int V, int ACT> __device__ void tile_grad(const GnArgs &a, const Tile &t)
+template <typename T, int V, int ACT, typename Ready> __device__ void tile_grad(const GnArgs &a, const Tile &t, Ready ready)
 {
     const Cover c = cover<V>(a.C);
-    if (!c.on) return;
     const int64_t bm = static_cast<int64_t>(t.b) * a.nmaps + t.map;
     const float *st = a.stats + bm * a.G * 2, *gr = a.group + bm * a.G * 2;
     const int aff = a.affine_scales ? a.maps[t.map].scale * a.C : 0;
-    for (int col = c.col; col < c.ncols; col += c.cols) {
-        float mean[V], rstd[V], gam[V], bet[V], m1[V], m2[V];
+    for (int c0 = 0; c0 < c.ncols; c0 += c.cols) {
+        const int col = c0 + c.col;
+        const bool on = c.on && col < c.ncols;
+        const int64_t at = t.row * a.C + static_cast<int64_t>(on ? col : 0) * V;
+        Rows<T, V, true, true, kBwdRows<T, V>> rows;
+        rows.begin(c, on, t.rows, a.C, a.x, a.g, at);
+        float mean[V], rstd[V], gam[V], bet[V], m1[V], m2[V];  // the last two times rstd
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int ch = col * V + i, g = ch / a.Cg;
-            mean[i] = st[g * 2];
-            rstd[i] = st[g * 2 + 1];
-            m1[i] = gr[g * 2];
-            m2[i] = gr[g * 2 + 1];
+            const int ch = (on ? col : 0) * V + i, g = static_cast<int>(a.div_Cg.div(ch));
+            const float2 ms = __ldg(reinterpret_cast<const float2 *>(st) + g);
+            mean[i] = ms.x;
+            rstd[i] = ms.y;
             gam[i] = a.gamma[aff + ch];
             bet[i] = a.beta[aff + ch];
         }
-        const int64_t at = t.row * a.C + static_cast<int64_t>(col) * V;
-#pragma unroll 2
-        for (int r = c.lane; r < t.rows; r += c.lanes) {
-            float v[V], h[V];
-            load_row<T, V>(a.x, at + static_cast<int64_t>(r) * a.C, v);
-            load_row<T, V>(a.g, at + static_cast<int64_t>(r) * a.C, h);
+        if (c0 == 0 && !ready()) return tile_nan<T, V>(a, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int g = static_cast<int>(a.div_Cg.div((on ? col : 0) * V + i));
+            const float2 gm = __ldcg(reinterpret_cast<const float2 *>(gr) + g);
+            m1[i] = rstd[i] * gm.x;
+            m2[i] = rstd[i] * gm.y;
+        }
+        rows.each([&](int o, float (&v)[V], const float (&h)[V]) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float n = (v[i] - mean[i]) * rstd[i];
                 const float d = h[i] * act_slope<ACT>(fmaf(n, gam[i], bet[i]));
-                v[i] = rstd[i] * (fmaf(gam[i], d, -m1[i]) - n * m2[i]);
+                v[i] = fmaf(gam[i] * rstd[i], d, -m1[i]) - n * m2[i];
             }
-            store_row<T, V>(a.y, at + static_cast<int64_t>(r) * a.C, v);
-        }
+            store_row<T, V>(a.y, at + o, v);
+        });
     }
 }
 
-// ---- kernels ---------------------------------------------------------------
+// ---- the queue -------------------------------------------------------------
 
-template <typename T, int V> __global__ void __launch_bounds__(kGnThreads) gn_stats_kernel(const __grid_constant__ GnArgs a)
+__device__ uint32_t g_gn_gave_up;
+
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t *p)
+{
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+enum ItemKind : int { kSums, kOutputs, kJoin };
+
+struct Item {
+    int kind, part, id;  // id: a tile's, or (batch item, map)'s
+    Tile t;
+};
+
+// Tickets before tile p's sums, joins aside: sums and outputs alternate, the
+// outputs `lag` tiles behind.
+__device__ __forceinline__ int tickets_before(const GnArgs &a, int p) { return p < a.lag ? p : 2 * p - a.lag; }
+
+// The work of ticket i. The joins of a map come right after its last tile's sums.
+__device__ __forceinline__ Item item_of(const GnArgs &a, int ticket)
+{
+    // Maps, over all batch items, whose joins come at or before the ticket.
+    int lo = 0, hi = a.B * a.nmaps;
+    const auto joins_at = [&](int i) {
+        const int b = i / a.nmaps, m = i - b * a.nmaps;
+        const int last = b * a.tiles + (m + 1 < a.nmaps ? a.maps[m + 1].tile0 : a.tiles) - 1;
+        return tickets_before(a, last) + 1 + i * a.joins;
+    };
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (joins_at(mid) <= ticket) lo = mid + 1; else hi = mid;
+    }
+    Item it;
+    it.part = lo > 0 ? ticket - joins_at(lo - 1) : a.joins;
+    if (it.part < a.joins) {
+        it.kind = kJoin;
+        it.id = lo - 1;
+        it.t.b = it.id / a.nmaps;
+        it.t.map = it.id - it.t.b * a.nmaps;
+        return it;
+    }
+    const int i = ticket - lo * a.joins, j = i - a.lag;
+    if (j < 0) {
+        it.kind = kSums;
+        it.id = i;
+    } else if (j < 2 * (a.ntiles - a.lag)) {
+        it.kind = j & 1 ? kOutputs : kSums;
+        it.id = j & 1 ? j >> 1 : a.lag + (j >> 1);
+    } else {
+        it.kind = kOutputs;
+        it.id = i - a.ntiles;
+    }
+    it.t = find_tile(a, it.id);
+    return it;
+}
+
+__device__ __forceinline__ bool wait_for(const uint32_t *counter, uint32_t want)
+{
+    for (int i = 0; i < kGnTries; ++i) {
+        if (load_acquire(counter) >= want) return true;
+        __nanosleep(100);
+    }
+    atomicOr(&g_gn_gave_up, 1u);
+    return false;
+}
+
+template <typename T, int V, int ACT, bool BACKWARD>
+__global__ void __launch_bounds__(kGnThreads, kGnCtas) gn_kernel(const __grid_constant__ GnArgs a)
 {
     extern __shared__ float smem[];
-    tile_stats<T, V>(a, find_tile(a, blockIdx.x), blockIdx.x, smem);
-}
-
-__global__ void __launch_bounds__(kGnThreads) gn_join_stats_kernel(const __grid_constant__ GnArgs a)
-{
-    join_stats(a, blockIdx.x / a.nmaps, blockIdx.x % a.nmaps);
-}
-
-template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kGnThreads) gn_apply_kernel(const __grid_constant__ GnArgs a)
-{
-    tile_apply<T, V, ACT>(a, find_tile(a, blockIdx.x));
-}
-
-template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kGnThreads) gn_sums_kernel(const __grid_constant__ GnArgs a)
-{
-    extern __shared__ float smem[];
-    tile_sums<T, V, ACT>(a, find_tile(a, blockIdx.x), blockIdx.x, smem);
-}
-
-__global__ void __launch_bounds__(kGnThreads) gn_join_sums_kernel(const __grid_constant__ GnArgs a)
-{
-    extern __shared__ float smem[];
-    join_sums(a, blockIdx.x / a.nmaps, blockIdx.x % a.nmaps, smem);
-}
-
-template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kGnThreads) gn_grad_kernel(const __grid_constant__ GnArgs a)
-{
-    tile_grad<T, V, ACT>(a, find_tile(a, blockIdx.x));
-}
-
-// grad_gamma and grad_beta: the maps' sums in the order (batch item, map).
-__global__ void __launch_bounds__(kGnThreads) gn_param_kernel(const __grid_constant__ GnArgs a)
-{
-    const int scales = a.affine_scales ? a.S : 1;
-    const int i = blockIdx.x * kGnThreads + threadIdx.x;
-    if (i >= scales * a.C) return;
-    const int s = i / a.C, ch = i - s * a.C;
-    float sg = 0.f, sb = 0.f;
-    for (int b = 0; b < a.B; ++b)
-        for (int m = 0; m < a.nmaps; ++m) {
-            if (a.affine_scales && a.maps[m].scale != s) continue;
-            const float *p = a.sums + (static_cast<int64_t>(b) * a.nmaps + m) * 2 * a.C + ch;
-            sb += p[0];
-            sg += p[a.C];
+    __shared__ Item item;
+    __shared__ uint32_t flag;
+    if (threadIdx.x == 0) {
+        item = item_of(a, static_cast<int>(atomicAdd(a.queue, 1u)));
+        flag = item.kind != kJoin || wait_for(a.tiles_done + static_cast<int64_t>(item.t.b) * a.nmaps + item.t.map,
+                                              (a.maps[item.t.map].rows + a.tr - 1) / a.tr);
+    }
+    __syncthreads();
+    const Tile t = item.t;
+    const int kind = item.kind;
+    const int64_t bm = static_cast<int64_t>(t.b) * a.nmaps + t.map;
+    if (kind == kOutputs) {
+        const auto ready = [&] {
+            if (threadIdx.x == 0) flag = wait_for(a.ready + bm, a.joins);
+            __syncthreads();
+            return flag != 0;
+        };
+        if (BACKWARD) tile_grad<T, V, ACT>(a, t, ready);
+        else tile_apply<T, V, ACT>(a, t, ready);
+    } else if (kind == kSums) {
+        if (BACKWARD) tile_sums<T, V, ACT>(a, t, item.id, smem);
+        else tile_stats<T, V>(a, t, item.id, smem);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            __threadfence();
+            atomicAdd(a.tiles_done + bm, 1u);
         }
-    a.grad_gamma[i] = sg;
-    a.grad_beta[i] = sb;
+    } else if (flag) {  // without the join its outputs' waits run out
+        const int part = item.part;
+        if (BACKWARD) join_sums(a, t.b, t.map, part * a.G / a.joins, (part + 1) * a.G / a.joins, smem);
+        else join_stats(a, t.b, t.map, smem);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            __threadfence();
+            atomicAdd(a.ready + bm, 1u);
+            if (BACKWARD) {
+                flag = atomicAdd(a.all_done, 1u) + 1 == static_cast<uint32_t>(a.B * a.nmaps * a.joins);
+                __threadfence();
+            }
+        }
+        __syncthreads();
+        if (BACKWARD && flag) param_grads(a);
+    }
 }
+
+// Maps of at most kGnSmall bytes: one CTA takes a map from its sums to its
+// outputs, without tickets, counters or waits.
+template <typename T, int V, int ACT, bool BACKWARD>
+__global__ void __launch_bounds__(kGnThreads, kGnCtas) gn_small_kernel(const __grid_constant__ GnArgs a)
+{
+    extern __shared__ float smem[];
+    const Tile t = find_tile(a, blockIdx.x);  // a tile is a whole map
+    const auto ready = [] { return true; };
+    if (BACKWARD) tile_sums<T, V, ACT>(a, t, blockIdx.x, smem);
+    else tile_stats<T, V>(a, t, blockIdx.x, smem);
+    __syncthreads();
+    if (BACKWARD) join_sums(a, t.b, t.map, 0, a.G, smem);
+    else join_stats(a, t.b, t.map, smem);
+    __syncthreads();
+    if (BACKWARD) tile_grad<T, V, ACT>(a, t, ready);
+    else tile_apply<T, V, ACT>(a, t, ready);
+    if (BACKWARD && gridDim.x == 1) param_grads(a);
+}
+
+__global__ void __launch_bounds__(kGnThreads) gn_param_kernel(const __grid_constant__ GnArgs a) { param_grads(a); }
 
 struct GnPlan {
     GnArgs a;
-    int elem, vec;     // bytes of an element, elements per access
+    int elem;          // bytes of an element
+    bool small;        // every map within kGnSmall bytes
+    bool wide;         // rows of whole 16-byte pieces: four channels to an access
     int64_t ntiles;    // B * tiles
     int64_t gaps;      // rows of no map, per batch item
-    size_t part, sums, group, total;  // workspace offsets and size
+    size_t part, sums, group, counters, total;  // workspace offsets and size
+    size_t counter_bytes;
 };
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -494,19 +775,32 @@ da_status gn_plan(const gn_dims *dims, const int32_t *shape, const int32_t *star
         a.maps[i] = GnMap{static_cast<int32_t>(n), st, 0, static_cast<int32_t>(i % d.num_scales)};
         covered += n;
     }
-    // 64-row tiles. Fewer rows per tile only add sums to join; more leave
-    // the smallest maps of a pyramid to too few CTAs.
-    a.tr = 64;
-    int64_t tiles = 0;
+    // Tiles of about 128 KB forward, 64 KB of each tensor backward, less where
+    // that leaves a resident CTA without one, and no fewer than 16 rows. What a
+    // CTA does once (ticket, waits, joins of its rows' sums) takes as long as
+    // some 20 KB: at 6 x 89760 rows of 256 fp32 channels, forward 378 us with
+    // tiles of 32 KB, 260 with 64 and 236 with 128, backward 556, 440 and 428
+    // with 32, 64 and 128; but at 1 x 132000 bf16 rows backward 94, 88 and 95.
+    const int64_t row_bytes = static_cast<int64_t>(d.num_embeds) * (d.feat_dtype == DA_F32 ? 4 : 2);
+    const int64_t by_size = (backward ? 65536 : 131072) / row_bytes, by_count = covered * d.batch / (kGnCtas * 152);
+    const int64_t tr = by_size < by_count ? by_size : by_count;
+    a.tr = static_cast<int32_t>(tr < 16 ? 16 : tr > 512 ? 512 : tr);
+    int64_t tiles = 0, largest = 0, most_rows = 0;
+    for (int i = 0; i < nmaps; ++i) most_rows = a.maps[i].rows > most_rows ? a.maps[i].rows : most_rows;
+    p.small = most_rows * row_bytes <= kGnSmall;
+    if (p.small && most_rows > 0) a.tr = static_cast<int32_t>(most_rows);
     for (int i = 0; i < nmaps; ++i) {
         a.maps[i].tile0 = static_cast<int32_t>(tiles);
-        tiles += (a.maps[i].rows + a.tr - 1) / a.tr;
+        const int64_t n = (a.maps[i].rows + a.tr - 1) / a.tr;
+        tiles += n;
+        largest = n > largest ? n : largest;
     }
     a.rows = d.num_feat_rows;
     a.B = d.batch;
     a.C = d.num_embeds;
     a.G = d.num_groups;
     a.Cg = a.C / a.G;
+    a.div_Cg = FastDiv::make(static_cast<uint32_t>(a.Cg));
     a.nmaps = static_cast<int>(nmaps);
     a.S = d.num_scales;
     a.K = d.num_cams;
@@ -516,7 +810,15 @@ da_status gn_plan(const gn_dims *dims, const int32_t *shape, const int32_t *star
     p.elem = d.feat_dtype == DA_F32 ? 4 : 2;
     p.ntiles = tiles * d.batch;
     p.gaps = d.num_feat_rows - covered;
-    if (p.ntiles > INT32_MAX) return fail(DA_ERR_UNSUPPORTED, "more than 2^31 tiles of %d rows", a.tr);
+    if (p.ntiles > INT32_MAX / 4) return fail(DA_ERR_UNSUPPORTED, "too many tiles of %d rows", a.tr);
+    a.ntiles = static_cast<int32_t>(p.ntiles);
+    // A map's outputs begin two thirds of a resident set of CTAs after its
+    // last sums, which are usually joined by then. Twice and three times as
+    // many measured within 4 % of it; none at all, 30 % slower.
+    const int64_t lag = largest + 2 * 152;
+    a.lag = static_cast<int32_t>(lag < p.ntiles ? lag : p.ntiles);
+    // A backward join reads 2 C floats of each tile: four CTAs share it.
+    a.joins = backward && a.G >= 4 ? 4 : 1;
     const size_t bm = static_cast<size_t>(d.batch) * nmaps;
     size_t at = 0;
     p.part = at;
@@ -525,6 +827,9 @@ da_status gn_plan(const gn_dims *dims, const int32_t *shape, const int32_t *star
     if (backward) at += round256(sizeof(float) * bm * 2 * a.C);
     p.group = at;
     if (backward) at += round256(sizeof(float) * bm * 2 * a.G);
+    p.counters = at;
+    p.counter_bytes = p.ntiles > 0 ? sizeof(uint32_t) * (2 + 2 * bm) : 0;
+    at += round256(p.counter_bytes);
     p.total = at;
     return DA_OK;
 }
@@ -545,8 +850,7 @@ da_status gn_buffers(GnPlan &p, const void *x, const void *g, void *y, const flo
             return fail(DA_ERR_WORKSPACE, "workspace of %zu bytes; %zu are needed", ws ? ws_bytes : size_t{0}, p.total);
         if (!aligned(ws, 256)) return fail(DA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     }
-    const bool wide = a.C * p.elem % 16 == 0 && aligned(x, 16) && aligned(y, 16) && aligned(g, 16);
-    p.vec = wide ? 16 / p.elem : 1;
+    p.wide = a.C * p.elem % 16 == 0 && aligned(x, 16) && aligned(y, 16) && aligned(g, 16);
     a.x = x;
     a.g = g;
     a.y = y;
@@ -557,6 +861,10 @@ da_status gn_buffers(GnPlan &p, const void *x, const void *g, void *y, const flo
     a.part = reinterpret_cast<float *>(w + p.part);
     a.sums = reinterpret_cast<float *>(w + p.sums);
     a.group = reinterpret_cast<float *>(w + p.group);
+    a.queue = reinterpret_cast<uint32_t *>(w + p.counters);
+    a.all_done = a.queue + 1;
+    a.tiles_done = a.queue + 2;
+    a.ready = a.tiles_done + static_cast<int64_t>(a.B) * a.nmaps;
     return DA_OK;
 }
 
@@ -584,41 +892,38 @@ da_status gn_zero_gaps(const GnPlan &p, cudaStream_t st)
     return DA_OK;
 }
 
-template <typename T, int V, int ACT> cudaError_t forward_launch(const GnPlan &p, cudaStream_t st)
+template <typename T, int V, int ACT, bool BACKWARD> cudaError_t width_launch(const GnPlan &p, cudaStream_t st)
 {
-    const unsigned n = static_cast<unsigned>(p.ntiles);
-    const size_t smem = sizeof(float) * (2 * kGnThreads * V + 2 * p.a.C);
-    gn_stats_kernel<T, V><<<n, kGnThreads, smem, st>>>(p.a);
-    gn_join_stats_kernel<<<p.a.B * p.a.nmaps, kGnThreads, 0, st>>>(p.a);
-    gn_apply_kernel<T, V, ACT><<<n, kGnThreads, 0, st>>>(p.a);
+    const size_t lanes = 2 * kGnThreads * V + (BACKWARD ? 0 : 2 * p.a.C), smem = sizeof(float) * (lanes < 3 * kGnThreads ? 3 * kGnThreads : lanes);
+    if (p.small) {
+        gn_small_kernel<T, V, ACT, BACKWARD><<<static_cast<unsigned>(p.ntiles), kGnThreads, smem, st>>>(p.a);
+        if (BACKWARD && p.ntiles > 1) gn_param_kernel<<<1, kGnThreads, 0, st>>>(p.a);
+        return cudaGetLastError();
+    }
+    const cudaError_t e = cudaMemsetAsync(p.a.queue, 0, p.counter_bytes, st);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(2 * p.ntiles + p.a.B * p.a.nmaps * p.a.joins);
+    gn_kernel<T, V, ACT, BACKWARD><<<grid, kGnThreads, smem, st>>>(p.a);
     return cudaGetLastError();
 }
 
-template <typename T, int V, int ACT> cudaError_t backward_launch(const GnPlan &p, cudaStream_t st)
+template <typename T, int ACT, bool BACKWARD> cudaError_t queue_launch(const GnPlan &p, cudaStream_t st)
 {
-    const unsigned n = static_cast<unsigned>(p.ntiles);
-    gn_sums_kernel<T, V, ACT><<<n, kGnThreads, sizeof(float) * 2 * kGnThreads * V, st>>>(p.a);
-    gn_join_sums_kernel<<<p.a.B * p.a.nmaps, kGnThreads, sizeof(float) * 2 * p.a.C, st>>>(p.a);
-    gn_grad_kernel<T, V, ACT><<<n, kGnThreads, 0, st>>>(p.a);
-    return cudaGetLastError();
+    return p.wide ? width_launch<T, 4, ACT, BACKWARD>(p, st) : width_launch<T, 1, ACT, BACKWARD>(p, st);
 }
 
-template <typename T, int V> cudaError_t launch_act(const GnPlan &p, int act, bool backward, cudaStream_t st)
+template <typename T> cudaError_t launch_act(const GnPlan &p, int act, bool backward, cudaStream_t st)
 {
-    if (act == GN_ACT_RELU) return backward ? backward_launch<T, V, GN_ACT_RELU>(p, st) : forward_launch<T, V, GN_ACT_RELU>(p, st);
-    if (act == GN_ACT_SILU) return backward ? backward_launch<T, V, GN_ACT_SILU>(p, st) : forward_launch<T, V, GN_ACT_SILU>(p, st);
-    return backward ? backward_launch<T, V, GN_ACT_NONE>(p, st) : forward_launch<T, V, GN_ACT_NONE>(p, st);
+    if (act == GN_ACT_RELU) return backward ? queue_launch<T, GN_ACT_RELU, true>(p, st) : queue_launch<T, GN_ACT_RELU, false>(p, st);
+    if (act == GN_ACT_SILU) return backward ? queue_launch<T, GN_ACT_SILU, true>(p, st) : queue_launch<T, GN_ACT_SILU, false>(p, st);
+    return backward ? queue_launch<T, GN_ACT_NONE, true>(p, st) : queue_launch<T, GN_ACT_NONE, false>(p, st);
 }
 
 cudaError_t gn_launch(const GnPlan &p, int dtype, int act, bool backward, cudaStream_t st)
 {
-    const bool wide = p.vec > 1;
-    switch (dtype) {
-    case DA_F32: return wide ? launch_act<float, 4>(p, act, backward, st) : launch_act<float, 1>(p, act, backward, st);
-    case DA_BF16:
-        return wide ? launch_act<__nv_bfloat16, 8>(p, act, backward, st) : launch_act<__nv_bfloat16, 1>(p, act, backward, st);
-    default: return wide ? launch_act<__half, 8>(p, act, backward, st) : launch_act<__half, 1>(p, act, backward, st);
-    }
+    if (dtype == DA_F32) return launch_act<float>(p, act, backward, st);
+    if (dtype == DA_BF16) return launch_act<__nv_bfloat16>(p, act, backward, st);
+    return launch_act<__half>(p, act, backward, st);
 }
 
 }  // namespace
@@ -674,12 +979,24 @@ da_status gn_backward(const gn_dims *dims, const void *feat, const int32_t *spat
         const cudaError_t e = da::gn_launch(p, dims->feat_dtype, dims->act, true, cs);
         if (e != cudaSuccess) return da::cuda_fail(e, "group norm backward launch");
     }
-    if (params > 0) {
-        da::gn_param_kernel<<<(params + da::kGnThreads - 1) / da::kGnThreads, da::kGnThreads, 0, cs>>>(p.a);
-        const cudaError_t e = cudaGetLastError();
+    if (p.ntiles == 0 && params > 0) {  // sums over nothing
+        cudaError_t e = cudaMemsetAsync(grad_gamma, 0, sizeof(float) * params, cs);
+        if (e == cudaSuccess) e = cudaMemsetAsync(grad_beta, 0, sizeof(float) * params, cs);
         if (e != cudaSuccess) return da::cuda_fail(e, "group norm parameter gradients");
     }
     return DA_OK;
+}
+
+da_status gn_device_status(uint32_t *gave_up, da_stream_t stream)
+{
+    if (!gave_up) return da::fail(DA_ERR_NULL, "gave_up is NULL");
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    void *word = nullptr;
+    cudaError_t e = cudaGetSymbolAddress(&word, da::g_gn_gave_up);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(gave_up, word, sizeof *gave_up, cudaMemcpyDeviceToHost, cs);
+    if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof *gave_up, cs);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(cs);
+    return e == cudaSuccess ? DA_OK : da::cuda_fail(e, "status word");
 }
 
 }  // extern "C"

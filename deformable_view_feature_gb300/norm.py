@@ -19,7 +19,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import DA_BF16, DA_F16, DA_F32, _check, _dptr, _host_i32, load_library
+from . import DA_BF16, DA_F16, DA_F32, _check, _dptr, _host_i32, _on_stream, load_library
 
 __all__ = ["gn_forward", "gn_backward", "GroupNormActFunction", "GN_ACTIVATIONS"]
 
@@ -86,12 +86,12 @@ def gn_forward(feat: torch.Tensor, spatial_shape, level_start_index, gamma: torc
     lib = load_library()
     ss, ls, ssp, lsp = _tables(spatial_shape, level_start_index)
     d = _gn_dims(feat, ss, ls, gamma, beta, num_groups, eps, act)
-    with torch.cuda.stream(stream):
+    with _on_stream(stream, feat.device) as handle:
         out = _like(out, "out", feat.shape, feat.dtype, feat.device)
         stats = torch.empty(d.batch, d.num_cams, d.num_scales, d.num_groups, 2, dtype=torch.float32, device=feat.device)
         ws = _scratch(lib, d, ssp, lsp, 0, feat.device)
         _check(lib.gn_forward(ctypes.byref(d), _dptr(feat), ssp, lsp, _dptr(gamma), _dptr(beta), _dptr(out),
-                              _dptr(stats), _dptr(ws), ws.numel(), torch.cuda.current_stream().cuda_stream or None))
+                              _dptr(stats), _dptr(ws), ws.numel(), handle))
     return out, stats
 
 
@@ -107,13 +107,13 @@ def gn_backward(feat: torch.Tensor, spatial_shape, level_start_index, gamma: tor
     if grad_out.shape != feat.shape or grad_out.dtype != feat.dtype:
         raise ValueError("grad_out must have feat's shape and type")
     _like(stats, "stats", (d.batch, d.num_cams, d.num_scales, d.num_groups, 2), torch.float32, feat.device)
-    with torch.cuda.stream(stream):
+    with _on_stream(stream, feat.device) as handle:
         grad_feat = _like(grad_feat, "grad_feat", feat.shape, feat.dtype, feat.device)
         grad_gamma, grad_beta = torch.empty_like(gamma), torch.empty_like(beta)
         ws = _scratch(lib, d, ssp, lsp, 1, feat.device)
         _check(lib.gn_backward(ctypes.byref(d), _dptr(feat), ssp, lsp, _dptr(gamma), _dptr(beta), _dptr(stats),
                                _dptr(grad_out), _dptr(grad_feat), _dptr(grad_gamma), _dptr(grad_beta), _dptr(ws),
-                               ws.numel(), torch.cuda.current_stream().cuda_stream or None))
+                               ws.numel(), handle))
     return grad_feat, grad_gamma, grad_beta
 
 

@@ -88,6 +88,14 @@ da_status gn_backward(const gn_dims *dims, const void *feat, const int32_t *spat
                       const void *grad_out, void *grad_feat, float *grad_gamma, float *grad_beta, void *workspace,
                       size_t workspace_bytes, da_stream_t stream);
 
+/*
+ * Tiles whose outputs wait for their map's statistics stop waiting after a
+ * bounded number of tries; that sets a word on the device and leaves NaN or
+ * nothing in the tiles' outputs (neither happens in a sound run). This call waits for
+ * `stream`, reads the word into *gave_up (host) and clears it.
+ */
+da_status gn_device_status(uint32_t *gave_up, da_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
