@@ -81,7 +81,7 @@ template <int DP, int VP> struct GradQShared {
                          bytes = at_s + 2 * s;
 };
 
-struct QKeyInfo {
+struct alignas(16) QKeyInfo {
     int pos[kStep];
     uint32_t valid[2];
     int lo, hi;
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __shared__ float part[2][2][kOwn];
     float *table = reinterpret_cast<float *>(base + F::bytes);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
     const int LP = kOwn / a.G;
     const int n = blockIdx.y, b = blockIdx.z, l0 = blockIdx.x * LP;
     const int len = dattn_length(a, b);
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = bars.tmem;
+    const uint32_t tmem = uniform(bars.tmem);
     volatile uint32_t *gave_up = &bars.gave_up;
     // Scores and e of two steps, 64 columns each, then grad_q of each map.
     auto tS = [&](int buf, int which) { return tmem + buf * 192 + which * 64; };
@@ -174,42 +174,52 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
         }
     } else if (warp == 9) {
-        if (lane == 0 && T_ > 0) {
+        if (T_ > 0) {
+            const bool issue = elect();
             constexpr uint32_t is = shape(is_bf16<T>, kStep, false), iq = shape(is_bf16<T>, DP, true);
+            const Operand<F::row> dq = along_row<F::row>(sbase), dk = along_row<F::row>(sbase + F::at_stage),
+                                  dkr = over_rows<F::row>(sbase + F::at_stage, F::k);
+            const Operand<128> dg = along_row<128>(sbase + F::at_g), dv = along_row<128>(sbase + F::at_stage + 2 * F::k),
+                               ds = along_row<128>(sbase + F::at_s);
             auto scores = [&](int t) {
-                const uint32_t st = sbase + F::at_stage + (t % NS) * F::stage;
-                bar_wait(&bars.kv_full[t % NS], (t / NS) & 1, gave_up);
-                bar_wait(&bars.ready[t % NS], (t / NS) & 1, gave_up);
+                const uint32_t st = (t % NS) * F::stage;
+                bar_wait_warp(&bars.kv_full[t % NS], (t / NS) & 1, gave_up);
+                bar_wait_warp(&bars.ready[t % NS], (t / NS) & 1, gave_up);
                 fence_after();
+                if (issue) {
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < DP / 16; ++i)
-                        mma_ss(tS(t & 1, m), along_row<F::row>(sbase + m * F::q, i), along_row<F::row>(st + m * F::k, i), is, i > 0);
+                        for (int i = 0; i < DP / 16; ++i)
+                            mma_ss(tS(t & 1, m), dq.at(m * F::q + i * 32), dk.at(st + m * F::k + i * 32), is, i > 0);
 #pragma unroll
-                for (int i = 0; i < VP / 16; ++i)
-                    mma_ss(tS(t & 1, 2), along_row<128>(sbase + F::at_g + (i / 4) * F::g, i % 4),
-                           along_row<128>(st + 2 * F::k + (i / 4) * F::v, i % 4), is, i > 0);
-                mma_commit(&bars.s_full[t & 1]);
+                    for (int i = 0; i < VP / 16; ++i)
+                        mma_ss(tS(t & 1, 2), dg.at((i / 4) * F::g + (i % 4) * 32), dv.at(st + (i / 4) * F::v + (i % 4) * 32), is, i > 0);
+                    mma_commit(&bars.s_full[t & 1]);
+                }
+                __syncwarp();
             };
-            bar_wait(&bars.q_full, 0, gave_up);
+            bar_wait_warp(&bars.q_full, 0, gave_up);
             scores(0);
             for (int t = 0; t < T_; ++t) {
                 if (t + 1 < T_) scores(t + 1);  // its columns were read by the end of step t - 1
-                bar_wait(&bars.ds_full, t & 1, gave_up);
+                bar_wait_warp(&bars.ds_full, t & 1, gave_up);
                 fence_after();
-                const uint32_t st = sbase + F::at_stage + (t % NS) * F::stage;
+                if (issue) {
+                    const uint32_t st = (t % NS) * F::stage;
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < kStep / 16; ++i)
-                        mma_ss(tQ(m), along_row<128>(sbase + F::at_s + m * F::s, i), over_rows<F::row>(st + m * F::k, i, F::k), iq,
-                               t > 0 || i > 0);
-                mma_commit(&bars.ds_free);
-                mma_commit(&bars.kv_empty[t % NS]);
+                        for (int i = 0; i < kStep / 16; ++i)
+                            mma_ss(tQ(m), ds.at(m * F::s + i * 32), dkr.at(st + m * F::k + i * 16 * F::row), iq, t > 0 || i > 0);
+                    mma_commit(&bars.ds_free);
+                    mma_commit(&bars.kv_empty[t % NS]);
+                }
+                __syncwarp();
             }
-            mma_commit(&bars.fin);
+            if (issue) mma_commit(&bars.fin);
             bar_drain(&bars.fin, 0);
+            __syncwarp();
         }
     } else if (warp == 10) {
         for (int t = 0; t < T_; ++t) {
@@ -397,7 +407,7 @@ template <int DP, int VP> struct GradKVShared {
 };
 
 // Per-query values of a step, the queries' positions among them.
-struct QueryInfo {
+struct alignas(16) QueryInfo {
     float nlse[2][kStep], nd[2][kStep];  // minus the log-sums, minus d_m
     int pos[kStep];
     int lo, hi;
@@ -429,7 +439,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint8_t *bucket = reinterpret_cast<uint8_t *>(table + span);
     float *sums = reinterpret_cast<float *>(bucket + (span + 3) / 4 * 4);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
     const int n = blockIdx.y, b = blockIdx.z, j0 = blockIdx.x * kOwn;
     const int len = dattn_length(a, b);
     int first = 0;
@@ -465,7 +475,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = bars.tmem;
+    const uint32_t tmem = uniform(bars.tmem);
     volatile uint32_t *gave_up = &bars.gave_up;
     auto tS = [&](int which) { return tmem + which * 64; };
     const uint32_t tV = tmem + 192;
@@ -491,48 +501,57 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
         }
     } else if (warp == 9) {
-        if (lane == 0 && T_ > 0) {
+        if (T_ > 0) {
+            const bool issue = elect();
             constexpr uint32_t is = shape(is_bf16<T>, kStep, false), iv = shape(is_bf16<T>, VP, true),
                                ik = shape(is_bf16<T>, DP, true);
+            const Operand<F::row> dk = along_row<F::row>(sbase), dq = along_row<F::row>(sbase + F::at_stage),
+                                  dqr = over_rows<F::row>(sbase + F::at_stage, F::q);
+            const Operand<128> dv = along_row<128>(sbase + F::at_v), dg = along_row<128>(sbase + F::at_stage + 2 * F::q),
+                               dgr = over_rows<128>(sbase + F::at_stage + 2 * F::q, F::g), ds = along_row<128>(sbase + F::at_s);
             auto scores = [&](int t) {
-                const uint32_t st = sbase + F::at_stage + (t % NS) * F::stage;
-                bar_wait(&bars.q_full[t % NS], (t / NS) & 1, gave_up);
-                bar_wait(&bars.ready[t % NS], (t / NS) & 1, gave_up);
-                if (t > 0) bar_wait(&bars.s_free, (t - 1) & 1, gave_up);
+                const uint32_t st = (t % NS) * F::stage;
+                bar_wait_warp(&bars.q_full[t % NS], (t / NS) & 1, gave_up);
+                bar_wait_warp(&bars.ready[t % NS], (t / NS) & 1, gave_up);
+                if (t > 0) bar_wait_warp(&bars.s_free, (t - 1) & 1, gave_up);
                 fence_after();
+                if (issue) {
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < DP / 16; ++i)
-                        mma_ss(tS(m), along_row<F::row>(sbase + m * F::k, i), along_row<F::row>(st + m * F::q, i), is, i > 0);
+                        for (int i = 0; i < DP / 16; ++i)
+                            mma_ss(tS(m), dk.at(m * F::k + i * 32), dq.at(st + m * F::q + i * 32), is, i > 0);
 #pragma unroll
-                for (int i = 0; i < VP / 16; ++i)
-                    mma_ss(tS(2), along_row<128>(sbase + F::at_v + (i / 4) * F::v, i % 4),
-                           along_row<128>(st + 2 * F::q + (i / 4) * F::g, i % 4), is, i > 0);
-                mma_commit(&bars.s_full);
+                    for (int i = 0; i < VP / 16; ++i)
+                        mma_ss(tS(2), dv.at((i / 4) * F::v + (i % 4) * 32), dg.at(st + (i / 4) * F::g + (i % 4) * 32), is, i > 0);
+                    mma_commit(&bars.s_full);
+                }
+                __syncwarp();
             };
-            bar_wait(&bars.kv_full, 0, gave_up);
-            bar_wait(&bars.kv_ready, 0, gave_up);
+            bar_wait_warp(&bars.kv_full, 0, gave_up);
+            bar_wait_warp(&bars.kv_ready, 0, gave_up);
             scores(0);
             for (int t = 0; t < T_; ++t) {
                 if (t + 1 < T_) scores(t + 1);
-                bar_wait(&bars.ds_full, t & 1, gave_up);
+                bar_wait_warp(&bars.ds_full, t & 1, gave_up);
                 fence_after();
-                const uint32_t st = sbase + F::at_stage + (t % NS) * F::stage;
+                if (issue) {
+                    const uint32_t st = (t % NS) * F::stage;
 #pragma unroll
-                for (int i = 0; i < kStep / 16; ++i)
-                    mma_ss(tV, along_row<128>(sbase + F::at_s, i), over_rows<128>(st + 2 * F::q, i, F::g), iv, t > 0 || i > 0);
+                    for (int i = 0; i < kStep / 16; ++i) mma_ss(tV, ds.at(i * 32), dgr.at(st + i * 16 * 128), iv, t > 0 || i > 0);
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < kStep / 16; ++i)
-                        mma_ss(tK(m), along_row<128>(sbase + F::at_s + (1 + m) * F::s, i), over_rows<F::row>(st + m * F::q, i, F::q), ik,
-                               t > 0 || i > 0);
-                mma_commit(&bars.ds_free);
-                mma_commit(&bars.q_empty[t % NS]);
+                        for (int i = 0; i < kStep / 16; ++i)
+                            mma_ss(tK(m), ds.at((1 + m) * F::s + i * 32), dqr.at(st + m * F::q + i * 16 * F::row), ik, t > 0 || i > 0);
+                    mma_commit(&bars.ds_free);
+                    mma_commit(&bars.q_empty[t % NS]);
+                }
+                __syncwarp();
             }
-            mma_commit(&bars.fin);
+            if (issue) mma_commit(&bars.fin);
             bar_drain(&bars.fin, 0);
+            __syncwarp();
         }
     } else if (warp == 10) {
         if (T_ > 0) {

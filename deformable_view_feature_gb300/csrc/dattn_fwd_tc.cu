@@ -2,19 +2,22 @@
 // bf16 and fp16.
 //
 // One CTA takes 128 rows (queries x the heads that share a key head) and
-// walks over the keys in tiles of 128. The two softmax maps take the place of
-// the two row tiles by which such a kernel usually keeps both of its units
-// busy: while the four warps of map 0 turn scores into weights, the tensor
-// core forms P v and the next scores of map 1, and the other way round; K is
-// loaded once for both scores and V once for both products.
+// walks over the keys in steps of 64. The two softmax maps take the place of
+// the two row tiles by which such a kernel usually keeps its units busy: four
+// warps turn the scores of map 0 into weights, four those of map 1, and the
+// tensor core meanwhile forms P v and the next scores of either; K is loaded
+// once for both scores and V once for both products.
 //
 // Warps: 0-3 softmax of map 0 and 4-7 of map 1 (a thread per row, so row
 // maxima and sums need no exchange), 8 loads by TMA, 9 issues the products,
-// 10 prepares each tile's positions and masks. Tensor memory: scores of each
-// map, 128 columns, whose first 64 then hold the map's weights in 16 bits as
-// the operand of P v, and the two outputs. A thread raises its row's reference
-// maximum, and rescales the row's output, only when a tile exceeds it by more
-// than 2^8: fp32 sums keep their digits and weights up to 256 fit both types.
+// 10 prepares each step's positions and masks. Tensor memory: two steps'
+// scores of each map, 64 columns, whose first 32 then hold the map's weights
+// in 16 bits as the operand of P v, and the two outputs. Steps of 128 keys
+// would use the tensor core better, but leave room for one step's scores
+// only: the softmax warps then waited 1500 of 3670 clocks for theirs.
+// A thread raises its row's reference maximum, and rescales the row's output,
+// only when a step exceeds it by more than 2^8: fp32 sums keep their digits
+// and weights up to 256 fit both types.
 #include "dattn_tc.cuh"
 
 namespace da {
@@ -22,33 +25,41 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTile = 128;            // rows, and keys per step
+constexpr int kTile = 128;            // rows
+constexpr int kKeys = 64;             // keys per step
 constexpr int kFwdThreads = 11 * 32;
 constexpr float kSlack = 8.f;         // log2 of how far weights may exceed 1
 
-// What the softmax warps need to know of a tile of keys.
-struct KeyInfo {
-    int pos[kTile];
-    uint32_t valid[4];  // one bit per key
-    int lo, hi;         // smallest and largest position
-    uint32_t all;       // every key is to be used
-    uint32_t pad;
+// What the softmax warps need to know of a step's keys.
+struct alignas(16) KeyInfo {
+    float bound[kKeys];  // +infinity, or -infinity for a key that is not to be used
+    int pos[kKeys];
+    int lo, hi;          // smallest and largest position of those used
+    uint32_t all;        // every key is to be used
+    uint32_t valid[2];   // one bit per key
+    uint32_t pad[3];
 };
 
 template <int DP, int VP> struct FwdShared {
     static constexpr int row = DP * 2;                 // bytes of a row of q or k
-    static constexpr int map = kTile * row;            // of one map's tile
-    static constexpr int vblock = kTile * 128;         // of 64 columns of V
-    static constexpr int stage = 2 * map + (VP / 64) * vblock;
-    // As many steps ahead as fit beside the bias table.
-    static constexpr int stages = stage > 49152 ? 2 : stage > 32768 ? 3 : 4;
-    static constexpr int bytes = 2 * map + stages * stage;
+    static constexpr int q = kTile * row, k = kKeys * row;  // of one map
+    static constexpr int vblock = kKeys * 128;         // of 64 columns of V
+    static constexpr int stage = 2 * k + (VP / 64) * vblock;
+    static constexpr int stages = 4;
+    static constexpr int bytes = 2 * q + stages * stage;
 };
 
+// Floats of the bias of G heads by relative position, with the ends' values
+// repeated for a step more on either side.
+__host__ __device__ inline int bias_span(int reach) { return 2 * (reach + kKeys) + 1; }
+
+// A barrier's wait names a phase by its parity only, so nobody may lag two
+// phases behind: what both sides pass once a step, with the tensor core up to
+// a step ahead, has a barrier for even steps and one for odd.
 struct FwdBars {
     uint64_t q_full, fin;
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], info[4], v_ready[4];
-    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // of each map, for even and odd steps
     uint32_t tmem, gave_up;
 };
 
@@ -68,21 +79,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     __shared__ FwdBars bars;
     __shared__ KeyInfo infos[NS];
     __shared__ float row_l[2][kTile], row_m[2][kTile];
-    float *table = reinterpret_cast<float *>(base + F::bytes);  // [G][2 reach + 1], times log2(e)
+    float *table = reinterpret_cast<float *>(base + F::bytes);  // [G][span], times log2(e)
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
     const int LP = kTile / a.G;  // queries of a tile
-    const int tile = blockIdx.x / a.splits, split = blockIdx.x - tile * a.splits;
-    const int n = blockIdx.y, b = blockIdx.z, l0 = tile * LP;
+    // The tiles with most keys to see first, of all heads and batch items.
+    const int bn = blockIdx.x % (a.B * a.Hkv), rest = blockIdx.x / (a.B * a.Hkv);
+    const int b = bn / a.Hkv, n = bn - b * a.Hkv, split = rest % a.splits;
+    const int l0 = ((a.Lq + LP - 1) / LP - 1 - rest / a.splits) * LP;
     const int len = dattn_length(a, b);
     int end = len;
     // Keys after the tile's last query end the walk where positions are indices.
-    if (a.causal && !a.pos_q && !a.pos_k) end = min(end, max(len - a.Lq + min(l0 + LP, a.Lq), 0));
-    const int per = ((end + kTile - 1) / kTile + a.splits - 1) / a.splits * kTile;
+    const bool indices = !a.pos_q && !a.pos_k;
+    if (a.causal && indices) end = min(end, max(len - a.Lq + min(l0 + LP, a.Lq), 0));
+    const int per = ((end + kKeys - 1) / kKeys + a.splits - 1) / a.splits * kKeys;
     const int jb = split * per;
     end = min(end, jb + per);
-    const int T_ = end > jb ? (end - jb + kTile - 1) / kTile : 0;
-    const int span = 2 * a.reach + 1;
+    const int T_ = end > jb ? (end - jb + kKeys - 1) / kKeys : 0;
+    const int span = bias_span(a.reach);
 
     if (threadIdx.x == 0) {
         bar_init(&bars.q_full, 1);
@@ -96,9 +110,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             bar_init(&bars.v_ready[s], 1);
         }
         for (int m = 0; m < 2; ++m) {
-            bar_init(&bars.s_full[m], 1);
-            bar_init(&bars.p_full[m], 4);
-            bar_init(&bars.o_done[m], 1);
+            for (int i = 0; i < 2; ++i) {
+                bar_init(&bars.s_full[m][i], 1);
+                bar_init(&bars.p_full[m][i], 4);
+                bar_init(&bars.o_done[m][i], 1);
+            }
         }
         bars.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -107,34 +123,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         tma_prefetch(&mv);
     }
     if (warp == 9) tmem_alloc(&bars.tmem, 512);
-    if (a.nb)
-        for (int i = threadIdx.x; i < a.G * span; i += kFwdThreads) {
-            const int g = i / span, bucket = min(max(a.bmap[i - g * span], 0), a.nb - 1);
-            table[i] = a.table[bucket * a.H + n * a.G + g] * kLog2e;
-        }
+    for (int i = threadIdx.x; i < a.G * span; i += kFwdThreads) {
+        const int g = i / span, rel = min(max(i - g * span - kKeys, 0), 2 * a.reach);
+        table[i] = a.nb ? a.table[min(max(a.bmap[rel], 0), a.nb - 1) * a.H + n * a.G + g] * kLog2e : 0.f;
+    }
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = bars.tmem;
+    const uint32_t tmem = uniform(bars.tmem);
     volatile uint32_t *gave_up = &bars.gave_up;
-    const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 256 + VP};
-    const uint32_t sq = smem_addr(base), sst = sq + 2 * F::map;
+    auto tS = [&](int m, int t) { return tmem + m * 128 + (t & 1) * 64; };
+    const uint32_t tO[2] = {tmem + 256, tmem + 256 + VP};
+    const uint32_t sq = smem_addr(base), sst = sq + 2 * F::q;
 
     if (warp == 8) {
         if (lane == 0 && T_ > 0) {
             bar_expect(&bars.q_full, 2 * F::row * a.G * LP);
-            for (int m = 0; m < 2; ++m) tma_load(&mq, &bars.q_full, base + m * F::map, 0, m, n * a.G, l0, b);
+            for (int m = 0; m < 2; ++m) tma_load(&mq, &bars.q_full, base + m * F::q, 0, m, n * a.G, l0, b);
             for (int t = 0; t < T_; ++t) {
                 const int s = t % NS;
                 const uint32_t parity = (t / NS) & 1;
-                unsigned char *st = base + 2 * F::map + s * F::stage;
+                unsigned char *st = base + 2 * F::q + s * F::stage;
                 bar_wait(&bars.k_empty[s], parity ^ 1, gave_up);
-                bar_expect(&bars.k_full[s], 2 * F::map);
-                for (int m = 0; m < 2; ++m) tma_load(&mk, &bars.k_full[s], st + m * F::map, 0, m, n, jb + t * kTile, b);
+                bar_expect(&bars.k_full[s], 2 * F::k);
+                for (int m = 0; m < 2; ++m) tma_load(&mk, &bars.k_full[s], st + m * F::k, 0, m, n, jb + t * kKeys, b);
                 bar_wait(&bars.v_empty[s], parity ^ 1, gave_up);
                 bar_expect(&bars.v_full[s], (VP / 64) * F::vblock);
                 for (int c = 0; c < VP / 64; ++c)
-                    tma_load(&mv, &bars.v_full[s], st + 2 * F::map + c * F::vblock, c * 64, 0, n, jb + t * kTile, b);
+                    tma_load(&mv, &bars.v_full[s], st + 2 * F::k + c * F::vblock, c * 64, 0, n, jb + t * kKeys, b);
             }
             if (*gave_up) {  // leave no copy in flight
                 bar_drain(&bars.q_full, 0);
@@ -145,67 +161,79 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
         }
     } else if (warp == 9) {
-        if (lane == 0 && T_ > 0) {
-            constexpr uint32_t iqk = shape(bf16, kTile, false), ipv = shape(bf16, VP, true);
-            auto scores = [&](int m, int t) {
-                const uint32_t k = sst + (t % NS) * F::stage + m * F::map;
+        if (T_ > 0) {
+            // All lanes walk through the steps, one issues: addresses then
+            // stay in uniform registers. (Issued from a branch of one lane's
+            // own, a product took some 85 clocks and bound the kernel.)
+            const bool issue = elect();
+            constexpr uint32_t iqk = shape(bf16, kKeys, false), ipv = shape(bf16, VP, true);
+            const Operand<F::row> dq = along_row<F::row>(sq), dk = along_row<F::row>(sst);
+            const Operand<128> dv = over_rows<128>(sst + 2 * F::k, F::vblock);
+            auto scores = [&](int t) {
+                const uint32_t st = (t % NS) * F::stage;
+                bar_wait_warp(&bars.k_full[t % NS], (t / NS) & 1, gave_up);
+                fence_after();
+                if (issue) {
 #pragma unroll
-                for (int i = 0; i < DP / 16; ++i)
-                    mma_ss(tS[m], along_row<F::row>(sq + m * F::map, i), along_row<F::row>(k, i), iqk, i > 0);
-                mma_commit(&bars.s_full[m]);
+                    for (int m = 0; m < 2; ++m) {
+#pragma unroll
+                        for (int i = 0; i < DP / 16; ++i)
+                            mma_ss(tS(m, t), dq.at(m * F::q + i * 32), dk.at(st + m * F::k + i * 32), iqk, i > 0);
+                        mma_commit(&bars.s_full[m][t & 1]);
+                    }
+                    mma_commit(&bars.k_empty[t % NS]);
+                }
+                __syncwarp();
             };
-            bar_wait(&bars.q_full, 0, gave_up);
-            bar_wait(&bars.k_full[0], 0, gave_up);
-            fence_after();
-            scores(0, 0);
-            scores(1, 0);
-            mma_commit(&bars.k_empty[0]);
+            bar_wait_warp(&bars.q_full, 0, gave_up);
+            scores(0);
             for (int t = 0; t < T_; ++t) {
                 const int s = t % NS;
-                const uint32_t v = sst + s * F::stage + 2 * F::map;
-                bar_wait(&bars.v_full[s], (t / NS) & 1, gave_up);
-                bar_wait(&bars.v_ready[s], (t / NS) & 1, gave_up);
-                for (int m = 0; m < 2; ++m) {
-                    bar_wait(&bars.p_full[m], t & 1, gave_up);
-                    fence_after();
+                // Their columns held the weights of step t - 1, whose products
+                // were issued before and are formed in this order.
+                if (t + 1 < T_) scores(t + 1);
+                bar_wait_warp(&bars.v_full[s], (t / NS) & 1, gave_up);
+                bar_wait_warp(&bars.v_ready[s], (t / NS) & 1, gave_up);
 #pragma unroll
-                    for (int i = 0; i < kTile / 16; ++i)
-                        mma_ts(tO[m], tS[m] + i * 8, over_rows<128>(v, i, F::vblock), ipv, t > 0 || i > 0);
-                    mma_commit(&bars.o_done[m]);
-                    if (t + 1 < T_) {
-                        if (m == 0) bar_wait(&bars.k_full[(t + 1) % NS], ((t + 1) / NS) & 1, gave_up);
-                        scores(m, t + 1);  // after P v, which reads its weights from these columns
+                for (int m = 0; m < 2; ++m) {
+                    bar_wait_warp(&bars.p_full[m][t & 1], (t >> 1) & 1, gave_up);
+                    fence_after();
+                    if (issue) {
+#pragma unroll
+                        for (int i = 0; i < kKeys / 16; ++i)
+                            mma_ts(tO[m], tS(m, t) + i * 8, dv.at(s * F::stage + i * 16 * 128), ipv, t > 0 || i > 0);
+                        mma_commit(&bars.o_done[m][t & 1]);
+                        if (m == 1) mma_commit(&bars.v_empty[s]);
                     }
+                    __syncwarp();
                 }
-                mma_commit(&bars.v_empty[s]);
-                if (t + 1 < T_) mma_commit(&bars.k_empty[(t + 1) % NS]);
             }
-            mma_commit(&bars.fin);
+            if (issue) mma_commit(&bars.fin);
             bar_drain(&bars.fin, 0);
+            __syncwarp();
         }
     } else if (warp == 10) {
         for (int t = 0; t < T_; ++t) {
-            const int s = t % NS, j0 = jb + t * kTile;
+            const int s = t % NS, j0 = jb + t * kKeys;
             KeyInfo &ki = infos[s];
             // The slot is free once P v of NS steps ago is done: the softmax
             // warps had by then read its infos, and the products its V.
             bar_wait_warp(&bars.v_empty[s], ((t / NS) & 1) ^ 1, gave_up);
             int lo = INT32_MAX, hi = INT32_MIN;
-            uint32_t every = 0xffffffffu, stale = 0;
+            uint32_t every = 0xffffffffu, stale = 0, valid[2];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
                 const int j = j0 + c * 32 + lane;
                 const bool in = j < end;
                 const int64_t at = static_cast<int64_t>(b) * a.Lk + j;
                 const bool use = in && (!a.mask || a.mask[at]);
                 const int pos = in && a.pos_k ? a.pos_k[at] : j;
                 ki.pos[c * 32 + lane] = pos;
-                const uint32_t bits = __ballot_sync(0xffffffffu, use);
+                ki.bound[c * 32 + lane] = use ? INFINITY : -INFINITY;
+                valid[c] = __ballot_sync(0xffffffffu, use);
                 // Unused keys inside the tensor; past its end TMA wrote zeros.
-                const uint32_t bad = __ballot_sync(0xffffffffu, !use && j < a.Lk);
-                every &= bits;
-                stale |= bad;
-                if (lane == 0) ki.valid[c] = bits;
+                stale |= __ballot_sync(0xffffffffu, !use && j < a.Lk);
+                every &= valid[c];
                 if (use) {
                     lo = min(lo, pos);
                     hi = max(hi, pos);
@@ -217,14 +245,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 ki.lo = lo;
                 ki.hi = hi;
                 ki.all = every == 0xffffffffu;
+                ki.valid[0] = valid[0];
+                ki.valid[1] = valid[1];
             }
             __syncwarp();
             if (lane == 0) bar_arrive(&bars.info[s]);
             if (stale) {  // 0 * NaN is NaN: the rows of V of unused keys become zeros
                 bar_wait_warp(&bars.v_full[s], (t / NS) & 1, gave_up);
-                unsigned char *v = base + 2 * F::map + s * F::stage + 2 * F::map;
-                for (int r = lane >> 3; r < kTile; r += 4)
-                    if (!(ki.valid[r >> 5] >> (r & 31) & 1))
+                unsigned char *v = base + 2 * F::q + s * F::stage + 2 * F::k;
+#pragma unroll 1
+                for (int r = lane >> 3; r < kKeys; r += 4)
+                    if (!(valid[r >> 5] >> (r & 31) & 1))
                         for (int c = 0; c < VP / 64; ++c)
                             *reinterpret_cast<uint4 *>(v + c * F::vblock + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
                 fence_async();
@@ -238,46 +269,63 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int dl = static_cast<int>(a.div_G.div(rl)), g = rl - dl * a.G, l = l0 + dl;
         const bool live = rl < LP * a.G && l < a.Lq;
         const int pos = !live ? 0 : a.pos_q ? a.pos_q[static_cast<int64_t>(b) * a.Lq + l] : len - a.Lq + l;
-        const float *tb = table + g * span + a.reach;  // a row past the tile's heads still reads inside the table
+        const float *tb = table + g * span + a.reach + kKeys;  // a row past the tile's heads still reads inside the table
         float ref = -INFINITY;
         float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
         for (int t = 0; t < T_; ++t) {
             const KeyInfo &ki = infos[t % NS];
             bar_wait_warp(&bars.info[t % NS], (t / NS) & 1, gave_up);
             const int rlo = ki.lo - pos, rhi = ki.hi - pos;
-            // One bias for the row's whole tile, and nothing hidden.
-            const bool even = !live || (ki.all && !(a.causal && rhi > 0) &&
-                                        (a.nb == 0 || rlo >= a.reach || rhi <= -a.reach || rlo == rhi));
-            const bool fast = __all_sync(0xffffffffu, even) && a.scale_log2 >= 0.f;
-            bar_wait_warp(&bars.s_full[m], t & 1, gave_up);
+            const bool all = ki.all;
+            // One bias for all of the row's keys in this step, none of them later.
+            const bool even = !live || (!(a.causal && rhi > 0) && (a.nb == 0 || rlo >= a.reach || rhi <= -a.reach || rlo == rhi));
+            const bool fast = __all_sync(0xffffffffu, even) && a.scale_log2 > 0.f;
+            bar_wait_warp(&bars.s_full[m][t & 1], (t >> 1) & 1, gave_up);
             fence_after();
-            float s[kTile];
-            tmem_load(tS[m] + lanes, s);
+            float s[kKeys];
+            tmem_load(tS(m, t) + lanes, s);
             float mul = a.scale_log2, add = 0.f;
             if (fast) {
-                if (a.nb) add = tb[min(max(rlo, -a.reach), a.reach)];
+                add = tb[min(max(rlo, -a.reach), a.reach)];
             } else {
                 const float mul_all = a.scale_log2;
+                if (indices) {
+                    // Positions rise by one from key to key: so do places in the table.
+                    const int rel = jb + t * kKeys - pos, seen = a.causal ? -rel : kKeys;
+                    const float *p = tb + min(max(rel, -a.reach - kKeys), a.reach + 1);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t valid = ki.valid[c];
+                    for (int i = 0; i < kKeys; ++i) {
+                        const float x = fmaf(s[i], mul_all, p[i]);
+                        s[i] = i <= seen ? x : -INFINITY;
+                    }
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int rel = ki.pos[c * 32 + i] - pos;
-                        float x = s[c * 32 + i] * mul_all;
-                        if (a.nb) x += tb[min(max(rel, -a.reach), a.reach)];
-                        s[c * 32 + i] = (valid >> i & 1) && !(a.causal && rel > 0) ? x : -INFINITY;
+                    for (int i = 0; i < kKeys; ++i) {
+                        const int rel = ki.pos[i] - pos;
+                        const float x = fmaf(s[i], mul_all, tb[min(max(rel, -a.reach), a.reach)]);
+                        s[i] = a.causal && rel > 0 ? -INFINITY : x;
                     }
                 }
                 mul = 1.f;
             }
+            if (!all) {
+                // The smaller of a NaN and -infinity is -infinity.
+#pragma unroll
+                for (int i = 0; i < kKeys; i += 4) {
+                    const float4 bound = *reinterpret_cast<const float4 *>(&ki.bound[i]);
+                    s[i] = fminf(s[i], bound.x);
+                    s[i + 1] = fminf(s[i + 1], bound.y);
+                    s[i + 2] = fminf(s[i + 2], bound.z);
+                    s[i + 3] = fminf(s[i + 3], bound.w);
+                }
+            }
             float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int i = 4; i < kTile - 4; i += 8)
+            for (int i = 4; i < kKeys - 4; i += 8)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) top[c] = max3(top[c], s[i + c], s[i + 4 + c]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], s[kTile - 4 + c]);
+            for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], s[kKeys - 4 + c]);
             const float best = fmaf(max3(fmaxf(top[0], top[1]), top[2], top[3]), mul, add);
             // Each row by its own scores alone, so that its roundings do not
             // depend on its neighbours'; rows past the end hold stale values.
@@ -290,7 +338,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 sum[0] = mul2(sum[0], sh);
                 sum[1] = mul2(sum[1], sh);
                 if (t > 0) {
-                    bar_wait_warp(&bars.o_done[m], (t - 1) & 1, gave_up);
+                    bar_wait_warp(&bars.o_done[m][(t - 1) & 1], ((t - 1) >> 1) & 1, gave_up);
                     fence_after();
 #pragma unroll 1
                     for (int c = 0; c < VP; c += 32) {
@@ -304,25 +352,25 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
             const float off = add - (ref == -INFINITY ? 0.f : ref);
             const float2 mul_2 = {mul, mul}, off_2 = {off, off};
-            uint32_t p[kTile / 2];
+            uint32_t p[kKeys / 2];
 #pragma unroll
-            for (int i = 0; i < kTile / 2; ++i) {
+            for (int i = 0; i < kKeys / 2; ++i) {
                 float2 x = fma2({s[2 * i], s[2 * i + 1]}, mul_2, off_2);
                 x.x = ex2(x.x);
                 x.y = ex2(x.y);
                 sum[i & 1] = add2(sum[i & 1], x);
                 p[i] = pack2<T>(x.x, x.y);
             }
-            tmem_store(tS[m] + lanes, p);
+            tmem_store(tS(m, t) + lanes, p);
             tmem_store_wait();
             fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(&bars.p_full[m]);
+            if (lane == 0) bar_arrive(&bars.p_full[m][t & 1]);
         }
         row_l[m][rl] = sum[0].x + sum[0].y + (sum[1].x + sum[1].y);
         row_m[m][rl] = ref;
         if (T_ > 0)
-            for (int i = 0; i < 2; ++i) bar_wait_warp(&bars.o_done[i], (T_ - 1) & 1, gave_up);
+            for (int i = 0; i < 2; ++i) bar_wait_warp(&bars.o_done[i][(T_ - 1) & 1], ((T_ - 1) >> 1) & 1, gave_up);
         fence_after();
         asm volatile("bar.sync 1, 256;" ::: "memory");
         const float s0 = row_l[0][rl], s1 = row_l[1][rl];
@@ -401,12 +449,12 @@ template <typename T, int DP, int VP>
 cudaError_t launch_fwd(const DattnArgs &a, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, cudaStream_t st)
 {
     using F = FwdShared<DP, VP>;
-    const size_t smem = F::bytes + 1024 + sizeof(float) * (a.nb ? a.G * (2 * a.reach + 1) : 0);
+    const size_t smem = F::bytes + 1024 + sizeof(float) * a.G * bias_span(a.reach);
     const auto kernel = dattn_fwd_tc_kernel<T, DP, VP>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const int LP = kTile / a.G;
-    const dim3 grid(static_cast<unsigned>((a.Lq + LP - 1) / LP * a.splits), a.Hkv, a.B);
+    const unsigned grid = static_cast<unsigned>((a.Lq + LP - 1) / LP * a.splits) * a.Hkv * a.B;
     kernel<<<grid, kFwdThreads, smem, st>>>(a, mq, mk, mv);
     return cudaGetLastError();
 }
@@ -430,8 +478,8 @@ da_status dattn_forward_tensor(const DattnArgs &a, int dtype, cudaStream_t st)
     const int wide = a.D <= 32 ? 32 : 64, LP = kTile / a.G;
     CUtensorMap mq, mk, mv;
     da_status e = tensor_map(mq, dtype, a.q, a.D, 2, a.H, a.Lq, a.B, a.qs[3], a.qs[2], a.qs[1], a.qs[0], wide, a.G, LP);
-    if (e == DA_OK) e = tensor_map(mk, dtype, a.k, a.D, 2, a.Hkv, a.Lk, a.B, a.ks[3], a.ks[2], a.ks[1], a.ks[0], wide, 1, kTile);
-    if (e == DA_OK) e = tensor_map(mv, dtype, a.v, a.Dv, 1, a.Hkv, a.Lk, a.B, 0, a.vs[2], a.vs[1], a.vs[0], 64, 1, kTile);
+    if (e == DA_OK) e = tensor_map(mk, dtype, a.k, a.D, 2, a.Hkv, a.Lk, a.B, a.ks[3], a.ks[2], a.ks[1], a.ks[0], wide, 1, kKeys);
+    if (e == DA_OK) e = tensor_map(mv, dtype, a.v, a.Dv, 1, a.Hkv, a.Lk, a.B, 0, a.vs[2], a.vs[1], a.vs[0], 64, 1, kKeys);
     if (e != DA_OK) return e;
     const cudaError_t c = dtype == DA_BF16 ? fwd_widths<__nv_bfloat16>(a, mq, mk, mv, st) : fwd_widths<__half>(a, mq, mk, mv, st);
     return c == cudaSuccess ? DA_OK : cuda_fail(c, "differential attention launch");
