@@ -11,10 +11,13 @@
 //
 // Since e = g v^T serves both maps, and P_0 - lam P_1 is formed before its
 // product with g, a pair costs three products forward and three (grad_k twice,
-// grad_v) or two (grad_q twice) back. All products sum in tensor memory; the
-// weights and s_m go through shared memory as 16-bit operands.
+// grad_v) or two (grad_q twice) back. All products sum in tensor memory.
+// With 64 columns a product reads its operands from shared memory for 48
+// clocks and multiplies for 32, so the operands that stay lie in tensor memory
+// too, as far as it goes: q, g and s_m of the rows in the first kernel, v in
+// the second, whose weights and s_m go through shared memory.
 //
-// Warps: 0-7 compute (two threads per row or key, each with half of a tile's
+// Warps: 0-7 compute (two threads per row or key, each with half of a step's
 // 64 columns of both maps), 8 loads by TMA, 9 issues the products, 10 prepares
 // positions, masks and per-query values. The scores of step t+1 are formed as
 // soon as the compute warps hold those of step t in registers.
@@ -42,6 +45,24 @@ __device__ __forceinline__ void store_operand(unsigned char *tile, int row, int 
     for (int i = 0; i < 4; ++i)
         *reinterpret_cast<uint4 *>(tile + row * kBlock + (((half * 4 + i) ^ (row & 7)) << 4)) =
             make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+}
+
+// 32 columns from `half` on of row `row` of a tile with rows of ROW bytes, to
+// 16 columns of tensor memory (two elements each).
+template <int ROW> __device__ __forceinline__ void operand_to_tmem(uint32_t addr, const unsigned char *tile, int row, int half)
+{
+    uint32_t p[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // 64-byte rows lie two to a swizzled line of 128 bytes.
+        const int piece = ROW == 128 ? (half * 4 + i) ^ (row & 7) : i ^ ((row >> 1) & 3);
+        const uint4 u = *reinterpret_cast<const uint4 *>(tile + row * ROW + (piece << 4));
+        p[4 * i] = u.x;
+        p[4 * i + 1] = u.y;
+        p[4 * i + 2] = u.z;
+        p[4 * i + 3] = u.w;
+    }
+    tmem_store(addr, p);
 }
 
 // Zeroes row r of a tile whose rows have `bytes` bytes, by 8 lanes.
@@ -75,10 +96,11 @@ template <int DP, int VP> struct GradQShared {
     static constexpr int q = kOwn * row, g = kOwn * kBlock;       // one map, one block of 64 columns
     static constexpr int k = kStep * row, v = kStep * kBlock;
     static constexpr int stage = 2 * k + (VP / 64) * v;
-    static constexpr int stages = stage > 16384 ? 3 : 4;
-    static constexpr int s = kOwn * kBlock;                       // s_m as an operand
-    static constexpr int at_g = 2 * q, at_stage = at_g + (VP / 64) * g, at_s = at_stage + stages * stage,
-                         bytes = at_s + 2 * s;
+    static constexpr int stages = 4;
+    static constexpr int at_g = 2 * q, at_stage = at_g + (VP / 64) * g, bytes = at_stage + stages * stage;
+    // Columns of tensor memory: two score tiles and e, grad_q, then q, g, s_m.
+    static constexpr int c_out = 3 * kStep, c_q = c_out + 2 * DP, c_g = c_q + DP, c_s = c_g + VP / 2;
+    static_assert(c_s + kStep <= 512, "tensor memory");
 };
 
 struct alignas(16) QKeyInfo {
@@ -89,8 +111,8 @@ struct alignas(16) QKeyInfo {
 };
 
 struct QBars {
-    uint64_t q_full, fin, s_full[2], ds_full, ds_free;
-    uint64_t kv_full[4], kv_empty[4], info[4], ready[4];
+    uint64_t q_full, q_ready, fin, s_full, s_free, ds_full;
+    uint64_t full[4], empty[4], ready[4];  // of a stage: loaded, free, cleared of unused keys
     uint32_t tmem, gave_up;
 };
 
@@ -111,7 +133,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
     const int warp = warp_number(), lane = threadIdx.x & 31;
     const int LP = kOwn / a.G;
-    const int n = blockIdx.y, b = blockIdx.z, l0 = blockIdx.x * LP;
+    // The tiles with most keys to see first, of all heads and batch items.
+    const int bn = blockIdx.x % (a.B * a.Hkv), b = bn / a.Hkv, n = bn - b * a.Hkv;
+    const int l0 = ((a.Lq + LP - 1) / LP - 1 - blockIdx.x / (a.B * a.Hkv)) * LP;
     const int len = dattn_length(a, b);
     int end = len;
     if (a.causal && !a.pos_q && !a.pos_k) end = min(end, max(len - a.Lq + min(l0 + LP, a.Lq), 0));
@@ -120,15 +144,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
     if (threadIdx.x == 0) {
         bar_init(&bars.q_full, 1);
+        bar_init(&bars.q_ready, 8);
         bar_init(&bars.fin, 1);
-        bar_init(&bars.s_full[0], 1);
-        bar_init(&bars.s_full[1], 1);
+        bar_init(&bars.s_full, 1);
+        bar_init(&bars.s_free, 8);
         bar_init(&bars.ds_full, 8);
-        bar_init(&bars.ds_free, 1);
         for (int s = 0; s < NS; ++s) {
-            bar_init(&bars.kv_full[s], 1);
-            bar_init(&bars.kv_empty[s], 1);
-            bar_init(&bars.info[s], 1);
+            bar_init(&bars.full[s], 1);
+            bar_init(&bars.empty[s], 1);
             bar_init(&bars.ready[s], 1);
         }
         bars.gave_up = 0;
@@ -149,9 +172,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     fence_after();
     const uint32_t tmem = uniform(bars.tmem);
     volatile uint32_t *gave_up = &bars.gave_up;
-    // Scores and e of two steps, 64 columns each, then grad_q of each map.
-    auto tS = [&](int buf, int which) { return tmem + buf * 192 + which * 64; };
-    auto tQ = [&](int m) { return tmem + 384 + m * DP; };
+    auto tS = [&](int which) { return tmem + which * kStep; };
+    auto tQ = [&](int m) { return tmem + F::c_out + m * DP; };
     const uint32_t sbase = smem_addr(base);
 
     if (warp == 8) {
@@ -162,47 +184,45 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int t = 0; t < T_; ++t) {
                 const int s = t % NS;
                 unsigned char *st = base + F::at_stage + s * F::stage;
-                bar_wait(&bars.kv_empty[s], ((t / NS) & 1) ^ 1, gave_up);
-                bar_expect(&bars.kv_full[s], F::stage);
-                for (int m = 0; m < 2; ++m) tma_load(&mk, &bars.kv_full[s], st + m * F::k, 0, m, n, t * kStep, b);
+                bar_wait(&bars.empty[s], ((t / NS) & 1) ^ 1, gave_up);
+                bar_expect(&bars.full[s], F::stage);
+                for (int m = 0; m < 2; ++m) tma_load(&mk, &bars.full[s], st + m * F::k, 0, m, n, t * kStep, b);
                 for (int c = 0; c < VP / 64; ++c)
-                    tma_load(&mv, &bars.kv_full[s], st + 2 * F::k + c * F::v, c * 64, 0, n, t * kStep, b);
+                    tma_load(&mv, &bars.full[s], st + 2 * F::k + c * F::v, c * 64, 0, n, t * kStep, b);
             }
             if (*gave_up) {
                 bar_drain(&bars.q_full, 0);
-                for (int t = max(0, T_ - NS); t < T_; ++t) bar_drain(&bars.kv_full[t % NS], (t / NS) & 1);
+                for (int t = max(0, T_ - NS); t < T_; ++t) bar_drain(&bars.full[t % NS], (t / NS) & 1);
             }
         }
     } else if (warp == 9) {
         if (T_ > 0) {
             const bool issue = elect();
             constexpr uint32_t is = shape(is_bf16<T>, kStep, false), iq = shape(is_bf16<T>, DP, true);
-            const Operand<F::row> dq = along_row<F::row>(sbase), dk = along_row<F::row>(sbase + F::at_stage),
-                                  dkr = over_rows<F::row>(sbase + F::at_stage, F::k);
-            const Operand<128> dg = along_row<128>(sbase + F::at_g), dv = along_row<128>(sbase + F::at_stage + 2 * F::k),
-                               ds = along_row<128>(sbase + F::at_s);
+            const Operand<F::row> dk = along_row<F::row>(sbase + F::at_stage), dkr = over_rows<F::row>(sbase + F::at_stage, F::k);
+            const Operand<128> dv = along_row<128>(sbase + F::at_stage + 2 * F::k);
             auto scores = [&](int t) {
                 const uint32_t st = (t % NS) * F::stage;
-                bar_wait_warp(&bars.kv_full[t % NS], (t / NS) & 1, gave_up);
                 bar_wait_warp(&bars.ready[t % NS], (t / NS) & 1, gave_up);
+                if (t > 0) bar_wait_warp(&bars.s_free, (t - 1) & 1, gave_up);
                 fence_after();
                 if (issue) {
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int i = 0; i < DP / 16; ++i)
-                            mma_ss(tS(t & 1, m), dq.at(m * F::q + i * 32), dk.at(st + m * F::k + i * 32), is, i > 0);
+                            mma_ts(tS(m), tmem + F::c_q + m * (DP / 2) + i * 8, dk.at(st + m * F::k + i * 32), is, i > 0);
 #pragma unroll
                     for (int i = 0; i < VP / 16; ++i)
-                        mma_ss(tS(t & 1, 2), dg.at((i / 4) * F::g + (i % 4) * 32), dv.at(st + (i / 4) * F::v + (i % 4) * 32), is, i > 0);
-                    mma_commit(&bars.s_full[t & 1]);
+                        mma_ts(tS(2), tmem + F::c_g + i * 8, dv.at(st + (i / 4) * F::v + (i % 4) * 32), is, i > 0);
+                    mma_commit(&bars.s_full);
                 }
                 __syncwarp();
             };
-            bar_wait_warp(&bars.q_full, 0, gave_up);
+            bar_wait_warp(&bars.q_ready, 0, gave_up);
             scores(0);
             for (int t = 0; t < T_; ++t) {
-                if (t + 1 < T_) scores(t + 1);  // its columns were read by the end of step t - 1
+                if (t + 1 < T_) scores(t + 1);
                 bar_wait_warp(&bars.ds_full, t & 1, gave_up);
                 fence_after();
                 if (issue) {
@@ -211,9 +231,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int i = 0; i < kStep / 16; ++i)
-                            mma_ss(tQ(m), ds.at(m * F::s + i * 32), dkr.at(st + m * F::k + i * 16 * F::row), iq, t > 0 || i > 0);
-                    mma_commit(&bars.ds_free);
-                    mma_commit(&bars.kv_empty[t % NS]);
+                            mma_ts(tQ(m), tmem + F::c_s + m * (kStep / 2) + i * 8, dkr.at(st + m * F::k + i * 16 * F::row), iq, t > 0 || i > 0);
+                    mma_commit(&bars.empty[t % NS]);
                 }
                 __syncwarp();
             }
@@ -225,7 +244,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int t = 0; t < T_; ++t) {
             const int s = t % NS, j0 = t * kStep;
             QKeyInfo &ki = infos[s];
-            bar_wait_warp(&bars.kv_empty[s], ((t / NS) & 1) ^ 1, gave_up);
+            bar_wait_warp(&bars.empty[s], ((t / NS) & 1) ^ 1, gave_up);
             int lo = INT32_MAX, hi = INT32_MIN;
             uint32_t every = 0xffffffffu, stale = 0;
 #pragma unroll
@@ -252,10 +271,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 ki.hi = hi;
                 ki.all = every == 0xffffffffu;
             }
-            __syncwarp();
-            if (lane == 0) bar_arrive(&bars.info[s]);
+            bar_wait_warp(&bars.full[s], (t / NS) & 1, gave_up);
             if (stale) {  // unused keys: 0 * NaN in s k would be NaN
-                bar_wait_warp(&bars.kv_full[s], (t / NS) & 1, gave_up);
                 unsigned char *st = base + F::at_stage + s * F::stage;
                 for (int r = lane >> 3; r < kStep; r += 4)
                     if (!(ki.valid[r >> 5] >> (r & 31) & 1))
@@ -298,21 +315,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         d[0] = fmaf(lam, d[1], part[0][0][rl] + part[0][1][rl]);  // out = o_0 - lam o_1
         const bool none = lse[0] == INFINITY;  // sees no key: whatever g holds there is not used
         if (none) d[0] = d[1] = 0.f;
+        if (T_ > 0) {  // the rows' operands to tensor memory
+            bar_wait_warp(&bars.q_full, 0, gave_up);
+            for (int m = 0; m < 2; ++m)
+                if (DP == 64 || half == m)
+                    operand_to_tmem<F::row>(tmem + F::c_q + m * (DP / 2) + (DP == 64 ? half * 16 : 0) + lanes, base + m * F::q, rl, half);
+            for (int c = 0; c < VP / 64; ++c)
+                operand_to_tmem<128>(tmem + F::c_g + c * 32 + half * 16 + lanes, base + F::at_g + c * F::g, rl, half);
+            tmem_store_wait();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bars.q_ready);
+        }
         const float2 nd[2] = {{-d[0], -d[0]}, {-d[1], -d[1]}};
         float2 rest[2] = {{0.f, 0.f}, {0.f, 0.f}};
         for (int t = 0; t < T_; ++t) {
             const QKeyInfo &ki = infos[t % NS];
-            bar_wait_warp(&bars.info[t % NS], (t / NS) & 1, gave_up);
+            bar_wait_warp(&bars.s_full, t & 1, gave_up);
+            fence_after();
+            float e[32], x[2][32];
+            tmem_load(tS(2) + lanes + half * 32, e);
+            tmem_load(tS(0) + lanes + half * 32, x[0]);
+            tmem_load(tS(1) + lanes + half * 32, x[1]);
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bars.s_free);
             const int rlo = ki.lo - pos, rhi = ki.hi - pos;
             const bool even = !live || (ki.all && !none && !(a.causal && rhi > 0) &&
                                         (a.nb == 0 || rlo >= a.reach || rhi <= -a.reach || rlo == rhi));
             const bool fast = __all_sync(0xffffffffu, even);
-            bar_wait_warp(&bars.s_full[t & 1], (t >> 1) & 1, gave_up);
-            fence_after();
-            float e[32], x[2][32];
-            tmem_load(tS(t & 1, 2) + lanes + half * 32, e);
-            tmem_load(tS(t & 1, 0) + lanes + half * 32, x[0]);
-            tmem_load(tS(t & 1, 1) + lanes + half * 32, x[1]);
             float add[2] = {-lse[0], -lse[1]}, mul = a.scale_log2;
             if (fast) {
                 if (a.nb) {
@@ -351,9 +382,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 p[0][i] = pack2<T>(s0.x, s0.y);
                 p[1][i] = pack2<T>(s1l.x, s1l.y);
             }
-            if (t > 0) bar_wait_warp(&bars.ds_free, (t - 1) & 1, gave_up);
-            for (int m = 0; m < 2; ++m) store_operand(base + F::at_s + m * F::s, rl, half, p[m]);
-            fence_async();
+            if (t > 0) bar_wait_warp(&bars.empty[(t - 1) % NS], ((t - 1) / NS) & 1, gave_up);  // s_m of step t - 1 was used
+            tmem_store(tmem + F::c_s + half * 16 + lanes, p[0]);
+            tmem_store(tmem + F::c_s + kStep / 2 + half * 16 + lanes, p[1]);
+            tmem_store_wait();
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(&bars.ds_full);
@@ -399,10 +431,13 @@ template <int DP, int VP> struct GradKVShared {
     static constexpr int k = kOwn * row, v = kOwn * kBlock;       // one map, one block of 64 columns
     static constexpr int q = kStep * row, g = kStep * kBlock;
     static constexpr int stage = 2 * q + (VP / 64) * g;
-    static constexpr int stages = stage > 24576 ? 2 : 3;
+    static constexpr int stages = 3;
     static constexpr int s = kOwn * kBlock;                       // P_0 - lam P_1 and s_m as operands
-    static constexpr int at_v = 2 * k, at_stage = at_v + (VP / 64) * v, at_s = at_stage + stages * stage,
-                         bytes = at_s + 3 * s;
+    static constexpr int at_stage = 2 * k, at_s = at_stage + stages * stage, bytes = at_s + 3 * s;
+    static constexpr int at_v = at_s;                             // until v is in tensor memory
+    // Columns of tensor memory: two score tiles and e, grad_v, grad_k, then v.
+    static constexpr int c_v = 3 * kStep + VP + 2 * DP;
+    static_assert(c_v + VP / 2 <= 512, "tensor memory");
     static constexpr int table(int nb, int reach) { return nb ? 4 * (2 * reach + 1) + (2 * reach + 4) / 4 * 4 + 4 * 256 * nb : 0; }
 };
 
@@ -415,8 +450,8 @@ struct alignas(16) QueryInfo {
 };
 
 struct KVBars {
-    uint64_t kv_full, kv_ready, fin, s_full, s_free, ds_full, ds_free;
-    uint64_t q_full[3], q_empty[3], info[3], ready[3];
+    uint64_t kv_full, kv_ready, v_ready, fin, s_full, s_free, ds_full;
+    uint64_t full[3], empty[3], ready[3];  // of a stage: loaded, free, cleared of idle queries
     uint32_t tmem, gave_up;
 };
 
@@ -440,7 +475,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     float *sums = reinterpret_cast<float *>(bucket + (span + 3) / 4 * 4);
 
     const int warp = warp_number(), lane = threadIdx.x & 31;
-    const int n = blockIdx.y, b = blockIdx.z, j0 = blockIdx.x * kOwn;
+    // The keys that most queries see first, of all heads and batch items.
+    const int bn = blockIdx.x % (a.B * a.Hkv), b = bn / a.Hkv, n = bn - b * a.Hkv;
+    const int key_tile = blockIdx.x / (a.B * a.Hkv), j0 = key_tile * kOwn;
     const int len = dattn_length(a, b);
     int first = 0;
     if (a.causal && !a.pos_q && !a.pos_k) first = min(max(j0 - (len - a.Lq), 0), a.Lq);
@@ -450,15 +487,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (threadIdx.x == 0) {
         bar_init(&bars.kv_full, 1);
         bar_init(&bars.kv_ready, 1);
+        bar_init(&bars.v_ready, 8);
         bar_init(&bars.fin, 1);
         bar_init(&bars.s_full, 1);
         bar_init(&bars.s_free, 8);
         bar_init(&bars.ds_full, 8);
-        bar_init(&bars.ds_free, 1);
         for (int s = 0; s < NS; ++s) {
-            bar_init(&bars.q_full[s], 1);
-            bar_init(&bars.q_empty[s], 1);
-            bar_init(&bars.info[s], 1);
+            bar_init(&bars.full[s], 1);
+            bar_init(&bars.empty[s], 1);
             bar_init(&bars.ready[s], 1);
         }
         bars.gave_up = 0;
@@ -484,20 +520,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
     if (warp == 8) {
         if (lane == 0 && T_ > 0) {
-            bar_expect(&bars.kv_full, F::at_stage);
+            bar_expect(&bars.kv_full, 2 * F::k + (VP / 64) * F::v);
             for (int m = 0; m < 2; ++m) tma_load(&mk, &bars.kv_full, base + m * F::k, 0, m, n, j0, b);
             for (int c = 0; c < VP / 64; ++c) tma_load(&mv, &bars.kv_full, base + F::at_v + c * F::v, c * 64, 0, n, j0, b);
             for (int t = 0; t < T_; ++t) {
                 const int s = t % NS, h = n * a.G + t / per, l = first + (t % per) * kStep;
                 unsigned char *st = base + F::at_stage + s * F::stage;
-                bar_wait(&bars.q_empty[s], ((t / NS) & 1) ^ 1, gave_up);
-                bar_expect(&bars.q_full[s], F::stage);
-                for (int m = 0; m < 2; ++m) tma_load(&mq, &bars.q_full[s], st + m * F::q, 0, m, h, l, b);
-                for (int c = 0; c < VP / 64; ++c) tma_load(&mg, &bars.q_full[s], st + 2 * F::q + c * F::g, c * 64, 0, h, l, b);
+                bar_wait(&bars.empty[s], ((t / NS) & 1) ^ 1, gave_up);
+                bar_expect(&bars.full[s], F::stage);
+                for (int m = 0; m < 2; ++m) tma_load(&mq, &bars.full[s], st + m * F::q, 0, m, h, l, b);
+                for (int c = 0; c < VP / 64; ++c) tma_load(&mg, &bars.full[s], st + 2 * F::q + c * F::g, c * 64, 0, h, l, b);
             }
             if (*gave_up) {
                 bar_drain(&bars.kv_full, 0);
-                for (int t = max(0, T_ - NS); t < T_; ++t) bar_drain(&bars.q_full[t % NS], (t / NS) & 1);
+                for (int t = max(0, T_ - NS); t < T_; ++t) bar_drain(&bars.full[t % NS], (t / NS) & 1);
             }
         }
     } else if (warp == 9) {
@@ -507,11 +543,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                ik = shape(is_bf16<T>, DP, true);
             const Operand<F::row> dk = along_row<F::row>(sbase), dq = along_row<F::row>(sbase + F::at_stage),
                                   dqr = over_rows<F::row>(sbase + F::at_stage, F::q);
-            const Operand<128> dv = along_row<128>(sbase + F::at_v), dg = along_row<128>(sbase + F::at_stage + 2 * F::q),
+            const Operand<128> dg = along_row<128>(sbase + F::at_stage + 2 * F::q),
                                dgr = over_rows<128>(sbase + F::at_stage + 2 * F::q, F::g), ds = along_row<128>(sbase + F::at_s);
             auto scores = [&](int t) {
                 const uint32_t st = (t % NS) * F::stage;
-                bar_wait_warp(&bars.q_full[t % NS], (t / NS) & 1, gave_up);
                 bar_wait_warp(&bars.ready[t % NS], (t / NS) & 1, gave_up);
                 if (t > 0) bar_wait_warp(&bars.s_free, (t - 1) & 1, gave_up);
                 fence_after();
@@ -523,13 +558,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                             mma_ss(tS(m), dk.at(m * F::k + i * 32), dq.at(st + m * F::q + i * 32), is, i > 0);
 #pragma unroll
                     for (int i = 0; i < VP / 16; ++i)
-                        mma_ss(tS(2), dv.at((i / 4) * F::v + (i % 4) * 32), dg.at(st + (i / 4) * F::g + (i % 4) * 32), is, i > 0);
+                        mma_ts(tS(2), tmem + F::c_v + i * 8, dg.at(st + (i / 4) * F::g + (i % 4) * 32), is, i > 0);
                     mma_commit(&bars.s_full);
                 }
                 __syncwarp();
             };
-            bar_wait_warp(&bars.kv_full, 0, gave_up);
-            bar_wait_warp(&bars.kv_ready, 0, gave_up);
+            bar_wait_warp(&bars.v_ready, 0, gave_up);
             scores(0);
             for (int t = 0; t < T_; ++t) {
                 if (t + 1 < T_) scores(t + 1);
@@ -544,8 +578,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
                         for (int i = 0; i < kStep / 16; ++i)
                             mma_ss(tK(m), ds.at((1 + m) * F::s + i * 32), dqr.at(st + m * F::q + i * 16 * F::row), ik, t > 0 || i > 0);
-                    mma_commit(&bars.ds_free);
-                    mma_commit(&bars.q_empty[t % NS]);
+                    mma_commit(&bars.empty[t % NS]);
                 }
                 __syncwarp();
             }
@@ -573,7 +606,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int t = 0; t < T_; ++t) {
             const int s = t % NS, g = t / per, h = n * a.G + g, l0 = first + (t % per) * kStep;
             QueryInfo &qi = infos[s];
-            bar_wait_warp(&bars.q_empty[s], ((t / NS) & 1) ^ 1, gave_up);
+            bar_wait_warp(&bars.empty[s], ((t / NS) & 1) ^ 1, gave_up);
             int lo = INT32_MAX, hi = INT32_MIN;
             uint32_t none[2];
             bool every = true;
@@ -604,10 +637,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 qi.hi = hi;
                 qi.all = every;
             }
-            __syncwarp();
-            if (lane == 0) bar_arrive(&bars.info[s]);
+            bar_wait_warp(&bars.full[s], (t / NS) & 1, gave_up);
             if (!every) {  // queries that see nothing take no part, whatever q and g hold
-                bar_wait_warp(&bars.q_full[s], (t / NS) & 1, gave_up);
                 unsigned char *st = base + F::at_stage + s * F::stage;
                 for (int r = lane >> 3; r < kStep; r += 4)
                     if (none[r >> 5] >> (r & 31) & 1) {
@@ -627,6 +658,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const bool use = j < len && (!a.mask || a.mask[kat]);
         const int pos = use && a.pos_k ? a.pos_k[kat] : j;
         float *mine = sums + tid;
+        if (T_ > 0) {  // v to tensor memory: its place is then that of the weights
+            bar_wait_warp(&bars.kv_full, 0, gave_up);
+            bar_wait_warp(&bars.kv_ready, 0, gave_up);
+            for (int c = 0; c < VP / 64; ++c)
+                operand_to_tmem<128>(tmem + F::c_v + c * 32 + half * 16 + lanes, base + F::at_v + c * F::v, rl, half);
+            tmem_store_wait();
+            fence_before();
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (lane == 0) bar_arrive(&bars.v_ready);
+        }
         for (int g = 0; g < a.G; ++g) {
             if (a.nb) {  // this head's bias, and sums from zero
                 asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -638,11 +679,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int u = 0; u < per; ++u) {
                 const int t = g * per + u;
                 const QueryInfo &qi = infos[t % NS];
-                bar_wait_warp(&bars.info[t % NS], (t / NS) & 1, gave_up);
-                const int rlo = pos - qi.hi, rhi = pos - qi.lo;
-                const bool same = rlo >= a.reach || rhi <= -a.reach || rlo == rhi;  // one bucket for the whole step
-                const bool even = !use || (!(a.causal && rhi > 0) && (a.nb == 0 || same));
-                const bool fast = __all_sync(0xffffffffu, even);
                 bar_wait_warp(&bars.s_full, t & 1, gave_up);
                 fence_after();
                 float e[32], x[2][32];
@@ -652,6 +688,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(&bars.s_free);
+                const int rlo = pos - qi.hi, rhi = pos - qi.lo;
+                const bool same = rlo >= a.reach || rhi <= -a.reach || rlo == rhi;  // one bucket for the whole step
+                const bool even = !use || (!(a.causal && rhi > 0) && (a.nb == 0 || same));
+                const bool fast = __all_sync(0xffffffffu, even);
                 float add = 0.f, mul = a.scale_log2;
                 int where = 0;
                 if (fast) {
@@ -717,7 +757,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         mine[last * 256] += run;
                     }
                 }
-                if (t > 0) bar_wait_warp(&bars.ds_free, (t - 1) & 1, gave_up);
+                if (t > 0) bar_wait_warp(&bars.empty[(t - 1) % NS], ((t - 1) / NS) & 1, gave_up);  // those of step t - 1 were used
                 store_operand(base + F::at_s, rl, half, pw);
                 store_operand(base + F::at_s + F::s, rl, half, p0);
                 store_operand(base + F::at_s + 2 * F::s, rl, half, p1);
@@ -727,7 +767,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             if (a.nb) {
                 asm volatile("bar.sync 1, 256;" ::: "memory");
-                float *out = a.part_table + ((static_cast<int64_t>(b) * a.Hkv + n) * a.table_ctas + blockIdx.x) * a.nb * a.G;
+                float *out = a.part_table + ((static_cast<int64_t>(b) * a.Hkv + n) * a.table_ctas + key_tile) * a.nb * a.G;
                 for (int k = warp; k < a.nb; k += 8) {
                     float s = 0.f;
 #pragma unroll
@@ -790,10 +830,10 @@ cudaError_t bwd_kernels(const DattnArgs &a, const BwdMaps &own_rows, const BwdMa
     using Q = GradQShared<DP, VP>;
     using KV = GradKVShared<DP, VP>;
     const int LP = kOwn / a.G;
-    const cudaError_t e = launch_bwd(dattn_grad_q_tc_kernel<T, DP, VP>, dim3((a.Lq + LP - 1) / LP, a.Hkv, a.B),
+    const cudaError_t e = launch_bwd(dattn_grad_q_tc_kernel<T, DP, VP>, dim3((a.Lq + LP - 1) / LP * a.Hkv * a.B),
                                      Q::bytes + 1024 + sizeof(float) * (a.nb ? a.G * (2 * a.reach + 1) : 0), a, own_rows, st);
     if (e != cudaSuccess) return e;
-    return launch_bwd(dattn_grad_kv_tc_kernel<T, DP, VP>, dim3((a.Lk + kOwn - 1) / kOwn, a.Hkv, a.B),
+    return launch_bwd(dattn_grad_kv_tc_kernel<T, DP, VP>, dim3((a.Lk + kOwn - 1) / kOwn * a.Hkv * a.B),
                       KV::bytes + 1024 + KV::table(a.nb, a.reach), a, own_keys, st);
 }
 

@@ -54,12 +54,15 @@ template <int DP, int VP> struct FwdShared {
 __host__ __device__ inline int bias_span(int reach) { return 2 * (reach + kKeys) + 1; }
 
 // A barrier's wait names a phase by its parity only, so nobody may lag two
-// phases behind: what both sides pass once a step, with the tensor core up to
-// a step ahead, has a barrier for even steps and one for odd.
+// phases behind: what the tensor core passes up to a step ahead has a barrier
+// for even steps and one for odd. A wait costs some 140 clocks even where it
+// does not wait, so the warp that issues the products has three to a step:
+// `ready` stands for K, V and the step's infos, and s_full for all products
+// issued before, P v of the step before last among them.
 struct FwdBars {
     uint64_t q_full, fin;
-    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], info[4], v_ready[4];
-    uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // of each map, for even and odd steps
+    uint64_t full[4], ready[4], empty[4];   // of a stage: loaded, cleared of unused keys, free
+    uint64_t s_full[2][2], p_full[2][2];    // of each map, for even and odd steps
     uint32_t tmem, gave_up;
 };
 
@@ -102,20 +105,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         bar_init(&bars.q_full, 1);
         bar_init(&bars.fin, 1);
         for (int s = 0; s < NS; ++s) {
-            bar_init(&bars.k_full[s], 1);
-            bar_init(&bars.k_empty[s], 1);
-            bar_init(&bars.v_full[s], 1);
-            bar_init(&bars.v_empty[s], 1);
-            bar_init(&bars.info[s], 1);
-            bar_init(&bars.v_ready[s], 1);
+            bar_init(&bars.full[s], 1);
+            bar_init(&bars.ready[s], 1);
+            bar_init(&bars.empty[s], 1);
         }
-        for (int m = 0; m < 2; ++m) {
+        for (int m = 0; m < 2; ++m)
             for (int i = 0; i < 2; ++i) {
                 bar_init(&bars.s_full[m][i], 1);
                 bar_init(&bars.p_full[m][i], 4);
-                bar_init(&bars.o_done[m][i], 1);
             }
-        }
         bars.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         tma_prefetch(&mq);
@@ -142,22 +140,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             for (int m = 0; m < 2; ++m) tma_load(&mq, &bars.q_full, base + m * F::q, 0, m, n * a.G, l0, b);
             for (int t = 0; t < T_; ++t) {
                 const int s = t % NS;
-                const uint32_t parity = (t / NS) & 1;
                 unsigned char *st = base + 2 * F::q + s * F::stage;
-                bar_wait(&bars.k_empty[s], parity ^ 1, gave_up);
-                bar_expect(&bars.k_full[s], 2 * F::k);
-                for (int m = 0; m < 2; ++m) tma_load(&mk, &bars.k_full[s], st + m * F::k, 0, m, n, jb + t * kKeys, b);
-                bar_wait(&bars.v_empty[s], parity ^ 1, gave_up);
-                bar_expect(&bars.v_full[s], (VP / 64) * F::vblock);
+                bar_wait(&bars.empty[s], ((t / NS) & 1) ^ 1, gave_up);
+                bar_expect(&bars.full[s], F::stage);
+                for (int m = 0; m < 2; ++m) tma_load(&mk, &bars.full[s], st + m * F::k, 0, m, n, jb + t * kKeys, b);
                 for (int c = 0; c < VP / 64; ++c)
-                    tma_load(&mv, &bars.v_full[s], st + 2 * F::k + c * F::vblock, c * 64, 0, n, jb + t * kKeys, b);
+                    tma_load(&mv, &bars.full[s], st + 2 * F::k + c * F::vblock, c * 64, 0, n, jb + t * kKeys, b);
             }
             if (*gave_up) {  // leave no copy in flight
                 bar_drain(&bars.q_full, 0);
-                for (int t = max(0, T_ - NS); t < T_; ++t) {
-                    bar_drain(&bars.k_full[t % NS], (t / NS) & 1);
-                    bar_drain(&bars.v_full[t % NS], (t / NS) & 1);
-                }
+                for (int t = max(0, T_ - NS); t < T_; ++t) bar_drain(&bars.full[t % NS], (t / NS) & 1);
             }
         }
     } else if (warp == 9) {
@@ -171,17 +163,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const Operand<128> dv = over_rows<128>(sst + 2 * F::k, F::vblock);
             auto scores = [&](int t) {
                 const uint32_t st = (t % NS) * F::stage;
-                bar_wait_warp(&bars.k_full[t % NS], (t / NS) & 1, gave_up);
+                if (t < T_) bar_wait_warp(&bars.ready[t % NS], (t / NS) & 1, gave_up);
                 fence_after();
                 if (issue) {
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
+                        if (t < T_)
 #pragma unroll
-                        for (int i = 0; i < DP / 16; ++i)
-                            mma_ss(tS(m, t), dq.at(m * F::q + i * 32), dk.at(st + m * F::k + i * 32), iqk, i > 0);
+                            for (int i = 0; i < DP / 16; ++i)
+                                mma_ss(tS(m, t), dq.at(m * F::q + i * 32), dk.at(st + m * F::k + i * 32), iqk, i > 0);
                         mma_commit(&bars.s_full[m][t & 1]);
                     }
-                    mma_commit(&bars.k_empty[t % NS]);
                 }
                 __syncwarp();
             };
@@ -191,9 +183,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 const int s = t % NS;
                 // Their columns held the weights of step t - 1, whose products
                 // were issued before and are formed in this order.
-                if (t + 1 < T_) scores(t + 1);
-                bar_wait_warp(&bars.v_full[s], (t / NS) & 1, gave_up);
-                bar_wait_warp(&bars.v_ready[s], (t / NS) & 1, gave_up);
+                scores(t + 1);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     bar_wait_warp(&bars.p_full[m][t & 1], (t >> 1) & 1, gave_up);
@@ -202,8 +192,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                         for (int i = 0; i < kKeys / 16; ++i)
                             mma_ts(tO[m], tS(m, t) + i * 8, dv.at(s * F::stage + i * 16 * 128), ipv, t > 0 || i > 0);
-                        mma_commit(&bars.o_done[m][t & 1]);
-                        if (m == 1) mma_commit(&bars.v_empty[s]);
+                        if (m == 1) mma_commit(&bars.empty[s]);
                     }
                     __syncwarp();
                 }
@@ -216,9 +205,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int t = 0; t < T_; ++t) {
             const int s = t % NS, j0 = jb + t * kKeys;
             KeyInfo &ki = infos[s];
-            // The slot is free once P v of NS steps ago is done: the softmax
+            // The stage is free once P v of NS steps ago is done: the softmax
             // warps had by then read its infos, and the products its V.
-            bar_wait_warp(&bars.v_empty[s], ((t / NS) & 1) ^ 1, gave_up);
+            bar_wait_warp(&bars.empty[s], ((t / NS) & 1) ^ 1, gave_up);
             int lo = INT32_MAX, hi = INT32_MIN;
             uint32_t every = 0xffffffffu, stale = 0, valid[2];
 #pragma unroll
@@ -248,10 +237,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 ki.valid[0] = valid[0];
                 ki.valid[1] = valid[1];
             }
-            __syncwarp();
-            if (lane == 0) bar_arrive(&bars.info[s]);
+            bar_wait_warp(&bars.full[s], (t / NS) & 1, gave_up);
             if (stale) {  // 0 * NaN is NaN: the rows of V of unused keys become zeros
-                bar_wait_warp(&bars.v_full[s], (t / NS) & 1, gave_up);
                 unsigned char *v = base + 2 * F::q + s * F::stage + 2 * F::k;
 #pragma unroll 1
                 for (int r = lane >> 3; r < kKeys; r += 4)
@@ -261,7 +248,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 fence_async();
             }
             __syncwarp();
-            if (lane == 0) bar_arrive(&bars.v_ready[s]);
+            if (lane == 0) bar_arrive(&bars.ready[s]);
         }
     } else {
         const int m = warp >> 2, rl = (warp & 3) * 32 + lane;
@@ -274,16 +261,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
         for (int t = 0; t < T_; ++t) {
             const KeyInfo &ki = infos[t % NS];
-            bar_wait_warp(&bars.info[t % NS], (t / NS) & 1, gave_up);
+            bar_wait_warp(&bars.s_full[m][t & 1], (t >> 1) & 1, gave_up);
+            fence_after();
+            float s[kKeys];
+            tmem_load(tS(m, t) + lanes, s);
             const int rlo = ki.lo - pos, rhi = ki.hi - pos;
             const bool all = ki.all;
             // One bias for all of the row's keys in this step, none of them later.
             const bool even = !live || (!(a.causal && rhi > 0) && (a.nb == 0 || rlo >= a.reach || rhi <= -a.reach || rlo == rhi));
             const bool fast = __all_sync(0xffffffffu, even) && a.scale_log2 > 0.f;
-            bar_wait_warp(&bars.s_full[m][t & 1], (t >> 1) & 1, gave_up);
-            fence_after();
-            float s[kKeys];
-            tmem_load(tS(m, t) + lanes, s);
             float mul = a.scale_log2, add = 0.f;
             if (fast) {
                 add = tb[min(max(rlo, -a.reach), a.reach)];
@@ -338,7 +324,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 sum[0] = mul2(sum[0], sh);
                 sum[1] = mul2(sum[1], sh);
                 if (t > 0) {
-                    bar_wait_warp(&bars.o_done[m][(t - 1) & 1], ((t - 1) >> 1) & 1, gave_up);
+                    // P v of step t - 1 was issued before the scores of step t + 1.
+                    bar_wait_warp(&bars.s_full[m][(t + 1) & 1], ((t + 1) >> 1) & 1, gave_up);
                     fence_after();
 #pragma unroll 1
                     for (int c = 0; c < VP; c += 32) {
@@ -369,8 +356,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         row_l[m][rl] = sum[0].x + sum[0].y + (sum[1].x + sum[1].y);
         row_m[m][rl] = ref;
-        if (T_ > 0)
-            for (int i = 0; i < 2; ++i) bar_wait_warp(&bars.o_done[i][(T_ - 1) & 1], ((T_ - 1) >> 1) & 1, gave_up);
+        if (T_ > 0) bar_wait_warp(&bars.fin, 0, gave_up);
         fence_after();
         asm volatile("bar.sync 1, 256;" ::: "memory");
         const float s0 = row_l[0][rl], s1 = row_l[1][rl];
