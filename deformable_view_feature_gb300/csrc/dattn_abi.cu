@@ -68,19 +68,19 @@ struct DattnPlan {
     DattnArgs a;
     int elem;
     bool tensor;
-    size_t part_o, part_ml, delta, part_table, total;
+    size_t part_o, part_ml, part_kv, delta, part_table, total;
 };
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-// CTAs per tile of rows. Where the tiles alone leave most of the 152 SMs
-// without work, the keys are split among enough CTAs to give each one about
-// one, and no fewer than two key tiles (128 keys) to each.
-int split_count(int64_t tiles, int keys)
+// CTAs to share a tile where the tiles alone leave SMs without work: enough
+// that each of the 152 SMs has its `resident` ones, each with at least one
+// of the `steps` that a tile's walk has.
+int split_count(int64_t tiles, int64_t steps, int resident)
 {
-    if (tiles <= 0 || tiles > 76) return 1;
-    const int64_t most = keys / 128, want = 152 / tiles;
-    return static_cast<int>(most < 1 ? 1 : want < most ? want : most);
+    const int64_t want = tiles > 0 ? 152 * resident / tiles : 1;
+    const int64_t n = want < steps ? want : steps;
+    return static_cast<int>(n < 1 ? 1 : n);
 }
 
 da_status dattn_plan(const dattn_problem *pr, bool backward, DattnPlan &p)
@@ -148,15 +148,19 @@ da_status dattn_plan(const dattn_problem *pr, bool backward, DattnPlan &p)
     p.tensor = tensor_serves(d, backward);
     const int64_t bn = static_cast<int64_t>(a.B) * a.Hkv;
     size_t at = 0;
-    a.splits = 1;
+    a.splits = a.row_splits = 1;
     a.keys_per_split = a.Lk > 0 ? a.Lk : 1;
-    if (!backward) {
-        const int qt = p.tensor ? 128 / G * G : dattn_general_row_tile(a);
-        const int n = split_count(bn * ((rows + qt - 1) / qt), a.Lk);
+    const auto split_keys = [&](int64_t tiles, int least, int resident) {
+        const int n = split_count(tiles, a.Lk / least, resident);
         if (n > 1) {
             a.keys_per_split = ((a.Lk + n - 1) / n + 63) / 64 * 64;
-            a.splits = p.tensor ? n : (a.Lk + a.keys_per_split - 1) / a.keys_per_split;
+            a.splits = (a.Lk + a.keys_per_split - 1) / a.keys_per_split;
         }
+    };
+    if (!backward) {
+        // A tensor-core CTA fills an SM, two of the general ones fit.
+        const int qt = p.tensor ? 128 / G * G : dattn_general_row_tile(a);
+        split_keys(bn * ((rows + qt - 1) / qt), 128, p.tensor ? 1 : 2);
         if (a.splits > 1) {
             p.part_o = at;
             at += round256(sizeof(float) * bn * rows * a.splits * 2 * a.Dv);
@@ -164,10 +168,23 @@ da_status dattn_plan(const dattn_problem *pr, bool backward, DattnPlan &p)
             at += round256(sizeof(float) * bn * rows * a.splits * 4);
         }
     } else {
-        // Sized for the general kernels too, which take over where grad_out
+        // Sized for the general kernels, which also take over where grad_out
         // turns out not to be aligned.
-        const int kt = dattn_general_key_tile(a);
-        a.table_ctas = (a.Lk + kt - 1) / kt;
+        const int tile = dattn_general_tile(a);
+        const int64_t key_tiles = (a.Lk + tile - 1) / tile, row_tiles = (rows + tile - 1) / tile;
+        split_keys(bn * row_tiles, tile, 2);
+        a.row_splits = split_count(bn * key_tiles, row_tiles, 1);  // one CTA fills an SM's shared memory
+        a.table_ctas = static_cast<int32_t>(key_tiles * a.row_splits);
+        if (a.splits > 1) {
+            p.part_o = at;
+            at += round256(sizeof(float) * bn * rows * a.splits * 2 * a.D);
+            p.part_ml = at;
+            at += round256(sizeof(float) * bn * rows * a.splits * 2);
+        }
+        if (a.row_splits > 1) {
+            p.part_kv = at;
+            at += round256(sizeof(float) * bn * a.Lk * a.row_splits * (a.Dv + 2 * a.D));
+        }
         p.delta = at;
         at += round256(sizeof(float) * bn * 2 * rows);
         p.part_table = at;
@@ -198,6 +215,7 @@ da_status dattn_buffers(DattnPlan &p, void *ws, size_t ws_bytes)
     char *w = static_cast<char *>(ws);
     a.part_o = reinterpret_cast<float *>(w + p.part_o);
     a.part_ml = reinterpret_cast<float *>(w + p.part_ml);
+    a.part_kv = reinterpret_cast<float *>(w + p.part_kv);
     a.delta = reinterpret_cast<float *>(w + p.delta);
     a.part_table = reinterpret_cast<float *>(w + p.part_table);
     return DA_OK;

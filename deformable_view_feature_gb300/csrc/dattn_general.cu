@@ -374,7 +374,8 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_co
     int *kpos = reinterpret_cast<int *>(sm + F::info), *kseen = kpos + KT;
     const BiasTable bt{sm + F::floats, reinterpret_cast<uint16_t *>(sm + F::floats + a.nb * a.G)};
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int n = blockIdx.y, b = blockIdx.z, r0 = blockIdx.x * QT;
+    const int tile = blockIdx.x / a.splits, split = blockIdx.x - tile * a.splits;
+    const int n = blockIdx.y, b = blockIdx.z, r0 = tile * QT;
     const int len = dattn_length(a, b);
     const int64_t ob = static_cast<int64_t>(b) * a.Lq * a.H * a.Dv;  // of out-like tensors
 
@@ -414,7 +415,9 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_co
     int end = len;
     if (a.causal && !a.pos_q && !a.pos_k)
         end = min(end, len - a.Lq + static_cast<int>(a.div_G.div(min(r0 + QT, a.rows) - 1)) + 1);
-    for (int j0 = 0; j0 < end; j0 += KT) {
+    const int first = split * a.keys_per_split;
+    end = min(end, first + a.keys_per_split);
+    for (int j0 = first; j0 < end; j0 += KT) {
         __syncthreads();
         load_key_info(a, b, end, j0, KT, kpos, kseen);
         __syncthreads();
@@ -453,18 +456,49 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_co
     for (int i = 0; i < M; ++i) {
         if (ri[i].l < 0) continue;
         const int r = r0 + ty + 16 * i, h = n * a.G + ri[i].g;
+        const int64_t row = (static_cast<int64_t>(b) * a.Hkv + n) * a.rows + r;
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            if (tx == 0) a.delta[((static_cast<int64_t>(b) * a.Hkv + n) * 2 + m) * a.rows + r] = dl[m][i] + rest[m][i];
+            float *delta = a.delta + ((static_cast<int64_t>(b) * a.Hkv + n) * 2 + m) * a.rows + r;
+            if (tx == 0) {
+                if (a.splits == 1) *delta = dl[m][i] + rest[m][i];
+                else if (split == 0) *delta = dl[m][i];
+                if (a.splits > 1) a.part_ml[(row * a.splits + split) * 2 + m] = rest[m][i];
+            }
             const int64_t at = (((static_cast<int64_t>(b) * a.Lq + ri[i].l) * a.H + h) * 2 + m) * a.D;
 #pragma unroll
             for (int c = 0; c < F::ND; ++c) {
                 const float x[4] = {acc[m][i][c].x, acc[m][i][c].y, acc[m][i][c].z, acc[m][i][c].w};
-                for (int e = 0; e < 4; ++e)
-                    if (4 * tx + 64 * c + e < a.D)
-                        static_cast<T *>(a.grad_q)[at + 4 * tx + 64 * c + e] = dattn_round<T>(x[e] * a.scale);
+                for (int e = 0; e < 4; ++e) {
+                    const int d = 4 * tx + 64 * c + e;
+                    if (d >= a.D) continue;
+                    if (a.splits > 1) a.part_o[((row * a.splits + split) * 2 + m) * a.D + d] = x[e];
+                    else static_cast<T *>(a.grad_q)[at + d] = dattn_round<T>(x[e] * a.scale);
+                }
             }
         }
+    }
+}
+
+// Joins the parts of grad_q and of the d_m: one warp per row.
+template <typename T> __global__ void __launch_bounds__(kThreadsG) dattn_join_q_kernel(const __grid_constant__ DattnArgs a)
+{
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreadsG / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const int64_t bn = row / a.rows;
+    if (bn >= static_cast<int64_t>(a.B) * a.Hkv) return;
+    const int r = static_cast<int>(row - bn * a.rows), b = static_cast<int>(bn / a.Hkv), n = static_cast<int>(bn - b * a.Hkv);
+    const int l = static_cast<int>(a.div_G.div(r)), h = n * a.G + r - l * a.G;
+    if (lane < 2) {
+        float s = 0.f;
+        for (int k = 0; k < a.splits; ++k) s += a.part_ml[(row * a.splits + k) * 2 + lane];
+        a.delta[(bn * 2 + lane) * a.rows + r] += s;
+    }
+    T *dst = static_cast<T *>(a.grad_q) + ((static_cast<int64_t>(b) * a.Lq + l) * a.H + h) * 2 * a.D;
+    for (int d = lane; d < 2 * a.D; d += 32) {
+        float s = 0.f;
+        for (int k = 0; k < a.splits; ++k) s += a.part_o[(row * a.splits + k) * 2 * a.D + d];
+        dst[d] = dattn_round<T>(s * a.scale);
     }
 }
 
@@ -485,7 +519,8 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_kv_kernel(const __grid_c
     // Each warp's sums per bucket and head.
     float *sums = sm + F::floats + bias_floats(a.nb, a.G, a.reach) + (threadIdx.x >> 5) * a.nb * a.G;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, lane = threadIdx.x & 31;
-    const int n = blockIdx.y, b = blockIdx.z, j0 = blockIdx.x * KT;
+    const int tile = blockIdx.x / a.row_splits, split = blockIdx.x - tile * a.row_splits;
+    const int n = blockIdx.y, b = blockIdx.z, j0 = tile * KT;
     const int len = dattn_length(a, b);
     const int64_t ob = static_cast<int64_t>(b) * a.Lq * a.H * a.Dv;
 
@@ -507,7 +542,10 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_kv_kernel(const __grid_c
     int first = 0;
     // The first query that sees the tile's first key, where positions are indices.
     if (a.causal && !a.pos_q && !a.pos_k) first = min(max(j0 - (len - a.Lq), 0), a.Lq) * a.G;
-    const int last = j0 < len ? a.rows : 0;
+    // This CTA's share of the rows, in whole tiles.
+    const int steps = (a.rows - first + RT - 1) / RT, share = (steps + a.row_splits - 1) / a.row_splits * RT;
+    first += split * share;
+    const int last = j0 < len ? min(a.rows, first + share) : 0;
     for (int r0 = first; r0 < last; r0 += RT) {
         __syncthreads();
         for (int i = threadIdx.x; i < RT; i += kThreadsG) {
@@ -590,12 +628,15 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_kv_kernel(const __grid_c
         const int j = j0 + ty + 16 * i;
         if (j >= a.Lk) continue;
         const int64_t at = (static_cast<int64_t>(b) * a.Lk + j) * a.Hkv + n;
+        float *part = a.row_splits > 1 ? a.part_kv + (at * a.row_splits + split) * (a.Dv + 2 * a.D) : nullptr;
 #pragma unroll
         for (int c = 0; c < F::NV; ++c) {
             const float x[4] = {gv[i][c].x, gv[i][c].y, gv[i][c].z, gv[i][c].w};
             for (int e = 0; e < 4; ++e)
-                if (4 * tx + 64 * c + e < a.Dv)
-                    static_cast<T *>(a.grad_v)[at * a.Dv + 4 * tx + 64 * c + e] = dattn_round<T>(x[e]);
+                if (4 * tx + 64 * c + e < a.Dv) {
+                    if (part) part[4 * tx + 64 * c + e] = x[e];
+                    else static_cast<T *>(a.grad_v)[at * a.Dv + 4 * tx + 64 * c + e] = dattn_round<T>(x[e]);
+                }
         }
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -603,8 +644,10 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_kv_kernel(const __grid_c
             for (int c = 0; c < F::ND; ++c) {
                 const float x[4] = {gk[m][i][c].x, gk[m][i][c].y, gk[m][i][c].z, gk[m][i][c].w};
                 for (int e = 0; e < 4; ++e)
-                    if (4 * tx + 64 * c + e < a.D)
-                        static_cast<T *>(a.grad_k)[(at * 2 + m) * a.D + 4 * tx + 64 * c + e] = dattn_round<T>(x[e] * a.scale);
+                    if (4 * tx + 64 * c + e < a.D) {
+                        if (part) part[a.Dv + m * a.D + 4 * tx + 64 * c + e] = x[e];
+                        else static_cast<T *>(a.grad_k)[(at * 2 + m) * a.D + 4 * tx + 64 * c + e] = dattn_round<T>(x[e] * a.scale);
+                    }
             }
     }
     if (a.nb) {
@@ -616,6 +659,20 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_kv_kernel(const __grid_c
             for (int w = 0; w < kThreadsG / 32; ++w) s += all[w * a.nb * a.G + i];
             out[i] = s;
         }
+    }
+}
+
+// Joins the parts of grad_v and grad_k: one warp per key and key head.
+template <typename T> __global__ void __launch_bounds__(kThreadsG) dattn_join_kv_kernel(const __grid_constant__ DattnArgs a)
+{
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * (kThreadsG / 32) + (threadIdx.x >> 5);
+    if (at >= static_cast<int64_t>(a.B) * a.Lk * a.Hkv) return;
+    const int width = a.Dv + 2 * a.D;
+    for (int d = threadIdx.x & 31; d < width; d += 32) {
+        float s = 0.f;
+        for (int k = 0; k < a.row_splits; ++k) s += a.part_kv[(at * a.row_splits + k) * width + d];
+        if (d < a.Dv) static_cast<T *>(a.grad_v)[at * a.Dv + d] = dattn_round<T>(s);
+        else static_cast<T *>(a.grad_k)[at * 2 * a.D + d - a.Dv] = dattn_round<T>(s * a.scale);
     }
 }
 
@@ -679,13 +736,24 @@ template <typename T, int DP> cudaError_t backward_width(const DattnArgs &a, cud
 {
     using F = BwdTile<T, DP>;
     cudaError_t e = cudaSuccess;
+    const int warps = kThreadsG / 32;
     if (a.rows > 0) {
-        const dim3 grid(static_cast<unsigned>((a.rows + F::RT - 1) / F::RT), a.Hkv, a.B);
+        const dim3 grid(static_cast<unsigned>((a.rows + F::RT - 1) / F::RT * a.splits), a.Hkv, a.B);
         e = launch(dattn_grad_q_kernel<T, DP>, grid, F::floats + table_floats(a), a, st);
+        if (e == cudaSuccess && a.splits > 1) {
+            const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv * a.rows;
+            dattn_join_q_kernel<T><<<static_cast<unsigned>((rows + warps - 1) / warps), kThreadsG, 0, st>>>(a);
+            e = cudaGetLastError();
+        }
     }
     if (e == cudaSuccess && a.Lk > 0) {
-        const dim3 grid(static_cast<unsigned>((a.Lk + F::KT - 1) / F::KT), a.Hkv, a.B);
-        e = launch(dattn_grad_kv_kernel<T, DP>, grid, F::floats + table_floats(a) + (kThreadsG / 32) * a.nb * a.G, a, st);
+        const dim3 grid(static_cast<unsigned>((a.Lk + F::KT - 1) / F::KT * a.row_splits), a.Hkv, a.B);
+        e = launch(dattn_grad_kv_kernel<T, DP>, grid, F::floats + table_floats(a) + warps * a.nb * a.G, a, st);
+        if (e == cudaSuccess && a.row_splits > 1) {
+            const int64_t keys = static_cast<int64_t>(a.B) * a.Lk * a.Hkv;
+            dattn_join_kv_kernel<T><<<static_cast<unsigned>((keys + warps - 1) / warps), kThreadsG, 0, st>>>(a);
+            e = cudaGetLastError();
+        }
     }
     return e;
 }
@@ -712,7 +780,7 @@ cudaError_t any_type(const DattnArgs &a, int dtype, bool backward, cudaStream_t 
 
 // Sixteen rows or fewer per key head (single tokens) take a 16-row tile.
 int dattn_general_row_tile(const DattnArgs &a) { return a.rows <= 16 ? 16 : 64; }
-int dattn_general_key_tile(const DattnArgs &a) { return padded_width(a) <= 64 ? 64 : 32; }
+int dattn_general_tile(const DattnArgs &a) { return padded_width(a) <= 64 ? 64 : 32; }
 
 cudaError_t dattn_forward_general(const DattnArgs &a, int dtype, cudaStream_t st) { return any_type(a, dtype, false, st); }
 

@@ -37,7 +37,12 @@ struct DattnArgs {
     float *grad_lam, *grad_table;
     float *delta;       // [B, Hkv, 2, rows] the d_m of dattn.h
     float *part_table;  // [key-tile CTAs, nb * G]
-    int32_t table_ctas; // key tiles per (b, key head)
+    int32_t table_ctas; // CTAs of the second kernel per (b, key head)
+    // The general kernels' splits backward: grad_q over the keys (splits,
+    // keys_per_split, part_o [.., 2, D], part_ml [.., 2]), grad_k and grad_v
+    // over the rows (part_kv [.., Dv + 2 D]).
+    int32_t row_splits;
+    float *part_kv;
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -72,6 +77,6 @@ cudaError_t dattn_backward_general(const DattnArgs &a, int dtype, cudaStream_t s
 cudaError_t dattn_merge(const DattnArgs &a, int dtype, cudaStream_t st);
 cudaError_t dattn_finish_backward(const DattnArgs &a, cudaStream_t st);
 int dattn_general_row_tile(const DattnArgs &a);   // rows of a forward tile
-int dattn_general_key_tile(const DattnArgs &a);   // keys of a backward key tile
+int dattn_general_tile(const DattnArgs &a);       // rows, and keys, of a backward tile
 
 }  // namespace da
