@@ -144,6 +144,8 @@ da_status dattn_plan(const dattn_problem *pr, bool backward, DattnPlan &p)
     a.div_G = FastDiv::make(static_cast<uint32_t>(G));
     a.scale = d.scale;
     a.scale_log2 = static_cast<float>(static_cast<double>(d.scale) * 1.4426950408889634);
+    a.wide = d.dtype == DA_F32 && d.width % 4 == 0 && d.value_width % 4 == 0 && aligned(d.q, 16) && aligned(d.k, 16) && aligned(d.v, 16);
+    for (int i = 0; i < 4; ++i) a.wide = a.wide && a.qs[i] % 4 == 0 && a.ks[i] % 4 == 0 && (i == 3 || a.vs[i] % 4 == 0);
     p.elem = d.dtype == DA_F32 ? 4 : 2;
     p.tensor = tensor_serves(d, backward);
     const int64_t bn = static_cast<int64_t>(a.B) * a.Hkv;
@@ -287,6 +289,7 @@ da_status dattn_backward(const dattn_problem *p, const void *out, const void *ou
     if (!grad_lam || (a.nb > 0 && !grad_table)) return da::fail(DA_ERR_NULL, "grad_lam or grad_table is NULL");
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
+    a.wide = a.wide && da::aligned(grad_out, 16);
     if (pl.tensor && da::aligned(grad_out, 16) && da::aligned(out, 16) && da::aligned(out1, 16)) {
         a.table_ctas = (a.Lk + 127) / 128;
         if ((st = da::dattn_backward_tensor(a, p->dtype, cs)) != DA_OK) return st;

@@ -137,33 +137,45 @@ __device__ __forceinline__ RowInfo row_info(const DattnArgs &a, int b, int len, 
     return i;
 }
 
+// Four channels d .. d + 3 of a row, zeros past the width. `wide`: fp32 rows
+// that 16-byte loads may read, whose width is a multiple of four.
+template <typename T> __device__ __forceinline__ float4 load4(const T *row, int d, int width, bool wide)
+{
+    if constexpr (sizeof(T) == 4)
+        if (wide) return d < width ? *reinterpret_cast<const float4 *>(row + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+    return make_float4(d < width ? dattn_float(row[d]) : 0.f, d + 1 < width ? dattn_float(row[d + 1]) : 0.f,
+                       d + 2 < width ? dattn_float(row[d + 2]) : 0.f, d + 3 < width ? dattn_float(row[d + 3]) : 0.f);
+}
+
 // Tile of rows of a tensor with two maps (or one) to shared memory as fp32;
 // channels past the width and rows without a query are zeros.
 template <typename T, int W>
 __device__ void load_rows(const DattnArgs &a, const void *base, int64_t at, int64_t sl, int64_t sh, int n, int r0,
                           int count, int width, float *dst)
 {
-    for (int i = threadIdx.x; i < count * W; i += kThreadsG) {
-        const int row = i / W, d = i - row * W, r = r0 + row;
-        float v = 0.f;
-        if (r < a.rows && d < width) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < count * (W / 4); i += kThreadsG) {
+        const int row = i / (W / 4), d = (i - row * (W / 4)) * 4, r = r0 + row;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < a.rows) {
             const int l = static_cast<int>(a.div_G.div(r)), g = r - l * a.G;
-            v = dattn_float(static_cast<const T *>(base)[at + l * sl + static_cast<int64_t>(n * a.G + g) * sh + d]);
+            v = load4(static_cast<const T *>(base) + at + l * sl + static_cast<int64_t>(n * a.G + g) * sh, d, width, a.wide);
         }
-        dst[row * (W + 4) + d] = v;
+        *reinterpret_cast<float4 *>(dst + row * (W + 4) + d) = v;
     }
 }
 
 // Tile of keys or values; keys that are not to be used are zeros.
 template <typename T, int W>
-__device__ void load_keys(const void *base, int64_t at, int64_t sl, int j0, int count, int width, const int *seen,
-                          float *dst)
+__device__ void load_keys(const DattnArgs &a, const void *base, int64_t at, int64_t sl, int j0, int count, int width,
+                          const int *seen, float *dst)
 {
-    for (int i = threadIdx.x; i < count * W; i += kThreadsG) {
-        const int row = i / W, d = i - row * W;
-        float v = 0.f;
-        if (d < width && seen[row]) v = dattn_float(static_cast<const T *>(base)[at + (j0 + row) * sl + d]);
-        dst[row * (W + 4) + d] = v;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < count * (W / 4); i += kThreadsG) {
+        const int row = i / (W / 4), d = (i - row * (W / 4)) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (seen[row]) v = load4(static_cast<const T *>(base) + at + (j0 + row) * sl, d, width, a.wide);
+        *reinterpret_cast<float4 *>(dst + row * (W + 4) + d) = v;
     }
 }
 
@@ -190,7 +202,7 @@ template <typename T, int DP, int QT> struct FwdTile {
 };
 
 template <typename T, int DP, int QT>
-__global__ void __launch_bounds__(kThreadsG) dattn_fwd_kernel(const __grid_constant__ DattnArgs a)
+__global__ void __launch_bounds__(kThreadsG, DP == 32 || (DP == 64 && QT == 16) ? 2 : 1) dattn_fwd_kernel(const __grid_constant__ DattnArgs a)
 {
     using F = FwdTile<T, DP, QT>;
     constexpr int M = F::M, N = F::N, NC = F::NC, KT = F::KT;
@@ -231,8 +243,8 @@ __global__ void __launch_bounds__(kThreadsG) dattn_fwd_kernel(const __grid_const
         load_key_info(a, b, end, j0, KT, kpos, kseen);
         __syncthreads();
         for (int m = 0; m < 2; ++m)
-            load_keys<T, DP>(a.k, b * a.ks[0] + n * a.ks[2] + m * a.ks[3], a.ks[1], j0, KT, a.D, kseen, sk + m * KT * (DP + 4));
-        load_keys<T, F::WV>(a.v, b * a.vs[0] + n * a.vs[2], a.vs[1], j0, KT, a.Dv, kseen, sv);
+            load_keys<T, DP>(a, a.k, b * a.ks[0] + n * a.ks[2] + m * a.ks[3], a.ks[1], j0, KT, a.D, kseen, sk + m * KT * (DP + 4));
+        load_keys<T, F::WV>(a, a.v, b * a.vs[0] + n * a.vs[2], a.vs[1], j0, KT, a.Dv, kseen, sv);
         __syncthreads();
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
@@ -422,8 +434,8 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_co
         load_key_info(a, b, end, j0, KT, kpos, kseen);
         __syncthreads();
         for (int m = 0; m < 2; ++m)
-            load_keys<T, DP>(a.k, b * a.ks[0] + n * a.ks[2] + m * a.ks[3], a.ks[1], j0, KT, a.D, kseen, sk + m * KT * (DP + 4));
-        load_keys<T, F::WV>(a.v, b * a.vs[0] + n * a.vs[2], a.vs[1], j0, KT, a.Dv, kseen, sv);
+            load_keys<T, DP>(a, a.k, b * a.ks[0] + n * a.ks[2] + m * a.ks[3], a.ks[1], j0, KT, a.D, kseen, sk + m * KT * (DP + 4));
+        load_keys<T, F::WV>(a, a.v, b * a.vs[0] + n * a.vs[2], a.vs[1], j0, KT, a.Dv, kseen, sv);
         __syncthreads();
         float e[M][N];
         scores<M, N, F::WV>(sg, sv, ty, tx, e);
@@ -529,8 +541,8 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_kv_kernel(const __grid_c
     load_key_info(a, b, len, j0, KT, kpos, kseen);
     __syncthreads();
     for (int m = 0; m < 2; ++m)
-        load_keys<T, DP>(a.k, b * a.ks[0] + n * a.ks[2] + m * a.ks[3], a.ks[1], j0, KT, a.D, kseen, sk + m * KT * (DP + 4));
-    load_keys<T, F::WV>(a.v, b * a.vs[0] + n * a.vs[2], a.vs[1], j0, KT, a.Dv, kseen, sv);
+        load_keys<T, DP>(a, a.k, b * a.ks[0] + n * a.ks[2] + m * a.ks[3], a.ks[1], j0, KT, a.D, kseen, sk + m * KT * (DP + 4));
+    load_keys<T, F::WV>(a, a.v, b * a.vs[0] + n * a.vs[2], a.vs[1], j0, KT, a.Dv, kseen, sv);
     float4 gv[M][F::NV], gk[2][M][F::ND];
 #pragma unroll
     for (int i = 0; i < M; ++i) {

@@ -21,6 +21,7 @@ struct DattnArgs {
     const int32_t *bmap, *pos_q, *pos_k, *lengths;
     const uint8_t *mask;
     int32_t B, Lq, Lk, H, Hkv, G, D, Dv, nb, reach, causal;
+    int32_t wide;       // fp32, widths and strides of whole 16 bytes, aligned
     int32_t rows;       // Lq * G
     FastDiv div_G;
     float scale;        // of the scores
