@@ -30,7 +30,7 @@ __all__ = ["da_forward", "da_backward", "da_forward_fused", "da_backward_fused",
            "da_backward_projected", "warpaffine_u8", "warpaffine_preprocess", "backward_workspace_size",
            "backward_path", "da_backward_bin", "DeformableAggregationFunction", "HostPipeline", "DaError", "library_path", "load_library", "da_version",
            "gn_forward", "gn_backward", "GroupNormActFunction", "dattn_forward", "dattn_backward", "dattn_path",
-           "relative_buckets", "DifferentialAttentionFunction"]
+           "relative_buckets", "DifferentialAttentionFunction", "waits_gave_up"]
 
 DA_F32, DA_BF16, DA_F16 = 0, 1, 2
 _STATUS = {0: "DA_OK", 1: "DA_ERR_NULL", 2: "DA_ERR_SHAPE", 3: "DA_ERR_ALIGN",
@@ -115,7 +115,8 @@ def load_library():
     lib.dattn_workspace_size.argtypes = [vp, ctypes.c_int32, psize]
     lib.dattn_forward.argtypes = [vp] * 5 + [ctypes.c_size_t, vp]
     lib.dattn_backward.argtypes = [vp] * 11 + [ctypes.c_size_t, vp]
-    for f in (lib.gn_workspace_size, lib.gn_forward, lib.gn_backward, lib.dattn_workspace_size, lib.dattn_forward,
+    lib.gn_device_status.argtypes = lib.dattn_device_status.argtypes = [vp, vp]
+    for f in (lib.gn_device_status, lib.dattn_device_status, lib.gn_workspace_size, lib.gn_forward, lib.gn_backward, lib.dattn_workspace_size, lib.dattn_forward,
               lib.dattn_backward):
         f.restype = ctypes.c_int
     lib.dattn_path.restype = ctypes.c_int32
@@ -145,6 +146,19 @@ def da_version() -> int:
 def _check(status: int):
     if status != 0:
         raise DaError(status, load_library().da_last_error().decode(errors="replace"))
+
+
+def waits_gave_up(stream=None) -> bool:
+    """Whether a bounded wait inside a gn_* or dattn_* kernel has run out since
+    the last call (gn_device_status, dattn_device_status): results since then
+    may hold NaN. None does in a sound run. Waits for the stream."""
+    lib, handle = load_library(), _stream_handle(stream)
+    any_of = 0
+    for status in (lib.gn_device_status, lib.dattn_device_status):
+        word = ctypes.c_uint32(0)
+        _check(status(ctypes.byref(word), handle))
+        any_of |= word.value
+    return any_of != 0
 
 
 def _host_i32(t) -> torch.Tensor:
