@@ -36,8 +36,6 @@ struct alignas(16) KeyInfo {
     int pos[kKeys];
     int lo, hi;          // smallest and largest position of those used
     uint32_t all;        // every key is to be used
-    uint32_t valid[2];   // one bit per key
-    uint32_t pad[3];
 };
 
 template <int DP, int VP> struct FwdShared {
@@ -58,7 +56,7 @@ __host__ __device__ inline int bias_span(int reach) { return 2 * (reach + kKeys)
 // for even steps and one for odd. A wait costs some 140 clocks even where it
 // does not wait, so the warp that issues the products has three to a step:
 // `ready` stands for K, V and the step's infos, and s_full for all products
-// issued before, P v of the step before last among them.
+// issued before, P v of two steps before among them.
 struct FwdBars {
     uint64_t q_full, fin;
     uint64_t full[4], ready[4], empty[4];   // of a stage: loaded, cleared of unused keys, free
@@ -161,29 +159,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             constexpr uint32_t iqk = shape(bf16, kKeys, false), ipv = shape(bf16, VP, true);
             const Operand<F::row> dq = along_row<F::row>(sq), dk = along_row<F::row>(sst);
             const Operand<128> dv = over_rows<128>(sst + 2 * F::k, F::vblock);
-            auto scores = [&](int t) {
+            // Scores of map m at step t; past the last, only the notice that
+            // the products before are done.
+            auto scores = [&](int m, int t) {
                 const uint32_t st = (t % NS) * F::stage;
-                if (t < T_) bar_wait_warp(&bars.ready[t % NS], (t / NS) & 1, gave_up);
+                if (t < T_ && m == 0) bar_wait_warp(&bars.ready[t % NS], (t / NS) & 1, gave_up);
                 fence_after();
                 if (issue) {
+                    if (t < T_)
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        if (t < T_)
-#pragma unroll
-                            for (int i = 0; i < DP / 16; ++i)
-                                mma_ss(tS(m, t), dq.at(m * F::q + i * 32), dk.at(st + m * F::k + i * 32), iqk, i > 0);
-                        mma_commit(&bars.s_full[m][t & 1]);
-                    }
+                        for (int i = 0; i < DP / 16; ++i)
+                            mma_ss(tS(m, t), dq.at(m * F::q + i * 32), dk.at(st + m * F::k + i * 32), iqk, i > 0);
+                    mma_commit(&bars.s_full[m][t & 1]);
                 }
                 __syncwarp();
             };
             bar_wait_warp(&bars.q_full, 0, gave_up);
-            scores(0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) scores(i & 1, i >> 1);
             for (int t = 0; t < T_; ++t) {
                 const int s = t % NS;
-                // Their columns held the weights of step t - 1, whose products
-                // were issued before and are formed in this order.
-                scores(t + 1);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     bar_wait_warp(&bars.p_full[m][t & 1], (t >> 1) & 1, gave_up);
@@ -194,7 +189,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                             mma_ts(tO[m], tS(m, t) + i * 8, dv.at(s * F::stage + i * 16 * 128), ipv, t > 0 || i > 0);
                         if (m == 1) mma_commit(&bars.empty[s]);
                     }
-                    __syncwarp();
+                    // Into the columns whose weights the products just issued
+                    // read: products are formed in the order of their issue.
+                    scores(m, t + 2);
                 }
             }
             if (issue) mma_commit(&bars.fin);
@@ -202,30 +199,40 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             __syncwarp();
         }
     } else if (warp == 10) {
+        // A step ahead: whether the lane's two keys are to be used, and where
+        // they are.
+        bool next_use[2];
+        int next_pos[2];
+        const auto fetch = [&](int t) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int j = jb + t * kKeys + c * 32 + lane;
+                const bool in = j < end;
+                const int64_t at = static_cast<int64_t>(b) * a.Lk + j;
+                next_use[c] = in && (!a.mask || a.mask[at]);
+                next_pos[c] = in && a.pos_k ? a.pos_k[at] : j;
+            }
+        };
+        fetch(0);
         for (int t = 0; t < T_; ++t) {
-            const int s = t % NS, j0 = jb + t * kKeys;
+            const int s = t % NS;
             KeyInfo &ki = infos[s];
+            const bool use[2] = {next_use[0], next_use[1]};
+            const int pos[2] = {next_pos[0], next_pos[1]};
+            fetch(t + 1);
             // The stage is free once P v of NS steps ago is done: the softmax
             // warps had by then read its infos, and the products its V.
             bar_wait_warp(&bars.empty[s], ((t / NS) & 1) ^ 1, gave_up);
             int lo = INT32_MAX, hi = INT32_MIN;
-            uint32_t every = 0xffffffffu, stale = 0, valid[2];
+            uint32_t every = 0xffffffffu;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int j = j0 + c * 32 + lane;
-                const bool in = j < end;
-                const int64_t at = static_cast<int64_t>(b) * a.Lk + j;
-                const bool use = in && (!a.mask || a.mask[at]);
-                const int pos = in && a.pos_k ? a.pos_k[at] : j;
-                ki.pos[c * 32 + lane] = pos;
-                ki.bound[c * 32 + lane] = use ? INFINITY : -INFINITY;
-                valid[c] = __ballot_sync(0xffffffffu, use);
-                // Unused keys inside the tensor; past its end TMA wrote zeros.
-                stale |= __ballot_sync(0xffffffffu, !use && j < a.Lk);
-                every &= valid[c];
-                if (use) {
-                    lo = min(lo, pos);
-                    hi = max(hi, pos);
+                ki.pos[c * 32 + lane] = pos[c];
+                ki.bound[c * 32 + lane] = use[c] ? INFINITY : -INFINITY;
+                every &= __ballot_sync(0xffffffffu, use[c]);
+                if (use[c]) {
+                    lo = min(lo, pos[c]);
+                    hi = max(hi, pos[c]);
                 }
             }
             lo = __reduce_min_sync(0xffffffffu, lo);
@@ -234,17 +241,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 ki.lo = lo;
                 ki.hi = hi;
                 ki.all = every == 0xffffffffu;
-                ki.valid[0] = valid[0];
-                ki.valid[1] = valid[1];
             }
             bar_wait_warp(&bars.full[s], (t / NS) & 1, gave_up);
-            if (stale) {  // 0 * NaN is NaN: the rows of V of unused keys become zeros
+            if (every != 0xffffffffu) {
+                // 0 * NaN is NaN: the rows of V of unused keys become zeros
+                // (past the tensor's end TMA wrote them).
                 unsigned char *v = base + 2 * F::q + s * F::stage + 2 * F::k;
-#pragma unroll 1
-                for (int r = lane >> 3; r < kKeys; r += 4)
-                    if (!(valid[r >> 5] >> (r & 31) & 1))
-                        for (int c = 0; c < VP / 64; ++c)
-                            *reinterpret_cast<uint4 *>(v + c * F::vblock + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (!use[c] && jb + t * kKeys + c * 32 + lane < a.Lk)
+#pragma unroll
+                        for (int i = 0; i < VP / 8; ++i)  // neighbouring rows start at different banks
+                            *reinterpret_cast<uint4 *>(v + (i / 8) * F::vblock + (c * 32 + lane) * 128 + (((i + lane) & 7) << 4)) =
+                                make_uint4(0, 0, 0, 0);
                 fence_async();
             }
             __syncwarp();
@@ -324,7 +333,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 sum[0] = mul2(sum[0], sh);
                 sum[1] = mul2(sum[1], sh);
                 if (t > 0) {
-                    // P v of step t - 1 was issued before the scores of step t + 1.
+                    // P v of step t - 1 was issued just before the scores of step t + 1.
                     bar_wait_warp(&bars.s_full[m][(t + 1) & 1], ((t + 1) >> 1) & 1, gave_up);
                     fence_after();
 #pragma unroll 1
