@@ -15,7 +15,7 @@
 // With 64 columns a product reads its operands from shared memory for 48
 // clocks and multiplies for 32, so the operands that stay lie in tensor memory
 // too, as far as it goes: q, g and s_m of the rows in the first kernel, v in
-// the second, whose weights and s_m go through shared memory.
+// the second, and its weights and s_m unless D is above 32 with Dv above 64.
 //
 // Warps: 0-7 compute (two threads per row or key, each with half of a step's
 // 64 columns of both maps), 8 loads by TMA, 9 issues the products, 10 prepares
@@ -65,10 +65,19 @@ template <int ROW> __device__ __forceinline__ void operand_to_tmem(uint32_t addr
     tmem_store(addr, p);
 }
 
-// Zeroes row r of a tile whose rows have `bytes` bytes, by 8 lanes.
-__device__ __forceinline__ void zero_row(unsigned char *tile, int row, int bytes, int lane8)
+// Zeroes row r of a tile of queries or keys, two maps of 2 DP bytes and VP / 64
+// blocks of 128, by one lane; neighbouring rows start at different banks.
+template <int DP, int VP>
+__device__ __forceinline__ void clear_key(unsigned char *tile, int row, int map, int blocks, int block)
 {
-    if (lane8 * 16 < bytes) *reinterpret_cast<uint4 *>(tile + row * bytes + lane8 * 16) = make_uint4(0, 0, 0, 0);
+    constexpr int pieces = DP / 8;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 2 * pieces; ++i)
+        *reinterpret_cast<uint4 *>(tile + (i / pieces) * map + row * DP * 2 + (((i + row) & (pieces - 1)) << 4)) = zero;
+#pragma unroll
+    for (int i = 0; i < VP / 8; ++i)
+        *reinterpret_cast<uint4 *>(tile + blocks + (i / 8) * block + row * kBlock + (((i + row) & 7) << 4)) = zero;
 }
 
 // A row of 32 values times `f`, rounded, `count` of them from column c.
@@ -104,10 +113,10 @@ template <int DP, int VP> struct GradQShared {
 };
 
 struct alignas(16) QKeyInfo {
+    float bound[kStep];  // +infinity, or -infinity for a key that is not to be used
     int pos[kStep];
-    uint32_t valid[2];
-    int lo, hi;
-    uint32_t all, pad[3];
+    int lo, hi;          // smallest and largest position of those used
+    uint32_t all;        // every key is to be used
 };
 
 struct QBars {
@@ -241,27 +250,38 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             __syncwarp();
         }
     } else if (warp == 10) {
-        for (int t = 0; t < T_; ++t) {
-            const int s = t % NS, j0 = t * kStep;
-            QKeyInfo &ki = infos[s];
-            bar_wait_warp(&bars.empty[s], ((t / NS) & 1) ^ 1, gave_up);
-            int lo = INT32_MAX, hi = INT32_MIN;
-            uint32_t every = 0xffffffffu, stale = 0;
+        // A step ahead: whether the lane's two keys are to be used, and where
+        // they are.
+        bool next_use[2];
+        int next_pos[2];
+        const auto fetch = [&](int t) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int j = j0 + c * 32 + lane;
+                const int j = t * kStep + c * 32 + lane;
                 const bool in = j < end;
                 const int64_t at = static_cast<int64_t>(b) * a.Lk + j;
-                const bool use = in && (!a.mask || a.mask[at]);
-                const int pos = in && a.pos_k ? a.pos_k[at] : j;
-                ki.pos[c * 32 + lane] = pos;
-                const uint32_t bits = __ballot_sync(0xffffffffu, use);
-                every &= bits;
-                stale |= __ballot_sync(0xffffffffu, !use && j < a.Lk);
-                if (lane == 0) ki.valid[c] = bits;
-                if (use) {
-                    lo = min(lo, pos);
-                    hi = max(hi, pos);
+                next_use[c] = in && (!a.mask || a.mask[at]);
+                next_pos[c] = in && a.pos_k ? a.pos_k[at] : j;
+            }
+        };
+        fetch(0);
+        for (int t = 0; t < T_; ++t) {
+            const int s = t % NS;
+            QKeyInfo &ki = infos[s];
+            const bool use[2] = {next_use[0], next_use[1]};
+            const int pos[2] = {next_pos[0], next_pos[1]};
+            fetch(t + 1);
+            bar_wait_warp(&bars.empty[s], ((t / NS) & 1) ^ 1, gave_up);
+            int lo = INT32_MAX, hi = INT32_MIN;
+            uint32_t every = 0xffffffffu;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                ki.pos[c * 32 + lane] = pos[c];
+                ki.bound[c * 32 + lane] = use[c] ? INFINITY : -INFINITY;
+                every &= __ballot_sync(0xffffffffu, use[c]);
+                if (use[c]) {
+                    lo = min(lo, pos[c]);
+                    hi = max(hi, pos[c]);
                 }
             }
             lo = __reduce_min_sync(0xffffffffu, lo);
@@ -272,11 +292,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 ki.all = every == 0xffffffffu;
             }
             bar_wait_warp(&bars.full[s], (t / NS) & 1, gave_up);
-            if (stale) {  // unused keys: 0 * NaN in s k would be NaN
+            if (every != 0xffffffffu) {
+                // Unused keys (past the tensor's end TMA wrote zeros): 0 * NaN
+                // in s k and e would be NaN.
                 unsigned char *st = base + F::at_stage + s * F::stage;
-                for (int r = lane >> 3; r < kStep; r += 4)
-                    if (!(ki.valid[r >> 5] >> (r & 31) & 1))
-                        for (int m = 0; m < 2; ++m) zero_row(st + m * F::k, r, F::row, lane & 7);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (!use[c] && t * kStep + c * 32 + lane < a.Lk) clear_key<DP, VP>(st, c * 32 + lane, F::k, 2 * F::k, F::v);
                 fence_async();
             }
             __syncwarp();
@@ -341,9 +363,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             __syncwarp();
             if (lane == 0) bar_arrive(&bars.s_free);
             const int rlo = ki.lo - pos, rhi = ki.hi - pos;
-            const bool even = !live || (ki.all && !none && !(a.causal && rhi > 0) &&
+            const bool even = !live || (!none && !(a.causal && rhi > 0) &&
                                         (a.nb == 0 || rlo >= a.reach || rhi <= -a.reach || rlo == rhi));
-            const bool fast = __all_sync(0xffffffffu, even);
+            const bool fast = __all_sync(0xffffffffu, even) && a.scale_log2 > 0.f;
             float add[2] = {-lse[0], -lse[1]}, mul = a.scale_log2;
             if (fast) {
                 if (a.nb) {
@@ -352,24 +374,36 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     add[1] += bias;
                 }
             } else {
-                const uint32_t valid = ki.valid[half];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const int rel = ki.pos[half * 32 + i] - pos;
                     const float bias = a.nb ? tb[min(max(rel, -a.reach), a.reach)] : 0.f;
-                    const bool on = (valid >> i & 1) && !(a.causal && rel > 0) && !none;
+                    const bool on = !(a.causal && rel > 0) && !none;
                     x[0][i] = on ? fmaf(x[0][i], mul, bias + add[0]) : -INFINITY;
                     x[1][i] = on ? fmaf(x[1][i], mul, bias + add[1]) : -INFINITY;
-                    e[i] = on ? e[i] : 0.f;  // may be NaN where nothing is seen
                 }
                 mul = 1.f;
                 add[0] = add[1] = 0.f;
+            }
+            if (!ki.all) {
+                // The smaller of a NaN and -infinity is -infinity; e is 0 there.
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 bound = *reinterpret_cast<const float4 *>(&ki.bound[half * 32 + i]);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        x[m][i] = fminf(x[m][i], bound.x);
+                        x[m][i + 1] = fminf(x[m][i + 1], bound.y);
+                        x[m][i + 2] = fminf(x[m][i + 2], bound.z);
+                        x[m][i + 3] = fminf(x[m][i + 3], bound.w);
+                    }
+                }
             }
             uint32_t p[2][16];
             const float2 mul_2 = {mul, mul}, a0 = {add[0], add[0]}, a1 = {add[1], add[1]}, nl = {nlam, nlam};
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float2 ei = {e[2 * i], e[2 * i + 1]};
+                const float2 ei = {none ? 0.f : e[2 * i], none ? 0.f : e[2 * i + 1]};
                 float2 w0 = fma2({x[0][2 * i], x[0][2 * i + 1]}, mul_2, a0), w1 = fma2({x[1][2 * i], x[1][2 * i + 1]}, mul_2, a1);
                 w0.x = ex2(w0.x);
                 w0.y = ex2(w0.y);
@@ -438,15 +472,18 @@ template <int DP, int VP> struct GradKVShared {
     // Columns of tensor memory: two score tiles and e, grad_v, grad_k, then v.
     static constexpr int c_v = 3 * kStep + VP + 2 * DP;
     static_assert(c_v + VP / 2 <= 512, "tensor memory");
+    // Where it has room, the weights and s_m too, in place of at_s.
+    static constexpr int c_s = c_v + VP / 2;
+    static constexpr bool s_in_tmem = c_s + 3 * kStep / 2 <= 512;
     static constexpr int table(int nb, int reach) { return nb ? 4 * (2 * reach + 1) + (2 * reach + 4) / 4 * 4 + 4 * 256 * nb : 0; }
 };
 
 // Per-query values of a step, the queries' positions among them.
 struct alignas(16) QueryInfo {
-    float nlse[2][kStep], nd[2][kStep];  // minus the log-sums, minus d_m
+    // Of each two queries: minus the log-sums of map 0, of map 1, minus d_0, d_1.
+    float values[kStep / 2][8];
     int pos[kStep];
     int lo, hi;
-    uint32_t all, pad;
 };
 
 struct KVBars {
@@ -572,12 +609,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (issue) {
                     const uint32_t st = (t % NS) * F::stage;
 #pragma unroll
-                    for (int i = 0; i < kStep / 16; ++i) mma_ss(tV, ds.at(i * 32), dgr.at(st + i * 16 * 128), iv, t > 0 || i > 0);
+                    for (int i = 0; i < kStep / 16; ++i) {
+                        const uint64_t g = dgr.at(st + i * 16 * 128);
+                        if (F::s_in_tmem) mma_ts(tV, tmem + F::c_s + i * 8, g, iv, t > 0 || i > 0);
+                        else mma_ss(tV, ds.at(i * 32), g, iv, t > 0 || i > 0);
+                    }
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int i = 0; i < kStep / 16; ++i)
-                            mma_ss(tK(m), ds.at((1 + m) * F::s + i * 32), dqr.at(st + m * F::q + i * 16 * F::row), ik, t > 0 || i > 0);
+                        for (int i = 0; i < kStep / 16; ++i) {
+                            const uint64_t q = dqr.at(st + m * F::q + i * 16 * F::row);
+                            if (F::s_in_tmem) mma_ts(tK(m), tmem + F::c_s + (1 + m) * (kStep / 2) + i * 8, q, ik, t > 0 || i > 0);
+                            else mma_ss(tK(m), ds.at((1 + m) * F::s + i * 32), q, ik, t > 0 || i > 0);
+                        }
                     mma_commit(&bars.empty[t % NS]);
                 }
                 __syncwarp();
@@ -588,14 +632,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
     } else if (warp == 10) {
         if (T_ > 0) {
-            // Keys that are not to be used become zeros, once.
+            // Keys that are not to be used become zeros, once (past the
+            // tensor's end TMA wrote them).
             bar_wait_warp(&bars.kv_full, 0, gave_up);
             bool any = false;
-            for (int r = lane >> 3; r < kOwn; r += 4) {
-                const int j = j0 + r;
+#pragma unroll
+            for (int c = 0; c < kOwn / 32; ++c) {
+                const int r = c * 32 + lane, j = j0 + r;
                 if (j < a.Lk && (j >= len || (a.mask && !a.mask[static_cast<int64_t>(b) * a.Lk + j]))) {
-                    for (int m = 0; m < 2; ++m) zero_row(base + m * F::k, r, F::row, lane & 7);
-                    for (int c = 0; c < VP / 64; ++c) zero_row(base + F::at_v + c * F::v, r, kBlock, lane & 7);
+                    clear_key<DP, VP>(base, r, F::k, F::at_v, F::v);
                     any = true;
                 }
             }
@@ -603,48 +648,72 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             __syncwarp();
             if (lane == 0) bar_arrive(&bars.kv_ready);
         }
-        for (int t = 0; t < T_; ++t) {
-            const int s = t % NS, g = t / per, h = n * a.G + g, l0 = first + (t % per) * kStep;
-            QueryInfo &qi = infos[s];
-            bar_wait_warp(&bars.empty[s], ((t / NS) & 1) ^ 1, gave_up);
-            int lo = INT32_MAX, hi = INT32_MIN;
-            uint32_t none[2];
-            bool every = true;
+        // A step ahead: the log-sums, d_m and positions of the lane's two queries.
+        float next_lse[2][2], next_d[2][2];
+        int next_pos[2];
+        const auto fetch = [&](int t) {
+            const int g = t / max(per, 1), h = n * a.G + g, l0 = first + (t - g * per) * kStep;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int i = c * 32 + lane, l = l0 + i;
-                const bool in = l < a.Lq;
-                float lse = INFINITY;
+                const int l = l0 + c * 32 + lane;
+                const bool in = t < T_ && l < a.Lq;
+#pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    const float x = in ? a.lse[((static_cast<int64_t>(b) * a.H + h) * 2 + m) * a.Lq + l] : INFINITY;
-                    qi.nlse[m][i] = -x;
-                    qi.nd[m][i] = in ? -a.delta[((static_cast<int64_t>(b) * a.Hkv + n) * 2 + m) * a.rows + static_cast<int64_t>(l) * a.G + g] : 0.f;
-                    lse = m == 0 ? x : lse;
+                    next_lse[c][m] = in ? a.lse[((static_cast<int64_t>(b) * a.H + h) * 2 + m) * a.Lq + l] : INFINITY;
+                    next_d[c][m] = in ? a.delta[((static_cast<int64_t>(b) * a.Hkv + n) * 2 + m) * a.rows + static_cast<int64_t>(l) * a.G + g] : 0.f;
                 }
-                const int pos = !in ? 0 : a.pos_q ? a.pos_q[static_cast<int64_t>(b) * a.Lq + l] : len - a.Lq + l;
-                qi.pos[i] = pos;
-                none[c] = __ballot_sync(0xffffffffu, in && lse == INFINITY);
+                next_pos[c] = !in ? 0 : a.pos_q ? a.pos_q[static_cast<int64_t>(b) * a.Lq + l] : len - a.Lq + l;
+            }
+        };
+        fetch(0);
+        for (int t = 0; t < T_; ++t) {
+            const int s = t % NS, l0 = first + (t % per) * kStep;
+            QueryInfo &qi = infos[s];
+            float lse[2][2], d[2][2];
+            int pos[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    lse[c][m] = next_lse[c][m];
+                    d[c][m] = next_d[c][m];
+                }
+                pos[c] = next_pos[c];
+            }
+            fetch(t + 1);
+            bar_wait_warp(&bars.empty[s], ((t / NS) & 1) ^ 1, gave_up);
+            int lo = INT32_MAX, hi = INT32_MIN;
+            bool idle[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int i = c * 32 + lane;
+                const bool in = l0 + i < a.Lq;
+                // Pairs of queries: {map 0 of both, map 1 of both}.
+                float *to = &qi.values[i >> 1][i & 1];
+                to[0] = -lse[c][0];
+                to[2] = -lse[c][1];
+                to[4] = -d[c][0];
+                to[6] = -d[c][1];
+                qi.pos[i] = pos[c];
+                idle[c] = in && lse[c][0] == INFINITY;
                 if (in) {
-                    lo = min(lo, pos);
-                    hi = max(hi, pos);
+                    lo = min(lo, pos[c]);
+                    hi = max(hi, pos[c]);
                 }
             }
             lo = __reduce_min_sync(0xffffffffu, lo);
             hi = __reduce_max_sync(0xffffffffu, hi);
-            every = (none[0] | none[1]) == 0;
             if (lane == 0) {
                 qi.lo = lo;
                 qi.hi = hi;
-                qi.all = every;
             }
             bar_wait_warp(&bars.full[s], (t / NS) & 1, gave_up);
-            if (!every) {  // queries that see nothing take no part, whatever q and g hold
+            // Queries that see nothing take no part, whatever q and g hold.
+            if (__any_sync(0xffffffffu, idle[0] || idle[1])) {
                 unsigned char *st = base + F::at_stage + s * F::stage;
-                for (int r = lane >> 3; r < kStep; r += 4)
-                    if (none[r >> 5] >> (r & 31) & 1) {
-                        for (int m = 0; m < 2; ++m) zero_row(st + m * F::q, r, F::row, lane & 7);
-                        for (int c = 0; c < VP / 64; ++c) zero_row(st + 2 * F::q + c * F::g, r, kBlock, lane & 7);
-                    }
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (idle[c]) clear_key<DP, VP>(st, c * 32 + lane, F::q, 2 * F::q, F::g);
                 fence_async();
             }
             __syncwarp();
@@ -716,10 +785,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 uint32_t pw[16], p0[16], p1[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 l0 = *reinterpret_cast<const float2 *>(&qi.nlse[0][half * 32 + 2 * i]);
-                    const float2 l1 = *reinterpret_cast<const float2 *>(&qi.nlse[1][half * 32 + 2 * i]);
-                    const float2 d0 = *reinterpret_cast<const float2 *>(&qi.nd[0][half * 32 + 2 * i]);
-                    const float2 d1 = *reinterpret_cast<const float2 *>(&qi.nd[1][half * 32 + 2 * i]);
+                    const float4 lse = *reinterpret_cast<const float4 *>(&qi.values[half * 16 + i][0]);
+                    const float4 nd = *reinterpret_cast<const float4 *>(&qi.values[half * 16 + i][4]);
+                    const float2 l0 = {lse.x, lse.y}, l1 = {lse.z, lse.w}, d0 = {nd.x, nd.y}, d1 = {nd.z, nd.w};
                     const float2 ei = {e[2 * i], e[2 * i + 1]};
                     float2 w0 = fma2({x[0][2 * i], x[0][2 * i + 1]}, mul_2, add2(add_2, l0));
                     float2 w1 = fma2({x[1][2 * i], x[1][2 * i + 1]}, mul_2, add2(add_2, l1));
@@ -758,10 +826,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     }
                 }
                 if (t > 0) bar_wait_warp(&bars.empty[(t - 1) % NS], ((t - 1) / NS) & 1, gave_up);  // those of step t - 1 were used
-                store_operand(base + F::at_s, rl, half, pw);
-                store_operand(base + F::at_s + F::s, rl, half, p0);
-                store_operand(base + F::at_s + 2 * F::s, rl, half, p1);
-                fence_async();
+                if (F::s_in_tmem) {
+                    const uint32_t to = tmem + F::c_s + half * 16 + lanes;
+                    tmem_store(to, pw);
+                    tmem_store(to + kStep / 2, p0);
+                    tmem_store(to + kStep, p1);
+                    tmem_store_wait();
+                    fence_before();
+                } else {
+                    store_operand(base + F::at_s, rl, half, pw);
+                    store_operand(base + F::at_s + F::s, rl, half, p0);
+                    store_operand(base + F::at_s + 2 * F::s, rl, half, p1);
+                    fence_async();
+                }
                 __syncwarp();
                 if (lane == 0) bar_arrive(&bars.ds_full);
             }
