@@ -14,8 +14,8 @@
 // grad_v) or two (grad_q twice) back. All products sum in tensor memory.
 // With 64 columns a product reads its operands from shared memory for 48
 // clocks and multiplies for 32, so the operands that stay lie in tensor memory
-// too, as far as it goes: q, g and s_m of the rows in the first kernel, v in
-// the second, and its weights and s_m unless D is above 32 with Dv above 64.
+// too, as far as it goes: q, g and s_m of the rows in the first kernel, s_m
+// in the second, and v and the weights unless Dv is above 64.
 //
 // Warps: 0-7 compute (two threads per row or key, each with half of a step's
 // 64 columns of both maps), 8 loads by TMA, 9 issues the products, 10 prepares
@@ -356,23 +356,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             bar_wait_warp(&bars.s_full, t & 1, gave_up);
             fence_after();
             float e[32], x[2][32];
-            tmem_load(tS(2) + lanes + half * 32, e);
-            tmem_load(tS(0) + lanes + half * 32, x[0]);
-            tmem_load(tS(1) + lanes + half * 32, x[1]);
+            tmem_load3(tS(2) + lanes + half * 32, tS(0) + lanes + half * 32, tS(1) + lanes + half * 32, e, x[0], x[1]);
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(&bars.s_free);
             const int rlo = ki.lo - pos, rhi = ki.hi - pos;
+            const bool all = ki.all;
             const bool even = !live || (!none && !(a.causal && rhi > 0) &&
                                         (a.nb == 0 || rlo >= a.reach || rhi <= -a.reach || rlo == rhi));
             const bool fast = __all_sync(0xffffffffu, even) && a.scale_log2 > 0.f;
+            const float bias_all = a.nb ? tb[min(max(rlo, -a.reach), a.reach)] : 0.f;
             float add[2] = {-lse[0], -lse[1]}, mul = a.scale_log2;
             if (fast) {
-                if (a.nb) {
-                    const float bias = tb[min(max(rlo, -a.reach), a.reach)];
-                    add[0] += bias;
-                    add[1] += bias;
-                }
+                add[0] += bias_all;
+                add[1] += bias_all;
             } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
@@ -385,7 +382,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 mul = 1.f;
                 add[0] = add[1] = 0.f;
             }
-            if (!ki.all) {
+            if (!all) {
                 // The smaller of a NaN and -infinity is -infinity; e is 0 there.
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
@@ -466,21 +463,20 @@ template <int DP, int VP> struct GradKVShared {
     static constexpr int q = kStep * row, g = kStep * kBlock;
     static constexpr int stage = 2 * q + (VP / 64) * g;
     static constexpr int stages = 3;
-    static constexpr int s = kOwn * kBlock;                       // P_0 - lam P_1 and s_m as operands
-    static constexpr int at_stage = 2 * k, at_s = at_stage + stages * stage, bytes = at_s + 3 * s;
-    static constexpr int at_v = at_s;                             // until v is in tensor memory
-    // Columns of tensor memory: two score tiles and e, grad_v, grad_k, then v.
-    static constexpr int c_v = 3 * kStep + VP + 2 * DP;
-    static_assert(c_v + VP / 2 <= 512, "tensor memory");
-    // Where it has room, the weights and s_m too, in place of at_s.
-    static constexpr int c_s = c_v + VP / 2;
-    static constexpr bool s_in_tmem = c_s + 3 * kStep / 2 <= 512;
+    static constexpr int s = kOwn * kBlock;                       // P_0 - lam P_1 as an operand
+    // Columns of tensor memory: two score tiles and e, grad_v, grad_k, s_m,
+    // and with room for them (Dv of at most 64) v and the weights.
+    static constexpr int c_s = 3 * kStep + VP + 2 * DP, c_v = c_s + kStep, c_w = c_v + VP / 2;
+    static constexpr bool roomy = c_w + kStep / 2 <= 512;
+    static_assert(c_v <= 512, "tensor memory");
+    static constexpr int at_v = 2 * k, at_stage = at_v + (VP / 64) * v, at_w = at_stage + stages * stage,
+                         bytes = at_w + (roomy ? 0 : s);
     static constexpr int table(int nb, int reach) { return nb ? 4 * (2 * reach + 1) + (2 * reach + 4) / 4 * 4 + 4 * 256 * nb : 0; }
 };
 
 // Per-query values of a step, the queries' positions among them.
 struct alignas(16) QueryInfo {
-    // Of each two queries: minus the log-sums of map 0, of map 1, minus d_0, d_1.
+    // Of each two queries: minus the log-sums of map 0, of map 1, -d_0, lam d_1.
     float values[kStep / 2][8];
     int pos[kStep];
     int lo, hi;
@@ -581,7 +577,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const Operand<F::row> dk = along_row<F::row>(sbase), dq = along_row<F::row>(sbase + F::at_stage),
                                   dqr = over_rows<F::row>(sbase + F::at_stage, F::q);
             const Operand<128> dg = along_row<128>(sbase + F::at_stage + 2 * F::q),
-                               dgr = over_rows<128>(sbase + F::at_stage + 2 * F::q, F::g), ds = along_row<128>(sbase + F::at_s);
+                               dgr = over_rows<128>(sbase + F::at_stage + 2 * F::q, F::g), dw = along_row<128>(sbase + F::at_w), dv = along_row<128>(sbase + F::at_v);
             auto scores = [&](int t) {
                 const uint32_t st = (t % NS) * F::stage;
                 bar_wait_warp(&bars.ready[t % NS], (t / NS) & 1, gave_up);
@@ -594,8 +590,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         for (int i = 0; i < DP / 16; ++i)
                             mma_ss(tS(m), dk.at(m * F::k + i * 32), dq.at(st + m * F::q + i * 32), is, i > 0);
 #pragma unroll
-                    for (int i = 0; i < VP / 16; ++i)
-                        mma_ts(tS(2), tmem + F::c_v + i * 8, dg.at(st + (i / 4) * F::g + (i % 4) * 32), is, i > 0);
+                    for (int i = 0; i < VP / 16; ++i) {
+                        const uint64_t g = dg.at(st + (i / 4) * F::g + (i % 4) * 32);
+                        if (F::roomy) mma_ts(tS(2), tmem + F::c_v + i * 8, g, is, i > 0);
+                        else mma_ss(tS(2), dv.at((i / 4) * F::v + (i % 4) * 32), g, is, i > 0);
+                    }
                     mma_commit(&bars.s_full);
                 }
                 __syncwarp();
@@ -611,17 +610,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kStep / 16; ++i) {
                         const uint64_t g = dgr.at(st + i * 16 * 128);
-                        if (F::s_in_tmem) mma_ts(tV, tmem + F::c_s + i * 8, g, iv, t > 0 || i > 0);
-                        else mma_ss(tV, ds.at(i * 32), g, iv, t > 0 || i > 0);
+                        if (F::roomy) mma_ts(tV, tmem + F::c_w + i * 8, g, iv, t > 0 || i > 0);
+                        else mma_ss(tV, dw.at(i * 32), g, iv, t > 0 || i > 0);
                     }
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int i = 0; i < kStep / 16; ++i) {
-                            const uint64_t q = dqr.at(st + m * F::q + i * 16 * F::row);
-                            if (F::s_in_tmem) mma_ts(tK(m), tmem + F::c_s + (1 + m) * (kStep / 2) + i * 8, q, ik, t > 0 || i > 0);
-                            else mma_ss(tK(m), ds.at((1 + m) * F::s + i * 32), q, ik, t > 0 || i > 0);
-                        }
+                        for (int i = 0; i < kStep / 16; ++i)
+                            mma_ts(tK(m), tmem + F::c_s + m * (kStep / 2) + i * 8, dqr.at(st + m * F::q + i * 16 * F::row), ik, t > 0 || i > 0);
                     mma_commit(&bars.empty[t % NS]);
                 }
                 __syncwarp();
@@ -668,6 +664,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         fetch(0);
         for (int t = 0; t < T_; ++t) {
             const int s = t % NS, l0 = first + (t % per) * kStep;
+            const float lam = a.lam[n * a.G + t / per];
             QueryInfo &qi = infos[s];
             float lse[2][2], d[2][2];
             int pos[2];
@@ -693,7 +690,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 to[0] = -lse[c][0];
                 to[2] = -lse[c][1];
                 to[4] = -d[c][0];
-                to[6] = -d[c][1];
+                to[6] = lam * d[c][1];
                 qi.pos[i] = pos[c];
                 idle[c] = in && lse[c][0] == INFINITY;
                 if (in) {
@@ -727,14 +724,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const bool use = j < len && (!a.mask || a.mask[kat]);
         const int pos = use && a.pos_k ? a.pos_k[kat] : j;
         float *mine = sums + tid;
-        if (T_ > 0) {  // v to tensor memory: its place is then that of the weights
+        if (T_ > 0) {
             bar_wait_warp(&bars.kv_full, 0, gave_up);
             bar_wait_warp(&bars.kv_ready, 0, gave_up);
-            for (int c = 0; c < VP / 64; ++c)
-                operand_to_tmem<128>(tmem + F::c_v + c * 32 + half * 16 + lanes, base + F::at_v + c * F::v, rl, half);
-            tmem_store_wait();
-            fence_before();
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (F::roomy) {
+                for (int c = 0; c < VP / 64; ++c)
+                    operand_to_tmem<128>(tmem + F::c_v + c * 32 + half * 16 + lanes, base + F::at_v + c * F::v, rl, half);
+                tmem_store_wait();
+                fence_before();
+            }
+            __syncwarp();
             if (lane == 0) bar_arrive(&bars.v_ready);
         }
         for (int g = 0; g < a.G; ++g) {
@@ -751,9 +750,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 bar_wait_warp(&bars.s_full, t & 1, gave_up);
                 fence_after();
                 float e[32], x[2][32];
-                tmem_load(tS(2) + lanes + half * 32, e);
-                tmem_load(tS(0) + lanes + half * 32, x[0]);
-                tmem_load(tS(1) + lanes + half * 32, x[1]);
+                tmem_load3(tS(2) + lanes + half * 32, tS(0) + lanes + half * 32, tS(1) + lanes + half * 32, e, x[0], x[1]);
                 fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(&bars.s_free);
@@ -763,13 +760,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const bool fast = __all_sync(0xffffffffu, even);
                 float add = 0.f, mul = a.scale_log2;
                 int where = 0;
-                if (fast) {
-                    if (a.nb) {
-                        where = min(max(rlo, -a.reach), a.reach) + a.reach;
-                        add = table[where];
-                    }
-                    if (!use) add = -INFINITY;
-                } else {
+                if (a.nb) {
+                    where = min(max(rlo, -a.reach), a.reach) + a.reach;
+                    add = table[where];
+                    where = bucket[where] * 256;
+                }
+                if (!use) add = -INFINITY;
+                if (!fast) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const int rel = pos - qi.pos[half * 32 + i];
@@ -779,6 +776,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         x[1][i] = on ? fmaf(x[1][i], mul, bias) : -INFINITY;
                     }
                     mul = 1.f;
+                    add = 0.f;
                 }
                 const float2 mul_2 = {mul, mul}, add_2 = {add, add}, nl = {nlam, nlam};
                 float2 total = {0.f, 0.f};
@@ -795,8 +793,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     w0.y = ex2(w0.y);
                     w1.x = ex2(w1.x);
                     w1.y = ex2(w1.y);
-                    w1 = mul2(w1, nl);
-                    const float2 s0 = mul2(w0, add2(ei, d0)), s1 = mul2(w1, add2(ei, d1)), w = add2(w0, w1);
+                    const float2 s0 = mul2(w0, add2(ei, d0)), s1 = mul2(w1, fma2(ei, nl, d1)), w = fma2(w1, nl, w0);
                     const float2 both = add2(s0, s1);
                     total = add2(total, both);
                     x[0][2 * i] = both.x;  // kept for the buckets
@@ -805,42 +802,36 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     p0[i] = pack2<T>(s0.x, s0.y);
                     p1[i] = pack2<T>(s1.x, s1.y);
                 }
-                if (a.nb) {
-                    if (fast) {
-                        mine[bucket[where] * 256] += total.x + total.y;
-                    } else {
-                        // Runs of one bucket are summed before they are added.
-                        int last = bucket[min(max(pos - qi.pos[half * 32], -a.reach), a.reach) + a.reach];
-                        float run = 0.f;
+                if (a.nb && !fast) {
+                    // Runs of one bucket are summed before they are added.
+                    int last = bucket[min(max(pos - qi.pos[half * 32], -a.reach), a.reach) + a.reach];
+                    float run = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int k = bucket[min(max(pos - qi.pos[half * 32 + i], -a.reach), a.reach) + a.reach];
-                            if (k != last) {
-                                mine[last * 256] += run;
-                                run = 0.f;
-                                last = k;
-                            }
-                            run += x[0][i];
+                    for (int i = 0; i < 32; ++i) {
+                        const int k = bucket[min(max(pos - qi.pos[half * 32 + i], -a.reach), a.reach) + a.reach];
+                        if (k != last) {
+                            mine[last * 256] += run;
+                            run = 0.f;
+                            last = k;
                         }
-                        mine[last * 256] += run;
+                        run += x[0][i];
                     }
+                    mine[last * 256] += run;
                 }
                 if (t > 0) bar_wait_warp(&bars.empty[(t - 1) % NS], ((t - 1) / NS) & 1, gave_up);  // those of step t - 1 were used
-                if (F::s_in_tmem) {
-                    const uint32_t to = tmem + F::c_s + half * 16 + lanes;
-                    tmem_store(to, pw);
-                    tmem_store(to + kStep / 2, p0);
-                    tmem_store(to + kStep, p1);
-                    tmem_store_wait();
-                    fence_before();
+                if (F::roomy) {
+                    tmem_store(tmem + F::c_w + half * 16 + lanes, pw);
                 } else {
-                    store_operand(base + F::at_s, rl, half, pw);
-                    store_operand(base + F::at_s + F::s, rl, half, p0);
-                    store_operand(base + F::at_s + 2 * F::s, rl, half, p1);
+                    store_operand(base + F::at_w, rl, half, pw);
                     fence_async();
                 }
+                tmem_store(tmem + F::c_s + half * 16 + lanes, p0);
+                tmem_store(tmem + F::c_s + kStep / 2 + half * 16 + lanes, p1);
+                tmem_store_wait();
+                fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(&bars.ds_full);
+                if (a.nb && fast) mine[where] += total.x + total.y;
             }
             if (a.nb) {
                 asm volatile("bar.sync 1, 256;" ::: "memory");
