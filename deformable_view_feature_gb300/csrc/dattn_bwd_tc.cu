@@ -398,20 +398,65 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             uint32_t p[2][16];
             const float2 mul_2 = {mul, mul}, a0 = {add[0], add[0]}, a1 = {add[1], add[1]}, nl = {nlam, nlam};
+            if (T_ == 1) {
+                // All of the row's keys are here: weights that sum to 1 and d_m
+                // from them. With few keys the rounding of the outputs would
+                // weigh most, and a row of one key has to give exactly 0.
+                float y[2] = {0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float2 ei = {none ? 0.f : e[2 * i], none ? 0.f : e[2 * i + 1]};
-                float2 w0 = fma2({x[0][2 * i], x[0][2 * i + 1]}, mul_2, a0), w1 = fma2({x[1][2 * i], x[1][2 * i + 1]}, mul_2, a1);
-                w0.x = ex2(w0.x);
-                w0.y = ex2(w0.y);
-                w1.x = ex2(w1.x);
-                w1.y = ex2(w1.y);
-                const float2 s0 = mul2(w0, add2(ei, nd[0])), s1 = mul2(w1, add2(ei, nd[1]));
-                rest[0] = add2(rest[0], s0);
-                rest[1] = add2(rest[1], s1);
-                const float2 s1l = mul2(s1, nl);
-                p[0][i] = pack2<T>(s0.x, s0.y);
-                p[1][i] = pack2<T>(s1l.x, s1l.y);
+                for (int m = 0; m < 2; ++m) {
+                    float z = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        x[m][i] = none ? 0.f : ex2(fmaf(x[m][i], mul, add[m]));
+                        z += x[m][i];
+                    }
+                    part[m][half][rl] = z;
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const float z = part[m][0][rl] + part[m][1][rl];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        x[m][i] = none ? 0.f : x[m][i] / z;
+                        e[i] = none ? 0.f : e[i];
+                        y[m] = fmaf(x[m][i], e[i], y[m]);
+                    }
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                part[0][half][rl] = y[0];
+                part[1][half][rl] = y[1];
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                for (int m = 0; m < 2; ++m) d[m] = part[m][0][rl] + part[m][1][rl];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float s[2][2];
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) s[m][k] = x[m][2 * i + k] * (e[2 * i + k] - d[m]);
+                    rest[0] = add2(rest[0], {s[0][0], s[0][1]});
+                    rest[1] = add2(rest[1], {s[1][0], s[1][1]});
+                    p[0][i] = pack2<T>(s[0][0], s[0][1]);
+                    p[1][i] = pack2<T>(nlam * s[1][0], nlam * s[1][1]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 ei = {none ? 0.f : e[2 * i], none ? 0.f : e[2 * i + 1]};
+                    float2 w0 = fma2({x[0][2 * i], x[0][2 * i + 1]}, mul_2, a0), w1 = fma2({x[1][2 * i], x[1][2 * i + 1]}, mul_2, a1);
+                    w0.x = ex2(w0.x);
+                    w0.y = ex2(w0.y);
+                    w1.x = ex2(w1.x);
+                    w1.y = ex2(w1.y);
+                    const float2 s0 = mul2(w0, add2(ei, nd[0])), s1 = mul2(w1, add2(ei, nd[1]));
+                    rest[0] = add2(rest[0], s0);
+                    rest[1] = add2(rest[1], s1);
+                    const float2 s1l = mul2(s1, nl);
+                    p[0][i] = pack2<T>(s0.x, s0.y);
+                    p[1][i] = pack2<T>(s1l.x, s1l.y);
+                }
             }
             if (t > 0) bar_wait_warp(&bars.empty[(t - 1) % NS], ((t - 1) / NS) & 1, gave_up);  // s_m of step t - 1 was used
             tmem_store(tmem + F::c_s + half * 16 + lanes, p[0]);
@@ -476,7 +521,7 @@ template <int DP, int VP> struct GradKVShared {
 
 // Per-query values of a step, the queries' positions among them.
 struct alignas(16) QueryInfo {
-    // Of each two queries: minus the log-sums of map 0, of map 1, -d_0, lam d_1.
+    // Of each two queries: minus the log-sums of map 0, of map 1, minus d_0, d_1.
     float values[kStep / 2][8];
     int pos[kStep];
     int lo, hi;
@@ -664,7 +709,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         fetch(0);
         for (int t = 0; t < T_; ++t) {
             const int s = t % NS, l0 = first + (t % per) * kStep;
-            const float lam = a.lam[n * a.G + t / per];
             QueryInfo &qi = infos[s];
             float lse[2][2], d[2][2];
             int pos[2];
@@ -690,7 +734,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 to[0] = -lse[c][0];
                 to[2] = -lse[c][1];
                 to[4] = -d[c][0];
-                to[6] = lam * d[c][1];
+                to[6] = -d[c][1];
                 qi.pos[i] = pos[c];
                 idle[c] = in && lse[c][0] == INFINITY;
                 if (in) {
@@ -793,7 +837,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     w0.y = ex2(w0.y);
                     w1.x = ex2(w1.x);
                     w1.y = ex2(w1.y);
-                    const float2 s0 = mul2(w0, add2(ei, d0)), s1 = mul2(w1, fma2(ei, nl, d1)), w = fma2(w1, nl, w0);
+                    const float2 s0 = mul2(w0, add2(ei, d0)), s1 = mul2(mul2(w1, nl), add2(ei, d1)), w = fma2(w1, nl, w0);
                     const float2 both = add2(s0, s1);
                     total = add2(total, both);
                     x[0][2 * i] = both.x;  // kept for the buckets

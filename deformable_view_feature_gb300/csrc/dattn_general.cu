@@ -428,6 +428,7 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_co
     if (a.causal && !a.pos_q && !a.pos_k)
         end = min(end, len - a.Lq + static_cast<int>(a.div_G.div(min(r0 + QT, a.rows) - 1)) + 1);
     const int first = split * a.keys_per_split;
+    const bool one = end <= KT;  // then within the first split
     end = min(end, first + a.keys_per_split);
     for (int j0 = first; j0 < end; j0 += KT) {
         __syncthreads();
@@ -445,14 +446,34 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_co
             scores<M, N, DP>(sq + m * QT * (DP + 4), sk + m * KT * (DP + 4), ty, tx, t);
 #pragma unroll
             for (int i = 0; i < M; ++i) {
-                float r = 0.f;
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
                     const int rel = kpos[tx + 16 * j] - ri[i].pos;
                     float x = t[i][j] * a.scale_log2 - lse[m][i];
                     if (a.nb) x += bt.table[bucket_of(a, bt, rel) * a.G + ri[i].g];
                     const bool on = kseen[tx + 16 * j] && !(a.causal && rel > 0) && lse[m][i] != INFINITY;
-                    const float s = on ? ex2(x) * (e[i][j] - dl[m][i]) : 0.f;
+                    t[i][j] = on ? ex2(x) : 0.f;
+                }
+                if (one) {
+                    // All of the row's keys are here: weights that sum to 1 and
+                    // d_m from them, so that a row of one key gives exactly 0.
+                    // (The whole warp takes this way: its rows' sums are
+                    // formed by shuffles.)
+                    float z = 0.f, d = 0.f;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) z += t[i][j];
+                    z = row_sum(z);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        t[i][j] = z == 0.f ? 0.f : t[i][j] / z;
+                        d += t[i][j] != 0.f ? t[i][j] * e[i][j] : 0.f;
+                    }
+                    dl[m][i] = row_sum(d);
+                }
+                float r = 0.f;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const float s = t[i][j] != 0.f ? t[i][j] * (e[i][j] - dl[m][i]) : 0.f;
                     r += s;
                     ss[(m * QT + ty + 16 * i) * (KT + 4) + tx + 16 * j] = m ? -lam[i] * s : s;
                 }

@@ -272,6 +272,29 @@ def test_masks_that_leave_rows_empty(kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_rows_of_one_key_give_exactly_no_score_gradient(kind):
+    # A softmax over one key is 1 whatever its score.
+    for Lk, lengths in ((1, None), (40, [1, 1]), (200, [1, 1])):
+        t, opt, grad = _case(B=2, Lq=70, Lk=Lk, H=4, Hk=2, kind=kind, buckets=8, lengths=lengths)
+        got = _all(t, opt, grad)
+        assert not got["grad_q"].any() and not got["grad_k"].any() and not got["grad_table"].any()
+        assert bool(got["grad_v"].any()) and bool(got["grad_lam"].all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_two_keys_keep_their_digits(kind):
+    # grad_q of two keys is their scores' difference: no more than 1.7 times
+    # the two roundings (of s_m and of the result) may be off, in 2-norm.
+    t, opt, grad = _case(B=4, Lq=64, Lk=2, H=4, Hk=4, kind=kind)
+    val, _ = _reference(t, opt, grad)
+    got = _all(t, opt, grad)
+    for n in ("grad_q", "grad_k"):
+        assert float((got[n].double() - val[n]).norm() / val[n].norm()) < 1.7 * torch.finfo(DT[kind]).eps / 2
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["f32", "f16"])
 def test_infinite_bias(kind):
     # A bucket of -infinity hides its keys; a row with no other keys gives 0.
