@@ -17,6 +17,12 @@
 // too, as far as it goes: q, g and s_m of the rows in the first kernel, s_m
 // in the second, and v and the weights unless Dv is above 64.
 //
+// At 2 x 8 heads of 8,192 tokens, causal, D = 64, Dv = 128: 478 us for the
+// first kernel and 743 for the second, 1,720 and 2,900 clocks a step for 768
+// and 1,024 of multiplication. All compute warps work on one step, so its
+// phases (scores to registers, exponentials, operands back) do not overlap each
+// other, only the products; tensor memory has no room for a second step.
+//
 // Warps: 0-7 compute (two threads per row or key, each with half of a step's
 // 64 columns of both maps), 8 loads by TMA, 9 issues the products, 10 prepares
 // positions, masks and per-query values. The scores of step t+1 are formed as

@@ -37,6 +37,8 @@
  * the weights P, and s_m in the backward pass, are rounded to the inputs'
  * type as operands of the second products, as the tensor cores require.
  * grad_lam and grad_table are formed from the unrounded values.
+ * In fp16 an s_m past 65504 becomes infinite and one below 2^-24 zero, as any
+ * such value of that type: gradients are to be scaled as fp16 training does.
  * Sums are taken in a fixed order: results do not vary from run to run.
  * Positions lie in (-2^30, 2^30). Device-side indices are bounded in every
  * build: key_lengths is clamped to [0, Lk] and bucket_map to the table.
