@@ -551,8 +551,13 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_kv_kernel(const __grid_c
     int *rpos = kseen + KT, *rg = rpos + RT;
     float *rlse = reinterpret_cast<float *>(rg + RT), *rdl = rlse + 2 * RT, *rlam = rdl + 2 * RT;
     const BiasTable bt{sm + F::floats, reinterpret_cast<uint16_t *>(sm + F::floats + a.nb * a.G)};
-    // Each warp's sums per bucket and head.
-    float *sums = sm + F::floats + bias_floats(a.nb, a.G, a.reach) + (threadIdx.x >> 5) * a.nb * a.G;
+    // Each thread's sums per bucket and head, or each warp's where shared memory
+    // does not hold 256 of them. (Warps' sums take a walk over the distinct
+    // buckets of every 32 scores: 160 us against 111 for the backward pass at
+    // 333 tokens, 32 buckets, 3 heads to a key head.)
+    const bool own_sums = a.own_sums;
+    float *all_sums = sm + F::floats + bias_floats(a.nb, a.G, a.reach);
+    float *sums = all_sums + (own_sums ? threadIdx.x : (threadIdx.x >> 5) * a.nb * a.G);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, lane = threadIdx.x & 31;
     const int tile = blockIdx.x / a.row_splits, split = blockIdx.x - tile * a.row_splits;
     const int n = blockIdx.y, b = blockIdx.z, j0 = tile * KT;
@@ -560,7 +565,10 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_kv_kernel(const __grid_c
     const int64_t ob = static_cast<int64_t>(b) * a.Lq * a.H * a.Dv;
 
     load_bias(a, n, bt);
-    for (int i = lane; i < a.nb * a.G; i += 32) sums[i] = 0.f;
+    if (own_sums)
+        for (int i = 0; i < a.nb * a.G; ++i) sums[i * kThreadsG] = 0.f;
+    else
+        for (int i = lane; i < a.nb * a.G; i += 32) sums[i] = 0.f;
     load_key_info(a, b, len, j0, KT, kpos, kseen);
     __syncthreads();
     for (int m = 0; m < 2; ++m)
@@ -636,7 +644,15 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_kv_kernel(const __grid_c
 #pragma unroll
         for (int m = 0; m < 2; ++m)
             products<M, RT, DP, F::ND>(ss + (1 + m) * KT * (RT + 4), sq + m * RT * (DP + 4), ty, tx, gk[m]);
-        if (a.nb) {
+        if (a.nb && own_sums) {
+#pragma unroll
+            for (int i = 0; i < M; ++i)
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int c = tx + 16 * j;
+                    sums[(bucket_of(a, bt, kpos[ty + 16 * i] - rpos[c]) * a.G + rg[c]) * kThreadsG] += both[i][j];
+                }
+        } else if (a.nb) {
             // The warp's sums per bucket, bucket by bucket in the order of
             // its lanes: no atomics, so the order is the same in every run.
 #pragma unroll
@@ -687,12 +703,22 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_kv_kernel(const __grid_c
     }
     if (a.nb) {
         __syncthreads();
-        float *all = sm + F::floats + bias_floats(a.nb, a.G, a.reach);
         float *out = a.part_table + ((static_cast<int64_t>(b) * a.Hkv + n) * a.table_ctas + blockIdx.x) * a.nb * a.G;
-        for (int i = threadIdx.x; i < a.nb * a.G; i += kThreadsG) {
-            float s = 0.f;
-            for (int w = 0; w < kThreadsG / 32; ++w) s += all[w * a.nb * a.G + i];
-            out[i] = s;
+        if (own_sums) {
+            for (int i = threadIdx.x >> 5; i < a.nb * a.G; i += kThreadsG / 32) {
+                float s = 0.f;
+#pragma unroll
+                for (int w = 0; w < kThreadsG / 32; ++w) s += all_sums[i * kThreadsG + w * 32 + lane];
+#pragma unroll
+                for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (lane == 0) out[i] = s;
+            }
+        } else {
+            for (int i = threadIdx.x; i < a.nb * a.G; i += kThreadsG) {
+                float s = 0.f;
+                for (int w = 0; w < kThreadsG / 32; ++w) s += all_sums[w * a.nb * a.G + i];
+                out[i] = s;
+            }
         }
     }
 }
@@ -783,7 +809,10 @@ template <typename T, int DP> cudaError_t backward_width(const DattnArgs &a, cud
     }
     if (e == cudaSuccess && a.Lk > 0) {
         const dim3 grid(static_cast<unsigned>((a.Lk + F::KT - 1) / F::KT * a.row_splits), a.Hkv, a.B);
-        e = launch(dattn_grad_kv_kernel<T, DP>, grid, F::floats + table_floats(a) + warps * a.nb * a.G, a, st);
+        const size_t base = F::floats + table_floats(a), own = base + kThreadsG * a.nb * a.G;
+        DattnArgs with = a;
+        with.own_sums = own * sizeof(float) <= 227 * 1024;
+        e = launch(dattn_grad_kv_kernel<T, DP>, grid, with.own_sums ? own : base + warps * a.nb * a.G, with, st);
         if (e == cudaSuccess && a.row_splits > 1) {
             const int64_t keys = static_cast<int64_t>(a.B) * a.Lk * a.Hkv;
             dattn_join_kv_kernel<T><<<static_cast<unsigned>((keys + warps - 1) / warps), kThreadsG, 0, st>>>(a);

@@ -43,6 +43,7 @@ struct DattnArgs {
     // keys_per_split, part_o [.., 2, D], part_ml [.., 2]), grad_k and grad_v
     // over the rows (part_kv [.., Dv + 2 D]).
     int32_t row_splits;
+    int32_t own_sums;   // bucket sums of every thread, not of every warp
     float *part_kv;
 };
 
