@@ -11,7 +11,7 @@
 // 4 tx + 64 c. All shared tiles are row-major with a pad of four floats:
 // sixteen neighbouring rows then fall on different banks in 16-byte reads, and
 // both products read their operands along a row, 64 multiply-adds to eight
-// 16-byte reads. 900 x 900 rows of 4 heads, D = 32, fp32: 57 us for 0.83
+// 16-byte reads. 900 x 900 rows of 4 heads, D = 32, fp32: 55 us for 0.83
 // GFLOP counted once, some 15 TFLOP/s; two CTAs per SM hide part of each
 // other's loads and of the latency between the two products.
 #include "dattn_internal.cuh"
@@ -120,6 +120,14 @@ __device__ void load_bias(const DattnArgs &a, int n, const BiasTable &t)
 __device__ __forceinline__ int bucket_of(const DattnArgs &a, const BiasTable &t, int rel)
 {
     return t.map[min(max(rel, -a.reach), a.reach) + a.reach];
+}
+
+// The bias of a pair, times log2(e); -infinity where the query does not see
+// the key. The same for both maps.
+__device__ __forceinline__ float bias_of(const DattnArgs &a, const BiasTable &t, int seen, int rel, int g)
+{
+    const float b = a.nb ? t.table[bucket_of(a, t, rel) * a.G + g] : 0.f;
+    return seen && !(a.causal && rel > 0) ? b : -INFINITY;
 }
 
 // Per-row data of a tile of rows.
@@ -248,6 +256,11 @@ __global__ void __launch_bounds__(kThreadsG, DP == 32 || (DP == 64 && QT == 16) 
             load_keys<T, DP>(a, a.k, b * a.ks[0] + n * a.ks[2] + m * a.ks[3], a.ks[1], j0, KT, a.D, kseen, sk + m * KT * (DP + 4));
         load_keys<T, F::WV>(a, a.v, b * a.vs[0] + n * a.vs[2], a.vs[1], j0, KT, a.Dv, kseen, sv);
         __syncthreads();
+        float bias[M][N];
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) bias[i][j] = bias_of(a, bt, kseen[tx + 16 * j], kpos[tx + 16 * j] - ri[i].pos, ri[i].g);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             float t[M][N];
@@ -257,10 +270,8 @@ __global__ void __launch_bounds__(kThreadsG, DP == 32 || (DP == 64 && QT == 16) 
                 float top = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const int rel = kpos[tx + 16 * j] - ri[i].pos;
-                    float s = t[i][j] * a.scale_log2;
-                    if (a.nb) s += bt.table[bucket_of(a, bt, rel) * a.G + ri[i].g];
-                    t[i][j] = kseen[tx + 16 * j] && !(a.causal && rel > 0) ? s : -INFINITY;
+                    const float s = fmaf(t[i][j], a.scale_log2, bias[i][j]);
+                    t[i][j] = bias[i][j] == -INFINITY ? -INFINITY : s;
                     top = fmaxf(top, t[i][j]);
                 }
                 top = fmaxf(mx[m][i], row_max(top));
@@ -442,6 +453,11 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_co
         __syncthreads();
         float e[M][N];
         scores<M, N, F::WV>(sg, sv, ty, tx, e);
+        float bias[M][N];
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) bias[i][j] = bias_of(a, bt, kseen[tx + 16 * j], kpos[tx + 16 * j] - ri[i].pos, ri[i].g);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             float t[M][N];
@@ -450,11 +466,8 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_co
             for (int i = 0; i < M; ++i) {
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const int rel = kpos[tx + 16 * j] - ri[i].pos;
-                    float x = t[i][j] * a.scale_log2 - lse[m][i];
-                    if (a.nb) x += bt.table[bucket_of(a, bt, rel) * a.G + ri[i].g];
-                    const bool on = kseen[tx + 16 * j] && !(a.causal && rel > 0) && lse[m][i] != INFINITY;
-                    t[i][j] = on ? ex2(x) : 0.f;
+                    const bool on = bias[i][j] != -INFINITY && lse[m][i] != INFINITY;
+                    t[i][j] = on ? ex2(fmaf(t[i][j], a.scale_log2, bias[i][j] - lse[m][i])) : 0.f;
                 }
                 if (one) {
                     // All of the row's keys are here: weights that sum to 1 and
@@ -615,8 +628,13 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_kv_kernel(const __grid_c
             }
         }
         __syncthreads();
-        float e[M][N], both[M][N];
+        float e[M][N], both[M][N], bias[M][N];
         scores<M, N, F::WV>(sv, sg, ty, tx, e);
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                bias[i][j] = bias_of(a, bt, kseen[ty + 16 * i], kpos[ty + 16 * i] - rpos[tx + 16 * j], rg[tx + 16 * j]);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             float t[M][N];
@@ -627,11 +645,8 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_kv_kernel(const __grid_c
                 const float lse = rlse[2 * c + m], dl = rdl[2 * c + m], f = m ? -rlam[c] : 1.f;
 #pragma unroll
                 for (int i = 0; i < M; ++i) {
-                    const int rel = kpos[ty + 16 * i] - rpos[c];
-                    float x = t[i][j] * a.scale_log2 - lse;
-                    if (a.nb) x += bt.table[bucket_of(a, bt, rel) * a.G + rg[c]];
-                    const bool on = kseen[ty + 16 * i] && !(a.causal && rel > 0) && lse != INFINITY;
-                    const float p = on ? f * ex2(x) : 0.f, s = on ? p * (e[i][j] - dl) : 0.f;
+                    const bool on = bias[i][j] != -INFINITY && lse != INFINITY;
+                    const float p = on ? f * ex2(fmaf(t[i][j], a.scale_log2, bias[i][j] - lse)) : 0.f, s = on ? p * (e[i][j] - dl) : 0.f;
                     float *w = ss + (ty + 16 * i) * (RT + 4) + c;
                     w[0] = m ? w[0] + p : p;
                     w[(1 + m) * KT * (RT + 4)] = s;
