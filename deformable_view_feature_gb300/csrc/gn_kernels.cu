@@ -55,11 +55,11 @@ struct GnArgs {
     float *grad_gamma, *grad_beta;
     // Counters, zero at launch: tickets drawn, joins done, then per (batch
     // item, map) tiles summed and joins done.
-    uint32_t *queue, *all_done, *tiles_done, *ready;
+    uint32_t *tickets, *all_done, *tiles_done, *ready;
     int32_t ntiles, lag; // tiles in all, tiles between a tile's sums and its outputs
     int32_t joins;       // CTAs that share a map's join
     int64_t rows;        // per batch item
-    int32_t B, C, G, Cg, nmaps, S, K, tiles, tr, affine_scales;
+    int32_t B, C, G, Cg, nmaps, S, tiles, tr, affine_scales;
     FastDiv div_Cg;
     float eps;
     GnMap maps[DA_MAX_MAPS];
@@ -74,7 +74,7 @@ template <> __device__ __forceinline__ float from_f(float v) { return v; }
 template <> __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
 
-// V consecutive channels as they are loaded: 16 or 8 bytes, or one element
+// V consecutive channels as they are loaded: four (16 or 8 bytes), or one
 // where rows are not multiples of 16 bytes.
 template <int BYTES> struct Raw;
 template <> struct Raw<16> { using type = uint4; };
@@ -117,10 +117,6 @@ template <typename T, int V> __device__ __forceinline__ void unpack(const Pack<T
     } else {
         two(p.x, f[0], f[1], static_cast<const T *>(nullptr));
         two(p.y, f[2], f[3], static_cast<const T *>(nullptr));
-        if constexpr (V == 8) {
-            two(p.z, f[4], f[5], static_cast<const T *>(nullptr));
-            two(p.w, f[6], f[7], static_cast<const T *>(nullptr));
-        }
     }
 }
 
@@ -140,11 +136,8 @@ template <typename T, int V> __device__ __forceinline__ void store_row(void *bas
         p = *reinterpret_cast<const Pack<T, V> *>(&v);
     } else if constexpr (sizeof(T) == 4) {
         p = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    } else if constexpr (V == 4) {
-        p = make_uint2(two(f[0], f[1], static_cast<const T *>(nullptr)), two(f[2], f[3], static_cast<const T *>(nullptr)));
     } else {
-        p = make_uint4(two(f[0], f[1], static_cast<const T *>(nullptr)), two(f[2], f[3], static_cast<const T *>(nullptr)),
-                       two(f[4], f[5], static_cast<const T *>(nullptr)), two(f[6], f[7], static_cast<const T *>(nullptr)));
+        p = make_uint2(two(f[0], f[1], static_cast<const T *>(nullptr)), two(f[2], f[3], static_cast<const T *>(nullptr)));
     }
     __stcs(reinterpret_cast<Pack<T, V> *>(static_cast<T *>(base) + at), p);
 }
@@ -342,13 +335,6 @@ template <typename T, int V> __device__ void tile_stats(const GnArgs &a, const T
         o[0] = m;
         o[1] = s + static_cast<float>(t.rows) * d2;
     }
-}
-
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
 }
 
 // The groups' statistics of a map from its tiles' means and squared
@@ -587,7 +573,7 @@ template <typename T, int V, int ACT, typename Ready> __device__ void tile_grad(
     }
 }
 
-// ---- the queue -------------------------------------------------------------
+// ---- tickets ---------------------------------------------------------------
 
 __device__ uint32_t g_gn_gave_up;
 
@@ -664,7 +650,7 @@ __global__ void __launch_bounds__(kGnThreads, kGnCtas) gn_kernel(const __grid_co
     __shared__ Item item;
     __shared__ uint32_t flag;
     if (threadIdx.x == 0) {
-        item = item_of(a, static_cast<int>(atomicAdd(a.queue, 1u)));
+        item = item_of(a, static_cast<int>(atomicAdd(a.tickets, 1u)));
         flag = item.kind != kJoin || wait_for(a.tiles_done + static_cast<int64_t>(item.t.b) * a.nmaps + item.t.map,
                                               (a.maps[item.t.map].rows + a.tr - 1) / a.tr);
     }
@@ -806,7 +792,6 @@ da_status gn_plan(const gn_dims *dims, const int32_t *shape, const int32_t *star
     a.div_Cg = FastDiv::make(static_cast<uint32_t>(a.Cg));
     a.nmaps = static_cast<int>(nmaps);
     a.S = d.num_scales;
-    a.K = d.num_cams;
     a.tiles = static_cast<int32_t>(tiles);
     a.affine_scales = d.affine_scales != 0;
     a.eps = d.eps;
@@ -864,9 +849,9 @@ da_status gn_buffers(GnPlan &p, const void *x, const void *g, void *y, const flo
     a.part = reinterpret_cast<float *>(w + p.part);
     a.sums = reinterpret_cast<float *>(w + p.sums);
     a.group = reinterpret_cast<float *>(w + p.group);
-    a.queue = reinterpret_cast<uint32_t *>(w + p.counters);
-    a.all_done = a.queue + 1;
-    a.tiles_done = a.queue + 2;
+    a.tickets = reinterpret_cast<uint32_t *>(w + p.counters);
+    a.all_done = a.tickets + 1;
+    a.tiles_done = a.tickets + 2;
     a.ready = a.tiles_done + static_cast<int64_t>(a.B) * a.nmaps;
     return DA_OK;
 }
@@ -903,23 +888,23 @@ template <typename T, int V, int ACT, bool BACKWARD> cudaError_t width_launch(co
         if (BACKWARD && p.ntiles > 1) gn_param_kernel<<<1, kGnThreads, 0, st>>>(p.a);
         return cudaGetLastError();
     }
-    const cudaError_t e = cudaMemsetAsync(p.a.queue, 0, p.counter_bytes, st);
+    const cudaError_t e = cudaMemsetAsync(p.a.tickets, 0, p.counter_bytes, st);
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(2 * p.ntiles + p.a.B * p.a.nmaps * p.a.joins);
     gn_kernel<T, V, ACT, BACKWARD><<<grid, kGnThreads, smem, st>>>(p.a);
     return cudaGetLastError();
 }
 
-template <typename T, int ACT, bool BACKWARD> cudaError_t queue_launch(const GnPlan &p, cudaStream_t st)
+template <typename T, int ACT, bool BACKWARD> cudaError_t map_launch(const GnPlan &p, cudaStream_t st)
 {
     return p.wide ? width_launch<T, 4, ACT, BACKWARD>(p, st) : width_launch<T, 1, ACT, BACKWARD>(p, st);
 }
 
 template <typename T> cudaError_t launch_act(const GnPlan &p, int act, bool backward, cudaStream_t st)
 {
-    if (act == GN_ACT_RELU) return backward ? queue_launch<T, GN_ACT_RELU, true>(p, st) : queue_launch<T, GN_ACT_RELU, false>(p, st);
-    if (act == GN_ACT_SILU) return backward ? queue_launch<T, GN_ACT_SILU, true>(p, st) : queue_launch<T, GN_ACT_SILU, false>(p, st);
-    return backward ? queue_launch<T, GN_ACT_NONE, true>(p, st) : queue_launch<T, GN_ACT_NONE, false>(p, st);
+    if (act == GN_ACT_RELU) return backward ? map_launch<T, GN_ACT_RELU, true>(p, st) : map_launch<T, GN_ACT_RELU, false>(p, st);
+    if (act == GN_ACT_SILU) return backward ? map_launch<T, GN_ACT_SILU, true>(p, st) : map_launch<T, GN_ACT_SILU, false>(p, st);
+    return backward ? map_launch<T, GN_ACT_NONE, true>(p, st) : map_launch<T, GN_ACT_NONE, false>(p, st);
 }
 
 cudaError_t gn_launch(const GnPlan &p, int dtype, int act, bool backward, cudaStream_t st)
