@@ -831,8 +831,8 @@ da_status gn_buffers(GnPlan &p, const void *x, const void *g, void *y, const flo
     if (p.ntiles > 0 && !stats) return fail(DA_ERR_NULL, "stats is NULL");
     if (!aligned(x, p.elem) || !aligned(y, p.elem) || !aligned(g, p.elem))
         return fail(DA_ERR_ALIGN, "feature tensors must be aligned to their elements");
-    if (!aligned(gamma, 4) || !aligned(beta, 4) || !aligned(stats, 4))
-        return fail(DA_ERR_ALIGN, "gamma, beta and stats must be 4-byte aligned");
+    if (!aligned(gamma, 4) || !aligned(beta, 4)) return fail(DA_ERR_ALIGN, "gamma and beta must be 4-byte aligned");
+    if (!aligned(stats, 8)) return fail(DA_ERR_ALIGN, "stats must be 8-byte aligned");  // a group's pair is one access
     if (p.total > 0) {
         if (!ws || ws_bytes < p.total)
             return fail(DA_ERR_WORKSPACE, "workspace of %zu bytes; %zu are needed", ws ? ws_bytes : size_t{0}, p.total);

@@ -68,8 +68,8 @@ da_status gn_workspace_size(const gn_dims *dims, const int32_t *spatial_shape, c
  *   gamma, beta       device [C] or [S, C] fp32.
  *   out               device, like feat; overwritten. Rows of no map get 0. It
  *                     may be feat itself.
- *   stats             device [B, K, S, G, 2] fp32: mean and 1/sqrt(var + eps);
- *                     overwritten. gn_backward reads it.
+ *   stats             device [B, K, S, G, 2] fp32, 8-byte aligned: mean and
+ *                     1/sqrt(var + eps); overwritten. gn_backward reads it.
  *   workspace         device, 256-byte aligned, gn_workspace_size bytes.
  */
 da_status gn_forward(const gn_dims *dims, const void *feat, const int32_t *spatial_shape,

@@ -74,6 +74,19 @@ def test_buffers_are_checked(lib):
     assert lib.gn_backward(ctypes.byref(d), vp(FAKE), shape, start, *args[:3], vp(FAKE), vp(FAKE), vp(FAKE + 2), vp(FAKE), vp(FAKE), need, None) == 3
 
 
+def test_stats_are_aligned_to_their_pairs(lib):
+    # The kernels access a group's mean and 1/sqrt(var + eps) together.
+    vp = ctypes.c_void_p
+    _, d, shape, start, need = _status(lib)
+    for off in (2, 4, 12):
+        assert lib.gn_forward(ctypes.byref(d), vp(FAKE), shape, start, vp(FAKE), vp(FAKE), vp(FAKE), vp(FAKE + off), vp(FAKE),
+                              need, None) == 3
+    _, d, shape, start, need = _status(lib, backward=1)
+    for off in (2, 4, 12):
+        assert lib.gn_backward(ctypes.byref(d), vp(FAKE), shape, start, vp(FAKE), vp(FAKE), vp(FAKE + off), vp(FAKE), vp(FAKE),
+                               vp(FAKE), vp(FAKE), vp(FAKE), need, None) == 3
+
+
 def test_binding_checks_shapes_and_types():
     x, g = torch.zeros(1, 16, 8), torch.ones(8)
     ss, ls, _, _ = _tables([(4, 4)], 1)
