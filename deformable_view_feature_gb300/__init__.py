@@ -151,13 +151,15 @@ def _check(status: int):
 def waits_gave_up(stream=None) -> bool:
     """Whether a bounded wait inside a gn_* or dattn_* kernel has run out since
     the last call (gn_device_status, dattn_device_status): results since then
-    may hold NaN. None does in a sound run. Waits for the stream."""
-    lib, handle = load_library(), _stream_handle(stream)
+    may hold NaN. None does in a sound run. Waits for the stream (the current
+    one by default); each device has its own status, that of the stream's is read."""
+    lib = load_library()
     any_of = 0
-    for status in (lib.gn_device_status, lib.dattn_device_status):
-        word = ctypes.c_uint32(0)
-        _check(status(ctypes.byref(word), handle))
-        any_of |= word.value
+    with _on_stream(stream, torch.device("cuda", torch.cuda.current_device()) if stream is None else stream.device) as handle:
+        for status in (lib.gn_device_status, lib.dattn_device_status):
+            word = ctypes.c_uint32(0)
+            _check(status(ctypes.byref(word), handle))
+            any_of |= word.value
     return any_of != 0
 
 
@@ -169,11 +171,14 @@ def _host_i32(t) -> torch.Tensor:
     return t.detach().to(device="cpu", dtype=torch.int32).contiguous()
 
 
-def _dptr(t: Optional[torch.Tensor]) -> Optional[int]:
+def _dptr(t: Optional[torch.Tensor], index: Optional[int] = None) -> Optional[int]:
+    """Data pointer of a device tensor, of the device with this index if one is given."""
     if t is None or t.numel() == 0:
         return None
     if not t.is_cuda:
         raise ValueError("device tensors must live on a CUDA device")
+    if index is not None and t.get_device() != index:
+        raise ValueError("tensors must all live on one CUDA device")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
     return t.data_ptr()
@@ -186,23 +191,31 @@ def _stream_handle(stream) -> Optional[int]:
 
 
 class _on_stream:
-    """The stream a call runs on, current for what it allocates: `stream`, or
-    the device's current one. Yields the handle for the library."""
+    """The stream a call runs on: `stream`, or the current one of the tensors'
+    device. Both are current inside, for what is launched and allocated there.
+    Yields the handle for the library."""
 
     __slots__ = ("given", "context", "device")
 
     def __init__(self, stream, device: torch.device):
-        self.given, self.device = stream, device
+        self.given, self.device, self.context = stream, device, None
 
     def __enter__(self) -> Optional[int]:
-        if self.given is None:
-            return torch.cuda.current_stream(self.device.index).cuda_stream or None
-        self.context = torch.cuda.stream(self.given)
-        self.context.__enter__()
-        return self.given.cuda_stream or None
+        index, stream = self.device.index, self.given
+        if stream is not None:
+            if index is not None and stream.device.index != index:
+                raise ValueError("the stream and the tensors must be of one CUDA device")
+            self.context = torch.cuda.stream(stream)  # makes its device current too
+        else:
+            if index is not None and index != torch.cuda.current_device():
+                self.context = torch.cuda.device(index)
+            stream = torch.cuda.current_stream(index)
+        if self.context is not None:
+            self.context.__enter__()
+        return stream.cuda_stream or None
 
     def __exit__(self, *exc):
-        if self.given is not None:
+        if self.context is not None:
             self.context.__exit__(*exc)
 
 

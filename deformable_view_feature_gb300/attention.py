@@ -72,23 +72,25 @@ def relative_buckets(num_buckets: int, max_distance: int, bidirectional: bool = 
     return torch.tensor(of, dtype=torch.int32)
 
 
-def _strided(t: torch.Tensor, name: str) -> int:
+def _strided(t: torch.Tensor, name: str, index: int) -> int:
     """Data pointer of a q, k or v whose last dimension is contiguous."""
     if t.numel() == 0:
         return 0
     if not t.is_cuda:
         raise ValueError("device tensors must live on a CUDA device")
+    if t.get_device() != index:
+        raise ValueError("tensors must all live on one CUDA device")
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     return t.data_ptr()
 
 
-def _small(t: Optional[torch.Tensor], name: str, shape, dtype) -> int:
+def _small(t: Optional[torch.Tensor], name: str, shape, dtype, index: int) -> int:
     if t is None:
         return 0
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} {shape}")
-    return _dptr(t) or 0
+    return _dptr(t, index) or 0
 
 
 def _problem(q, k, v, lam, bias_table, bucket_map, pos_q, pos_k, key_mask, key_lengths, causal, scale) -> bytes:
@@ -111,22 +113,23 @@ def _problem(q, k, v, lam, bias_table, bucket_map, pos_q, pos_k, key_mask, key_l
     if k.dtype != dtype or v.dtype != dtype:
         raise TypeError("q, k and v must have one type")
     table = buckets = num_buckets = reach = 0
+    at = q.get_device()
     if bias_table is not None or bucket_map is not None:
         if bias_table is None or bucket_map is None:
             raise ValueError("bias_table and bucket_map go together")
         if bias_table.dim() != 2 or bucket_map.dim() != 1 or bucket_map.shape[0] % 2 != 1:
             raise ValueError("bias_table must be [num_buckets, H] and bucket_map [2 * reach + 1]")
         num_buckets, reach = bias_table.shape[0], bucket_map.shape[0] // 2
-        table = _small(bias_table, "bias_table", (num_buckets, H), torch.float32)
-        buckets = _small(bucket_map, "bucket_map", (2 * reach + 1,), torch.int32)
+        table = _small(bias_table, "bias_table", (num_buckets, H), torch.float32, at)
+        buckets = _small(bucket_map, "bucket_map", (2 * reach + 1,), torch.int32, at)
     sq, sk, sv = q.stride(), k.stride(), v.stride()
     return _PROBLEM.pack(B, Lq, Lk, H, Hkv, D, Dv, _DTYPES[dtype], num_buckets, reach, 1 if causal else 0,
-                         D ** -0.5 if scale is None else scale, _strided(q, "q"), _strided(k, "k"), _strided(v, "v"),
+                         D ** -0.5 if scale is None else scale, _strided(q, "q", at), _strided(k, "k", at), _strided(v, "v", at),
                          sq[0], sq[1], sq[2], sq[3], sk[0], sk[1], sk[2], sk[3], sv[0], sv[1], sv[2],
-                         _small(lam, "lam", (H,), torch.float32), table, buckets,
-                         _small(pos_q, "pos_q", (B, Lq), torch.int32), _small(pos_k, "pos_k", (B, Lk), torch.int32),
-                         _small(key_mask, "key_mask", (B, Lk), torch.bool),
-                         _small(key_lengths, "key_lengths", (B,), torch.int32))
+                         _small(lam, "lam", (H,), torch.float32, at), table, buckets,
+                         _small(pos_q, "pos_q", (B, Lq), torch.int32, at), _small(pos_k, "pos_k", (B, Lk), torch.int32, at),
+                         _small(key_mask, "key_mask", (B, Lk), torch.bool, at),
+                         _small(key_lengths, "key_lengths", (B,), torch.int32, at))
 
 
 def _scratch(lib, p, backward, device):
@@ -178,7 +181,7 @@ def dattn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.
             out1 = torch.empty(shape, dtype=q.dtype, device=q.device)
             lse = torch.empty(shape[0], shape[2], 2, shape[1], dtype=torch.float32, device=q.device)
         ws, n = _scratch(lib, p, 0, q.device)
-        _check(lib.dattn_forward(p, _dptr(out), _dptr(out1), _dptr(lse), _dptr(ws), n, handle))
+        _check(lib.dattn_forward(p, _dptr(out, q.get_device()), _dptr(out1), _dptr(lse), _dptr(ws), n, handle))
     return (out, (out1, lse)) if keep_for_backward else out
 
 
@@ -205,8 +208,9 @@ def dattn_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch
         gl = torch.empty_like(lam)
         gt = torch.empty_like(bias_table) if bias_table is not None else None
         ws, n = _scratch(lib, p, 1, q.device)
-        _check(lib.dattn_backward(p, _dptr(out), _dptr(out1), _dptr(lse), _dptr(grad_out), _dptr(gq), _dptr(gk),
-                                  _dptr(gv), _dptr(gl), _dptr(gt), _dptr(ws), n, handle))
+        at = q.get_device()
+        _check(lib.dattn_backward(p, _dptr(out, at), _dptr(out1, at), _dptr(lse, at), _dptr(grad_out, at), _dptr(gq),
+                                  _dptr(gk), _dptr(gv), _dptr(gl), _dptr(gt), _dptr(ws), n, handle))
     return gq, gk, gv, gl, gt
 
 

@@ -90,7 +90,8 @@ def gn_forward(feat: torch.Tensor, spatial_shape, level_start_index, gamma: torc
         out = _like(out, "out", feat.shape, feat.dtype, feat.device)
         stats = torch.empty(d.batch, d.num_cams, d.num_scales, d.num_groups, 2, dtype=torch.float32, device=feat.device)
         ws = _scratch(lib, d, ssp, lsp, 0, feat.device)
-        _check(lib.gn_forward(ctypes.byref(d), _dptr(feat), ssp, lsp, _dptr(gamma), _dptr(beta), _dptr(out),
+        at = feat.get_device()
+        _check(lib.gn_forward(ctypes.byref(d), _dptr(feat), ssp, lsp, _dptr(gamma, at), _dptr(beta, at), _dptr(out, at),
                               _dptr(stats), _dptr(ws), ws.numel(), handle))
     return out, stats
 
@@ -111,9 +112,10 @@ def gn_backward(feat: torch.Tensor, spatial_shape, level_start_index, gamma: tor
         grad_feat = _like(grad_feat, "grad_feat", feat.shape, feat.dtype, feat.device)
         grad_gamma, grad_beta = torch.empty_like(gamma), torch.empty_like(beta)
         ws = _scratch(lib, d, ssp, lsp, 1, feat.device)
-        _check(lib.gn_backward(ctypes.byref(d), _dptr(feat), ssp, lsp, _dptr(gamma), _dptr(beta), _dptr(stats),
-                               _dptr(grad_out), _dptr(grad_feat), _dptr(grad_gamma), _dptr(grad_beta), _dptr(ws),
-                               ws.numel(), handle))
+        at = feat.get_device()
+        _check(lib.gn_backward(ctypes.byref(d), _dptr(feat), ssp, lsp, _dptr(gamma, at), _dptr(beta, at),
+                               _dptr(stats, at), _dptr(grad_out, at), _dptr(grad_feat, at), _dptr(grad_gamma),
+                               _dptr(grad_beta), _dptr(ws), ws.numel(), handle))
     return grad_feat, grad_gamma, grad_beta
 
 
