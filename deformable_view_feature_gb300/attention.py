@@ -21,6 +21,7 @@ import struct
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import DA_BF16, DA_F16, DA_F32, DaError, _check, _dptr, _on_stream, load_library
 
@@ -217,7 +218,8 @@ def dattn_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch
 class DifferentialAttentionFunction(torch.autograd.Function):
     """Autograd wrapper: apply(q, k, v, lam, bias_table, bucket_map, pos_q,
     pos_k, key_mask, key_lengths, causal, scale) -> out, with gradients for q,
-    k, v, lam and bias_table."""
+    k, v, lam and bias_table. It has no second derivative: asking for one
+    raises RuntimeError."""
 
     @staticmethod
     def forward(ctx, q, k, v, lam, bias_table=None, bucket_map=None, pos_q=None, pos_k=None, key_mask=None,
@@ -233,6 +235,7 @@ class DifferentialAttentionFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_output):
         q, k, v, lam, out, out1, lse, *opt = ctx.saved_tensors
         names = ("bias_table", "bucket_map", "pos_q", "pos_k", "key_mask", "key_lengths")

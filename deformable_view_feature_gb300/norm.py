@@ -18,6 +18,7 @@ import ctypes
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import DA_BF16, DA_F16, DA_F32, _check, _dptr, _host_i32, _on_stream, load_library
 
@@ -121,7 +122,8 @@ def gn_backward(feat: torch.Tensor, spatial_shape, level_start_index, gamma: tor
 
 class GroupNormActFunction(torch.autograd.Function):
     """Autograd wrapper: apply(feat, spatial_shape, level_start_index, gamma,
-    beta, num_groups, eps, act) -> out."""
+    beta, num_groups, eps, act) -> out. It has no second derivative: asking
+    for one raises RuntimeError."""
 
     @staticmethod
     def forward(ctx, feat, spatial_shape, level_start_index, gamma, beta, num_groups, eps=1e-5, act="none"):
@@ -133,6 +135,7 @@ class GroupNormActFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_output):
         feat, gamma, beta, stats = ctx.saved_tensors
         ss, ls, num_groups, act = ctx.rest
