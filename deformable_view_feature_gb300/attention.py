@@ -23,7 +23,7 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import DA_BF16, DA_F16, DA_F32, DaError, _check, _dptr, _on_stream, load_library
+from . import DA_BF16, DA_F16, DA_F32, _check, _dptr, _on_stream, load_library
 
 __all__ = ["dattn_forward", "dattn_backward", "dattn_path", "relative_buckets", "DifferentialAttentionFunction"]
 
@@ -142,10 +142,9 @@ def _scratch(lib, p, backward, device):
 def dattn_path(q, k, v, lam, backward: bool = False, **options) -> str:
     """Which kernels dattn_forward (or dattn_backward) takes for these
     arguments: "tensor" (the tensor cores) or "general" (fp32 units)."""
-    r = load_library().dattn_path(_options(q, k, v, lam, **options), int(backward))
-    if r < 0:
-        raise DaError(4, load_library().da_last_error().decode(errors="replace"))
-    return "tensor" if r == 1 else "general"
+    lib, p = load_library(), _options(q, k, v, lam, **options)
+    _check(lib.dattn_workspace_size(p, int(backward), ctypes.byref(ctypes.c_size_t(0))))  # the status of an invalid problem
+    return "tensor" if lib.dattn_path(p, int(backward)) == 1 else "general"
 
 
 def _options(q, k, v, lam, bias_table=None, bucket_map=None, pos_q=None, pos_k=None, key_mask=None, key_lengths=None,

@@ -5,6 +5,7 @@ import ctypes
 
 import pytest
 import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
 
 import deformable_view_feature_gb300 as da
 from deformable_view_feature_gb300 import attention
@@ -92,6 +93,16 @@ def test_binding_checks_shapes_and_types():
         da.dattn_forward(q, k.half(), v, lam)
     with pytest.raises(ValueError, match="together"):
         da.dattn_forward(q, k, v, lam, bias_table=torch.zeros(4, 4))
+
+
+@pytest.mark.filterwarnings("ignore")
+@pytest.mark.parametrize("H,D,status", [(3, 8, 2), (4, 129, 4)])  # no multiple of the key heads; too wide
+def test_path_of_an_invalid_problem(lib, H, D, status):
+    with FakeTensorMode():  # tensors of a device without storage; nothing is launched
+        t = [torch.empty(*s, device="cuda:0") for s in ((1, 3, H, 2, D), (1, 5, 2, 2, D), (1, 5, 2, 16), (H,))]
+        with pytest.raises(da.DaError) as e:
+            da.dattn_path(*t)
+    assert e.value.status == status
 
 
 def test_relative_buckets():
