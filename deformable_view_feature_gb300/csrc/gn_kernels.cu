@@ -18,12 +18,12 @@
 // waiting. It is bounded all the same; a wait that ran out turns the outputs
 // into NaN and sets a word that gn_device_status reads.
 //
-// Forward statistics: a tile sums x - p and (x - p)^2 per channel, p being
-// the tile's first row, and turns them into a mean and a sum of squared
-// deviations per group; tiles are then joined by
+// Forward statistics: a thread takes the rows of a batch about their own mean,
+// while they are in registers, and batches, the tile's threads, its channels
+// and at last the tiles are joined by
 //   M2 = sum M2_t + sum n_t (mean_t - mean)^2.
-// No sum of squares about zero occurs, so a mean far larger than the spread
-// costs no digits.
+// No sum of squares about another value occurs, so neither a mean far larger
+// than the spread nor a row unlike the rest costs digits.
 #include <cmath>
 #include <cuda_bf16.h>
 
@@ -213,7 +213,8 @@ template <int V> __device__ __forceinline__ Cover cover(int C)
 
 // The lane's rows of a tile, U at a time; of one tensor, or of two at the same
 // places (if TWO). begin() sends the first loads, which need nothing but the
-// tile, ahead of whatever else the CTA has to wait for; each() then calls
+// tile, ahead of whatever else the CTA has to wait for; batches() then calls
+// use() for every U rows, there(u) of which are in p and q, and each()
 // use(offset from the column's place in the tile's first row, x, g) per row.
 template <typename T, int V, bool TWO, bool LAST, int U> struct Rows {
     Pack<T, V> p[U], q[TWO ? U : 1];
@@ -224,7 +225,7 @@ template <typename T, int V, bool TWO, bool LAST, int U> struct Rows {
     {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (o + u * step < end) {
+            if (there(u)) {
                 p[u] = load_pack<T, V, LAST>(px, o + u * step);
                 if (TWO) q[u] = load_pack<T, V, LAST>(pg, o + u * step);
             }
@@ -238,20 +239,27 @@ template <typename T, int V, bool TWO, bool LAST, int U> struct Rows {
         end = on ? rows * C : 0;
         load();
     }
-    template <typename Use> __device__ __forceinline__ void each(Use use)
+    __device__ __forceinline__ bool there(int u) const { return o + u * step < end; }
+    template <typename Use> __device__ __forceinline__ void batches(Use use)
     {
         while (o < end) {
+            use();
+            o += U * step;
+            load();
+        }
+    }
+    template <typename Use> __device__ __forceinline__ void each(Use use)
+    {
+        batches([&] {
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (o + u * step < end) {
+                if (there(u)) {
                     float v[V], h[V];
                     unpack<T, V>(p[u], v);
                     if (TWO) unpack<T, V>(q[u], h);
                     use(o + u * step, v, h);
                 }
-            o += U * step;
-            load();
-        }
+        });
     }
 };
 
@@ -291,33 +299,90 @@ template <typename T, int V> __device__ void tile_stats(const GnArgs &a, const T
     float *scratch = smem;                               // [2][lanes][cols*V] <= 2 * kGnThreads * V
     float *mean_c = smem + 2 * kGnThreads * V, *m2_c = mean_c + a.C;
     const Cover c = cover<V>(a.C);
-    const float inv = 1.f / static_cast<float>(t.rows);
+    constexpr int U = kFwdRows<T, V>;
+    // A batch's mean comes from sums about its first row, except in 16 bits:
+    // 16 such values of one magnitude sum exactly in fp32 as they are.
+    constexpr bool pivot = sizeof(T) == 4;
     for (int c0 = 0; c0 < c.ncols; c0 += c.cols) {
         const int col = c0 + c.col;
         const bool on = c.on && col < c.ncols;
         const int64_t at = t.row * a.C + static_cast<int64_t>(on ? col : 0) * V;
-        Rows<T, V, false, false, kFwdRows<T, V>> rows;
+        Rows<T, V, false, false, U> rows;
         rows.begin(c, on, t.rows, a.C, a.x, a.x, at);
-        float p[V], s[V], q[V];
-        unpack<T, V>(load_pack<T, V, false>(static_cast<const T *>(a.x) + at, 0), p);
+        // Lane l of the rows has `each` of them, or one more.
+        const int each = t.rows / c.lanes, more = t.rows - each * c.lanes;
+        float mean[V], m2[V], count = 0.f;
+        int left = each + (c.lane < more);
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = q[i] = 0.f;
-        rows.each([&](int, const float (&v)[V], const float (&)[V]) {
+        for (int i = 0; i < V; ++i) mean[i] = m2[i] = 0.f;
+        rows.batches([&] {
+            float v[V], first[V], s[V], q[V];
+            const auto add = [&](int u) {
+                unpack<T, V>(rows.p[u], v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[i] += pivot ? v[i] - first[i] : v[i];
+            };
+            const auto square = [&](int u) {
+                unpack<T, V>(rows.p[u], v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float d = v[i] - s[i];
+                    q[i] = fmaf(d, d, q[i]);
+                }
+            };
+            if (pivot) unpack<T, V>(rows.p[0], first);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] = q[i] = 0.f;
+            const float n = static_cast<float>(min(left, U)), inv = __fdividef(1.f, n), share = __fdividef(n, count + n);
+            const auto means = [&] {
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[i] = pivot ? fmaf(s[i], inv, first[i]) : s[i] * inv;
+            };
+            if (left >= U) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) add(u);
+                means();
+#pragma unroll
+                for (int u = 0; u < U; ++u) square(u);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (u < left) add(u);
+                means();
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (u < left) square(u);
+            }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float d = v[i] - p[i];
-                s[i] += d;
-                q[i] = fmaf(d, d, q[i]);
+                const float d = s[i] - mean[i];
+                mean[i] = fmaf(d, share, mean[i]);
+                m2[i] += q[i] + d * d * (count * share);
             }
+            count += n;
+            left -= U;
         });
-        const int w = min(c.cols, c.ncols - c0) * V;
-        const int second = c.lanes * c.cols * V;
-        lane_sums<V>(c, s, q, scratch);
-        for (int ch = threadIdx.x; ch < w; ch += kGnThreads) {
-            const float sum = scratch[ch], sq = scratch[second + ch];
-            const float piv = to_f(static_cast<const T *>(a.x)[t.row * a.C + static_cast<int64_t>(c0) * V + ch]);
-            mean_c[c0 * V + ch] = piv + sum * inv;
-            m2_c[c0 * V + ch] = fmaxf(sq - sum * sum * inv, 0.f);
+        const int w = c.cols * V, second = c.lanes * w;
+        if (c.on) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                scratch[c.lane * w + c.col * V + i] = mean[i];
+                scratch[second + c.lane * w + c.col * V + i] = m2[i];
+            }
+        }
+        __syncthreads();
+        const int lanes = min(c.lanes, t.rows);
+        for (int ch = threadIdx.x; ch < min(c.cols, c.ncols - c0) * V; ch += kGnThreads) {
+            const float m0 = scratch[ch];
+            float s = 0.f, q = 0.f;
+            for (int l = 1; l < lanes; ++l) s = fmaf(static_cast<float>(each + (l < more)), scratch[l * w + ch] - m0, s);
+            const float m = m0 + s / static_cast<float>(t.rows);
+            for (int l = 0; l < lanes; ++l) {
+                const float d = scratch[l * w + ch] - m;
+                q += fmaf(static_cast<float>(each + (l < more)) * d, d, scratch[second + l * w + ch]);
+            }
+            mean_c[c0 * V + ch] = m;
+            m2_c[c0 * V + ch] = q;
         }
         __syncthreads();
     }
