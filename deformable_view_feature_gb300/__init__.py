@@ -120,6 +120,8 @@ def load_library():
               lib.dattn_backward):
         f.restype = ctypes.c_int
     lib.dattn_path.restype = ctypes.c_int32
+    lib.da_gn_wait_tries.argtypes = [ctypes.c_int32]
+    lib.da_gn_wait_tries.restype = ctypes.c_int32
     lib.da_status_string.argtypes = [ctypes.c_int]
     lib.da_status_string.restype = ctypes.c_char_p
     lib.da_last_error.argtypes = []

@@ -15,8 +15,8 @@
 //
 // The wait for a map's sums cannot stall: a CTA that waits has a later ticket
 // than every tile it waits for, and those, already running, are summed without
-// waiting. It is bounded all the same; a wait that ran out turns the outputs
-// into NaN and sets a word that gn_device_status reads.
+// waiting. It is bounded all the same; a wait that ran out turns what depended
+// on it into NaN and sets a word that gn_device_status reads.
 //
 // Forward statistics: a thread takes the rows of a batch about their own mean,
 // while they are in registers, and batches, the tile's threads, its channels
@@ -24,6 +24,7 @@
 //   M2 = sum M2_t + sum n_t (mean_t - mean)^2.
 // No sum of squares about another value occurs, so neither a mean far larger
 // than the spread nor a row unlike the rest costs digits.
+#include <atomic>
 #include <cmath>
 #include <cuda_bf16.h>
 
@@ -36,7 +37,9 @@ namespace {
 constexpr int kGnThreads = 256;
 constexpr int kGnCtas = 3;         // resident per SM: up to 85 registers a thread
 constexpr int kGnSmall = 65536;    // bytes of a map that one CTA takes alone
-constexpr int kGnTries = 1 << 22;  // of a wait, about a microsecond each at most
+constexpr int kGnTries = 1 << 22;  // of a wait, about a microsecond each at most (da_gn_wait_tries)
+
+std::atomic<int32_t> g_gn_tries{kGnTries};
 
 struct GnMap {
     int32_t rows, start;  // pixels, first feature row
@@ -53,9 +56,10 @@ struct GnArgs {
     float *sums;         // backward: [B, maps, 2, C]
     float *group;        // backward: [B, maps, G, 2] mean(gamma*h), mean(gamma*h*n)
     float *grad_gamma, *grad_beta;
-    // Counters, zero at launch: tickets drawn, joins done, then per (batch
-    // item, map) tiles summed and joins done.
-    uint32_t *tickets, *all_done, *tiles_done, *ready;
+    // Counters, zero at launch: tickets drawn, joins done or left out, whether
+    // one was left out, then per (batch item, map) tiles summed and joins done.
+    uint32_t *tickets, *all_done, *left_out, *tiles_done, *ready;
+    int32_t tries;       // of a wait
     int32_t ntiles, lag; // tiles in all, tiles between a tile's sums and its outputs
     int32_t joins;       // CTAs that share a map's join
     int64_t rows;        // per batch item
@@ -449,6 +453,13 @@ __device__ void join_stats(const GnArgs &a, int b, int map, float *smem)
     }
 }
 
+// In the place of a join that its tiles' sums did not reach in time.
+__device__ void nan_stats(const GnArgs &a, int b, int map)
+{
+    float *out = a.stats + (static_cast<int64_t>(b) * a.nmaps + map) * a.G * 2;
+    for (int i = threadIdx.x; i < 2 * a.G; i += kGnThreads) out[i] = NAN;
+}
+
 template <typename T, int V> __device__ void tile_nan(const GnArgs &a, const Tile &t)
 {
     float nan[V];
@@ -577,8 +588,9 @@ __device__ void join_sums(const GnArgs &a, int b, int map, int g0, int g1, float
     __syncthreads();
 }
 
-// grad_gamma and grad_beta: the maps' sums in the order (batch item, map).
-__device__ void param_grads(const GnArgs &a)
+// grad_gamma and grad_beta: the maps' sums in the order (batch item, map), or
+// NaN where a map's were left out.
+__device__ void param_grads(const GnArgs &a, bool left_out)
 {
     const int scales = a.affine_scales ? a.S : 1, maps = a.B * a.nmaps;
     for (int i = threadIdx.x; i < 2 * scales * a.C; i += kGnThreads) {
@@ -592,7 +604,7 @@ __device__ void param_grads(const GnArgs &a)
 #pragma unroll 16
             for (int m = 0; m < maps; ++m) sum += __ldcg(p + static_cast<int64_t>(m) * 2 * a.C);
         }
-        (which ? a.grad_gamma : a.grad_beta)[at] = sum;
+        (which ? a.grad_gamma : a.grad_beta)[at] = left_out ? NAN : sum;
     }
 }
 
@@ -698,9 +710,9 @@ __device__ __forceinline__ Item item_of(const GnArgs &a, int ticket)
     return it;
 }
 
-__device__ __forceinline__ bool wait_for(const uint32_t *counter, uint32_t want)
+__device__ __forceinline__ bool wait_for(const uint32_t *counter, uint32_t want, int tries)
 {
-    for (int i = 0; i < kGnTries; ++i) {
+    for (int i = 0; i < tries; ++i) {
         if (load_acquire(counter) >= want) return true;
         __nanosleep(100);
     }
@@ -717,7 +729,7 @@ __global__ void __launch_bounds__(kGnThreads, kGnCtas) gn_kernel(const __grid_co
     if (threadIdx.x == 0) {
         item = item_of(a, static_cast<int>(atomicAdd(a.tickets, 1u)));
         flag = item.kind != kJoin || wait_for(a.tiles_done + static_cast<int64_t>(item.t.b) * a.nmaps + item.t.map,
-                                              (a.maps[item.t.map].rows + a.tr - 1) / a.tr);
+                                              (a.maps[item.t.map].rows + a.tr - 1) / a.tr, a.tries);
     }
     __syncthreads();
     const Tile t = item.t;
@@ -725,7 +737,7 @@ __global__ void __launch_bounds__(kGnThreads, kGnCtas) gn_kernel(const __grid_co
     const int64_t bm = static_cast<int64_t>(t.b) * a.nmaps + t.map;
     if (kind == kOutputs) {
         const auto ready = [&] {
-            if (threadIdx.x == 0) flag = wait_for(a.ready + bm, a.joins);
+            if (threadIdx.x == 0) flag = wait_for(a.ready + bm, a.joins, a.tries);
             __syncthreads();
             return flag != 0;
         };
@@ -739,21 +751,24 @@ __global__ void __launch_bounds__(kGnThreads, kGnCtas) gn_kernel(const __grid_co
             __threadfence();
             atomicAdd(a.tiles_done + bm, 1u);
         }
-    } else if (flag) {  // without the join its outputs' waits run out
+    } else {
         const int part = item.part;
-        if (BACKWARD) join_sums(a, t.b, t.map, part * a.G / a.joins, (part + 1) * a.G / a.joins, smem);
-        else join_stats(a, t.b, t.map, smem);
+        const bool summed = flag;  // if not, no outputs of the map come to be
+        if (BACKWARD && summed) join_sums(a, t.b, t.map, part * a.G / a.joins, (part + 1) * a.G / a.joins, smem);
+        if (!BACKWARD) summed ? join_stats(a, t.b, t.map, smem) : nan_stats(a, t.b, t.map);
         __syncthreads();
         if (threadIdx.x == 0) {
             __threadfence();
-            atomicAdd(a.ready + bm, 1u);
+            if (summed) atomicAdd(a.ready + bm, 1u);
             if (BACKWARD) {
+                if (!summed) atomicOr(a.left_out, 1u);
+                __threadfence();
                 flag = atomicAdd(a.all_done, 1u) + 1 == static_cast<uint32_t>(a.B * a.nmaps * a.joins);
                 __threadfence();
             }
         }
         __syncthreads();
-        if (BACKWARD && flag) param_grads(a);
+        if (BACKWARD && flag) param_grads(a, __ldcg(a.left_out) != 0);
     }
 }
 
@@ -773,10 +788,10 @@ __global__ void __launch_bounds__(kGnThreads, kGnCtas) gn_small_kernel(const __g
     __syncthreads();
     if (BACKWARD) tile_grad<T, V, ACT>(a, t, ready);
     else tile_apply<T, V, ACT>(a, t, ready);
-    if (BACKWARD && gridDim.x == 1) param_grads(a);
+    if (BACKWARD && gridDim.x == 1) param_grads(a, false);
 }
 
-__global__ void __launch_bounds__(kGnThreads) gn_param_kernel(const __grid_constant__ GnArgs a) { param_grads(a); }
+__global__ void __launch_bounds__(kGnThreads) gn_param_kernel(const __grid_constant__ GnArgs a) { param_grads(a, false); }
 
 struct GnPlan {
     GnArgs a;
@@ -860,6 +875,7 @@ da_status gn_plan(const gn_dims *dims, const int32_t *shape, const int32_t *star
     a.tiles = static_cast<int32_t>(tiles);
     a.affine_scales = d.affine_scales != 0;
     a.eps = d.eps;
+    a.tries = g_gn_tries;
     p.elem = d.feat_dtype == DA_F32 ? 4 : 2;
     p.ntiles = tiles * d.batch;
     p.gaps = d.num_feat_rows - covered;
@@ -881,7 +897,7 @@ da_status gn_plan(const gn_dims *dims, const int32_t *shape, const int32_t *star
     p.group = at;
     if (backward) at += round256(sizeof(float) * bm * 2 * a.G);
     p.counters = at;
-    p.counter_bytes = p.ntiles > 0 ? sizeof(uint32_t) * (2 + 2 * bm) : 0;
+    p.counter_bytes = p.ntiles > 0 ? sizeof(uint32_t) * (3 + 2 * bm) : 0;
     at += round256(p.counter_bytes);
     p.total = at;
     return DA_OK;
@@ -916,7 +932,8 @@ da_status gn_buffers(GnPlan &p, const void *x, const void *g, void *y, const flo
     a.group = reinterpret_cast<float *>(w + p.group);
     a.tickets = reinterpret_cast<uint32_t *>(w + p.counters);
     a.all_done = a.tickets + 1;
-    a.tiles_done = a.tickets + 2;
+    a.left_out = a.tickets + 2;
+    a.tiles_done = a.tickets + 3;
     a.ready = a.tiles_done + static_cast<int64_t>(a.B) * a.nmaps;
     return DA_OK;
 }
@@ -1039,6 +1056,8 @@ da_status gn_backward(const gn_dims *dims, const void *feat, const int32_t *spat
     }
     return DA_OK;
 }
+
+int32_t da_gn_wait_tries(int32_t tries) { return tries < 0 ? da::g_gn_tries.load() : da::g_gn_tries.exchange(tries); }
 
 da_status gn_device_status(uint32_t *gave_up, da_stream_t stream)
 {

@@ -90,11 +90,19 @@ da_status gn_backward(const gn_dims *dims, const void *feat, const int32_t *spat
 
 /*
  * Tiles whose outputs wait for their map's statistics stop waiting after a
- * bounded number of tries; that sets a word on the device and leaves NaN or
- * nothing in the tiles' outputs (neither happens in a sound run). This call waits for
- * `stream`, reads the word into *gave_up (host) and clears it.
+ * bounded number of tries (this happens in no sound run). That sets a word on
+ * the device and turns what depended on the wait into NaN: the tiles' outputs,
+ * the map's stats, grad_gamma and grad_beta. This call waits for `stream`,
+ * reads the word into *gave_up (host) and clears it.
  */
 da_status gn_device_status(uint32_t *gave_up, da_stream_t stream);
+
+/*
+ * Sets how many tries a wait of later calls, of the whole process, has, and
+ * returns the former number; a negative one only returns it. With 0 every wait
+ * gives up at once, which is how the way out of a wait is tested.
+ */
+int32_t da_gn_wait_tries(int32_t tries);
 
 #ifdef __cplusplus
 }

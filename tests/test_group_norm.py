@@ -245,6 +245,34 @@ def test_autograd_and_graph_capture():
         assert torch.equal(y, eager) and all(torch.equal(a, b) for a, b in zip(g, eg))
 
 
+def test_wait_tries_are_returned(lib):
+    usual = lib.da_gn_wait_tries(-1)
+    assert usual > 1000 and lib.da_gn_wait_tries(7) == usual and lib.da_gn_wait_tries(usual) == 7
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["pyramid", "pyramid f32"])
+def test_waits_that_give_up_leave_nan(lib, name):
+    # Waits of no tries: every tile's outputs, the statistics and the
+    # parameters' gradients are NaN, not what the memory held.
+    args, maps, grad, S = _inputs(name)
+    assert not da.waits_gave_up()
+    out, stats = da.gn_forward(*args[:6], act=args[6])
+    grads = da.gn_backward(*args[:5], stats, grad, args[5], act=args[6])
+    usual = lib.da_gn_wait_tries(0)
+    try:
+        bad, bad_stats = da.gn_forward(*args[:6], act=args[6])
+        bad_grads = da.gn_backward(*args[:5], stats, grad, args[5], act=args[6])
+        assert da.waits_gave_up() and not da.waits_gave_up()
+    finally:
+        lib.da_gn_wait_tries(usual)
+    assert all(bool(torch.isnan(t).all()) for t in (bad, bad_stats, *bad_grads))
+    again, stats2 = da.gn_forward(*args[:6], act=args[6])
+    assert torch.equal(again, out) and torch.equal(stats2, stats)
+    assert all(torch.equal(a, b) for a, b in zip(da.gn_backward(*args[:5], stats, grad, args[5], act=args[6]), grads))
+    assert not da.waits_gave_up()
+
+
 @pytest.mark.gpu
 def test_empty_sizes():
     ss, ls, _, _ = _tables([(2, 2)], 1)
