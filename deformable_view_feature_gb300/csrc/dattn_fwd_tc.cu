@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 a.part_ml[(pt * 2 + m) * 2] = ref;
                 a.part_ml[(pt * 2 + m) * 2 + 1] = s + nan;
             } else if (a.lse) {
-                a.lse[((static_cast<int64_t>(b) * a.H + h) * 2 + m) * a.Lq + l] = s == 0.f ? INFINITY : ref + log2f(s);
+                a.lse[((static_cast<int64_t>(b) * a.H + h) * 2 + m) * a.Lq + l] = (s == 0.f ? INFINITY : ref + log2f(s)) + nan;
             }
         }
     }
