@@ -133,6 +133,11 @@ def _problem(q, k, v, lam, bias_table, bucket_map, pos_q, pos_k, key_mask, key_l
                          _small(key_lengths, "key_lengths", (B,), torch.int32, at))
 
 
+def _saved_shape(shape, dtype):
+    """Shape of saved[0] (out1 of include/dattn.h) for an output of this shape."""
+    return shape if dtype == torch.float32 else (*shape[:3], 3, shape[3])
+
+
 def _scratch(lib, p, backward, device):
     n = ctypes.c_size_t(0)
     _check(lib.dattn_workspace_size(p, backward, ctypes.byref(n)))
@@ -178,7 +183,7 @@ def dattn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.
             out = torch.empty(shape, dtype=q.dtype, device=q.device)
         out1 = lse = None
         if keep_for_backward:
-            out1 = torch.empty(shape, dtype=q.dtype, device=q.device)
+            out1 = torch.empty(_saved_shape(shape, q.dtype), dtype=q.dtype, device=q.device)
             lse = torch.empty(shape[0], shape[2], 2, shape[1], dtype=torch.float32, device=q.device)
         ws, n = _scratch(lib, p, 0, q.device)
         _check(lib.dattn_forward(p, _dptr(out, q.get_device()), _dptr(out1), _dptr(lse), _dptr(ws), n, handle))
@@ -198,11 +203,12 @@ def dattn_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch
     p = _problem(q, k, v, lam, bias_table, bucket_map, pos_q, pos_k, key_mask, key_lengths, causal, scale)
     shape = (*q.shape[:3], v.shape[3])
     out1, lse = saved
-    for name, t in (("out", out), ("saved[0]", out1), ("grad_out", grad_out)):
+    for name, t in (("out", out), ("grad_out", grad_out)):
         if t.shape != shape or t.dtype != q.dtype:
             raise ValueError(f"{name} must be {q.dtype} {shape}")
-    if lse.shape != (shape[0], shape[2], 2, shape[1]) or lse.dtype != torch.float32:
-        raise ValueError("saved[1] must be what dattn_forward returned")
+    if (out1.shape != _saved_shape(shape, q.dtype) or out1.dtype != q.dtype
+            or lse.shape != (shape[0], shape[2], 2, shape[1]) or lse.dtype != torch.float32):
+        raise ValueError("saved must be what dattn_forward returned")
     with _on_stream(stream, q.device) as handle:
         gq, gk, gv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
         gl = torch.empty_like(lam)

@@ -319,28 +319,43 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int pos = !live ? 0 : a.pos_q ? a.pos_q[static_cast<int64_t>(b) * a.Lq + l] : len - a.Lq + l;
         const float *tb = table + g * span + a.reach;
         const float lam = a.lam[h], nlam = -lam;
-        float lse[2] = {INFINITY, INFINITY}, d[2] = {0.f, 0.f};
-        if (live) {
-            const int64_t at = ((static_cast<int64_t>(b) * a.Lq + l) * a.H + h) * a.Dv;
-            const T *pg = static_cast<const T *>(a.grad_out) + at, *po = static_cast<const T *>(a.out) + at,
-                    *p1 = static_cast<const T *>(a.out1) + at;
-            for (int c = half * 8; c < a.Dv; c += 16) {
-                const uint4 ug = *reinterpret_cast<const uint4 *>(pg + c), uo = *reinterpret_cast<const uint4 *>(po + c),
-                            u1 = *reinterpret_cast<const uint4 *>(p1 + c);
-                const T *vg = reinterpret_cast<const T *>(&ug), *vo = reinterpret_cast<const T *>(&uo), *v1 = reinterpret_cast<const T *>(&u1);
+        float lse[2] = {INFINITY, INFINITY}, d[2];
+        if (live)
+            for (int m = 0; m < 2; ++m) lse[m] = a.lse[((static_cast<int64_t>(b) * a.H + h) * 2 + m) * a.Lq + l];
+        // g times the saved outputs: a row's pieces by neighbouring lanes.
+        constexpr int P = VP / 8;
+        const int piece = threadIdx.x % P;
+#pragma unroll 1
+        for (int r = threadIdx.x / P; r < kOwn; r += 256 / P) {
+            const int dr = static_cast<int>(a.div_G.div(r)), of = r - dr * a.G;
+            float d0 = 0.f, d1 = 0.f;
+            if (dr < LP && l0 + dr < a.Lq && piece * 8 < a.Dv) {
+                const int64_t row = (static_cast<int64_t>(b) * a.Lq + l0 + dr) * a.H + n * a.G + of;
+                const auto eight = [](const void *p, int64_t at) { return *reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + at); };
+                const int64_t at = row * a.Dv + piece * 8, save = row * kSaved<T> * a.Dv + piece * 8;
+                const uint4 ug = eight(a.grad_out, at), uo = eight(a.out, at), ur = eight(a.out1, save), u1 = eight(a.out1, save + a.Dv),
+                            u1r = eight(a.out1, save + 2 * a.Dv);
+                const T *vg = reinterpret_cast<const T *>(&ug), *vo = reinterpret_cast<const T *>(&uo), *vr = reinterpret_cast<const T *>(&ur),
+                        *v1 = reinterpret_cast<const T *>(&u1), *v1r = reinterpret_cast<const T *>(&u1r);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    d[0] = fmaf(dattn_float(vg[e]), dattn_float(vo[e]), d[0]);
-                    d[1] = fmaf(dattn_float(vg[e]), dattn_float(v1[e]), d[1]);
+                    d0 = fmaf(dattn_float(vg[e]), dattn_whole(vo[e], vr[e]), d0);
+                    d1 = fmaf(dattn_float(vg[e]), dattn_whole(v1[e], v1r[e]), d1);
                 }
             }
-            for (int m = 0; m < 2; ++m) lse[m] = a.lse[((static_cast<int64_t>(b) * a.H + h) * 2 + m) * a.Lq + l];
+#pragma unroll
+            for (int o = P / 2; o; o >>= 1) {
+                d0 += __shfl_xor_sync(0xffffffffu, d0, o);
+                d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+            }
+            if (piece == 0) {
+                part[0][0][r] = d0;
+                part[1][0][r] = d1;
+            }
         }
-        part[0][half][rl] = d[0];
-        part[1][half][rl] = d[1];
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        d[1] = part[1][0][rl] + part[1][1][rl];
-        d[0] = fmaf(lam, d[1], part[0][0][rl] + part[0][1][rl]);  // out = o_0 - lam o_1
+        d[1] = part[1][0][rl];
+        d[0] = fmaf(lam, d[1], part[0][0][rl]);  // out = o_0 - lam o_1
         const bool none = lse[0] == INFINITY;  // sees no key: whatever g holds there is not used
         if (none) d[0] = d[1] = 0.f;
         if (T_ > 0) {  // the rows' operands to tensor memory

@@ -49,7 +49,9 @@ template <int DP, int VP> struct FwdShared {
     static constexpr int vblock = kKeys * 128;         // of 64 columns of V
     static constexpr int stage = 2 * k + (VP / 64) * vblock;
     static constexpr int stages = 4;
-    static constexpr int bytes = 2 * q + stages * stage;
+    static constexpr int outputs = kTile * VP * 2;     // of the tile's output, and of each word saved with it
+    static constexpr int operands = 2 * q + stages * stage;
+    static constexpr int bytes = operands > 4 * outputs ? operands : 4 * outputs;
 };
 
 // Floats of the bias of G heads by relative position, with the ends' values
@@ -377,11 +379,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float w0 = s0 == 0.f ? 0.f : 1.f / s0, w1 = s1 == 0.f ? 0.f : 1.f / s1;
         const int h = n * a.G + (live ? g : 0);
         const float nan = *gave_up ? NAN : 0.f;
-        const float lam = a.lam[h] + nan;
-        const int64_t at = ((static_cast<int64_t>(b) * a.Lq + l) * a.H + h) * a.Dv;
+        const float lam = a.lam[h];
         const int64_t pt = ((static_cast<int64_t>(b) * a.Hkv + n) * a.rows + static_cast<int64_t>(l) * a.G + g) * a.splits + split;
-        const bool wide = aligned16(a.out) && aligned16(a.out1);
-        // The warps of map m write the m-th half of the columns.
+        // Outputs go through shared memory, which the products have left, so
+        // that neighbouring lanes store neighbouring pieces: piece p of row r
+        // of word k lies at piece p ^ (r % 8).
+        const auto cell = [&](int k, int r, int p) { return reinterpret_cast<uint4 *>(base + k * F::outputs + r * VP * 2 + ((p ^ (r & 7)) << 4)); };
+        // The warps of map m take the m-th half of the columns.
 #pragma unroll 1
         for (int c = m * (VP / 2); c < (m + 1) * (VP / 2); c += 32) {
             float x[32], y[32];
@@ -405,22 +409,54 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     }
                     continue;
                 }
-                uint32_t u[4], w[4];
+                const int p = (c + i) / 8;
+                uint32_t u[4], w[4], ru[4], rw[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float y0 = y[i + 2 * e] * w1, y1 = y[i + 2 * e + 1] * w1;
-                    u[e] = pack2<T>(fmaf(-lam, y0, x[i + 2 * e] * w0), fmaf(-lam, y1, x[i + 2 * e + 1] * w0));
-                    w[e] = pack2<T>(y0 + nan, y1 + nan);
+                    const float x0 = fmaf(-lam, y0, x[i + 2 * e] * w0), x1 = fmaf(-lam, y1, x[i + 2 * e + 1] * w0);
+                    u[e] = pack2<T>(x0, x1);
+                    if (!a.out1) continue;
+                    w[e] = pack2<T>(y0, y1);
+                    ru[e] = rest2<T>(u[e], x0, x1);
+                    rw[e] = rest2<T>(w[e], y0, y1);
                 }
-                T *o = static_cast<T *>(a.out) + at + c + i, *o1 = static_cast<T *>(a.out1) + at + c + i;
-                if (wide) {
-                    *reinterpret_cast<uint4 *>(o) = make_uint4(u[0], u[1], u[2], u[3]);
-                    if (a.out1) *reinterpret_cast<uint4 *>(o1) = make_uint4(w[0], w[1], w[2], w[3]);
-                } else {
+                *cell(0, rl, p) = make_uint4(u[0], u[1], u[2], u[3]);
+                if (!a.out1) continue;
+                *cell(1, rl, p) = make_uint4(ru[0], ru[1], ru[2], ru[3]);
+                *cell(2, rl, p) = make_uint4(w[0], w[1], w[2], w[3]);
+                *cell(3, rl, p) = make_uint4(rw[0], rw[1], rw[2], rw[3]);
+            }
+        }
+        if (a.splits == 1) {
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            constexpr int P = VP / 8, passes = kTile * P / 256;
+            const bool wide = aligned16(a.out) && aligned16(a.out1), bad = *gave_up;
+            const int p = threadIdx.x % P, r0 = threadIdx.x / P, words = a.out1 ? 1 + kSaved<T> : 1;
+            int64_t at[passes];  // of the thread's rows, or -1
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        o[e] = reinterpret_cast<const T *>(u)[e];
-                        if (a.out1) o1[e] = reinterpret_cast<const T *>(w)[e];
+            for (int i = 0; i < passes; ++i) {
+                const int r = r0 + i * (256 / P), dr = static_cast<int>(a.div_G.div(r));
+                at[i] = dr >= LP || l0 + dr >= a.Lq || p * 8 >= a.Dv
+                            ? -1
+                            : ((static_cast<int64_t>(b) * a.Lq + l0 + dr) * a.H + n * a.G + r - dr * a.G) * a.Dv;
+            }
+#pragma unroll 1
+            for (int k = 0; k < words; ++k) {
+                T *to = k == 0 ? static_cast<T *>(a.out) + p * 8 : static_cast<T *>(a.out1) + (k - 1) * a.Dv + p * 8;
+                uint4 v[passes];
+#pragma unroll
+                for (int i = 0; i < passes; ++i) v[i] = *cell(k, r0 + i * (256 / P), p);
+#pragma unroll
+                for (int i = 0; i < passes; ++i) {
+                    if (at[i] < 0) continue;
+                    if (bad) v[i] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);  // NaN of either type
+                    T *o = to + at[i] * (k == 0 ? 1 : kSaved<T>);
+                    if (wide) {
+                        *reinterpret_cast<uint4 *>(o) = v[i];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = reinterpret_cast<const T *>(&v[i])[e];
                     }
                 }
             }

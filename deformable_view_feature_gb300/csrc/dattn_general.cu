@@ -324,16 +324,14 @@ __global__ void __launch_bounds__(kThreadsG, DP == 32 || (DP == 64 && QT == 16) 
         const float w0 = sum[0][i] == 0.f ? 0.f : 1.f / sum[0][i];
         const float w1 = sum[1][i] == 0.f ? 0.f : 1.f / sum[1][i];
         const float lam = a.lam[h];
-        const int64_t at = ((static_cast<int64_t>(b) * a.Lq + ri[i].l) * a.H + h) * a.Dv;
+        const int64_t row = (static_cast<int64_t>(b) * a.Lq + ri[i].l) * a.H + h;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const float x[4] = {acc[0][i][c].x, acc[0][i][c].y, acc[0][i][c].z, acc[0][i][c].w};
             const float y[4] = {acc[1][i][c].x, acc[1][i][c].y, acc[1][i][c].z, acc[1][i][c].w};
             for (int e = 0; e < 4; ++e) {
                 const int d = 4 * tx + 64 * c + e;
-                if (d >= a.Dv) continue;
-                static_cast<T *>(a.out)[at + d] = dattn_round<T>(x[e] * w0 - lam * (y[e] * w1));
-                if (a.out1) static_cast<T *>(a.out1)[at + d] = dattn_round<T>(y[e] * w1);
+                if (d < a.Dv) dattn_store<T>(a, row, d, x[e] * w0 - lam * (y[e] * w1), y[e] * w1);
             }
         }
         if (a.lse && tx < 2)
@@ -365,14 +363,13 @@ template <typename T> __global__ void __launch_bounds__(kThreadsG) dattn_merge_k
         top[m] = base;
     }
     const float lam = a.lam[h];
-    const int64_t at = ((static_cast<int64_t>(b) * a.Lq + l) * a.H + h) * a.Dv;
+    const int64_t orow = (static_cast<int64_t>(b) * a.Lq + l) * a.H + h;
     for (int d = lane; d < a.Dv; d += 32) {
         float o[2] = {0.f, 0.f};
         for (int s = 0; s < a.splits; ++s)
             for (int m = 0; m < 2; ++m)
                 o[m] = fmaf(po[(s * 2 + m) * a.Dv + d], ex2(ml[(s * 2 + m) * 2] - top[m]), o[m]);
-        static_cast<T *>(a.out)[at + d] = dattn_round<T>(o[0] * inv[0] - lam * (o[1] * inv[1]));
-        if (a.out1) static_cast<T *>(a.out1)[at + d] = dattn_round<T>(o[1] * inv[1]);
+        dattn_store<T>(a, orow, d, o[0] * inv[0] - lam * (o[1] * inv[1]), o[1] * inv[1]);
     }
 }
 
@@ -387,8 +384,8 @@ template <typename T, int DP> struct BwdTile {
 };
 
 // grad_q, and the exact d_m of dattn.h. The d_m that s_m needs comes from the
-// outputs (g . out and g . out1), which 16-bit types have rounded; the walk
-// over the keys then gives the remainder, sum_j s_m, in fp32.
+// saved outputs, which hold 16 bits or more; the walk over the keys then gives
+// the remainder, sum_j s_m, in fp32.
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_constant__ DattnArgs a)
 {
@@ -419,11 +416,17 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_co
         lam[i] = a.lam[h];
         float d0 = 0.f, d1 = 0.f;
         if (ri[i].l >= 0) {
-            const int64_t at = ob + (static_cast<int64_t>(ri[i].l) * a.H + h) * a.Dv;
+            const int64_t row = (static_cast<int64_t>(b) * a.Lq + ri[i].l) * a.H + h;
+            const T *out = static_cast<const T *>(a.out) + row * a.Dv, *save = static_cast<const T *>(a.out1) + row * kSaved<T> * a.Dv;
             for (int d = tx; d < a.Dv; d += 16) {
                 const float gv = sg[(ty + 16 * i) * (F::WV + 4) + d];
-                d0 = fmaf(gv, dattn_float(static_cast<const T *>(a.out)[at + d]), d0);
-                d1 = fmaf(gv, dattn_float(static_cast<const T *>(a.out1)[at + d]), d1);
+                if constexpr (sizeof(T) == 2) {
+                    d0 = fmaf(gv, dattn_whole(out[d], save[d]), d0);
+                    d1 = fmaf(gv, dattn_whole(save[a.Dv + d], save[2 * a.Dv + d]), d1);
+                } else {
+                    d0 = fmaf(gv, out[d], d0);
+                    d1 = fmaf(gv, save[d], d1);
+                }
             }
         }
         dl[1][i] = row_sum(d1);

@@ -26,7 +26,7 @@ struct DattnArgs {
     FastDiv div_G;
     float scale;        // of the scores
     float scale_log2;   // scale * log2(e): scores are kept times log2(e)
-    void *out, *out1;   // forward outputs (backward: inputs)
+    void *out, *out1;   // forward outputs (backward: inputs); out1 [B, Lq, H, kSaved, Dv]
     float *lse;         // [B, H, 2, Lq]
     // Forward split over the keys: `splits` CTAs share a tile of rows, each
     // leaving its unnormalised sums [.., 2, Dv], and maximum and sum [.., 2, 2].
@@ -69,6 +69,42 @@ template <typename T> __device__ __forceinline__ T dattn_round(float v);
 template <> __device__ __forceinline__ float dattn_round(float v) { return v; }
 template <> __device__ __forceinline__ __half dattn_round(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 dattn_round(float v) { return __float2bfloat16_rn(v); }
+
+// What the backward pass needs of the outputs, kSaved<T> words for each value:
+// map 1's own output, and in 16 bits also what rounding took from out, before
+// it, and from map 1's, after it. The d_m of dattn.h are sums over g times the
+// outputs; from rounded ones their error, times the mean key, is the largest
+// of grad_q wherever keys have a common part. Two words hold 16 bits of a bf16
+// output and 22 of an fp16 one, whose second word is scaled to stay normal.
+template <typename T> constexpr int kSaved = sizeof(T) == 2 ? 3 : 1;
+template <typename T> constexpr float kRest = 1.f;
+template <> constexpr float kRest<__half> = 2048.f;
+template <typename T> __device__ __forceinline__ T dattn_rest(float v, T rounded)
+{
+    return dattn_round<T>((v - dattn_float(rounded)) * kRest<T>);
+}
+template <typename T> __device__ __forceinline__ float dattn_whole(T rounded, T rest)
+{
+    return fmaf(dattn_float(rest), 1.f / kRest<T>, dattn_float(rounded));
+}
+
+// Stores value d of an output and of map 1's own, and what is saved of them
+// (out1 may be null).
+template <typename T> __device__ __forceinline__ void dattn_store(const DattnArgs &a, int64_t row, int d, float out, float own1)
+{
+    const T u = dattn_round<T>(out);
+    static_cast<T *>(a.out)[row * a.Dv + d] = u;
+    if (!a.out1) return;
+    T *save = static_cast<T *>(a.out1) + row * kSaved<T> * a.Dv + d;
+    const T w = dattn_round<T>(own1);
+    if constexpr (sizeof(T) == 2) {
+        save[0] = dattn_rest(out, u);
+        save[a.Dv] = w;
+        save[2 * a.Dv] = dattn_rest(own1, w);
+    } else {
+        save[0] = w;
+    }
+}
 
 da_status dattn_forward_tensor(const DattnArgs &a, int dtype, cudaStream_t st);
 da_status dattn_backward_tensor(const DattnArgs &a, int dtype, cudaStream_t st);

@@ -328,6 +328,20 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi
     return r;
 }
 
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t v);
+template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v)
+{
+    return {__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)};
+}
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+
+// What rounding took from them (dattn_rest).
+template <typename T> __device__ __forceinline__ uint32_t rest2(uint32_t rounded, float lo, float hi)
+{
+    const float2 r = unpack2<T>(rounded);
+    return pack2<T>((lo - r.x) * kRest<T>, (hi - r.y) * kRest<T>);
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;

@@ -95,11 +95,13 @@ da_status dattn_workspace_size(const dattn_problem *p, int32_t backward, size_t 
 /*
  * dattn_forward
  *   out   device [B, Lq, H, Dv], dtype, contiguous; overwritten.
- *   out1  device, like out, and
- *   lse   device [B, H, 2, Lq] fp32: what dattn_backward needs besides out,
- *         the second map's own output sum_j P_1 v and the log2 of both maps'
- *         sums of 2^(t*log2 e), +infinity where a query sees no key. Both
- *         NULL, or neither.
+ *   out1  device [B, Lq, H, n, Dv], dtype, contiguous, and
+ *   lse   device [B, H, 2, Lq] fp32: what dattn_backward needs besides out.
+ *         fp32: n = 1, the second map's own output sum_j P_1 v. bf16 and fp16:
+ *         n = 3, what rounding took from out, the second map's own output, and
+ *         what rounding took from that (both rests times 2^11 in fp16).
+ *         lse is the log2 of both maps' sums of 2^(t*log2 e), +infinity where
+ *         a query sees no key. Both NULL, or neither.
  *   workspace  device, 256-byte aligned.
  */
 da_status dattn_forward(const dattn_problem *p, void *out, void *out1, float *lse, void *workspace,

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import deformable_view_feature_gb300 as da
-from operator_refs import check, gn_reference
+from operator_refs import check, dattn_reference, gn_reference
 
 DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 pytestmark = pytest.mark.gpu
@@ -48,3 +48,52 @@ def test_first_row_unlike_the_rest(shape, C, groups, first, rest, kind):
     var = t.var((0, 2), correction=0) + 1e-5
     got = stats[0, 0, 0, :, 1].double() ** -2
     assert float(((got - var).abs() / var).max()) < 32 * 2.0 ** -24
+
+
+# ---- differential attention ------------------------------------------------
+
+NAMES = ("grad_q", "grad_k", "grad_v", "grad_lam", "grad_table")
+
+
+def _both(t, opt, grad):
+    """What the kernels give, and the reference's values and tolerances."""
+    out, saved = da.dattn_forward(**t, **opt, keep_for_backward=True)
+    rest = {n: x for n, x in t.items() if n not in ("q", "k", "v", "lam")}
+    g = da.dattn_backward(t["q"], t["k"], t["v"], t["lam"], out, saved, grad, **rest, **opt)
+    got = {"out": out, **{n: x for n, x in zip(NAMES, g) if x is not None}}
+    val, tol = dattn_reference(**{"table" if n == "bias_table" else n: x for n, x in t.items()}, **opt, grad=grad)
+    return got, val, tol
+
+
+def _off(got, val, n):
+    return float((got[n].double() - val[n]).norm() / val[n].norm())
+
+
+def _normal(g, kind, *shape, std=1.0):
+    return (torch.randn(*shape, generator=g) * std).to(DT[kind]).cuda()
+
+
+@pytest.mark.parametrize("kind,D,layout", [("bf16", 32, "tensor"), ("f16", 64, "tensor"), ("bf16", 36, "general"), ("f16", 20, "general")])
+@pytest.mark.parametrize("common", [1.0, 2.0])
+def test_tokens_with_a_common_part(kind, D, layout, common):
+    # q, k and v are projections of tokens that share a part `common` times
+    # their own. s_m sums to 0 over the keys, so the common part of the keys
+    # takes no part in grad_q, but the roundings of s_m meet it: in 2-norm
+    # half a step times sqrt(1 + common^2) for these, and one for the result.
+    g = torch.Generator().manual_seed(D)
+    B, L, H, C = 1, 400, 4, 256
+    x = torch.randn(B, L, C, generator=g) + common * torch.randn(C, generator=g)
+    x = x / (1 + common ** 2) ** 0.5
+
+    def project(*shape):
+        n = 1
+        for s in shape:
+            n *= s
+        return (x @ torch.randn(C, n, generator=g) / C ** 0.5).reshape(B, L, *shape).to(DT[kind]).cuda()
+
+    t = dict(q=project(H, 2, D), k=project(H, 2, D), v=project(H, 2 * D), lam=torch.full((H,), 0.5).cuda())
+    assert da.dattn_path(t["q"], t["k"], t["v"], t["lam"], backward=True) == layout
+    got, val, tol = _both(t, dict(causal=False), _normal(g, kind, B, L, H, 2 * D))
+    check(got, val, tol)
+    step = torch.finfo(DT[kind]).eps / 2
+    assert _off(got, val, "grad_q") < step * (1 + (1 + common ** 2) ** 0.5)
