@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __shared__ QBars bars;
     __shared__ QKeyInfo infos[NS];
     __shared__ float part[2][2][kOwn];
+    __shared__ int used[2];  // first and last step with a key to be used
     float *table = reinterpret_cast<float *>(base + F::bytes);
 
     const int warp = warp_number(), lane = threadIdx.x & 31;
@@ -153,8 +154,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int l0 = ((a.Lq + LP - 1) / LP - 1 - blockIdx.x / (a.B * a.Hkv)) * LP;
     const int len = dattn_length(a, b);
     int end = len;
-    if (a.causal && !a.pos_q && !a.pos_k) end = min(end, max(len - a.Lq + min(l0 + LP, a.Lq), 0));
-    const int T_ = (end + kStep - 1) / kStep;
+    const bool steps_down = a.causal && !a.pos_q && !a.pos_k;  // a query sees the keys up to its own index
+    if (steps_down) end = min(end, max(len - a.Lq + min(l0 + LP, a.Lq), 0));
     const int span = 2 * a.reach + 1;
 
     if (threadIdx.x == 0) {
@@ -177,6 +178,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tma_prefetch(&mg);
     }
     if (warp == 9) tmem_alloc(&bars.tmem, 512);
+    if (a.mask && (warp == 8 || warp == 10)) {
+        // From the first key on, or from the last one back, 256 at a time.
+        const uint8_t *mask = a.mask + static_cast<int64_t>(b) * a.Lk;
+        int step = warp == 8 ? 0 : -1;  // without any: none from 0 to -1
+        for (int i = 0; i * 256 < end; ++i) {
+            const int j = (warp == 8 ? i : (end - 1) / 256 - i) * 256 + lane * 8;
+            bool any = false;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) any |= j + c < end && mask[j + c];
+            const uint32_t hit = __ballot_sync(0xffffffffu, any);
+            if (hit) {
+                step = (j - lane * 8 + (warp == 8 ? __ffs(hit) - 1 : 31 - __clz(hit)) * 8) / kStep;
+                break;
+            }
+        }
+        if (lane == 0) used[warp == 10] = step;
+    }
     if (a.nb)
         for (int i = threadIdx.x; i < a.G * span; i += kBwdThreads) {
             const int g = i / span, bucket = min(max(a.bmap[i - g * span], 0), a.nb - 1);
@@ -187,6 +205,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     fence_after();
     const uint32_t tmem = uniform(bars.tmem);
     volatile uint32_t *gave_up = &bars.gave_up;
+    // The walk: from key jb on, T_ steps.
+    const int jb = a.mask ? used[0] * kStep : 0, T_ = a.mask ? used[1] - used[0] + 1 : (end + kStep - 1) / kStep;
     auto tS = [&](int which) { return tmem + which * kStep; };
     auto tQ = [&](int m) { return tmem + F::c_out + m * DP; };
     const uint32_t sbase = smem_addr(base);
@@ -201,9 +221,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 unsigned char *st = base + F::at_stage + s * F::stage;
                 bar_wait(&bars.empty[s], ((t / NS) & 1) ^ 1, gave_up);
                 bar_expect(&bars.full[s], F::stage);
-                for (int m = 0; m < 2; ++m) tma_load(&mk, &bars.full[s], st + m * F::k, 0, m, n, t * kStep, b);
+                for (int m = 0; m < 2; ++m) tma_load(&mk, &bars.full[s], st + m * F::k, 0, m, n, jb + t * kStep, b);
                 for (int c = 0; c < VP / 64; ++c)
-                    tma_load(&mv, &bars.full[s], st + 2 * F::k + c * F::v, c * 64, 0, n, t * kStep, b);
+                    tma_load(&mv, &bars.full[s], st + 2 * F::k + c * F::v, c * 64, 0, n, jb + t * kStep, b);
             }
             if (*gave_up) {
                 bar_drain(&bars.q_full, 0);
@@ -263,7 +283,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const auto fetch = [&](int t) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int j = t * kStep + c * 32 + lane;
+                const int j = jb + t * kStep + c * 32 + lane;
                 const bool in = j < end;
                 const int64_t at = static_cast<int64_t>(b) * a.Lk + j;
                 next_use[c] = in && (!a.mask || a.mask[at]);
@@ -304,7 +324,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 unsigned char *st = base + F::at_stage + s * F::stage;
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    if (!use[c] && t * kStep + c * 32 + lane < a.Lk) clear_key<DP, VP>(st, c * 32 + lane, F::k, 2 * F::k, F::v);
+                    if (!use[c] && jb + t * kStep + c * 32 + lane < a.Lk) clear_key<DP, VP>(st, c * 32 + lane, F::k, 2 * F::k, F::v);
                 fence_async();
             }
             __syncwarp();
@@ -372,6 +392,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         const float2 nd[2] = {{-d[0], -d[0]}, {-d[1], -d[1]}};
         float2 rest[2] = {{0.f, 0.f}, {0.f, 0.f}};
+        // Whether the first step holds all keys that the row sees, or that some row of the tile does.
+        const bool whole = T_ == 1 || (steps_down && pos < jb + kStep), some = T_ == 1 || (steps_down && len - a.Lq + l0 < jb + kStep);
         for (int t = 0; t < T_; ++t) {
             const QKeyInfo &ki = infos[t % NS];
             bar_wait_warp(&bars.s_full, t & 1, gave_up);
@@ -419,10 +441,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             uint32_t p[2][16];
             const float2 mul_2 = {mul, mul}, a0 = {add[0], add[0]}, a1 = {add[1], add[1]}, nl = {nlam, nlam};
-            if (T_ == 1) {
-                // All of the row's keys are here: weights that sum to 1 and d_m
-                // from them. With few keys the rounding of the outputs would
-                // weigh most, and a row of one key has to give exactly 0.
+            if (t == 0 && some) {
+                // All of a whole row's keys are here: weights that sum to 1 and
+                // d_m from them, so that a row of one key gives exactly 0.
                 float y[2] = {0.f, 0.f};
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
@@ -437,7 +458,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 asm volatile("bar.sync 1, 256;" ::: "memory");
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    const float z = part[m][0][rl] + part[m][1][rl];
+                    const float z = whole ? part[m][0][rl] + part[m][1][rl] : 1.f;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         x[m][i] = none ? 0.f : x[m][i] / z;
@@ -449,7 +470,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 part[0][half][rl] = y[0];
                 part[1][half][rl] = y[1];
                 asm volatile("bar.sync 1, 256;" ::: "memory");
-                for (int m = 0; m < 2; ++m) d[m] = part[m][0][rl] + part[m][1][rl];
+                if (whole)
+                    for (int m = 0; m < 2; ++m) d[m] = part[m][0][rl] + part[m][1][rl];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     float s[2][2];

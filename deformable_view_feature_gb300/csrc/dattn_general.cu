@@ -441,11 +441,37 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_co
         }
     }
     int end = len;
-    if (a.causal && !a.pos_q && !a.pos_k)
-        end = min(end, len - a.Lq + static_cast<int>(a.div_G.div(min(r0 + QT, a.rows) - 1)) + 1);
-    const int first = split * a.keys_per_split;
-    const bool one = end <= KT;  // then within the first split
-    end = min(end, first + a.keys_per_split);
+    const bool steps_down = a.causal && !a.pos_q && !a.pos_k;  // a query sees the keys up to its own index
+    if (steps_down) end = min(end, len - a.Lq + static_cast<int>(a.div_G.div(min(r0 + QT, a.rows) - 1)) + 1);
+    int begin = 0;
+    if (a.mask) {  // from the first tile with a key to be used to the last such key
+        __shared__ int first_used, last_used;
+        const uint8_t *mask = a.mask + static_cast<int64_t>(b) * a.Lk;
+        if (threadIdx.x == 0) {
+            first_used = INT32_MAX;
+            last_used = -1;
+        }
+        __syncthreads();
+        for (int i = 0; i < end; i += kThreadsG) {
+            const int j = i + static_cast<int>(threadIdx.x);
+            const bool use = j < end && mask[j];
+            if (use) atomicMin(&first_used, j);
+            if (__syncthreads_or(use)) break;
+        }
+        for (int i = end - 1; i >= 0; i -= kThreadsG) {
+            const int j = i - static_cast<int>(threadIdx.x);
+            const bool use = j >= 0 && mask[j];
+            if (use) atomicMax(&last_used, j);
+            if (__syncthreads_or(use)) break;
+        }
+        begin = last_used < 0 ? 0 : first_used / KT * KT;
+        end = last_used + 1;
+    }
+    // Whether the first tile holds all keys that a row of the tile sees; the
+    // split that has it then knows the rows' d_m best.
+    const bool one = end <= begin + KT, some = one || (steps_down && len - a.Lq + static_cast<int>(a.div_G.div(r0)) < begin + KT);
+    const int writer = begin / a.keys_per_split, first = max(begin, split * a.keys_per_split);
+    end = min(end, (split + 1) * a.keys_per_split);
     for (int j0 = first; j0 < end; j0 += KT) {
         __syncthreads();
         load_key_info(a, b, end, j0, KT, kpos, kseen);
@@ -472,21 +498,24 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_co
                     const bool on = bias[i][j] != -INFINITY && lse[m][i] != INFINITY;
                     t[i][j] = on ? ex2(fmaf(t[i][j], a.scale_log2, bias[i][j] - lse[m][i])) : 0.f;
                 }
-                if (one) {
-                    // All of the row's keys are here: weights that sum to 1 and
-                    // d_m from them, so that a row of one key gives exactly 0.
-                    // (The whole warp takes this way: its rows' sums are
+                if (j0 == begin && some) {
+                    // All of a whole row's keys are here: weights that sum to 1
+                    // and d_m from them, so that a row of one key gives exactly
+                    // 0. (The whole warp takes this way: its rows' sums are
                     // formed by shuffles.)
+                    const bool whole = one || ri[i].pos < begin + KT;
                     float z = 0.f, d = 0.f;
 #pragma unroll
                     for (int j = 0; j < N; ++j) z += t[i][j];
                     z = row_sum(z);
+                    if (!whole) z = 1.f;
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
                         t[i][j] = z == 0.f ? 0.f : t[i][j] / z;
                         d += t[i][j] != 0.f ? t[i][j] * e[i][j] : 0.f;
                     }
-                    dl[m][i] = row_sum(d);
+                    d = row_sum(d);
+                    if (whole) dl[m][i] = d;
                 }
                 float r = 0.f;
 #pragma unroll
@@ -513,7 +542,7 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_co
             float *delta = a.delta + ((static_cast<int64_t>(b) * a.Hkv + n) * 2 + m) * a.rows + r;
             if (tx == 0) {
                 if (a.splits == 1) *delta = dl[m][i] + rest[m][i];
-                else if (split == 0) *delta = dl[m][i];
+                else if (split == writer) *delta = dl[m][i];
                 if (a.splits > 1) a.part_ml[(row * a.splits + split) * 2 + m] = rest[m][i];
             }
             const int64_t at = (((static_cast<int64_t>(b) * a.Lq + ri[i].l) * a.H + h) * 2 + m) * a.D;

@@ -97,3 +97,35 @@ def test_tokens_with_a_common_part(kind, D, layout, common):
     check(got, val, tol)
     step = torch.finfo(DT[kind]).eps / 2
     assert _off(got, val, "grad_q") < step * (1 + (1 + common ** 2) ** 0.5)
+
+
+@pytest.mark.parametrize("kind,H,Hk,D", [("bf16", 2, 2, 32), ("f16", 2, 2, 64), ("bf16", 6, 2, 64), ("f32", 2, 2, 32),
+                                         ("f32", 6, 2, 24), ("bf16", 2, 2, 20), ("f32", 2, 2, 72)])
+def test_first_causal_rows(kind, H, Hk, D):
+    # The first query sees one key: a softmax over one key is 1 whatever its
+    # score. The next few keep their digits, as rows of few keys do elsewhere:
+    # 1.7 times the two roundings (of s_m and of the result).
+    g = torch.Generator().manual_seed(H + D)
+    B, L = 2, 130
+    t = dict(q=_normal(g, kind, B, L, H, 2, D), k=_normal(g, kind, B, L, Hk, 2, D), v=_normal(g, kind, B, L, Hk, 2 * D),
+             lam=(torch.rand(H, generator=g) + 0.1).cuda(), bias_table=torch.randn(8, H, generator=g).cuda(),
+             bucket_map=da.relative_buckets(8, 16).cuda())
+    got, val, tol = _both(t, dict(causal=True), _normal(g, kind, B, L, H, 2 * D))
+    check(got, val, tol)
+    assert not got["grad_q"][:, 0].any()
+    few = {n: x["grad_q"][:, 1:4] for n, x in (("got", got), ("val", val))}
+    if kind != "f32":
+        assert float((few["got"].double() - few["val"]).norm() / few["val"].norm()) < 1.7 * torch.finfo(DT[kind]).eps / 2
+
+
+@pytest.mark.parametrize("kind,D", [("bf16", 32), ("f16", 64), ("f32", 32), ("bf16", 20)])
+@pytest.mark.parametrize("kept", [3, 100, 199])
+def test_one_key_kept_of_many(kind, D, kept):
+    g = torch.Generator().manual_seed(D)
+    B, L, H = 2, 200, 2
+    t = dict(q=_normal(g, kind, B, 70, H, 2, D), k=_normal(g, kind, B, L, H, 2, D), v=_normal(g, kind, B, L, H, 2 * D),
+             lam=(torch.rand(H, generator=g) + 0.1).cuda(), key_mask=torch.zeros(B, L, dtype=torch.bool).cuda())
+    t["key_mask"][0, kept] = True  # the other item sees nothing
+    got, val, tol = _both(t, dict(causal=False), _normal(g, kind, B, 70, H, 2 * D))
+    check(got, val, tol)
+    assert not got["grad_q"].any()
