@@ -20,9 +20,11 @@
 // 50 %, exponentials 27 % of their peak). 2 x 8 heads of 8,192 tokens, causal,
 // D = 64, Dv = 128: 366 us, 1.1 PFLOP/s. Eight caches of up to 32,768 keys:
 // 114 us, 3.7 TB/s.
-// A thread raises its row's reference maximum, and rescales the row's output,
-// only when a step exceeds it by more than 2^8: fp32 sums keep their digits
-// and weights up to 256 fit both types.
+// A thread raises its row's reference, and rescales the row's output, only
+// when a step's best score exceeds the one that the reference was made from by
+// more than 2^8. In fp16 the reference lies 2^7 below that score: weights of up
+// to 2^15 use the type's whole range, and weights round to nothing below 2^-32
+// of the best instead of 2^-25. Many keys of 2^-25 each are not nothing together.
 #include "dattn_tc.cuh"
 
 namespace da {
@@ -33,7 +35,8 @@ using namespace tc;
 constexpr int kTile = 128;            // rows
 constexpr int kKeys = 64;             // keys per step
 constexpr int kFwdThreads = 11 * 32;
-constexpr float kSlack = 8.f;         // log2 of how far weights may exceed 1
+constexpr float kSlack = 8.f;         // log2 of how far weights may exceed their first best
+template <typename T> constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;  // log2 of that best
 
 // What the softmax warps need to know of a step's keys.
 struct alignas(16) KeyInfo {
@@ -331,9 +334,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const float best = fmaf(max3(fmaxf(top[0], top[1]), top[2], top[3]), mul, add);
             // Each row by its own scores alone, so that its roundings do not
             // depend on its neighbours'; rows past the end hold stale values.
-            const bool raise = live && best > ref + kSlack;
+            const bool raise = live && best > ref + (kLift<T> + kSlack);
             if (__any_sync(0xffffffffu, raise)) {
-                const float next = raise ? best : ref;
+                const float next = raise ? best - kLift<T> : ref;
                 const float shrink = raise ? ex2(ref - next) : 1.f;
                 ref = next;
                 const float2 sh = {shrink, shrink};

@@ -129,3 +129,19 @@ def test_one_key_kept_of_many(kind, D, kept):
     got, val, tol = _both(t, dict(causal=False), _normal(g, kind, B, 70, H, 2 * D))
     check(got, val, tol)
     assert not got["grad_q"].any()
+
+
+def test_fp16_many_small_weights():
+    # One key of weight 1 and 16,384 of 2^-25 each, together 2^-11: half of
+    # fp16's smallest number each, as much as eight steps of the result together.
+    B, Lq, Lk, H, D = 1, 3, 16385, 2, 64
+    q, k, v = torch.zeros(B, Lq, H, 2, D), torch.zeros(B, Lk, H, 2, D), torch.full((B, Lk, H, 2 * D), 8.0)
+    q[..., 0] = 1.0
+    k[:, 0, :, :, 0] = 25.0
+    v[:, 0] = 0.0
+    t = dict(q=q.half().cuda(), k=k.half().cuda(), v=v.half().cuda(), lam=torch.tensor([0.5, 0.25]).cuda())
+    opt = dict(scale=0.6931471805599453)  # scores in powers of two
+    out = da.dattn_forward(**t, **opt)
+    val, tol = dattn_reference(**t, **opt)
+    assert float(val["out"].abs().min()) > 1e-3
+    assert float((out.double() - val["out"]).abs().max() / val["out"].abs().max()) < 2.0 ** -10
