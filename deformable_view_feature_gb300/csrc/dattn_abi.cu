@@ -68,7 +68,7 @@ struct DattnPlan {
     DattnArgs a;
     int elem;
     bool tensor;
-    size_t part_o, part_ml, part_kv, delta, part_table, total;
+    size_t part_o, part_ml, part_kv, delta, part_table, most, total;
 };
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -191,6 +191,8 @@ da_status dattn_plan(const dattn_problem *pr, bool backward, DattnPlan &p)
         at += round256(sizeof(float) * bn * 2 * rows);
         p.part_table = at;
         at += round256(sizeof(float) * bn * a.table_ctas * a.nb * G);
+        p.most = at;
+        if (p.tensor && d.dtype == DA_F16) at += round256(sizeof(uint32_t) * 2 * bn);
     }
     p.total = at;
     return DA_OK;
@@ -220,6 +222,7 @@ da_status dattn_buffers(DattnPlan &p, void *ws, size_t ws_bytes)
     a.part_kv = reinterpret_cast<float *>(w + p.part_kv);
     a.delta = reinterpret_cast<float *>(w + p.delta);
     a.part_table = reinterpret_cast<float *>(w + p.part_table);
+    a.most = reinterpret_cast<uint32_t *>(w + p.most);
     return DA_OK;
 }
 

@@ -43,6 +43,47 @@ __device__ uint32_t g_gave_up_backward;
 
 template <typename T> constexpr bool is_bf16 = !std::is_same<T, __half>::value;
 
+// fp16 operands need scales of their own: s_m is about a gradient over a
+// number of keys, far below the type's normal numbers or, times g v, past its
+// largest. |s_m| <= P |e - d| and |e|, |d| <= sum |g| max |v|, so with
+//   bound = 2 sum_c |g_c| max(1, |lam|) max |v|
+// a power of two brings s_m to at most 2^15: of each row in the first kernel,
+// of all rows of the key head in the second, where one sum goes over them. It
+// enters with e and d, in the place of their difference's addition, and is
+// taken out of the sums in fp32. The weights are formed 2^15 / (1 + max |lam|)
+// higher by the exponent. bf16 has fp32's exponents and needs none of it.
+template <typename T> constexpr bool kScaled = std::is_same<T, __half>::value;
+
+// The power of two that takes values of up to `bound` to at most 2^15.
+__device__ __forceinline__ float scale_to_range(float bound)
+{
+    if (!(bound > 0.f && bound < INFINITY)) return 1.f;  // nothing to scale, or nothing that would help
+    const int e = 14 - (static_cast<int>(__float_as_uint(bound) >> 23) - 127);  // bound < 2^(15 - e)
+    return __uint_as_float(static_cast<uint32_t>(min(max(e, -100), 100) + 127) << 23);
+}
+
+// Largest |v| of each batch item and key head, over the keys to be used.
+constexpr int kMostKeys = 128;  // keys of a CTA
+__global__ void __launch_bounds__(256) dattn_most_v_kernel(const __grid_constant__ DattnArgs a)
+{
+    const int bn = blockIdx.x % (a.B * a.Hkv), b = bn / a.Hkv, n = bn - b * a.Hkv, j0 = blockIdx.x / (a.B * a.Hkv) * kMostKeys;
+    const int piece = threadIdx.x & 15;  // of 8 channels
+    const int len = dattn_length(a, b);
+    const __half *v = static_cast<const __half *>(a.v) + b * a.vs[0] + n * a.vs[2] + piece * 8;
+    uint32_t most = 0;  // bits of |v|, in fp16: they order as the values do
+#pragma unroll
+    for (int i = 0; i < kMostKeys; i += 16) {
+        const int j = j0 + i + static_cast<int>(threadIdx.x >> 4);
+        if (j >= len || piece * 8 >= a.Dv || (a.mask && !a.mask[static_cast<int64_t>(b) * a.Lk + j])) continue;
+        const uint4 u = *reinterpret_cast<const uint4 *>(v + j * a.vs[1]);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) most = __vmaxu2(most, w[c] & 0x7fff7fffu);
+    }
+    most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
+    if ((threadIdx.x & 31) == 0) atomicMax(a.most + bn, __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(most)))));
+}
+
 // 32 columns of one row of a [128][64] operand of 16 bits, swizzled as TMA
 // would: 16-byte piece i of row r lies at piece i ^ (r % 8).
 __device__ __forceinline__ void store_operand(unsigned char *tile, int row, int half, const uint32_t (&p)[16])
@@ -348,7 +389,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll 1
         for (int r = threadIdx.x / P; r < kOwn; r += 256 / P) {
             const int dr = static_cast<int>(a.div_G.div(r)), of = r - dr * a.G;
-            float d0 = 0.f, d1 = 0.f;
+            float d0 = 0.f, d1 = 0.f, sum = 0.f;  // the last of |g|
             if (dr < LP && l0 + dr < a.Lq && piece * 8 < a.Dv) {
                 const int64_t row = (static_cast<int64_t>(b) * a.Lq + l0 + dr) * a.H + n * a.G + of;
                 const auto eight = [](const void *p, int64_t at) { return *reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + at); };
@@ -361,16 +402,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 for (int e = 0; e < 8; ++e) {
                     d0 = fmaf(dattn_float(vg[e]), dattn_whole(vo[e], vr[e]), d0);
                     d1 = fmaf(dattn_float(vg[e]), dattn_whole(v1[e], v1r[e]), d1);
+                    if (kScaled<T>) sum += fabsf(dattn_float(vg[e]));
                 }
             }
 #pragma unroll
             for (int o = P / 2; o; o >>= 1) {
                 d0 += __shfl_xor_sync(0xffffffffu, d0, o);
                 d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+                if (kScaled<T>) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             }
             if (piece == 0) {
                 part[0][0][r] = d0;
                 part[1][0][r] = d1;
+                if (kScaled<T>) part[0][1][r] = sum;
             }
         }
         asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -378,6 +422,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         d[0] = fmaf(lam, d[1], part[0][0][rl]);  // out = o_0 - lam o_1
         const bool none = lse[0] == INFINITY;  // sees no key: whatever g holds there is not used
         if (none) d[0] = d[1] = 0.f;
+        float f = 1.f;  // s_m is formed times f
+        if (kScaled<T>) {
+            const float of_g = none ? 0.f : 2.f * part[0][1][rl] * fmaxf(1.f, fabsf(lam));
+            f = scale_to_range(of_g * __uint_as_float(a.most[bn]));
+            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(of_g));
+            if (half == 0 && lane == 0) atomicMax(a.most + a.B * a.Hkv + bn, most);
+        }
         if (T_ > 0) {  // the rows' operands to tensor memory
             bar_wait_warp(&bars.q_full, 0, gave_up);
             for (int m = 0; m < 2; ++m)
@@ -390,7 +441,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             __syncwarp();
             if (lane == 0) bar_arrive(&bars.q_ready);
         }
-        const float2 nd[2] = {{-d[0], -d[0]}, {-d[1], -d[1]}};
+        const float2 nd[2] = {{-d[0] * f, -d[0] * f}, {-d[1] * f, -d[1] * f}}, f_2 = {f, f};
+        const auto less_d = [&](float2 e, int m) { return kScaled<T> ? fma2(e, f_2, nd[m]) : add2(e, nd[m]); };
         float2 rest[2] = {{0.f, 0.f}, {0.f, 0.f}};
         // Whether the first step holds all keys that the row sees, or that some row of the tile does.
         const bool whole = T_ == 1 || (steps_down && pos < jb + kStep), some = T_ == 1 || (steps_down && len - a.Lq + l0 < jb + kStep);
@@ -478,7 +530,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) s[m][k] = x[m][2 * i + k] * (e[2 * i + k] - d[m]);
+                        for (int k = 0; k < 2; ++k) s[m][k] = x[m][2 * i + k] * ((e[2 * i + k] - d[m]) * f);
                     rest[0] = add2(rest[0], {s[0][0], s[0][1]});
                     rest[1] = add2(rest[1], {s[1][0], s[1][1]});
                     p[0][i] = pack2<T>(s[0][0], s[0][1]);
@@ -493,7 +545,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     w0.y = ex2(w0.y);
                     w1.x = ex2(w1.x);
                     w1.y = ex2(w1.y);
-                    const float2 s0 = mul2(w0, add2(ei, nd[0])), s1 = mul2(w1, add2(ei, nd[1]));
+                    const float2 s0 = mul2(w0, less_d(ei, 0)), s1 = mul2(w1, less_d(ei, 1));
                     rest[0] = add2(rest[0], s0);
                     rest[1] = add2(rest[1], s1);
                     const float2 s1l = mul2(s1, nl);
@@ -518,7 +570,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const float nan = *gave_up ? NAN : 0.f;
         if (live)
             a.delta[((static_cast<int64_t>(b) * a.Hkv + n) * 2 + m) * a.rows + static_cast<int64_t>(l) * a.G + g] =
-                d[m] + part[m][0][rl] + part[m][1][rl] + nan;
+                d[m] + (part[m][0][rl] + part[m][1][rl]) / f + nan;
         T *dst = static_cast<T *>(a.grad_q) + (((static_cast<int64_t>(b) * a.Lq + l) * a.H + h) * 2 + m) * a.D;
         const bool wide = aligned16(a.grad_q);
 #pragma unroll 1
@@ -531,7 +583,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = 0.f;
             }
-            if (live) store_row(dst + c, x, a.scale + nan, a.D - c, wide);
+            if (live) store_row(dst + c, x, a.scale / f + nan, a.D - c, wide);
         }
     }
     fence_before();
@@ -564,7 +616,8 @@ template <int DP, int VP> struct GradKVShared {
 
 // Per-query values of a step, the queries' positions among them.
 struct alignas(16) QueryInfo {
-    // Of each two queries: minus the log-sums of map 0, of map 1, minus d_0, d_1.
+    // Of each two queries: minus the log-sums of map 0, of map 1, minus d_0,
+    // d_1, with the scales that the weights and s_m are formed with.
     float values[kStep / 2][8];
     int pos[kStep];
     int lo, hi;
@@ -638,6 +691,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t tV = tmem + 192;
     auto tK = [&](int m) { return tmem + 192 + VP + m * DP; };
     const uint32_t sbase = smem_addr(base);
+    // Weights are formed times lift, s_m times lift * f.
+    float lift = 1.f, f = 1.f;
+    if (kScaled<T> && (warp < 8 || warp == 10)) {
+        float most = 0.f;
+        for (int g = lane; g < a.G; g += 32) most = fmaxf(most, fabsf(a.lam[n * a.G + g]));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        lift = scale_to_range(1.f + most);
+        f = scale_to_range(__uint_as_float(a.most[a.B * a.Hkv + bn]) * __uint_as_float(a.most[bn])) / lift;
+    }
 
     if (warp == 8) {
         if (lane == 0 && T_ > 0) {
@@ -750,6 +813,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
         };
         fetch(0);
+        const float higher = static_cast<float>(static_cast<int>(__float_as_uint(lift) >> 23) - 127);  // log2(lift)
         for (int t = 0; t < T_; ++t) {
             const int s = t % NS, l0 = first + (t % per) * kStep;
             QueryInfo &qi = infos[s];
@@ -774,10 +838,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const bool in = l0 + i < a.Lq;
                 // Pairs of queries: {map 0 of both, map 1 of both}.
                 float *to = &qi.values[i >> 1][i & 1];
-                to[0] = -lse[c][0];
-                to[2] = -lse[c][1];
-                to[4] = -d[c][0];
-                to[6] = -d[c][1];
+                to[0] = higher - lse[c][0];
+                to[2] = higher - lse[c][1];
+                to[4] = -d[c][0] * f;
+                to[6] = -d[c][1] * f;
                 qi.pos[i] = pos[c];
                 idle[c] = in && lse[c][0] == INFINITY;
                 if (in) {
@@ -865,7 +929,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     mul = 1.f;
                     add = 0.f;
                 }
-                const float2 mul_2 = {mul, mul}, add_2 = {add, add}, nl = {nlam, nlam};
+                const float2 mul_2 = {mul, mul}, add_2 = {add, add}, nl = {nlam, nlam}, f_2 = {f, f};
+                const auto less_d = [&](float2 e, float2 nd) { return kScaled<T> ? fma2(e, f_2, nd) : add2(e, nd); };
                 float2 total = {0.f, 0.f};
                 uint32_t pw[16], p0[16], p1[16];
 #pragma unroll
@@ -880,7 +945,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     w0.y = ex2(w0.y);
                     w1.x = ex2(w1.x);
                     w1.y = ex2(w1.y);
-                    const float2 s0 = mul2(w0, add2(ei, d0)), s1 = mul2(mul2(w1, nl), add2(ei, d1)), w = fma2(w1, nl, w0);
+                    const float2 s0 = mul2(w0, less_d(ei, d0)), s1 = mul2(mul2(w1, nl), less_d(ei, d1)), w = fma2(w1, nl, w0);
                     const float2 both = add2(s0, s1);
                     total = add2(total, both);
                     x[0][2 * i] = both.x;  // kept for the buckets
@@ -929,7 +994,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     for (int i = 0; i < 8; ++i) s += sums[k * 256 + i * 32 + lane];
 #pragma unroll
                     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                    if (lane == 0) out[k * a.G + g] = *gave_up ? NAN : s;
+                    if (lane == 0) out[k * a.G + g] = *gave_up ? NAN : s / (lift * f);
                 }
             }
         }
@@ -953,8 +1018,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 for (int i = 0; i < 32; ++i) x[i] = 0.f;
             }
             if (!in) continue;
-            if (of_v) store_row(static_cast<T *>(a.grad_v) + at * a.Dv + col, x, 1.f + nan, a.Dv - col, wide_v);
-            else store_row(static_cast<T *>(a.grad_k) + (at * 2 + half) * a.D + col, x, a.scale + nan, a.D - col, wide_k);
+            if (of_v) store_row(static_cast<T *>(a.grad_v) + at * a.Dv + col, x, 1.f / lift + nan, a.Dv - col, wide_v);
+            else store_row(static_cast<T *>(a.grad_k) + (at * 2 + half) * a.D + col, x, a.scale / (lift * f) + nan, a.D - col, wide_k);
         }
     }
     fence_before();
@@ -985,7 +1050,15 @@ cudaError_t bwd_kernels(const DattnArgs &a, const BwdMaps &own_rows, const BwdMa
     using Q = GradQShared<DP, VP>;
     using KV = GradKVShared<DP, VP>;
     const int LP = kOwn / a.G;
-    const cudaError_t e = launch_bwd(dattn_grad_q_tc_kernel<T, DP, VP>, dim3((a.Lq + LP - 1) / LP * a.Hkv * a.B),
+    cudaError_t e = cudaSuccess;
+    if (kScaled<T>) {
+        const int heads = a.B * a.Hkv;
+        e = cudaMemsetAsync(a.most, 0, sizeof(uint32_t) * 2 * heads, st);
+        if (e != cudaSuccess) return e;
+        dattn_most_v_kernel<<<static_cast<unsigned>((a.Lk + kMostKeys - 1) / kMostKeys) * heads, 256, 0, st>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    e = launch_bwd(dattn_grad_q_tc_kernel<T, DP, VP>, dim3((a.Lq + LP - 1) / LP * a.Hkv * a.B),
                                      Q::bytes + 1024 + sizeof(float) * (a.nb ? a.G * (2 * a.reach + 1) : 0), a, own_rows, st);
     if (e != cudaSuccess) return e;
     return launch_bwd(dattn_grad_kv_tc_kernel<T, DP, VP>, dim3((a.Lk + kOwn - 1) / kOwn * a.Hkv * a.B),

@@ -37,6 +37,7 @@ struct DattnArgs {
     void *grad_q, *grad_k, *grad_v;
     float *grad_lam, *grad_table;
     float *delta;       // [B, Hkv, 2, rows] the d_m of dattn.h
+    uint32_t *most;     // fp16 on the tensor cores: [2, B * Hkv] bits of the largest |v| and bound of grad_out
     float *part_table;  // [key-tile CTAs, nb * G]
     int32_t table_ctas; // CTAs of the second kernel per (b, key head)
     // The general kernels' splits backward: grad_q over the keys (splits,

@@ -145,3 +145,51 @@ def test_fp16_many_small_weights():
     val, tol = dattn_reference(**t, **opt)
     assert float(val["out"].abs().min()) > 1e-3
     assert float((out.double() - val["out"]).abs().max() / val["out"].abs().max()) < 2.0 ** -10
+
+
+@pytest.mark.parametrize("size", [1.0, 1e-2, 1e-4])
+def test_fp16_small_gradients(size):
+    # s_m and the weights are about size / keys: their roundings as operands
+    # may be no more than half a step each, in 2-norm, beside the result's.
+    # q, k and the scale are chosen so that the results themselves are not small.
+    g = torch.Generator().manual_seed(7)
+    B, L, H, D = 1, 2048, 2, 64
+    t = dict(q=_normal(g, "f16", B, L, H, 2, D, std=2.0 ** -5), k=_normal(g, "f16", B, L, H, 2, D, std=2.0 ** -5),
+             v=_normal(g, "f16", B, L, H, 2 * D), lam=torch.tensor([0.5, 0.8]).cuda())
+    got, val, _ = _both(t, dict(scale=2.0 ** 10 / 8), _normal(g, "f16", B, L, H, 2 * D, std=size))
+    for n in ("grad_q", "grad_k", "grad_v"):
+        step = 2.0 ** -11
+        once = float((val[n].half().double() - val[n]).norm() / val[n].norm())
+        assert _off(got, val, n) < 1.7 * step + 1.5 * once, n
+
+
+@pytest.mark.parametrize("Lk,std_v", [(5, 8.0), (130, 64.0)])
+@pytest.mark.parametrize("D", [32, 64])
+def test_fp16_large_gradients(D, Lk, std_v):
+    # e = g v reaches 10^6 and s_m 10^5, past fp16; grad_q, grad_k and grad_v do not.
+    g = torch.Generator().manual_seed(D)
+    B, Lq, H = 1, 9, 2
+    t = dict(q=_normal(g, "f16", B, Lq, H, 2, D, std=3.0), k=_normal(g, "f16", B, Lk, H, 2, D, std=3.0),
+             v=_normal(g, "f16", B, Lk, H, 2 * D, std=std_v), lam=torch.tensor([0.5, 0.8]).cuda())
+    got, val, tol = _both(t, dict(scale=2.0 ** -7), _normal(g, "f16", B, Lq, H, 2 * D, std=4096.0))
+    assert all(float(val[n].abs().max()) < 65504 for n in ("grad_q", "grad_k", "grad_v"))
+    check(got, val, tol)
+    for n in ("grad_q", "grad_k", "grad_v"):
+        assert _off(got, val, n) < 1.7 * 2.0 ** -11, n
+
+
+def test_fp16_gradients_of_all_sizes():
+    # Rows whose gradients differ by 2^20, one head's lam far above 1, a key
+    # that is not to be used with infinite values.
+    g = torch.Generator().manual_seed(3)
+    B, L, H, D = 2, 300, 4, 32
+    grad = torch.randn(B, L, H, 2 * D, generator=g) * 2.0 ** torch.randint(-16, 5, (B, L, 1, 1), generator=g)
+    t = dict(q=_normal(g, "f16", B, L, H, 2, D), k=_normal(g, "f16", B, L, 2, 2, D), v=_normal(g, "f16", B, L, 2, 2 * D),
+             lam=torch.tensor([0.5, 30.0, -0.8, 0.0]).cuda(), key_mask=(torch.rand(B, L, generator=g) < 0.8).cuda(),
+             bias_table=torch.randn(8, H, generator=g).cuda(), bucket_map=da.relative_buckets(8, 16).cuda())
+    t["v"][~t["key_mask"]] = float("inf")
+    got, val, tol = _both(t, dict(causal=True), grad.half().cuda())
+    check(got, val, tol)
+    each = (got["grad_q"].double() - val["grad_q"]).flatten(2).norm(dim=2)
+    once = (val["grad_q"].half().double() - val["grad_q"]).flatten(2).norm(dim=2)
+    assert bool((each <= 4 * 2.0 ** -11 * val["grad_q"].flatten(2).norm(dim=2) + 2 * once).all())
