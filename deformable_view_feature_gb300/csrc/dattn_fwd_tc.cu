@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
     __shared__ FwdBars bars;
     __shared__ KeyInfo infos[NS];
-    __shared__ float row_l[2][kTile], row_m[2][kTile];
+    __shared__ float row_l[2][kTile];
     float *table = reinterpret_cast<float *>(base + F::bytes);  // [G][span], times log2(e)
 
     const int warp = warp_number(), lane = threadIdx.x & 31;
@@ -332,8 +332,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], s[kKeys - 4 + c]);
             const float best = fmaf(max3(fmaxf(top[0], top[1]), top[2], top[3]), mul, add);
-            // Each row by its own scores alone, so that its roundings do not
-            // depend on its neighbours'; rows past the end hold stale values.
+            // Each row's reference by its own scores alone; rows past the end
+            // hold stale values. (Whether the bias is added before the
+            // exponent's product or with it is one choice for a warp's rows, so
+            // that a row's last bits can depend on which rows lie beside it.)
             const bool raise = live && best > ref + (kLift<T> + kSlack);
             if (__any_sync(0xffffffffu, raise)) {
                 const float next = raise ? best - kLift<T> : ref;
@@ -374,7 +376,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (lane == 0) bar_arrive(&bars.p_full[m][t & 1]);
         }
         row_l[m][rl] = sum[0].x + sum[0].y + (sum[1].x + sum[1].y);
-        row_m[m][rl] = ref;
         if (T_ > 0) bar_wait_warp(&bars.fin, 0, gave_up);
         fence_after();
         asm volatile("bar.sync 1, 256;" ::: "memory");
