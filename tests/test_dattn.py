@@ -380,6 +380,42 @@ def test_streams_and_graph_capture():
         assert all(torch.equal(r[n], want[n]) for n in r)
 
 
+def _off_by_one(x):
+    """The same values one element further in memory."""
+    y = torch.empty(x.numel() + 1, dtype=x.dtype, device=x.device)[1:].view(x.shape)
+    return y.copy_(x)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,D", [("f32", 32), ("bf16", 32), ("f16", 64), ("bf16", 20)])
+@pytest.mark.parametrize("odd", ["out", "saved", "grad"])
+def test_outputs_and_gradients_of_odd_alignment(kind, D, odd):
+    # The backward pass then takes the general kernels, after any forward.
+    t, opt, grad = _case(B=2, Lq=90, Lk=130, H=4, Hk=2, D=D, kind=kind, buckets=8, causal=True)
+    out, saved = da.dattn_forward(**t, **opt, keep_for_backward=True)
+    if odd == "out":
+        aligned, out = out, _off_by_one(torch.zeros_like(out))
+        again, saved = da.dattn_forward(**t, **opt, out=out, keep_for_backward=True)
+        assert again.data_ptr() == out.data_ptr() and torch.equal(out, aligned)
+    elif odd == "saved":
+        saved = tuple(_off_by_one(x) for x in saved)
+    else:
+        grad = _off_by_one(grad)
+    args = {n: x for n, x in t.items() if n not in ("q", "k", "v", "lam")}
+    g = da.dattn_backward(t["q"], t["k"], t["v"], t["lam"], out, saved, grad, **args, **opt)
+    val, tol = _reference(t, opt, grad)
+    check(dict(zip(("grad_q", "grad_k", "grad_v", "grad_lam", "grad_table"), g), out=out), val, tol)
+
+
+@pytest.mark.gpu
+def test_saved_of_another_type_is_refused():
+    t, opt, grad = _case(Lq=4, Lk=4, kind="bf16")
+    out, (out1, lse) = da.dattn_forward(**t, **opt, keep_for_backward=True)
+    for bad in ((out1.half(), lse), (out1[:, :, :, :1], lse), (out1, lse.double()), (out1, lse[:, :1])):
+        with pytest.raises(ValueError, match="saved"):
+            da.dattn_backward(t["q"], t["k"], t["v"], t["lam"], out, bad, grad)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_offsets_past_32_bits(kind):

@@ -170,6 +170,53 @@ def test_relu_gradient_away_from_its_border():
     _check_all((x, ss, ls, one, zero, 2, "relu"), maps, grad, 1, out, grads)
 
 
+LARGE = {
+    # shapes, C, groups, type, act: maps above 64 KB, which several tiles share
+    "relu f32": ([(150, 200)], 64, 8, "f32", "relu"),
+    "relu bf16": ([(90, 120), (45, 60)], 96, 12, "bf16", "relu"),
+    "relu f16": ([(75, 99)], 40, 8, "f16", "relu"),
+    "three groups": ([(150, 200)], 24, 3, "f32", "silu"),
+    "one group": ([(64, 99)], 32, 1, "bf16", "none"),
+    "scalar columns": ([(150, 101), (1, 1)], 15, 5, "f16", "silu"),
+    "two scalar groups": ([(201, 200)], 6, 2, "bf16", "silu"),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", list(LARGE))
+def test_large_maps(name):
+    shapes, C, groups, kind, act = LARGE[name]
+    ss, ls, maps, rows = _tables(shapes, 2)
+    g = torch.Generator().manual_seed(C)
+    x = (torch.randn(2, rows, C, generator=g) + torch.randn(C, generator=g)).to(DT[kind]).cuda()
+    gamma, beta = torch.randn(C, generator=g).cuda() * 0.3 + 1, torch.randn(C, generator=g).cuda() * 0.3
+    grad = torch.randn(2, rows, C, generator=g).to(DT[kind]).cuda()
+    S = len(shapes)
+    if act == "relu":  # next to z = 0 a rounding decides the slope: no gradient comes in there
+        z, off = gn_reference(x, maps, gamma.expand(S, C), beta.expand(S, C), groups, 1e-5, "none")
+        near = z["out"].abs() <= off["out"]
+        assert bool(near.any())
+        grad = grad.masked_fill(near, 0)
+    out, stats = da.gn_forward(x, ss, ls, gamma, beta, groups, act=act)
+    grads = da.gn_backward(x, ss, ls, gamma, beta, stats, grad, groups, act=act)
+    val, tol = gn_reference(x, maps, gamma.expand(S, C), beta.expand(S, C), groups, 1e-5, act, grad)
+    for d in (val, tol):
+        d["grad_gamma"], d["grad_beta"] = d["grad_gamma"].sum(0), d["grad_beta"].sum(0)
+    check({"out": out, "grad_feat": grads[0], "grad_gamma": grads[1], "grad_beta": grads[2]}, val, tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["one group", "gaps", "scalar columns", "odd width", "most scalar channels"])
+def test_in_place_on_small_maps(name):
+    args, maps, grad, S = _inputs(name)
+    out, stats = da.gn_forward(*args[:6], act=args[6])
+    grads = da.gn_backward(*args[:5], stats, grad, args[5], act=args[6])
+    x, g = args[0].clone(), grad.clone()
+    da.gn_forward(x, *args[1:6], act=args[6], out=x)
+    da.gn_backward(*args[:5], stats, g, args[5], act=args[6], grad_feat=g)
+    assert torch.equal(x, out) and torch.equal(g, grads[0])
+
+
 @pytest.mark.gpu
 def test_mean_far_above_the_spread():
     args, maps, grad, S = _inputs("pyramid f32", mean=0.0)
