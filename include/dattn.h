@@ -17,6 +17,10 @@
  * gradient. What q holds for such a query, and k and v for a key that
  * key_lengths or key_mask excludes, is not used: NaN or infinity there
  * reaches no result.
+ * A bias of -infinity hides its bucket's keys in the same way, and so does one
+ * whose product with log2(e) is not finite, such as the lowest finite value: a
+ * query that sees no other key gets 0. Other biases and scores may have any
+ * size; a weight is good to 2^-24 times the size of its score.
  *
  * Without pos_k, key j is at position j; without pos_q, query i is at
  * key_lengths[b] - Lq + i (the queries are the last of the sequence), with

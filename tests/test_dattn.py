@@ -325,6 +325,19 @@ def test_infinite_bias(kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_lowest_finite_bias_hides_as_infinity_does(kind):
+    t, opt, grad = _case(Lq=150, Lk=150, kind=kind, buckets=8, reach=16, causal=True)
+    got = []
+    for hidden in (-float("inf"), torch.finfo(torch.float32).min):
+        u = {**t, "bias_table": t["bias_table"].clone()}
+        u["bias_table"][:2] = hidden  # the key at the query's own place and the one before it
+        got.append(_all(u, opt, grad))
+    assert all(torch.equal(got[0][n], got[1][n]) for n in got[0])
+    assert not got[0]["out"][:, :2].any() and bool(got[0]["out"][:, 2:].any(-1).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_empty_sizes(kind):
     for Lq, Lk in ((0, 5), (5, 0), (0, 0)):
