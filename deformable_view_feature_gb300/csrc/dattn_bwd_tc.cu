@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // g times the saved outputs: a row's pieces by neighbouring lanes.
         constexpr int P = VP / 8;
         const int piece = threadIdx.x % P;
-#pragma unroll 1
+#pragma unroll 4
         for (int r = threadIdx.x / P; r < kOwn; r += 256 / P) {
             const int dr = static_cast<int>(a.div_G.div(r)), of = r - dr * a.G;
             float d0 = 0.f, d1 = 0.f, sum = 0.f;  // the last of |g|
