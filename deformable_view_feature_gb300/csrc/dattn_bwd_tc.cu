@@ -3,7 +3,8 @@
 //
 // Two kernels, each of which forms the scores again from q, k and the saved
 // log-sums. The first owns 128 rows and walks over the keys in tiles of 64:
-// grad_q, and the d_m in full fp32 precision. The second owns 128 keys and
+// grad_q, and the d_m in full fp32 precision (it begins with those of the
+// saved outputs, which hold two words a value). The second owns 128 keys and
 // walks over the queries of every head that shares them in tiles of 64:
 // grad_k, grad_v and the bias table's gradient. Forming e and the scores twice
 // costs 28 D products per pair in place of 20 D, but no sum then crosses CTAs:
@@ -17,8 +18,8 @@
 // too, as far as it goes: q, g and s_m of the rows in the first kernel, s_m
 // in the second, and v and the weights unless Dv is above 64.
 //
-// At 2 x 8 heads of 8,192 tokens, causal, D = 64, Dv = 128: 478 us for the
-// first kernel and 743 for the second, 1,720 and 2,900 clocks a step for 768
+// At 2 x 8 heads of 8,192 tokens, causal, D = 64, Dv = 128: 476 us for the
+// first kernel and 737 for the second, 1,710 and 2,880 clocks a step for 768
 // and 1,024 of multiplication. All compute warps work on one step, so its
 // phases (scores to registers, exponentials, operands back) do not overlap each
 // other, only the products; tensor memory has no room for a second step.

@@ -15,11 +15,17 @@
 // in 16 bits as the operand of P v, and the two outputs. Steps of 128 keys
 // would use the tensor core better, but leave room for one step's scores
 // only: the softmax warps then waited 1500 of 3670 clocks for theirs.
-// A step now takes 1,450 clocks, 768 of them multiplication; the chain from
+// A step now takes 1,470 clocks, 768 of them multiplication; the chain from
 // scores to weights to the next products bounds it, not a unit (tensor pipe
-// 50 %, exponentials 27 % of their peak). 2 x 8 heads of 8,192 tokens, causal,
-// D = 64, Dv = 128: 366 us, 1.1 PFLOP/s. Eight caches of up to 32,768 keys:
-// 114 us, 3.7 TB/s.
+// 49 %, exponentials 26 % of their peak). 2 x 8 heads of 8,192 tokens, causal,
+// D = 64, Dv = 128: 363 us, 376 with what the backward pass needs, 1.1 PFLOP/s.
+// Eight caches of 18,432 to 32,768 keys: 114 us, 3.7 TB/s; each is split into
+// four, so that the longest's CTAs walk 128 steps where an even share of all
+// steps on 152 SMs would be 84.
+// The weights go into their product rounded to the inputs' type: with what the
+// rounding took as a second operand the outputs' errors were those of fp32
+// weights (bf16 0.0017 for 0.0025, 2-norm), but 8,192 tokens took 440 us and
+// the caches 140.
 // A thread raises its row's reference, and rescales the row's output, only
 // when a step's best score exceeds the one that the reference was made from by
 // more than 2^8. In fp16 the reference lies 2^7 below that score: weights of up

@@ -9,8 +9,8 @@
 // order. A CTA's threads form a grid of 4-channel columns
 // x rows of its tile, so every access is a full row segment and a thread keeps
 // its channels' parameters in registers; it sends its first loads before it
-// waits for anything. 6 x 89,760 rows of 256 fp32 channels: 238 us forward and
-// 443 backward, 4.6 and 3.7 TB/s of what has to be moved (three launches, each
+// waits for anything. 6 x 89,760 rows of 256 fp32 channels: 235 us forward and
+// 439 backward, 4.7 and 3.8 TB/s of what has to be moved (three launches, each
 // reading everything: 289 and 577).
 //
 // The wait for a map's sums cannot stall: a CTA that waits has a later ticket
