@@ -446,6 +446,34 @@ def test_offsets_past_32_bits(kind):
 
 
 @pytest.mark.gpu
+def test_fp16_scales_in_a_graph_on_another_stream_and_far_apart():
+    # fp16 takes a maximum over v and one over grad_out before its products.
+    t, opt, grad = _case(B=2, Lq=130, Lk=200, H=4, Hk=2, D=64, kind="f16", buckets=8, causal=True, mask=0.8, lengths=[200, 150])
+    static = {n: torch.zeros_like(x) if n in ("q", "k", "v") else x for n, x in t.items()}
+    sgrad = torch.zeros_like(grad)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        r = _all(static, opt, sgrad)
+    for size in (1.0, 2.0 ** -12, 2.0 ** 8):  # a maximum is not kept from one replay to the next
+        for n in ("q", "k", "v"):
+            static[n].copy_(t[n])
+        sgrad.copy_(grad * size)
+        graph.replay()
+        want = _all(t, opt, grad * size)
+        assert all(torch.equal(r[n], want[n]) for n in r)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = _all(t, opt, grad * size)
+    torch.cuda.current_stream().wait_stream(side)
+    gap = (1 << 31) + 64
+    for n in ("k", "v"):
+        store = torch.empty(gap + t[n][0].numel(), dtype=t[n].dtype, device="cuda")
+        t[n] = torch.as_strided(store, t[n].shape, (gap, *t[n].stride()[1:])).copy_(t[n])
+    far = _all(t, opt, grad * size)
+    assert all(torch.equal(other[n], want[n]) and torch.equal(far[n], want[n]) for n in want)
+
+
+@pytest.mark.gpu
 def test_tensors_off_the_gpu_are_refused():
     t, opt, _ = _case(Lq=4, Lk=4)
     with pytest.raises(ValueError, match="CUDA"):

@@ -10,8 +10,6 @@ from torch._subclasses.fake_tensor import FakeTensorMode
 
 import deformable_view_feature_gb300 as da
 
-FAKE = FakeTensorMode()
-
 
 @pytest.fixture(scope="module", autouse=True)
 def lib():
@@ -74,43 +72,40 @@ def test_the_status_of_waits_is_read_on_the_streams_device(cuda, monkeypatch):
     assert [s[0] for s in seen] == [101, 101, 100, 100] and seen[0][1] == [("enter", 1)]
 
 
-def _cases():
+NORM = dict(feat=(1, 16, 8), gamma=(8,), beta=(8,), out=(1, 16, 8))
+NORM_BACK = dict(feat=(1, 16, 8), gamma=(8,), beta=(8,), stats=(1, 1, 1, 2, 2), grad_out=(1, 16, 8), grad_feat=(1, 16, 8))
+ATTENTION = dict(q=(1, 3, 2, 2, 8), k=(1, 5, 2, 2, 8), v=(1, 5, 2, 16), lam=(2,), bias_table=(4, 2), bucket_map=(5,),
+                 pos_q=(1, 3), pos_k=(1, 5), key_mask=(1, 5), key_lengths=(1,), out=(1, 3, 2, 16))
+ATTENTION_BACK = {**ATTENTION, "out1": (1, 3, 2, 16), "lse": (1, 2, 2, 3), "grad_out": (1, 3, 2, 16)}
+KINDS = dict(bucket_map=torch.int32, pos_q=torch.int32, pos_k=torch.int32, key_mask=torch.bool, key_lengths=torch.int32)
+
+
+def _gn_forward(ss, ls, a):
+    return da.gn_forward(a["feat"], ss, ls, a["gamma"], a["beta"], 2, out=a["out"])
+
+
+def _gn_backward(ss, ls, a):
+    return da.gn_backward(a["feat"], ss, ls, a["gamma"], a["beta"], a["stats"], a["grad_out"], 2, grad_feat=a["grad_feat"])
+
+
+def _dattn_forward(ss, ls, a):
+    return da.dattn_forward(**a)
+
+
+def _dattn_backward(ss, ls, a):
+    return da.dattn_backward(saved=(a.pop("out1"), a.pop("lse")), **a)
+
+
+CASES = [(call, shapes, other) for call, shapes in ((_gn_forward, NORM), (_gn_backward, NORM_BACK), (_dattn_forward, ATTENTION),
+                                                    (_dattn_backward, ATTENTION_BACK)) for other in list(shapes)[1:]]
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="with a GPU there, tensors without storage need its devices")
+@pytest.mark.parametrize("call,shapes,other", CASES, ids=[f"{c[0].__name__[1:]}-{c[2]}" for c in CASES])
+def test_tensors_of_two_devices_are_refused(cuda, call, shapes, other):
     ss, ls = torch.tensor([[[4, 4]]], dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32)
-    with FAKE, warnings.catch_warnings():
-        def new(*shape, kind=torch.float32, on=1):
-            return torch.empty(*shape, dtype=kind, device=f"cuda:{on}")
-
-        norm = dict(feat=(1, 16, 8), gamma=(8,), beta=(8,), out=(1, 16, 8))
-        back = dict(feat=(1, 16, 8), gamma=(8,), beta=(8,), stats=(1, 1, 1, 2, 2), grad_out=(1, 16, 8), grad_feat=(1, 16, 8))
-        att = dict(q=((1, 3, 2, 2, 8),), k=((1, 5, 2, 2, 8),), v=((1, 5, 2, 16),), lam=((2,),), bias_table=((4, 2),),
-                   bucket_map=((5,), torch.int32), pos_q=((1, 3), torch.int32), pos_k=((1, 5), torch.int32),
-                   key_mask=((1, 5), torch.bool), key_lengths=((1,), torch.int32), out=((1, 3, 2, 16),))
-        for other in norm:
-            if other != "feat":
-                a = {n: new(*s, on=0 if n == other else 1) for n, s in norm.items()}
-                yield f"gn_forward {other}", lambda a=a: da.gn_forward(a["feat"], ss, ls, a["gamma"], a["beta"], 2, out=a["out"])
-        for other in back:
-            if other != "feat":
-                a = {n: new(*s, on=0 if n == other else 1) for n, s in back.items()}
-                yield f"gn_backward {other}", lambda a=a: da.gn_backward(a["feat"], ss, ls, a["gamma"], a["beta"], a["stats"],
-                                                                         a["grad_out"], 2, grad_feat=a["grad_feat"])
-        for other in att:
-            if other != "q":
-                a = {n: new(*s[0], kind=s[1] if len(s) > 1 else torch.float32, on=0 if n == other else 1) for n, s in att.items()}
-                yield f"dattn_forward {other}", lambda a=a: da.dattn_forward(**a)
-        a = {n: new(*s[0], kind=s[1] if len(s) > 1 else torch.float32) for n, s in att.items()}
-        out, near, far = a.pop("out"), new(1, 2, 2, 3), new(1, 3, 2, 16, on=0)
-        yield "dattn_backward grad_out", lambda: da.dattn_backward(out=out, saved=(out, near), grad_out=far, **a)
-        yield "dattn_backward out", lambda: da.dattn_backward(out=far, saved=(out, near), grad_out=out, **a)
-        yield "dattn_backward saved", lambda: da.dattn_backward(out=out, saved=(far, near), grad_out=out, **a)
-
-
-CASES = dict(_cases())
-
-
-@pytest.mark.parametrize("name", list(CASES))
-def test_tensors_of_two_devices_are_refused(cuda, name):
-    with FAKE, warnings.catch_warnings():
+    with FakeTensorMode(), warnings.catch_warnings():
         warnings.simplefilter("ignore")
+        a = {n: torch.empty(s, dtype=KINDS.get(n, torch.float32), device="cuda:0" if n == other else "cuda:1") for n, s in shapes.items()}
         with pytest.raises(ValueError, match="one CUDA device"):
-            CASES[name]()
+            call(ss, ls, a)
