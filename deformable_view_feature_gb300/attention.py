@@ -223,15 +223,25 @@ def dattn_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch
 class DifferentialAttentionFunction(torch.autograd.Function):
     """Autograd wrapper: apply(q, k, v, lam, bias_table, bucket_map, pos_q,
     pos_k, key_mask, key_lengths, causal, scale) -> out, with gradients for q,
-    k, v, lam and bias_table. It has no second derivative: asking for one
-    raises RuntimeError."""
+    k, v, lam and bias_table. Without a gradient to come (torch.no_grad, or no
+    argument that requires one) nothing is kept for it. It has no second
+    derivative: asking for one raises RuntimeError."""
+
+    @classmethod
+    def apply(cls, q, k, v, lam, bias_table=None, *rest):
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, v, lam, bias_table)):
+            return super().apply(q, k, v, lam, bias_table, *rest)
+        return dattn_forward(*cls._contiguous(q, k, v, lam, bias_table), *rest)  # no backward pass: nothing kept for one
+
+    @staticmethod
+    def _contiguous(q, k, v, lam, bias_table):
+        q, k, v = (t if t.shape[-1] == 1 or t.stride(-1) == 1 else t.contiguous() for t in (q, k, v))
+        return q, k, v, lam.contiguous(), None if bias_table is None else bias_table.contiguous()
 
     @staticmethod
     def forward(ctx, q, k, v, lam, bias_table=None, bucket_map=None, pos_q=None, pos_k=None, key_mask=None,
                 key_lengths=None, causal=False, scale=None):
-        q, k, v = (t if t.shape[-1] == 1 or t.stride(-1) == 1 else t.contiguous() for t in (q, k, v))
-        lam = lam.contiguous()
-        bias_table = None if bias_table is None else bias_table.contiguous()
+        q, k, v, lam, bias_table = DifferentialAttentionFunction._contiguous(q, k, v, lam, bias_table)
         opt = dict(bias_table=bias_table, bucket_map=bucket_map, pos_q=pos_q, pos_k=pos_k, key_mask=key_mask,
                    key_lengths=key_lengths, causal=causal, scale=scale)
         out, saved = dattn_forward(q, k, v, lam, **opt, keep_for_backward=True)

@@ -30,6 +30,23 @@ def calls(monkeypatch):
     monkeypatch.setattr(attention, "dattn_backward", dattn_backward)
 
 
+@pytest.mark.parametrize("enabled,requires,keeps", [(True, True, True), (True, False, False), (False, True, False)])
+def test_attention_keeps_nothing_without_a_backward_pass(calls, monkeypatch, enabled, requires, keeps):
+    asked, forward = [], attention.dattn_forward
+
+    def recorded(*args, keep_for_backward=False, **opt):
+        asked.append(keep_for_backward)
+        out, saved = forward(*args, **opt)
+        return (out, saved) if keep_for_backward else out
+
+    monkeypatch.setattr(attention, "dattn_forward", recorded)
+    x = torch.randn(1, 4, 2, 2, 3, requires_grad=requires)
+    with torch.set_grad_enabled(enabled):
+        y = _attention(x)
+    assert asked == [keeps] and y.requires_grad == keeps
+    assert torch.equal(y.detach(), (2 * x[..., 0, :] + x[..., 0, :]).detach())
+
+
 def _norm(x):
     ss, ls = torch.tensor([[[2, 2]]], dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32)
     return da.GroupNormActFunction.apply(x, ss, ls, torch.full((3,), 2.0), torch.zeros(3), 1, 1e-5, "none")
