@@ -41,10 +41,10 @@
  * the weights P, and s_m in the backward pass, are rounded to the inputs'
  * type as operands of the second products, as the tensor cores require.
  * grad_lam and grad_table are formed from the unrounded values.
- * In fp16 both have a power of two of their own, by bounds of grad_out and v,
- * that brings them into the type's range and is taken out of the sums: only
- * the gradients themselves, as values of that type, are to be scaled as fp16
- * training does.
+ * In fp16 these operands have powers of two of their own, by bounds of lam,
+ * grad_out and v, that bring them into the type's range and are taken out of
+ * the sums: only the gradients themselves, as values of that type, are to be
+ * scaled as fp16 training does.
  * Sums are taken in a fixed order: results do not vary from run to run.
  * Positions lie in (-2^30, 2^30). Device-side indices are bounded in every
  * build: key_lengths is clamped to [0, Lk] and bucket_map to the table.
