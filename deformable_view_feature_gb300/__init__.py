@@ -30,7 +30,8 @@ __all__ = ["da_forward", "da_backward", "da_forward_fused", "da_backward_fused",
            "da_backward_projected", "warpaffine_u8", "warpaffine_preprocess", "backward_workspace_size",
            "backward_path", "da_backward_bin", "DeformableAggregationFunction", "HostPipeline", "DaError", "library_path", "load_library", "da_version",
            "gn_forward", "gn_backward", "GroupNormActFunction", "dattn_forward", "dattn_backward", "dattn_path",
-           "relative_buckets", "DifferentialAttentionFunction", "waits_gave_up"]
+           "relative_buckets", "DifferentialAttentionFunction", "qkr_forward", "qkr_backward", "rotary_frequencies",
+           "QkRotaryFunction", "paged_append", "paged_attention", "waits_gave_up"]
 
 DA_F32, DA_BF16, DA_F16 = 0, 1, 2
 _STATUS = {0: "DA_OK", 1: "DA_ERR_NULL", 2: "DA_ERR_SHAPE", 3: "DA_ERR_ALIGN",
@@ -120,6 +121,13 @@ def load_library():
               lib.dattn_backward):
         f.restype = ctypes.c_int
     lib.dattn_path.restype = ctypes.c_int32
+    lib.qkr_forward.argtypes = [vp] * 4
+    lib.qkr_workspace_size.argtypes = lib.pg_workspace_size.argtypes = [vp, psize]
+    lib.qkr_backward.argtypes = [vp] * 8 + [ctypes.c_size_t, vp]
+    lib.pg_append.argtypes = [vp, vp, vp, ctypes.c_int32, vp, vp, vp]
+    lib.pg_attention.argtypes = [vp] * 3 + [ctypes.c_size_t, vp]
+    for f in (lib.qkr_forward, lib.qkr_workspace_size, lib.qkr_backward, lib.pg_append, lib.pg_workspace_size, lib.pg_attention):
+        f.restype = ctypes.c_int
     lib.da_gn_wait_tries.argtypes = [ctypes.c_int32]
     lib.da_gn_wait_tries.restype = ctypes.c_int32
     lib.da_status_string.argtypes = [ctypes.c_int]
@@ -687,3 +695,5 @@ class DeformableAggregationFunction(torch.autograd.Function):
 from .attention import (DifferentialAttentionFunction, dattn_backward, dattn_forward, dattn_path,  # noqa: E402
                         relative_buckets)
 from .norm import GroupNormActFunction, gn_backward, gn_forward  # noqa: E402
+from .rotary import QkRotaryFunction, qkr_backward, qkr_forward, rotary_frequencies  # noqa: E402
+from .paged import paged_append, paged_attention  # noqa: E402

@@ -189,6 +189,41 @@ __device__ void load_keys(const DattnArgs &a, const void *base, int64_t at, int6
     }
 }
 
+// The same from a paged cache, whose rows lie at `at` [count].
+template <typename T, int W>
+__device__ void load_paged(const DattnArgs &a, const void *base, int64_t first, int64_t s_page, int64_t s_place, int count,
+                           int width, const int *seen, const int2 *at, float *dst)
+{
+#pragma unroll 4
+    for (int i = threadIdx.x; i < count * (W / 4); i += kThreadsG) {
+        const int row = i / (W / 4), d = (i - row * (W / 4)) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (seen[row]) v = load4(static_cast<const T *>(base) + first + at[row].x * s_page + at[row].y * s_place, d, width, a.wide);
+        *reinterpret_cast<float4 *>(dst + row * (W + 4) + d) = v;
+    }
+}
+
+// Positions, use and places of the keys j0 .. of a paged cache.
+__device__ __forceinline__ void load_paged_info(const DattnArgs &a, int b, int end, int j0, int count, int *pos, int *seen, int2 *at)
+{
+    for (int i = threadIdx.x; i < count; i += kThreadsG) {
+        const int j = j0 + i;
+        const bool in = j < end;
+        const int64_t of = static_cast<int64_t>(b) * a.Lk + j;
+        at[i] = make_int2(-1, 0);
+        if (in) at[i].x = paged_page(a, b, j, at[i].y);
+        seen[i] = at[i].x >= 0 && (!a.mask || a.mask[of]);
+        pos[i] = in && a.pos_k ? a.pos_k[of] : j;
+    }
+}
+
+// Whether new token l sees key j, below the sequence's length, by the tree;
+// `old`: the keys before the new ones.
+__device__ __forceinline__ bool tree_sees(const DattnArgs &a, int b, int l, int j, int old)
+{
+    return j < old || a.pg.tree[(static_cast<int64_t>(b) * a.Lq + l) * a.Lq + j - old];
+}
+
 // Positions and use of the keys j0 .. j0 + count - 1.
 __device__ __forceinline__ void load_key_info(const DattnArgs &a, int b, int end, int j0, int count, int *pos, int *seen)
 {
@@ -211,7 +246,7 @@ template <typename T, int DP, int QT> struct FwdTile {
                          info = p + 2 * QT * (KT + 4), floats = info + 2 * KT;
 };
 
-template <typename T, int DP, int QT>
+template <typename T, int DP, int QT, bool PAGED>
 __global__ void __launch_bounds__(kThreadsG, DP == 32 || (DP == 64 && QT == 16) ? 2 : 1) dattn_fwd_kernel(const __grid_constant__ DattnArgs a)
 {
     using F = FwdTile<T, DP, QT>;
@@ -224,6 +259,8 @@ __global__ void __launch_bounds__(kThreadsG, DP == 32 || (DP == 64 && QT == 16) 
     const int tile = blockIdx.x / a.splits, split = blockIdx.x - tile * a.splits;
     const int n = blockIdx.y, b = blockIdx.z, r0 = tile * QT;
     const int len = dattn_length(a, b);
+    __shared__ int2 at[PAGED ? KT : 1];  // pages and places of the keys
+    const int count = PAGED ? paged_count(a, b) : a.Lq, old = len - count;  // queries, keys before them
 
     load_bias(a, n, bt);
     for (int m = 0; m < 2; ++m)
@@ -233,7 +270,7 @@ __global__ void __launch_bounds__(kThreadsG, DP == 32 || (DP == 64 && QT == 16) 
     float4 acc[2][M][NC];
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-        ri[i] = row_info(a, b, len, r0 + ty + 16 * i);
+        ri[i] = row_info(a, b, PAGED ? old + a.Lq : len, r0 + ty + 16 * i);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             mx[m][i] = -INFINITY;
@@ -243,24 +280,42 @@ __global__ void __launch_bounds__(kThreadsG, DP == 32 || (DP == 64 && QT == 16) 
         }
     }
     int j0 = split * a.keys_per_split, end = min(len, j0 + a.keys_per_split);
+    if constexpr (PAGED) {
+        // Shares of the sequence's own keys: the table is as wide as the longest's.
+        const int per = ((len + a.splits - 1) / a.splits + KT - 1) / KT * KT;
+        j0 = split * per;
+        end = r0 < count * a.G ? min(len, j0 + per) : 0;
+    }
     // Keys after the last row's query end the walk where positions are indices.
     if (a.causal && !a.pos_q && !a.pos_k) {
         const int last = static_cast<int>(a.div_G.div(min(r0 + QT, a.rows) - 1));
-        end = min(end, len - a.Lq + last + 1);
+        end = min(end, (PAGED ? old : len - a.Lq) + last + 1);
     }
     for (; j0 < end; j0 += KT) {
         __syncthreads();
-        load_key_info(a, b, end, j0, KT, kpos, kseen);
+        if constexpr (PAGED) load_paged_info(a, b, end, j0, KT, kpos, kseen, at);
+        else load_key_info(a, b, end, j0, KT, kpos, kseen);
         __syncthreads();
-        for (int m = 0; m < 2; ++m)
-            load_keys<T, DP>(a, a.k, b * a.ks[0] + n * a.ks[2] + m * a.ks[3], a.ks[1], j0, KT, a.D, kseen, sk + m * KT * (DP + 4));
-        load_keys<T, F::WV>(a, a.v, b * a.vs[0] + n * a.vs[2], a.vs[1], j0, KT, a.Dv, kseen, sv);
+        if constexpr (PAGED) {
+            for (int m = 0; m < 2; ++m)
+                load_paged<T, DP>(a, a.k, n * a.ks[2] + m * a.ks[3], a.ks[0], a.ks[1], KT, a.D, kseen, at, sk + m * KT * (DP + 4));
+            load_paged<T, F::WV>(a, a.v, n * a.vs[2], a.vs[0], a.vs[1], KT, a.Dv, kseen, at, sv);
+        } else {
+            for (int m = 0; m < 2; ++m)
+                load_keys<T, DP>(a, a.k, b * a.ks[0] + n * a.ks[2] + m * a.ks[3], a.ks[1], j0, KT, a.D, kseen, sk + m * KT * (DP + 4));
+            load_keys<T, F::WV>(a, a.v, b * a.vs[0] + n * a.vs[2], a.vs[1], j0, KT, a.Dv, kseen, sv);
+        }
         __syncthreads();
         float bias[M][N];
 #pragma unroll
         for (int i = 0; i < M; ++i)
 #pragma unroll
-            for (int j = 0; j < N; ++j) bias[i][j] = bias_of(a, bt, kseen[tx + 16 * j], kpos[tx + 16 * j] - ri[i].pos, ri[i].g);
+            for (int j = 0; j < N; ++j) {
+                int seen = kseen[tx + 16 * j];
+                if constexpr (PAGED)
+                    if (ri[i].l >= count || (a.pg.tree && seen && ri[i].l >= 0 && !tree_sees(a, b, ri[i].l, j0 + tx + 16 * j, old))) seen = 0;
+                bias[i][j] = bias_of(a, bt, seen, kpos[tx + 16 * j] - ri[i].pos, ri[i].g);
+            }
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             float t[M][N];
@@ -832,12 +887,12 @@ template <typename K> cudaError_t launch(K kernel, dim3 grid, size_t floats, con
     return cudaGetLastError();
 }
 
-template <typename T, int DP> cudaError_t forward_width(const DattnArgs &a, cudaStream_t st)
+template <typename T, int DP, bool PAGED> cudaError_t forward_width(const DattnArgs &a, cudaStream_t st)
 {
     const int qt = dattn_general_row_tile(a);
     const dim3 grid(static_cast<unsigned>((a.rows + qt - 1) / qt * a.splits), a.Hkv, a.B);
-    if (qt == 16) return launch(dattn_fwd_kernel<T, DP, 16>, grid, FwdTile<T, DP, 16>::floats + table_floats(a), a, st);
-    return launch(dattn_fwd_kernel<T, DP, 64>, grid, FwdTile<T, DP, 64>::floats + table_floats(a), a, st);
+    if (qt == 16) return launch(dattn_fwd_kernel<T, DP, 16, PAGED>, grid, FwdTile<T, DP, 16>::floats + table_floats(a), a, st);
+    return launch(dattn_fwd_kernel<T, DP, 64, PAGED>, grid, FwdTile<T, DP, 64>::floats + table_floats(a), a, st);
 }
 
 template <typename T, int DP> cudaError_t backward_width(const DattnArgs &a, cudaStream_t st)
@@ -872,9 +927,18 @@ template <typename T, int DP> cudaError_t backward_width(const DattnArgs &a, cud
 template <typename T> cudaError_t any_width(const DattnArgs &a, bool backward, cudaStream_t st)
 {
     switch (padded_width(a)) {
-    case 32: return backward ? backward_width<T, 32>(a, st) : forward_width<T, 32>(a, st);
-    case 64: return backward ? backward_width<T, 64>(a, st) : forward_width<T, 64>(a, st);
-    default: return backward ? backward_width<T, 128>(a, st) : forward_width<T, 128>(a, st);
+    case 32: return backward ? backward_width<T, 32>(a, st) : forward_width<T, 32, false>(a, st);
+    case 64: return backward ? backward_width<T, 64>(a, st) : forward_width<T, 64, false>(a, st);
+    default: return backward ? backward_width<T, 128>(a, st) : forward_width<T, 128, false>(a, st);
+    }
+}
+
+template <typename T> cudaError_t paged_width(const DattnArgs &a, cudaStream_t st)
+{
+    switch (padded_width(a)) {
+    case 32: return forward_width<T, 32, true>(a, st);
+    case 64: return forward_width<T, 64, true>(a, st);
+    default: return forward_width<T, 128, true>(a, st);
     }
 }
 
@@ -894,6 +958,15 @@ int dattn_general_row_tile(const DattnArgs &a) { return a.rows <= 16 ? 16 : 64; 
 int dattn_general_tile(const DattnArgs &a) { return padded_width(a) <= 64 ? 64 : 32; }
 
 cudaError_t dattn_forward_general(const DattnArgs &a, int dtype, cudaStream_t st) { return any_type(a, dtype, false, st); }
+
+cudaError_t paged_forward_general(const DattnArgs &a, int dtype, cudaStream_t st)
+{
+    switch (dtype) {
+    case DA_F32: return paged_width<float>(a, st);
+    case DA_BF16: return paged_width<__nv_bfloat16>(a, st);
+    default: return paged_width<__half>(a, st);
+    }
+}
 
 cudaError_t dattn_backward_general(const DattnArgs &a, int dtype, cudaStream_t st) { return any_type(a, dtype, true, st); }
 

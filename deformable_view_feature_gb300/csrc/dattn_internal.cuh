@@ -14,7 +14,18 @@ namespace da {
 // key head n being query r / G of head n*G + r % G. One token of a serving
 // batch thus still fills a tile with its G heads, and keys are read once for
 // all of them.
+// Where the keys of a paged cache lie (paged.h): then DattnArgs' k and v are
+// the cache, their first two strides those of pages and places, Lk the places
+// of a sequence, and the queries' rows Lq those of padded new tokens.
+struct PagedArgs {
+    const int32_t *table, *counts;
+    const uint8_t *tree;
+    int32_t table_pages, page_size, num_pages;
+    FastDiv div_page;
+};
+
 struct DattnArgs {
+    PagedArgs pg;
     const void *q, *k, *v;
     int64_t qs[4], ks[4], vs[3];
     const float *lam, *table;
@@ -55,6 +66,21 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// New tokens of a sequence.
+__device__ __forceinline__ int paged_count(const DattnArgs &a, int b)
+{
+    return a.pg.counts ? min(max(a.pg.counts[b], 0), a.Lq) : a.Lq;
+}
+
+// The page of place j, or -1 where it is not in the cache.
+__device__ __forceinline__ int paged_page(const DattnArgs &a, int b, int j, int &place)
+{
+    const int n = static_cast<int>(a.pg.div_page.div(static_cast<uint32_t>(j)));
+    const int page = a.pg.table[static_cast<int64_t>(b) * a.pg.table_pages + n];
+    place = j - n * a.pg.page_size;
+    return page >= 0 && page < a.pg.num_pages ? page : -1;
 }
 
 __device__ __forceinline__ int dattn_length(const DattnArgs &a, int b)
@@ -111,6 +137,7 @@ da_status dattn_forward_tensor(const DattnArgs &a, int dtype, cudaStream_t st);
 da_status dattn_backward_tensor(const DattnArgs &a, int dtype, cudaStream_t st);
 uint32_t *dattn_gave_up_word();           // of the forward kernels
 uint32_t *dattn_gave_up_backward_word();  // of the backward kernels
+cudaError_t paged_forward_general(const DattnArgs &a, int dtype, cudaStream_t st);
 cudaError_t dattn_forward_general(const DattnArgs &a, int dtype, cudaStream_t st);
 cudaError_t dattn_backward_general(const DattnArgs &a, int dtype, cudaStream_t st);
 cudaError_t dattn_merge(const DattnArgs &a, int dtype, cudaStream_t st);
