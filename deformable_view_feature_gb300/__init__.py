@@ -31,7 +31,7 @@ __all__ = ["da_forward", "da_backward", "da_forward_fused", "da_backward_fused",
            "backward_path", "da_backward_bin", "DeformableAggregationFunction", "HostPipeline", "DaError", "library_path", "load_library", "da_version",
            "gn_forward", "gn_backward", "GroupNormActFunction", "dattn_forward", "dattn_backward", "dattn_path",
            "relative_buckets", "DifferentialAttentionFunction", "qkr_forward", "qkr_backward", "rotary_frequencies",
-           "QkRotaryFunction", "paged_append", "paged_attention", "waits_gave_up"]
+           "QkRotaryFunction", "paged_append", "paged_attention", "paged_path", "waits_gave_up"]
 
 DA_F32, DA_BF16, DA_F16 = 0, 1, 2
 _STATUS = {0: "DA_OK", 1: "DA_ERR_NULL", 2: "DA_ERR_SHAPE", 3: "DA_ERR_ALIGN",
@@ -124,6 +124,8 @@ def load_library():
     lib.qkr_forward.argtypes = [vp] * 4
     lib.qkr_workspace_size.argtypes = lib.pg_workspace_size.argtypes = [vp, psize]
     lib.qkr_backward.argtypes = [vp] * 8 + [ctypes.c_size_t, vp]
+    lib.pg_path.argtypes = [vp]
+    lib.pg_path.restype = ctypes.c_int32
     lib.pg_append.argtypes = [vp, vp, vp, ctypes.c_int32, vp, vp, vp]
     lib.pg_attention.argtypes = [vp] * 3 + [ctypes.c_size_t, vp]
     for f in (lib.qkr_forward, lib.qkr_workspace_size, lib.qkr_backward, lib.pg_append, lib.pg_workspace_size, lib.pg_attention):
@@ -159,7 +161,7 @@ def _check(status: int):
 
 
 def waits_gave_up(stream=None) -> bool:
-    """Whether a bounded wait inside a gn_* or dattn_* kernel has run out since
+    """Whether a bounded wait inside a gn_*, dattn_* or pg_* kernel has run out since
     the last call (gn_device_status, dattn_device_status): results since then
     may hold NaN. None does in a sound run. Waits for the stream (the current
     one by default); each device has its own status, that of the stream's is read."""
@@ -696,4 +698,4 @@ from .attention import (DifferentialAttentionFunction, dattn_backward, dattn_for
                         relative_buckets)
 from .norm import GroupNormActFunction, gn_backward, gn_forward  # noqa: E402
 from .rotary import QkRotaryFunction, qkr_backward, qkr_forward, rotary_frequencies  # noqa: E402
-from .paged import paged_append, paged_attention  # noqa: E402
+from .paged import paged_append, paged_attention, paged_path  # noqa: E402

@@ -307,15 +307,16 @@ da_status dattn_device_status(uint32_t *gave_up, da_stream_t stream)
 {
     if (!gave_up) return da::fail(DA_ERR_NULL, "gave_up is NULL");
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    uint32_t *words[2] = {da::dattn_gave_up_word(), da::dattn_gave_up_backward_word()}, got[2] = {0, 0};
+    uint32_t *words[4] = {da::dattn_gave_up_word(), da::dattn_gave_up_backward_word(), da::paged_gave_up_bf16(), da::paged_gave_up_f16()};
+    uint32_t got[4] = {0, 0, 0, 0};
     cudaError_t e = cudaSuccess;
-    for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+    for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
         if (!words[i]) return da::cuda_fail(cudaGetLastError(), "address of a status word");
         e = cudaMemcpyAsync(&got[i], words[i], sizeof got[i], cudaMemcpyDeviceToHost, cs);
         if (e == cudaSuccess) e = cudaMemsetAsync(words[i], 0, sizeof got[i], cs);
     }
     if (e == cudaSuccess) e = cudaStreamSynchronize(cs);
-    *gave_up = got[0] | got[1];
+    *gave_up = got[0] | got[1] | got[2] | got[3];
     return e == cudaSuccess ? DA_OK : da::cuda_fail(e, "status word");
 }
 

@@ -137,6 +137,8 @@ da_status dattn_forward_tensor(const DattnArgs &a, int dtype, cudaStream_t st);
 da_status dattn_backward_tensor(const DattnArgs &a, int dtype, cudaStream_t st);
 uint32_t *dattn_gave_up_word();           // of the forward kernels
 uint32_t *dattn_gave_up_backward_word();  // of the backward kernels
+uint32_t *paged_gave_up_bf16();           // of the attention over a paged cache
+uint32_t *paged_gave_up_f16();
 cudaError_t paged_forward_general(const DattnArgs &a, int dtype, cudaStream_t st);
 cudaError_t dattn_forward_general(const DattnArgs &a, int dtype, cudaStream_t st);
 cudaError_t dattn_backward_general(const DattnArgs &a, int dtype, cudaStream_t st);

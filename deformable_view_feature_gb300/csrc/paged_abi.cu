@@ -2,7 +2,7 @@
 // the plan (kernels, workspace) and launches.
 #include <cmath>
 
-#include "dattn_internal.cuh"
+#include "paged_internal.cuh"
 #include "qkr_internal.cuh"
 
 namespace da {
@@ -24,9 +24,31 @@ da_status check_cache(const pg_cache &c, int batch, int elem)
     return DA_OK;
 }
 
+// The tensor-core kernel's rule. 16-bit types; widths that its tiles hold and
+// whose rows are multiples of 16 bytes; a group of heads within a tile; pages of
+// whole groups of eight places, by which shared memory is swizzled; a bias that
+// it has room for; and what a TMA box needs: 16-byte aligned addresses and
+// strides, none of them zero.
+bool tensor_serves(const pg_problem &d)
+{
+    const pg_cache &c = d.cache;
+    if (d.dtype != DA_BF16 && d.dtype != DA_F16) return false;
+    if (d.width % 8 || d.value_width % 8 || d.width > 64 || d.value_width > 128 || d.num_heads / d.num_kv_heads > 64) return false;
+    if (c.page_size % 8 || c.num_pages < 1 || c.table_pages < 1 || d.batch < 1 || d.num_tokens < 1) return false;
+    if (d.num_buckets > 0 && paged_bias_bytes(d.num_buckets, d.num_heads, d.reach) > kPgBias) return false;
+    if (!aligned(d.q, 16) || !aligned(c.k, 16) || !aligned(c.v, 16)) return false;
+    const int nq[4] = {d.batch, d.num_tokens, d.num_heads, 2}, nk[4] = {c.num_pages, c.page_size, d.num_kv_heads, 2};
+    auto fits = [](int64_t stride, int size) { return size == 1 || (stride > 0 && stride % 8 == 0 && stride < (int64_t{1} << 38)); };
+    for (int i = 0; i < 4; ++i)
+        if (!fits(d.q_stride[i], nq[i]) || !fits(c.k_stride[i], nk[i]) || (i < 3 && !fits(c.v_stride[i], nk[i]))) return false;
+    return true;
+}
+
 struct PagedPlan {
     DattnArgs a;
-    size_t part_o, part_ml, total;
+    PagedTcArgs tc;
+    size_t part_o, part_ml, slots, total;
+    bool tensor;
 };
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -97,9 +119,28 @@ da_status paged_plan(const pg_problem *pr, PagedPlan &p)
     a.scale_log2 = static_cast<float>(static_cast<double>(d.scale) * 1.4426950408889634);
     a.wide = d.dtype == DA_F32 && d.width % 4 == 0 && d.value_width % 4 == 0 && aligned(d.q, 16) && aligned(c.k, 16) && aligned(c.v, 16);
     for (int i = 0; i < 4; ++i) a.wide = a.wide && a.qs[i] % 4 == 0 && a.ks[i] % 4 == 0 && (i == 3 || a.vs[i] % 4 == 0);
-    p.part_o = p.part_ml = p.total = 0;
+    p.part_o = p.part_ml = p.slots = p.total = 0;
     a.splits = 1;
     a.keys_per_split = a.Lk > 0 ? a.Lk : 1;
+    p.tensor = tensor_serves(d);
+    if (p.tensor) {
+        // Tiles of 64 rows for many tokens; fewer columns cost less where there are few.
+        PagedTcArgs &t = p.tc;
+        t.RT = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+        t.LP = t.RT / G;
+        t.row_tiles = (d.num_tokens + t.LP - 1) / t.LP;
+        t.box = 8;
+        while (t.box < 128 && c.page_size % (2 * t.box) == 0) t.box *= 2;
+        const int64_t tiles = static_cast<int64_t>(d.batch) * d.num_kv_heads * t.row_tiles, steps = tiles * ((a.Lk + 127) / 128);
+        if (steps / 152 >= INT32_MAX / 2) return fail(DA_ERR_UNSUPPORTED, "too many rows and keys");
+        t.ctas = static_cast<int32_t>(steps < 152 ? steps : 152);  // one fills an SM
+        p.total += round256(sizeof(float) * 2 * t.ctas * t.RT * 2 * a.Dv);
+        p.part_ml = p.total;
+        p.total += round256(sizeof(float) * 2 * t.ctas * t.RT * 4);
+        p.slots = p.total;
+        p.total += round256(sizeof(int32_t) * 4 * t.ctas);
+        return DA_OK;
+    }
     // CTAs to share a tile where tiles alone leave SMs without work, two of
     // them on each, each with 64 keys or more of a full table.
     const int64_t bn = static_cast<int64_t>(a.B) * a.Hkv, qt = dattn_general_row_tile(a), tiles = bn * ((rows + qt - 1) / qt);
@@ -168,6 +209,12 @@ da_status pg_append(const qkr_problem *p, const void *v, const int64_t *v_stride
     return da::qkr_launch_forward(a, p->dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
+int32_t pg_path(const pg_problem *p)
+{
+    da::PagedPlan pl{};
+    return da::paged_plan(p, pl) == DA_OK ? static_cast<int32_t>(pl.tensor) : -1;
+}
+
 da_status pg_workspace_size(const pg_problem *p, size_t *bytes)
 {
     if (!bytes) return da::fail(DA_ERR_NULL, "bytes is NULL");
@@ -202,6 +249,11 @@ da_status pg_attention(const pg_problem *p, void *out, void *workspace, size_t w
     a.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + pl.part_o);
     a.part_ml = reinterpret_cast<float *>(static_cast<char *>(workspace) + pl.part_ml);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (pl.tensor) {
+        pl.tc.slots = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + pl.slots);
+        pl.tc.d = a;
+        return p->dtype == DA_BF16 ? da::paged_forward_bf16(pl.tc, cs) : da::paged_forward_f16(pl.tc, cs);
+    }
     cudaError_t e = da::paged_forward_general(a, p->dtype, cs);
     if (e == cudaSuccess && a.splits > 1) e = da::dattn_merge(a, p->dtype, cs);
     return e == cudaSuccess ? DA_OK : da::cuda_fail(e, "paged attention launch");

@@ -24,7 +24,7 @@ from . import _check, _dptr, _on_stream, load_library
 from . import rotary as _rotary
 from .attention import _DTYPES, _small, _strided
 
-__all__ = ["paged_append", "paged_attention"]
+__all__ = ["paged_append", "paged_attention", "paged_path"]
 
 
 class PgCache(ctypes.Structure):
@@ -172,3 +172,15 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         ws = torch.empty(n.value, dtype=torch.uint8, device=q.device) if n.value else None
         _check(lib.pg_attention(p, to, _dptr(ws), n.value, handle))
     return out
+
+
+def paged_path(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, lam: torch.Tensor, page_table: torch.Tensor,
+               key_lengths: torch.Tensor, counts=None, tree=None, bias_table=None, bucket_map=None, pos_q=None, pos_k=None,
+               key_mask=None, causal: bool = True, scale: Optional[float] = None) -> str:
+    """Which kernels paged_attention takes for these arguments: "tensor" (the
+    tensor cores) or "general" (fp32 units)."""
+    lib = load_library()
+    p = _attention(q, k_cache, v_cache, lam, page_table, key_lengths, counts, tree, bias_table, bucket_map, pos_q, pos_k,
+                   key_mask, causal, scale)
+    _check(lib.pg_workspace_size(p, ctypes.byref(ctypes.c_size_t(0))))  # the status of an invalid problem
+    return "tensor" if lib.pg_path(p) == 1 else "general"

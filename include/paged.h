@@ -77,8 +77,11 @@ da_status pg_append(const qkr_problem *p, const void *v, const int64_t *v_stride
  * holds at places that no query may see (by length, mask or page) is not used:
  * NaN or infinity there reaches no result. Biases hide keys as in dattn.h.
  *
- * Scores, softmax statistics and sums are fp32. Sums are taken in a fixed order:
- * results do not vary from run to run.
+ * Scores, softmax statistics and sums are fp32. On the tensor cores (bf16, fp16;
+ * pg_path) the weights are operands in the inputs' type; tiles of up to 32 rows
+ * (T * H / Hkv) carry what that rounding took as a second operand, larger ones
+ * do not. Sums are taken in an order that lengths and counts fix: results do not
+ * vary from run to run.
  */
 typedef struct pg_problem {
     int32_t batch;        /* B >= 0 */
@@ -104,12 +107,17 @@ typedef struct pg_problem {
     const uint8_t *tree;        /* device [B, T, T], 0 or 1, or NULL */
 } pg_problem;
 
+/* Which kernels pg_attention takes (a host-only rule on types, sizes and
+ * alignment): 1 the tensor-core ones, 0 the general ones, < 0 invalid. */
+int32_t pg_path(const pg_problem *p);
+
 /* Bytes of device scratch of pg_attention; host-only. */
 da_status pg_workspace_size(const pg_problem *p, size_t *bytes);
 
 /*
  * pg_attention
  *   out        device [B, T, H, Dv], dtype, contiguous; overwritten.
+ * Its kernels' bounded waits are dattn.h's: dattn_device_status reads them too.
  *   workspace  device, 256-byte aligned.
  */
 da_status pg_attention(const pg_problem *p, void *out, void *workspace, size_t workspace_bytes, da_stream_t stream);

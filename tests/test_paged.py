@@ -619,3 +619,14 @@ def test_training_through_the_rotary_norm_and_the_attention(kind):
     r = 2e-5 if kind == "f32" else 8 * 2.0 ** -8
     for name, x, y in zip(("out", "q", "k", "v", "wq", "wk", "lam"), got, want):
         assert float((x.double() - y).norm()) <= r * float(y.norm()), name
+
+
+@pytest.mark.parametrize("kw,path", [
+    (dict(), 1), (dict(dtype=2), 1), (dict(dtype=0), 0), (dict(width=64, value_width=128), 1), (dict(width=20), 0), (dict(width=72), 0),
+    (dict(value_width=136), 0), (dict(num_heads=130, num_buckets=0, reach=0), 0), (dict(cache=dict(page_size=20)), 0), (dict(cache=dict(page_size=24)), 1),
+    (dict(cache=dict(num_pages=0)), 0), (dict(cache=dict(table_pages=0)), 0), (dict(q=FAKE + 8), 0), (dict(cache=dict(k=FAKE + 8)), 0),
+    (dict(num_buckets=128, num_heads=4, reach=1024), 0), (dict(num_tokens=0), 0), (dict(q_stride=(1024, 252, 64, 32)), 0),
+    (dict(q_stride=(0, 256, 64, 32)), 0), (dict(width=-1), -1),
+])
+def test_which_kernels_a_problem_takes(lib, kw, path):
+    assert lib.pg_path(ctypes.byref(_problem(**kw))) == path
