@@ -19,6 +19,8 @@ CUDA core" (§6).
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional, Tuple
 
@@ -121,15 +123,6 @@ def load_library():
               lib.dattn_backward):
         f.restype = ctypes.c_int
     lib.dattn_path.restype = ctypes.c_int32
-    lib.qkr_forward.argtypes = [vp] * 4
-    lib.qkr_workspace_size.argtypes = lib.pg_workspace_size.argtypes = [vp, psize]
-    lib.qkr_backward.argtypes = [vp] * 8 + [ctypes.c_size_t, vp]
-    lib.pg_path.argtypes = [vp]
-    lib.pg_path.restype = ctypes.c_int32
-    lib.pg_append.argtypes = [vp, vp, vp, ctypes.c_int32, vp, vp, vp]
-    lib.pg_attention.argtypes = [vp] * 3 + [ctypes.c_size_t, vp]
-    for f in (lib.qkr_forward, lib.qkr_workspace_size, lib.qkr_backward, lib.pg_append, lib.pg_workspace_size, lib.pg_attention):
-        f.restype = ctypes.c_int
     lib.da_gn_wait_tries.argtypes = [ctypes.c_int32]
     lib.da_gn_wait_tries.restype = ctypes.c_int32
     lib.da_status_string.argtypes = [ctypes.c_int]
@@ -149,6 +142,25 @@ def load_library():
     lib.da_pipeline_destroy.restype = ctypes.c_int
     _lib = lib
     return lib
+
+
+_binding_module = None
+
+
+def _binding():
+    """The compiled marshalling of the serving calls (csrc/binding.cpp), bound to libda.so."""
+    global _binding_module
+    if _binding_module is None:
+        lib = load_library()
+        if not os.path.exists(_build.BINDING):
+            raise RuntimeError(f"the binding is not built for this torch ({_build.BINDING}); run "
+                               "`python -m deformable_view_feature_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_binding", _build.BINDING)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_binding", _build.BINDING, loader=loader))
+        loader.exec_module(module)
+        module.bind(lib._handle, DaError)
+        _binding_module = module
+    return _binding_module
 
 
 def da_version() -> int:

@@ -4,6 +4,10 @@ Every .cu file under csrc/ is compiled to its own object in parallel, and the
 objects are linked into deformable_view_feature_gb300/_build/libda.so. The
 CUDA runtime is linked statically. nvcc cross-compiles, so this needs no GPU.
 
+csrc/binding.cpp, which marshals tensors for the calls of serving, is compiled
+next to it by the host compiler against the installed torch
+(_build/_binding-<torch version>.so).
+
 --debug-bounds builds the bounds-checking variant instead
 (_build/debug/libda_debug.so, compiled with DA_DEBUG_BOUNDS): every index a
 kernel computes is checked before use, and the entry points return
@@ -21,6 +25,9 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -30,6 +37,9 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libda.so")
 DEBUG_DIR = os.path.join(OUT_DIR, "debug")
 DEBUG_LIB = os.path.join(DEBUG_DIR, "libda_debug.so")
+
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(OUT_DIR, f"_binding-{torch.__version__}.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -58,6 +68,28 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
+def _binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    t = os.path.getmtime(BINDING)
+    return all(os.path.getmtime(p) <= t for p in [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+
+
+def _build_binding():
+    """Compile binding.cpp against the installed torch."""
+    at = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    includes = [INCLUDE, sysconfig.get_paths()["include"], at, os.path.join(at, "torch", "csrc", "api", "include"), cuda]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[x for i in includes for x in ("-I", i)], BINDING_SRC, "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the host compiler failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, debug_bounds: bool | None = None) -> str:
     """Compile and link libda.so (libda_debug.so with debug_bounds) unless it
     is newer than every source; return its path. debug_bounds=None follows
@@ -65,9 +97,11 @@ def build(force: bool = False, verbose: bool = False, debug_bounds: bool | None 
     if debug_bounds is None:
         debug_bounds = os.environ.get("DA_DEBUG_BOUNDS") == "1"
     out_dir, lib = (DEBUG_DIR, DEBUG_LIB) if debug_bounds else (OUT_DIR, LIB)
-    if not force and up_to_date(lib):
-        return lib
     os.makedirs(out_dir, exist_ok=True)
+    if not force and up_to_date(lib):
+        if not _binding_up_to_date():
+            _build_binding()
+        return lib
     cc = nvcc()
     srcs = _sources()
     objs = [os.path.join(out_dir, os.path.basename(s)[:-3] + ".o") for s in srcs]
@@ -81,8 +115,11 @@ def build(force: bool = False, verbose: bool = False, debug_bounds: bool | None 
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, r
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(_build_binding) if force or not _binding_up_to_date() else None
         results = list(ex.map(compile_one, zip(srcs, objs)))
+        if binding:
+            binding.result()
     for src, r in results:
         if verbose and r.stderr:
             sys.stderr.write(r.stderr)

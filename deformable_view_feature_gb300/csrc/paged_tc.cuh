@@ -17,9 +17,8 @@
 // second kernel joins them. The shares are made on the device, from lengths and
 // counts, so a captured graph stays balanced while its sequences grow.
 //
-// Warps: groups of four for the weights of up to 32 rows of a map, one that loads
-// by TMA (a box lies in one page: gcd(page size, 128) places), one that issues the
-// products. Weights go through shared memory, rounded to the inputs' type; tiles
+// Warps: 0-3 for the weights of map 0 and 4-7 of map 1, 8 loads by TMA (a box lies in
+// one page: gcd(page size, 128) places), 9 issues the products. Weights go through shared memory, rounded to the inputs' type; tiles
 // of up to 32 rows, which memory bounds, carry what that took as a second operand.
 #pragma once
 
@@ -68,12 +67,27 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const float (&v)[16])
                  : "memory");
 }
 
+// The same without the wait, and the wait, which hands the values on.
+__device__ __forceinline__ void tmem_ask(uint32_t addr, float (&v)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+                 "}, [%16];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+                   "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void tmem_got(float (&v)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+}
+
 // A stage is [V | K_0 | K_1]: with VP = 64 the product's second 64 rows, which
 // nothing reads, are of K.
 template <int DP, int VP, int RT> struct PgShared {
-    static constexpr int C = RT < 32 ? RT : 32;          // rows of a group of warps
-    static constexpr int groups = 2 * RT / C;            // map 0's, then map 1's
-    static constexpr int threads = groups * 128 + 64;
+    static constexpr int threads = 2 * 128 + 64;
     static constexpr int row = DP * 2;                   // bytes of a row of q or k
     static constexpr int q = RT * row, k = kStep * row;  // of one map
     static constexpr int vblock = kStep * 128;           // of 64 columns of V
@@ -86,10 +100,10 @@ template <int DP, int VP, int RT> struct PgShared {
     static constexpr int qbufs = RT == 64 ? 1 : 2;
     static constexpr int pbufs = RT == 64 ? 2 : 1;
     static constexpr int fixed = qbufs * 2 * q + pbufs * pbuf;
-    static constexpr int arrays = RT * 96 + 768;         // the kernel's static ones, at most
+    static constexpr int arrays = RT * 120 + 768 + (DP == 32 ? 6 : 3) * (48 + kStep * 4);  // the kernel's static ones, at most
     static constexpr int room = 227 * 1024 - 1024 - kPgBias - arrays;  // 1024 for alignment
     static constexpr int fit = (room - fixed) / stage;
-    static constexpr int stages = fit > 6 ? 6 : fit;
+    static constexpr int stages = fit > (DP == 32 ? 6 : 3) ? (DP == 32 ? 6 : 3) : fit;
     static constexpr int at_stage = qbufs * 2 * q, at_p = at_stage + stages * stage, bytes = at_p + pbufs * pbuf;
     static_assert(stages >= 2 && bytes <= room, "shared memory");
 };
@@ -106,9 +120,9 @@ struct PgBars {
 
 __device__ uint32_t g_paged_gave_up;
 
-// A tile of a sequence's rows: rt-th of sequence b (all key heads have the same).
+// A tile of a sequence's rows (all key heads have the same).
 struct Tile {
-    int b, l0, len, count, end, steps;  // first query, keys, queries, keys that some query sees, steps of them
+    int b, l0, len, count, end, steps;  // sequence, first query, keys, queries, keys that some query sees, steps of them
 };
 
 __device__ __forceinline__ Tile tile_of(const PagedTcArgs &a, int e)
@@ -121,39 +135,67 @@ __device__ __forceinline__ Tile tile_of(const PagedTcArgs &a, int e)
     t.end = t.l0 < t.count ? t.len : 0;
     // Keys after the tile's last query end the walk where positions are indices.
     if (a.d.causal && !a.d.pos_q && !a.d.pos_k) t.end = min(t.end, max(t.len - t.count + min(t.l0 + a.LP, t.count), 0));
-    t.steps = max((t.end + kStep - 1) / kStep, 1);
+    t.steps = (t.end + kStep - 1) / kStep;
     return t;
 }
 
-// A CTA's walk over its share, segment by segment: `steps` of tile (e, n) from `first` on.
+// What a tile costs, in steps: to begin and end one takes as long as kOpen.
+constexpr int kOpen = 2;
+__device__ __forceinline__ int units(const Tile &t) { return t.steps ? t.steps + kOpen : 0; }
+
+// A CTA's walk over its share of units, segment by segment: `steps` of tile
+// (e, n) from `first` on. Units that only open a tile bring no segment.
 struct Walk {
     int64_t left;
-    int e, n, first, steps;
+    int e, n, at, first, steps;
     Tile t;
 
-    __device__ __forceinline__ void open() { steps = static_cast<int>(min(static_cast<int64_t>(t.steps - first), left)); }
-    __device__ __forceinline__ void start(const PagedTcArgs &a, int64_t share, int e_, int n_, int first_)
+    __device__ __forceinline__ void settle(const PagedTcArgs &a)
+    {
+        while (left > 0) {
+            if (t.steps > 0) {
+                const int64_t to = min(static_cast<int64_t>(units(t)), at + left);
+                first = max(at - kOpen, 0);
+                steps = static_cast<int>(max(to - kOpen, int64_t{0})) - first;
+                if (steps > 0) return;
+            }
+            pass(a);
+        }
+    }
+    __device__ __forceinline__ void pass(const PagedTcArgs &a)
+    {
+        left -= units(t) - at;
+        at = 0;
+        if (left <= 0) return;
+        if (t.steps == 0 || ++n == a.d.Hkv) {
+            n = 0;
+            t = tile_of(a, ++e);
+        }
+    }
+    __device__ __forceinline__ void start(const PagedTcArgs &a, int64_t share, int e_, int n_, int at_)
     {
         left = share;
         e = e_;
         n = n_;
-        first = first_;
-        if (left > 0) {
-            t = tile_of(a, e);
-            open();
-        }
+        at = at_;
+        if (left <= 0) return;
+        t = tile_of(a, e);
+        settle(a);
     }
     __device__ __forceinline__ void next(const PagedTcArgs &a)
     {
-        left -= steps;
-        first = 0;
-        if (left <= 0) return;
-        if (++n == a.d.Hkv) {
-            n = 0;
-            t = tile_of(a, ++e);
-        }
-        open();
+        pass(a);
+        settle(a);
     }
+};
+
+constexpr int kFar = 1 << 30;  // beyond every position
+
+// What is known of a step's keys, by groups of 32: which are to be used, and
+// the least and largest of their positions.
+struct StepInfo {
+    uint32_t use[4];
+    int lo[4], hi[4];
 };
 
 // Sums of N columns over the warp's lanes; lane i is left with columns
@@ -175,19 +217,19 @@ template <int N> __device__ __forceinline__ void fold(float (&v)[N], int lane, i
     }
 }
 
-// Whether any of the 128 threads of a group has `flag`.
-__device__ __forceinline__ bool vote(int group, bool flag)
+// Whether any of the 128 threads of a map has `flag`.
+__device__ __forceinline__ bool vote(int m, bool flag)
 {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
                  "bar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r)
-                 : "r"(static_cast<uint32_t>(flag)), "r"(1 + group)
+                 : "r"(static_cast<uint32_t>(flag)), "r"(1 + m)
                  : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void sync_group(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
-template <int THREADS> __device__ __forceinline__ void sync_groups() { asm volatile("bar.sync 7, %0;" ::"n"(THREADS) : "memory"); }
+__device__ __forceinline__ void sync_map(int m) { asm volatile("bar.sync %0, 128;" ::"r"(1 + m) : "memory"); }
+__device__ __forceinline__ void sync_maps() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 
 // Whether a phase has ended, without waiting; the same in all lanes of a warp.
 // kIdle tests of nothing to do, some 100 ns each, end the wait (bar_wait).
@@ -217,18 +259,22 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                     const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv)
 {
     using F = PgShared<DP, VP, RT>;
-    constexpr int NS = F::stages, C = F::C, kThreads = F::threads, kLoad = F::groups * 4, kIssue = kLoad + 1;
+    constexpr int NS = F::stages, kThreads = F::threads, kLoad = 8, kIssue = 9;
     constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t columns = RT == 16 ? 128 : RT == 32 ? 256 : 512;
     extern __shared__ unsigned char raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
     __shared__ PgBars bars;
-    // Each group's rows.
-    __shared__ __align__(16) float noff[F::groups][C];     // minus the row's reference
-    __shared__ __align__(16) float shrink[F::groups][C];
-    __shared__ __align__(16) float wide[F::groups][4][C];  // a warp's maxima, or sums
-    __shared__ int row_pos[F::groups][C], row_l[F::groups][C], row_h[F::groups][C];
-    __shared__ float far_bias[F::groups][2][C];            // of keys `reach` or more before and after the query
+    __shared__ StepInfo infos[NS];
+    __shared__ int key_pos[NS][kStep];                     // where positions are given
+    // Each map's rows.
+    __shared__ __align__(16) float noff[2][RT];            // minus the row's reference
+    __shared__ __align__(16) float off[2][2][RT];          // the same, with far_bias
+    __shared__ __align__(16) float shrink[2][RT];
+    __shared__ __align__(16) float wide[2][4][RT];         // a warp's maxima, or sums
+    __shared__ __align__(16) float far_bias[2][2][RT];     // of keys `reach` or more before and after the query
+    __shared__ int row_pos[2][RT], row_l[2][RT], row_h[2][RT];
+    __shared__ int64_t row_out[RT];                        // where the row's output is, or -1
     __shared__ int64_t warp_total[kThreads / 32];
     __shared__ int start[3];
     float *table = reinterpret_cast<float *>(base + F::bytes);  // [nb][H], times log2(e)
@@ -241,7 +287,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
             bar_init(&bars.q_full[i], 1);
             bar_init(&bars.q_empty[i], 1);
             bar_init(&bars.s_full[i], 1);
-            bar_init(&bars.p_full[i], F::groups * 4);
+            bar_init(&bars.p_full[i], 8);
         }
         for (int s = 0; s < NS; ++s) {
             bar_init(&bars.full[s], 1);
@@ -265,11 +311,20 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
     }
     fence_async();
 
-    // The CTA's share: threads take consecutive tiles' steps, a scan adds them up.
-    const int entries = d.B * a.row_tiles, per = (entries + kThreads - 1) / kThreads;
+    // Rows that see nothing: all heads' outputs of such tiles lie in a row.
+    const int entries = d.B * a.row_tiles;
+    for (int e = blockIdx.x; e < entries; e += gridDim.x) {
+        const Tile t = tile_of(a, e);
+        if (t.steps) continue;
+        T *to = static_cast<T *>(d.out) + (static_cast<int64_t>(t.b) * d.Lq + t.l0) * d.H * d.Dv;
+        const int n = min(a.LP, d.Lq - t.l0) * d.H * d.Dv;
+        for (int i = threadIdx.x; i < n; i += kThreads) to[i] = dattn_round<T>(0.f);
+    }
+    // The CTA's share: threads take consecutive tiles' units, a scan adds them up.
+    const int per = (entries + kThreads - 1) / kThreads;
     const int e0 = min(static_cast<int>(threadIdx.x) * per, entries), e1 = min(e0 + per, entries);
     int64_t own = 0;
-    for (int e = e0; e < e1; ++e) own += tile_of(a, e).steps;
+    for (int e = e0; e < e1; ++e) own += units(tile_of(a, e));
     own *= d.Hkv;
     int64_t upto = own;
     for (int o = 1; o < 32; o <<= 1) {
@@ -286,19 +341,19 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
         total += warp_total[w];
     }
     // CTAs without a share are the last ones, so that a tile's pieces lie in CTAs in a row.
-    const int64_t active = min(total, static_cast<int64_t>(gridDim.x)), cta = min(static_cast<int64_t>(blockIdx.x), active);
+    const int64_t active = max(min(total, static_cast<int64_t>(gridDim.x)), int64_t{1}), cta = min(static_cast<int64_t>(blockIdx.x), active);
     const int64_t from = total * cta / active, share = cta < active ? total * (cta + 1) / active - from : 0;
     if (share > 0 && from < upto && from >= upto - own) {
         int64_t at = upto - own;
-        int e = e0, steps = 0;
+        int e = e0, u = 0;
         for (;; ++e) {
-            steps = tile_of(a, e).steps;
-            if (from < at + static_cast<int64_t>(steps) * d.Hkv) break;
-            at += static_cast<int64_t>(steps) * d.Hkv;
+            u = units(tile_of(a, e));
+            if (from < at + static_cast<int64_t>(u) * d.Hkv) break;
+            at += static_cast<int64_t>(u) * d.Hkv;
         }
         start[0] = e;
-        start[1] = static_cast<int>((from - at) / steps);
-        start[2] = static_cast<int>((from - at) % steps);
+        start[1] = static_cast<int>((from - at) / u);
+        start[2] = static_cast<int>((from - at) % u);
     }
     __syncthreads();
     const uint32_t tmem = uniform(bars.tmem);
@@ -320,18 +375,46 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                 for (int m = 0; m < 2; ++m) tma_load(&mq, &bars.q_full[qb], base + (qb * 2 + m) * F::q, 0, m, w.n * d.G, w.t.l0, w.t.b);
             }
             for (int i = 0; i < w.steps; ++i, ++t) {
-                const int s = t % NS, j = (w.first + i) * kStep + lane * a.box;
+                const int s = t % NS, j0 = (w.first + i) * kStep, j = j0 + lane * a.box;
                 int place = 0, page = -1;
                 if (lane < boxes && j < w.t.end) page = paged_page(d, w.t.b, j, place);
                 const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+                uint32_t used_keys[4];
+                int pos[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int r = g * 32 + lane;
+                    bool use = j0 + r < w.t.end && (there >> (r / a.box) & 1);
+                    const int64_t of = static_cast<int64_t>(w.t.b) * d.Lk + j0 + r;
+                    if (use && d.mask) use = d.mask[of] != 0;
+                    pos[g] = use && d.pos_k ? d.pos_k[of] : j0 + r;
+                    used_keys[g] = __ballot_sync(0xffffffffu, use);
+                }
+                int lo[4], hi[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const bool use = used_keys[g] >> lane & 1;
+                    lo[g] = __reduce_min_sync(0xffffffffu, use ? pos[g] : kFar);
+                    hi[g] = __reduce_max_sync(0xffffffffu, use ? pos[g] : -kFar);
+                }
+                // The copies first: their bytes may arrive before they are expected, the phase ends after.
                 bar_wait_warp(&bars.empty[s], ((t / NS) & 1) ^ 1, gave_up);
-                if (lane == 0) bar_expect(&bars.full[s], __popc(there) * a.box * (2 * F::row + blocks * 128));
-                __syncwarp();
                 if (page >= 0) {
                     unsigned char *st = base + F::at_stage + s * F::stage;
                     for (int m = 0; m < 2; ++m) tma_load(&mk, &bars.full[s], st + F::v + m * F::k + lane * a.box * F::row, 0, m, w.n, place, page);
                     for (int c = 0; c < blocks; ++c) tma_load(&mv, &bars.full[s], st + c * F::vblock + lane * a.box * 128, c * 64, 0, w.n, place, page);
                 }
+                __syncwarp();
+                if (lane < 4) {
+                    infos[s].use[lane] = lane == 0 ? used_keys[0] : lane == 1 ? used_keys[1] : lane == 2 ? used_keys[2] : used_keys[3];
+                    infos[s].lo[lane] = lane == 0 ? lo[0] : lane == 1 ? lo[1] : lane == 2 ? lo[2] : lo[3];
+                    infos[s].hi[lane] = lane == 0 ? hi[0] : lane == 1 ? hi[1] : lane == 2 ? hi[2] : hi[3];
+                }
+                if (d.pos_k)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) key_pos[s][g * 32 + lane] = pos[g];
+                __syncwarp();
+                if (lane == 0) bar_expect(&bars.full[s], __popc(there) * a.box * (2 * F::row + blocks * 128));
                 __syncwarp();
             }
         }
@@ -353,11 +436,10 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
         // weights. Whichever can is issued next: sums that waited behind scores
         // would hold their stage for as long as the next keys take to arrive.
         Walk ws = w;
-        const int steps = static_cast<int>(share);
         int u = 0, t = 0, at = 0, seg = 0, done = 0;  // scores and sums issued, scores of the segment, its number, sums of theirs
-        for (uint32_t idle = 0; t < steps;) {
+        for (uint32_t idle = 0; w.left > 0;) {
             const int qb = seg % F::qbufs;
-            if (u < steps && u <= t + 1 && bar_test(&bars.full[u % NS], (u / NS) & 1, gave_up) &&
+            if (ws.left > 0 && u <= t + 1 && bar_test(&bars.full[u % NS], (u / NS) & 1, gave_up) &&
                 (at > 0 || bar_test(&bars.q_full[qb], (seg / F::qbufs) & 1, gave_up))) {
                 const int s = u % NS;
                 const bool last = ++at == ws.steps;
@@ -400,175 +482,183 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                 }
                 ++t;
                 idle = 0;
-            } else if (++idle > kIdle) {
-                *gave_up = 1;
+            } else {
+                if (++idle > kIdle) *gave_up = 1;
+                __nanosleep(20);  // leaves the SM's issue slots to the others
             }
         }
         for (int i = max(0, t - NS); i < t; ++i) bar_drain(&bars.empty[i % NS], (i / NS) & 1);
         __syncwarp();
     } else {
-        // Group `gr` has rows r0 .. r0 + C - 1 of map m, columns gr * C .. of the
-        // scores and sums; a thread has key kr of each step.
-        const int gr = warp >> 2, m = gr * C / RT, r0 = gr * C % RT, kr = (warp & 3) * 32 + lane;
+        // A thread has key kr of each step, and that key's scores of map m with all rows.
+        constexpr int X = 16;  // scores that it takes at once
+        const int m = warp >> 2, kr = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const float mul = d.scale_log2;
+        const float2 mul = {d.scale_log2, d.scale_log2};
         int t = 0, slot_tile[2] = {-1, -1}, slot_last = 0;
         for (; w.left > 0; w.next(a)) {
             const Tile tile = w.t;
             const int b = tile.b, old = tile.len - tile.count;
-            if (kr < C) {
-                const int dl = static_cast<int>(d.div_G.div(r0 + kr)), l = min(tile.l0 + dl, d.Lq - 1);
-                const int h = min(w.n * d.G + r0 + kr - dl * d.G, d.H - 1);
-                row_l[gr][kr] = l;
-                row_h[gr][kr] = h;
-                row_pos[gr][kr] = d.pos_q ? d.pos_q[static_cast<int64_t>(b) * d.Lq + l] : old + l;
-                noff[gr][kr] = FLT_MAX;
-                for (int i = 0; i < 2; ++i) far_bias[gr][i][kr] = d.nb ? table[bmap[i * 2 * d.reach] + h] : 0.f;
-            }
-            // A step ahead: whether the thread's key is to be used, and where it is.
-            bool next_use;
-            int next_pos;
-            const auto fetch = [&](int step) {
-                const int j = step * kStep + kr;
-                next_use = j < tile.end;
-                next_pos = j;
-                if (next_use) {
-                    const int64_t of = static_cast<int64_t>(b) * d.Lk + j;
-                    int place;
-                    if (d.pos_k) next_pos = d.pos_k[of];
-                    if (d.mask && !d.mask[of]) next_use = false;
-                    if (paged_page(d, b, j, place) < 0) next_use = false;
+            if (kr < RT) {
+                const int dl = static_cast<int>(d.div_G.div(kr)), l = min(tile.l0 + dl, d.Lq - 1), h = min(w.n * d.G + kr - dl * d.G, d.H - 1);
+                row_l[m][kr] = l;
+                row_h[m][kr] = h;
+                row_pos[m][kr] = d.pos_q ? d.pos_q[static_cast<int64_t>(b) * d.Lq + l] : old + l;
+                noff[m][kr] = FLT_MAX;
+                for (int i = 0; i < 2; ++i) {
+                    far_bias[m][i][kr] = d.nb ? table[bmap[i * 2 * d.reach] + h] : 0.f;
+                    off[m][i][kr] = FLT_MAX + far_bias[m][i][kr];
                 }
-            };
-            fetch(w.first);
-            sync_group(gr);
-            int qmin = INT32_MAX, qmax = INT32_MIN;
-            if (lane < C && r0 + lane < used && tile.l0 + static_cast<int>(d.div_G.div(r0 + lane)) < tile.count) qmin = qmax = row_pos[gr][lane];
+                if (m == 0) row_out[kr] = kr < used && tile.l0 + dl < d.Lq ? ((static_cast<int64_t>(b) * d.Lq + l) * d.H + h) * d.Dv : -1;
+            }
+            sync_map(m);
+            int qmin = kFar, qmax = -kFar;
+#pragma unroll
+            for (int r = lane; r < RT; r += 32)
+                if (r < used && tile.l0 + static_cast<int>(d.div_G.div(r)) < tile.count) {
+                    qmin = min(qmin, row_pos[m][r]);
+                    qmax = max(qmax, row_pos[m][r]);
+                }
             qmin = __reduce_min_sync(0xffffffffu, qmin);
             qmax = __reduce_max_sync(0xffffffffu, qmax);
-            float sum[C];
+            float2 sum[RT / 2];
 #pragma unroll
-            for (int c = 0; c < C; ++c) sum[c] = 0.f;
+            for (int c = 0; c < RT / 2; ++c) sum[c] = {0.f, 0.f};
+#pragma unroll 1
             for (int i = 0; i < w.steps; ++i, ++t) {
                 const int s = t % NS, j = (w.first + i) * kStep + kr;
-                const bool use = next_use;
-                const int pos = next_pos;
-                if (i + 1 < w.steps) fetch(w.first + i + 1);
-                const bool all = __all_sync(0xffffffffu, use);
-                const int64_t kmin = __reduce_min_sync(0xffffffffu, use ? pos : INT32_MAX), kmax = __reduce_max_sync(0xffffffffu, use ? pos : INT32_MIN);
+                bar_wait_warp(&bars.s_full[t & 1], (t >> 1) & 1, gave_up);
+                fence_after();
+                const StepInfo &info = infos[s];
+                const uint32_t used_keys = info.use[warp & 3];
+                const bool use = used_keys >> lane & 1, all = used_keys == 0xffffffffu;
+                const int pos = d.pos_k ? key_pos[s][kr] : j, kmin = info.lo[warp & 3], kmax = info.hi[warp & 3];
                 // Whether every row sees all of the warp's keys, with one bias for each row.
                 const bool before = d.nb == 0 || kmax - qmin <= -d.reach, after = !before && kmin - qmax >= d.reach;
                 const bool fast = (before || after) && !(d.causal && kmax > qmin) && !(d.pg.tree && (j - lane + 31) >= old);
-                bar_wait_warp(&bars.s_full[t & 1], (t >> 1) & 1, gave_up);
-                fence_after();
-                float x[C];
-                // First the scores in base 2 less the rows' references; if some
-                // weight would be too large, then the scores alone, for new
-                // references, and then once more.
+                // Scores of rows c0 .. in base 2, less the rows' references (or not).
+                const auto finish = [&](float (&x)[X], int c0, bool less) {
+                    bool leaf = true;
+#pragma unroll
+                    for (int c = 0; c < X; ++c) {
+                        const int r = c0 + c, rel = pos - row_pos[m][r];
+                        if (d.pg.tree && use && j >= old && (c == 0 || row_l[m][r] != row_l[m][r - 1]))
+                            leaf = d.pg.tree[(static_cast<int64_t>(b) * d.Lq + row_l[m][r]) * d.Lq + j - old] != 0;
+                        const float bias = fast || !d.nb ? far_bias[m][after][r] : table[bmap[min(max(rel, -d.reach), d.reach) + d.reach] + row_h[m][r]];
+                        const float y = fmaf(x[c], mul.x, bias) + (less ? noff[m][r] : 0.f);
+                        x[c] = use && leaf && !(d.causal && rel > 0) ? y : -INFINITY;
+                    }
+                };
+                // The step's weights; once more where one would be too large for
+                // its row's reference.
+                uint32_t hi[RT / 2], lo[F::rests ? RT / 2 : 1];
+                const auto weigh = [&](const float (&x)[X], int c0) {
+#pragma unroll
+                    for (int c = 0; c < X; c += 2) {
+                        const float2 w2 = {ex2(x[c]), ex2(x[c + 1])};
+                        uint32_t &h = hi[(c0 + c) / 2];
+                        h = pack2<T>(w2.x, w2.y);
+                        if constexpr (F::rests) {
+                            const float2 r = unpack2<T>(h);
+                            lo[(c0 + c) / 2] = pack2<T>(w2.x - r.x, w2.y - r.y);
+                        }
+                    }
+                };
 #pragma unroll 1
-                for (int pass = 0;; ++pass) {
-                    const bool less = pass != 1;
-                    tmem_load(tS(0, t) + gr * C + lanes, x);
-                    if (fast) {
+                for (bool again = false;; again = true) {
+                    float x[2][X], top[2] = {-INFINITY, -INFINITY};
+                    if (fast && all) {
+                        // Most steps: no branches, for the sake of the order of instructions.
+                        const float *o = off[m][after];
+                        tmem_ask(tS(m, t) + lanes, x[0]);
 #pragma unroll
-                        for (int c = 0; c < C; c += 4) {
-                            float4 o = less ? *reinterpret_cast<const float4 *>(&noff[gr][c]) : make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (d.nb) {
-                                x[c] = fmaf(x[c], mul, far_bias[gr][after][c]) + o.x;
-                                x[c + 1] = fmaf(x[c + 1], mul, far_bias[gr][after][c + 1]) + o.y;
-                                x[c + 2] = fmaf(x[c + 2], mul, far_bias[gr][after][c + 2]) + o.z;
-                                x[c + 3] = fmaf(x[c + 3], mul, far_bias[gr][after][c + 3]) + o.w;
-                            } else {
-                                x[c] = fmaf(x[c], mul, o.x);
-                                x[c + 1] = fmaf(x[c + 1], mul, o.y);
-                                x[c + 2] = fmaf(x[c + 2], mul, o.z);
-                                x[c + 3] = fmaf(x[c + 3], mul, o.w);
+                        for (int c0 = 0; c0 < RT; c0 += X) {
+                            float (&y)[X] = x[c0 / X % 2];
+                            tmem_got(y);
+                            if (c0 + X < RT) tmem_ask(tS(m, t) + c0 + X + lanes, x[(c0 / X + 1) % 2]);
+#pragma unroll
+                            for (int c = 0; c < X; c += 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(o + c0 + c);
+                                const float2 u = fma2({y[c], y[c + 1]}, mul, {f.x, f.y}), v = fma2({y[c + 2], y[c + 3]}, mul, {f.z, f.w});
+                                y[c] = u.x;
+                                y[c + 1] = u.y;
+                                y[c + 2] = v.x;
+                                y[c + 3] = v.y;
+                                top[0] = max3(top[0], u.x, u.y);
+                                top[1] = max3(top[1], v.x, v.y);
                             }
+                            weigh(y, c0);
                         }
-                        if (!all)
-#pragma unroll
-                            for (int c = 0; c < C; ++c) x[c] = use ? x[c] : -INFINITY;
                     } else {
-                        bool leaf = true;
 #pragma unroll
-                        for (int c = 0; c < C; ++c) {
-                            const int rel = pos - row_pos[gr][c];
-                            if (d.pg.tree && use && j >= old && (c == 0 || row_l[gr][c] != row_l[gr][c - 1]))
-                                leaf = d.pg.tree[(static_cast<int64_t>(b) * d.Lq + row_l[gr][c]) * d.Lq + j - old] != 0;
-                            const float bias = d.nb ? table[bmap[min(max(rel, -d.reach), d.reach) + d.reach] + row_h[gr][c]] : 0.f;
-                            const float y = fmaf(x[c], mul, bias) + (less ? noff[gr][c] : 0.f);
-                            x[c] = use && leaf && !(d.causal && rel > 0) ? y : -INFINITY;
+                        for (int c0 = 0; c0 < RT; c0 += X) {
+                            tmem_load(tS(m, t) + c0 + lanes, x[0]);
+                            finish(x[0], c0, true);
+#pragma unroll
+                            for (int c = 0; c < X; c += 2) top[0] = max3(top[0], x[0][c], x[0][c + 1]);
+                            weigh(x[0], c0);
                         }
                     }
-                    if (pass == 2) break;
-                    if (pass == 0) {
-                        bool over = false;
+                    if (again || !vote(m, fmaxf(top[0], top[1]) > kLift<T> + kSlack)) break;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < RT; c0 += X) {
+                        tmem_load(tS(m, t) + c0 + lanes, x[0]);
+                        finish(x[0], c0, false);
 #pragma unroll
-                        for (int c = 0; c < C; ++c) over |= x[c] > kLift<T> + kSlack;
-                        if (!vote(gr, over)) break;
-                        continue;
+                        for (int c = 0; c < X; ++c) {
+                            const float best = warp_max(x[0][c]);
+                            if (lane == c) wide[m][warp & 3][c0 + c] = best;
+                        }
                     }
-#pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        const float best = warp_max(x[c]);
-                        if (lane == c) wide[gr][warp & 3][c] = best;
-                    }
-                    sync_group(gr);
-                    if (kr < C) {
-                        const float best = fmaxf(fmaxf(wide[gr][0][kr], wide[gr][1][kr]), fmaxf(wide[gr][2][kr], wide[gr][3][kr]));
-                        const float ref = -noff[gr][kr];
-                        const bool raise = best + noff[gr][kr] > kLift<T> + kSlack;
+                    sync_map(m);
+                    if (kr < RT) {
+                        const float best = fmaxf(fmaxf(wide[m][0][kr], wide[m][1][kr]), fmaxf(wide[m][2][kr], wide[m][3][kr]));
+                        const float ref = -noff[m][kr];
+                        const bool raise = best + noff[m][kr] > kLift<T> + kSlack;
                         const float next = raise ? best - kLift<T> : ref;
-                        noff[gr][kr] = -next;
-                        shrink[gr][kr] = raise ? ex2(ref - next) : 1.f;
+                        noff[m][kr] = -next;
+                        for (int i = 0; i < 2; ++i) off[m][i][kr] = far_bias[m][i][kr] - next;
+                        shrink[m][kr] = raise ? ex2(ref - next) : 1.f;
                     }
-                    sync_group(gr);
+                    sync_map(m);
                     if (i > 0) {
                         bar_wait_warp(&bars.empty[(t - 1) % NS], ((t - 1) / NS) & 1, gave_up);
                         fence_after();
 #pragma unroll 1
-                        for (int c0 = 0; c0 < C; c0 += 16) {
+                        for (int c0 = 0; c0 < RT; c0 += 16) {
                             float o[16];
-                            tmem_load(tO + gr * C + c0 + lanes, o);
+                            tmem_load(tO + m * RT + c0 + lanes, o);
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) o[c] *= shrink[gr][c0 + c];
-                            tmem_store(tO + gr * C + c0 + lanes, o);
+                            for (int c = 0; c < 16; ++c) o[c] *= shrink[m][c0 + c];
+                            tmem_store(tO + m * RT + c0 + lanes, o);
                         }
                         tmem_store_wait();
                     }
 #pragma unroll
-                    for (int c = 0; c < C; ++c) sum[c] *= shrink[gr][c];
+                    for (int c = 0; c < RT / 2; ++c) sum[c] = mul2(sum[c], *reinterpret_cast<const float2 *>(&shrink[m][2 * c]));
+                }
+                // The sum is of the weights as the product takes them.
+#pragma unroll
+                for (int c = 0; c < RT / 2; ++c) {
+                    sum[c] = add2(sum[c], unpack2<T>(hi[c]));
+                    if constexpr (F::rests) sum[c] = add2(sum[c], unpack2<T>(lo[c]));
                 }
                 // The weights' buffer is free when the products before have read
                 // it: those two steps ago, for which the scores' barrier stands
                 // too, or with one buffer those of the last step.
-                if (F::pbufs == 1 && t > 0) {
-                    bar_wait_warp(&bars.empty[(t - 1) % NS], ((t - 1) / NS) & 1, gave_up);
-                }
+                if (F::pbufs == 1 && t > 0) bar_wait_warp(&bars.empty[(t - 1) % NS], ((t - 1) / NS) & 1, gave_up);
                 unsigned char *pt = base + F::at_p + (t % F::pbufs) * F::pbuf + (RT == 64 ? m * (F::p / 2) : 0) + kr * F::prow;
-                const int swz = RT == 16 ? (kr >> 1) & 3 : kr & 7, piece0 = (RT == 64 ? r0 : gr * C) / 8;
+                const int swz = RT == 16 ? (kr >> 1) & 3 : kr & 7, piece0 = RT == 64 ? 0 : m * RT / 8;
 #pragma unroll
-                for (int c = 0; c < C; c += 8) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float p0 = ex2(x[c + 2 * k]), p1 = ex2(x[c + 2 * k + 1]);
-                        sum[c + 2 * k] += p0;
-                        sum[c + 2 * k + 1] += p1;
-                        hi[k] = pack2<T>(p0, p1);
-                        if (F::rests) {
-                            const float2 r = unpack2<T>(hi[k]);
-                            lo[k] = pack2<T>(p0 - r.x, p1 - r.y);
-                        }
-                    }
-                    const int at = ((piece0 + c / 8) ^ swz) << 4;
-                    *reinterpret_cast<uint4 *>(pt + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    if (F::rests) *reinterpret_cast<uint4 *>(pt + F::p + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                for (int c = 0; c < RT / 2; c += 4) {
+                    const int at = ((piece0 + c / 4) ^ swz) << 4;
+                    *reinterpret_cast<uint4 *>(pt + at) = make_uint4(hi[c], hi[c + 1], hi[c + 2], hi[c + 3]);
+                    if constexpr (F::rests) *reinterpret_cast<uint4 *>(pt + F::p + at) = make_uint4(lo[c], lo[c + 1], lo[c + 2], lo[c + 3]);
                 }
-                if (!all && gr < VP / 64) {
+                if (!all && m < VP / 64) {
                     // 0 * NaN is NaN: unused keys' rows of V become zeros.
                     bar_wait_warp(&bars.full[s], (t / NS) & 1, gave_up);
-                    unsigned char *v = base + F::at_stage + s * F::stage + gr * F::vblock + kr * 128;
+                    unsigned char *v = base + F::at_stage + s * F::stage + m * F::vblock + kr * 128;
                     if (!use)
 #pragma unroll
                         for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(v + (((c + lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -579,57 +669,67 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                 if (lane == 0) bar_arrive(&bars.p_full[t & 1]);
             }
             // The segment's end: weights' sums over the threads, then the sums themselves.
-            fold<C>(sum, lane, 16);
-            if (C == 32) wide[gr][warp & 3][lane] = sum[0];
-            else if ((lane & 1) == 0) wide[gr][warp & 3][lane >> 1] = sum[0];
+            {
+                float all_sums[RT];
+#pragma unroll
+                for (int c = 0; c < RT / 2; ++c) {
+                    all_sums[2 * c] = sum[c].x;
+                    all_sums[2 * c + 1] = sum[c].y;
+                }
+                fold<RT>(all_sums, lane, 16);
+                if constexpr (RT == 16) {
+                    if ((lane & 1) == 0) wide[m][warp & 3][lane >> 1] = all_sums[0];
+                } else {
+#pragma unroll
+                    for (int c = 0; c < RT / 32; ++c) wide[m][warp & 3][lane * (RT / 32) + c] = all_sums[c];
+                }
+            }
             bar_wait_warp(&bars.empty[(t - 1) % NS], ((t - 1) / NS) & 1, gave_up);
             fence_after();
-            sync_groups<F::groups * 128>();
-            const float nan = *gave_up ? NAN : 0.f;
-            const auto whole_sum = [&](int g, int c) { return wide[g][0][c] + wide[g][1][c] + (wide[g][2][c] + wide[g][3][c]) + nan; };
-            const int dv = (warp & 3) * 32 + lane;
-            if (w.first == 0 && w.steps == tile.steps) {
-                // Each group takes its share of the rows, of both maps.
-                constexpr int share_rows = RT / F::groups;
+            sync_maps();
+            const bool whole = w.first == 0 && w.steps == tile.steps;
+            const int dv = (warp & 3) * 32 + lane, k = w.first == 0;
+            const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + k;
+            if (kr < RT) {
+                const float total = wide[m][0][kr] + wide[m][1][kr] + (wide[m][2][kr] + wide[m][3][kr]) + (*gave_up ? NAN : 0.f);
+                if (whole) {
+                    shrink[m][kr] = total == 0.f || row_l[m][kr] >= tile.count ? 0.f : (m ? d.lam[row_h[m][kr]] : 1.f) / total;
+                } else if (kr < used) {
+                    *reinterpret_cast<float2 *>(d.part_ml + ((slot * RT + kr) * 2 + m) * 2) = make_float2(-noff[m][kr], total);
+                }
+            }
+            if (whole) {
+                sync_maps();
+                // The warps of map m take the m-th half of the rows, of both maps.
 #pragma unroll 1
-                for (int q0 = gr * share_rows; q0 < (gr + 1) * share_rows; q0 += 8) {
-                    float x[8], y[8];
+                for (int r0 = m * (RT / 2); r0 < (m + 1) * (RT / 2); r0 += 8) {
+                    float u[8], v[8];
                     __syncwarp();
-                    tmem_load(tO + q0 + lanes, x);
-                    tmem_load(tO + RT + q0 + lanes, y);
+                    tmem_load(tO + r0 + lanes, u);
+                    tmem_load(tO + RT + r0 + lanes, v);
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
-                        const int r = q0 + c, l = tile.l0 + static_cast<int>(d.div_G.div(r));
-                        if (r >= used || l >= d.Lq || dv >= d.Dv) continue;
-                        const int h = row_h[r / C][r % C];
-                        const float s0 = whole_sum(r / C, r % C), s1 = whole_sum(F::groups / 2 + r / C, r % C);
-                        const float o = (s0 == 0.f ? 0.f : x[c] / s0) - d.lam[h] * (s1 == 0.f ? 0.f : y[c] / s1);
-                        static_cast<T *>(d.out)[((static_cast<int64_t>(b) * d.Lq + l) * d.H + h) * d.Dv + dv] =
-                            dattn_round<T>(l < tile.count ? o : 0.f);
+                        // A row without keys has no sums, not even of NaN.
+                        const float f0 = shrink[0][r0 + c], f1 = shrink[1][r0 + c], o = (f0 == 0.f ? 0.f : u[c] * f0) - (f1 == 0.f ? 0.f : v[c] * f1);
+                        if (row_out[r0 + c] >= 0 && dv < d.Dv) static_cast<T *>(d.out)[row_out[r0 + c] + dv] = dattn_round<T>(o);
                     }
                 }
             } else {
-                const int k = w.first == 0;
-                const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + k;
                 slot_tile[k] = w.e * d.Hkv + w.n;
                 if (!k) slot_last = w.first + w.steps == tile.steps;
+                float *to = d.part_o + (slot * RT * 2 + m) * d.Dv + dv;
 #pragma unroll 1
-                for (int c0 = 0; c0 < C; c0 += 8) {
-                    float x[8];
+                for (int r0 = 0; r0 < used; r0 += 8) {
+                    float u[8];
                     __syncwarp();
-                    tmem_load(tO + gr * C + c0 + lanes, x);
+                    tmem_load(tO + m * RT + r0 + lanes, u);
+                    if (dv < d.Dv)
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        if (r0 + c0 + c < used && dv < d.Dv) d.part_o[((slot * RT + r0 + c0 + c) * 2 + m) * d.Dv + dv] = x[c];
-                }
-                if (kr < C && r0 + kr < used) {
-                    float *ml = d.part_ml + ((slot * RT + r0 + kr) * 2 + m) * 2;
-                    ml[0] = -noff[gr][kr];
-                    ml[1] = whole_sum(gr, kr);
+                        for (int c = 0; c < 8; ++c) to[(r0 + c) * 2 * d.Dv] = u[c];
                 }
             }
             __syncwarp();
-            sync_groups<F::groups * 128>();  // the next segment's arrays are the same
+            sync_maps();  // the next segment's arrays are the same
         }
         if (threadIdx.x < 2) {
             a.slots[blockIdx.x * 4 + threadIdx.x * 2] = threadIdx.x ? slot_tile[1] : slot_tile[0];
@@ -715,7 +815,7 @@ cudaError_t launch_tc(const PagedTcArgs &a, const CUtensorMap &mq, const CUtenso
     if (e != cudaSuccess) return e;
     kernel<<<a.ctas, F::threads, smem, st>>>(a, mq, mk, mv);
     e = cudaGetLastError();
-    if (e == cudaSuccess && a.ctas > 1)  // one CTA has no pieces
+    if (e == cudaSuccess && a.ctas > 1 && a.d.Lk > kStep)  // otherwise no tile has pieces
         e = launch_pdl(paged_join_kernel<T>, dim3(a.ctas, a.LP * a.d.G), dim3(256), 0, st, a, a.ctas, RT);
     return e;
 }

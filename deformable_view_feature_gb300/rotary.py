@@ -14,34 +14,15 @@ there is no fallback.
 """
 from __future__ import annotations
 
-import ctypes
 import math
-import struct
 from typing import Optional
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import DA_BF16, DA_F16, DA_F32, _check, _dptr, _on_stream, load_library
-from .attention import _small, _strided
+from . import _binding, _on_stream
 
 __all__ = ["qkr_forward", "qkr_backward", "rotary_frequencies", "QkRotaryFunction"]
-
-_DTYPES = {torch.float32: DA_F32, torch.bfloat16: DA_BF16, torch.float16: DA_F16}
-
-
-class QkrProblem(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "num_queries", "num_keys", "num_heads", "num_kv_heads", "width",
-                                               "rotated", "dtype", "interleaved", "normed")]
-                + [("eps", ctypes.c_float), ("magnitude", ctypes.c_float), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
-                   ("q_stride", ctypes.c_int64 * 4), ("k_stride", ctypes.c_int64 * 4)]
-                + [(n, ctypes.c_void_p) for n in ("q_weight", "k_weight", "turns", "pos_q", "pos_k")])
-
-
-# The same as bytes, which take a fifth of the time to fill.
-_PROBLEM = struct.Struct("@10i2f2P8q5P")
-assert _PROBLEM.size == ctypes.sizeof(QkrProblem)
-
 
 def rotary_frequencies(rotated: int, base: float = 10000.0, stretch: float = 1.0, method: str = "linear",
                        original_length: Optional[int] = None, fast: float = 32.0, slow: float = 1.0) -> torch.Tensor:
@@ -83,62 +64,6 @@ def rotary_frequencies(rotated: int, base: float = 10000.0, stretch: float = 1.0
     return torch.tensor(of, dtype=torch.int64)
 
 
-def _problem(q, k, frequencies, q_weight, k_weight, pos_q, pos_k, eps, interleaved, magnitude) -> bytes:
-    """The qkr_problem of these arguments, after the checks that only the
-    tensors' shapes and types allow. q or k may be None."""
-    if q is None and k is None:
-        raise ValueError("there must be q or k")
-    one = k if q is None else q
-    at, dtype = one.get_device(), one.dtype
-    if dtype not in _DTYPES:
-        raise TypeError("q and k must be float32, bfloat16 or float16")
-    size, stride = [], []
-    for name, t in (("q", q), ("k", k)):
-        if t is None:
-            size.append((one.shape[0], 0, 1, 2, one.shape[-1]))
-            stride.append((0, 0, 0, 0))
-            continue
-        if t.dim() != 5 or t.shape[3] != 2:
-            raise ValueError(f"{name} must be [B, L, heads, 2, D]")
-        if t.dtype != dtype:
-            raise TypeError("q and k must have one type")
-        size.append(t.shape)
-        stride.append(t.stride()[:4])
-    if size[0][0] != size[1][0] or size[0][4] != size[1][4]:
-        raise ValueError("q and k disagree on batch or width")
-    for name, t, w, pos in (("q", q, q_weight, pos_q), ("k", k, k_weight, pos_k)):
-        if t is None and (w is not None or pos is not None):
-            raise ValueError(f"{name}_weight and pos_{name} go with {name}")
-    if eps is None and (q_weight is not None or k_weight is not None):
-        raise ValueError("a weight needs the norm (eps)")
-    B, Lq, H, _, D = size[0]
-    _, Lk, Hkv = size[1][:3]
-    pairs = 0
-    if frequencies is not None:
-        if frequencies.dim() != 1 or frequencies.dtype != torch.int64:
-            raise ValueError("frequencies must be int64 [rotated / 2] (rotary_frequencies)")
-        pairs = frequencies.shape[0]
-    wq, wk = _small(q_weight, "q_weight", (D,), torch.float32, at), _small(k_weight, "k_weight", (D,), torch.float32, at)
-    pq, pk = _small(pos_q, "pos_q", (B, Lq), torch.int32, at), _small(pos_k, "pos_k", (B, Lk), torch.int32, at)
-    return _PROBLEM.pack(B, Lq, Lk, H, Hkv, D, 2 * pairs, _DTYPES[dtype], 1 if interleaved else 0, 0 if eps is None else 1,
-                         0.0 if eps is None else eps, magnitude, 0 if q is None else _strided(q, "q", at),
-                         0 if k is None else _strided(k, "k", at), *stride[0], *stride[1], wq, wk,
-                         0 if frequencies is None else _dptr(frequencies, at) or 0, pq, pk)
-
-
-def _result(t, out, name):
-    """The output for t: `out`, or a new one."""
-    if t is None:
-        if out is not None:
-            raise ValueError(f"{name} has no input")
-        return None
-    if out is None:
-        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
-    if out.shape != t.shape or out.dtype != t.dtype:
-        raise ValueError(f"{name} must be {t.dtype} {tuple(t.shape)}")
-    return out
-
-
 def qkr_forward(q: Optional[torch.Tensor], k: Optional[torch.Tensor] = None, frequencies: Optional[torch.Tensor] = None,
                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
                 pos_q: Optional[torch.Tensor] = None, pos_k: Optional[torch.Tensor] = None, eps: Optional[float] = 1e-6,
@@ -155,14 +80,11 @@ def qkr_forward(q: Optional[torch.Tensor], k: Optional[torch.Tensor] = None, fre
     (2 i, 2 i + 1) with interleaved; magnitude multiplies the rotated channels.
     out_q and out_k may be q and k themselves where these are contiguous. What
     the call allocates belongs to the stream it runs on."""
-    lib = load_library()
-    p = _problem(q, k, frequencies, q_weight, k_weight, pos_q, pos_k, eps, interleaved, magnitude)
-    device = (k if q is None else q).device
-    with _on_stream(stream, device) as handle:
-        out_q, out_k = _result(q, out_q, "out_q"), _result(k, out_k, "out_k")
-        at = device.index
-        _check(lib.qkr_forward(p, _dptr(out_q, at), _dptr(out_k, at), handle))
-    return out_q, out_k
+    args = (q, k, frequencies, q_weight, k_weight, pos_q, pos_k, eps, interleaved, magnitude, out_q, out_k)
+    if stream is None:
+        return _binding().rotary_forward(*args)
+    with _on_stream(stream, (k if q is None else q).device):
+        return _binding().rotary_forward(*args)
 
 
 def qkr_backward(q: Optional[torch.Tensor], k: Optional[torch.Tensor], grad_out_q: Optional[torch.Tensor],
@@ -174,22 +96,11 @@ def qkr_backward(q: Optional[torch.Tensor], k: Optional[torch.Tensor], grad_out_
     were before it); returns (grad_q, grad_k, grad_q_weight, grad_k_weight), the
     first two contiguous in q's type, the others fp32 [D], None where there is
     no such input."""
-    lib = load_library()
-    p = _problem(q, k, frequencies, q_weight, k_weight, pos_q, pos_k, eps, interleaved, magnitude)
-    for name, t, g in (("grad_out_q", q, grad_out_q), ("grad_out_k", k, grad_out_k)):
-        if (t is None) != (g is None):
-            raise ValueError(f"{name} goes with its input")
-        if t is not None and (g.shape != t.shape or g.dtype != t.dtype):
-            raise ValueError(f"{name} must be {t.dtype} {tuple(t.shape)}")
-    device = (k if q is None else q).device
-    with _on_stream(stream, device) as handle:
-        gq, gk = _result(q, None, "grad_q"), _result(k, None, "grad_k")
-        gwq, gwk = (None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
-        given, n = (_dptr(grad_out_q, device.index), _dptr(grad_out_k, device.index)), ctypes.c_size_t(0)
-        _check(lib.qkr_workspace_size(p, ctypes.byref(n)))
-        ws = torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
-        _check(lib.qkr_backward(p, *given, _dptr(gq), _dptr(gk), _dptr(gwq), _dptr(gwk), _dptr(ws), n.value, handle))
-    return gq, gk, gwq, gwk
+    args = (q, k, frequencies, q_weight, k_weight, pos_q, pos_k, eps, interleaved, magnitude, grad_out_q, grad_out_k)
+    if stream is None:
+        return _binding().rotary_backward(*args)
+    with _on_stream(stream, (k if q is None else q).device):
+        return _binding().rotary_backward(*args)
 
 
 class QkRotaryFunction(torch.autograd.Function):

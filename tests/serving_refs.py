@@ -4,11 +4,47 @@ which the tests' tolerances are made. Plain torch; shares no code with the
 package. Tolerances count roundings as in operator_refs.py: U = 2^-24 is half a
 step of fp32, half_step(t) that of the tensors' type.
 """
+import ctypes
 import math
 
 import torch
 
 from operator_refs import U, half_step
+
+
+# The structures of include/qkr.h and include/paged.h, for tests of the C ABI.
+
+class QkrProblem(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "num_queries", "num_keys", "num_heads", "num_kv_heads", "width",
+                                               "rotated", "dtype", "interleaved", "normed")]
+                + [("eps", ctypes.c_float), ("magnitude", ctypes.c_float), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                   ("q_stride", ctypes.c_int64 * 4), ("k_stride", ctypes.c_int64 * 4)]
+                + [(n, ctypes.c_void_p) for n in ("q_weight", "k_weight", "turns", "pos_q", "pos_k")])
+
+
+class PgCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 4), ("v_stride", ctypes.c_int64 * 3),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("table_pages", ctypes.c_int32),
+                ("page_table", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("counts", ctypes.c_void_p)]
+
+
+class PgProblem(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "num_tokens", "num_heads", "num_kv_heads", "width", "value_width",
+                                               "dtype", "num_buckets", "reach", "causal")]
+                + [("scale", ctypes.c_float), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64 * 4), ("cache", PgCache)]
+                + [(n, ctypes.c_void_p) for n in ("lam", "bias_table", "bucket_map", "pos_q", "pos_k", "key_mask", "tree")])
+
+
+def serving_library(lib):
+    """libda.so with the argument types of the calls that the tests make themselves."""
+    vp = ctypes.c_void_p
+    size = ctypes.POINTER(ctypes.c_size_t)
+    for name, types in (("qkr_forward", [vp] * 4), ("qkr_workspace_size", [vp, size]), ("qkr_backward", [vp] * 8 + [ctypes.c_size_t, vp]),
+                        ("pg_append", [vp, vp, vp, ctypes.c_int32, vp, vp, vp]), ("pg_path", [vp]), ("pg_workspace_size", [vp, size]),
+                        ("pg_attention", [vp] * 3 + [ctypes.c_size_t, vp])):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = types, ctypes.c_int
+    return lib
 
 
 def radians(turns):
@@ -132,7 +168,8 @@ def paged_reference(q, k_cache, v_cache, lam, page_table, key_lengths, counts=No
         eps = U * (2 * (D / 4 + 16) * (big + 1) + 64 + L / 64)
         M = (p[:, 0] + lm.abs() * p[:, 1]) @ v.abs()
         out[b, :c] = res.permute(1, 0, 2)
-        tol[b, :c] = (M * (eps + r) + o * res.abs()).permute(1, 0, 2)
+        # Rounded weights p + e are divided by their own sum: off by sum e (v - out), at most r (M + |out|).
+        tol[b, :c] = (M * (eps + r) + (o + r) * res.abs()).permute(1, 0, 2)
     if dt != torch.float32:  # weights below fp16's normal numbers round to absolute steps
         tol += torch.finfo(dt).smallest_normal * torch.finfo(dt).eps * (1 + 8 * L ** 0.5)
     return {"out": out}, {"out": tol}

@@ -6,9 +6,8 @@ import pytest
 import torch
 
 import deformable_view_feature_gb300 as da
-from deformable_view_feature_gb300 import paged, rotary
 from operator_refs import check
-from serving_refs import paged_reference, qkr_reference
+from serving_refs import PgCache, PgProblem, QkrProblem, paged_reference, qkr_reference, serving_library
 
 DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 FAKE = 0x7F0000000000  # never dereferenced
@@ -17,7 +16,7 @@ FAKE = 0x7F0000000000  # never dereferenced
 @pytest.fixture(scope="module", autouse=True)
 def lib():
     da.build.build()
-    return da.load_library()
+    return serving_library(da.load_library())
 
 
 # ---- refusals and host logic: no GPU, nothing is launched ------------------
@@ -25,7 +24,7 @@ def lib():
 def _fake_cache(**kw):
     d = dict(k=FAKE, v=FAKE, num_pages=9, page_size=16, table_pages=4, page_table=FAKE, lengths=FAKE)
     d.update(kw)
-    c = paged.PgCache(**d)
+    c = PgCache(**d)
     c.k_stride[:] = (2048, 128, 64, 32)
     c.v_stride[:] = (2048, 128, 64)
     return c
@@ -35,7 +34,7 @@ def _problem(cache=None, q_stride=(1024, 256, 64, 32), **kw):
     d = dict(batch=2, num_tokens=4, num_heads=4, num_kv_heads=2, width=32, value_width=64, dtype=1, num_buckets=8, reach=16, causal=1,
              scale=0.1, q=FAKE, lam=FAKE, bias_table=FAKE, bucket_map=FAKE)
     d.update(kw)
-    p = paged.PgProblem(**d)
+    p = PgProblem(**d)
     p.q_stride[:] = q_stride
     p.cache = _fake_cache(**(cache or {}))
     return p
@@ -80,7 +79,7 @@ def test_appends_are_checked(lib):
         d = dict(batch=2, num_queries=4, num_keys=4, num_heads=4, num_kv_heads=2, width=32, rotated=32, dtype=1, normed=1, eps=1e-6,
                  magnitude=1.0, q=FAKE, k=FAKE, turns=FAKE)
         d.update(kw)
-        p = rotary.QkrProblem(**d)
+        p = QkrProblem(**d)
         p.q_stride[:] = q_stride
         p.k_stride[:] = (1024, 128, 64, 32)
         vp = ctypes.c_void_p
@@ -618,7 +617,7 @@ def test_training_through_the_rotary_norm_and_the_attention(kind):
     # In 16 bits: q, k, weights, s_m and results are each rounded once on the way, and scores move by D/4 such steps at most.
     r = 2e-5 if kind == "f32" else 8 * 2.0 ** -8
     for name, x, y in zip(("out", "q", "k", "v", "wq", "wk", "lam"), got, want):
-        assert float((x.double() - y).norm()) <= r * float(y.norm()), name
+        assert float((x.detach().double() - y.detach()).norm()) <= r * float(y.detach().norm()), name
 
 
 @pytest.mark.parametrize("kw,path", [

@@ -8,9 +8,8 @@ import pytest
 import torch
 
 import deformable_view_feature_gb300 as da
-from deformable_view_feature_gb300 import rotary
 from operator_refs import check
-from serving_refs import qkr_reference, radians
+from serving_refs import QkrProblem, qkr_reference, radians, serving_library
 
 DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 FAKE = 0x7F0000000000  # never dereferenced
@@ -19,7 +18,7 @@ FAKE = 0x7F0000000000  # never dereferenced
 @pytest.fixture(scope="module", autouse=True)
 def lib():
     da.build.build()
-    return da.load_library()
+    return serving_library(da.load_library())
 
 
 # ---- refusals and host logic: no GPU, nothing is launched ------------------
@@ -29,7 +28,7 @@ def _problem(**kw):
              magnitude=1.0, q=FAKE, k=FAKE, q_weight=FAKE, k_weight=FAKE, turns=FAKE)
     stride = kw.pop("q_stride", (1024, 256, 64, 32))
     d.update(kw)
-    p = rotary.QkrProblem(**d)
+    p = QkrProblem(**d)
     p.q_stride[:] = stride
     p.k_stride[:] = (1024, 128, 64, 32)
     return p
@@ -89,9 +88,15 @@ def test_binding_checks_shapes_and_types():
     with pytest.raises(ValueError, match="go with k"):
         da.qkr_forward(q, k_weight=w)
     with pytest.raises(ValueError, match="no input"):
-        rotary._result(None, k, "out_k")
+        da.qkr_forward(q, out_k=k)
     with pytest.raises(ValueError, match="out_k must be"):
-        rotary._result(k, k[:, :1], "out_k")
+        da.qkr_forward(q, k, out_k=k[:, :1])
+    with pytest.raises(ValueError, match="CUDA device"):
+        da.qkr_forward(q, k)
+    with pytest.raises(TypeError):
+        da.qkr_forward(q, [k])
+    with pytest.raises(TypeError):
+        da.qkr_forward(q, k, eps="x")
     for grads in ((q, None), (q[:, :2], k), (q.half(), k)):
         with pytest.raises(ValueError):
             da.qkr_backward(q, k, *grads)

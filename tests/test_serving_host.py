@@ -12,7 +12,7 @@ import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
 
 import deformable_view_feature_gb300 as da
-from deformable_view_feature_gb300 import paged, rotary
+from serving_refs import PgCache, PgProblem, QkrProblem, serving_library
 
 INCLUDE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
 
@@ -20,7 +20,7 @@ INCLUDE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__)
 @pytest.fixture(scope="module", autouse=True)
 def lib():
     da.build.build()
-    return da.load_library()
+    return serving_library(da.load_library())
 
 
 def test_library_exports_what_the_headers_declare(lib):
@@ -42,7 +42,7 @@ def test_headers_are_plain_c_and_structures_agree(tmp_path):
     exe = tmp_path / "use"
     subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", INCLUDE, str(src), "-o", str(exe)], check=True)
     got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
-    Q, C, P = rotary.QkrProblem, paged.PgCache, paged.PgProblem
+    Q, C, P = QkrProblem, PgCache, PgProblem
     assert got == [ctypes.sizeof(Q), Q.q_stride.offset, Q.turns.offset, ctypes.sizeof(C), C.page_table.offset, ctypes.sizeof(P),
                    P.cache.offset, P.tree.offset]
 
