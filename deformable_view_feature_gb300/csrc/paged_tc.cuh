@@ -17,8 +17,9 @@
 // second kernel joins them. The shares are made on the device, from lengths and
 // counts, so a captured graph stays balanced while its sequences grow.
 //
-// Warps: 0-3 for the weights of map 0 and 4-7 of map 1, 8 loads by TMA (a box lies in
-// one page: gcd(page size, 128) places), 9 issues the products. Weights go through shared memory, rounded to the inputs' type; tiles
+// Warps: 0-3 make the weights of map 0 and 4-7 of map 1, 8 loads keys by TMA and 10
+// values (a box lies in one page: gcd(page size, 128) places), 9 issues the scores'
+// products and 11 the sums', each as soon as what it needs is there. Weights go through shared memory, rounded to the inputs' type; tiles
 // of up to 32 rows, which memory bounds, carry what that took as a second operand.
 #pragma once
 
@@ -84,37 +85,38 @@ __device__ __forceinline__ void tmem_got(float (&v)[16])
                    "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
 }
 
-// A stage is [V | K_0 | K_1]: with VP = 64 the product's second 64 rows, which
-// nothing reads, are of K.
+// Shared memory: q, then rings of values and of keys, then weights. With VP = 64
+// the product's second 64 rows, which nothing reads, are whatever follows a
+// stage of values.
 template <int DP, int VP, int RT> struct PgShared {
-    static constexpr int threads = 2 * 128 + 64;
     static constexpr int row = DP * 2;                   // bytes of a row of q or k
-    static constexpr int q = RT * row, k = kStep * row;  // of one map
+    static constexpr int q = RT * row;                   // of one map
+    static constexpr int kmap = kStep * row;             // of one map's keys of a step
+    static constexpr int k = 2 * kmap;
     static constexpr int vblock = kStep * 128;           // of 64 columns of V
     static constexpr int v = VP / 64 * vblock;
-    static constexpr int stage = v + 2 * k;
     static constexpr bool rests = RT <= 32;              // weights carry what rounding took
     static constexpr int prow = RT == 16 ? 64 : 128;     // bytes of a key's row of weights
     static constexpr int p = kStep * 2 * RT * 2;         // of both maps' weights
     static constexpr int pbuf = p * (rests ? 2 : 1);
-    static constexpr int qbufs = RT == 64 ? 1 : 2;
-    static constexpr int pbufs = RT == 64 ? 2 : 1;
-    static constexpr int fixed = qbufs * 2 * q + pbufs * pbuf;
-    static constexpr int arrays = RT * 120 + 768 + (DP == 32 ? 6 : 3) * (48 + kStep * 4);  // the kernel's static ones, at most
-    static constexpr int room = 227 * 1024 - 1024 - kPgBias - arrays;  // 1024 for alignment
-    static constexpr int fit = (room - fixed) / stage;
-    static constexpr int stages = fit > (DP == 32 ? 6 : 3) ? (DP == 32 ? 6 : 3) : fit;
-    static constexpr int at_stage = qbufs * 2 * q, at_p = at_stage + stages * stage, bytes = at_p + pbufs * pbuf;
-    static_assert(stages >= 2 && bytes <= room, "shared memory");
+    // Steps that each ring holds, and the weights' buffers: what 227 KB allow.
+    // Values stay longer than keys, until a step's weights are made.
+    static constexpr int ks = DP == 32 ? 4 : RT == 16 ? 3 : 2, vs = DP == 32 ? 4 : RT <= 32 ? 3 : 2;
+    static constexpr int pbufs = RT == 64 || DP == 32 ? 2 : 1;
+    static constexpr int at_v = 2 * q, at_k = at_v + vs * v, at_p = at_k + ks * k, bytes = at_p + pbufs * pbuf;
+    static constexpr int arrays = RT * 128 + 3840;     // the kernel's static ones, at most
+    static_assert(bytes + 1024 + kPgBias + arrays <= 227 * 1024, "shared memory");
 };
+
+constexpr int kInfos = 6;  // of the steps' infos: two more than keys are ahead of the weights made from them
 
 // What passes a phase ahead has a barrier for even and one for odd steps; the
 // others' next phase cannot end before everyone has seen the last one.
-// empty[s]: the products with P of a step are done, and its stage is free.
 struct PgBars {
-    uint64_t q_full[2], q_empty[2];
-    uint64_t full[6], empty[6];
-    uint64_t s_full[2], p_full[2];
+    uint64_t q_full, q_empty;
+    uint64_t k_full[4], k_empty[4];  // empty: the step's scores are done
+    uint64_t v_full[4], v_empty[4];  // empty: its sums are done, and its weights' buffer is free
+    uint64_t s_full[2], p_full[2];   // scores, weights
     uint32_t tmem, gave_up;
 };
 
@@ -231,19 +233,6 @@ __device__ __forceinline__ bool vote(int m, bool flag)
 __device__ __forceinline__ void sync_map(int m) { asm volatile("bar.sync %0, 128;" ::"r"(1 + m) : "memory"); }
 __device__ __forceinline__ void sync_maps() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 
-// Whether a phase has ended, without waiting; the same in all lanes of a warp.
-// kIdle tests of nothing to do, some 100 ns each, end the wait (bar_wait).
-constexpr uint32_t kIdle = 10u << 20;
-__device__ __forceinline__ bool bar_test(uint64_t *bar, uint32_t parity, volatile uint32_t *gave_up)
-{
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok)
-                 : "r"(smem_addr(bar)), "r"(parity)
-                 : "memory");
-    return __all_sync(0xffffffffu, ok != 0 || *gave_up);
-}
-
 // Maximum over the warp, by the floats' order as integers.
 __device__ __forceinline__ float warp_max(float v)
 {
@@ -253,45 +242,51 @@ __device__ __forceinline__ float warp_max(float v)
     return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff);
 }
 
+constexpr int kPgThreads = 12 * 32;
+
 template <typename T, int DP, int VP, int RT>
-__global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
+__global__ void __launch_bounds__(kPgThreads, 1)
     paged_tc_kernel(const __grid_constant__ PagedTcArgs a, const __grid_constant__ CUtensorMap mq,
                     const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv)
 {
     using F = PgShared<DP, VP, RT>;
-    constexpr int NS = F::stages, kThreads = F::threads, kLoad = 8, kIssue = 9;
+    constexpr int NK = F::ks, NV = F::vs;
     constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t columns = RT == 16 ? 128 : RT == 32 ? 256 : 512;
     extern __shared__ unsigned char raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
     __shared__ PgBars bars;
-    __shared__ StepInfo infos[NS];
-    __shared__ int key_pos[NS][kStep];                     // where positions are given
+    __shared__ StepInfo infos[kInfos];
+    __shared__ int key_pos[kInfos][kStep];                 // where positions are given
     // Each map's rows.
     __shared__ __align__(16) float noff[2][RT];            // minus the row's reference
     __shared__ __align__(16) float off[2][2][RT];          // the same, with far_bias
     __shared__ __align__(16) float shrink[2][RT];
     __shared__ __align__(16) float wide[2][4][RT];         // a warp's maxima, or sums
     __shared__ __align__(16) float far_bias[2][2][RT];     // of keys `reach` or more before and after the query
-    __shared__ int row_pos[2][RT], row_l[2][RT], row_h[2][RT];
+    __shared__ __align__(16) int row_pos[2][RT], row_l[2][RT], row_h[2][RT];
+    __shared__ uint64_t row_tree[2][RT];                   // which of at most 64 new tokens the row sees
     __shared__ int64_t row_out[RT];                        // where the row's output is, or -1
-    __shared__ int64_t warp_total[kThreads / 32];
+    __shared__ int64_t warp_total[kPgThreads / 32];
     __shared__ int start[3];
     float *table = reinterpret_cast<float *>(base + F::bytes);  // [nb][H], times log2(e)
     uint16_t *bmap = reinterpret_cast<uint16_t *>(table + a.d.nb * a.d.H);
     const DattnArgs &d = a.d;
     const int warp = warp_number(), lane = threadIdx.x & 31;
+    pdl_trigger();  // the kernel that joins the pieces waits for this one's end, but not to be launched
 
     if (threadIdx.x == 0) {
+        bar_init(&bars.q_full, 1);
+        bar_init(&bars.q_empty, 1);
         for (int i = 0; i < 2; ++i) {
-            bar_init(&bars.q_full[i], 1);
-            bar_init(&bars.q_empty[i], 1);
             bar_init(&bars.s_full[i], 1);
             bar_init(&bars.p_full[i], 8);
         }
-        for (int s = 0; s < NS; ++s) {
-            bar_init(&bars.full[s], 1);
-            bar_init(&bars.empty[s], 1);
+        for (int s = 0; s < 4; ++s) {
+            bar_init(&bars.k_full[s], 1);
+            bar_init(&bars.k_empty[s], 1);
+            bar_init(&bars.v_full[s], 1);
+            bar_init(&bars.v_empty[s], 1);
         }
         bars.gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -299,29 +294,21 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
         tma_prefetch(&mk);
         tma_prefetch(&mv);
     }
-    if (warp == kIssue) tmem_alloc(&bars.tmem, columns);
-    for (int i = threadIdx.x; i < d.nb * d.H; i += kThreads) table[i] = d.table[i] * kLog2e;
-    for (int i = threadIdx.x; i < 2 * d.reach + 1 && d.nb; i += kThreads)
+    if (warp == 9) tmem_alloc(&bars.tmem, columns);
+    for (int i = threadIdx.x; i < d.nb * d.H; i += kPgThreads) table[i] = d.table[i] * kLog2e;
+    for (int i = threadIdx.x; i < 2 * d.reach + 1 && d.nb; i += kPgThreads)
         bmap[i] = static_cast<uint16_t>(min(max(d.bmap[i], 0), d.nb - 1) * d.H);
     // Rows of q that a tile's queries leave free.
     const int used = a.LP * d.G;
-    for (int i = threadIdx.x; i < F::qbufs * 2 * (RT - used) * (F::row / 16); i += kThreads) {
-        const int m = i / ((RT - used) * (F::row / 16)), rest = i - m * (RT - used) * (F::row / 16);
+    for (int i = threadIdx.x; i < 2 * (RT - used) * (F::row / 16); i += kPgThreads) {
+        const int m = i >= (RT - used) * (F::row / 16), rest = i - m * (RT - used) * (F::row / 16);
         *reinterpret_cast<uint4 *>(base + m * F::q + used * F::row + rest * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_async();
 
-    // Rows that see nothing: all heads' outputs of such tiles lie in a row.
     const int entries = d.B * a.row_tiles;
-    for (int e = blockIdx.x; e < entries; e += gridDim.x) {
-        const Tile t = tile_of(a, e);
-        if (t.steps) continue;
-        T *to = static_cast<T *>(d.out) + (static_cast<int64_t>(t.b) * d.Lq + t.l0) * d.H * d.Dv;
-        const int n = min(a.LP, d.Lq - t.l0) * d.H * d.Dv;
-        for (int i = threadIdx.x; i < n; i += kThreads) to[i] = dattn_round<T>(0.f);
-    }
     // The CTA's share: threads take consecutive tiles' units, a scan adds them up.
-    const int per = (entries + kThreads - 1) / kThreads;
+    const int per = (entries + kPgThreads - 1) / kPgThreads;
     const int e0 = min(static_cast<int>(threadIdx.x) * per, entries), e1 = min(e0 + per, entries);
     int64_t own = 0;
     for (int e = e0; e < e1; ++e) own += units(tile_of(a, e));
@@ -336,13 +323,14 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
     __syncthreads();
     fence_after();
     int64_t total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kPgThreads / 32; ++w) {
         if (w == warp) upto += total;
         total += warp_total[w];
     }
     // CTAs without a share are the last ones, so that a tile's pieces lie in CTAs in a row.
     const int64_t active = max(min(total, static_cast<int64_t>(gridDim.x)), int64_t{1}), cta = min(static_cast<int64_t>(blockIdx.x), active);
-    const int64_t from = total * cta / active, share = cta < active ? total * (cta + 1) / active - from : 0;
+    const int64_t each = total < INT32_MAX ? static_cast<uint32_t>(total) / static_cast<uint32_t>(active) : total / active;
+    const int64_t more = total - each * active, from = each * cta + min(cta, more), share = cta < active ? each + (cta < more) : 0;
     if (share > 0 && from < upto && from >= upto - own) {
         int64_t at = upto - own;
         int e = e0, u = 0;
@@ -359,28 +347,44 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
     const uint32_t tmem = uniform(bars.tmem);
     volatile uint32_t *gave_up = &bars.gave_up;
     const auto tS = [&](int m, int t) { return tmem + ((t & 1) * 2 + m) * RT; };
-    const uint32_t tO = tmem + 4 * RT;
+    const uint32_t tO = tmem + 4 * RT, sb = smem_addr(base);
     Walk w;
     w.start(a, share, start[0], start[1], start[2]);
 
-    if (warp == kLoad) {
-        const int boxes = kStep / a.box;  // of a step, one to a lane
-        const int blocks = (d.Dv + 63) / 64;
+    if (warp == 8 || warp == 10) {
+        // Copies of keys (and queries), and of values: a lane brings one box of a step.
+        const bool keys = warp == 8;
+        const int boxes = kStep / a.box, blocks = (d.Dv + 63) / 64;
         int t = 0, seg = 0;
         for (; w.left > 0; w.next(a), ++seg) {
-            const int qb = seg % F::qbufs;
-            bar_wait_warp(&bars.q_empty[qb], ((seg / F::qbufs) & 1) ^ 1, gave_up);
-            if (lane == 0) {
-                bar_expect(&bars.q_full[qb], 2 * F::row * used);
-                for (int m = 0; m < 2; ++m) tma_load(&mq, &bars.q_full[qb], base + (qb * 2 + m) * F::q, 0, m, w.n * d.G, w.t.l0, w.t.b);
+            if (keys) {
+                bar_wait_warp(&bars.q_empty, (seg & 1) ^ 1, gave_up);
+                if (lane == 0) {
+                    bar_expect(&bars.q_full, 2 * F::row * used);
+                    for (int m = 0; m < 2; ++m) tma_load(&mq, &bars.q_full, base + m * F::q, 0, m, w.n * d.G, w.t.l0, w.t.b);
+                }
             }
             for (int i = 0; i < w.steps; ++i, ++t) {
-                const int s = t % NS, j0 = (w.first + i) * kStep, j = j0 + lane * a.box;
+                const int j0 = (w.first + i) * kStep, j = j0 + lane * a.box;
                 int place = 0, page = -1;
                 if (lane < boxes && j < w.t.end) page = paged_page(d, w.t.b, j, place);
                 const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+                // The copies are issued before their bytes are expected, with
+                // which the phase's only arrival comes.
+                if (!keys) {
+                    const int s = t % NV;
+                    bar_wait_warp(&bars.v_empty[s], ((t / NV) & 1) ^ 1, gave_up);
+                    if (page >= 0)
+                        for (int c = 0; c < blocks; ++c)
+                            tma_load(&mv, &bars.v_full[s], base + F::at_v + s * F::v + c * F::vblock + lane * a.box * 128, c * 64, 0, w.n, place, page);
+                    __syncwarp();
+                    if (lane == 0) bar_expect(&bars.v_full[s], __popc(there) * a.box * blocks * 128);
+                    __syncwarp();
+                    continue;
+                }
+                const int s = t % NK;
                 uint32_t used_keys[4];
-                int pos[4];
+                int pos[4], lo[4], hi[4];
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int r = g * 32 + lane;
@@ -389,105 +393,91 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                     if (use && d.mask) use = d.mask[of] != 0;
                     pos[g] = use && d.pos_k ? d.pos_k[of] : j0 + r;
                     used_keys[g] = __ballot_sync(0xffffffffu, use);
-                }
-                int lo[4], hi[4];
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const bool use = used_keys[g] >> lane & 1;
                     lo[g] = __reduce_min_sync(0xffffffffu, use ? pos[g] : kFar);
                     hi[g] = __reduce_max_sync(0xffffffffu, use ? pos[g] : -kFar);
                 }
-                // The copies first: their bytes may arrive before they are expected, the phase ends after.
-                bar_wait_warp(&bars.empty[s], ((t / NS) & 1) ^ 1, gave_up);
-                if (page >= 0) {
-                    unsigned char *st = base + F::at_stage + s * F::stage;
-                    for (int m = 0; m < 2; ++m) tma_load(&mk, &bars.full[s], st + F::v + m * F::k + lane * a.box * F::row, 0, m, w.n, place, page);
-                    for (int c = 0; c < blocks; ++c) tma_load(&mv, &bars.full[s], st + c * F::vblock + lane * a.box * 128, c * 64, 0, w.n, place, page);
-                }
-                __syncwarp();
+                bar_wait_warp(&bars.k_empty[s], ((t / NK) & 1) ^ 1, gave_up);
+                if (page >= 0)
+                    for (int m = 0; m < 2; ++m)
+                        tma_load(&mk, &bars.k_full[s], base + F::at_k + s * F::k + m * F::kmap + lane * a.box * F::row, 0, m, w.n, place, page);
+                // Their last reader, the weights of kInfos steps ago, came before the scores that freed the keys' place.
+                StepInfo &info = infos[t % kInfos];
                 if (lane < 4) {
-                    infos[s].use[lane] = lane == 0 ? used_keys[0] : lane == 1 ? used_keys[1] : lane == 2 ? used_keys[2] : used_keys[3];
-                    infos[s].lo[lane] = lane == 0 ? lo[0] : lane == 1 ? lo[1] : lane == 2 ? lo[2] : lo[3];
-                    infos[s].hi[lane] = lane == 0 ? hi[0] : lane == 1 ? hi[1] : lane == 2 ? hi[2] : hi[3];
+                    info.use[lane] = lane == 0 ? used_keys[0] : lane == 1 ? used_keys[1] : lane == 2 ? used_keys[2] : used_keys[3];
+                    info.lo[lane] = lane == 0 ? lo[0] : lane == 1 ? lo[1] : lane == 2 ? lo[2] : lo[3];
+                    info.hi[lane] = lane == 0 ? hi[0] : lane == 1 ? hi[1] : lane == 2 ? hi[2] : hi[3];
                 }
                 if (d.pos_k)
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) key_pos[s][g * 32 + lane] = pos[g];
+                    for (int g = 0; g < 4; ++g) key_pos[t % kInfos][g * 32 + lane] = pos[g];
                 __syncwarp();
-                if (lane == 0) bar_expect(&bars.full[s], __popc(there) * a.box * (2 * F::row + blocks * 128));
+                if (lane == 0) bar_expect(&bars.k_full[s], __popc(there) * a.box * 2 * F::row);
                 __syncwarp();
             }
         }
         if (*gave_up) {  // leave no copy in flight
-            for (int i = max(0, seg - F::qbufs); i < seg; ++i) bar_drain(&bars.q_full[i % F::qbufs], (i / F::qbufs) & 1);
-            for (int i = max(0, t - NS); i < t; ++i) bar_drain(&bars.full[i % NS], (i / NS) & 1);
+            if (keys && seg > 0) bar_drain(&bars.q_full, (seg - 1) & 1);
+            const int n = keys ? NK : NV;
+            for (int i = max(0, t - n); i < t; ++i) bar_drain(keys ? &bars.k_full[i % n] : &bars.v_full[i % n], (i / n) & 1);
         }
-    } else if (warp == kIssue) {
-        // All lanes walk through the steps, one issues: addresses then stay in
-        // uniform registers.
+    } else if (warp == 9) {
+        // Scores. (All lanes walk through the steps, one issues: addresses then
+        // stay in uniform registers.)
         const bool issue = elect();
-        constexpr uint32_t is = shape(bf16, RT, false), io = shape(bf16, 2 * RT, true) | (1u << 15);
-        const uint32_t sb = smem_addr(base);
-        const Operand<F::row> dk = along_row<F::row>(sb + F::at_stage + F::v), dq = along_row<F::row>(sb);
-        const Operand<128> dv = over_rows<128>(sb + F::at_stage, F::vblock);
-        const Operand<F::prow> dp = over_rows<F::prow>(sb + F::at_p, F::p / 2);
-        // Scores of step u need its keys, and the weights of step u - 2 in
-        // place of the scores that they overwrite; sums of step t need its
-        // weights. Whichever can is issued next: sums that waited behind scores
-        // would hold their stage for as long as the next keys take to arrive.
-        Walk ws = w;
-        int u = 0, t = 0, at = 0, seg = 0, done = 0;  // scores and sums issued, scores of the segment, its number, sums of theirs
-        for (uint32_t idle = 0; w.left > 0;) {
-            const int qb = seg % F::qbufs;
-            if (ws.left > 0 && u <= t + 1 && bar_test(&bars.full[u % NS], (u / NS) & 1, gave_up) &&
-                (at > 0 || bar_test(&bars.q_full[qb], (seg / F::qbufs) & 1, gave_up))) {
-                const int s = u % NS;
-                const bool last = ++at == ws.steps;
+        constexpr uint32_t is = shape(bf16, RT, false);
+        const Operand<F::row> dk = along_row<F::row>(sb + F::at_k), dq = along_row<F::row>(sb);
+        int t = 0, seg = 0;
+        for (; w.left > 0; w.next(a), ++seg) {
+            bar_wait_warp(&bars.q_full, seg & 1, gave_up);
+            for (int i = 0; i < w.steps; ++i, ++t) {
+                const int s = t % NK;
+                bar_wait_warp(&bars.k_full[s], (t / NK) & 1, gave_up);
+                // Into the columns of two steps ago, which its weights have read.
+                if (t > 1) bar_wait_warp(&bars.p_full[t & 1], ((t >> 1) & 1) ^ 1, gave_up);
                 fence_after();
                 if (issue) {
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int i = 0; i < DP / 16; ++i)
-                            mma_ss(tS(m, u), dk.at(s * F::stage + m * F::k + i * 32), dq.at((qb * 2 + m) * F::q + i * 32), is, i > 0);
-                    mma_commit(&bars.s_full[u & 1]);
-                    if (last) mma_commit(&bars.q_empty[qb]);
+                        for (int c = 0; c < DP / 16; ++c)
+                            mma_ss(tS(m, t), dk.at(s * F::k + m * F::kmap + c * 32), dq.at(m * F::q + c * 32), is, c > 0);
+                    mma_commit(&bars.s_full[t & 1]);
+                    mma_commit(&bars.k_empty[s]);
+                    if (i == w.steps - 1) mma_commit(&bars.q_empty);
                 }
                 __syncwarp();
-                if (last) {
-                    ws.next(a);
-                    at = 0;
-                    ++seg;
-                }
-                ++u;
-                idle = 0;
-            } else if (t < u && bar_test(&bars.p_full[t & 1], (t >> 1) & 1, gave_up)) {
-                const int s = t % NS;
+            }
+        }
+        for (int i = max(0, t - NK); i < t; ++i) bar_drain(&bars.k_empty[i % NK], (i / NK) & 1);
+        __syncwarp();
+    } else if (warp == 11) {
+        // Sums.
+        const bool issue = elect();
+        constexpr uint32_t io = shape(bf16, 2 * RT, true) | (1u << 15);
+        const Operand<128> dv = over_rows<128>(sb + F::at_v, F::vblock);
+        const Operand<F::prow> dp = over_rows<F::prow>(sb + F::at_p, F::p / 2);
+        int t = 0;
+        for (; w.left > 0; w.next(a)) {
+            for (int i = 0; i < w.steps; ++i, ++t) {
+                const int s = t % NV;
                 const uint32_t pb = (t % F::pbufs) * F::pbuf;
+                bar_wait_warp(&bars.v_full[s], (t / NV) & 1, gave_up);
+                bar_wait_warp(&bars.p_full[t & 1], (t >> 1) & 1, gave_up);
                 fence_after();
                 if (issue) {
 #pragma unroll
-                    for (int k = 0; k < kStep / 16; ++k)
-                        mma_ss(tO, dv.at(s * F::stage + k * 16 * 128), dp.at(pb + k * 16 * F::prow), io, done > 0 || k > 0);
+                    for (int c = 0; c < kStep / 16; ++c)
+                        mma_ss(tO, dv.at(s * F::v + c * 16 * 128), dp.at(pb + c * 16 * F::prow), io, i > 0 || c > 0);
                     if (F::rests)
 #pragma unroll
-                        for (int k = 0; k < kStep / 16; ++k)
-                            mma_ss(tO, dv.at(s * F::stage + k * 16 * 128), dp.at(pb + F::p + k * 16 * F::prow), io, true);
-                    mma_commit(&bars.empty[s]);
+                        for (int c = 0; c < kStep / 16; ++c)
+                            mma_ss(tO, dv.at(s * F::v + c * 16 * 128), dp.at(pb + F::p + c * 16 * F::prow), io, true);
+                    mma_commit(&bars.v_empty[s]);
                 }
                 __syncwarp();
-                if (++done == w.steps) {
-                    w.next(a);
-                    done = 0;
-                }
-                ++t;
-                idle = 0;
-            } else {
-                if (++idle > kIdle) *gave_up = 1;
-                __nanosleep(20);  // leaves the SM's issue slots to the others
             }
         }
-        for (int i = max(0, t - NS); i < t; ++i) bar_drain(&bars.empty[i % NS], (i / NS) & 1);
+        for (int i = max(0, t - NV); i < t; ++i) bar_drain(&bars.v_empty[i % NV], (i / NV) & 1);
         __syncwarp();
     } else {
         // A thread has key kr of each step, and that key's scores of map m with all rows.
@@ -495,6 +485,17 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
         const int m = warp >> 2, kr = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float2 mul = {d.scale_log2, d.scale_log2};
+        // The sums with weights of step `of` are done.
+        const auto summed = [&](int of) { bar_wait_warp(&bars.v_empty[of % NV], (of / NV) & 1, gave_up); };
+        // Rows that see nothing: all heads' outputs of such tiles lie in a row.
+        for (int e = blockIdx.x; e < entries; e += gridDim.x) {
+            const Tile none = tile_of(a, e);
+            if (none.steps) continue;
+            T *to = static_cast<T *>(d.out) + (static_cast<int64_t>(none.b) * d.Lq + none.l0) * d.H * d.Dv;
+            const int n = min(a.LP, d.Lq - none.l0) * d.H * d.Dv;
+            for (int i = threadIdx.x; i < n; i += 256) to[i] = dattn_round<T>(0.f);
+        }
+        const bool few = d.pg.tree && d.Lq <= 64;  // the tree's rows are bits in shared memory
         int t = 0, slot_tile[2] = {-1, -1}, slot_last = 0;
         for (; w.left > 0; w.next(a)) {
             const Tile tile = w.t;
@@ -511,6 +512,13 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                 }
                 if (m == 0) row_out[kr] = kr < used && tile.l0 + dl < d.Lq ? ((static_cast<int64_t>(b) * d.Lq + l) * d.H + h) * d.Dv : -1;
             }
+            if (few && (w.first + w.steps) * kStep > old)
+                for (int r = warp & 3; r < used; r += 4) {
+                    const int l = min(tile.l0 + static_cast<int>(d.div_G.div(r)), d.Lq - 1);
+                    const uint8_t *of = d.pg.tree + (static_cast<int64_t>(b) * d.Lq + l) * d.Lq;
+                    const uint32_t low = __ballot_sync(0xffffffffu, lane < d.Lq && of[lane]), high = __ballot_sync(0xffffffffu, lane + 32 < d.Lq && of[lane + 32]);
+                    if (lane == 0) row_tree[m][r] = low | static_cast<uint64_t>(high) << 32;
+                }
             sync_map(m);
             int qmin = kFar, qmax = -kFar;
 #pragma unroll
@@ -526,27 +534,47 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
             for (int c = 0; c < RT / 2; ++c) sum[c] = {0.f, 0.f};
 #pragma unroll 1
             for (int i = 0; i < w.steps; ++i, ++t) {
-                const int s = t % NS, j = (w.first + i) * kStep + kr;
+                const int j = (w.first + i) * kStep + kr;
                 bar_wait_warp(&bars.s_full[t & 1], (t >> 1) & 1, gave_up);
                 fence_after();
-                const StepInfo &info = infos[s];
+                const StepInfo &info = infos[t % kInfos];
                 const uint32_t used_keys = info.use[warp & 3];
                 const bool use = used_keys >> lane & 1, all = used_keys == 0xffffffffu;
-                const int pos = d.pos_k ? key_pos[s][kr] : j, kmin = info.lo[warp & 3], kmax = info.hi[warp & 3];
+                const int pos = d.pos_k ? key_pos[t % kInfos][kr] : j, kmin = info.lo[warp & 3], kmax = info.hi[warp & 3];
                 // Whether every row sees all of the warp's keys, with one bias for each row.
                 const bool before = d.nb == 0 || kmax - qmin <= -d.reach, after = !before && kmin - qmax >= d.reach;
                 const bool fast = (before || after) && !(d.causal && kmax > qmin) && !(d.pg.tree && (j - lane + 31) >= old);
                 // Scores of rows c0 .. in base 2, less the rows' references (or not).
                 const auto finish = [&](float (&x)[X], int c0, bool less) {
-                    bool leaf = true;
+                    uint32_t see = use ? 0xffffffffu : 0u;
+                    if (d.causal)
+#pragma unroll
+                        for (int c = 0; c < X; ++c)
+                            if (pos > row_pos[m][c0 + c]) see &= ~(1u << c);
+                    if (d.pg.tree && use && j >= old) {
+                        if (few) {
+#pragma unroll
+                            for (int c = 0; c < X; ++c)
+                                if (!(row_tree[m][c0 + c] >> (j - old) & 1)) see &= ~(1u << c);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < X; ++c)
+                                if (!d.pg.tree[(static_cast<int64_t>(b) * d.Lq + row_l[m][c0 + c]) * d.Lq + j - old]) see &= ~(1u << c);
+                        }
+                    }
+                    float bias[X];
+                    if (fast || d.nb == 0) {
+#pragma unroll
+                        for (int c = 0; c < X; ++c) bias[c] = far_bias[m][after][c0 + c];
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < X; ++c)
+                            bias[c] = table[bmap[min(max(pos - row_pos[m][c0 + c], -d.reach), d.reach) + d.reach] + row_h[m][c0 + c]];
+                    }
 #pragma unroll
                     for (int c = 0; c < X; ++c) {
-                        const int r = c0 + c, rel = pos - row_pos[m][r];
-                        if (d.pg.tree && use && j >= old && (c == 0 || row_l[m][r] != row_l[m][r - 1]))
-                            leaf = d.pg.tree[(static_cast<int64_t>(b) * d.Lq + row_l[m][r]) * d.Lq + j - old] != 0;
-                        const float bias = fast || !d.nb ? far_bias[m][after][r] : table[bmap[min(max(rel, -d.reach), d.reach) + d.reach] + row_h[m][r]];
-                        const float y = fmaf(x[c], mul.x, bias) + (less ? noff[m][r] : 0.f);
-                        x[c] = use && leaf && !(d.causal && rel > 0) ? y : -INFINITY;
+                        const float y = fmaf(x[c], mul.x, bias[c]) + (less ? noff[m][c0 + c] : 0.f);
+                        x[c] = see >> c & 1 ? y : -INFINITY;
                     }
                 };
                 // The step's weights; once more where one would be too large for
@@ -622,7 +650,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                     }
                     sync_map(m);
                     if (i > 0) {
-                        bar_wait_warp(&bars.empty[(t - 1) % NS], ((t - 1) / NS) & 1, gave_up);
+                        summed(t - 1);
                         fence_after();
 #pragma unroll 1
                         for (int c0 = 0; c0 < RT; c0 += 16) {
@@ -643,10 +671,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                     sum[c] = add2(sum[c], unpack2<T>(hi[c]));
                     if constexpr (F::rests) sum[c] = add2(sum[c], unpack2<T>(lo[c]));
                 }
-                // The weights' buffer is free when the products before have read
-                // it: those two steps ago, for which the scores' barrier stands
-                // too, or with one buffer those of the last step.
-                if (F::pbufs == 1 && t > 0) bar_wait_warp(&bars.empty[(t - 1) % NS], ((t - 1) / NS) & 1, gave_up);
+                if (t >= F::pbufs) summed(t - F::pbufs);  // the weights' buffer is free
                 unsigned char *pt = base + F::at_p + (t % F::pbufs) * F::pbuf + (RT == 64 ? m * (F::p / 2) : 0) + kr * F::prow;
                 const int swz = RT == 16 ? (kr >> 1) & 3 : kr & 7, piece0 = RT == 64 ? 0 : m * RT / 8;
 #pragma unroll
@@ -657,8 +682,8 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                 }
                 if (!all && m < VP / 64) {
                     // 0 * NaN is NaN: unused keys' rows of V become zeros.
-                    bar_wait_warp(&bars.full[s], (t / NS) & 1, gave_up);
-                    unsigned char *v = base + F::at_stage + s * F::stage + m * F::vblock + kr * 128;
+                    bar_wait_warp(&bars.v_full[t % NV], (t / NV) & 1, gave_up);
+                    unsigned char *v = base + F::at_v + (t % NV) * F::v + m * F::vblock + kr * 128;
                     if (!use)
 #pragma unroll
                         for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(v + (((c + lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -684,7 +709,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                     for (int c = 0; c < RT / 32; ++c) wide[m][warp & 3][lane * (RT / 32) + c] = all_sums[c];
                 }
             }
-            bar_wait_warp(&bars.empty[(t - 1) % NS], ((t - 1) / NS) & 1, gave_up);
+            summed(t - 1);
             fence_after();
             sync_maps();
             const bool whole = w.first == 0 && w.steps == tile.steps;
@@ -739,7 +764,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
     }
     fence_before();
     __syncthreads();
-    if (warp == kIssue) {
+    if (warp == 9) {
         fence_after();
         tmem_free(tmem, columns);
     }
@@ -747,62 +772,84 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
 }
 
 // Joins a tile's pieces: the one that begins it is in the second slot of CTA
-// blockIdx.x, the others in the first slots of the CTAs after it. A block per
-// row, its warps share the pieces.
-template <typename T> __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedTcArgs a, int ctas, int RT)
+// blockIdx.x, the others in the first slots of the CTAs after it. A warp takes
+// two rows, or with many pieces the block's warps share each row's.
+constexpr int kJoinRows = 16, kJoinMany = 24;
+
+template <typename T> __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedTcArgs a)
 {
     pdl_wait();
     const DattnArgs &d = a.d;
-    const int c = blockIdx.x, r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v = lane * 4;
     const int tile = a.slots[c * 4 + 2];
-    if (tile < 0 || r >= a.LP * d.G) return;
-    const int e = tile / d.Hkv, n = tile - e * d.Hkv, b = e / a.row_tiles;
-    const int dl = static_cast<int>(d.div_G.div(r)), l = (e - b * a.row_tiles) * a.LP + dl, h = n * d.G + r - dl * d.G;
-    if (l >= d.Lq) return;
-    int pieces = ctas - c;
-    for (int i = 1; i < ctas - c; i += 32) {
-        const bool last = i + lane < ctas - c && a.slots[(c + i + lane) * 4 + 1];
-        const uint32_t any = __ballot_sync(0xffffffffu, last);
+    if (tile < 0) return;
+    const int e = tile / d.Hkv, n = tile - e * d.Hkv, b = e / a.row_tiles, l0 = (e - b * a.row_tiles) * a.LP;
+    int pieces = a.ctas - c;
+    for (int i = 1; i < a.ctas - c; i += 32) {
+        const uint32_t any = __ballot_sync(0xffffffffu, i + lane < a.ctas - c && a.slots[(c + i + lane) * 4 + 1]);
         if (any) {
             pieces = i + __ffs(any);
             break;
         }
     }
-    const auto slot = [&](int i) { return i == 0 ? static_cast<int64_t>(c) * 2 + 1 : static_cast<int64_t>(c + i) * 2; };
-    const auto ml = [&](int i, int m) { return *reinterpret_cast<const float2 *>(d.part_ml + ((slot(i) * RT + r) * 2 + m) * 2); };
-    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-    for (int i = lane; i < pieces; i += 32)
-        for (int m = 0; m < 2; ++m) top[m] = fmaxf(top[m], ml(i, m).x);
-    for (int m = 0; m < 2; ++m) {
-        for (int o = 16; o; o >>= 1) top[m] = fmaxf(top[m], __shfl_xor_sync(0xffffffffu, top[m], o));
-        for (int i = lane; i < pieces; i += 32) {
-            const float2 x = ml(i, m);
-            sum[m] = fmaf(x.y, ex2(x.x - top[m]), sum[m]);
-        }
-        for (int o = 16; o; o >>= 1) sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], o);
-    }
+    const int count = paged_count(d, b);
+    const bool many = pieces > kJoinMany;
     __shared__ float part[8][2][128];
-    const int v = lane * 4;
-    float4 o[2] = {};
-    if (v < d.Dv)
-        for (int i = warp; i < pieces; i += 8)
-            for (int m = 0; m < 2; ++m) {
-                const float f = ex2(ml(i, m).x - top[m]);
-                const float4 x = *reinterpret_cast<const float4 *>(d.part_o + ((slot(i) * RT + r) * 2 + m) * d.Dv + v);
-                o[m].x = fmaf(x.x, f, o[m].x);
-                o[m].y = fmaf(x.y, f, o[m].y);
-                o[m].z = fmaf(x.z, f, o[m].z);
-                o[m].w = fmaf(x.w, f, o[m].w);
+    const int rows = min(a.LP * d.G - static_cast<int>(blockIdx.y) * kJoinRows, kJoinRows);
+    for (int k = many ? 0 : warp; k < rows; k += many ? 1 : 8) {
+        const int r = blockIdx.y * kJoinRows + k, dl = static_cast<int>(d.div_G.div(r)), l = l0 + dl, h = n * d.G + r - dl * d.G;
+        if (l >= d.Lq) break;
+        const auto slot = [&](int i) { return i == 0 ? static_cast<int64_t>(c) * 2 + 1 : static_cast<int64_t>(c + i) * 2; };
+        const auto ml = [&](int i, int m) { return *reinterpret_cast<const float2 *>(d.part_ml + ((slot(i) * a.RT + r) * 2 + m) * 2); };
+        float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+        for (int i = lane; i < pieces; i += 32)
+            for (int m = 0; m < 2; ++m) top[m] = fmaxf(top[m], ml(i, m).x);
+        for (int m = 0; m < 2; ++m) {
+            for (int o = 16; o; o >>= 1) top[m] = fmaxf(top[m], __shfl_xor_sync(0xffffffffu, top[m], o));
+            for (int i = lane; i < pieces; i += 32) {
+                const float2 x = ml(i, m);
+                sum[m] = fmaf(x.y, ex2(x.x - top[m]), sum[m]);
             }
-    for (int m = 0; m < 2; ++m) *reinterpret_cast<float4 *>(&part[warp][m][v]) = o[m];
-    __syncthreads();
-    if (static_cast<int>(threadIdx.x) >= d.Dv) return;
-    float x[2] = {0.f, 0.f};
-    for (int m = 0; m < 2; ++m)
-        for (int i = 0; i < 8; ++i) x[m] += part[i][m][threadIdx.x];
-    const float out = (sum[0] == 0.f ? 0.f : x[0] / sum[0]) - d.lam[h] * (sum[1] == 0.f ? 0.f : x[1] / sum[1]);
-    static_cast<T *>(d.out)[((static_cast<int64_t>(b) * d.Lq + l) * d.H + h) * d.Dv + threadIdx.x] =
-        dattn_round<T>(l < paged_count(d, b) ? out : 0.f);
+            for (int o = 16; o; o >>= 1) sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], o);
+        }
+        float4 o[2] = {};
+        if (v < d.Dv)
+#pragma unroll 4
+            for (int i = many ? warp : 0; i < pieces; i += many ? 8 : 1)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const float f = ex2(ml(i, m).x - top[m]);
+                    const float4 x = *reinterpret_cast<const float4 *>(d.part_o + ((slot(i) * a.RT + r) * 2 + m) * d.Dv + v);
+                    o[m].x = fmaf(x.x, f, o[m].x);
+                    o[m].y = fmaf(x.y, f, o[m].y);
+                    o[m].z = fmaf(x.z, f, o[m].z);
+                    o[m].w = fmaf(x.w, f, o[m].w);
+                }
+        if (many) {
+            for (int m = 0; m < 2; ++m) *reinterpret_cast<float4 *>(&part[warp][m][v]) = o[m];
+            __syncthreads();
+            for (int m = 0; m < 2; ++m) {
+                o[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int i = 0; i < 8; ++i) {
+                    const float4 x = *reinterpret_cast<const float4 *>(&part[i][m][v]);
+                    o[m].x += x.x;
+                    o[m].y += x.y;
+                    o[m].z += x.z;
+                    o[m].w += x.w;
+                }
+            }
+            __syncthreads();
+        }
+        if (v < d.Dv && (!many || warp == 0)) {
+            const float f0 = sum[0] == 0.f || l >= count ? 0.f : 1.f / sum[0], f1 = sum[1] == 0.f || l >= count ? 0.f : d.lam[h] / sum[1];
+            const auto out = [&](float x, float y) { return dattn_round<T>((f0 == 0.f ? 0.f : x * f0) - (f1 == 0.f ? 0.f : y * f1)); };
+            T *to = static_cast<T *>(d.out) + ((static_cast<int64_t>(b) * d.Lq + l) * d.H + h) * d.Dv + v;
+            to[0] = out(o[0].x, o[1].x);
+            to[1] = out(o[0].y, o[1].y);
+            to[2] = out(o[0].z, o[1].z);
+            to[3] = out(o[0].w, o[1].w);
+        }
+    }
 }
 
 template <typename T, int DP, int VP, int RT>
@@ -813,10 +860,10 @@ cudaError_t launch_tc(const PagedTcArgs &a, const CUtensorMap &mq, const CUtenso
     const auto kernel = paged_tc_kernel<T, DP, VP, RT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    kernel<<<a.ctas, F::threads, smem, st>>>(a, mq, mk, mv);
+    kernel<<<a.ctas, kPgThreads, smem, st>>>(a, mq, mk, mv);
     e = cudaGetLastError();
     if (e == cudaSuccess && a.ctas > 1 && a.d.Lk > kStep)  // otherwise no tile has pieces
-        e = launch_pdl(paged_join_kernel<T>, dim3(a.ctas, a.LP * a.d.G), dim3(256), 0, st, a, a.ctas, RT);
+        e = launch_pdl(paged_join_kernel<T>, dim3(a.ctas, (a.LP * a.d.G + kJoinRows - 1) / kJoinRows), dim3(256), 0, st, a);
     return e;
 }
 
