@@ -233,13 +233,12 @@ __device__ __forceinline__ bool vote(int m, bool flag)
 __device__ __forceinline__ void sync_map(int m) { asm volatile("bar.sync %0, 128;" ::"r"(1 + m) : "memory"); }
 __device__ __forceinline__ void sync_maps() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 
-// Maximum over the warp, by the floats' order as integers.
+// Maximum over the warp; a NaN counts for nothing.
 __device__ __forceinline__ float warp_max(float v)
 {
-    int i = __float_as_int(v);
-    i = i >= 0 ? i : i ^ 0x7fffffff;
-    i = __reduce_max_sync(0xffffffffu, i);
-    return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff);
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 constexpr int kPgThreads = 12 * 32;
@@ -541,6 +540,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 const uint32_t used_keys = info.use[warp & 3];
                 const bool use = used_keys >> lane & 1, all = used_keys == 0xffffffffu;
                 const int pos = d.pos_k ? key_pos[t % kInfos][kr] : j, kmin = info.lo[warp & 3], kmax = info.hi[warp & 3];
+                float x[2][X];
+                tmem_load(tS(m, t) + lanes, x[0]);
                 // Whether every row sees all of the warp's keys, with one bias for each row.
                 const bool before = d.nb == 0 || kmax - qmin <= -d.reach, after = !before && kmin - qmax >= d.reach;
                 const bool fast = (before || after) && !(d.causal && kmax > qmin) && !(d.pg.tree && (j - lane + 31) >= old);
@@ -578,7 +579,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                     }
                 };
                 // The step's weights; once more where one would be too large for
-                // its row's reference.
+                // its row's reference. A segment begins with references.
                 uint32_t hi[RT / 2], lo[F::rests ? RT / 2 : 1];
                 const auto weigh = [&](const float (&x)[X], int c0) {
 #pragma unroll
@@ -594,15 +595,16 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 };
 #pragma unroll 1
                 for (bool again = false;; again = true) {
-                    float x[2][X], top[2] = {-INFINITY, -INFINITY};
-                    if (fast && all) {
+                    float top[2] = {-INFINITY, -INFINITY};
+                    if (i == 0 && !again) {
+                        top[0] = INFINITY;
+                    } else if (fast && all) {
                         // Most steps: no branches, for the sake of the order of instructions.
                         const float *o = off[m][after];
-                        tmem_ask(tS(m, t) + lanes, x[0]);
 #pragma unroll
                         for (int c0 = 0; c0 < RT; c0 += X) {
                             float (&y)[X] = x[c0 / X % 2];
-                            tmem_got(y);
+                            if (c0 > 0) tmem_got(y);
                             if (c0 + X < RT) tmem_ask(tS(m, t) + c0 + X + lanes, x[(c0 / X + 1) % 2]);
 #pragma unroll
                             for (int c = 0; c < X; c += 4) {
@@ -620,24 +622,27 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                     } else {
 #pragma unroll
                         for (int c0 = 0; c0 < RT; c0 += X) {
-                            tmem_load(tS(m, t) + c0 + lanes, x[0]);
+                            if (c0 > 0) tmem_load(tS(m, t) + c0 + lanes, x[0]);
                             finish(x[0], c0, true);
 #pragma unroll
                             for (int c = 0; c < X; c += 2) top[0] = max3(top[0], x[0][c], x[0][c + 1]);
                             weigh(x[0], c0);
                         }
                     }
-                    if (again || !vote(m, fmaxf(top[0], top[1]) > kLift<T> + kSlack)) break;
+                    if (again || (i > 0 && !vote(m, fmaxf(top[0], top[1]) > kLift<T> + kSlack))) break;
 #pragma unroll 1
                     for (int c0 = 0; c0 < RT; c0 += X) {
                         tmem_load(tS(m, t) + c0 + lanes, x[0]);
                         finish(x[0], c0, false);
+                        float best = -INFINITY;  // of row c0 + lane
 #pragma unroll
                         for (int c = 0; c < X; ++c) {
-                            const float best = warp_max(x[0][c]);
-                            if (lane == c) wide[m][warp & 3][c0 + c] = best;
+                            const float of = warp_max(x[0][c]);
+                            best = lane == c ? of : best;
                         }
+                        if (lane < X) wide[m][warp & 3][c0 + lane] = best;
                     }
+                    tmem_load(tS(m, t) + lanes, x[0]);
                     sync_map(m);
                     if (kr < RT) {
                         const float best = fmaxf(fmaxf(wide[m][0][kr], wide[m][1][kr]), fmaxf(wide[m][2][kr], wide[m][3][kr]));
@@ -772,84 +777,74 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 }
 
 // Joins a tile's pieces: the one that begins it is in the second slot of CTA
-// blockIdx.x, the others in the first slots of the CTAs after it. A warp takes
-// two rows, or with many pieces the block's warps share each row's.
-constexpr int kJoinRows = 16, kJoinMany = 24;
+// blockIdx.x, the others in the first slots of the CTAs after it. A warp per row;
+// what it reads depends on two loads before.
+constexpr int kJoinRows = 8;
 
-template <typename T> __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedTcArgs a)
+template <typename T> __global__ void __launch_bounds__(32 * kJoinRows) paged_join_kernel(const __grid_constant__ PagedTcArgs a)
 {
-    pdl_wait();
     const DattnArgs &d = a.d;
-    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v = lane * 4;
+    const int c = blockIdx.x, lane = threadIdx.x & 31, v = lane * 4, r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+    if (r >= a.LP * d.G) return;
+    pdl_wait();
     const int tile = a.slots[c * 4 + 2];
+    int last = lane > 0 && c + lane < a.ctas ? a.slots[(c + lane) * 4 + 1] : 0, pieces = a.ctas - c;
     if (tile < 0) return;
-    const int e = tile / d.Hkv, n = tile - e * d.Hkv, b = e / a.row_tiles, l0 = (e - b * a.row_tiles) * a.LP;
-    int pieces = a.ctas - c;
-    for (int i = 1; i < a.ctas - c; i += 32) {
-        const uint32_t any = __ballot_sync(0xffffffffu, i + lane < a.ctas - c && a.slots[(c + i + lane) * 4 + 1]);
+    for (int i = 0; i < a.ctas - c; i += 32) {
+        if (i > 0) last = c + i + lane < a.ctas ? a.slots[(c + i + lane) * 4 + 1] : 0;
+        const uint32_t any = __ballot_sync(0xffffffffu, last);
         if (any) {
             pieces = i + __ffs(any);
             break;
         }
     }
-    const int count = paged_count(d, b);
-    const bool many = pieces > kJoinMany;
-    __shared__ float part[8][2][128];
-    const int rows = min(a.LP * d.G - static_cast<int>(blockIdx.y) * kJoinRows, kJoinRows);
-    for (int k = many ? 0 : warp; k < rows; k += many ? 1 : 8) {
-        const int r = blockIdx.y * kJoinRows + k, dl = static_cast<int>(d.div_G.div(r)), l = l0 + dl, h = n * d.G + r - dl * d.G;
-        if (l >= d.Lq) break;
-        const auto slot = [&](int i) { return i == 0 ? static_cast<int64_t>(c) * 2 + 1 : static_cast<int64_t>(c + i) * 2; };
-        const auto ml = [&](int i, int m) { return *reinterpret_cast<const float2 *>(d.part_ml + ((slot(i) * a.RT + r) * 2 + m) * 2); };
-        float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-        for (int i = lane; i < pieces; i += 32)
-            for (int m = 0; m < 2; ++m) top[m] = fmaxf(top[m], ml(i, m).x);
-        for (int m = 0; m < 2; ++m) {
-            for (int o = 16; o; o >>= 1) top[m] = fmaxf(top[m], __shfl_xor_sync(0xffffffffu, top[m], o));
-            for (int i = lane; i < pieces; i += 32) {
-                const float2 x = ml(i, m);
-                sum[m] = fmaf(x.y, ex2(x.x - top[m]), sum[m]);
-            }
-            for (int o = 16; o; o >>= 1) sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], o);
-        }
-        float4 o[2] = {};
-        if (v < d.Dv)
-#pragma unroll 4
-            for (int i = many ? warp : 0; i < pieces; i += many ? 8 : 1)
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const float f = ex2(ml(i, m).x - top[m]);
-                    const float4 x = *reinterpret_cast<const float4 *>(d.part_o + ((slot(i) * a.RT + r) * 2 + m) * d.Dv + v);
-                    o[m].x = fmaf(x.x, f, o[m].x);
-                    o[m].y = fmaf(x.y, f, o[m].y);
-                    o[m].z = fmaf(x.z, f, o[m].z);
-                    o[m].w = fmaf(x.w, f, o[m].w);
-                }
-        if (many) {
-            for (int m = 0; m < 2; ++m) *reinterpret_cast<float4 *>(&part[warp][m][v]) = o[m];
-            __syncthreads();
-            for (int m = 0; m < 2; ++m) {
-                o[m] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int i = 0; i < 8; ++i) {
-                    const float4 x = *reinterpret_cast<const float4 *>(&part[i][m][v]);
-                    o[m].x += x.x;
-                    o[m].y += x.y;
-                    o[m].z += x.z;
-                    o[m].w += x.w;
-                }
-            }
-            __syncthreads();
-        }
-        if (v < d.Dv && (!many || warp == 0)) {
-            const float f0 = sum[0] == 0.f || l >= count ? 0.f : 1.f / sum[0], f1 = sum[1] == 0.f || l >= count ? 0.f : d.lam[h] / sum[1];
-            const auto out = [&](float x, float y) { return dattn_round<T>((f0 == 0.f ? 0.f : x * f0) - (f1 == 0.f ? 0.f : y * f1)); };
-            T *to = static_cast<T *>(d.out) + ((static_cast<int64_t>(b) * d.Lq + l) * d.H + h) * d.Dv + v;
-            to[0] = out(o[0].x, o[1].x);
-            to[1] = out(o[0].y, o[1].y);
-            to[2] = out(o[0].z, o[1].z);
-            to[3] = out(o[0].w, o[1].w);
-        }
+    const int e = tile / d.Hkv, n = tile - e * d.Hkv, b = e / a.row_tiles, dl = static_cast<int>(d.div_G.div(r));
+    const int l = (e - b * a.row_tiles) * a.LP + dl, h = n * d.G + r - dl * d.G;
+    if (l >= d.Lq) return;
+    const auto slot = [&](int i) { return i == 0 ? static_cast<int64_t>(c) * 2 + 1 : static_cast<int64_t>(c + i) * 2; };
+    const auto ml = [&](int i) {  // of both maps
+        return i < pieces ? *reinterpret_cast<const float4 *>(d.part_ml + (slot(i) * a.RT + r) * 4) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    };
+    float4 w = ml(lane);
+    float top[2] = {w.x, w.z};
+    for (int i = lane + 32; i < pieces; i += 32) {
+        const float4 x = ml(i);
+        top[0] = fmaxf(top[0], x.x);
+        top[1] = fmaxf(top[1], x.z);
     }
+    for (int m = 0; m < 2; ++m) top[m] = warp_max(top[m]);
+    float sum[2] = {0.f, 0.f};
+    float4 o[2] = {};
+    for (int base = 0; base < pieces; base += 32) {
+        if (base > 0) w = ml(base + lane);
+        const float f[2] = {ex2(w.x - top[0]), ex2(w.z - top[1])};
+        sum[0] = fmaf(w.y, f[0], sum[0]);
+        sum[1] = fmaf(w.w, f[1], sum[1]);
+        const int here = min(pieces - base, 32);
+#pragma unroll 4
+        for (int i = 0; i < here; ++i)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const float g = __shfl_sync(0xffffffffu, f[m], i);
+                if (v >= d.Dv) continue;
+                const float4 x = *reinterpret_cast<const float4 *>(d.part_o + ((slot(base + i) * a.RT + r) * 2 + m) * d.Dv + v);
+                o[m].x = fmaf(x.x, g, o[m].x);
+                o[m].y = fmaf(x.y, g, o[m].y);
+                o[m].z = fmaf(x.z, g, o[m].z);
+                o[m].w = fmaf(x.w, g, o[m].w);
+            }
+    }
+    for (int m = 0; m < 2; ++m)
+        for (int k = 16; k; k >>= 1) sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], k);
+    if (v >= d.Dv) return;
+    const bool live = l < paged_count(d, b);
+    const float f0 = sum[0] == 0.f || !live ? 0.f : 1.f / sum[0], f1 = sum[1] == 0.f || !live ? 0.f : d.lam[h] / sum[1];
+    const auto out = [&](float x, float y) { return dattn_round<T>((f0 == 0.f ? 0.f : x * f0) - (f1 == 0.f ? 0.f : y * f1)); };
+    T *to = static_cast<T *>(d.out) + ((static_cast<int64_t>(b) * d.Lq + l) * d.H + h) * d.Dv + v;
+    to[0] = out(o[0].x, o[1].x);
+    to[1] = out(o[0].y, o[1].y);
+    to[2] = out(o[0].z, o[1].z);
+    to[3] = out(o[0].w, o[1].w);
 }
 
 template <typename T, int DP, int VP, int RT>
@@ -863,7 +858,7 @@ cudaError_t launch_tc(const PagedTcArgs &a, const CUtensorMap &mq, const CUtenso
     kernel<<<a.ctas, kPgThreads, smem, st>>>(a, mq, mk, mv);
     e = cudaGetLastError();
     if (e == cudaSuccess && a.ctas > 1 && a.d.Lk > kStep)  // otherwise no tile has pieces
-        e = launch_pdl(paged_join_kernel<T>, dim3(a.ctas, (a.LP * a.d.G + kJoinRows - 1) / kJoinRows), dim3(256), 0, st, a);
+        e = launch_pdl(paged_join_kernel<T>, dim3(a.ctas, (a.LP * a.d.G + kJoinRows - 1) / kJoinRows), dim3(32 * kJoinRows), 0, st, a);
     return e;
 }
 
