@@ -17,9 +17,10 @@
 // second kernel joins them. The shares are made on the device, from lengths and
 // counts, so a captured graph stays balanced while its sequences grow.
 //
-// Warps: 0-3 make the weights of map 0 and 4-7 of map 1, 8 loads keys by TMA and 10
-// values (a box lies in one page: gcd(page size, 128) places), 9 issues the scores'
-// products and 11 the sums', each as soon as what it needs is there. Weights go through shared memory, rounded to the inputs' type; tiles
+// Warps: groups of four make the weights of up to 32 rows of a map; of four more,
+// one loads keys by TMA and one values (a box lies in one page: gcd(page size, 128)
+// places), one issues the scores' products and one the sums', each as soon as what
+// it needs is there. Weights go through shared memory, rounded to the inputs' type; tiles
 // of up to 32 rows, which memory bounds, carry what that took as a second operand.
 #pragma once
 
@@ -68,27 +69,12 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const float (&v)[16])
                  : "memory");
 }
 
-// The same without the wait, and the wait, which hands the values on.
-__device__ __forceinline__ void tmem_ask(uint32_t addr, float (&v)[16])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
-                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
-                 "}, [%16];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-                   "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-                 : "r"(addr));
-}
-__device__ __forceinline__ void tmem_got(float (&v)[16])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
-}
-
 // Shared memory: q, then rings of values and of keys, then weights. With VP = 64
 // the product's second 64 rows, which nothing reads, are whatever follows a
 // stage of values.
 template <int DP, int VP, int RT> struct PgShared {
+    // Groups of four warps make the weights of C rows of a map, map 0's groups first.
+    static constexpr int C = RT, groups = 2 * RT / C, threads = (groups + 1) * 128;
     static constexpr int row = DP * 2;                   // bytes of a row of q or k
     static constexpr int q = RT * row;                   // of one map
     static constexpr int kmap = kStep * row;             // of one map's keys of a step
@@ -142,7 +128,7 @@ __device__ __forceinline__ Tile tile_of(const PagedTcArgs &a, int e)
 }
 
 // What a tile costs, in steps: to begin and end one takes as long as kOpen.
-constexpr int kOpen = 2;
+constexpr int kOpen = 4;
 __device__ __forceinline__ int units(const Tile &t) { return t.steps ? t.steps + kOpen : 0; }
 
 // A CTA's walk over its share of units, segment by segment: `steps` of tile
@@ -219,19 +205,19 @@ template <int N> __device__ __forceinline__ void fold(float (&v)[N], int lane, i
     }
 }
 
-// Whether any of the 128 threads of a map has `flag`.
-__device__ __forceinline__ bool vote(int m, bool flag)
+// Whether any of the 128 threads of a group has `flag`.
+__device__ __forceinline__ bool vote(int group, bool flag)
 {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
                  "bar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r)
-                 : "r"(static_cast<uint32_t>(flag)), "r"(1 + m)
+                 : "r"(static_cast<uint32_t>(flag)), "r"(1 + group)
                  : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void sync_map(int m) { asm volatile("bar.sync %0, 128;" ::"r"(1 + m) : "memory"); }
-__device__ __forceinline__ void sync_maps() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ void sync_group(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
+template <int THREADS> __device__ __forceinline__ void sync_groups() { asm volatile("bar.sync 7, %0;" ::"n"(THREADS) : "memory"); }
 
 // Maximum over the warp; a NaN counts for nothing.
 __device__ __forceinline__ float warp_max(float v)
@@ -241,15 +227,13 @@ __device__ __forceinline__ float warp_max(float v)
     return r;
 }
 
-constexpr int kPgThreads = 12 * 32;
-
 template <typename T, int DP, int VP, int RT>
-__global__ void __launch_bounds__(kPgThreads, 1)
+__global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
     paged_tc_kernel(const __grid_constant__ PagedTcArgs a, const __grid_constant__ CUtensorMap mq,
                     const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv)
 {
     using F = PgShared<DP, VP, RT>;
-    constexpr int NK = F::ks, NV = F::vs;
+    constexpr int NK = F::ks, NV = F::vs, C = F::C, kThreads = F::threads, kFirst = F::groups * 4;  // warps of weights, then four
     constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t columns = RT == 16 ? 128 : RT == 32 ? 256 : 512;
     extern __shared__ unsigned char raw[];
@@ -266,7 +250,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     __shared__ __align__(16) int row_pos[2][RT], row_l[2][RT], row_h[2][RT];
     __shared__ uint64_t row_tree[2][RT];                   // which of at most 64 new tokens the row sees
     __shared__ int64_t row_out[RT];                        // where the row's output is, or -1
-    __shared__ int64_t warp_total[kPgThreads / 32];
+    __shared__ int64_t warp_total[kThreads / 32];
     __shared__ int start[3];
     float *table = reinterpret_cast<float *>(base + F::bytes);  // [nb][H], times log2(e)
     uint16_t *bmap = reinterpret_cast<uint16_t *>(table + a.d.nb * a.d.H);
@@ -279,7 +263,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         bar_init(&bars.q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             bar_init(&bars.s_full[i], 1);
-            bar_init(&bars.p_full[i], 8);
+            bar_init(&bars.p_full[i], kFirst);
         }
         for (int s = 0; s < 4; ++s) {
             bar_init(&bars.k_full[s], 1);
@@ -293,13 +277,13 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         tma_prefetch(&mk);
         tma_prefetch(&mv);
     }
-    if (warp == 9) tmem_alloc(&bars.tmem, columns);
-    for (int i = threadIdx.x; i < d.nb * d.H; i += kPgThreads) table[i] = d.table[i] * kLog2e;
-    for (int i = threadIdx.x; i < 2 * d.reach + 1 && d.nb; i += kPgThreads)
+    if (warp == kFirst + 1) tmem_alloc(&bars.tmem, columns);
+    for (int i = threadIdx.x; i < d.nb * d.H; i += kThreads) table[i] = d.table[i] * kLog2e;
+    for (int i = threadIdx.x; i < 2 * d.reach + 1 && d.nb; i += kThreads)
         bmap[i] = static_cast<uint16_t>(min(max(d.bmap[i], 0), d.nb - 1) * d.H);
     // Rows of q that a tile's queries leave free.
     const int used = a.LP * d.G;
-    for (int i = threadIdx.x; i < 2 * (RT - used) * (F::row / 16); i += kPgThreads) {
+    for (int i = threadIdx.x; i < 2 * (RT - used) * (F::row / 16); i += kThreads) {
         const int m = i >= (RT - used) * (F::row / 16), rest = i - m * (RT - used) * (F::row / 16);
         *reinterpret_cast<uint4 *>(base + m * F::q + used * F::row + rest * 16) = make_uint4(0, 0, 0, 0);
     }
@@ -307,7 +291,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 
     const int entries = d.B * a.row_tiles;
     // The CTA's share: threads take consecutive tiles' units, a scan adds them up.
-    const int per = (entries + kPgThreads - 1) / kPgThreads;
+    const int per = (entries + kThreads - 1) / kThreads;
     const int e0 = min(static_cast<int>(threadIdx.x) * per, entries), e1 = min(e0 + per, entries);
     int64_t own = 0;
     for (int e = e0; e < e1; ++e) own += units(tile_of(a, e));
@@ -322,7 +306,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     __syncthreads();
     fence_after();
     int64_t total = 0;
-    for (int w = 0; w < kPgThreads / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         if (w == warp) upto += total;
         total += warp_total[w];
     }
@@ -350,9 +334,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     Walk w;
     w.start(a, share, start[0], start[1], start[2]);
 
-    if (warp == 8 || warp == 10) {
+    if (warp == kFirst || warp == kFirst + 2) {
         // Copies of keys (and queries), and of values: a lane brings one box of a step.
-        const bool keys = warp == 8;
+        const bool keys = warp == kFirst;
         const int boxes = kStep / a.box, blocks = (d.Dv + 63) / 64;
         int t = 0, seg = 0;
         for (; w.left > 0; w.next(a), ++seg) {
@@ -419,7 +403,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             const int n = keys ? NK : NV;
             for (int i = max(0, t - n); i < t; ++i) bar_drain(keys ? &bars.k_full[i % n] : &bars.v_full[i % n], (i / n) & 1);
         }
-    } else if (warp == 9) {
+    } else if (warp == kFirst + 1) {
         // Scores. (All lanes walk through the steps, one issues: addresses then
         // stay in uniform registers.)
         const bool issue = elect();
@@ -449,7 +433,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         }
         for (int i = max(0, t - NK); i < t; ++i) bar_drain(&bars.k_empty[i % NK], (i / NK) & 1);
         __syncwarp();
-    } else if (warp == 11) {
+    } else if (warp == kFirst + 3) {
         // Sums.
         const bool issue = elect();
         constexpr uint32_t io = shape(bf16, 2 * RT, true) | (1u << 15);
@@ -479,9 +463,10 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         for (int i = max(0, t - NV); i < t; ++i) bar_drain(&bars.v_empty[i % NV], (i / NV) & 1);
         __syncwarp();
     } else {
-        // A thread has key kr of each step, and that key's scores of map m with all rows.
+        // Group `gr` has rows g0 .. g0 + C - 1 of map m, columns gr * C .. of the
+        // scores and of the sums; a thread has key kr of each step.
         constexpr int X = 16;  // scores that it takes at once
-        const int m = warp >> 2, kr = (warp & 3) * 32 + lane;
+        const int gr = warp >> 2, m = gr * C / RT, g0 = gr * C % RT, kr = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float2 mul = {d.scale_log2, d.scale_log2};
         // The sums with weights of step `of` are done.
@@ -492,45 +477,42 @@ __global__ void __launch_bounds__(kPgThreads, 1)
             if (none.steps) continue;
             T *to = static_cast<T *>(d.out) + (static_cast<int64_t>(none.b) * d.Lq + none.l0) * d.H * d.Dv;
             const int n = min(a.LP, d.Lq - none.l0) * d.H * d.Dv;
-            for (int i = threadIdx.x; i < n; i += 256) to[i] = dattn_round<T>(0.f);
+            for (int i = threadIdx.x; i < n; i += F::groups * 128) to[i] = dattn_round<T>(0.f);
         }
         const bool few = d.pg.tree && d.Lq <= 64;  // the tree's rows are bits in shared memory
         int t = 0, slot_tile[2] = {-1, -1}, slot_last = 0;
         for (; w.left > 0; w.next(a)) {
             const Tile tile = w.t;
             const int b = tile.b, old = tile.len - tile.count;
-            if (kr < RT) {
-                const int dl = static_cast<int>(d.div_G.div(kr)), l = min(tile.l0 + dl, d.Lq - 1), h = min(w.n * d.G + kr - dl * d.G, d.H - 1);
-                row_l[m][kr] = l;
-                row_h[m][kr] = h;
-                row_pos[m][kr] = d.pos_q ? d.pos_q[static_cast<int64_t>(b) * d.Lq + l] : old + l;
-                noff[m][kr] = FLT_MAX;
-                for (int i = 0; i < 2; ++i) {
-                    far_bias[m][i][kr] = d.nb ? table[bmap[i * 2 * d.reach] + h] : 0.f;
-                    off[m][i][kr] = FLT_MAX + far_bias[m][i][kr];
-                }
-                if (m == 0) row_out[kr] = kr < used && tile.l0 + dl < d.Lq ? ((static_cast<int64_t>(b) * d.Lq + l) * d.H + h) * d.Dv : -1;
+            if (kr < C) {
+                const int r = g0 + kr, dl = static_cast<int>(d.div_G.div(r)), l = min(tile.l0 + dl, d.Lq - 1), h = min(w.n * d.G + r - dl * d.G, d.H - 1);
+                row_l[m][r] = l;
+                row_h[m][r] = h;
+                row_pos[m][r] = d.pos_q ? d.pos_q[static_cast<int64_t>(b) * d.Lq + l] : old + l;
+                noff[m][r] = FLT_MAX;
+                for (int i = 0; i < 2; ++i) far_bias[m][i][r] = d.nb ? table[bmap[i * 2 * d.reach] + h] : 0.f;
+                if (m == 0) row_out[r] = r < used && tile.l0 + dl < d.Lq ? ((static_cast<int64_t>(b) * d.Lq + l) * d.H + h) * d.Dv : -1;
             }
             if (few && (w.first + w.steps) * kStep > old)
-                for (int r = warp & 3; r < used; r += 4) {
+                for (int r = g0 + (warp & 3); r < min(used, g0 + C); r += 4) {
                     const int l = min(tile.l0 + static_cast<int>(d.div_G.div(r)), d.Lq - 1);
                     const uint8_t *of = d.pg.tree + (static_cast<int64_t>(b) * d.Lq + l) * d.Lq;
                     const uint32_t low = __ballot_sync(0xffffffffu, lane < d.Lq && of[lane]), high = __ballot_sync(0xffffffffu, lane + 32 < d.Lq && of[lane + 32]);
                     if (lane == 0) row_tree[m][r] = low | static_cast<uint64_t>(high) << 32;
                 }
-            sync_map(m);
+            sync_group(gr);
             int qmin = kFar, qmax = -kFar;
 #pragma unroll
-            for (int r = lane; r < RT; r += 32)
-                if (r < used && tile.l0 + static_cast<int>(d.div_G.div(r)) < tile.count) {
+            for (int c = lane; c < C; c += 32)
+                if (const int r = g0 + c; r < used && tile.l0 + static_cast<int>(d.div_G.div(r)) < tile.count) {
                     qmin = min(qmin, row_pos[m][r]);
                     qmax = max(qmax, row_pos[m][r]);
                 }
             qmin = __reduce_min_sync(0xffffffffu, qmin);
             qmax = __reduce_max_sync(0xffffffffu, qmax);
-            float2 sum[RT / 2];
+            float2 sum[C / 2];
 #pragma unroll
-            for (int c = 0; c < RT / 2; ++c) sum[c] = {0.f, 0.f};
+            for (int c = 0; c < C / 2; ++c) sum[c] = {0.f, 0.f};
 #pragma unroll 1
             for (int i = 0; i < w.steps; ++i, ++t) {
                 const int j = (w.first + i) * kStep + kr;
@@ -540,8 +522,6 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 const uint32_t used_keys = info.use[warp & 3];
                 const bool use = used_keys >> lane & 1, all = used_keys == 0xffffffffu;
                 const int pos = d.pos_k ? key_pos[t % kInfos][kr] : j, kmin = info.lo[warp & 3], kmax = info.hi[warp & 3];
-                float x[2][X];
-                tmem_load(tS(m, t) + lanes, x[0]);
                 // Whether every row sees all of the warp's keys, with one bias for each row.
                 const bool before = d.nb == 0 || kmax - qmin <= -d.reach, after = !before && kmin - qmax >= d.reach;
                 const bool fast = (before || after) && !(d.causal && kmax > qmin) && !(d.pg.tree && (j - lane + 31) >= old);
@@ -551,48 +531,58 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                     if (d.causal)
 #pragma unroll
                         for (int c = 0; c < X; ++c)
-                            if (pos > row_pos[m][c0 + c]) see &= ~(1u << c);
+                            if (pos > row_pos[m][g0 + c0 + c]) see &= ~(1u << c);
                     if (d.pg.tree && use && j >= old) {
                         if (few) {
 #pragma unroll
                             for (int c = 0; c < X; ++c)
-                                if (!(row_tree[m][c0 + c] >> (j - old) & 1)) see &= ~(1u << c);
+                                if (!(row_tree[m][g0 + c0 + c] >> (j - old) & 1)) see &= ~(1u << c);
                         } else {
 #pragma unroll
                             for (int c = 0; c < X; ++c)
-                                if (!d.pg.tree[(static_cast<int64_t>(b) * d.Lq + row_l[m][c0 + c]) * d.Lq + j - old]) see &= ~(1u << c);
+                                if (!d.pg.tree[(static_cast<int64_t>(b) * d.Lq + row_l[m][g0 + c0 + c]) * d.Lq + j - old]) see &= ~(1u << c);
                         }
                     }
                     float bias[X];
                     if (fast || d.nb == 0) {
 #pragma unroll
-                        for (int c = 0; c < X; ++c) bias[c] = far_bias[m][after][c0 + c];
+                        for (int c = 0; c < X; ++c) bias[c] = far_bias[m][after][g0 + c0 + c];
                     } else {
 #pragma unroll
                         for (int c = 0; c < X; ++c)
-                            bias[c] = table[bmap[min(max(pos - row_pos[m][c0 + c], -d.reach), d.reach) + d.reach] + row_h[m][c0 + c]];
+                            bias[c] = table[bmap[min(max(pos - row_pos[m][g0 + c0 + c], -d.reach), d.reach) + d.reach] + row_h[m][g0 + c0 + c]];
                     }
 #pragma unroll
                     for (int c = 0; c < X; ++c) {
-                        const float y = fmaf(x[c], mul.x, bias[c]) + (less ? noff[m][c0 + c] : 0.f);
+                        const float y = fmaf(x[c], mul.x, bias[c]) + (less ? noff[m][g0 + c0 + c] : 0.f);
                         x[c] = see >> c & 1 ? y : -INFINITY;
                     }
                 };
                 // The step's weights; once more where one would be too large for
-                // its row's reference. A segment begins with references.
-                uint32_t hi[RT / 2], lo[F::rests ? RT / 2 : 1];
+                // its row's reference. A segment begins with references. Weights go
+                // to shared memory at once; sums take them from there when they stand.
+                if (t >= F::pbufs) summed(t - F::pbufs);  // the weights' buffer is free
+                const int swz = RT == 16 ? (kr >> 1) & 3 : kr & 7, piece0 = (RT == 64 ? g0 : gr * C) / 8;
+                unsigned char *const pt = base + F::at_p + (t % F::pbufs) * F::pbuf + (RT == 64 ? m * (F::p / 2) : 0) + kr * F::prow;
+                const auto piece = [&](int c) { return reinterpret_cast<uint4 *>(pt + (((piece0 + c / 8) ^ swz) << 4)); };
                 const auto weigh = [&](const float (&x)[X], int c0) {
 #pragma unroll
-                    for (int c = 0; c < X; c += 2) {
-                        const float2 w2 = {ex2(x[c]), ex2(x[c + 1])};
-                        uint32_t &h = hi[(c0 + c) / 2];
-                        h = pack2<T>(w2.x, w2.y);
-                        if constexpr (F::rests) {
-                            const float2 r = unpack2<T>(h);
-                            lo[(c0 + c) / 2] = pack2<T>(w2.x - r.x, w2.y - r.y);
+                    for (int c = 0; c < X; c += 8) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 w2 = {ex2(x[c + 2 * k]), ex2(x[c + 2 * k + 1])};
+                            hi[k] = pack2<T>(w2.x, w2.y);
+                            if constexpr (F::rests) {
+                                const float2 r = unpack2<T>(hi[k]);
+                                lo[k] = pack2<T>(w2.x - r.x, w2.y - r.y);
+                            }
                         }
+                        *piece(c0 + c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        if constexpr (F::rests) piece(c0 + c)[F::p / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 };
+                const uint32_t scores = tS(0, t) + gr * C + lanes;
 #pragma unroll 1
                 for (bool again = false;; again = true) {
                     float top[2] = {-INFINITY, -INFINITY};
@@ -600,95 +590,81 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                         top[0] = INFINITY;
                     } else if (fast && all) {
                         // Most steps: no branches, for the sake of the order of instructions.
-                        const float *o = off[m][after];
+                        const float *o = &off[m][after][g0];
 #pragma unroll
-                        for (int c0 = 0; c0 < RT; c0 += X) {
-                            float (&y)[X] = x[c0 / X % 2];
-                            if (c0 > 0) tmem_got(y);
-                            if (c0 + X < RT) tmem_ask(tS(m, t) + c0 + X + lanes, x[(c0 / X + 1) % 2]);
+                        for (int c0 = 0; c0 < C; c0 += X) {
+                            float x[X];
+                            tmem_load(scores + c0, x);
 #pragma unroll
                             for (int c = 0; c < X; c += 4) {
                                 const float4 f = *reinterpret_cast<const float4 *>(o + c0 + c);
-                                const float2 u = fma2({y[c], y[c + 1]}, mul, {f.x, f.y}), v = fma2({y[c + 2], y[c + 3]}, mul, {f.z, f.w});
-                                y[c] = u.x;
-                                y[c + 1] = u.y;
-                                y[c + 2] = v.x;
-                                y[c + 3] = v.y;
+                                const float2 u = fma2({x[c], x[c + 1]}, mul, {f.x, f.y}), v = fma2({x[c + 2], x[c + 3]}, mul, {f.z, f.w});
+                                x[c] = u.x;
+                                x[c + 1] = u.y;
+                                x[c + 2] = v.x;
+                                x[c + 3] = v.y;
                                 top[0] = max3(top[0], u.x, u.y);
                                 top[1] = max3(top[1], v.x, v.y);
                             }
-                            weigh(y, c0);
+                            weigh(x, c0);
                         }
                     } else {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < C; c0 += X) {
+                            float x[X];
+                            tmem_load(scores + c0, x);
+                            finish(x, c0, true);
 #pragma unroll
-                        for (int c0 = 0; c0 < RT; c0 += X) {
-                            if (c0 > 0) tmem_load(tS(m, t) + c0 + lanes, x[0]);
-                            finish(x[0], c0, true);
-#pragma unroll
-                            for (int c = 0; c < X; c += 2) top[0] = max3(top[0], x[0][c], x[0][c + 1]);
-                            weigh(x[0], c0);
+                            for (int c = 0; c < X; c += 2) top[0] = max3(top[0], x[c], x[c + 1]);
+                            weigh(x, c0);
                         }
                     }
-                    if (again || (i > 0 && !vote(m, fmaxf(top[0], top[1]) > kLift<T> + kSlack))) break;
+                    if (again || (i > 0 && !vote(gr, fmaxf(top[0], top[1]) > kLift<T> + kSlack))) break;
 #pragma unroll 1
-                    for (int c0 = 0; c0 < RT; c0 += X) {
-                        tmem_load(tS(m, t) + c0 + lanes, x[0]);
-                        finish(x[0], c0, false);
-                        float best = -INFINITY;  // of row c0 + lane
+                    for (int c0 = 0; c0 < C; c0 += X) {
+                        float x[X];
+                        tmem_load(scores + c0, x);
+                        finish(x, c0, false);
+                        float best = -INFINITY;  // of row g0 + c0 + lane
 #pragma unroll
                         for (int c = 0; c < X; ++c) {
-                            const float of = warp_max(x[0][c]);
+                            const float of = warp_max(x[c]);
                             best = lane == c ? of : best;
                         }
-                        if (lane < X) wide[m][warp & 3][c0 + lane] = best;
+                        if (lane < X) wide[m][warp & 3][g0 + c0 + lane] = best;
                     }
-                    tmem_load(tS(m, t) + lanes, x[0]);
-                    sync_map(m);
-                    if (kr < RT) {
-                        const float best = fmaxf(fmaxf(wide[m][0][kr], wide[m][1][kr]), fmaxf(wide[m][2][kr], wide[m][3][kr]));
-                        const float ref = -noff[m][kr];
-                        const bool raise = best + noff[m][kr] > kLift<T> + kSlack;
+                    sync_group(gr);
+                    if (kr < C) {
+                        const int r = g0 + kr;
+                        const float best = fmaxf(fmaxf(wide[m][0][r], wide[m][1][r]), fmaxf(wide[m][2][r], wide[m][3][r]));
+                        const float ref = -noff[m][r];
+                        const bool raise = best + noff[m][r] > kLift<T> + kSlack;
                         const float next = raise ? best - kLift<T> : ref;
-                        noff[m][kr] = -next;
-                        for (int i = 0; i < 2; ++i) off[m][i][kr] = far_bias[m][i][kr] - next;
-                        shrink[m][kr] = raise ? ex2(ref - next) : 1.f;
+                        noff[m][r] = -next;
+                        for (int k = 0; k < 2; ++k) off[m][k][r] = far_bias[m][k][r] - next;
+                        shrink[m][r] = raise ? ex2(ref - next) : 1.f;
                     }
-                    sync_map(m);
+                    sync_group(gr);
                     if (i > 0) {
                         summed(t - 1);
                         fence_after();
 #pragma unroll 1
-                        for (int c0 = 0; c0 < RT; c0 += 16) {
+                        for (int c0 = 0; c0 < C; c0 += 16) {
                             float o[16];
-                            tmem_load(tO + m * RT + c0 + lanes, o);
+                            tmem_load(tO + gr * C + c0 + lanes, o);
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) o[c] *= shrink[m][c0 + c];
-                            tmem_store(tO + m * RT + c0 + lanes, o);
+                            for (int c = 0; c < 16; ++c) o[c] *= shrink[m][g0 + c0 + c];
+                            tmem_store(tO + gr * C + c0 + lanes, o);
                         }
                         tmem_store_wait();
                     }
 #pragma unroll
-                    for (int c = 0; c < RT / 2; ++c) sum[c] = mul2(sum[c], *reinterpret_cast<const float2 *>(&shrink[m][2 * c]));
+                    for (int c = 0; c < C / 2; ++c) sum[c] = mul2(sum[c], *reinterpret_cast<const float2 *>(&shrink[m][g0 + 2 * c]));
                 }
-                // The sum is of the weights as the product takes them.
-#pragma unroll
-                for (int c = 0; c < RT / 2; ++c) {
-                    sum[c] = add2(sum[c], unpack2<T>(hi[c]));
-                    if constexpr (F::rests) sum[c] = add2(sum[c], unpack2<T>(lo[c]));
-                }
-                if (t >= F::pbufs) summed(t - F::pbufs);  // the weights' buffer is free
-                unsigned char *pt = base + F::at_p + (t % F::pbufs) * F::pbuf + (RT == 64 ? m * (F::p / 2) : 0) + kr * F::prow;
-                const int swz = RT == 16 ? (kr >> 1) & 3 : kr & 7, piece0 = RT == 64 ? 0 : m * RT / 8;
-#pragma unroll
-                for (int c = 0; c < RT / 2; c += 4) {
-                    const int at = ((piece0 + c / 4) ^ swz) << 4;
-                    *reinterpret_cast<uint4 *>(pt + at) = make_uint4(hi[c], hi[c + 1], hi[c + 2], hi[c + 3]);
-                    if constexpr (F::rests) *reinterpret_cast<uint4 *>(pt + F::p + at) = make_uint4(lo[c], lo[c + 1], lo[c + 2], lo[c + 3]);
-                }
-                if (!all && m < VP / 64) {
+                if (!all && gr < VP / 64) {
                     // 0 * NaN is NaN: unused keys' rows of V become zeros.
                     bar_wait_warp(&bars.v_full[t % NV], (t / NV) & 1, gave_up);
-                    unsigned char *v = base + F::at_v + (t % NV) * F::v + m * F::vblock + kr * 128;
+                    unsigned char *v = base + F::at_v + (t % NV) * F::v + gr * F::vblock + kr * 128;
                     if (!use)
 #pragma unroll
                         for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(v + (((c + lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -697,42 +673,58 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(&bars.p_full[t & 1]);
+                // The sum is of the weights as the product takes them.
+#pragma unroll
+                for (int c = 0; c < C; c += 8) {
+                    const uint4 h = *piece(c);
+                    sum[c / 2] = add2(sum[c / 2], unpack2<T>(h.x));
+                    sum[c / 2 + 1] = add2(sum[c / 2 + 1], unpack2<T>(h.y));
+                    sum[c / 2 + 2] = add2(sum[c / 2 + 2], unpack2<T>(h.z));
+                    sum[c / 2 + 3] = add2(sum[c / 2 + 3], unpack2<T>(h.w));
+                    if constexpr (F::rests) {
+                        const uint4 r = piece(c)[F::p / 16];
+                        sum[c / 2] = add2(sum[c / 2], unpack2<T>(r.x));
+                        sum[c / 2 + 1] = add2(sum[c / 2 + 1], unpack2<T>(r.y));
+                        sum[c / 2 + 2] = add2(sum[c / 2 + 2], unpack2<T>(r.z));
+                        sum[c / 2 + 3] = add2(sum[c / 2 + 3], unpack2<T>(r.w));
+                    }
+                }
             }
             // The segment's end: weights' sums over the threads, then the sums themselves.
             {
-                float all_sums[RT];
+                float all_sums[C];
 #pragma unroll
-                for (int c = 0; c < RT / 2; ++c) {
+                for (int c = 0; c < C / 2; ++c) {
                     all_sums[2 * c] = sum[c].x;
                     all_sums[2 * c + 1] = sum[c].y;
                 }
-                fold<RT>(all_sums, lane, 16);
-                if constexpr (RT == 16) {
+                fold<C>(all_sums, lane, 16);
+                if constexpr (C == 16) {
                     if ((lane & 1) == 0) wide[m][warp & 3][lane >> 1] = all_sums[0];
                 } else {
 #pragma unroll
-                    for (int c = 0; c < RT / 32; ++c) wide[m][warp & 3][lane * (RT / 32) + c] = all_sums[c];
+                    for (int c = 0; c < C / 32; ++c) wide[m][warp & 3][g0 + lane * (C / 32) + c] = all_sums[c];
                 }
             }
             summed(t - 1);
             fence_after();
-            sync_maps();
+            sync_groups<F::groups * 128>();
             const bool whole = w.first == 0 && w.steps == tile.steps;
             const int dv = (warp & 3) * 32 + lane, k = w.first == 0;
             const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + k;
-            if (kr < RT) {
-                const float total = wide[m][0][kr] + wide[m][1][kr] + (wide[m][2][kr] + wide[m][3][kr]) + (*gave_up ? NAN : 0.f);
+            if (const int r = g0 + kr; kr < C) {
+                const float total = wide[m][0][r] + wide[m][1][r] + (wide[m][2][r] + wide[m][3][r]) + (*gave_up ? NAN : 0.f);
                 if (whole) {
-                    shrink[m][kr] = total == 0.f || row_l[m][kr] >= tile.count ? 0.f : (m ? d.lam[row_h[m][kr]] : 1.f) / total;
-                } else if (kr < used) {
-                    *reinterpret_cast<float2 *>(d.part_ml + ((slot * RT + kr) * 2 + m) * 2) = make_float2(-noff[m][kr], total);
+                    shrink[m][r] = total == 0.f || row_l[m][r] >= tile.count ? 0.f : (m ? d.lam[row_h[m][r]] : 1.f) / total;
+                } else if (r < used) {
+                    *reinterpret_cast<float2 *>(d.part_ml + ((slot * RT + r) * 2 + m) * 2) = make_float2(-noff[m][r], total);
                 }
             }
             if (whole) {
-                sync_maps();
-                // The warps of map m take the m-th half of the rows, of both maps.
+                sync_groups<F::groups * 128>();
+                // Each group takes its share of the rows, of both maps.
 #pragma unroll 1
-                for (int r0 = m * (RT / 2); r0 < (m + 1) * (RT / 2); r0 += 8) {
+                for (int r0 = gr * (RT / F::groups); r0 < (gr + 1) * (RT / F::groups); r0 += 8) {
                     float u[8], v[8];
                     __syncwarp();
                     tmem_load(tO + r0 + lanes, u);
@@ -749,7 +741,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 if (!k) slot_last = w.first + w.steps == tile.steps;
                 float *to = d.part_o + (slot * RT * 2 + m) * d.Dv + dv;
 #pragma unroll 1
-                for (int r0 = 0; r0 < used; r0 += 8) {
+                for (int r0 = g0; r0 < min(used, g0 + C); r0 += 8) {
                     float u[8];
                     __syncwarp();
                     tmem_load(tO + m * RT + r0 + lanes, u);
@@ -759,7 +751,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 }
             }
             __syncwarp();
-            sync_maps();  // the next segment's arrays are the same
+            sync_groups<F::groups * 128>();  // the next segment's arrays are the same
         }
         if (threadIdx.x < 2) {
             a.slots[blockIdx.x * 4 + threadIdx.x * 2] = threadIdx.x ? slot_tile[1] : slot_tile[0];
@@ -769,7 +761,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     }
     fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kFirst + 1) {
         fence_after();
         tmem_free(tmem, columns);
     }
@@ -784,7 +776,7 @@ constexpr int kJoinRows = 8;
 template <typename T> __global__ void __launch_bounds__(32 * kJoinRows) paged_join_kernel(const __grid_constant__ PagedTcArgs a)
 {
     const DattnArgs &d = a.d;
-    const int c = blockIdx.x, lane = threadIdx.x & 31, v = lane * 4, r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+    const int c = blockIdx.x, lane = threadIdx.x & 31, v = min(lane * 4, d.Dv - 4), r = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
     if (r >= a.LP * d.G) return;
     pdl_wait();
     const int tile = a.slots[c * 4 + 2];
@@ -821,22 +813,31 @@ template <typename T> __global__ void __launch_bounds__(32 * kJoinRows) paged_jo
         sum[0] = fmaf(w.y, f[0], sum[0]);
         sum[1] = fmaf(w.w, f[1], sum[1]);
         const int here = min(pieces - base, 32);
-#pragma unroll 4
-        for (int i = 0; i < here; ++i)
+        // Four pieces at a time, which the loads' latency is spread over; one past
+        // the last has a factor of 0 and is read in the last's place.
+        for (int i0 = 0; i0 < here; i0 += 4) {
+            float4 x[4][2];
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const float g = __shfl_sync(0xffffffffu, f[m], i);
-                if (v >= d.Dv) continue;
-                const float4 x = *reinterpret_cast<const float4 *>(d.part_o + ((slot(base + i) * a.RT + r) * 2 + m) * d.Dv + v);
-                o[m].x = fmaf(x.x, g, o[m].x);
-                o[m].y = fmaf(x.y, g, o[m].y);
-                o[m].z = fmaf(x.z, g, o[m].z);
-                o[m].w = fmaf(x.w, g, o[m].w);
-            }
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    x[k][m] = *reinterpret_cast<const float4 *>(d.part_o + ((slot(min(base + i0 + k, pieces - 1)) * a.RT + r) * 2 + m) * d.Dv + v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const float g = __shfl_sync(0xffffffffu, f[m], i0 + k), keep = i0 + k < here ? g : 0.f;
+                    if (keep == 0.f) continue;  // uniform; what is there may be anything
+                    o[m].x = fmaf(x[k][m].x, g, o[m].x);
+                    o[m].y = fmaf(x[k][m].y, g, o[m].y);
+                    o[m].z = fmaf(x[k][m].z, g, o[m].z);
+                    o[m].w = fmaf(x[k][m].w, g, o[m].w);
+                }
+        }
     }
     for (int m = 0; m < 2; ++m)
         for (int k = 16; k; k >>= 1) sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], k);
-    if (v >= d.Dv) return;
+    if (lane * 4 >= d.Dv) return;
     const bool live = l < paged_count(d, b);
     const float f0 = sum[0] == 0.f || !live ? 0.f : 1.f / sum[0], f1 = sum[1] == 0.f || !live ? 0.f : d.lam[h] / sum[1];
     const auto out = [&](float x, float y) { return dattn_round<T>((f0 == 0.f ? 0.f : x * f0) - (f1 == 0.f ? 0.f : y * f1)); };
@@ -855,7 +856,7 @@ cudaError_t launch_tc(const PagedTcArgs &a, const CUtensorMap &mq, const CUtenso
     const auto kernel = paged_tc_kernel<T, DP, VP, RT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    kernel<<<a.ctas, kPgThreads, smem, st>>>(a, mq, mk, mv);
+    kernel<<<a.ctas, F::threads, smem, st>>>(a, mq, mk, mv);
     e = cudaGetLastError();
     if (e == cudaSuccess && a.ctas > 1 && a.d.Lk > kStep)  // otherwise no tile has pieces
         e = launch_pdl(paged_join_kernel<T>, dim3(a.ctas, (a.LP * a.d.G + kJoinRows - 1) / kJoinRows), dim3(32 * kJoinRows), 0, st, a);
