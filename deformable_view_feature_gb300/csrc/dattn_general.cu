@@ -203,17 +203,54 @@ __device__ void load_paged(const DattnArgs &a, const void *base, int64_t first, 
     }
 }
 
+// The same in two halves, so that a step's rows are on their way while the one
+// before is worked on: N pieces of a thread's own, asked for and then stored.
+template <typename T, int W, int N>
+__device__ __forceinline__ void ask_paged(const DattnArgs &a, const void *base, int64_t first, int64_t s_page, int64_t s_place,
+                                          int width, const int *seen, const int2 *at, float4 (&r)[N])
+{
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const int i = threadIdx.x + u * kThreadsG, row = i / (W / 4), d = (i - row * (W / 4)) * 4;
+        r[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (seen[row]) r[u] = load4(static_cast<const T *>(base) + first + at[row].x * s_page + at[row].y * s_place, d, width, a.wide);
+    }
+}
+template <int W, int N> __device__ __forceinline__ void put_paged(const float4 (&r)[N], float *dst)
+{
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const int i = threadIdx.x + u * kThreadsG, row = i / (W / 4), d = (i - row * (W / 4)) * 4;
+        *reinterpret_cast<float4 *>(dst + row * (W + 4) + d) = r[u];
+    }
+}
+
+struct PagedKey {
+    int2 at;
+    int seen, pos;
+};
+
+// Position, use and place of key j of a paged cache.
+__device__ __forceinline__ PagedKey paged_key(const DattnArgs &a, int b, int end, int j)
+{
+    PagedKey k{make_int2(-1, 0), 0, j};
+    if (j < end) {
+        const int64_t of = static_cast<int64_t>(b) * a.Lk + j;
+        k.at.x = paged_page(a, b, j, k.at.y);
+        k.seen = k.at.x >= 0 && (!a.mask || a.mask[of]);
+        if (a.pos_k) k.pos = a.pos_k[of];
+    }
+    return k;
+}
+
 // Positions, use and places of the keys j0 .. of a paged cache.
 __device__ __forceinline__ void load_paged_info(const DattnArgs &a, int b, int end, int j0, int count, int *pos, int *seen, int2 *at)
 {
     for (int i = threadIdx.x; i < count; i += kThreadsG) {
-        const int j = j0 + i;
-        const bool in = j < end;
-        const int64_t of = static_cast<int64_t>(b) * a.Lk + j;
-        at[i] = make_int2(-1, 0);
-        if (in) at[i].x = paged_page(a, b, j, at[i].y);
-        seen[i] = at[i].x >= 0 && (!a.mask || a.mask[of]);
-        pos[i] = in && a.pos_k ? a.pos_k[of] : j;
+        const PagedKey k = paged_key(a, b, end, j0 + i);
+        at[i] = k.at;
+        seen[i] = k.seen;
+        pos[i] = k.pos;
     }
 }
 
@@ -259,7 +296,14 @@ __global__ void __launch_bounds__(kThreadsG, DP == 32 || (DP == 64 && QT == 16) 
     const int tile = blockIdx.x / a.splits, split = blockIdx.x - tile * a.splits;
     const int n = blockIdx.y, b = blockIdx.z, r0 = tile * QT;
     const int len = dattn_length(a, b);
-    __shared__ int2 at[PAGED ? KT : 1];  // pages and places of the keys
+    // Paged: pages and places of the keys, and their infos, of up to three steps.
+    constexpr bool AHEAD = PAGED && DP <= 64;
+    constexpr int NKA = KT * DP / 4 / kThreadsG, NVA = KT * F::WV / 4 / kThreadsG;
+    __shared__ int2 at[PAGED ? 3 * KT : 1];
+    __shared__ int infos[AHEAD ? 6 * KT : 1];
+    float4 ak[2][AHEAD ? NKA : 1], av[AHEAD ? NVA : 1];
+    PagedKey ahead{};
+    int step = 0;
     const int count = PAGED ? paged_count(a, b) : a.Lq, old = len - count;  // queries, keys before them
 
     load_bias(a, n, bt);
@@ -291,12 +335,43 @@ __global__ void __launch_bounds__(kThreadsG, DP == 32 || (DP == 64 && QT == 16) 
         const int last = static_cast<int>(a.div_G.div(min(r0 + QT, a.rows) - 1));
         end = min(end, (PAGED ? old : len - a.Lq) + last + 1);
     }
-    for (; j0 < end; j0 += KT) {
+    const auto ask = [&](int of) {  // the rows of step `of`, whose infos are there
+        const int *seen = infos + (of % 3 * 2 + 1) * KT;
+        const int2 *where = at + of % 3 * KT;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+            ask_paged<T, DP>(a, a.k, n * a.ks[2] + m * a.ks[3], a.ks[0], a.ks[1], a.D, seen, where, ak[m]);
+        ask_paged<T, F::WV>(a, a.v, n * a.vs[2], a.vs[0], a.vs[1], a.Dv, seen, where, av);
+    };
+    if constexpr (AHEAD) {
+        for (int i = 0; i < 2; ++i) load_paged_info(a, b, end, j0 + i * KT, KT, infos + i * 2 * KT, infos + (i * 2 + 1) * KT, at + i * KT);
         __syncthreads();
-        if constexpr (PAGED) load_paged_info(a, b, end, j0, KT, kpos, kseen, at);
-        else load_key_info(a, b, end, j0, KT, kpos, kseen);
+        ask(0);
+    }
+    for (; j0 < end; j0 += KT, ++step) {
         __syncthreads();
-        if constexpr (PAGED) {
+        if constexpr (AHEAD) {
+            kpos = infos + step % 3 * 2 * KT;
+            kseen = kpos + KT;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) put_paged<DP>(ak[m], sk + m * KT * (DP + 4));
+            put_paged<F::WV>(av, sv);
+            if (step > 0 && threadIdx.x < KT) {
+                const int x = (step + 1) % 3;
+                at[x * KT + threadIdx.x] = ahead.at;
+                infos[(x * 2 + 1) * KT + threadIdx.x] = ahead.seen;
+                infos[x * 2 * KT + threadIdx.x] = ahead.pos;
+            }
+        } else if constexpr (PAGED) {
+            load_paged_info(a, b, end, j0, KT, kpos, kseen, at);
+        } else {
+            load_key_info(a, b, end, j0, KT, kpos, kseen);
+        }
+        __syncthreads();
+        if constexpr (AHEAD) {
+            ask(step + 1);
+            if (threadIdx.x < KT) ahead = paged_key(a, b, end, j0 + 2 * KT + threadIdx.x);
+        } else if constexpr (PAGED) {
             for (int m = 0; m < 2; ++m)
                 load_paged<T, DP>(a, a.k, n * a.ks[2] + m * a.ks[3], a.ks[0], a.ks[1], KT, a.D, kseen, at, sk + m * KT * (DP + 4));
             load_paged<T, F::WV>(a, a.v, n * a.vs[2], a.vs[0], a.vs[1], KT, a.Dv, kseen, at, sv);
@@ -305,7 +380,7 @@ __global__ void __launch_bounds__(kThreadsG, DP == 32 || (DP == 64 && QT == 16) 
                 load_keys<T, DP>(a, a.k, b * a.ks[0] + n * a.ks[2] + m * a.ks[3], a.ks[1], j0, KT, a.D, kseen, sk + m * KT * (DP + 4));
             load_keys<T, F::WV>(a, a.v, b * a.vs[0] + n * a.vs[2], a.vs[1], j0, KT, a.Dv, kseen, sv);
         }
-        __syncthreads();
+        if constexpr (!AHEAD) __syncthreads();
         float bias[M][N];
 #pragma unroll
         for (int i = 0; i < M; ++i)

@@ -44,11 +44,13 @@ bool tensor_serves(const pg_problem &d)
     return true;
 }
 
+constexpr int kFewRows = 8;
+
 struct PagedPlan {
     DattnArgs a;
     PagedTcArgs tc;
     size_t part_o, part_ml, slots, total;
-    bool tensor;
+    bool tensor, few, quads;
 };
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -141,11 +143,16 @@ da_status paged_plan(const pg_problem *pr, PagedPlan &p)
         p.total += round256(sizeof(int32_t) * 4 * t.ctas);
         return DA_OK;
     }
-    // CTAs to share a tile where tiles alone leave SMs without work, two of
-    // them on each, each with 64 keys or more of a full table.
-    const int64_t bn = static_cast<int64_t>(a.B) * a.Hkv, qt = dattn_general_row_tile(a), tiles = bn * ((rows + qt - 1) / qt);
+    // CTAs to share a tile where tiles alone leave SMs without work: two to an SM
+    // with 64 keys or more of a full table each; of the few rows' CTAs twice as
+    // many, so that sequences' different lengths leave fewer SMs idle, with 256
+    // keys or more, 32 for each warp.
+    p.few = rows <= kFewRows;
+    p.quads = d.width % 4 == 0 && d.value_width % 4 == 0 && aligned(d.q, 4 * elem) && aligned(c.k, 4 * elem) && aligned(c.v, 4 * elem);
+    for (int i = 0; i < 4; ++i) p.quads = p.quads && a.qs[i] % 4 == 0 && a.ks[i] % 4 == 0 && (i == 3 || a.vs[i] % 4 == 0);
+    const int64_t bn = static_cast<int64_t>(a.B) * a.Hkv, qt = p.few ? rows : dattn_general_row_tile(a), tiles = rows > 0 ? bn * ((rows + qt - 1) / qt) : 0;
     if (tiles > 0) {
-        const int64_t want = 152 * 2 / tiles, steps = a.Lk / 64, n = want < steps ? want : steps;
+        const int64_t want = 152 * (p.few ? 4 : 2) / tiles, steps = a.Lk / (p.few ? 256 : 64), n = want < steps ? want : steps;
         a.splits = static_cast<int32_t>(n < 1 ? 1 : n);
     }
     if (a.splits > 1) {
@@ -254,8 +261,8 @@ da_status pg_attention(const pg_problem *p, void *out, void *workspace, size_t w
         pl.tc.d = a;
         return p->dtype == DA_BF16 ? da::paged_forward_bf16(pl.tc, cs) : da::paged_forward_f16(pl.tc, cs);
     }
-    cudaError_t e = da::paged_forward_general(a, p->dtype, cs);
-    if (e == cudaSuccess && a.splits > 1) e = da::dattn_merge(a, p->dtype, cs);
+    cudaError_t e = pl.few ? da::paged_forward_few(a, p->dtype, pl.quads, cs) : da::paged_forward_general(a, p->dtype, cs);
+    if (e == cudaSuccess && a.splits > 1) e = da::paged_merge(a, p->dtype, cs);
     return e == cudaSuccess ? DA_OK : da::cuda_fail(e, "paged attention launch");
 }
 

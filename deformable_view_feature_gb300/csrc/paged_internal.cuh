@@ -24,4 +24,9 @@ struct PagedTcArgs {
 da_status paged_forward_bf16(const PagedTcArgs &a, cudaStream_t st);
 da_status paged_forward_f16(const PagedTcArgs &a, cudaStream_t st);
 
+// On the fp32 units: few rows (quads: four elements to a load), and the join of
+// rows that were split over the keys.
+cudaError_t paged_forward_few(const DattnArgs &a, int dtype, bool quads, cudaStream_t st);
+cudaError_t paged_merge(const DattnArgs &a, int dtype, cudaStream_t st);
+
 }  // namespace da
