@@ -26,11 +26,12 @@ struct QkrSide {
     int32_t first;       // position of token 0 without pos
     int32_t nr, slots, sg_log2;  // slots that rotate, slots, log2 of the lanes of a vector
     int32_t tpw;         // tokens that a warp takes at once
+    int32_t parts, per;  // forward: warps that share a token, vectors of each
     int32_t paged, normed, keys;
     float inv_D;         // 1 / D
     int64_t tokens;      // B * L
-    int64_t unit0;       // forward: the side's first warp; backward: its first CTA
-    int32_t units;       // backward: its CTAs
+    int64_t unit0;       // its first CTA
+    int32_t units;       // its CTAs
     FastDiv div_L, div_vec, div_hp;  // by L, H * M, R / 2
     float *grad_w, *part;            // backward: [D], and [units, D]
 };

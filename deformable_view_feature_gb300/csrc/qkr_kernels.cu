@@ -28,24 +28,77 @@ template <> struct QkrRaw<8> { using type = uint2; };
 template <> struct QkrRaw<4> { using type = uint32_t; };
 template <> struct QkrRaw<2> { using type = unsigned short; };
 
-template <typename T> __device__ __forceinline__ float qkr_float(T v);
-template <> __device__ __forceinline__ float qkr_float(float v) { return v; }
-template <> __device__ __forceinline__ float qkr_float(__half v) { return __half2float(v); }
-template <> __device__ __forceinline__ float qkr_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T> __device__ __forceinline__ T qkr_round(float v);
-template <> __device__ __forceinline__ float qkr_round(float v) { return v; }
-template <> __device__ __forceinline__ __half qkr_round(float v) { return __float2half_rn(v); }
-template <> __device__ __forceinline__ __nv_bfloat16 qkr_round(float v) { return __float2bfloat16_rn(v); }
+// V channels as they lie in memory, and as pairs of floats (with one channel
+// the second of the pair is zero). Arithmetic on pairs takes half the
+// instructions, which bound these passes before memory does otherwise.
+template <typename T, int V> using Piece = typename QkrRaw<static_cast<int>(sizeof(T)) * V>::type;
+template <int V> constexpr int kPairsOf = (V + 1) / 2;
 
-// V channels as they lie in memory.
-template <typename T, int V> union Piece {
-    typename QkrRaw<static_cast<int>(sizeof(T)) * V>::type raw;
-    T v[V];
-    __device__ __forceinline__ Piece() {}
-};
+__device__ __forceinline__ float2 widen(uint32_t w, const __nv_bfloat16 *) { return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)}; }
+__device__ __forceinline__ float2 widen(uint32_t w, const __half *) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+__device__ __forceinline__ uint32_t narrow(float2 v, const __nv_bfloat16 *)
+{
+    const __nv_bfloat162 r = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t narrow(float2 v, const __half *)
+{
+    const __half2 r = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+template <typename T, int V> __device__ __forceinline__ void unpack(const Piece<T, V> &p, float2 (&f)[kPairsOf<V>])
+{
+    if constexpr (sizeof(T) == 4) {
+        const float *x = reinterpret_cast<const float *>(&p);
+#pragma unroll
+        for (int i = 0; i < kPairsOf<V>; ++i) f[i] = {x[2 * i], V == 1 ? 0.f : x[2 * i + (V > 1)]};
+    } else if constexpr (V == 1) {
+        f[0] = {widen(p, static_cast<const T *>(nullptr)).x, 0.f};
+    } else {
+        const uint32_t *x = reinterpret_cast<const uint32_t *>(&p);
+#pragma unroll
+        for (int i = 0; i < kPairsOf<V>; ++i) f[i] = widen(x[i], static_cast<const T *>(nullptr));
+    }
+}
+
+template <typename T, int V> __device__ __forceinline__ Piece<T, V> pack(const float2 (&f)[kPairsOf<V>])
+{
+    Piece<T, V> p;
+    if constexpr (sizeof(T) == 4) {
+        float *x = reinterpret_cast<float *>(&p);
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = i % 2 ? f[i / 2].y : f[i / 2].x;
+    } else if constexpr (V == 1) {
+        p = static_cast<unsigned short>(narrow(f[0], static_cast<const T *>(nullptr)) & 0xffffu);
+    } else {
+        uint32_t *x = reinterpret_cast<uint32_t *>(&p);
+#pragma unroll
+        for (int i = 0; i < kPairsOf<V>; ++i) x[i] = narrow(f[i], static_cast<const T *>(nullptr));
+    }
+    return p;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)), "l"(reinterpret_cast<uint64_t &>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 minus(float2 a) { return {-a.x, -a.y}; }
 
 // A lane's two pieces of each of its slots: SPL slots, 2 V channels each.
-template <typename T, int V> constexpr int kSlots = V >= 4 ? 1 : V == 2 ? 2 : 4;
+template <int V> constexpr int kSlots = V >= 4 ? 1 : V == 2 ? 2 : 4;
 
 struct Slot {
     int a, b;      // first channels of the pieces, or -1
@@ -66,78 +119,126 @@ template <int V> __device__ __forceinline__ Slot slot_of(const QkrSide &s, int t
     return r;
 }
 
+template <int V> __device__ __forceinline__ void weights_of(const QkrSide &s, int at, float2 (&w)[kPairsOf<V>])
+{
+#pragma unroll
+    for (int i = 0; i < kPairsOf<V>; ++i)
+        w[i] = {s.w && at >= 0 ? s.w[at + 2 * i] : 1.f, V > 1 && s.w && at >= 0 ? s.w[at + 2 * i + 1] : 1.f};
+}
+
 // Cosine and sine of pos * turns / 2^64 of a turn: the product's quarter turn
-// next to it exactly, the rest, at most an eighth of a turn, in fp32.
+// next to it exactly, the rest, an angle of at most pi / 4, to 2^-34 of a turn
+// and then by the first terms of their Taylor series, whose next ones are below
+// 2^-25 there.
 __device__ __forceinline__ float2 angle(int pos, int64_t turns)
 {
     const uint64_t at = static_cast<uint64_t>(static_cast<int64_t>(pos)) * static_cast<uint64_t>(turns);
     const uint32_t quarter = static_cast<uint32_t>((at + (uint64_t{1} << 61)) >> 62);
     const int64_t rest = static_cast<int64_t>(at - (static_cast<uint64_t>(quarter) << 62));
-    float s, c;
-    sincospif(static_cast<float>(rest) * 0x1p-63f, &s, &c);
-    if (quarter & 1) {
-        const float t = c;
-        c = -s;
-        s = t;
-    }
-    return (quarter & 2) ? make_float2(-c, -s) : make_float2(c, s);
+    const float x = static_cast<float>(static_cast<int32_t>(rest >> 30)) * 3.657295198e-10f, y = x * x;  // 2 pi / 2^34
+    const float s = fmaf(x * y, fmaf(y, fmaf(y, fmaf(y, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), x);
+    const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24), -0.5f), 1.f);
+    const float u = quarter & 1 ? -s : c, v = quarter & 1 ? c : s;
+    return (quarter & 2) ? make_float2(-u, -v) : make_float2(u, v);
 }
 
-// Which token a warp's vectors are of, and where they lie.
+// What a warp has in shared memory: its tokens' angles, and where they lie.
+struct WarpTokens {
+    float c[kPairs], s[kPairs];       // [token][R / 2], times the magnitude
+    int64_t from[kTokens], to[kTokens];  // first element of a token's vectors, or to < 0: not to be stored
+};
+
+// Which tokens a warp's vectors are of.
 struct Run {
     int64_t token0;
     int count;     // tokens
 };
 
-__device__ __forceinline__ void token_place(const QkrSide &s, int64_t token, int &b, int &l)
+// Where a run's tokens lie; paged: by page and place.
+template <bool PAGED> __device__ __forceinline__ void fill_places(const QkrArgs &a, const QkrSide &s, const Run &run, WarpTokens &w)
 {
-    b = static_cast<int>(s.div_L.div(static_cast<uint32_t>(token)));
-    l = static_cast<int>(token - static_cast<int64_t>(b) * s.L);
-}
-
-__device__ __forceinline__ int position(const QkrArgs &a, const QkrSide &s, int64_t token)
-{
-    if (s.pos) return s.pos[token];
-    int b, l;
-    token_place(s, token, b, l);
-    return static_cast<int>(static_cast<uint32_t>(a.lengths ? a.lengths[b] : s.first) + static_cast<uint32_t>(l));
-}
-
-// The angles of a run's tokens, [token][R / 2], times the magnitude.
-__device__ __forceinline__ void fill_angles(const QkrArgs &a, const QkrSide &s, const Run &run, float2 *cs)
-{
-    const int hp = s.R / 2;
-    for (int i = threadIdx.x & 31; i < run.count * hp; i += 32) {
-        const int t = static_cast<int>(s.div_hp.div(i));
-        const float2 v = angle(position(a, s, run.token0 + t), a.turns[i - t * hp]);
-        cs[i] = make_float2(v.x * a.magnitude, v.y * a.magnitude);
+    for (int t = threadIdx.x & 31; t < run.count; t += 32) {
+        const int64_t token = run.token0 + t;
+        const int b = static_cast<int>(s.div_L.div(static_cast<uint32_t>(token))), l = static_cast<int>(token - static_cast<int64_t>(b) * s.L);
+        w.from[t] = b * s.xs[0] + l * s.xs[1];
+        int64_t to = b * s.ys[0] + l * s.ys[1];
+        if (PAGED && s.paged) {
+            to = -1;
+            const int64_t place = static_cast<int64_t>(a.lengths[b]) + l;
+            if (l < (a.counts ? a.counts[b] : s.L) && place >= 0 && place < static_cast<int64_t>(a.table_pages) * a.page_size) {
+                const int n = static_cast<int>(a.div_page.div(static_cast<uint32_t>(place)));
+                const int page = a.table[static_cast<int64_t>(b) * a.table_pages + n];
+                if (page >= 0 && page < a.num_pages) to = page * s.ys[0] + (place - static_cast<int64_t>(n) * a.page_size) * s.ys[1];
+            }
+        }
+        w.to[t] = to;
     }
 }
 
-// z_a, z_b of the pairs of a slot; back: the turn in the other direction.
-template <int V, bool BACK>
-__device__ __forceinline__ void turn(const float2 *cs, int interleaved, float (&a)[V], float (&b)[V])
+// The angles of a run's tokens.
+__device__ __forceinline__ void fill_angles(const QkrArgs &a, const QkrSide &s, const Run &run, WarpTokens &w)
 {
+    const int hp = s.R / 2;
+    for (int i = threadIdx.x & 31; i < run.count * hp; i += 32) {
+        const int t = run.count == 1 ? 0 : static_cast<int>(s.div_hp.div(i));
+        const int64_t token = run.token0 + t;
+        int pos;
+        if (s.pos) {
+            pos = s.pos[token];
+        } else {
+            const int b = static_cast<int>(s.div_L.div(static_cast<uint32_t>(token)));
+            const uint32_t l = static_cast<uint32_t>(token - static_cast<int64_t>(b) * s.L);
+            pos = static_cast<int>(static_cast<uint32_t>(a.lengths ? a.lengths[b] : s.first) + l);
+        }
+        const float2 v = angle(pos, a.turns[i - t * hp]);
+        w.c[i] = v.x * a.magnitude;
+        w.s[i] = v.y * a.magnitude;
+    }
+}
+
+// V angles' cosines or sines as pairs; they lie on multiples of V.
+template <int V> __device__ __forceinline__ void load_angles(const float *p, float2 (&v)[kPairsOf<V>])
+{
+    if constexpr (V >= 4) {
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j) {
+            const float4 x = reinterpret_cast<const float4 *>(p)[j];
+            v[2 * j] = {x.x, x.y};
+            v[2 * j + 1] = {x.z, x.w};
+        }
+    } else if constexpr (V == 2) {
+        v[0] = *reinterpret_cast<const float2 *>(p);
+    } else {
+        v[0] = {*p, 0.f};
+    }
+}
+
+// z_a, z_b of the pairs of a slot; BACK: the turn in the other direction.
+template <int V, bool BACK>
+__device__ __forceinline__ void turn(const float *c, const float *s, int interleaved, float2 (&a)[kPairsOf<V>], float2 (&b)[kPairsOf<V>])
+{
+    constexpr int P = kPairsOf<V>;
+    float2 u[P], v[P];
+    load_angles<V>(c, u);
+    load_angles<V>(s, v);
     if (V > 1 && interleaved) {
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-            if constexpr (V > 1) {
-                const float2 u = cs[j / 2], v = cs[V / 2 + j / 2];
-                const float us = BACK ? -u.y : u.y, vs = BACK ? -v.y : v.y;
-                const float a0 = a[j], a1 = a[j + 1], b0 = b[j], b1 = b[j + 1];
-                a[j] = a0 * u.x - a1 * us;
-                a[j + 1] = a0 * us + a1 * u.x;
-                b[j] = b0 * v.x - b1 * vs;
-                b[j + 1] = b0 * vs + b1 * v.x;
-            }
+        for (int j = 0; j < P; ++j) {
+            // Pair j of piece a turns by angle j, of piece b by angle V / 2 + j.
+            constexpr int half = V / 2;
+            const float c0 = j % 2 ? u[j / 2].y : u[j / 2].x, s0 = BACK ? -(j % 2 ? v[j / 2].y : v[j / 2].x) : j % 2 ? v[j / 2].y : v[j / 2].x;
+            const int k = half + j;
+            const float c1 = k % 2 ? u[k / 2].y : u[k / 2].x, s1 = BACK ? -(k % 2 ? v[k / 2].y : v[k / 2].x) : k % 2 ? v[k / 2].y : v[k / 2].x;
+            const float2 x = a[j], y = b[j];
+            a[j] = {x.x * c0 - x.y * s0, x.x * s0 + x.y * c0};
+            b[j] = {y.x * c1 - y.y * s1, y.x * s1 + y.y * c1};
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float2 u = cs[j];
-            const float us = BACK ? -u.y : u.y, x = a[j], y = b[j];
-            a[j] = x * u.x - y * us;
-            b[j] = x * us + y * u.x;
+        for (int j = 0; j < P; ++j) {
+            const float2 x = a[j], y = b[j], n = minus(v[j]);
+            a[j] = fma2(y, BACK ? v[j] : n, mul2(x, u[j]));
+            b[j] = fma2(x, BACK ? n : v[j], mul2(y, u[j]));
         }
     }
 }
@@ -148,137 +249,131 @@ __device__ __forceinline__ float lanes_sum(float v, int sg_log2)
     return v;
 }
 
-template <typename T, int V> __device__ __forceinline__ Piece<T, V> load_piece(const T *base, int at)
+// A piece, zeros where there is none.
+template <typename T, int V> __device__ __forceinline__ Piece<T, V> load_piece(const T *base, int at, bool live)
 {
-    Piece<T, V> p;
-    p.raw = __ldcs(reinterpret_cast<const decltype(p.raw) *>(base + at));
+    Piece<T, V> p{};
+    if (live && at >= 0) p = __ldcs(reinterpret_cast<const Piece<T, V> *>(base + at));
     return p;
 }
-
-// ---- forward, and append ---------------------------------------------------
+template <typename T, int V> __device__ __forceinline__ void store_piece(T *base, int at, const float2 (&f)[kPairsOf<V>])
+{
+    if (at >= 0) *reinterpret_cast<Piece<T, V> *>(base + at) = pack<T, V>(f);
+}
 
 // Vectors that a group of lanes has under way at once.
 constexpr int kAhead = 2;
 
-template <typename T, int V, bool PAGED>
-__global__ void __launch_bounds__(kQkrThreads) qkr_forward_kernel(const __grid_constant__ QkrArgs a)
-{
-    constexpr int SPL = kSlots<T, V>;
-    __shared__ __align__(16) float2 all_cs[kQkrWarps][kPairs];
-    __shared__ int2 all_where[PAGED ? kQkrWarps : 1][kTokens];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kQkrWarps + warp;
-    int which = 0;
-    while (which + 1 < a.sides && unit >= a.side[which + 1].unit0) ++which;
-    const QkrSide &s = a.side[which];
-    Run run;
-    run.token0 = (unit - s.unit0) * s.tpw;
-    if (run.token0 >= s.tokens) return;
-    run.count = static_cast<int>(min(static_cast<int64_t>(s.tpw), s.tokens - run.token0));
-    float2 *cs = all_cs[warp];
+// ---- forward, and append ---------------------------------------------------
 
-    const int lanes = 1 << s.sg_log2, sub = lane >> s.sg_log2, step = 32 >> s.sg_log2;
-    const int HM = s.H * s.M, vectors = run.count * HM;
+template <typename T, int V, bool PAGED>
+__device__ __forceinline__ void forward_side(const QkrArgs &a, const QkrSide &s, WarpTokens &w)
+{
+    constexpr int SPL = kSlots<V>, P = kPairsOf<V>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lanes = 1 << s.sg_log2, sub = lane >> s.sg_log2, step = 32 >> s.sg_log2, HM = s.H * s.M;
     Slot slot[SPL];
-    float wa[SPL][V], wb[SPL][V];
+    float2 wa[SPL][P], wb[SPL][P];
 #pragma unroll
     for (int p = 0; p < SPL; ++p) {
         slot[p] = slot_of<V>(s, (lane & (lanes - 1)) + p * 32, a.interleaved);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            wa[p][j] = s.w && slot[p].a >= 0 ? s.w[slot[p].a + j] : 1.f;
-            wb[p][j] = s.w && slot[p].b >= 0 ? s.w[slot[p].b + j] : 1.f;
-        }
+        weights_of<V>(s, slot[p].a, wa[p]);
+        weights_of<V>(s, slot[p].b, wb[p]);
     }
+    // A warp's turns: runs of tokens, or parts of one token's vectors.
+    for (int64_t of = (blockIdx.x - s.unit0) * kQkrWarps + warp;; of += static_cast<int64_t>(s.units) * kQkrWarps) {
+    const int64_t part = s.parts > 1 ? of % s.parts : 0;
+    Run run;
+    run.token0 = s.parts > 1 ? of / s.parts : of * s.tpw;
+    if (run.token0 >= s.tokens) return;
+    run.count = static_cast<int>(min(static_cast<int64_t>(s.tpw), s.tokens - run.token0));
+    __syncwarp();  // the turn before has been read
+    fill_places<PAGED>(a, s, run, w);
+    __syncwarp();
+    const int begin = static_cast<int>(part) * s.per, vectors = s.parts > 1 ? min(begin + s.per, HM) : run.count * HM;
     Piece<T, V> xa[kAhead][SPL], xb[kAhead][SPL];
-    int64_t to[kAhead];  // where the vector goes, or -1
+    int at[kAhead];  // the vector's token and place in it, or -1
     const auto fetch = [&](int i0) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int i = i0 + u * step;
-            to[u] = -1;
-            if (i >= vectors) continue;
-            const int t = static_cast<int>(s.div_vec.div(i)), hm = i - t * HM, h = s.M == 2 ? hm >> 1 : hm, m = s.M == 2 ? hm & 1 : 0;
-            int b, l;
-            token_place(s, run.token0 + t, b, l);
-            const T *x = static_cast<const T *>(s.x) + b * s.xs[0] + l * s.xs[1] + h * s.xs[2] + m * s.xs[3];
+            const bool live = i < vectors;
+            const int t = live ? static_cast<int>(s.div_vec.div(i)) : 0, hm = i - t * HM, h = s.M == 2 ? hm >> 1 : hm, m = s.M == 2 ? hm & 1 : 0;
+            const T *x = static_cast<const T *>(s.x) + w.from[t] + h * s.xs[2] + m * s.xs[3];
 #pragma unroll
             for (int p = 0; p < SPL; ++p) {
-                if (slot[p].a >= 0) xa[u][p] = load_piece<T, V>(x, slot[p].a);
-                if (slot[p].b >= 0) xb[u][p] = load_piece<T, V>(x, slot[p].b);
+                xa[u][p] = load_piece<T, V>(x, slot[p].a, live);
+                xb[u][p] = load_piece<T, V>(x, slot[p].b, live);
             }
-            to[u] = b * s.ys[0] + l * s.ys[1] + h * s.ys[2] + m * s.ys[3];
+            at[u] = live ? i : -1;
         }
     };
-    fetch(sub);
-
-    fill_angles(a, s, run, cs);
-    if (PAGED && s.paged && lane < run.count) {
-        int b, l;
-        token_place(s, run.token0 + lane, b, l);
-        int2 at = make_int2(-1, 0);
-        const int64_t place = static_cast<int64_t>(a.lengths[b]) + l;
-        const int count = a.counts ? a.counts[b] : s.L;
-        if (l < count && place >= 0 && place < static_cast<int64_t>(a.table_pages) * a.page_size) {
-            const int n = static_cast<int>(a.div_page.div(static_cast<uint32_t>(place)));
-            const int page = a.table[static_cast<int64_t>(b) * a.table_pages + n];
-            if (page >= 0 && page < a.num_pages) at = make_int2(page, static_cast<int>(place) - n * a.page_size);
-        }
-        all_where[warp][lane] = at;
-    }
+    fetch(begin + sub);
+    fill_angles(a, s, run, w);
     __syncwarp();
 
-    for (int i0 = sub; i0 - sub < vectors; i0 += kAhead * step) {
+    for (int i0 = begin + sub; i0 - sub < vectors; i0 += kAhead * step) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int i = i0 + u * step;
-            const bool live = to[u] >= 0;
-            const int t = live ? static_cast<int>(s.div_vec.div(i)) : 0;
-            float fa[SPL][V], fb[SPL][V];
-            float sq = 0.f;
+            const int i = at[u], t = i >= 0 ? static_cast<int>(s.div_vec.div(i)) : 0;
+            float2 fa[SPL][P], fb[SPL][P], sq = {0.f, 0.f};
 #pragma unroll
-            for (int p = 0; p < SPL; ++p)
+            for (int p = 0; p < SPL; ++p) {
+                unpack<T, V>(xa[u][p], fa[p]);
+                unpack<T, V>(xb[u][p], fb[p]);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    fa[p][j] = live && slot[p].a >= 0 ? qkr_float(xa[u][p].v[j]) : 0.f;
-                    fb[p][j] = live && slot[p].b >= 0 ? qkr_float(xb[u][p].v[j]) : 0.f;
-                    sq = fmaf(fa[p][j], fa[p][j], sq);
-                    sq = fmaf(fb[p][j], fb[p][j], sq);
+                for (int j = 0; j < P; ++j) {
+                    sq = fma2(fa[p][j], fa[p][j], sq);
+                    sq = fma2(fb[p][j], fb[p][j], sq);
                 }
+            }
             if (s.normed) {
-                const float r = rsqrtf(fmaf(lanes_sum(sq, s.sg_log2), s.inv_D, a.eps));
+                const float r1 = rsqrtf(fmaf(lanes_sum(sq.x + sq.y, s.sg_log2), s.inv_D, a.eps));
+                const float2 r = {r1, r1};
 #pragma unroll
                 for (int p = 0; p < SPL; ++p)
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        fa[p][j] = fa[p][j] * r * wa[p][j];
-                        fb[p][j] = fb[p][j] * r * wb[p][j];
+                    for (int j = 0; j < P; ++j) {
+                        fa[p][j] = mul2(mul2(fa[p][j], r), wa[p][j]);
+                        fb[p][j] = mul2(mul2(fb[p][j], r), wb[p][j]);
                     }
             }
-            if (!live) continue;
-            int64_t at = to[u];
-            if (PAGED && s.paged) {
-                const int2 w = all_where[warp][t];
-                if (w.x < 0) continue;
-                const int hm = i - t * HM, h = s.M == 2 ? hm >> 1 : hm, m = s.M == 2 ? hm & 1 : 0;
-                at = w.x * s.ys[0] + w.y * s.ys[1] + h * s.ys[2] + m * s.ys[3];
-            }
-            T *y = static_cast<T *>(s.y) + at;
+            const int64_t to = w.to[t];
+            if (i < 0 || (PAGED && to < 0)) continue;
+            const int hm = i - t * HM, h = s.M == 2 ? hm >> 1 : hm, m = s.M == 2 ? hm & 1 : 0;
+            T *y = static_cast<T *>(s.y) + to + h * s.ys[2] + m * s.ys[3];
 #pragma unroll
             for (int p = 0; p < SPL; ++p) {
-                if (slot[p].pair >= 0) turn<V, false>(cs + t * (s.R / 2) + slot[p].pair, a.interleaved, fa[p], fb[p]);
-                Piece<T, V> oa, ob;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    oa.v[j] = qkr_round<T>(fa[p][j]);
-                    ob.v[j] = qkr_round<T>(fb[p][j]);
+                if (slot[p].pair >= 0) {
+                    const int k = t * (s.R / 2) + slot[p].pair;
+                    turn<V, false>(w.c + k, w.s + k, a.interleaved, fa[p], fb[p]);
                 }
-                if (slot[p].a >= 0) *reinterpret_cast<decltype(oa.raw) *>(y + slot[p].a) = oa.raw;
-                if (slot[p].b >= 0) *reinterpret_cast<decltype(ob.raw) *>(y + slot[p].b) = ob.raw;
+                store_piece<T, V>(y, slot[p].a, fa[p]);
+                store_piece<T, V>(y, slot[p].b, fb[p]);
             }
         }
-        fetch(i0 + kAhead * step);
+        if (i0 - sub + kAhead * step < vectors) fetch(i0 + kAhead * step);
     }
+    }
+}
+
+// A CTA's side. The sides are told apart here and not by an index, so that their
+// fields are operands of instructions and not loads.
+__device__ __forceinline__ int which_side(const QkrArgs &a)
+{
+    const int64_t cta = blockIdx.x;
+    return a.sides > 2 && cta >= a.side[2].unit0 ? 2 : a.sides > 1 && cta >= a.side[1].unit0 ? 1 : 0;
+}
+
+template <typename T, int V, bool PAGED>
+__global__ void __launch_bounds__(kQkrThreads, 3) qkr_forward_kernel(const __grid_constant__ QkrArgs a)
+{
+    __shared__ __align__(16) WarpTokens all[kQkrWarps];
+    WarpTokens &w = all[threadIdx.x >> 5];
+    const int which = which_side(a);
+    if (which == 0) forward_side<T, V, PAGED>(a, a.side[0], w);
+    else if (which == 1) forward_side<T, V, PAGED>(a, a.side[1], w);
+    else if (PAGED) forward_side<T, V, PAGED>(a, a.side[2], w);
 }
 
 // ---- backward --------------------------------------------------------------
@@ -287,132 +382,113 @@ __global__ void __launch_bounds__(kQkrThreads) qkr_forward_kernel(const __grid_c
 // weight's gradient over all of its vectors in registers, and a CTA leaves one
 // row of sums.
 template <typename T, int V>
-__global__ void __launch_bounds__(kQkrThreads) qkr_backward_kernel(const __grid_constant__ QkrArgs a)
+__device__ __forceinline__ void backward_side(const QkrArgs &a, const QkrSide &s, WarpTokens &w, float (&sums)[kQkrWarps][QKR_MAX_WIDTH])
 {
-    constexpr int SPL = kSlots<T, V>;
-    __shared__ __align__(16) float2 all_cs[kQkrWarps][kPairs];
-    __shared__ float sums[kQkrWarps][QKR_MAX_WIDTH];
+    constexpr int SPL = kSlots<V>, P = kPairsOf<V>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int which = 0;
-    while (which + 1 < a.sides && static_cast<int64_t>(blockIdx.x) >= a.side[which + 1].unit0) ++which;
-    const QkrSide &s = a.side[which];
     const int cta = static_cast<int>(blockIdx.x - s.unit0);
-    float2 *cs = all_cs[warp];
     const int lanes = 1 << s.sg_log2, sub = lane >> s.sg_log2, step = 32 >> s.sg_log2, HM = s.H * s.M;
     Slot slot[SPL];
-    float wa[SPL][V], wb[SPL][V], ga[SPL][V], gb[SPL][V];
+    float2 wa[SPL][P], wb[SPL][P], ga[SPL][P], gb[SPL][P];
 #pragma unroll
     for (int p = 0; p < SPL; ++p) {
         slot[p] = slot_of<V>(s, (lane & (lanes - 1)) + p * 32, a.interleaved);
+        weights_of<V>(s, slot[p].a, wa[p]);
+        weights_of<V>(s, slot[p].b, wb[p]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            wa[p][j] = s.w && slot[p].a >= 0 ? s.w[slot[p].a + j] : 1.f;
-            wb[p][j] = s.w && slot[p].b >= 0 ? s.w[slot[p].b + j] : 1.f;
-            ga[p][j] = gb[p][j] = 0.f;
-        }
+        for (int j = 0; j < P; ++j) ga[p][j] = gb[p][j] = {0.f, 0.f};
     }
     for (int64_t r = static_cast<int64_t>(cta) * kQkrWarps + warp; r * s.tpw < s.tokens; r += static_cast<int64_t>(s.units) * kQkrWarps) {
         Run run;
         run.token0 = r * s.tpw;
         run.count = static_cast<int>(min(static_cast<int64_t>(s.tpw), s.tokens - run.token0));
         const int vectors = run.count * HM;
+        __syncwarp();  // the run before has been read
+        fill_places<false>(a, s, run, w);
+        __syncwarp();
         Piece<T, V> xa[kAhead][SPL], xb[kAhead][SPL], za[kAhead][SPL], zb[kAhead][SPL];
-        int64_t to[kAhead];
         const auto fetch = [&](int i0) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int i = i0 + u * step;
-                to[u] = -1;
-                if (i >= vectors) continue;
-                const int t = static_cast<int>(s.div_vec.div(i)), hm = i - t * HM;
-                int b, l;
-                token_place(s, run.token0 + t, b, l);
-                const T *x = static_cast<const T *>(s.x) + b * s.xs[0] + l * s.xs[1] + (hm >> 1) * s.xs[2] + (hm & 1) * s.xs[3];
-                to[u] = (run.token0 * HM + i) * s.D;
-                const T *g = static_cast<const T *>(s.g) + to[u];
+                const bool live = i < vectors;
+                const int t = live ? static_cast<int>(s.div_vec.div(i)) : 0, hm = i - t * HM;
+                const T *x = static_cast<const T *>(s.x) + w.from[t] + (hm >> 1) * s.xs[2] + (hm & 1) * s.xs[3];
+                const T *g = static_cast<const T *>(s.g) + (run.token0 * HM + i) * s.D;
 #pragma unroll
                 for (int p = 0; p < SPL; ++p) {
-                    if (slot[p].a >= 0) {
-                        za[u][p] = load_piece<T, V>(g, slot[p].a);
-                        if (s.normed) xa[u][p] = load_piece<T, V>(x, slot[p].a);
-                    }
-                    if (slot[p].b >= 0) {
-                        zb[u][p] = load_piece<T, V>(g, slot[p].b);
-                        if (s.normed) xb[u][p] = load_piece<T, V>(x, slot[p].b);
-                    }
+                    za[u][p] = load_piece<T, V>(g, slot[p].a, live);
+                    zb[u][p] = load_piece<T, V>(g, slot[p].b, live);
+                    xa[u][p] = load_piece<T, V>(x, slot[p].a, live && s.normed);
+                    xb[u][p] = load_piece<T, V>(x, slot[p].b, live && s.normed);
                 }
             }
         };
         fetch(sub);
-        __syncwarp();  // the run before has been read
-        fill_angles(a, s, run, cs);
+        fill_angles(a, s, run, w);
         __syncwarp();
         for (int i0 = sub; i0 - sub < vectors; i0 += kAhead * step) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int i = i0 + u * step;
-                const bool live = to[u] >= 0;
+                const bool live = i < vectors;
                 const int t = live ? static_cast<int>(s.div_vec.div(i)) : 0;
-                float ha[SPL][V], hb[SPL][V];
+                float2 ha[SPL][P], hb[SPL][P];
 #pragma unroll
                 for (int p = 0; p < SPL; ++p) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        ha[p][j] = live && slot[p].a >= 0 ? qkr_float(za[u][p].v[j]) : 0.f;
-                        hb[p][j] = live && slot[p].b >= 0 ? qkr_float(zb[u][p].v[j]) : 0.f;
+                    unpack<T, V>(za[u][p], ha[p]);
+                    unpack<T, V>(zb[u][p], hb[p]);
+                    if (slot[p].pair >= 0) {
+                        const int k = t * (s.R / 2) + slot[p].pair;
+                        turn<V, true>(w.c + k, w.s + k, a.interleaved, ha[p], hb[p]);
                     }
-                    if (slot[p].pair >= 0 && live) turn<V, true>(cs + t * (s.R / 2) + slot[p].pair, a.interleaved, ha[p], hb[p]);
                 }
                 if (s.normed) {
-                    float na[SPL][V], nb[SPL][V], sq = 0.f;
+                    float2 na[SPL][P], nb[SPL][P], sq = {0.f, 0.f}, dot = {0.f, 0.f};
 #pragma unroll
-                    for (int p = 0; p < SPL; ++p)
+                    for (int p = 0; p < SPL; ++p) {
+                        unpack<T, V>(xa[u][p], na[p]);
+                        unpack<T, V>(xb[u][p], nb[p]);
 #pragma unroll
-                        for (int j = 0; j < V; ++j) {
-                            na[p][j] = live && slot[p].a >= 0 ? qkr_float(xa[u][p].v[j]) : 0.f;
-                            nb[p][j] = live && slot[p].b >= 0 ? qkr_float(xb[u][p].v[j]) : 0.f;
-                            sq = fmaf(na[p][j], na[p][j], sq);
-                            sq = fmaf(nb[p][j], nb[p][j], sq);
+                        for (int j = 0; j < P; ++j) {
+                            sq = fma2(na[p][j], na[p][j], sq);
+                            sq = fma2(nb[p][j], nb[p][j], sq);
                         }
-                    const float rn = rsqrtf(fmaf(lanes_sum(sq, s.sg_log2), s.inv_D, a.eps));
-                    float dot = 0.f;
+                    }
+                    const float rn = rsqrtf(fmaf(lanes_sum(sq.x + sq.y, s.sg_log2), s.inv_D, a.eps));
+                    const float2 r2 = {rn, rn};
 #pragma unroll
                     for (int p = 0; p < SPL; ++p)
 #pragma unroll
-                        for (int j = 0; j < V; ++j) {
-                            na[p][j] *= rn;
-                            nb[p][j] *= rn;
-                            ga[p][j] = fmaf(ha[p][j], na[p][j], ga[p][j]);
-                            gb[p][j] = fmaf(hb[p][j], nb[p][j], gb[p][j]);
-                            ha[p][j] *= wa[p][j];
-                            hb[p][j] *= wb[p][j];
-                            dot = fmaf(ha[p][j], na[p][j], dot);
-                            dot = fmaf(hb[p][j], nb[p][j], dot);
+                        for (int j = 0; j < P; ++j) {
+                            na[p][j] = mul2(na[p][j], r2);
+                            nb[p][j] = mul2(nb[p][j], r2);
+                            ga[p][j] = fma2(ha[p][j], na[p][j], ga[p][j]);
+                            gb[p][j] = fma2(hb[p][j], nb[p][j], gb[p][j]);
+                            ha[p][j] = mul2(ha[p][j], wa[p][j]);
+                            hb[p][j] = mul2(hb[p][j], wb[p][j]);
+                            dot = fma2(ha[p][j], na[p][j], dot);
+                            dot = fma2(hb[p][j], nb[p][j], dot);
                         }
-                    const float mean = lanes_sum(dot, s.sg_log2) * s.inv_D;
+                    const float mean = -lanes_sum(dot.x + dot.y, s.sg_log2) * s.inv_D;
+                    const float2 m2 = {mean, mean};
 #pragma unroll
                     for (int p = 0; p < SPL; ++p)
 #pragma unroll
-                        for (int j = 0; j < V; ++j) {
-                            ha[p][j] = rn * fmaf(-na[p][j], mean, ha[p][j]);
-                            hb[p][j] = rn * fmaf(-nb[p][j], mean, hb[p][j]);
+                        for (int j = 0; j < P; ++j) {
+                            ha[p][j] = mul2(r2, fma2(na[p][j], m2, ha[p][j]));
+                            hb[p][j] = mul2(r2, fma2(nb[p][j], m2, hb[p][j]));
                         }
                 }
                 if (!live) continue;
-                T *y = static_cast<T *>(s.y) + to[u];
+                T *y = static_cast<T *>(s.y) + (run.token0 * HM + i) * s.D;
 #pragma unroll
                 for (int p = 0; p < SPL; ++p) {
-                    Piece<T, V> oa, ob;
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        oa.v[j] = qkr_round<T>(ha[p][j]);
-                        ob.v[j] = qkr_round<T>(hb[p][j]);
-                    }
-                    if (slot[p].a >= 0) *reinterpret_cast<decltype(oa.raw) *>(y + slot[p].a) = oa.raw;
-                    if (slot[p].b >= 0) *reinterpret_cast<decltype(ob.raw) *>(y + slot[p].b) = ob.raw;
+                    store_piece<T, V>(y, slot[p].a, ha[p]);
+                    store_piece<T, V>(y, slot[p].b, hb[p]);
                 }
             }
-            fetch(i0 + kAhead * step);
+            if (i0 - sub + kAhead * step < vectors) fetch(i0 + kAhead * step);
         }
     }
     if (!s.part) return;
@@ -420,35 +496,51 @@ __global__ void __launch_bounds__(kQkrThreads) qkr_backward_kernel(const __grid_
     for (int p = 0; p < SPL; ++p)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
+            float x = j % 2 ? ga[p][j / 2].y : ga[p][j / 2].x, y = j % 2 ? gb[p][j / 2].y : gb[p][j / 2].x;
             for (int o = lanes; o < 32; o <<= 1) {
-                ga[p][j] += __shfl_xor_sync(0xffffffffu, ga[p][j], o);
-                gb[p][j] += __shfl_xor_sync(0xffffffffu, gb[p][j], o);
+                x += __shfl_xor_sync(0xffffffffu, x, o);
+                y += __shfl_xor_sync(0xffffffffu, y, o);
             }
             if (sub == 0) {
-                if (slot[p].a >= 0) sums[warp][slot[p].a + j] = ga[p][j];
-                if (slot[p].b >= 0) sums[warp][slot[p].b + j] = gb[p][j];
+                if (slot[p].a >= 0) sums[warp][slot[p].a + j] = x;
+                if (slot[p].b >= 0) sums[warp][slot[p].b + j] = y;
             }
         }
     __syncthreads();
     for (int d = threadIdx.x; d < s.D; d += kQkrThreads) {
         float t = 0.f;
 #pragma unroll
-        for (int w = 0; w < kQkrWarps; ++w) t += sums[w][d];
+        for (int k = 0; k < kQkrWarps; ++k) t += sums[k][d];
         s.part[static_cast<int64_t>(cta) * s.D + d] = t;
     }
 }
 
-// grad_weight of a side: the CTAs' rows in a fixed order, one warp per channel.
-__global__ void __launch_bounds__(kQkrThreads) qkr_weight_kernel(const __grid_constant__ QkrArgs a)
+template <typename T, int V> __global__ void __launch_bounds__(kQkrThreads, 2) qkr_backward_kernel(const __grid_constant__ QkrArgs a)
 {
-    pdl_wait();
+    __shared__ __align__(16) WarpTokens all[kQkrWarps];
+    __shared__ float sums[kQkrWarps][QKR_MAX_WIDTH];
+    WarpTokens &w = all[threadIdx.x >> 5];
+    if (which_side(a) == 0) backward_side<T, V>(a, a.side[0], w, sums);
+    else backward_side<T, V>(a, a.side[1], w, sums);
+}
+
+// grad_weight of a side: the CTAs' rows in a fixed order. A block takes 32
+// channels, its 32 warps share the rows.
+__global__ void __launch_bounds__(1024) qkr_weight_kernel(const __grid_constant__ QkrArgs a)
+{
+    __shared__ float sums[32][33];
     const QkrSide &s = a.side[blockIdx.y];
-    const int d = blockIdx.x * kQkrWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (!s.part || d >= s.D) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = blockIdx.x * 32 + lane;
+    pdl_wait();
+    if (!s.part) return;
     float t = 0.f;
-    for (int c = lane; c < s.units; c += 32) t += s.part[static_cast<int64_t>(c) * s.D + d];
-    t = lanes_sum(t, 5);
-    if (lane == 0) s.grad_w[d] = t;
+    if (d < s.D)
+#pragma unroll 4
+        for (int c = warp; c < s.units; c += 32) t += s.part[static_cast<int64_t>(c) * s.D + d];
+    sums[warp][lane] = t;
+    __syncthreads();
+    t = lanes_sum(sums[lane][warp], 5);  // of channel blockIdx.x * 32 + warp
+    if (lane == 0 && blockIdx.x * 32 + warp < s.D) s.grad_w[blockIdx.x * 32 + warp] = t;
 }
 
 // ---- host ------------------------------------------------------------------
@@ -481,6 +573,15 @@ int plan_sides(QkrArgs &a, int elem, bool backward)
         int tpw = (want + vec - 1) / vec;
         while (tpw > 1 && (s.tokens / tpw < 152 * 16 || tpw * (s.R / 2) > kPairs || tpw > kTokens)) tpw = (tpw + 1) / 2;
         s.tpw = tpw;
+        // Few tokens of many heads: warps share a token, two vectors at a time each.
+        s.parts = 1;
+        s.per = vec;
+        if (!backward && tpw == 1 && vec > want)
+            while (s.parts < 16 && s.tokens * s.parts < 152 * 8 && vec > want * s.parts) s.parts *= 2;
+        if (s.parts > 1) {
+            s.per = ((vec + s.parts - 1) / s.parts + 1) / 2 * 2;
+            s.parts = (vec + s.per - 1) / s.per;
+        }
         s.div_L = FastDiv::make(static_cast<uint32_t>(s.L));
         s.div_vec = FastDiv::make(static_cast<uint32_t>(vec));
         s.div_hp = FastDiv::make(static_cast<uint32_t>(s.R > 0 ? s.R / 2 : 1));
@@ -515,22 +616,30 @@ template <typename T> cudaError_t backward_pieces(const QkrArgs &a, int V, unsig
     return V == 4 ? backward_run<T, 4>(a, grid, st) : V == 2 ? backward_run<T, 2>(a, grid, st) : backward_run<T, 1>(a, grid, st);
 }
 
-constexpr int kBackwardCtas = 152 * 4;  // of both sides together
+// CTAs of all sides together where their warps take many turns, as many as are
+// resident: a warp then sets up once.
+constexpr int kBackwardCtas = 152 * 2, kForwardCtas = 152 * 3;
 
-// Units of each side, in proportion to its vectors.
-void backward_units(QkrArgs &a)
+// CTAs of each side, in proportion to its vectors; in the forward pass a warp
+// for each turn where it would take fewer than `least` of them, because turns
+// that do not come out even leave SMs idle at the end.
+unsigned share_ctas(QkrArgs &a, int ctas, int least)
 {
-    int64_t all = 0, unit = 0;
-    for (int i = 0; i < a.sides; ++i) all += a.side[i].tokens * a.side[i].H;
+    int64_t all = 0, unit = 0, every = 0;
+    for (int i = 0; i < a.sides; ++i) {
+        all += a.side[i].tokens * a.side[i].H;
+        every += (a.side[i].tokens + a.side[i].tpw - 1) / a.side[i].tpw * a.side[i].parts;
+    }
+    const bool one = every < static_cast<int64_t>(ctas) * kQkrWarps * least;
     for (int i = 0; i < a.sides; ++i) {
         QkrSide &s = a.side[i];
-        const int64_t runs = (s.tokens + static_cast<int64_t>(s.tpw) * kQkrWarps - 1) / (static_cast<int64_t>(s.tpw) * kQkrWarps);
-        int64_t n = static_cast<int64_t>(static_cast<double>(kBackwardCtas) * s.tokens * s.H / all);
-        n = n < 1 ? 1 : n;
-        s.units = static_cast<int32_t>(n < runs ? n : runs);
+        const int64_t turns = (s.tokens + s.tpw - 1) / s.tpw * s.parts, most = (turns + kQkrWarps - 1) / kQkrWarps;
+        const int64_t n = static_cast<int64_t>(static_cast<double>(ctas) * s.tokens * s.H / all);
+        s.units = static_cast<int32_t>(one ? most : n < 1 ? 1 : n < most ? n : most);
         s.unit0 = unit;
         unit += s.units;
     }
+    return static_cast<unsigned>(unit);
 }
 
 size_t part_bytes(const QkrSide &s) { return (static_cast<size_t>(kBackwardCtas + 1) * s.D * sizeof(float) + 255) & ~size_t{255}; }
@@ -603,12 +712,7 @@ da_status qkr_launch_forward(QkrArgs &a, int dtype, cudaStream_t st)
 {
     if (a.sides == 0) return DA_OK;
     const int V = plan_sides(a, dtype == DA_F32 ? 4 : 2, false);
-    int64_t units = 0;
-    for (int i = 0; i < a.sides; ++i) {
-        a.side[i].unit0 = units;
-        units += (a.side[i].tokens + a.side[i].tpw - 1) / a.side[i].tpw;
-    }
-    const unsigned grid = static_cast<unsigned>((units + kQkrWarps - 1) / kQkrWarps);
+    const unsigned grid = share_ctas(a, kForwardCtas, 4);
     const cudaError_t e = dtype == DA_F32    ? forward_pieces<float>(a, V, grid, st)
                           : dtype == DA_BF16 ? forward_pieces<__nv_bfloat16>(a, V, grid, st)
                                              : forward_pieces<__half>(a, V, grid, st);
@@ -677,15 +781,12 @@ da_status qkr_backward(const qkr_problem *p, const void *grad_out_q, const void 
         if (float *w = i ? grad_k_weight : grad_q_weight; w && !had[i]) e = cudaMemsetAsync(w, 0, sizeof(float) * p->width, cs);
     if (e == cudaSuccess && a.sides > 0) {
         const int V = da::plan_sides(a, elem, true);
-        da::backward_units(a);
-        const da::QkrSide &last = a.side[a.sides - 1];
-        const unsigned grid = static_cast<unsigned>(last.unit0 + last.units);
+        const unsigned grid = da::share_ctas(a, da::kBackwardCtas, 0);
         e = p->dtype == DA_F32    ? da::backward_pieces<float>(a, V, grid, cs)
             : p->dtype == DA_BF16 ? da::backward_pieces<__nv_bfloat16>(a, V, grid, cs)
                                   : da::backward_pieces<__half>(a, V, grid, cs);
         if (e == cudaSuccess && need > 0)
-            e = da::launch_pdl(da::qkr_weight_kernel, dim3((p->width + da::kQkrWarps - 1) / da::kQkrWarps, a.sides),
-                               dim3(da::kQkrThreads), 0, cs, a);
+            e = da::launch_pdl(da::qkr_weight_kernel, dim3((p->width + 31) / 32, a.sides), dim3(1024), 0, cs, a);
     }
     return e == cudaSuccess ? DA_OK : da::cuda_fail(e, "rotary norm backward launch");
 }
