@@ -162,8 +162,13 @@ void strides(const Tensor &t, int64_t *to, int n)
     for (int i = 0; i < n; ++i) to[i] = t.stride(i);
 }
 
-// The tensors' device and its current stream.
+// The tensors' device and its current stream, without Python's lock: allocations
+// and launches can block.
 struct On {
+    struct Unlocked {
+        PyThreadState *state = PyEval_SaveThread();
+        ~Unlocked() { PyEval_RestoreThread(state); }
+    } unlocked;
     c10::cuda::OptionalCUDAGuard guard;
     da_stream_t stream = nullptr;
 
@@ -288,15 +293,17 @@ PyObject *rotary_forward(PyObject *, PyObject *const *a, Py_ssize_t n)
         }
         together({given[0], given[1]}, r.index);
         r.fill();
-        const On at(r.any());
         Tensor out[2];
-        void *to[2] = {nullptr, nullptr};
-        for (int i = 0; i < 2; ++i)
-            if (ins[i]) {
-                out[i] = given[i] ? *given[i] : fresh(*ins[i], ins[i]->sizes());
-                to[i] = plain(out[i]);
-            }
-        check(g_lib.qkr_forward_(&r.p, to[0], to[1], at.stream));
+        {
+            const On at(r.any());
+            void *to[2] = {nullptr, nullptr};
+            for (int i = 0; i < 2; ++i)
+                if (ins[i]) {
+                    out[i] = given[i] ? *given[i] : fresh(*ins[i], ins[i]->sizes());
+                    to[i] = plain(out[i]);
+                }
+            check(g_lib.qkr_forward_(&r.p, to[0], to[1], at.stream));
+        }
         return wrap(out);
     });
 }
@@ -316,20 +323,22 @@ PyObject *rotary_backward(PyObject *, PyObject *const *a, Py_ssize_t n)
         together({gs[0], gs[1]}, r.index);
         r.fill();
         const void *g[2] = {data<void>(gs[0]), data<void>(gs[1])};
-        const On at(r.any());
         Tensor out[4];
-        void *to[4] = {};
-        for (int i = 0; i < 2; ++i) {
-            if (ins[i]) out[i] = fresh(*ins[i], ins[i]->sizes());
-            if (ws[i]) out[2 + i] = fresh(*ws[i], ws[i]->sizes());
+        {
+            const On at(r.any());
+            void *to[4] = {};
+            for (int i = 0; i < 2; ++i) {
+                if (ins[i]) out[i] = fresh(*ins[i], ins[i]->sizes());
+                if (ws[i]) out[2 + i] = fresh(*ws[i], ws[i]->sizes());
+            }
+            for (int i = 0; i < 4; ++i)
+                if (out[i].defined()) to[i] = plain(out[i]);
+            size_t bytes = 0;
+            check(g_lib.qkr_workspace_size_(&r.p, &bytes));
+            const Tensor scratch_ = bytes ? scratch(r.any(), bytes) : Tensor();
+            check(g_lib.qkr_backward_(&r.p, g[0], g[1], to[0], to[1], static_cast<float *>(to[2]), static_cast<float *>(to[3]),
+                                      bytes ? scratch_.data_ptr() : nullptr, bytes, at.stream));
         }
-        for (int i = 0; i < 4; ++i)
-            if (out[i].defined()) to[i] = plain(out[i]);
-        size_t bytes = 0;
-        check(g_lib.qkr_workspace_size_(&r.p, &bytes));
-        const Tensor scratch_ = bytes ? scratch(r.any(), bytes) : Tensor();
-        check(g_lib.qkr_backward_(&r.p, g[0], g[1], to[0], to[1], static_cast<float *>(to[2]), static_cast<float *>(to[3]),
-                                  bytes ? scratch_.data_ptr() : nullptr, bytes, at.stream));
         return wrap(out);
     });
 }
@@ -406,10 +415,12 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
         int64_t vs[3];
         strides(v, vs, 3);
         const void *vp = strided(v, "v");
-        const On at(k);
         Tensor out;
-        if (q) out = given ? *given : fresh(*q, q->sizes());
-        check(g_lib.pg_append_(&r.p, vp, vs, static_cast<int32_t>(v.size(3)), &c, q ? plain(out) : nullptr, at.stream));
+        {
+            const On at(k);
+            if (q) out = given ? *given : fresh(*q, q->sizes());
+            check(g_lib.pg_append_(&r.p, vp, vs, static_cast<int32_t>(v.size(3)), &c, q ? plain(out) : nullptr, at.stream));
+        }
         return wrap(out);
     });
 }
@@ -484,13 +495,16 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n)
         count(n, kAttention + 1);
         const Tensor *given = tensor(a[kAttention], "out");
         const Attention r(a, given);
-        const On at(r.q);
-        const Tensor out = given ? *given : fresh(r.q, at::IntArrayRef(r.shape, 4));
-        void *to = plain(out);
-        size_t bytes = 0;
-        check(g_lib.pg_workspace_size_(&r.p, &bytes));
-        const Tensor ws = bytes ? scratch(r.q, bytes) : Tensor();
-        check(g_lib.pg_attention_(&r.p, to, bytes ? ws.data_ptr() : nullptr, bytes, at.stream));
+        Tensor out;
+        {
+            const On at(r.q);
+            out = given ? *given : fresh(r.q, at::IntArrayRef(r.shape, 4));
+            void *to = plain(out);
+            size_t bytes = 0;
+            check(g_lib.pg_workspace_size_(&r.p, &bytes));
+            const Tensor ws = bytes ? scratch(r.q, bytes) : Tensor();
+            check(g_lib.pg_attention_(&r.p, to, bytes ? ws.data_ptr() : nullptr, bytes, at.stream));
+        }
         return wrap(out);
     });
 }
