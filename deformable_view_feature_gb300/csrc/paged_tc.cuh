@@ -17,11 +17,11 @@
 // second kernel joins them. The shares are made on the device, from lengths and
 // counts, so a captured graph stays balanced while its sequences grow.
 //
-// Warps: groups of four make the weights of up to 32 rows of a map; of four more,
-// one loads keys by TMA and one values (a box lies in one page: gcd(page size, 128)
-// places), one issues the scores' products and one the sums', each as soon as what
-// it needs is there. Weights go through shared memory, rounded to the inputs' type; tiles
-// of up to 32 rows, which memory bounds, carry what that took as a second operand.
+// Warps: 0-3 make the weights of map 0 and 4-7 of map 1, 8 loads keys by TMA and 10
+// values (a box lies in one page: gcd(page size, 128) places), 9 issues the scores'
+// products and 11 the sums', each as soon as what it needs is there. Weights go
+// through shared memory, rounded to the inputs' type; tiles of up to 32 rows,
+// which memory bounds, carry what that took as a second operand.
 #pragma once
 
 #include <cfloat>
@@ -73,8 +73,6 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const float (&v)[16])
 // the product's second 64 rows, which nothing reads, are whatever follows a
 // stage of values.
 template <int DP, int VP, int RT> struct PgShared {
-    // Groups of four warps make the weights of C rows of a map, map 0's groups first.
-    static constexpr int C = RT, groups = 2 * RT / C, threads = (groups + 1) * 128;
     static constexpr int row = DP * 2;                   // bytes of a row of q or k
     static constexpr int q = RT * row;                   // of one map
     static constexpr int kmap = kStep * row;             // of one map's keys of a step
@@ -205,19 +203,19 @@ template <int N> __device__ __forceinline__ void fold(float (&v)[N], int lane, i
     }
 }
 
-// Whether any of the 128 threads of a group has `flag`.
-__device__ __forceinline__ bool vote(int group, bool flag)
+// Whether any of the 128 threads of map m has `flag`.
+__device__ __forceinline__ bool vote(int m, bool flag)
 {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
                  "bar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r)
-                 : "r"(static_cast<uint32_t>(flag)), "r"(1 + group)
+                 : "r"(static_cast<uint32_t>(flag)), "r"(1 + m)
                  : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void sync_group(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
-template <int THREADS> __device__ __forceinline__ void sync_groups() { asm volatile("bar.sync 7, %0;" ::"n"(THREADS) : "memory"); }
+__device__ __forceinline__ void sync_map(int m) { asm volatile("bar.sync %0, 128;" ::"r"(1 + m) : "memory"); }
+__device__ __forceinline__ void sync_maps() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 
 // Maximum over the warp; a NaN counts for nothing.
 __device__ __forceinline__ float warp_max(float v)
@@ -227,13 +225,15 @@ __device__ __forceinline__ float warp_max(float v)
     return r;
 }
 
+constexpr int kPgThreads = 12 * 32;
+
 template <typename T, int DP, int VP, int RT>
-__global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
+__global__ void __launch_bounds__(kPgThreads, 1)
     paged_tc_kernel(const __grid_constant__ PagedTcArgs a, const __grid_constant__ CUtensorMap mq,
                     const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv)
 {
     using F = PgShared<DP, VP, RT>;
-    constexpr int NK = F::ks, NV = F::vs, C = F::C, kThreads = F::threads, kFirst = F::groups * 4;  // warps of weights, then four
+    constexpr int NK = F::ks, NV = F::vs;
     constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t columns = RT == 16 ? 128 : RT == 32 ? 256 : 512;
     extern __shared__ unsigned char raw[];
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
     __shared__ __align__(16) int row_pos[2][RT], row_l[2][RT], row_h[2][RT];
     __shared__ uint64_t row_tree[2][RT];                   // which of at most 64 new tokens the row sees
     __shared__ int64_t row_out[RT];                        // where the row's output is, or -1
-    __shared__ int64_t warp_total[kThreads / 32];
+    __shared__ int64_t warp_total[kPgThreads / 32];
     __shared__ int start[3];
     float *table = reinterpret_cast<float *>(base + F::bytes);  // [nb][H], times log2(e)
     uint16_t *bmap = reinterpret_cast<uint16_t *>(table + a.d.nb * a.d.H);
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
         bar_init(&bars.q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             bar_init(&bars.s_full[i], 1);
-            bar_init(&bars.p_full[i], kFirst);
+            bar_init(&bars.p_full[i], 8);
         }
         for (int s = 0; s < 4; ++s) {
             bar_init(&bars.k_full[s], 1);
@@ -277,13 +277,13 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
         tma_prefetch(&mk);
         tma_prefetch(&mv);
     }
-    if (warp == kFirst + 1) tmem_alloc(&bars.tmem, columns);
-    for (int i = threadIdx.x; i < d.nb * d.H; i += kThreads) table[i] = d.table[i] * kLog2e;
-    for (int i = threadIdx.x; i < 2 * d.reach + 1 && d.nb; i += kThreads)
+    if (warp == 9) tmem_alloc(&bars.tmem, columns);
+    for (int i = threadIdx.x; i < d.nb * d.H; i += kPgThreads) table[i] = d.table[i] * kLog2e;
+    for (int i = threadIdx.x; i < 2 * d.reach + 1 && d.nb; i += kPgThreads)
         bmap[i] = static_cast<uint16_t>(min(max(d.bmap[i], 0), d.nb - 1) * d.H);
     // Rows of q that a tile's queries leave free.
     const int used = a.LP * d.G;
-    for (int i = threadIdx.x; i < 2 * (RT - used) * (F::row / 16); i += kThreads) {
+    for (int i = threadIdx.x; i < 2 * (RT - used) * (F::row / 16); i += kPgThreads) {
         const int m = i >= (RT - used) * (F::row / 16), rest = i - m * (RT - used) * (F::row / 16);
         *reinterpret_cast<uint4 *>(base + m * F::q + used * F::row + rest * 16) = make_uint4(0, 0, 0, 0);
     }
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
 
     const int entries = d.B * a.row_tiles;
     // The CTA's share: threads take consecutive tiles' units, a scan adds them up.
-    const int per = (entries + kThreads - 1) / kThreads;
+    const int per = (entries + kPgThreads - 1) / kPgThreads;
     const int e0 = min(static_cast<int>(threadIdx.x) * per, entries), e1 = min(e0 + per, entries);
     int64_t own = 0;
     for (int e = e0; e < e1; ++e) own += units(tile_of(a, e));
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
     __syncthreads();
     fence_after();
     int64_t total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kPgThreads / 32; ++w) {
         if (w == warp) upto += total;
         total += warp_total[w];
     }
@@ -334,9 +334,9 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
     Walk w;
     w.start(a, share, start[0], start[1], start[2]);
 
-    if (warp == kFirst || warp == kFirst + 2) {
+    if (warp == 8 || warp == 10) {
         // Copies of keys (and queries), and of values: a lane brings one box of a step.
-        const bool keys = warp == kFirst;
+        const bool keys = warp == 8;
         const int boxes = kStep / a.box, blocks = (d.Dv + 63) / 64;
         int t = 0, seg = 0;
         for (; w.left > 0; w.next(a), ++seg) {
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
             const int n = keys ? NK : NV;
             for (int i = max(0, t - n); i < t; ++i) bar_drain(keys ? &bars.k_full[i % n] : &bars.v_full[i % n], (i / n) & 1);
         }
-    } else if (warp == kFirst + 1) {
+    } else if (warp == 9) {
         // Scores. (All lanes walk through the steps, one issues: addresses then
         // stay in uniform registers.)
         const bool issue = elect();
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
         }
         for (int i = max(0, t - NK); i < t; ++i) bar_drain(&bars.k_empty[i % NK], (i / NK) & 1);
         __syncwarp();
-    } else if (warp == kFirst + 3) {
+    } else if (warp == 11) {
         // Sums.
         const bool issue = elect();
         constexpr uint32_t io = shape(bf16, 2 * RT, true) | (1u << 15);
@@ -463,10 +463,9 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
         for (int i = max(0, t - NV); i < t; ++i) bar_drain(&bars.v_empty[i % NV], (i / NV) & 1);
         __syncwarp();
     } else {
-        // Group `gr` has rows g0 .. g0 + C - 1 of map m, columns gr * C .. of the
-        // scores and of the sums; a thread has key kr of each step.
+        // A thread has key kr of each step, and that key's scores of map m with all rows.
         constexpr int X = 16;  // scores that it takes at once
-        const int gr = warp >> 2, m = gr * C / RT, g0 = gr * C % RT, kr = (warp & 3) * 32 + lane;
+        const int m = warp >> 2, kr = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float2 mul = {d.scale_log2, d.scale_log2};
         // The sums with weights of step `of` are done.
@@ -477,15 +476,15 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
             if (none.steps) continue;
             T *to = static_cast<T *>(d.out) + (static_cast<int64_t>(none.b) * d.Lq + none.l0) * d.H * d.Dv;
             const int n = min(a.LP, d.Lq - none.l0) * d.H * d.Dv;
-            for (int i = threadIdx.x; i < n; i += F::groups * 128) to[i] = dattn_round<T>(0.f);
+            for (int i = threadIdx.x; i < n; i += 256) to[i] = dattn_round<T>(0.f);
         }
         const bool few = d.pg.tree && d.Lq <= 64;  // the tree's rows are bits in shared memory
         int t = 0, slot_tile[2] = {-1, -1}, slot_last = 0;
         for (; w.left > 0; w.next(a)) {
             const Tile tile = w.t;
             const int b = tile.b, old = tile.len - tile.count;
-            if (kr < C) {
-                const int r = g0 + kr, dl = static_cast<int>(d.div_G.div(r)), l = min(tile.l0 + dl, d.Lq - 1), h = min(w.n * d.G + r - dl * d.G, d.H - 1);
+            if (const int r = kr; r < RT) {
+                const int dl = static_cast<int>(d.div_G.div(r)), l = min(tile.l0 + dl, d.Lq - 1), h = min(w.n * d.G + r - dl * d.G, d.H - 1);
                 row_l[m][r] = l;
                 row_h[m][r] = h;
                 row_pos[m][r] = d.pos_q ? d.pos_q[static_cast<int64_t>(b) * d.Lq + l] : old + l;
@@ -494,25 +493,25 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                 if (m == 0) row_out[r] = r < used && tile.l0 + dl < d.Lq ? ((static_cast<int64_t>(b) * d.Lq + l) * d.H + h) * d.Dv : -1;
             }
             if (few && (w.first + w.steps) * kStep > old)
-                for (int r = g0 + (warp & 3); r < min(used, g0 + C); r += 4) {
+                for (int r = warp & 3; r < used; r += 4) {
                     const int l = min(tile.l0 + static_cast<int>(d.div_G.div(r)), d.Lq - 1);
                     const uint8_t *of = d.pg.tree + (static_cast<int64_t>(b) * d.Lq + l) * d.Lq;
                     const uint32_t low = __ballot_sync(0xffffffffu, lane < d.Lq && of[lane]), high = __ballot_sync(0xffffffffu, lane + 32 < d.Lq && of[lane + 32]);
                     if (lane == 0) row_tree[m][r] = low | static_cast<uint64_t>(high) << 32;
                 }
-            sync_group(gr);
+            sync_map(m);
             int qmin = kFar, qmax = -kFar;
 #pragma unroll
-            for (int c = lane; c < C; c += 32)
-                if (const int r = g0 + c; r < used && tile.l0 + static_cast<int>(d.div_G.div(r)) < tile.count) {
+            for (int r = lane; r < RT; r += 32)
+                if (r < used && tile.l0 + static_cast<int>(d.div_G.div(r)) < tile.count) {
                     qmin = min(qmin, row_pos[m][r]);
                     qmax = max(qmax, row_pos[m][r]);
                 }
             qmin = __reduce_min_sync(0xffffffffu, qmin);
             qmax = __reduce_max_sync(0xffffffffu, qmax);
-            float2 sum[C / 2];
+            float2 sum[RT / 2];
 #pragma unroll
-            for (int c = 0; c < C / 2; ++c) sum[c] = {0.f, 0.f};
+            for (int c = 0; c < RT / 2; ++c) sum[c] = {0.f, 0.f};
 #pragma unroll 1
             for (int i = 0; i < w.steps; ++i, ++t) {
                 const int j = (w.first + i) * kStep + kr;
@@ -531,30 +530,30 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                     if (d.causal)
 #pragma unroll
                         for (int c = 0; c < X; ++c)
-                            if (pos > row_pos[m][g0 + c0 + c]) see &= ~(1u << c);
+                            if (pos > row_pos[m][c0 + c]) see &= ~(1u << c);
                     if (d.pg.tree && use && j >= old) {
                         if (few) {
 #pragma unroll
                             for (int c = 0; c < X; ++c)
-                                if (!(row_tree[m][g0 + c0 + c] >> (j - old) & 1)) see &= ~(1u << c);
+                                if (!(row_tree[m][c0 + c] >> (j - old) & 1)) see &= ~(1u << c);
                         } else {
 #pragma unroll
                             for (int c = 0; c < X; ++c)
-                                if (!d.pg.tree[(static_cast<int64_t>(b) * d.Lq + row_l[m][g0 + c0 + c]) * d.Lq + j - old]) see &= ~(1u << c);
+                                if (!d.pg.tree[(static_cast<int64_t>(b) * d.Lq + row_l[m][c0 + c]) * d.Lq + j - old]) see &= ~(1u << c);
                         }
                     }
                     float bias[X];
                     if (fast || d.nb == 0) {
 #pragma unroll
-                        for (int c = 0; c < X; ++c) bias[c] = far_bias[m][after][g0 + c0 + c];
+                        for (int c = 0; c < X; ++c) bias[c] = far_bias[m][after][c0 + c];
                     } else {
 #pragma unroll
                         for (int c = 0; c < X; ++c)
-                            bias[c] = table[bmap[min(max(pos - row_pos[m][g0 + c0 + c], -d.reach), d.reach) + d.reach] + row_h[m][g0 + c0 + c]];
+                            bias[c] = table[bmap[min(max(pos - row_pos[m][c0 + c], -d.reach), d.reach) + d.reach] + row_h[m][c0 + c]];
                     }
 #pragma unroll
                     for (int c = 0; c < X; ++c) {
-                        const float y = fmaf(x[c], mul.x, bias[c]) + (less ? noff[m][g0 + c0 + c] : 0.f);
+                        const float y = fmaf(x[c], mul.x, bias[c]) + (less ? noff[m][c0 + c] : 0.f);
                         x[c] = see >> c & 1 ? y : -INFINITY;
                     }
                 };
@@ -562,7 +561,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                 // its row's reference. A segment begins with references. Weights go
                 // to shared memory at once; sums take them from there when they stand.
                 if (t >= F::pbufs) summed(t - F::pbufs);  // the weights' buffer is free
-                const int swz = RT == 16 ? (kr >> 1) & 3 : kr & 7, piece0 = (RT == 64 ? g0 : gr * C) / 8;
+                const int swz = RT == 16 ? (kr >> 1) & 3 : kr & 7, piece0 = RT == 64 ? 0 : m * RT / 8;
                 unsigned char *const pt = base + F::at_p + (t % F::pbufs) * F::pbuf + (RT == 64 ? m * (F::p / 2) : 0) + kr * F::prow;
                 const auto piece = [&](int c) { return reinterpret_cast<uint4 *>(pt + (((piece0 + c / 8) ^ swz) << 4)); };
                 const auto weigh = [&](const float (&x)[X], int c0) {
@@ -582,7 +581,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                         if constexpr (F::rests) piece(c0 + c)[F::p / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 };
-                const uint32_t scores = tS(0, t) + gr * C + lanes;
+                const uint32_t scores = tS(m, t) + lanes;
 #pragma unroll 1
                 for (bool again = false;; again = true) {
                     float top[2] = {-INFINITY, -INFINITY};
@@ -590,9 +589,9 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                         top[0] = INFINITY;
                     } else if (fast && all) {
                         // Most steps: no branches, for the sake of the order of instructions.
-                        const float *o = &off[m][after][g0];
+                        const float *o = &off[m][after][0];
 #pragma unroll
-                        for (int c0 = 0; c0 < C; c0 += X) {
+                        for (int c0 = 0; c0 < RT; c0 += X) {
                             float x[X];
                             tmem_load(scores + c0, x);
 #pragma unroll
@@ -610,7 +609,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                         }
                     } else {
 #pragma unroll 1
-                        for (int c0 = 0; c0 < C; c0 += X) {
+                        for (int c0 = 0; c0 < RT; c0 += X) {
                             float x[X];
                             tmem_load(scores + c0, x);
                             finish(x, c0, true);
@@ -619,23 +618,22 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                             weigh(x, c0);
                         }
                     }
-                    if (again || (i > 0 && !vote(gr, fmaxf(top[0], top[1]) > kLift<T> + kSlack))) break;
+                    if (again || (i > 0 && !vote(m, fmaxf(top[0], top[1]) > kLift<T> + kSlack))) break;
 #pragma unroll 1
-                    for (int c0 = 0; c0 < C; c0 += X) {
+                    for (int c0 = 0; c0 < RT; c0 += X) {
                         float x[X];
                         tmem_load(scores + c0, x);
                         finish(x, c0, false);
-                        float best = -INFINITY;  // of row g0 + c0 + lane
+                        float best = -INFINITY;  // of row c0 + lane
 #pragma unroll
                         for (int c = 0; c < X; ++c) {
                             const float of = warp_max(x[c]);
                             best = lane == c ? of : best;
                         }
-                        if (lane < X) wide[m][warp & 3][g0 + c0 + lane] = best;
+                        if (lane < X) wide[m][warp & 3][c0 + lane] = best;
                     }
-                    sync_group(gr);
-                    if (kr < C) {
-                        const int r = g0 + kr;
+                    sync_map(m);
+                    if (const int r = kr; r < RT) {
                         const float best = fmaxf(fmaxf(wide[m][0][r], wide[m][1][r]), fmaxf(wide[m][2][r], wide[m][3][r]));
                         const float ref = -noff[m][r];
                         const bool raise = best + noff[m][r] > kLift<T> + kSlack;
@@ -644,27 +642,27 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                         for (int k = 0; k < 2; ++k) off[m][k][r] = far_bias[m][k][r] - next;
                         shrink[m][r] = raise ? ex2(ref - next) : 1.f;
                     }
-                    sync_group(gr);
+                    sync_map(m);
                     if (i > 0) {
                         summed(t - 1);
                         fence_after();
 #pragma unroll 1
-                        for (int c0 = 0; c0 < C; c0 += 16) {
+                        for (int c0 = 0; c0 < RT; c0 += 16) {
                             float o[16];
-                            tmem_load(tO + gr * C + c0 + lanes, o);
+                            tmem_load(tO + m * RT + c0 + lanes, o);
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) o[c] *= shrink[m][g0 + c0 + c];
-                            tmem_store(tO + gr * C + c0 + lanes, o);
+                            for (int c = 0; c < 16; ++c) o[c] *= shrink[m][c0 + c];
+                            tmem_store(tO + m * RT + c0 + lanes, o);
                         }
                         tmem_store_wait();
                     }
 #pragma unroll
-                    for (int c = 0; c < C / 2; ++c) sum[c] = mul2(sum[c], *reinterpret_cast<const float2 *>(&shrink[m][g0 + 2 * c]));
+                    for (int c = 0; c < RT / 2; ++c) sum[c] = mul2(sum[c], *reinterpret_cast<const float2 *>(&shrink[m][2 * c]));
                 }
-                if (!all && gr < VP / 64) {
+                if (!all && m < VP / 64) {
                     // 0 * NaN is NaN: unused keys' rows of V become zeros.
                     bar_wait_warp(&bars.v_full[t % NV], (t / NV) & 1, gave_up);
-                    unsigned char *v = base + F::at_v + (t % NV) * F::v + gr * F::vblock + kr * 128;
+                    unsigned char *v = base + F::at_v + (t % NV) * F::v + m * F::vblock + kr * 128;
                     if (!use)
 #pragma unroll
                         for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(v + (((c + lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -675,7 +673,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                 if (lane == 0) bar_arrive(&bars.p_full[t & 1]);
                 // The sum is of the weights as the product takes them.
 #pragma unroll
-                for (int c = 0; c < C; c += 8) {
+                for (int c = 0; c < RT; c += 8) {
                     const uint4 h = *piece(c);
                     sum[c / 2] = add2(sum[c / 2], unpack2<T>(h.x));
                     sum[c / 2 + 1] = add2(sum[c / 2 + 1], unpack2<T>(h.y));
@@ -692,27 +690,27 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
             }
             // The segment's end: weights' sums over the threads, then the sums themselves.
             {
-                float all_sums[C];
+                float all_sums[RT];
 #pragma unroll
-                for (int c = 0; c < C / 2; ++c) {
+                for (int c = 0; c < RT / 2; ++c) {
                     all_sums[2 * c] = sum[c].x;
                     all_sums[2 * c + 1] = sum[c].y;
                 }
-                fold<C>(all_sums, lane, 16);
-                if constexpr (C == 16) {
+                fold<RT>(all_sums, lane, 16);
+                if constexpr (RT == 16) {
                     if ((lane & 1) == 0) wide[m][warp & 3][lane >> 1] = all_sums[0];
                 } else {
 #pragma unroll
-                    for (int c = 0; c < C / 32; ++c) wide[m][warp & 3][g0 + lane * (C / 32) + c] = all_sums[c];
+                    for (int c = 0; c < RT / 32; ++c) wide[m][warp & 3][lane * (RT / 32) + c] = all_sums[c];
                 }
             }
             summed(t - 1);
             fence_after();
-            sync_groups<F::groups * 128>();
+            sync_maps();
             const bool whole = w.first == 0 && w.steps == tile.steps;
             const int dv = (warp & 3) * 32 + lane, k = w.first == 0;
             const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + k;
-            if (const int r = g0 + kr; kr < C) {
+            if (const int r = kr; r < RT) {
                 const float total = wide[m][0][r] + wide[m][1][r] + (wide[m][2][r] + wide[m][3][r]) + (*gave_up ? NAN : 0.f);
                 if (whole) {
                     shrink[m][r] = total == 0.f || row_l[m][r] >= tile.count ? 0.f : (m ? d.lam[row_h[m][r]] : 1.f) / total;
@@ -721,10 +719,10 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                 }
             }
             if (whole) {
-                sync_groups<F::groups * 128>();
-                // Each group takes its share of the rows, of both maps.
+                sync_maps();
+                // The warps of map m take the m-th half of the rows, of both maps.
 #pragma unroll 1
-                for (int r0 = gr * (RT / F::groups); r0 < (gr + 1) * (RT / F::groups); r0 += 8) {
+                for (int r0 = m * (RT / 2); r0 < (m + 1) * (RT / 2); r0 += 8) {
                     float u[8], v[8];
                     __syncwarp();
                     tmem_load(tO + r0 + lanes, u);
@@ -741,7 +739,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                 if (!k) slot_last = w.first + w.steps == tile.steps;
                 float *to = d.part_o + (slot * RT * 2 + m) * d.Dv + dv;
 #pragma unroll 1
-                for (int r0 = g0; r0 < min(used, g0 + C); r0 += 8) {
+                for (int r0 = 0; r0 < used; r0 += 8) {
                     float u[8];
                     __syncwarp();
                     tmem_load(tO + m * RT + r0 + lanes, u);
@@ -751,7 +749,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
                 }
             }
             __syncwarp();
-            sync_groups<F::groups * 128>();  // the next segment's arrays are the same
+            sync_maps();  // the next segment's arrays are the same
         }
         if (threadIdx.x < 2) {
             a.slots[blockIdx.x * 4 + threadIdx.x * 2] = threadIdx.x ? slot_tile[1] : slot_tile[0];
@@ -761,7 +759,7 @@ __global__ void __launch_bounds__(PgShared<DP, VP, RT>::threads, 1)
     }
     fence_before();
     __syncthreads();
-    if (warp == kFirst + 1) {
+    if (warp == 9) {
         fence_after();
         tmem_free(tmem, columns);
     }
@@ -856,7 +854,7 @@ cudaError_t launch_tc(const PagedTcArgs &a, const CUtensorMap &mq, const CUtenso
     const auto kernel = paged_tc_kernel<T, DP, VP, RT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    kernel<<<a.ctas, F::threads, smem, st>>>(a, mq, mk, mv);
+    kernel<<<a.ctas, kPgThreads, smem, st>>>(a, mq, mk, mv);
     e = cudaGetLastError();
     if (e == cudaSuccess && a.ctas > 1 && a.d.Lk > kStep)  // otherwise no tile has pieces
         e = launch_pdl(paged_join_kernel<T>, dim3(a.ctas, (a.LP * a.d.G + kJoinRows - 1) / kJoinRows), dim3(32 * kJoinRows), 0, st, a);

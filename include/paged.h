@@ -65,7 +65,7 @@ da_status pg_append(const qkr_problem *p, const void *v, const int64_t *v_stride
  * sequence b at place j, N * S for Lk, and lengths (clamped to [0, N * S]) for
  * key_lengths: what was there before and the new tokens, whose own places are
  * the last counts[b]. By default query i is at position
- * lengths[b] - counts[b] + i and key j at j.
+ * lengths[b] - counts[b] + i and key j at j. Positions lie in (-2^30, 2^30).
  *
  * Query i < counts[b] sees key j when j < lengths[b], its page is in the cache,
  * key_mask[b, j] != 0, and
