@@ -260,6 +260,16 @@ CASES = {
     "maps outside": dict(B=2, N=9, S=16, T=2, H=4, Hk=2, kind="f16", lengths=[144, 77], layout="maps outside"),
     "long": dict(B=2, N=200, S=64, H=8, Hk=2, D=64, kind="bf16", lengths=[12800, 7001]),
     "long f16": dict(B=3, N=200, S=32, T=3, H=8, Hk=4, D=64, kind="f16", lengths=[6400, 1, 3001], buckets=16, reach=64),
+    "three rows f32": dict(B=2, N=9, S=16, T=1, H=6, Hk=2, D=64, lengths=[144, 77], buckets=8, reach=20),
+    "six rows f32": dict(B=2, N=9, S=16, T=3, H=4, Hk=2, D=64, lengths=[144, 77], tree="random", mask=0.8),
+    "eight rows f16": dict(B=2, N=20, S=20, T=4, H=4, Hk=2, D=40, kind="f16", lengths=[400, 301], tree="random", buckets=8, reach=20, pos="depth"),
+    "three wide rows": dict(B=2, N=9, S=16, T=1, H=3, Hk=1, D=96, Dv=200, lengths=[144, 77]),
+    "five odd rows": dict(B=2, N=30, S=3, T=5, H=1, Hk=1, D=127, Dv=255, kind="bf16", lengths=[90, 33]),
+    "nine rows f32": dict(B=2, N=40, S=20, T=3, H=3, Hk=1, D=64, lengths=[800, 333]),
+    "thirty rows f32": dict(B=2, N=40, S=20, T=15, H=4, Hk=2, D=64, lengths=[800, 333], tree="random", mask=0.7),
+    "thirty wide rows f32": dict(B=2, N=40, S=20, T=15, H=4, Hk=2, D=100, lengths=[800, 333], counts=[15, 4], buckets=8, reach=20),
+    "small pages, many rows": dict(B=2, N=300, S=3, T=45, H=4, Hk=2, D=32, kind="bf16", lengths=[900, 333], tree="random"),
+    "many parts f32": dict(B=1, N=500, S=16, T=1, H=2, Hk=1, lengths=[8000]),
     "long f32": dict(B=2, N=200, S=20, H=4, Hk=2, lengths=[4000, 3001]),
     "one long among short": dict(B=40, N=40, S=64, H=4, Hk=2, D=32, kind="bf16", lengths=[2560] + [3 + b for b in range(39)]),
     "many short": dict(B=300, N=2, S=16, H=4, Hk=4, kind="bf16", lengths=[(b * 7) % 33 for b in range(300)]),
@@ -279,6 +289,19 @@ def test_against_64_bits(name):
     val, tol = paged_reference(**t, **opt)
     check({"out": got}, val, tol)
     assert torch.equal(got, da.paged_attention(**t, **opt)), "results vary from run to run"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("T,H", [(1, 4), (4, 4), (8, 4)])
+def test_few_rows_are_rounded_once(kind, T, H):
+    """Tiles of up to 32 rows carry what rounding took from the weights: in a norm their outputs are off by what one
+    rounding of the exact ones costs, and by a thousandth more for 64 bits' own and fp32's steps."""
+    t, opt = _attention_case(B=2, T=T, N=40, S=16, H=H, Hk=1, D=64, kind=kind, lengths=[640, 401])
+    assert da.paged_path(**t, **opt) == "tensor" and T * H <= 32
+    want = paged_reference(**t, **opt)[0]["out"]
+    once = float((want.to(DT[kind]).double() - want).norm())
+    assert float((da.paged_attention(**t, **opt).double() - want).norm()) <= 1.02 * once
 
 
 @pytest.mark.gpu

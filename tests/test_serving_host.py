@@ -5,14 +5,16 @@ import ctypes
 import os
 import re
 import subprocess
+import types
 import warnings
 
 import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
 
+import __graft_entry__
 import deformable_view_feature_gb300 as da
-from serving_refs import PgCache, PgProblem, QkrProblem, serving_library
+from serving_refs import PgCache, PgProblem, QkrProblem, paged_reference, qkr_reference, serving_library
 
 INCLUDE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
 
@@ -84,3 +86,48 @@ def test_tensors_of_two_devices_are_refused(monkeypatch, call, other):
         a = {n: torch.empty(s, dtype=t, device="cuda:0" if n == other else "cuda:1") for n, (s, t) in CALLS[call].items()}
         with pytest.raises(ValueError, match="one CUDA device"):
             getattr(da, call)(**a)
+
+
+# ---- smoke()'s check of these operators: plain ones pass, zeros do not ------
+
+def _plain():
+    def forward(q, k, turns, wq, wk):
+        return tuple(qkr_reference(x, turns, w)[0]["out"].to(x.dtype) for x, w in ((q, wq), (k, wk)))
+
+    def backward(q, k, gq, gk, turns, wq, wk):
+        v = [qkr_reference(x, turns, w, grad=g)[0] for x, w, g in ((q, wq, gq), (k, wk, gk))]
+        return v[0]["grad_x"].to(q.dtype), v[1]["grad_x"].to(k.dtype), v[0]["grad_weight"], v[1]["grad_weight"]
+
+    def append(k, v, k_cache, v_cache, table, lengths, q, frequencies, q_weight, k_weight):
+        place = lengths[:, None] + torch.arange(k.shape[1])
+        at = table.long().gather(1, place // k_cache.shape[1]), place % k_cache.shape[1]
+        k_cache[at] = qkr_reference(k, frequencies, k_weight, place)[0]["out"].to(k.dtype)
+        v_cache[at] = v
+        return qkr_reference(q, frequencies, q_weight, place)[0]["out"].to(q.dtype)
+
+    def attention(q, k_cache, v_cache, lam, table, lengths):
+        return paged_reference(q, k_cache, v_cache, lam, table, lengths)[0]["out"].to(q.dtype)
+
+    return types.SimpleNamespace(rotary_frequencies=da.rotary_frequencies, qkr_forward=forward, qkr_backward=backward, paged_append=append,
+                                 paged_attention=attention)
+
+
+def test_plain_operators_pass_smoke():
+    __graft_entry__._serving(_plain(), torch.device("cpu"))
+
+
+@pytest.mark.parametrize("name,at", [("qkr_forward", 0), ("qkr_forward", 1), ("qkr_backward", 0), ("qkr_backward", 1), ("qkr_backward", 2),
+                                     ("qkr_backward", 3), ("paged_append", None), ("paged_attention", None)])
+def test_zeros_do_not_pass_smoke(name, at):
+    ops = _plain()
+    right = getattr(ops, name)
+
+    def wrong(*args, **kw):
+        r = right(*args, **kw)
+        if at is None:
+            return torch.zeros_like(r)
+        return tuple(torch.zeros_like(x) if i == at else x for i, x in enumerate(r))
+
+    setattr(ops, name, wrong)
+    with pytest.raises(AssertionError, match="off by"):
+        __graft_entry__._serving(ops, torch.device("cpu"))
