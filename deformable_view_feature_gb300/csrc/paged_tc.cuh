@@ -88,7 +88,7 @@ template <int DP, int VP, int RT> struct PgShared {
     static constexpr int ks = DP == 32 ? 4 : RT == 16 ? 3 : 2, vs = DP == 32 ? 4 : RT <= 32 ? 3 : 2;
     static constexpr int pbufs = RT == 64 || DP == 32 ? 2 : 1;
     static constexpr int at_v = 2 * q, at_k = at_v + vs * v, at_p = at_k + ks * k, bytes = at_p + pbufs * pbuf;
-    static constexpr int arrays = RT * 128 + 3840;     // the kernel's static ones, at most
+    static constexpr int arrays = RT * 128 + 4096;     // the kernel's static ones, at most
     static_assert(bytes + 1024 + kPgBias + arrays <= 227 * 1024, "shared memory");
 };
 
@@ -184,25 +184,6 @@ struct StepInfo {
     int lo[4], hi[4];
 };
 
-// Sums of N columns over the warp's lanes; lane i is left with columns
-// i * N / 32 .. (N >= 32), or with column i / 2 (N = 16).
-template <int N> __device__ __forceinline__ void fold(float (&v)[N], int lane, int o)
-{
-    if constexpr (N == 1) {
-        for (; o; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-    } else if (o) {
-        float h[N / 2];
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            const float keep = lane & o ? v[i + N / 2] : v[i], send = lane & o ? v[i] : v[i + N / 2];
-            h[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-        }
-        fold<N / 2>(h, lane, o >> 1);
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) v[i] = h[i];
-    }
-}
-
 // Whether any of the 128 threads of map m has `flag`.
 __device__ __forceinline__ bool vote(int m, bool flag)
 {
@@ -227,6 +208,18 @@ __device__ __forceinline__ float warp_max(float v)
 
 constexpr int kPgThreads = 12 * 32;
 
+// Weights are summed by a product with ones, as the products take them, so that
+// numerator and denominator have the same roundings. Sums by the threads, which
+// read back their weights, cost 300 instructions and 64 registers of a thread at
+// 64 rows: 1,021 new tokens over 8,001 keys took 149 us with them, 126 without.
+// The operand of [128, 16] ones: its blocks of 8 rows by 16 bytes begin 16 bytes
+// after one another, so that 16 by 2 of them take 384 bytes.
+constexpr int kOnes = 192;
+__device__ __forceinline__ uint64_t ones_operand(const void *ones)
+{
+    return static_cast<uint64_t>((1u << 14) | 1u) << 32 | (smem_addr(ones) >> 4 | (1u << 16));
+}
+
 template <typename T, int DP, int VP, int RT>
 __global__ void __launch_bounds__(kPgThreads, 1)
     paged_tc_kernel(const __grid_constant__ PagedTcArgs a, const __grid_constant__ CUtensorMap mq,
@@ -245,13 +238,14 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     __shared__ __align__(16) float noff[2][RT];            // minus the row's reference
     __shared__ __align__(16) float off[2][2][RT];          // the same, with far_bias
     __shared__ __align__(16) float shrink[2][RT];
-    __shared__ __align__(16) float wide[2][4][RT];         // a warp's maxima, or sums
+    __shared__ __align__(16) float wide[2][4][RT];         // a warp's maxima; weights' sums in [0]
     __shared__ __align__(16) float far_bias[2][2][RT];     // of keys `reach` or more before and after the query
     __shared__ __align__(16) int row_pos[2][RT], row_l[2][RT], row_h[2][RT];
     __shared__ uint64_t row_tree[2][RT];                   // which of at most 64 new tokens the row sees
     __shared__ int64_t row_out[RT];                        // where the row's output is, or -1
     __shared__ int64_t warp_total[kPgThreads / 32];
     __shared__ int start[3];
+    __shared__ __align__(16) T ones[kOnes];
     float *table = reinterpret_cast<float *>(base + F::bytes);  // [nb][H], times log2(e)
     uint16_t *bmap = reinterpret_cast<uint16_t *>(table + a.d.nb * a.d.H);
     const DattnArgs &d = a.d;
@@ -281,6 +275,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     for (int i = threadIdx.x; i < d.nb * d.H; i += kPgThreads) table[i] = d.table[i] * kLog2e;
     for (int i = threadIdx.x; i < 2 * d.reach + 1 && d.nb; i += kPgThreads)
         bmap[i] = static_cast<uint16_t>(min(max(d.bmap[i], 0), d.nb - 1) * d.H);
+    if (threadIdx.x < kOnes) ones[threadIdx.x] = dattn_round<T>(1.f);
     // Rows of q that a tile's queries leave free.
     const int used = a.LP * d.G;
     for (int i = threadIdx.x; i < 2 * (RT - used) * (F::row / 16); i += kPgThreads) {
@@ -330,7 +325,7 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     const uint32_t tmem = uniform(bars.tmem);
     volatile uint32_t *gave_up = &bars.gave_up;
     const auto tS = [&](int m, int t) { return tmem + ((t & 1) * 2 + m) * RT; };
-    const uint32_t tO = tmem + 4 * RT, sb = smem_addr(base);
+    const uint32_t tO = tmem + 4 * RT, tL = tO + 2 * RT, sb = smem_addr(base);  // outputs' sums, weights' sums
     Walk w;
     w.start(a, share, start[0], start[1], start[2]);
 
@@ -436,7 +431,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
     } else if (warp == 11) {
         // Sums.
         const bool issue = elect();
-        constexpr uint32_t io = shape(bf16, 2 * RT, true) | (1u << 15);
+        constexpr uint32_t il = shape(bf16, 2 * RT, true), io = il | (1u << 15);
+        const uint64_t all = ones_operand(ones);
         const Operand<128> dv = over_rows<128>(sb + F::at_v, F::vblock);
         const Operand<F::prow> dp = over_rows<F::prow>(sb + F::at_p, F::p / 2);
         int t = 0;
@@ -455,6 +451,11 @@ __global__ void __launch_bounds__(kPgThreads, 1)
 #pragma unroll
                         for (int c = 0; c < kStep / 16; ++c)
                             mma_ss(tO, dv.at(s * F::v + c * 16 * 128), dp.at(pb + F::p + c * 16 * F::prow), io, true);
+#pragma unroll
+                    for (int c = 0; c < kStep / 16; ++c) mma_ss(tL, all, dp.at(pb + c * 16 * F::prow), il, i > 0 || c > 0);
+                    if (F::rests)
+#pragma unroll
+                        for (int c = 0; c < kStep / 16; ++c) mma_ss(tL, all, dp.at(pb + F::p + c * 16 * F::prow), il, true);
                     mma_commit(&bars.v_empty[s]);
                 }
                 __syncwarp();
@@ -509,9 +510,6 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 }
             qmin = __reduce_min_sync(0xffffffffu, qmin);
             qmax = __reduce_max_sync(0xffffffffu, qmax);
-            float2 sum[RT / 2];
-#pragma unroll
-            for (int c = 0; c < RT / 2; ++c) sum[c] = {0.f, 0.f};
 #pragma unroll 1
             for (int i = 0; i < w.steps; ++i, ++t) {
                 const int j = (w.first + i) * kStep + kr;
@@ -647,17 +645,16 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                         summed(t - 1);
                         fence_after();
 #pragma unroll 1
-                        for (int c0 = 0; c0 < RT; c0 += 16) {
+                        for (int c0 = 0; c0 < 2 * RT; c0 += 16) {
+                            const uint32_t at = (c0 < RT ? tO + c0 : tL + c0 - RT) + m * RT + lanes;
                             float o[16];
-                            tmem_load(tO + m * RT + c0 + lanes, o);
+                            tmem_load(at, o);
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) o[c] *= shrink[m][c0 + c];
-                            tmem_store(tO + m * RT + c0 + lanes, o);
+                            for (int c = 0; c < 16; ++c) o[c] *= shrink[m][(c0 + c) % RT];
+                            tmem_store(at, o);
                         }
                         tmem_store_wait();
                     }
-#pragma unroll
-                    for (int c = 0; c < RT / 2; ++c) sum[c] = mul2(sum[c], *reinterpret_cast<const float2 *>(&shrink[m][2 * c]));
                 }
                 if (!all && m < VP / 64) {
                     // 0 * NaN is NaN: unused keys' rows of V become zeros.
@@ -671,47 +668,25 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(&bars.p_full[t & 1]);
-                // The sum is of the weights as the product takes them.
-#pragma unroll
-                for (int c = 0; c < RT; c += 8) {
-                    const uint4 h = *piece(c);
-                    sum[c / 2] = add2(sum[c / 2], unpack2<T>(h.x));
-                    sum[c / 2 + 1] = add2(sum[c / 2 + 1], unpack2<T>(h.y));
-                    sum[c / 2 + 2] = add2(sum[c / 2 + 2], unpack2<T>(h.z));
-                    sum[c / 2 + 3] = add2(sum[c / 2 + 3], unpack2<T>(h.w));
-                    if constexpr (F::rests) {
-                        const uint4 r = piece(c)[F::p / 16];
-                        sum[c / 2] = add2(sum[c / 2], unpack2<T>(r.x));
-                        sum[c / 2 + 1] = add2(sum[c / 2 + 1], unpack2<T>(r.y));
-                        sum[c / 2 + 2] = add2(sum[c / 2 + 2], unpack2<T>(r.z));
-                        sum[c / 2 + 3] = add2(sum[c / 2 + 3], unpack2<T>(r.w));
-                    }
-                }
-            }
-            // The segment's end: weights' sums over the threads, then the sums themselves.
-            {
-                float all_sums[RT];
-#pragma unroll
-                for (int c = 0; c < RT / 2; ++c) {
-                    all_sums[2 * c] = sum[c].x;
-                    all_sums[2 * c + 1] = sum[c].y;
-                }
-                fold<RT>(all_sums, lane, 16);
-                if constexpr (RT == 16) {
-                    if ((lane & 1) == 0) wide[m][warp & 3][lane >> 1] = all_sums[0];
-                } else {
-#pragma unroll
-                    for (int c = 0; c < RT / 32; ++c) wide[m][warp & 3][lane * (RT / 32) + c] = all_sums[c];
-                }
             }
             summed(t - 1);
             fence_after();
+            if ((warp & 3) == 0)
+#pragma unroll 1
+                for (int c0 = 0; c0 < RT; c0 += 16) {
+                    float l[16];
+                    __syncwarp();
+                    tmem_load(tL + m * RT + c0, l);
+                    if (lane == 0)
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) wide[m][0][c0 + c] = l[c];
+                }
             sync_maps();
             const bool whole = w.first == 0 && w.steps == tile.steps;
             const int dv = (warp & 3) * 32 + lane, k = w.first == 0;
             const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + k;
             if (const int r = kr; r < RT) {
-                const float total = wide[m][0][r] + wide[m][1][r] + (wide[m][2][r] + wide[m][3][r]) + (*gave_up ? NAN : 0.f);
+                const float total = wide[m][0][r] + (*gave_up ? NAN : 0.f);
                 if (whole) {
                     shrink[m][r] = total == 0.f || row_l[m][r] >= tile.count ? 0.f : (m ? d.lam[row_h[m][r]] : 1.f) / total;
                 } else if (r < used) {
