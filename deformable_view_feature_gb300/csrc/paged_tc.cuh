@@ -1,5 +1,7 @@
 // Differential attention over a paged cache on the tensor cores
-// (include/paged.h), for bf16 and fp16.
+// (include/paged.h), for bf16 and fp16: O = P_0 V - lam P_1 V, P_m the softmax of
+// scale K_m q_m^T and the bias over the keys that a row sees, in one pass with a
+// running reference for its maximum.
 //
 // New tokens are few and keys are many, so the keys take the 128 rows of a
 // product and the queries its columns: S_m = K_m q_m^T is [128 keys, RT], RT
@@ -21,7 +23,26 @@
 // values (a box lies in one page: gcd(page size, 128) places), 9 issues the scores'
 // products and 11 the sums', each as soon as what it needs is there. Weights go
 // through shared memory, rounded to the inputs' type; tiles of up to 32 rows,
-// which memory bounds, carry what that took as a second operand.
+// which memory bounds, carry what that took as a second operand, so that their
+// outputs are off by one rounding (2-norm 0.0017 in bf16). With 64 rows, where
+// the warps that make weights bound the kernel, outputs have the error of two
+// independent roundings (0.0025 for bf16, 0.00031 for fp16): a second operand
+// there takes 195 us instead of 149 at 1,021 tokens over 8,001 keys.
+//
+// Measured, in replayed graphs, with the kernel that joins pieces:
+// - a token each over eight caches of up to 32,768 keys (16 heads, 4 key heads,
+//   D = 64, bf16): 80 us, 5.3 TB/s of the 6.8 that a copy reaches; memory bounds
+//   it (DRAM 66 % busy under a cold start), then the uneven ends and the join
+//   (5 us). One ring for keys and values together: 89 us, since values are
+//   needed later than keys and held their places;
+// - 31 drafted tokens over four caches of 8,191 keys (fp16): 31 us, ten steps
+//   for a CTA, so beginnings, ends and the join are most of it;
+// - 1,021 tokens over 8,001 keys twice (8 heads, 2 key heads): 120 us. A step of
+//   128 keys and 64 rows of both maps takes some 2,000 clocks, 1,000 of them of
+//   products; its 16,384 exponentials would take 512. What is left is the
+//   chain of a step: wait, read scores, weights, vote, fence, arrive. 16 warps to
+//   make weights take 151 us (their barriers cost more than they hide), scores
+//   16, 32 or 64 at once and loops rolled or not 124 to 127.
 #pragma once
 
 #include <cfloat>
@@ -465,7 +486,8 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         __syncwarp();
     } else {
         // A thread has key kr of each step, and that key's scores of map m with all rows.
-        constexpr int X = 16;  // scores that it takes at once
+        // Scores that it takes at once, and where nothing is masked.
+        constexpr int X = 16, XF = RT < 32 ? RT : 32;
         const int m = warp >> 2, kr = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float2 mul = {d.scale_log2, d.scale_log2};
@@ -562,9 +584,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                 const int swz = RT == 16 ? (kr >> 1) & 3 : kr & 7, piece0 = RT == 64 ? 0 : m * RT / 8;
                 unsigned char *const pt = base + F::at_p + (t % F::pbufs) * F::pbuf + (RT == 64 ? m * (F::p / 2) : 0) + kr * F::prow;
                 const auto piece = [&](int c) { return reinterpret_cast<uint4 *>(pt + (((piece0 + c / 8) ^ swz) << 4)); };
-                const auto weigh = [&](const float (&x)[X], int c0) {
+                const auto weigh = [&](const auto &x, int c0) {
 #pragma unroll
-                    for (int c = 0; c < X; c += 8) {
+                    for (int c = 0; c < static_cast<int>(sizeof(x) / sizeof(float)); c += 8) {
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -588,12 +610,12 @@ __global__ void __launch_bounds__(kPgThreads, 1)
                     } else if (fast && all) {
                         // Most steps: no branches, for the sake of the order of instructions.
                         const float *o = &off[m][after][0];
-#pragma unroll
-                        for (int c0 = 0; c0 < RT; c0 += X) {
-                            float x[X];
+#pragma unroll 1
+                        for (int c0 = 0; c0 < RT; c0 += XF) {
+                            float x[XF];
                             tmem_load(scores + c0, x);
 #pragma unroll
-                            for (int c = 0; c < X; c += 4) {
+                            for (int c = 0; c < XF; c += 4) {
                                 const float4 f = *reinterpret_cast<const float4 *>(o + c0 + c);
                                 const float2 u = fma2({x[c], x[c + 1]}, mul, {f.x, f.y}), v = fma2({x[c + 2], x[c + 3]}, mul, {f.z, f.w});
                                 x[c] = u.x;
