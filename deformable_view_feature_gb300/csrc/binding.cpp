@@ -2,8 +2,9 @@
 // token, where the host's time per call counts: rotary.py and paged.py call it.
 // It checks shapes, types and devices, allocates outputs and workspaces on the
 // tensors' device and current stream, and calls libda.so. What depends on
-// values and sizes alone the library checks itself. From Python the same work
-// took 20 to 25 us a call, here 3 to 4.
+// values and sizes alone the library checks itself. A whole call takes the host
+// 6.5 us (rotary norm), 5.1 (append) and 6.5 (attention), launches among it; in
+// Python it took 23, 27 and 32.
 #include <Python.h>
 
 #include <dlfcn.h>

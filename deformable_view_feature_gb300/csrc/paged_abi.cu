@@ -24,7 +24,9 @@ da_status check_cache(const pg_cache &c, int batch, int elem)
     return DA_OK;
 }
 
-// The tensor-core kernel's rule. 16-bit types; widths that its tiles hold and
+// The tensor-core kernel's rule; the fp32 units take 36 us instead of 24 for 4
+// rows of bf16 over four caches of 8,192 keys, 164 instead of 29 for 64.
+// 16-bit types; widths that its tiles hold and
 // whose rows are multiples of 16 bytes; a group of heads within a tile; pages of
 // whole groups of eight places, by which shared memory is swizzled; a bias that
 // it has room for; and what a TMA box needs: 16-byte aligned addresses and
@@ -44,6 +46,9 @@ bool tensor_serves(const pg_problem &d)
     return true;
 }
 
+// Up to here rows are taken straight from memory. Four caches of 8,192 keys in
+// fp32 (2 key heads, D = 64) take 26, 55, 79 and 95 us so for 4, 8, 12 and 16
+// rows, and 73 us each in tiles.
 constexpr int kFewRows = 8;
 
 struct PagedPlan {
@@ -126,9 +131,13 @@ da_status paged_plan(const pg_problem *pr, PagedPlan &p)
     a.keys_per_split = a.Lk > 0 ? a.Lk : 1;
     p.tensor = tensor_serves(d);
     if (p.tensor) {
-        // Tiles of 64 rows for many tokens; fewer columns cost less where there are few.
+        // Rows of a tile. Four caches of 8,192 keys (2 key heads, D = 64, bf16) take
+        // 24 us with 16 or 32 for 16 rows and 28 with 64; 27.0 with 16, 26.9 with 32
+        // and 29.0 with 64 for 32 rows; 33, 29.8 and 29.5 for 64, where 32 is taken
+        // because its weights carry what their rounding took. 124 rows take 40 us
+        // with 32 and 35 with 64, 4,084 rows 298 and 124.
         PagedTcArgs &t = p.tc;
-        t.RT = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+        t.RT = rows <= 16 ? 16 : rows <= 64 && G <= 32 ? 32 : 64;
         t.LP = t.RT / G;
         t.row_tiles = (d.num_tokens + t.LP - 1) / t.LP;
         t.box = 8;
@@ -144,9 +153,10 @@ da_status paged_plan(const pg_problem *pr, PagedPlan &p)
         return DA_OK;
     }
     // CTAs to share a tile where tiles alone leave SMs without work: two to an SM
-    // with 64 keys or more of a full table each; of the few rows' CTAs twice as
-    // many, so that sequences' different lengths leave fewer SMs idle, with 256
-    // keys or more, 32 for each warp.
+    // with 64 keys or more of a full table each (73 us for 16 rows over 8,192 keys
+    // four times in fp32, four to an SM 83); of the few rows' CTAs twice as many, so
+    // that sequences' different lengths leave fewer SMs idle, with 256 keys or
+    // more, 32 for each warp (26 us for 4 rows; with 64 keys or more 40).
     p.few = rows <= kFewRows;
     p.quads = d.width % 4 == 0 && d.value_width % 4 == 0 && aligned(d.q, 4 * elem) && aligned(c.k, 4 * elem) && aligned(c.v, 4 * elem);
     for (int i = 0; i < 4; ++i) p.quads = p.quads && a.qs[i] % 4 == 0 && a.ks[i] % 4 == 0 && (i == 3 || a.vs[i] % 4 == 0);

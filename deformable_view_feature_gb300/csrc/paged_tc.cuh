@@ -22,12 +22,12 @@
 // Warps: 0-3 make the weights of map 0 and 4-7 of map 1, 8 loads keys by TMA and 10
 // values (a box lies in one page: gcd(page size, 128) places), 9 issues the scores'
 // products and 11 the sums', each as soon as what it needs is there. Weights go
-// through shared memory, rounded to the inputs' type; tiles of up to 32 rows,
-// which memory bounds, carry what that took as a second operand, so that their
-// outputs are off by one rounding (2-norm 0.0017 in bf16). With 64 rows, where
-// the warps that make weights bound the kernel, outputs have the error of two
-// independent roundings (0.0025 for bf16, 0.00031 for fp16): a second operand
-// there takes 195 us instead of 149 at 1,021 tokens over 8,001 keys.
+// through shared memory, rounded to the inputs' type. Tiles of 16 and 32 rows,
+// which take up to 64 rows and which memory bounds, carry what that rounding took
+// as a second operand, so that their outputs are off by one rounding (2-norm
+// 0.0017 in bf16). With tiles of 64 rows outputs have the error of two independent
+// roundings (0.0025 in bf16, 0.00031 in fp16): a second operand there took 195 us
+// where one takes 149, at 1,021 tokens over 8,001 keys.
 //
 // Measured, in replayed graphs, with the kernel that joins pieces:
 // - a token each over eight caches of up to 32,768 keys (16 heads, 4 key heads,

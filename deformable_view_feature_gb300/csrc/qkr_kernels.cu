@@ -8,7 +8,18 @@
 // takes the token, and read by all of the token's heads from shared memory.
 // The angle is a product modulo 2^64 of a 32-bit position and a 64-bit fraction
 // of a turn; it is exact, so no position costs digits, and needs no 64-bit
-// floating point. Memory traffic bounds both passes.
+// floating point.
+//
+// Measured in replayed graphs: 8,192 tokens of 8 heads (4 key heads) of 2 x 64
+// in bf16, twice, forward and backward 75 us for 251 MB: 3.4 TB/s, half of what a
+// copy reaches. The forward kernel issues on 60 % of its clocks and waits for
+// loads on most others, the backward kernel the same: instructions and the
+// latency of a warp's two vectors under way bound them together, not memory (25
+// and 35 % busy). 4,095 tokens of 16 heads in fp16, forward: 14 us for 42 MB; a
+// prompt's append, 4 x 4,095 tokens of 8 heads with values: 37 us for 134 MB. One
+// token: 7 us, launch and latency. Four vectors under way, or one; two, three or
+// four CTAs to an SM; registers held back for them: 77 to 110 us for the first,
+// 17 to 23 (against 14 to 17) for the second.
 #include <cmath>
 #include <cuda_bf16.h>
 

@@ -78,10 +78,10 @@ da_status pg_append(const qkr_problem *p, const void *v, const int64_t *v_stride
  * NaN or infinity there reaches no result. Biases hide keys as in dattn.h.
  *
  * Scores, softmax statistics and sums are fp32. On the tensor cores (bf16, fp16;
- * pg_path) the weights are operands in the inputs' type; tiles of up to 32 rows
- * (T * H / Hkv) carry what that rounding took as a second operand, larger ones
- * do not. Sums are taken in an order that lengths and counts fix: results do not
- * vary from run to run.
+ * pg_path) the weights are operands in the inputs' type; up to 64 rows (T * H / Hkv)
+ * of groups of up to 32 heads carry what that rounding took as a second operand,
+ * more do not. Sums are taken in an order that lengths and counts fix: results do
+ * not vary from run to run.
  */
 typedef struct pg_problem {
     int32_t batch;        /* B >= 0 */
