@@ -29,14 +29,13 @@
 // roundings (0.0025 in bf16, 0.00031 in fp16): a second operand there took 195 us
 // where one takes 149, at 1,021 tokens over 8,001 keys.
 //
-// Measured, in replayed graphs, with the kernel that joins pieces:
+// Measured, a call among others, with the kernel that joins pieces:
 // - a token each over eight caches of up to 32,768 keys (16 heads, 4 key heads,
 //   D = 64, bf16): 80 us, 5.3 TB/s of the 6.8 that a copy reaches; memory bounds
-//   it (DRAM 66 % busy under a cold start), then the uneven ends and the join
-//   (5 us). One ring for keys and values together: 89 us, since values are
-//   needed later than keys and held their places;
-// - 31 drafted tokens over four caches of 8,191 keys (fp16): 31 us, ten steps
-//   for a CTA, so beginnings, ends and the join are most of it;
+//   it (DRAM 67 % busy from a cold L2), then the uneven ends and the join (6 us).
+//   Keys and values have rings of their own because values are needed later;
+// - 31 drafted tokens over four caches of 8,191 keys (fp16): 31 us, six steps
+//   for a CTA, so set-up, beginnings, ends and the join (7 us) are most of it;
 // - 1,021 tokens over 8,001 keys twice (8 heads, 2 key heads): 120 us. A step of
 //   128 keys and 64 rows of both maps takes some 2,000 clocks, 1,000 of them of
 //   products; its 16,384 exponentials would take 512. What is left is the
@@ -146,7 +145,9 @@ __device__ __forceinline__ Tile tile_of(const PagedTcArgs &a, int e)
     return t;
 }
 
-// What a tile costs, in steps: to begin and end one takes as long as kOpen.
+// What a tile costs, in steps: to begin and end one takes as long as kOpen. (With
+// 0 instead the trees and prompts above take 40 and 132 us instead of 35 and
+// 125 in a replayed graph; with 2 or 8 38 and 35, 126 and 125.)
 constexpr int kOpen = 4;
 __device__ __forceinline__ int units(const Tile &t) { return t.steps ? t.steps + kOpen : 0; }
 
