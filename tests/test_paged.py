@@ -308,6 +308,23 @@ def test_few_rows_are_rounded_once(kind, T, H):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,D", [(1, 64), (9, 32), (12, 64), (70, 32), (70, 64)])
+def test_maxima_that_climb(kind, T, D):
+    """Scores that grow along the keys by hundreds in all, or fall, so that references are raised in most steps or never."""
+    t, opt = _attention_case(B=2, T=T, N=60, S=16, H=4, Hk=2, D=D, kind=kind, lengths=[960, 777])
+    t["q"] = t["q"].abs()
+    t["k_cache"] = t["k_cache"].abs()
+    for b, n in enumerate([960, 777]):
+        at = torch.arange(n, device="cuda")
+        slope = 8 * at / n if b == 0 else 8 - 8 * at / n
+        places = t["page_table"][b].long()[at // 16], at % 16
+        t["k_cache"][places] = (t["k_cache"][places].float() * slope[:, None, None, None]).to(DT[kind])
+    val, tol = paged_reference(**t, **opt)
+    check({"out": da.paged_attention(**t, **opt)}, val, tol)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind,T,D", [("f32", 3, 32), ("bf16", 3, 32), ("f16", 30, 64), ("bf16", 90, 64), ("bf16", 3, 17)])
 def test_what_masked_places_hold_is_not_used(kind, T, D):
     t, opt = _attention_case(B=4, T=T, N=20, S=16, H=4, Hk=2, D=D, kind=kind, mask=0.6, lengths=[320, 130, 0, 100], holes=True)
