@@ -428,6 +428,12 @@ __global__ void __launch_bounds__(kThreadsG, DP == 32 || (DP == 64 && QT == 16) 
     for (int i = 0; i < M; ++i) {
         if (ri[i].l < 0) continue;
         const int r = r0 + ty + 16 * i, h = n * a.G + ri[i].g;
+        // A row that saw no key has no sums, not even 0 times a value that is not finite.
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+            if (sum[m][i] == 0.f)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) acc[m][i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (a.splits > 1) {
             const int64_t at = ((static_cast<int64_t>(b) * a.Hkv + n) * a.rows + r) * a.splits + split;
 #pragma unroll
@@ -447,7 +453,7 @@ __global__ void __launch_bounds__(kThreadsG, DP == 32 || (DP == 64 && QT == 16) 
         }
         const float w0 = sum[0][i] == 0.f ? 0.f : 1.f / sum[0][i];
         const float w1 = sum[1][i] == 0.f ? 0.f : 1.f / sum[1][i];
-        const float lam = a.lam[h];
+        const float lam = sum[1][i] == 0.f ? 0.f : a.lam[h];
         const int64_t row = (static_cast<int64_t>(b) * a.Lq + ri[i].l) * a.H + h;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {

@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kFewThreads, R == 8 ? 1 : 2) paged_few_kernel(
                 total[i] = fmaf(sums[w][i][r], f, total[i]);
                 all[i] = fmaf(outs[((w * R + r) * 2 + i) * a.Dv + d], f, all[i]);
             }
+            if (total[i] == 0.f) all[i] = 0.f;  // no keys: not even 0 times a value that is not finite
         }
         if (a.splits > 1) {
             const int64_t at = ((static_cast<int64_t>(b) * a.Hkv + n) * a.rows + row) * a.splits + split;
@@ -318,7 +319,8 @@ template <typename T, int WARPS> __global__ void __launch_bounds__(256) paged_me
                 for (int w = 0; w < WARPS; ++w) o[m][c] += outs[w][m][c * 32 + lane];
             }
     }
-    const float lam = a.lam[h], f0 = sum[0] == 0.f ? 0.f : 1.f / sum[0], f1 = sum[1] == 0.f ? 0.f : 1.f / sum[1];
+    // Parts of a row without keys are zeros; lam may be anything.
+    const float f0 = sum[0] == 0.f ? 0.f : 1.f / sum[0], f1 = sum[1] == 0.f ? 0.f : 1.f / sum[1], lam = sum[1] == 0.f ? 0.f : a.lam[h];
 #pragma unroll
     for (int c = 0; c < NC; ++c)
         if (c * 32 + lane < a.Dv)

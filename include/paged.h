@@ -73,9 +73,12 @@ da_status pg_append(const qkr_problem *p, const void *v, const int64_t *v_stride
  *   with tree [B, T, T]: j is before the new tokens, or new token
  *   j' = j - (lengths[b] - counts[b]) has tree[b, i, j'] != 0. causal is not
  *   looked at.
- * A query that sees no key, and one with i >= counts[b], gets 0. What the cache
- * holds at places that no query may see (by length, mask or page) is not used:
- * NaN or infinity there reaches no result. Biases hide keys as in dattn.h.
+ * A query that sees no key, and one with i >= counts[b], gets 0, whatever the
+ * cache and lam hold. What the cache holds at places that no query may see (by
+ * length, mask or page) is not used: NaN or infinity there reaches no result.
+ * (A value that is not finite at a place that some query sees may reach other
+ * queries of the sequence, which weigh it with 0, but none that sees no key.)
+ * Biases hide keys as in dattn.h.
  *
  * Scores, softmax statistics and sums are fp32. On the tensor cores (bf16, fp16;
  * pg_path) the weights are operands in the inputs' type; up to 64 rows (T * H / Hkv)

@@ -1,0 +1,65 @@
+"""A query that sees no key gives exactly 0, whatever the keys and values hold
+that other queries of its tile see, and whatever lam is: padding of a batch and
+rows that a mask leaves empty. Every way out of the attention over a paged
+cache: rows walked by one CTA or split over the keys, on the fp32 units (few
+rows, tiles) and on the tensor cores."""
+import pytest
+import torch
+
+import deformable_view_feature_gb300 as da
+from test_paged import _attention_case
+
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    da.build.build()
+
+
+def _paged(**kw):
+    """Sequence 1 has one new token and padding, the last token of sequence 2, whose cache holds its new tokens alone, sees nothing."""
+    T, L = kw["T"], kw["N"] * kw.get("S", 16)
+    t, opt = _attention_case(B=3, lengths=[L, L, T], counts=[T, 1, T], tree="random", **kw)
+    t["tree"][2, T - 1] = False
+    empty = torch.zeros(3, T, dtype=torch.bool, device="cuda")
+    empty[1, 1:] = empty[2, T - 1] = True
+    return t, opt, empty
+
+
+# Which way out: the kernels by type, width and rows, a split by the table's length.
+PAGED = {
+    "few rows": dict(kind="f32", T=2, N=8),
+    "few rows, split": dict(kind="f32", T=2, N=80),
+    "few rows, many parts": dict(kind="f32", T=2, N=500),
+    "few rows, shared heads": dict(kind="f32", T=2, N=80, H=8, Hk=2, D=64),
+    "few odd rows, split": dict(kind="bf16", T=2, N=80, D=17),
+    "tiles": dict(kind="f32", T=30, N=7),
+    "tiles, split": dict(kind="f32", T=30, N=40),
+    "tiles, many parts": dict(kind="f32", T=30, N=200, H=1, Hk=1),
+    "wide tiles, split": dict(kind="f32", T=30, N=40, D=100),
+    "odd tiles, split": dict(kind="f16", T=30, N=40, D=17),
+    "tensor cores": dict(kind="bf16", T=3, N=8),
+    "tensor cores, split": dict(kind="bf16", T=3, N=200, D=64),
+    "tensor cores, many rows": dict(kind="f16", T=70, N=8, H=4, Hk=2),
+    "tensor cores, many rows, split": dict(kind="bf16", T=70, N=100, H=4, Hk=2, D=64),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", list(PAGED))
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+def test_paged_attention(name, bad):
+    t, opt, empty = _paged(**PAGED[name])
+    want = da.paged_attention(**t, **opt)
+    assert not bool(want[empty].any())
+    first = t["page_table"][:, 0].long()        # place 0: every query that sees a key sees it
+    for where, value in (("v_cache", bad), ("k_cache", bad), ("lam", bad)):
+        u = {**t, where: t[where].clone()}
+        if where == "lam":
+            u["lam"][:] = value
+        else:
+            u[where][first, 0] = value
+        got = da.paged_attention(**u, **opt)
+        assert not bool((got[empty] != 0).any()), where
+        assert where == "k_cache" or not bool(torch.isfinite(got[~empty]).any()), "nothing reached the others"
