@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float w0 = s0 == 0.f ? 0.f : 1.f / s0, w1 = s1 == 0.f ? 0.f : 1.f / s1;
         const int h = n * a.G + (live ? g : 0);
         const float nan = *gave_up ? NAN : 0.f;
-        const float lam = a.lam[h];
+        const float lam = s1 == 0.f ? 0.f : a.lam[h];
         const int64_t pt = ((static_cast<int64_t>(b) * a.Hkv + n) * a.rows + static_cast<int64_t>(l) * a.G + g) * a.splits + split;
         // Outputs go through shared memory, which the products have left, so
         // that neighbouring lanes store neighbouring pieces: piece p of row r
@@ -406,6 +406,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = y[i] = 0.f;
+            }
+            // A row that saw no key has no sums, not even 0 times a value that is not finite.
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (s0 == 0.f) x[i] = 0.f;
+                if (s1 == 0.f) y[i] = 0.f;
             }
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {

@@ -40,7 +40,7 @@ template <typename T> __global__ void __launch_bounds__(kThreadsG) dattn_merge_k
             a.lse[((static_cast<int64_t>(b) * a.H + h) * 2 + m) * a.Lq + l] = sum[m] == 0.f ? INFINITY : top[m] + log2f(sum[m]);
         top[m] = base;
     }
-    const float lam = a.lam[h];
+    const float lam = sum[1] == 0.f ? 0.f : a.lam[h];  // parts of a row without keys are zeros
     const int64_t orow = (static_cast<int64_t>(b) * a.Lq + l) * a.H + h;
     for (int d = lane; d < a.Dv; d += 32) {
         float o[2] = {0.f, 0.f};

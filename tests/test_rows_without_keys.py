@@ -1,8 +1,8 @@
 """A query that sees no key gives exactly 0, whatever the keys and values hold
 that other queries of its tile see, and whatever lam is: padding of a batch and
-rows that a mask leaves empty. Every way out of the attention over a paged
-cache: rows walked by one CTA or split over the keys, on the fp32 units (few
-rows, tiles) and on the tensor cores."""
+rows that a mask leaves empty. Every way out of the attention over a paged cache
+and of the contiguous one: rows walked by one CTA or split over the keys, on the
+fp32 units (few rows, tiles) and on the tensor cores."""
 import pytest
 import torch
 
@@ -10,6 +10,7 @@ import deformable_view_feature_gb300 as da
 from test_paged import _attention_case
 
 INF, NAN = float("inf"), float("nan")
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -63,3 +64,37 @@ def test_paged_attention(name, bad):
         got = da.paged_attention(**u, **opt)
         assert not bool((got[empty] != 0).any()), where
         assert where == "k_cache" or not bool(torch.isfinite(got[~empty]).any()), "nothing reached the others"
+
+
+def _contiguous(kind, D, Lq=30, Lk=100, H=4, Hk=2):
+    """Item 1 has 5 keys, so that its first queries are before all of them."""
+    g = torch.Generator().manual_seed(D + Lk)
+    t = [torch.randn(2, *s, generator=g).to(DT[kind]).cuda() for s in ((Lq, H, 2, D), (Lk, Hk, 2, D), (Lk, Hk, 2 * D))]
+    opt = dict(key_lengths=torch.tensor([Lk, 5], dtype=torch.int32, device="cuda"), causal=True)
+    empty = opt["key_lengths"][:, None] - Lq + torch.arange(Lq, device="cuda") < 0  # positions before key 0
+    return *t, torch.rand(H, generator=g).cuda() + 0.1, opt, empty
+
+
+CONTIGUOUS = {
+    "tiles": dict(kind="f32", D=32), "tiles, split": dict(kind="f32", D=32, Lk=1000), "few rows, split": dict(kind="f32", D=64, Lq=7, Lk=1000),
+    "odd tiles, split": dict(kind="bf16", D=17, Lk=1000), "tensor cores": dict(kind="bf16", D=32), "tensor cores, wide": dict(kind="f16", D=64, Lq=300),
+    "tensor cores, split": dict(kind="bf16", D=64, Lk=1000), "tensor cores, fp16, split": dict(kind="f16", D=32, Lk=1000),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", list(CONTIGUOUS))
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+def test_contiguous_attention(name, bad):
+    q, k, v, lam, opt, empty = _contiguous(**CONTIGUOUS[name])
+    for where in ("v", "lam"):
+        u = {"v": v.clone(), "lam": lam.clone()}
+        if where == "v":
+            u["v"][:, 0] = bad
+        else:
+            u["lam"][:] = bad
+        out, (out1, lse) = da.dattn_forward(q, k, **u, **opt, keep_for_backward=True)
+        assert torch.equal(torch.nan_to_num(out, 0, 1, -1) != 0, torch.nan_to_num(da.dattn_forward(q, k, **u, **opt), 0, 1, -1) != 0)
+        assert not bool((out[empty] != 0).any()) and not bool((out1[empty] != 0).any()), where
+        assert bool((lse[1, :, :, : int(empty[1].sum())] == INF).all())
+        assert not bool(torch.isfinite(out[~empty]).any()), "nothing reached the others"
