@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const float nan = *gave_up ? NAN : 0.f;
         if (live)
             a.delta[((static_cast<int64_t>(b) * a.Hkv + n) * 2 + m) * a.rows + static_cast<int64_t>(l) * a.G + g] =
-                d[m] + (part[m][0][rl] + part[m][1][rl]) / f + nan;
+                (none ? 0.f : d[m] + (part[m][0][rl] + part[m][1][rl]) / f) + nan;
         T *dst = static_cast<T *>(a.grad_q) + (((static_cast<int64_t>(b) * a.Lq + l) * a.H + h) * 2 + m) * a.D;
         const bool wide = aligned16(a.grad_q);
 #pragma unroll 1
@@ -589,6 +589,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = 0.f;
             }
+            // A row that sees no key has no gradient, not even 0 times a key or lam that is not finite.
+            if (none)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = 0.f;
             if (live) store_row(dst + c, x, a.scale / f + nan, a.D - c, wide);
         }
     }

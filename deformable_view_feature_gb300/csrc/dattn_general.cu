@@ -217,6 +217,10 @@ __global__ void __launch_bounds__(kThreadsG) dattn_grad_q_kernel(const __grid_co
         const int64_t row = (static_cast<int64_t>(b) * a.Hkv + n) * a.rows + r;
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
+            // A row that sees no key has no gradient, not even 0 times a key or lam that is not finite.
+            if (lse[m][i] == INFINITY)
+#pragma unroll
+                for (int c = 0; c < F::ND; ++c) acc[m][i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
             float *delta = a.delta + ((static_cast<int64_t>(b) * a.Hkv + n) * 2 + m) * a.rows + r;
             if (tx == 0) {
                 if (a.splits == 1) *delta = dl[m][i] + rest[m][i];

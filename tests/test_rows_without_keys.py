@@ -98,3 +98,21 @@ def test_contiguous_attention(name, bad):
         assert not bool((out[empty] != 0).any()) and not bool((out1[empty] != 0).any()), where
         assert bool((lse[1, :, :, : int(empty[1].sum())] == INF).all())
         assert not bool(torch.isfinite(out[~empty]).any()), "nothing reached the others"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", list(CONTIGUOUS))
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+def test_contiguous_gradients(name, bad):
+    """Such a query's grad_q is 0."""
+    q, k, v, lam, opt, empty = _contiguous(**CONTIGUOUS[name])
+    grad = torch.randn(v.shape[0], q.shape[1], q.shape[2], v.shape[3], generator=torch.Generator().manual_seed(1)).to(q.dtype).cuda()
+    for where in ("k", "v", "lam"):
+        u = {"k": k.clone(), "v": v.clone(), "lam": lam.clone()}
+        if where == "lam":
+            u["lam"][:] = bad
+        else:
+            u[where][:, 0] = bad
+        out, saved = da.dattn_forward(q, **u, **opt, keep_for_backward=True)
+        got = da.dattn_backward(q, u["k"], u["v"], u["lam"], out, saved, grad, **opt)
+        assert not bool((got[0][empty] != 0).any()), where
