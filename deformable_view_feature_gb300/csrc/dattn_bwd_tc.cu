@@ -1028,6 +1028,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 for (int i = 0; i < 32; ++i) x[i] = 0.f;
             }
             if (!in) continue;
+            // A key that no query may see has no gradient, not even 0 times another's that is not finite.
+            if (!use)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = 0.f;
             if (of_v) store_row(static_cast<T *>(a.grad_v) + at * a.Dv + col, x, 1.f / lift + nan, a.Dv - col, wide_v);
             else store_row(static_cast<T *>(a.grad_k) + (at * 2 + half) * a.D + col, x, a.scale / (lift * f) + nan, a.D - col, wide_k);
         }

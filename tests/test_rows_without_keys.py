@@ -116,3 +116,16 @@ def test_contiguous_gradients(name, bad):
         out, saved = da.dattn_forward(q, **u, **opt, keep_for_backward=True)
         got = da.dattn_backward(q, u["k"], u["v"], u["lam"], out, saved, grad, **opt)
         assert not bool((got[0][empty] != 0).any()), where
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", list(CONTIGUOUS))
+def test_gradients_of_keys_past_the_length(name):
+    """They are 0 too where the other keys' are NaN."""
+    q, k, v, lam, opt, _ = _contiguous(**CONTIGUOUS[name])
+    grad = torch.randn(v.shape[0], q.shape[1], q.shape[2], v.shape[3], generator=torch.Generator().manual_seed(1)).to(q.dtype).cuda()
+    k[:, 0] = NAN
+    out, saved = da.dattn_forward(q, k, v, lam, **opt, keep_for_backward=True)
+    _, gk, gv, _, _ = da.dattn_backward(q, k, v, lam, out, saved, grad, **opt)
+    assert not bool((gk[1, 5:] != 0).any()) and not bool((gv[1, 5:] != 0).any())
+    assert bool(torch.isnan(gk[1, :5]).all()) and bool(torch.isnan(gv[1, :5]).all())
