@@ -242,7 +242,7 @@ da_status backward_impl(const da_dims &d, da::BwdArgs &a, int chunks, const floa
     // The per-CTA grad_loc staging area of the scatter path must fit in
     // shared memory.
     const size_t smem = da::scatter_smem_bytes(pb);
-    if (smem > 200 * 1024)
+    if (smem > da::kScatterSmemMax)
         return fail(DA_ERR_UNSUPPORTED, "num_pts = %d too large for the grad_loc staging area", pb.P);
     a.grad_out = grad_out;
     a.grad_feat = grad_feat;

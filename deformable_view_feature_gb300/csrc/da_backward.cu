@@ -421,8 +421,7 @@ cudaError_t launch_layout(const BwdArgs &a, cudaStream_t st)
     if (grid == 0) return cudaSuccess;
     const size_t smem = scatter_smem_bytes(a.pb);
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(bwd_kernel<T, CH, FUSED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+        const cudaError_t e = allow_shared(bwd_kernel<T, CH, FUSED>, kScatterSmemMax);
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(bwd_kernel<T, CH, FUSED>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, st, a);

@@ -739,9 +739,7 @@ cudaError_t launch(const FwdArgs &a, cudaStream_t st)
         case kLayoutProj: {
             const size_t smem = projected_smem_bytes(a.pb);
             if (smem > 48 * 1024) {
-                const cudaError_t e = cudaFuncSetAttribute(fwd_proj_kernel<T, CH>,
-                                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                           static_cast<int>(smem));
+                const cudaError_t e = allow_shared(fwd_proj_kernel<T, CH>, kProjectedSmemMax);
                 if (e != cudaSuccess) return e;
             }
             fwd_proj_kernel<T, CH><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a);

@@ -212,6 +212,7 @@ inline size_t scatter_smem_bytes(const Problem &pb)
     return static_cast<size_t>(pb.anchors_per_cta) * (pb.layout == kLayoutFused ? pb.G : 1) * pb.P * 2 *
            sizeof(float);
 }
+constexpr size_t kScatterSmemMax = 200 * 1024;
 
 // Whether the forward and the scatter backward take the thread-per-chunk
 // kernels: few samples per (anchor, group) (the DCNv4 form has 9), and an
@@ -441,6 +442,15 @@ __device__ __forceinline__ void red_add_v4_if(bool pred, float *p, float a, floa
 // pitch of 36 entries (288 B) staggers the four corners by 8 banks, so the
 // four corner groups of a warp read conflict-free.
 constexpr int kTabPitch = 36;
+
+// Allows `kernel` the dynamic shared memory that its largest call takes. The limit
+// belongs to the function on the device and not to a launch: set to what each
+// call takes, one host thread would lower it between another's setting and its
+// launch. So every call of a kernel gives the same `most`.
+template <typename K> cudaError_t allow_shared(K kernel, size_t most)
+{
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+}
 
 // Programmatic dependent launch for the kernels of one call that follow one
 // another on a stream (the binned backward's chain): such a kernel may be

@@ -51,11 +51,11 @@ bool tensor_serves(const dattn_problem &d, bool backward)
     const int G = d.num_heads / d.num_kv_heads;
     if (d.width % 8 || d.value_width % 8 || d.width > 64 || d.value_width > 128 || G > 128) return false;
     if (d.batch < 1 || d.num_queries < 1 || d.num_keys < 1) return false;
-    if (G * (2 * (d.num_buckets > 0 ? d.reach : 0) + 129) > (backward ? 4096 : 8192)) return false;
+    if (G * (2 * (d.num_buckets > 0 ? d.reach : 0) + 129) > (backward ? kTcBiasBackward : kTcBias)) return false;
     // Their grids are one-dimensional.
     const int64_t tiles = (static_cast<int64_t>(d.num_queries > d.num_keys ? d.num_queries : d.num_keys) * G / 64 + 1);
     if (tiles * d.batch * d.num_kv_heads > INT32_MAX / 4) return false;
-    if (backward && d.num_buckets > 32) return false;
+    if (backward && d.num_buckets > kTcBuckets) return false;
     if (!aligned(d.q, 16) || !aligned(d.k, 16) || !aligned(d.v, 16)) return false;
     const int nq[4] = {d.batch, d.num_queries, d.num_heads, 2}, nk[4] = {d.batch, d.num_keys, d.num_kv_heads, 2};
     auto fits = [](int64_t stride, int size) { return size == 1 || (stride > 0 && stride % 8 == 0 && stride < (int64_t{1} << 38)); };

@@ -1050,9 +1050,9 @@ struct BwdMaps {
 };
 
 template <typename K>
-cudaError_t launch_bwd(K kernel, dim3 grid, size_t smem, const DattnArgs &a, const BwdMaps &m, cudaStream_t st)
+cudaError_t launch_bwd(K kernel, dim3 grid, size_t smem, size_t most, const DattnArgs &a, const BwdMaps &m, cudaStream_t st)
 {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_shared(kernel, most);
     if (e != cudaSuccess) return e;
     kernel<<<grid, kBwdThreads, smem, st>>>(a, m.q, m.k, m.v, m.g);
     return cudaGetLastError();
@@ -1073,10 +1073,11 @@ cudaError_t bwd_kernels(const DattnArgs &a, const BwdMaps &own_rows, const BwdMa
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     e = launch_bwd(dattn_grad_q_tc_kernel<T, DP, VP>, dim3((a.Lq + LP - 1) / LP * a.Hkv * a.B),
-                                     Q::bytes + 1024 + sizeof(float) * (a.nb ? a.G * (2 * a.reach + 1) : 0), a, own_rows, st);
+                   Q::bytes + 1024 + sizeof(float) * (a.nb ? a.G * (2 * a.reach + 1) : 0), Q::bytes + 1024 + sizeof(float) * kTcBiasBackward, a,
+                   own_rows, st);
     if (e != cudaSuccess) return e;
     return launch_bwd(dattn_grad_kv_tc_kernel<T, DP, VP>, dim3((a.Lk + kOwn - 1) / kOwn * a.Hkv * a.B),
-                      KV::bytes + 1024 + KV::table(a.nb, a.reach), a, own_keys, st);
+                      KV::bytes + 1024 + KV::table(a.nb, a.reach), KV::bytes + 1024 + KV::table(kTcBuckets, DATTN_MAX_REACH), a, own_keys, st);
 }
 
 template <typename T> cudaError_t bwd_widths(const DattnArgs &a, const BwdMaps &r, const BwdMaps &k, cudaStream_t st)

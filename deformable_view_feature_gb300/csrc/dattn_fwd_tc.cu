@@ -503,7 +503,7 @@ cudaError_t launch_fwd(const DattnArgs &a, const CUtensorMap &mq, const CUtensor
     using F = FwdShared<DP, VP>;
     const size_t smem = F::bytes + 1024 + sizeof(float) * a.G * bias_span(a.reach);
     const auto kernel = dattn_fwd_tc_kernel<T, DP, VP>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_shared(kernel, F::bytes + 1024 + sizeof(float) * kTcBias);
     if (e != cudaSuccess) return e;
     const int LP = kTile / a.G;
     const unsigned grid = static_cast<unsigned>((a.Lq + LP - 1) / LP * a.splits) * a.Hkv * a.B;

@@ -504,7 +504,7 @@ template <typename T, int DP> cudaError_t backward_width(const DattnArgs &a, cud
     const int warps = kThreadsG / 32;
     if (a.rows > 0) {
         const dim3 grid(static_cast<unsigned>((a.rows + F::RT - 1) / F::RT * a.splits), a.Hkv, a.B);
-        e = launch(dattn_grad_q_kernel<T, DP>, grid, F::floats + table_floats(a), a, st);
+        e = launch(dattn_grad_q_kernel<T, DP>, grid, F::floats + table_floats(a), F::floats + kTableFloats, a, st);
         if (e == cudaSuccess && a.splits > 1) {
             const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv * a.rows;
             dattn_join_q_kernel<T><<<static_cast<unsigned>((rows + warps - 1) / warps), kThreadsG, 0, st>>>(a);
@@ -515,8 +515,9 @@ template <typename T, int DP> cudaError_t backward_width(const DattnArgs &a, cud
         const dim3 grid(static_cast<unsigned>((a.Lk + F::KT - 1) / F::KT * a.row_splits), a.Hkv, a.B);
         const size_t base = F::floats + table_floats(a), own = base + kThreadsG * a.nb * a.G;
         DattnArgs with = a;
-        with.own_sums = own * sizeof(float) <= 227 * 1024;
-        e = launch(dattn_grad_kv_kernel<T, DP>, grid, with.own_sums ? own : base + warps * a.nb * a.G, with, st);
+        constexpr size_t most = 227 * 1024 / sizeof(float);
+        with.own_sums = own <= most;
+        e = launch(dattn_grad_kv_kernel<T, DP>, grid, with.own_sums ? own : base + warps * a.nb * a.G, most, with, st);
         if (e == cudaSuccess && a.row_splits > 1) {
             const int64_t keys = static_cast<int64_t>(a.B) * a.Lk * a.Hkv;
             dattn_join_kv_kernel<T><<<static_cast<unsigned>((keys + warps - 1) / warps), kThreadsG, 0, st>>>(a);

@@ -479,12 +479,13 @@ int padded_width(const DattnArgs &a)
 
 size_t table_floats(const DattnArgs &a) { return a.nb ? a.nb * a.G + (2 * a.reach + 2) / 2 + 2 : 0; }
 
-template <typename K> cudaError_t launch(K kernel, dim3 grid, size_t floats, const DattnArgs &a, cudaStream_t st)
+constexpr size_t kTableFloats = DATTN_MAX_TABLE + (2 * DATTN_MAX_REACH + 2) / 2 + 2;  // at most
+
+template <typename K> cudaError_t launch(K kernel, dim3 grid, size_t floats, size_t most, const DattnArgs &a, cudaStream_t st)
 {
-    const size_t smem = floats * sizeof(float);
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_shared(kernel, most * sizeof(float));
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreadsG, smem, st>>>(a);
+    kernel<<<grid, kThreadsG, floats * sizeof(float), st>>>(a);
     return cudaGetLastError();
 }
 
@@ -492,8 +493,9 @@ template <typename T, int DP, bool PAGED> cudaError_t forward_width(const DattnA
 {
     const int qt = dattn_general_row_tile(a);
     const dim3 grid(static_cast<unsigned>((a.rows + qt - 1) / qt * a.splits), a.Hkv, a.B);
-    if (qt == 16) return launch(dattn_fwd_kernel<T, DP, 16, PAGED>, grid, FwdTile<T, DP, 16>::floats + table_floats(a), a, st);
-    return launch(dattn_fwd_kernel<T, DP, 64, PAGED>, grid, FwdTile<T, DP, 64>::floats + table_floats(a), a, st);
+    constexpr size_t few = FwdTile<T, DP, 16>::floats, many = FwdTile<T, DP, 64>::floats;
+    if (qt == 16) return launch(dattn_fwd_kernel<T, DP, 16, PAGED>, grid, few + table_floats(a), few + kTableFloats, a, st);
+    return launch(dattn_fwd_kernel<T, DP, 64, PAGED>, grid, many + table_floats(a), many + kTableFloats, a, st);
 }
 
 }  // namespace

@@ -15,6 +15,11 @@
 #include "dattn_internal.cuh"
 
 namespace da {
+
+// Floats of expanded bias that the forward and the backward kernels have room
+// for, and buckets that the backward ones sum.
+constexpr int kTcBias = 8192, kTcBiasBackward = 4096, kTcBuckets = 32;
+
 namespace tc {
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }

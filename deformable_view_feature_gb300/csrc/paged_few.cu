@@ -337,10 +337,10 @@ template <typename T> cudaError_t merge(const DattnArgs &a, cudaStream_t st)
 
 template <typename T, int R, int KB, int V, int NK, int NV> cudaError_t launch_few(const DattnArgs &a, cudaStream_t st)
 {
-    const size_t smem = sizeof(float) * kFewWarps * R * 2 * a.Dv;
+    const size_t row = sizeof(float) * kFewWarps * R * 2;  // of one channel
     const auto kernel = paged_few_kernel<T, R, KB, V, NK, NV>;
-    if (const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)); e != cudaSuccess) return e;
-    kernel<<<dim3(static_cast<unsigned>((a.rows + R - 1) / R * a.splits), a.Hkv, a.B), kFewThreads, smem, st>>>(a);
+    if (const cudaError_t e = allow_shared(kernel, row * NV * 32 * V); e != cudaSuccess) return e;
+    kernel<<<dim3(static_cast<unsigned>((a.rows + R - 1) / R * a.splits), a.Hkv, a.B), kFewThreads, row * a.Dv, st>>>(a);
     return cudaGetLastError();
 }
 

@@ -850,7 +850,7 @@ cudaError_t launch_tc(const PagedTcArgs &a, const CUtensorMap &mq, const CUtenso
     using F = PgShared<DP, VP, RT>;
     const size_t smem = F::bytes + 1024 + paged_bias_bytes(a.d.nb, a.d.H, a.d.reach);
     const auto kernel = paged_tc_kernel<T, DP, VP, RT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t e = allow_shared(kernel, F::bytes + 1024 + kPgBias);
     if (e != cudaSuccess) return e;
     kernel<<<a.ctas, kPgThreads, smem, st>>>(a, mq, mk, mv);
     e = cudaGetLastError();
