@@ -30,10 +30,22 @@ da_status tensor_map(CUtensorMap &m, int dtype, const void *base, int width, int
     const cuuint32_t box[5] = {static_cast<cuuint32_t>(box_width), 1, static_cast<cuuint32_t>(box_heads),
                                static_cast<cuuint32_t>(box_len), 1};
     const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
-    const CUresult r = encode(&m, dtype == DA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
-                              const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              box_width == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const auto run = [&] {
+        return encode(&m, dtype == DA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+                      const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      box_width == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = run();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {
+        // The host thread's first call: the runtime makes its device's context
+        // current, which the driver does not do by itself.
+        int device = 0;
+        cudaError_t e = cudaGetDevice(&device);
+        if (e == cudaSuccess) e = cudaSetDevice(device);
+        if (e != cudaSuccess) return cuda_fail(e, "context of a host thread");
+        r = run();
+    }
     return r == CUDA_SUCCESS ? DA_OK : fail(DA_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", static_cast<int>(r));
 }
 

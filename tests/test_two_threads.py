@@ -104,6 +104,28 @@ def test_calls_of_different_sizes(name):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("call", ["paged_attention", "dattn_forward", "dattn_backward"])
+def test_a_threads_first_call(call):
+    """Of a thread that has made no CUDA call before: each of these uses the tensor cores, whose operands the driver describes."""
+    make = {"paged_attention": _paged, "dattn_forward": _forward, "dattn_backward": _backward}[call]
+    run = make(**(dict(B=2, N=9, T=3, H=4, Hk=2, kind="bf16", lengths=[144, 77]) if call == "paged_attention" else dict(B=2, Lq=40, Lk=50, kind="bf16")))
+    want, wrong, got = run(), [], []
+    torch.cuda.synchronize()
+
+    def work():
+        try:
+            got.append(run())
+        except Exception as e:  # noqa: BLE001 - any of them is the test's finding
+            wrong.append(e)
+
+    for _ in range(20):
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+    assert wrong == [] and all(torch.equal(x, want) for x in got)
+
+
+@pytest.mark.gpu
 def test_a_serving_loop_beside_another():
     """Appends and attention of two caches, each on a thread and a stream of its own."""
     def loop(kind, seed):
