@@ -19,6 +19,8 @@ def built():
 CASES = [
     ("sixty-five rows of narrow heads", "tensor", dict(B=2, N=9, S=64, T=65, kind="bf16", lengths=[576, 300])),
     ("sixty-five rows of one narrow head", "tensor", dict(B=2, N=9, S=64, T=65, H=1, Hk=1, kind="f16", lengths=[576, 65])),
+    ("narrowest heads", "tensor", dict(B=2, N=9, S=16, T=3, D=8, Dv=8, kind="bf16", lengths=[144, 77])),
+    ("narrowest heads, many rows", "tensor", dict(B=2, N=9, S=8, T=70, D=8, Dv=16, kind="f16", lengths=[72, 71])),
     ("wide heads, a prompt's part", "general", dict(B=2, N=20, S=32, T=150, H=4, Hk=2, D=128, kind="bf16", lengths=[640, 201])),
     ("wide heads, few rows", "general", dict(B=2, N=20, S=32, T=2, H=4, Hk=2, D=128, kind="bf16", lengths=[640, 201])),
     ("a little wider than the tiles", "general", dict(B=2, N=20, S=32, T=70, H=4, Hk=2, D=72, kind="f16", lengths=[640, 201], tree="random")),
