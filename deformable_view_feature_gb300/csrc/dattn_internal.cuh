@@ -9,11 +9,6 @@
 
 namespace da {
 
-// The problem as the kernels see it. The G = H / Hkv query heads that share a
-// key head are handled together: a "row" is one (query, head) pair, row r of
-// key head n being query r / G of head n*G + r % G. One token of a serving
-// batch thus still fills a tile with its G heads, and keys are read once for
-// all of them.
 // Where the keys of a paged cache lie (paged.h): then DattnArgs' k and v are
 // the cache, their first two strides those of pages and places, Lk the places
 // of a sequence, and the queries' rows Lq those of padded new tokens.
@@ -24,6 +19,11 @@ struct PagedArgs {
     FastDiv div_page;
 };
 
+// The problem as the kernels see it. The G = H / Hkv query heads that share a
+// key head are handled together: a "row" is one (query, head) pair, row r of
+// key head n being query r / G of head n*G + r % G. One token of a serving
+// batch thus still fills a tile with its G heads, and keys are read once for
+// all of them.
 struct DattnArgs {
     PagedArgs pg;
     const void *q, *k, *v;

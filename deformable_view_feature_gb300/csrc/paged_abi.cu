@@ -24,13 +24,13 @@ da_status check_cache(const pg_cache &c, int batch, int elem)
     return DA_OK;
 }
 
-// The tensor-core kernel's rule; the fp32 units take 36 us instead of 24 for 4
-// rows of bf16 over four caches of 8,192 keys, 164 instead of 29 for 64.
-// 16-bit types; widths that its tiles hold and
+// The tensor-core kernel's rule. 16-bit types; widths that its tiles hold and
 // whose rows are multiples of 16 bytes; a group of heads within a tile; pages of
-// whole groups of eight places, by which shared memory is swizzled; a bias that
-// it has room for; and what a TMA box needs: 16-byte aligned addresses and
-// strides, none of them zero.
+// whole groups of eight places, by which shared memory is swizzled; a bias (of all
+// heads) that it has room for; and what a TMA box needs: 16-byte aligned addresses
+// and strides, none of them zero. Over four caches of up to 8,192 keys (2 key heads,
+// D = 64, bf16) it takes 25 us for 4 rows, 31 for 64 and 79 for 1,024 in a replayed
+// graph; outside the rule, with pages of 20, the fp32 units take 36, 165 and 1,803.
 bool tensor_serves(const pg_problem &d)
 {
     const pg_cache &c = d.cache;

@@ -1,19 +1,21 @@
 // Differential attention over a paged cache on the fp32 units for few rows
 // (include/paged.h): single tokens, of every type, width, stride and alignment.
-// fp32 caches always come here or to the tiles of dattn_general.cu.
+// fp32 caches always come here or to the tiles of paged_general.cu.
 //
-// Memory bounds it, so nothing is staged: a warp reads its keys' rows straight
-// into registers, half its lanes map 0's key and half map 1's, all of them the
+// A key is used for little arithmetic, so nothing is staged: a warp reads its keys'
+// rows straight into registers, half its lanes map 0's key and half map 1's, all of them the
 // value, and holds the running maxima, sums and outputs of R rows. The dot
 // products of KB keys with R rows, KB * R <= 16, are 16 sums over the 16 lanes of
 // a half-warp; folded together they take 15 exchanges and leave each lane one
 // (key, row) score of its map, which is where biases, masks and the exponential
-// are applied, once. Sixteen warps to an SM, with KB keys each under way, cover
-// the latency of memory.
+// are applied, once. Sixteen warps to an SM (eight with 8 rows, whose registers
+// leave room for one CTA) have KB keys each under way.
 //
 // Four ragged caches of up to 8,192 keys (2 key heads, D = 64, Dv = 128, a token
-// of 8 heads; 55 MB) take 26 us in fp32, the tiles of dattn_general.cu
-// 73; with 8 rows 55 us, where the arithmetic of the dot products bounds it.
+// of 8 heads; 55 MB) take 26 us in fp32, the tiles of paged_general.cu 73; with 8
+// rows 55 us. That is 2.1 and 1.0 TB/s of the 6.8 of a copy: not memory bounds it
+// but a batch's exchanges, for 4 keys and 4 rows 8 of pages and places, 15 to fold
+// and 32 to spread the weights, which grow with the rows.
 #include <cfloat>
 
 #include "paged_internal.cuh"
@@ -66,7 +68,7 @@ __global__ void __launch_bounds__(kFewThreads, R == 8 ? 1 : 2) paged_few_kernel(
     const int groups = (a.rows + R - 1) / R;
     const int split = blockIdx.x % a.splits, r0 = blockIdx.x / a.splits % groups * R, n = blockIdx.y, b = blockIdx.z;
     const int len = dattn_length(a, b), count = paged_count(a, b), old = len - count;
-    // Shares of the sequence's own keys, in whole turns of the CTA's warps.
+    // Shares of the sequence's own keys, in whole turns of a warp.
     const int per = ((len + a.splits - 1) / a.splits + 31) / 32 * 32;
     int jb = split * per, end = min(len, jb + per);
     if (r0 >= count * a.G) end = 0;

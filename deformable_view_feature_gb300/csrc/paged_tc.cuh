@@ -25,9 +25,10 @@
 // through shared memory, rounded to the inputs' type. Tiles of 16 and 32 rows,
 // which take up to 64 rows and which memory bounds, carry what that rounding took
 // as a second operand, so that their outputs are off by one rounding (2-norm
-// 0.0017 in bf16). With tiles of 64 rows outputs have the error of two independent
-// roundings (0.0025 in bf16, 0.00031 in fp16): a second operand there took 195 us
-// where one takes 149, at 1,021 tokens over 8,001 keys.
+// 0.0017 in bf16, 0.00021 in fp16). With tiles of 64 rows outputs have the error of
+// two independent roundings, 1.55 times that (0.0026 and 0.00032): a second operand
+// there took 222 us where one took 126, in a replayed graph at 1,021 tokens over
+// 8,001 keys.
 //
 // Measured, a call among others, with the kernel that joins pieces:
 // - a token each over eight caches of up to 32,768 keys (16 heads, 4 key heads,

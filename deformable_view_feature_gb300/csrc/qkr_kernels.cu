@@ -17,7 +17,9 @@
 // latency of a warp's two vectors under way bound them together, not memory (25
 // and 35 % busy). 4,095 tokens of 16 heads in fp16, forward: 14 us for 42 MB; a
 // prompt's append, 4 x 4,095 tokens of 8 heads with values: 37 us for 134 MB. One
-// token: 7 us, launch and latency. Four vectors under way, or one; two, three or
+// token: 7 us, launch and latency. The forward forms with 16-byte pieces do not fit
+// in the 80 registers that three CTAs to an SM leave: 200 B of a thread's are stored
+// and 288 B read in bf16, 304 and 448 with a paged side. Four vectors under way, or one; two, three or
 // four CTAs to an SM; registers held back for them: 77 to 110 us for the first,
 // 17 to 23 (against 14 to 17) for the second.
 #include <cmath>

@@ -111,7 +111,11 @@ typedef struct pg_problem {
 } pg_problem;
 
 /* Which kernels pg_attention takes (a host-only rule on types, sizes and
- * alignment): 1 the tensor-core ones, 0 the general ones, < 0 invalid. */
+ * alignment): 1 the tensor-core ones, 0 the general ones, < 0 invalid. The
+ * tensor cores take bf16 and fp16 with D and Dv multiples of 8 up to 64 and 128,
+ * up to 64 heads to a key head, a page_size that is a multiple of 8, up to 6,144
+ * bytes of bias (4 * num_buckets * H + 2 * (2 * reach + 1)), and addresses and
+ * strides that are multiples of 16 bytes, none of the strides zero. */
 int32_t pg_path(const pg_problem *p);
 
 /* Bytes of device scratch of pg_attention; host-only. */
