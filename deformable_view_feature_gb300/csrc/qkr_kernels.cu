@@ -19,9 +19,11 @@
 // prompt's append, 4 x 4,095 tokens of 8 heads with values: 37 us for 134 MB. One
 // token: 7 us, launch and latency. The forward forms with 16-byte pieces do not fit
 // in the 80 registers that three CTAs to an SM leave: 200 B of a thread's are stored
-// and 288 B read in bf16, 304 and 448 with a paged side. Four vectors under way, or one; two, three or
-// four CTAs to an SM; registers held back for them: 77 to 110 us for the first,
-// 17 to 23 (against 14 to 17) for the second.
+// and 288 B read in bf16, 304 and 448 with a paged side. With two CTAs to an SM
+// nothing is spilled and fewer warps hide the loads: 73 us for the first of these
+// cases, but 16.4 for the second and 41 for the third. Four vectors under way, or
+// one, with two to four CTAs to an SM: 77 to 110 us for the first, 17 to 23 for the
+// second.
 #include <cmath>
 #include <cuda_bf16.h>
 
